@@ -251,6 +251,162 @@ int specverify_quantile_cut(specverify_ctx *ctx, void *hip_stream, int P, int N,
                             const float *scores, float *r_cut, uint8_t *keep, int32_t *n_keep);
 
 /*
+ * Cut laws.  A filter holds per-row (or per-sequence) parameters in device arrays; a NULL array,
+ * or a NULL filter, cuts nothing (temperature 1).  The law of a row x with temperature T, top-k k,
+ * top-p p and min-p m: order the ids by x descending, ties lowest id first (-0 equals +0), and let
+ * w_i = exp((x_i - max x) / T).
+ *  - S_k = the first k ids (all V for k <= 0 or k >= V);
+ *  - S_p = the ids of S_k whose exclusive prefix sum of w, in that order, is below p times the sum
+ *    over S_k (the first id always; all for p = 1);
+ *  - S = the ids of S_p with w_i >= m; the law is w_i / sum_S w on S and 0 elsewhere.
+ * T = 0 is the greedy law: the first id of the order has probability 1.
+ * A row has no law when it holds NaN or +inf or nothing finite, or when its parameters are out of
+ * range (T finite and >= 0; p and m in [0, 1]; any k): see each call for what it returns then.
+ * -inf entries are ids of zero weight.  Values lie in device memory, so none of this is checked on
+ * the host.  All weights, sums and decisions are fp64 and every cut is the exact one.
+ */
+typedef struct specverify_filter {
+    const float *temperature;
+    const int32_t *top_k;
+    const float *top_p;
+    const float *min_p;
+} specverify_filter;
+
+/*
+ * Draft-token sampler with cut laws: one draw per row.  out_tokens[n] = the first id (ascending)
+ * whose inclusive prefix sum of row n's kept w exceeds uniforms[n] times their sum (the last id of
+ * positive weight if rounding leaves none); out_probs [N] float = its probability, or NULL.
+ * logits: N rows of V ids (dtype), row n at element n * row_stride (row_stride >= V); `filter`
+ * arrays [N]; uniforms [N] float in [0,1].  A row without a law gets token -1 and probability NaN.
+ * One kernel, no workspace.  Errors as for specverify_sample, and EINVAL for row_stride < V,
+ * ECAPACITY for N >= 2^22 (one 1024-thread workgroup per row).
+ */
+int specverify_sample_filtered(specverify_ctx *ctx, void *hip_stream, int dtype, int N, int V,
+                               int64_t row_stride, const specverify_filter *filter,
+                               const void *logits, const float *uniforms, int32_t *out_tokens,
+                               float *out_probs);
+
+/*
+ * Sampling verify with cut laws: specverify_run_sampling with p_j the cut law of target row j and
+ * q_j that of draft row j: a draft sampled with a filter has to be verified with it.  `filter`
+ * arrays [B], one entry per sequence; a NULL draft_filter is the target's.  A sequence with bad
+ * ids, or any of whose 2K+1 rows has no law, gets accepted_len -1, tokens -1 and probabilities
+ * NaN.  Layouts and errors as specverify_run_sampling; ECAPACITY also for
+ * B * (2K+1) >= 2^22 (one 1024-thread workgroup per row).
+ */
+int specverify_run_sampling_filtered(specverify_ctx *ctx, void *hip_stream, int dtype, int B, int K,
+                                     int V, const specverify_filter *target_filter,
+                                     const specverify_filter *draft_filter,
+                                     const void *target_logits, const void *draft_logits,
+                                     const int32_t *draft_tokens, const float *uniforms,
+                                     int32_t *accepted_len, int32_t *out_tokens, float *out_probs);
+
+/*
+ * Pages of a key-value cache around a verify step.  A cache handle describes pages of page_tokens
+ * tokens: num_pools arrays (keys and values of each layer, say) of num_pages pages of page_bytes
+ * bytes, page p of pool i at pools[i] + p * page_bytes, and the state, four int32 device arrays
+ * that the caller owns, fills before the first call and may read or write between calls:
+ *   refs [num_pages]                holders of each page; a page is free exactly when it is 0
+ *   tables [num_seqs][max_blocks]   a sequence's pages in order, -1 from entry blocks[seq] on
+ *   blocks [num_seqs]               pages held
+ *   lengths [num_seqs]              tokens held, at most blocks * page_tokens
+ * An empty cache is refs 0, tables -1, blocks 0, lengths 0.  Pages may have several holders.
+ *
+ * Conventions of the calls: they run on the handle's device and the given stream, only launch
+ * kernels (capturable in a HIP graph), and read lists of n entries from device memory (n = 0 does
+ * nothing).  One call may be in flight per handle.  Where `seqs` may be NULL it stands for
+ * 0..n-1.  Pages are taken lowest free id first, in list order, so that a call's result depends
+ * only on its inputs.  status [n] (or NULL) receives 0, or -1 for an entry that was refused and
+ * changed nothing: a sequence outside [0, num_seqs), named by an earlier entry of the list, or
+ * whose blocks and lengths contradict each other; or what the call names.  Page ids outside
+ * [0, num_pages) in a table are skipped.
+ * Errors: EINVAL (NULL handle or required array, n < 0, misaligned pointers), ECAPACITY (n above
+ * num_seqs; for specverify_cache_copy above num_pages), EHIP.
+ */
+typedef struct specverify_cache specverify_cache;
+
+#define SPECVERIFY_MAX_PAGES (1 << 30)
+#define SPECVERIFY_MAX_SEQS (1 << 20)
+#define SPECVERIFY_MAX_BLOCKS (1 << 20)
+#define SPECVERIFY_MAX_POOLS (1 << 16)
+#define SPECVERIFY_MAX_PAGE_BYTES (1 << 30)
+
+/*
+ * Create a cache handle on HIP device `device`.  pools is a HOST array of num_pools device
+ * addresses, read during the call; num_pools = 0 keeps books without page contents.  Allocates the
+ * handle's workspace and synchronises the device; touches neither state nor pages.
+ * Errors: EINVAL (NULL pointers, sizes < 1, page_bytes not a positive multiple of 16, pools not
+ * 16-byte aligned), ECAPACITY (a size above the limits, max_blocks * page_tokens above 2^31 - 1),
+ * EHIP, ENOMEM.
+ */
+int specverify_cache_create(specverify_cache **out, int device, int num_pages, int page_tokens,
+                            int num_seqs, int max_blocks, int num_pools, int64_t page_bytes,
+                            void *const *pools, int32_t *refs, int32_t *tables, int32_t *blocks,
+                            int32_t *lengths);
+
+/* Bytes of device workspace the handle holds. */
+int64_t specverify_cache_workspace_bytes(const specverify_cache *cache);
+
+/* Release the handle and its workspace, not the state or the pages.  NULL-safe. */
+int specverify_cache_destroy(specverify_cache *cache);
+
+/*
+ * Make room: sequence seqs[i] will hold pages for lengths + counts[i] tokens (K + 1 places before
+ * a verify; the prompt's before a prefill), and if counts[i] > 0 and the partly filled page it
+ * will write into has other holders, a page of its own with the same contents.  Lengths stay.
+ * What is shared is decided by the state before the call: of two listed holders of one page each
+ * gets a copy.  Refused besides: counts[i] < 0, more than max_blocks pages, or more pages asked
+ * for up to this entry than are free.
+ */
+int specverify_cache_reserve(specverify_cache *cache, void *hip_stream, int n, const int32_t *seqs,
+                             const int32_t *counts, int32_t *status);
+
+/*
+ * After a verify: lengths[seqs[i]] grows by accepted_len[i] + 1 (the token fed before the drafts
+ * and the accepted drafts; the emitted replacement is fed next) and the pages past it are
+ * released.  accepted_len is what specverify_run_* wrote; its -1 only releases.  After a prefill
+ * of c tokens accepted_len is c - 1.  Refused besides: accepted_len < -1, or a length past the
+ * pages held.
+ */
+int specverify_cache_commit(specverify_cache *cache, void *hip_stream, int n, const int32_t *seqs,
+                            const int32_t *accepted_len, int32_t *status);
+
+/*
+ * children[i], an empty sequence, becomes a copy of parents[i]: the full pages get one holder
+ * more, a partly filled last page is copied into a page of the child's own.  Pages that the parent
+ * holds past its length stay the parent's.  Many children may name one parent.  Refused besides: a
+ * parent outside [0, num_seqs), a child that is its own parent or holds anything, or more pages
+ * asked for up to this entry than are free.  `children` are the list's sequences.
+ */
+int specverify_cache_fork(specverify_cache *cache, void *hip_stream, int n, const int32_t *parents,
+                          const int32_t *children, int32_t *status);
+
+/*
+ * Empty the sequences seqs[i] with keep[i] == 0 (keep NULL: all), releasing their pages; `keep` is
+ * what specverify_quantile_cut wrote.  Sequences out of range are skipped, one named twice is
+ * emptied if any entry says so.
+ */
+int specverify_cache_free(specverify_cache *cache, void *hip_stream, int n, const int32_t *seqs,
+                          const uint8_t *keep);
+
+/*
+ * Move pages so that the U pages in use become 0..U-1: the i-th page in use at or past U moves to
+ * the i-th free page below U, in every pool, with its references and the tables that name it.
+ * page_map [num_pages] (or NULL) receives each page's new id, -1 for pages that were free;
+ * num_used [1] (or NULL) receives U.
+ */
+int specverify_cache_compact(specverify_cache *cache, void *hip_stream, int32_t *page_map,
+                             int32_t *num_used);
+
+/*
+ * Copy the contents of page src[i] to page dst[i] in every pool; references and tables stay.
+ * Refused: ids outside [0, num_pages), a destination that an earlier entry names, a source that
+ * any entry names as its destination.
+ */
+int specverify_cache_copy(specverify_cache *cache, void *hip_stream, int n, const int32_t *src,
+                          const int32_t *dst, int32_t *status);
+
+/*
  * Test hook: flags that force draw paths which data rarely reaches, so that tests can compare
  * them with a reference.  Normal callers never set them (a new context has 0).
  *   SPECVERIFY_TEST_CHUNK_FALLBACK  a draw from p_L alone (the bonus draw, the sampler) skips

@@ -29,6 +29,11 @@ SPECVERIFY_MAX_VOCAB = 1 << 20
 SPECVERIFY_STATIC_SCRATCH_BYTES = 4 << 20
 SPECVERIFY_MAX_CUT_N = 8192
 SPECVERIFY_NUM_KERNELS = 7
+SPECVERIFY_MAX_PAGES = 1 << 30
+SPECVERIFY_MAX_SEQS = 1 << 20
+SPECVERIFY_MAX_BLOCKS = 1 << 20
+SPECVERIFY_MAX_POOLS = 1 << 16
+SPECVERIFY_MAX_PAGE_BYTES = 1 << 30
 SPECVERIFY_TEST_CHUNK_FALLBACK = 1
 SPECVERIFY_TEST_EXACT_TWO_PASS = 2
 KERNEL_NAMES = ("row_stats", "accept_draw", "row_argmax", "greedy_emit", "quantile_cut",
@@ -36,6 +41,21 @@ KERNEL_NAMES = ("row_stats", "accept_draw", "row_argmax", "greedy_emit", "quanti
 
 _lib = None
 _lock = threading.Lock()
+
+
+class SpecVerifyFilter(ctypes.Structure):
+    """Per-row parameters of a cut law: device tensors (or addresses), None for what cuts nothing.
+    The tensors are held for as long as the filter lives."""
+    _fields_ = [(name, ctypes.c_void_p) for name in ("temperature", "top_k", "top_p", "min_p")]
+
+    def __init__(self, temperature=None, top_k=None, top_p=None, min_p=None):
+        self.tensors = {"temperature": temperature, "top_k": top_k, "top_p": top_p, "min_p": min_p}
+        super().__init__(*(_ptr(t) for t in self.tensors.values()))
+
+    def check(self, count: int):
+        """The tensors' types and sizes against a call of `count` rows or sequences."""
+        for name, t in self.tensors.items():
+            _arr(t, count, "i32" if name == "top_k" else "f32", name)
 
 
 class SpecVerifyError(RuntimeError):
@@ -89,6 +109,21 @@ def load():
         lib.specverify_run_greedy_heads.restype = i
         lib.specverify_quantile_cut.argtypes = [vp, vp, i, i, f, vp, vp, vp, vp]
         lib.specverify_quantile_cut.restype = i
+        flt = ctypes.POINTER(SpecVerifyFilter)
+        lib.specverify_sample_filtered.argtypes = [vp, vp, i, i, i, i64, flt, vp, vp, vp, vp]
+        lib.specverify_run_sampling_filtered.argtypes = [vp, vp, i, i, i, i, flt, flt, vp, vp, vp,
+                                                         vp, vp, vp, vp]
+        lib.specverify_cache_create.argtypes = [ctypes.POINTER(vp), i, i, i, i, i, i, i64,
+                                                ctypes.POINTER(vp), vp, vp, vp, vp]
+        lib.specverify_cache_workspace_bytes.argtypes = [vp]
+        lib.specverify_cache_workspace_bytes.restype = i64
+        lib.specverify_cache_destroy.argtypes = [vp]
+        lib.specverify_cache_reserve.argtypes = [vp, vp, i, vp, vp, vp]
+        lib.specverify_cache_commit.argtypes = [vp, vp, i, vp, vp, vp]
+        lib.specverify_cache_fork.argtypes = [vp, vp, i, vp, vp, vp]
+        lib.specverify_cache_free.argtypes = [vp, vp, i, vp, vp]
+        lib.specverify_cache_compact.argtypes = [vp, vp, vp, vp]
+        lib.specverify_cache_copy.argtypes = [vp, vp, i, vp, vp, vp]
         lib.specverify_set_test_flags.argtypes = [vp, ctypes.c_uint]
         lib.specverify_set_test_flags.restype = i
         lib.specverify_destroy.argtypes = [vp]
@@ -288,6 +323,109 @@ def specverify_quantile_cut(ctx, stream, P, N, alpha, scores, r_cut, keep, n_kee
         *_ptrs((scores, P * N, "f32", "scores"), (r_cut, P, "f32", "r_cut"),
                (keep, P * N, "u8", "keep"), (n_keep, P, "i32", "n_keep"))),
         "specverify_quantile_cut")
+
+
+def _filter(f, count: int):
+    if f is None:
+        return None
+    f.check(count)
+    return ctypes.byref(f)
+
+
+def specverify_sample_filtered(ctx, stream, dtype, N, V, row_stride, filter, logits, uniforms,
+                               out_tokens, out_probs=None) -> None:
+    """logits: a contiguous tensor, or an [N, V] tensor of unit column stride and row stride
+    row_stride."""
+    span = (N - 1) * row_stride + V if N > 0 else 0
+    if hasattr(logits, "data_ptr") and not logits.is_contiguous():
+        if logits.dim() != 2 or logits.stride() != (row_stride, 1) or logits.shape != (N, V):
+            raise ValueError("logits: expected [%d, %d] with strides (%d, 1), got %s with strides %s"
+                             % (N, V, row_stride, tuple(logits.shape), logits.stride()))
+        _arr(logits, 0, dtype, "logits")
+        if not logits.is_cuda:
+            raise ValueError("expected a device tensor, got one on %s" % logits.device)
+        x = logits.data_ptr()
+    else:
+        x, = _ptrs((logits, span, dtype, "logits"))
+    _check(load().specverify_sample_filtered(
+        ctx, _stream(stream), dtype, N, V, row_stride, _filter(filter, N), x,
+        *_ptrs((uniforms, N, "f32", "uniforms"), (out_tokens, N, "i32", "out_tokens"),
+               (out_probs, N, "f32", "out_probs"))), "specverify_sample_filtered")
+
+
+def specverify_run_sampling_filtered(ctx, stream, dtype, B, K, V, target_filter, draft_filter,
+                                     target_logits, draft_logits, draft_tokens, uniforms,
+                                     accepted_len, out_tokens, out_probs=None) -> None:
+    ptrs = _verify_args(dtype, B, K, V, target_logits, draft_logits, draft_tokens, uniforms,
+                        accepted_len, out_tokens, out_probs, K)
+    _check(load().specverify_run_sampling_filtered(ctx, _stream(stream), dtype, B, K, V,
+                                                   _filter(target_filter, B),
+                                                   _filter(draft_filter, B), *ptrs),
+           "specverify_run_sampling_filtered")
+
+
+def specverify_cache_create(device, num_pages, page_tokens, num_seqs, max_blocks, page_bytes, pools,
+                            refs, tables, blocks, lengths) -> int:
+    """Returns the handle (an int).  pools: a sequence of device tensors (or addresses) of
+    num_pages * page_bytes bytes each.  The caller keeps pools and state alive while the handle
+    lives."""
+    for p in pools:
+        if hasattr(p, "data_ptr") and p.numel() * p.element_size() < num_pages * page_bytes:
+            raise ValueError("pools: needs at least %d bytes, has %d"
+                             % (num_pages * page_bytes, p.numel() * p.element_size()))
+    state = _ptrs((refs, num_pages, "i32", "refs"), (tables, num_seqs * max_blocks, "i32", "tables"),
+                  (blocks, num_seqs, "i32", "blocks"), (lengths, num_seqs, "i32", "lengths"))
+    arr = (ctypes.c_void_p * max(len(pools), 1))(*(_ptr(p) for p in pools))
+    h = ctypes.c_void_p()
+    _check(load().specverify_cache_create(ctypes.byref(h), device, num_pages, page_tokens, num_seqs,
+                                          max_blocks, len(pools), page_bytes, arr, *state),
+           "specverify_cache_create")
+    return h.value
+
+
+def specverify_cache_workspace_bytes(cache: int) -> int:
+    return int(load().specverify_cache_workspace_bytes(cache))
+
+
+def specverify_cache_destroy(cache) -> None:
+    _check(load().specverify_cache_destroy(cache), "specverify_cache_destroy")
+
+
+def _cache_call(name, cache, stream, n, *lists):
+    _check(getattr(load(), name)(cache, _stream(stream), n, *_ptrs(*lists)), name)
+
+
+def specverify_cache_reserve(cache, stream, n, seqs, counts, status=None) -> None:
+    _cache_call("specverify_cache_reserve", cache, stream, n, (seqs, n, "i32", "seqs"),
+                (counts, n, "i32", "counts"), (status, n, "i32", "status"))
+
+
+def specverify_cache_commit(cache, stream, n, seqs, accepted_len, status=None) -> None:
+    _cache_call("specverify_cache_commit", cache, stream, n, (seqs, n, "i32", "seqs"),
+                (accepted_len, n, "i32", "accepted_len"), (status, n, "i32", "status"))
+
+
+def specverify_cache_fork(cache, stream, n, parents, children, status=None) -> None:
+    _cache_call("specverify_cache_fork", cache, stream, n, (parents, n, "i32", "parents"),
+                (children, n, "i32", "children"), (status, n, "i32", "status"))
+
+
+def specverify_cache_free(cache, stream, n, seqs=None, keep=None) -> None:
+    _cache_call("specverify_cache_free", cache, stream, n, (seqs, n, "i32", "seqs"),
+                (keep, n, "u8", "keep"))
+
+
+def specverify_cache_compact(cache, stream, page_map=None, num_used=None) -> None:
+    """The arrays' sizes are the caller's to guarantee: num_pages and 1."""
+    _check(load().specverify_cache_compact(cache, _stream(stream),
+                                           *_ptrs((page_map, 0, "i32", "page_map"),
+                                                  (num_used, 1, "i32", "num_used"))),
+           "specverify_cache_compact")
+
+
+def specverify_cache_copy(cache, stream, n, src, dst, status=None) -> None:
+    _cache_call("specverify_cache_copy", cache, stream, n, (src, n, "i32", "src"),
+                (dst, n, "i32", "dst"), (status, n, "i32", "status"))
 
 
 def specverify_set_test_flags(ctx, flags: int) -> None:

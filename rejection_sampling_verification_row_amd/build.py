@@ -13,8 +13,10 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libspecverify.so")
-SOURCES = [os.path.join(CSRC, "sv_kernels.hip"), os.path.join(CSRC, "specverify.cpp")]
-HEADERS = [os.path.join(CSRC, "sv_internal.h"), os.path.join(INCLUDE, "specverify.h")]
+SOURCES = [os.path.join(CSRC, f) for f in ("sv_kernels.hip", "sv_filter.hip", "sv_cache.hip",
+                                           "specverify.cpp")]
+HEADERS = [os.path.join(CSRC, "sv_internal.h"), os.path.join(CSRC, "sv_device.h"),
+           os.path.join(INCLUDE, "specverify.h")]
 
 ARCH = "gfx950"
 FLAGS = [

@@ -29,6 +29,14 @@ struct specverify_ctx {
     std::vector<unsigned> launched;       // per recorded call: bit k = kernel kind k ran
 };
 
+struct specverify_cache {
+    int device;
+    int num_cus;
+    void *mem;
+    size_t bytes;
+    sv::CacheView view;
+};
+
 namespace {
 
 constexpr int NK = SPECVERIFY_NUM_KERNELS;
@@ -161,6 +169,43 @@ int run_sampling_like(specverify_ctx *ctx, void *stream, int mode, int dtype, in
     }
     note_call(ctx, ev, kinds);
     return e == hipSuccess ? SPECVERIFY_OK : SPECVERIFY_EHIP;
+}
+
+sv::FilterPtrs filter_ptrs(const specverify_filter *f)
+{
+    sv::FilterPtrs p = {nullptr, nullptr, nullptr, nullptr};
+    if (f) {
+        p.temperature = f->temperature;
+        p.top_k = f->top_k;
+        p.top_p = f->top_p;
+        p.min_p = f->min_p;
+    }
+    return p;
+}
+
+bool filter_aligned(const sv::FilterPtrs &p)
+{
+    return aligned_to(p.temperature, 4) && aligned_to(p.top_k, 4) && aligned_to(p.top_p, 4) &&
+           aligned_to(p.min_p, 4);
+}
+
+// The checks of a call over a list of n entries, at most `most`: OK to go on, or 1 for nothing
+// to do.
+int cache_check(const specverify_cache *cache, int n, int most)
+{
+    if (!cache || n < 0)
+        return SPECVERIFY_EINVAL;
+    if (n > most)
+        return SPECVERIFY_ECAPACITY;
+    return n == 0 ? 1 : SPECVERIFY_OK;
+}
+
+template <typename F> int cache_launch(const specverify_cache *cache, F f)
+{
+    DeviceGuard g(cache->device);
+    if (g.err != hipSuccess)
+        return SPECVERIFY_EHIP;
+    return f() == hipSuccess ? SPECVERIFY_OK : SPECVERIFY_EHIP;
 }
 
 }  // namespace
@@ -506,6 +551,265 @@ int specverify_quantile_cut(specverify_ctx *ctx, void *hip_stream, int P, int N,
     return e == hipSuccess ? SPECVERIFY_OK : SPECVERIFY_EHIP;
 }
 
+int specverify_sample_filtered(specverify_ctx *ctx, void *hip_stream, int dtype, int N, int V,
+                               int64_t row_stride, const specverify_filter *filter,
+                               const void *logits, const float *uniforms, int32_t *out_tokens,
+                               float *out_probs)
+{
+    int rc = check_common(ctx, dtype, N, 0, V);
+    if (rc != SPECVERIFY_OK)
+        return rc;
+    // the last row's offset in bytes must fit 63 bits
+    if (row_stride < V || row_stride > INT64_MAX / 4 / ((int64_t)N + 1))
+        return SPECVERIFY_EINVAL;
+    if ((size_t)N * sv::FILTER_WG > MAX_ITEMS)
+        return SPECVERIFY_ECAPACITY;
+    if (N == 0)
+        return SPECVERIFY_OK;
+    if (!logits || !uniforms || !out_tokens)
+        return SPECVERIFY_EINVAL;
+    const sv::FilterPtrs f = filter_ptrs(filter);
+    const size_t es = dtype == SPECVERIFY_BF16 ? 2 : 4;
+    if (!aligned_to(logits, es) || !aligned_to(uniforms, 4) || !aligned_to(out_tokens, 4) ||
+        !aligned_to(out_probs, 4) || !filter_aligned(f))
+        return SPECVERIFY_EINVAL;
+    DeviceGuard g(ctx->device);
+    if (g.err != hipSuccess)
+        return SPECVERIFY_EHIP;
+    hipEvent_t *ev = next_events(ctx);
+    sv::Launch ln{static_cast<hipStream_t>(hip_stream), ev, ctx->prof_mask};
+    hipError_t e = sv::launch_filter_sample(ln, dtype, N, V, row_stride, f, logits, uniforms,
+                                            out_tokens, out_probs);
+    note_call(ctx, ev, 1u << sv::KIND_TAIL);
+    return e == hipSuccess ? SPECVERIFY_OK : SPECVERIFY_EHIP;
+}
+
+int specverify_run_sampling_filtered(specverify_ctx *ctx, void *hip_stream, int dtype, int B, int K,
+                                     int V, const specverify_filter *target_filter,
+                                     const specverify_filter *draft_filter,
+                                     const void *target_logits, const void *draft_logits,
+                                     const int32_t *draft_tokens, const float *uniforms,
+                                     int32_t *accepted_len, int32_t *out_tokens, float *out_probs)
+{
+    int rc = check_common(ctx, dtype, B, K, V);
+    if (rc != SPECVERIFY_OK)
+        return rc;
+    // one workgroup per row
+    if ((size_t)B * (2 * (size_t)K + 1) * sv::FILTER_WG > MAX_ITEMS)
+        return SPECVERIFY_ECAPACITY;
+    if (B == 0)
+        return SPECVERIFY_OK;
+    if (!target_logits || !uniforms || !accepted_len || !out_tokens ||
+        (K > 0 && (!draft_logits || !draft_tokens)))
+        return SPECVERIFY_EINVAL;
+    const sv::FilterPtrs ft = filter_ptrs(target_filter);
+    const sv::FilterPtrs fd = draft_filter ? filter_ptrs(draft_filter) : ft;
+    const size_t es = dtype == SPECVERIFY_BF16 ? 2 : 4;
+    if (!aligned_to(target_logits, es) || !aligned_to(draft_logits, es) ||
+        !aligned_to(draft_tokens, 4) || !aligned_to(uniforms, 4) || !aligned_to(accepted_len, 4) ||
+        !aligned_to(out_tokens, 4) || !aligned_to(out_probs, 4) || !filter_aligned(ft) ||
+        !filter_aligned(fd))
+        return SPECVERIFY_EINVAL;
+    DeviceGuard g(ctx->device);
+    if (g.err != hipSuccess)
+        return SPECVERIFY_EHIP;
+    hipEvent_t *ev = next_events(ctx);
+    sv::Launch ln{static_cast<hipStream_t>(hip_stream), ev, ctx->prof_mask};
+    hipError_t e = sv::launch_filter_verify(ln, ctx->ws, dtype, B, K, V, ft, fd, target_logits,
+                                            draft_logits, draft_tokens, uniforms, accepted_len,
+                                            out_tokens, out_probs);
+    note_call(ctx, ev, (1u << sv::KIND_STATS) | (1u << sv::KIND_TAIL));
+    return e == hipSuccess ? SPECVERIFY_OK : SPECVERIFY_EHIP;
+}
+
+int specverify_cache_create(specverify_cache **out, int device, int num_pages, int page_tokens,
+                            int num_seqs, int max_blocks, int num_pools, int64_t page_bytes,
+                            void *const *pools, int32_t *refs, int32_t *tables, int32_t *blocks,
+                            int32_t *lengths)
+{
+    if (!out)
+        return SPECVERIFY_EINVAL;
+    *out = nullptr;
+    if (num_pages < 1 || page_tokens < 1 || num_seqs < 1 || max_blocks < 1 || num_pools < 0 ||
+        !refs || !tables || !blocks || !lengths || !aligned_to(refs, 4) || !aligned_to(tables, 4) ||
+        !aligned_to(blocks, 4) || !aligned_to(lengths, 4))
+        return SPECVERIFY_EINVAL;
+    if (num_pools > 0 && (page_bytes < 16 || page_bytes % 16 != 0 || !pools))
+        return SPECVERIFY_EINVAL;
+    for (int i = 0; i < num_pools; ++i)
+        if (!pools[i] || !aligned_to(pools[i], 16))
+            return SPECVERIFY_EINVAL;
+    if (num_pages > SPECVERIFY_MAX_PAGES || num_seqs > SPECVERIFY_MAX_SEQS ||
+        max_blocks > SPECVERIFY_MAX_BLOCKS || num_pools > SPECVERIFY_MAX_POOLS ||
+        (int64_t)max_blocks * page_tokens > INT32_MAX || page_bytes > INT64_MAX / num_pages / 2 ||
+        page_bytes > SPECVERIFY_MAX_PAGE_BYTES)
+        return SPECVERIFY_ECAPACITY;
+    int ndev = 0;
+    if (hipGetDeviceCount(&ndev) != hipSuccess || device < 0 || device >= ndev)
+        return SPECVERIFY_EHIP;
+    DeviceGuard g(device);
+    if (g.err != hipSuccess)
+        return SPECVERIFY_EHIP;
+    int cus = 0;
+    if (hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, device) != hipSuccess ||
+        cus < 1)
+        return SPECVERIFY_EHIP;
+
+    const size_t both = (size_t)std::max(num_seqs, num_pages);
+    const size_t b_pools = align_up((size_t)std::max(num_pools, 1) * sizeof(void *));
+    const size_t b_both = align_up(both * sizeof(int));
+    const size_t b_pages = align_up((size_t)num_pages * sizeof(int));
+    const size_t b_seqs = align_up((size_t)num_seqs * sizeof(int));
+    const size_t total = b_pools + 3 * b_both + 2 * b_pages + 2 * b_seqs + align_up(sizeof(int));
+    specverify_cache *c = new (std::nothrow) specverify_cache();
+    if (!c)
+        return SPECVERIFY_ENOMEM;
+    if (hipMalloc(&c->mem, total) != hipSuccess) {
+        delete c;
+        return SPECVERIFY_ENOMEM;
+    }
+    char *p = static_cast<char *>(c->mem);
+    auto take = [&](size_t n) {
+        char *q = p;
+        p += n;
+        return q;
+    };
+    sv::CacheView &v = c->view;
+    v.num_pages = num_pages;
+    v.page_tokens = page_tokens;
+    v.num_seqs = num_seqs;
+    v.max_blocks = max_blocks;
+    v.num_pools = num_pools;
+    v.page_bytes = num_pools > 0 ? page_bytes : 0;
+    v.refs = refs;
+    v.tables = tables;
+    v.blocks = blocks;
+    v.lengths = lengths;
+    char *dpools = take(b_pools);
+    v.pools = reinterpret_cast<char *const *>(dpools);
+    v.owner = reinterpret_cast<int *>(take(b_both));
+    v.src = reinterpret_cast<int *>(take(b_both));
+    v.dst = reinterpret_cast<int *>(take(b_both));
+    v.free_ids = reinterpret_cast<int *>(take(b_pages));
+    v.map = reinterpret_cast<int *>(take(b_pages));
+    v.off = reinterpret_cast<int *>(take(b_seqs));
+    v.len = reinterpret_cast<int *>(take(b_seqs));
+    v.count = reinterpret_cast<int *>(take(align_up(sizeof(int))));
+    c->device = device;
+    c->num_cus = cus;
+    c->bytes = total;
+    if ((num_pools > 0 && hipMemcpy(dpools, pools, (size_t)num_pools * sizeof(void *),
+                                    hipMemcpyHostToDevice) != hipSuccess) ||
+        sv::launch_cache_init(nullptr, v) != hipSuccess || hipDeviceSynchronize() != hipSuccess) {
+        (void)hipFree(c->mem);
+        delete c;
+        return SPECVERIFY_EHIP;
+    }
+    *out = c;
+    return SPECVERIFY_OK;
+}
+
+int64_t specverify_cache_workspace_bytes(const specverify_cache *cache)
+{
+    return cache ? (int64_t)cache->bytes : 0;
+}
+
+int specverify_cache_destroy(specverify_cache *cache)
+{
+    if (!cache)
+        return SPECVERIFY_OK;
+    {
+        DeviceGuard g(cache->device);
+        if (cache->mem)
+            (void)hipFree(cache->mem);
+    }
+    delete cache;
+    return SPECVERIFY_OK;
+}
+
+int specverify_cache_reserve(specverify_cache *cache, void *hip_stream, int n, const int32_t *seqs,
+                             const int32_t *counts, int32_t *status)
+{
+    const int rc = cache_check(cache, n, cache ? cache->view.num_seqs : 0);
+    if (rc != SPECVERIFY_OK)
+        return rc == 1 ? SPECVERIFY_OK : rc;
+    if (!counts || !aligned_to(seqs, 4) || !aligned_to(counts, 4) || !aligned_to(status, 4))
+        return SPECVERIFY_EINVAL;
+    return cache_launch(cache, [&] {
+        return sv::launch_cache_reserve(static_cast<hipStream_t>(hip_stream), cache->view,
+                                        cache->num_cus, n, seqs, counts, status);
+    });
+}
+
+int specverify_cache_commit(specverify_cache *cache, void *hip_stream, int n, const int32_t *seqs,
+                            const int32_t *accepted_len, int32_t *status)
+{
+    const int rc = cache_check(cache, n, cache ? cache->view.num_seqs : 0);
+    if (rc != SPECVERIFY_OK)
+        return rc == 1 ? SPECVERIFY_OK : rc;
+    if (!accepted_len || !aligned_to(seqs, 4) || !aligned_to(accepted_len, 4) ||
+        !aligned_to(status, 4))
+        return SPECVERIFY_EINVAL;
+    return cache_launch(cache, [&] {
+        return sv::launch_cache_commit(static_cast<hipStream_t>(hip_stream), cache->view, n, seqs,
+                                       accepted_len, status);
+    });
+}
+
+int specverify_cache_fork(specverify_cache *cache, void *hip_stream, int n, const int32_t *parents,
+                          const int32_t *children, int32_t *status)
+{
+    const int rc = cache_check(cache, n, cache ? cache->view.num_seqs : 0);
+    if (rc != SPECVERIFY_OK)
+        return rc == 1 ? SPECVERIFY_OK : rc;
+    if (!parents || !children || !aligned_to(parents, 4) || !aligned_to(children, 4) ||
+        !aligned_to(status, 4))
+        return SPECVERIFY_EINVAL;
+    return cache_launch(cache, [&] {
+        return sv::launch_cache_fork(static_cast<hipStream_t>(hip_stream), cache->view,
+                                     cache->num_cus, n, parents, children, status);
+    });
+}
+
+int specverify_cache_free(specverify_cache *cache, void *hip_stream, int n, const int32_t *seqs,
+                          const uint8_t *keep)
+{
+    const int rc = cache_check(cache, n, cache ? cache->view.num_seqs : 0);
+    if (rc != SPECVERIFY_OK)
+        return rc == 1 ? SPECVERIFY_OK : rc;
+    if (!aligned_to(seqs, 4))
+        return SPECVERIFY_EINVAL;
+    return cache_launch(cache, [&] {
+        return sv::launch_cache_free(static_cast<hipStream_t>(hip_stream), cache->view, n, seqs,
+                                     keep);
+    });
+}
+
+int specverify_cache_compact(specverify_cache *cache, void *hip_stream, int32_t *page_map,
+                             int32_t *num_used)
+{
+    if (!cache || !aligned_to(page_map, 4) || !aligned_to(num_used, 4))
+        return SPECVERIFY_EINVAL;
+    return cache_launch(cache, [&] {
+        return sv::launch_cache_compact(static_cast<hipStream_t>(hip_stream), cache->view,
+                                        cache->num_cus, page_map, num_used);
+    });
+}
+
+int specverify_cache_copy(specverify_cache *cache, void *hip_stream, int n, const int32_t *src,
+                          const int32_t *dst, int32_t *status)
+{
+    const int rc = cache_check(cache, n, cache ? cache->view.num_pages : 0);
+    if (rc != SPECVERIFY_OK)
+        return rc == 1 ? SPECVERIFY_OK : rc;
+    if (!src || !dst || !aligned_to(src, 4) || !aligned_to(dst, 4) || !aligned_to(status, 4))
+        return SPECVERIFY_EINVAL;
+    return cache_launch(cache, [&] {
+        return sv::launch_cache_copy(static_cast<hipStream_t>(hip_stream), cache->view,
+                                     cache->num_cus, n, src, dst, status);
+    });
+}
+
 int specverify_set_test_flags(specverify_ctx *ctx, unsigned flags)
 {
     if (!ctx || (flags & ~(unsigned)sv::TEST_FLAGS_ALL) != 0)
@@ -537,7 +841,7 @@ const char *specverify_strerror(int status)
     case SPECVERIFY_EUNSUPPORTED: return "unsupported dtype";
     case SPECVERIFY_ENOMEM: return "device memory allocation failed";
     case SPECVERIFY_EHIP: return "HIP runtime or launch error";
-    case SPECVERIFY_ECAPACITY: return "batch, draft length or vocabulary exceeds the context's capacity";
+    case SPECVERIFY_ECAPACITY: return "batch, draft length or vocabulary exceeds the context's capacity, or a list the cache's";
     default: return "unknown status";
     }
 }

@@ -199,6 +199,73 @@ hipError_t launch_greedy_heads(const Launch &ln, const Workspace &ws, int dtype,
 hipError_t launch_quantile_cut(const Launch &ln, int P, int N, int k, const float *scores,
                                float *r_cut, uint8_t *keep, int32_t *n_keep);
 
+constexpr int FILTER_WG = 1024;   // threads per row of a cut law, and per sequence of its verify
+
+// Per-row parameters of a cut law (device arrays, NULL: that cut is off, temperature 1).
+struct FilterPtrs {
+    const float *temperature;
+    const int *top_k;
+    const float *top_p, *min_p;
+};
+
+// A row's cut law: the ids above the cut key and, among those equal to it, the ids up to `tie`;
+// P(i) = 2^((x_i - max) c) / z there.  32 bytes, no more than a row's statistics partials, whose
+// workspace holds them.
+struct RowCut {
+    double z;        // sum of the kept weights 2^((x - max) c)
+    double c;        // log2(e) / T
+    float max;
+    uint32_t cut;    // order key
+    int tie;
+    int ok;          // 0: no law (NaN, +inf, nothing finite, or parameters out of range)
+};
+static_assert(sizeof(RowCut) <= WAVES * sizeof(float2), "a row's record must fit its partials");
+
+// one draw per row from the row's cut law
+hipError_t launch_filter_sample(const Launch &ln, int dtype, int N, int V, int64_t stride,
+                                const FilterPtrs &f, const void *logits, const float *unif,
+                                int32_t *tok, float *prob);
+// sampling verify whose target and draft laws are cut
+hipError_t launch_filter_verify(const Launch &ln, const Workspace &ws, int dtype, int B, int K,
+                                int V, const FilterPtrs &ft, const FilterPtrs &fd, const void *tgt,
+                                const void *drf, const int32_t *tokens, const float *unif,
+                                int32_t *acc, int32_t *out, float *probs);
+
+// The pages of a key-value cache: the caller's state and the handle's scratch (device arrays).
+struct CacheView {
+    int num_pages, page_tokens, num_seqs, max_blocks, num_pools;
+    int64_t page_bytes;
+    char *const *pools;  // [num_pools] base addresses
+    int *refs;           // [num_pages] holders of each page, 0 = free
+    int *tables;         // [num_seqs][max_blocks] page ids, -1 past a sequence's blocks
+    int *blocks;         // [num_seqs] pages held
+    int *lengths;        // [num_seqs] tokens
+    // scratch
+    int *owner;          // [max(num_seqs, num_pages)] first list entry naming an id; INT_MAX between calls
+    int *free_ids;       // [num_pages] the free pages a call takes, ascending
+    int *off;            // [num_seqs] an entry's first place in free_ids, -1 refused
+    int *len;            // [num_seqs] an entry's length at the start of the call
+    int *src, *dst;      // [max(num_seqs, num_pages)] pages to copy, -1 none
+    int *map;            // [num_pages] a compaction's new page ids
+    int *count;          // number of src / dst entries of a compaction
+};
+
+constexpr int CACHE_NO_OWNER = 0x7fffffff;
+
+hipError_t launch_cache_init(hipStream_t st, const CacheView &c);
+hipError_t launch_cache_reserve(hipStream_t st, const CacheView &c, int cus, int n, const int *seqs,
+                                const int *counts, int *status);
+hipError_t launch_cache_commit(hipStream_t st, const CacheView &c, int n, const int *seqs,
+                               const int *accepted, int *status);
+hipError_t launch_cache_fork(hipStream_t st, const CacheView &c, int cus, int n,
+                             const int *parents, const int *children, int *status);
+hipError_t launch_cache_free(hipStream_t st, const CacheView &c, int n, const int *seqs,
+                             const uint8_t *keep);
+hipError_t launch_cache_compact(hipStream_t st, const CacheView &c, int cus, int *page_map,
+                                int *num_used);
+hipError_t launch_cache_copy(hipStream_t st, const CacheView &c, int cus, int n, const int *src,
+                             const int *dst, int *status);
+
 // The workspace of the entry point that allocates nothing: a file-scope device array of
 // STATIC_SCRATCH_BYTES per device (see static_scratch in the kernels' source).
 constexpr size_t STATIC_SCRATCH_BYTES = size_t(4) << 20;

@@ -19,7 +19,8 @@ CSRC="$ROOT/rejection_sampling_verification_row_amd/csrc"
     -Xarch_host -fsanitize=address -Xarch_host -fsanitize=undefined \
     -Xarch_host -fno-sanitize-recover=undefined -Xarch_host -shared-libsan \
     -Xarch_host -fno-omit-frame-pointer \
-    -I"$ROOT/include" -I"$CSRC" "$CSRC/sv_kernels.hip" "$CSRC/specverify.cpp" \
+    -I"$ROOT/include" -I"$CSRC" "$CSRC/sv_kernels.hip" "$CSRC/sv_filter.hip" "$CSRC/sv_cache.hip" \
+    "$CSRC/specverify.cpp" \
     -o "$OUT/libspecverify.so" 2>&1 | grep -v "packed-fp32-ops" || true
 test -s "$OUT/libspecverify.so"
 RT="$(ls "$LLVM"/lib/clang/*/lib/linux/libclang_rt.asan-x86_64.so | head -1)"
