@@ -208,16 +208,22 @@ struct FilterPtrs {
     const float *top_p, *min_p;
 };
 
-// A row's cut law: the ids above the cut key and, among those equal to it, the ids up to `tie`;
+// A row's cut law: the ids above the cut key and, among those equal to it, the lowest ids;
 // P(i) = 2^((x_i - max) c) / z there.  32 bytes, no more than a row's statistics partials, whose
 // workspace holds them.
+enum CutState {
+    CUT_NONE = 0,    // no law (NaN, +inf, nothing finite, or parameters out of range)
+    CUT_READY = 1,   // tie = the last id kept among those equal to the cut
+    CUT_TIES = 2,    // tie = how many of those equal to the cut are kept; which, is to be found
+    CUT_EXACT = 3    // the row needs cut_by_bisection
+};
 struct RowCut {
     double z;        // sum of the kept weights 2^((x - max) c)
     double c;        // log2(e) / T
     float max;
     uint32_t cut;    // order key
     int tie;
-    int ok;          // 0: no law (NaN, +inf, nothing finite, or parameters out of range)
+    int state;       // CutState
 };
 static_assert(sizeof(RowCut) <= WAVES * sizeof(float2), "a row's record must fit its partials");
 
