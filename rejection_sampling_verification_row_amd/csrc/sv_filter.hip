@@ -17,6 +17,8 @@
 // weights and sums are fp64.
 #include <float.h>
 
+#include <type_traits>
+
 #include "sv_device.h"
 #include "sv_internal.h"
 
@@ -24,17 +26,27 @@ namespace sv {
 
 namespace {
 
+// f(0), ..., f(N - 1) with constant arguments: arrays indexed by them stay in registers.
+template <int I, int N, typename F> __device__ __forceinline__ void unroll(F &&f)
+{
+    if constexpr (I < N) {
+        f(std::integral_constant<int, I>{});
+        unroll<I + 1, N>(f);
+    }
+}
+#define SV_INLINE __attribute__((always_inline))
+
 constexpr int FWG = FILTER_WG;
 constexpr int FWAVES = FWG / 64;
 
 // Order-preserving 32-bit key of a logit: larger value, larger key; -0 and +0 are one key.
-__device__ inline uint32_t order_key(float x)
+__device__ __forceinline__ uint32_t order_key(float x)
 {
     const uint32_t u = __float_as_uint(x == 0.0f ? 0.0f : x);
     return u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
 }
 
-__device__ inline float key_value(uint32_t k)
+__device__ __forceinline__ float key_value(uint32_t k)
 {
     return __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k);
 }
@@ -42,7 +54,34 @@ __device__ inline float key_value(uint32_t k)
 constexpr uint32_t KEY_POS_INF = 0xff800000u;   // order_key(+inf); NaNs lie above it
 constexpr uint32_t KEY_NEG_INF = 0x007fffffu;   // order_key(-inf); negative NaNs lie below it
 
-__device__ inline double weight(float x, float m, double c) { return exp2(((double)x - (double)m) * c); }
+// 2^a for a <= 0, within 2^-51: a = n + r with |r| <= 1/2, the Taylor polynomial of 2^r to r^13
+// (whose rest is below (ln 2 / 2)^14 / 14! = 2^-57), scaled by 2^n.  Half the instructions of the
+// general function, which every term of every sum would pay; 0 at and below 2^-1100.
+__device__ __forceinline__ double exp2_neg(double a)
+{
+    a = fmax(a, -1100.0);
+    const double n = rint(a), r = a - n;
+    double p = 1.3691488853904128881e-12;
+    p = fma(p, r, 2.5678435993488205142e-11);
+    p = fma(p, r, 4.4455382718708114976e-10);
+    p = fma(p, r, 7.0549116208011233299e-09);
+    p = fma(p, r, 1.0178086009239699728e-07);
+    p = fma(p, r, 1.3215486790144309488e-06);
+    p = fma(p, r, 1.5252733804059840280e-05);
+    p = fma(p, r, 1.5403530393381609954e-04);
+    p = fma(p, r, 1.3333558146428443423e-03);
+    p = fma(p, r, 9.6181291076284771620e-03);
+    p = fma(p, r, 5.5504108664821579953e-02);
+    p = fma(p, r, 2.4022650695910071233e-01);
+    p = fma(p, r, 6.9314718055994530942e-01);
+    p = fma(p, r, 1.0);
+    return ldexp(p, (int)n);
+}
+
+__device__ __forceinline__ double weight(float x, float m, double c)
+{
+    return exp2_neg(((double)x - (double)m) * c);
+}
 
 struct Params {
     double c;       // log2(e) / T
@@ -53,7 +92,7 @@ struct Params {
 
 // One row's or sequence's parameters: absent arrays cut nothing.  T = 0 is the first id of the
 // order, which is k = 1 at any temperature.
-__device__ inline Params load_params(const FilterPtrs &f, int i, int V)
+__device__ __forceinline__ Params load_params(const FilterPtrs &f, int i, int V)
 {
     Params q;
     const float T = f.temperature ? f.temperature[i] : 1.0f;
@@ -69,7 +108,7 @@ __device__ inline Params load_params(const FilterPtrs &f, int i, int V)
 }
 
 // Sum over the workgroup, the same bits in every thread (fixed order).
-template <typename T> __device__ T block_sum(T v, T *lds)
+template <typename T> __device__ __forceinline__ T block_sum(T v, T *lds)
 {
     v = wave_sum_lds(v);
     __syncthreads();
@@ -82,7 +121,7 @@ template <typename T> __device__ T block_sum(T v, T *lds)
     return s;
 }
 
-__device__ inline uint32_t block_max(uint32_t v, uint32_t *lds)
+__device__ __forceinline__ uint32_t block_max(uint32_t v, uint32_t *lds)
 {
 #pragma unroll
     for (int o = 32; o > 0; o >>= 1)
@@ -103,7 +142,7 @@ struct RedLds {
     int i[FWAVES];
 };
 
-__device__ inline bool kept(uint32_t key, int id, const RowCut &r)
+__device__ __forceinline__ bool kept(uint32_t key, int id, const RowCut &r)
 {
     return key > r.cut || (key == r.cut && id <= r.tie);
 }
@@ -111,7 +150,7 @@ __device__ inline bool kept(uint32_t key, int id, const RowCut &r)
 // The row's cut by bisection on the order keys: every step is one pass over the row that counts
 // or sums what lies above a key.  Exact for any row; 32 passes per active cut.
 template <int DT>
-__device__ RowCut cut_by_bisection(const char *row, int V, const Params &q, RedLds &lds)
+__device__ __forceinline__ RowCut cut_by_bisection(const char *row, int V, const Params &q, RedLds &lds)
 {
     RowCut r;
     const int t = threadIdx.x;
@@ -211,6 +250,66 @@ __device__ RowCut cut_by_bisection(const char *row, int V, const Params &q, RedL
     return r;
 }
 
+// ------------------------------------------------------------------ reading a row
+//
+// Group g of a row is its ids g * E .. g * E + E - 1, one 16-byte vector.  Rows start at any
+// element (an odd vocabulary, a stride), and the memory pipe takes 16-byte loads at any address,
+// so the groups count from the row's first id whatever its alignment; only the last, partial
+// group is read by elements.
+
+typedef unsigned int u32x4_any __attribute__((ext_vector_type(4), aligned(2)));
+
+template <int DT> struct Groups {
+    static constexpr int E = Elt<DT>::EPV;
+    const char *row;
+    int V, whole, per_wave;    // whole groups; units of 64 groups that each wave takes in a draw
+
+    __device__ __forceinline__ Groups(const char *r, int v) : row(r), V(v), whole(v / E)
+    {
+        per_wave = ((v + E - 1) / E + FWAVES * 64 - 1) / (FWAVES * 64);
+    }
+    __device__ __forceinline__ int group_of(int wave, int unit, int lane) const
+    {
+        return (wave * per_wave + unit) * 64 + lane;
+    }
+    __device__ __forceinline__ uint4 load_whole(int g) const
+    {
+        const u32x4_any v =
+            __builtin_nontemporal_load(reinterpret_cast<const u32x4_any *>(row + (size_t)g * 16));
+        return make_uint4(v.x, v.y, v.z, v.w);
+    }
+    // the group's logits; -inf where it has no id
+    __device__ __forceinline__ uint4 load(int g) const
+    {
+        if (g < whole)
+            return load_whole(g);
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            w[i] = DT == 1 ? 0xff80ff80u : 0xff800000u;
+        if (g == whole) {
+#pragma unroll
+            for (int k = 0; k < E; ++k) {
+                const int id = g * E + k;
+                if (id >= V)
+                    continue;
+                if constexpr (DT == 1) {
+                    const uint32_t p = reinterpret_cast<const uint16_t *>(row)[id];
+                    w[k / 2] = k & 1 ? (w[k / 2] & 0xffffu) | p << 16 : (w[k / 2] & 0xffff0000u) | p;
+                } else {
+                    w[k] = reinterpret_cast<const uint32_t *>(row)[id];
+                }
+            }
+        }
+        return make_uint4(w[0], w[1], w[2], w[3]);
+    }
+};
+
+__device__ __forceinline__ uint32_t vec_word(const uint4 &v, int i)
+{
+    return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
+}
+
 // ------------------------------------------------------------------ bfloat16: the cut by counting
 //
 // A bfloat16 row has few distinct values, so its cut comes from how often each occurs: one pass
@@ -225,55 +324,57 @@ __device__ RowCut cut_by_bisection(const char *row, int V, const Params &q, RedL
 
 constexpr uint32_t HLO = 103u << 7;        // pattern of 2^-24
 constexpr int HMAG = 4096;
-constexpr int HBINS = 2 * HMAG;            // bin = 2 * (magnitude - HLO) + sign
+constexpr int HBINS = 2 * HMAG;            // bin = sign * HMAG + magnitude - HLO: neighbouring
+                                           // magnitudes lie in neighbouring LDS banks
 constexpr int HX = 64;                     // values outside the window kept apart
-// Bins are put in order 64 at a time: tile 0 the values above the window, 1..64 the positive
-// bins, 65 the values around zero, 66..129 the negative bins.
-constexpr int NTILES = 2 * (HMAG / 64) + 2;
-constexpr int TILE_ZERO = 1 + HMAG / 64;
 
 typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
 
-__device__ inline uint32_t as_u32(u16x2 v) { return __builtin_bit_cast(uint32_t, v); }
-__device__ inline u16x2 as_u16x2(uint32_t v) { return __builtin_bit_cast(u16x2, v); }
+__device__ __forceinline__ uint32_t as_u32(u16x2 v) { return __builtin_bit_cast(uint32_t, v); }
+__device__ __forceinline__ u16x2 as_u16x2(uint32_t v) { return __builtin_bit_cast(u16x2, v); }
 
 // Two patterns less HLO; a half is inside the window exactly when its bits 12..14 are 0.
-__device__ inline uint32_t window_words(uint32_t w)
+__device__ __forceinline__ uint32_t window_words(uint32_t w)
 {
     const u16x2 lo = {(unsigned short)HLO, (unsigned short)HLO};
     return as_u32(as_u16x2(w) - lo);
 }
-// bin * 4 of both halves: magnitude in bits 3..14, sign in bit 2
-__device__ inline uint32_t bin_offsets(uint32_t t)
+// 4 * bin of both halves: magnitude in bits 2..13, sign in bit 14
+__device__ __forceinline__ uint32_t bin_offsets(uint32_t t)
 {
-    const u16x2 v = as_u16x2(t), a = {3, 3}, b = {13, 13};
-    return as_u32(v << a) | as_u32(v >> b);
+    const u16x2 two = {2, 2};
+    return as_u32(as_u16x2(t) << two) | (t >> 1 & 0x40004000u);
 }
 
-__device__ inline float pattern_value(uint32_t p) { return __uint_as_float(p << 16); }
-__device__ inline uint32_t vec_word(const uint4 &v, int i)
+__device__ __forceinline__ float pattern_value(uint32_t p) { return __uint_as_float(p << 16); }
+__device__ __forceinline__ uint32_t bin_pattern(int bin)
 {
-    return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
+    return HLO + (uint32_t)(bin & (HMAG - 1)) + (bin >= HMAG ? 0x8000u : 0u);
 }
+
+// The order of a row's values as rows of four positions to a thread, largest first: row 0 the
+// values above the window, then PR rows of positive bins, the values around zero, PR rows of
+// negative bins.  Rows 0 and PR + 1 have one position to a lane of wave 0.
+constexpr int order_rows(int wgt) { return 2 + 2 * (HMAG / (4 * wgt)); }
 
 struct CutLds {
-    uint32_t count[NTILES];        // ids per tile
-    uint32_t before[NTILES];       // ids in earlier tiles
-    double sum[NTILES];            // kept weight per tile after top-k
-    double sum_m[NTILES];          // of it the weights that pass min-p
-    float xval[2][64];             // tiles 0 and 65: values, largest first
+    uint32_t count[64];            // ids per order row and wave
+    float first[64];               // the first value there
+    double sum[64];                // kept weight there, after top-k
+    float xval[2][64];             // the values kept apart, above the window and around zero
     uint32_t xcnt[2][64];
     uint32_t xlist[HX];            // patterns outside the window as they were met
     uint32_t nx, zeros, low, bad;  // how many; zeros; largest order key <= -2^8; NaN or +inf met
-    int total, first;              // ids counted; first tile with any
-    float max;
+    int last[3];                   // last place that top-k, top-p, min-p leave something of
     RowCut cut;
 };
 
-__device__ inline void cut_lds_clear(CutLds &c)
+__device__ __forceinline__ void cut_lds_clear(CutLds &c)
 {
-    if (threadIdx.x == 0)
+    if (threadIdx.x == 0) {
         c.nx = c.zeros = c.low = c.bad = 0;
+        c.last[0] = c.last[1] = c.last[2] = -1;
+    }
 }
 
 // What a thread meets outside the window.
@@ -281,7 +382,7 @@ struct Outside {
     uint32_t zeros = 0, low = 0, bad = 0;
 };
 
-__device__ inline void count_outside(uint32_t p, CutLds &c, Outside &o)
+__device__ __forceinline__ void count_outside(uint32_t p, CutLds &c, Outside &o)
 {
     const uint32_t a = p & 0x7fffu;
     if (a == 0) {
@@ -297,23 +398,14 @@ __device__ inline void count_outside(uint32_t p, CutLds &c, Outside &o)
     }
 }
 
-__device__ inline void count_one(uint32_t p, uint32_t *hist, CutLds &c, Outside &o)
-{
-    const uint32_t t = (p - HLO) & 0xffffu;
-    if ((t & 0x7000u) == 0)
-        atomicAdd(&hist[((t & 0xfffu) << 1) | (t >> 15)], 1u);
-    else
-        count_outside(p, c, o);
-}
-
-__device__ inline void bump(uint32_t *hist, uint32_t off)
+__device__ __forceinline__ void bump(uint32_t *hist, uint32_t off)
 {
     atomicAdd(reinterpret_cast<uint32_t *>(reinterpret_cast<char *>(hist) + off), 1u);
 }
 
 // Counts eight patterns.  The common case, all lanes inside the window, takes seven VALU
 // instructions for two patterns and one LDS add for each.
-__device__ inline void count_vec(const uint4 &v, uint32_t *hist, CutLds &c, Outside &o)
+__device__ __forceinline__ void count_vec(const uint4 &v, uint32_t *hist, CutLds &c, Outside &o)
 {
     uint32_t t[4], out = 0;
 #pragma unroll
@@ -329,96 +421,51 @@ __device__ inline void count_vec(const uint4 &v, uint32_t *hist, CutLds &c, Outs
             bump(hist, b >> 16);
         }
     } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            count_one(vec_word(v, i) & 0xffffu, hist, c, o);
-            count_one(vec_word(v, i) >> 16, hist, c, o);
+        // rare, so one body for all pairs
+        uint32_t w0 = v.x, w1 = v.y, w2 = v.z, w3 = v.w;
+#pragma nounroll
+        for (int i = 0; i < 8; ++i) {
+            const uint32_t p = w0 & 0xffffu, u = window_words(p) & 0xffffu;
+            if ((u & 0x7000u) == 0)
+                bump(hist, bin_offsets(u) & 0xffffu);
+            else
+                count_outside(p, c, o);
+            w0 = __builtin_amdgcn_alignbit(w1, w0, 16);
+            w1 = __builtin_amdgcn_alignbit(w2, w1, 16);
+            w2 = __builtin_amdgcn_alignbit(w3, w2, 16);
+            w3 >>= 16;
         }
     }
 }
 
-// A row as whole 16-byte vectors, with the ids before the first and after the last one by one.
-struct RowSpan {
-    const char *row;
-    const uint4 *vec;
-    int head, nvec, tail0;     // ids before vec; vectors; first id after them
-};
-
-__device__ inline RowSpan row_span(const char *row, int V)
+__device__ __forceinline__ uint32_t wave_scan_u32(uint32_t x)
 {
-    RowSpan r;
-    r.row = row;
-    const int mis = (int)(reinterpret_cast<uintptr_t>(row) & 15);
-    r.head = min(V, mis ? (16 - mis) / 2 : 0);
-    r.vec = reinterpret_cast<const uint4 *>(row + 2 * (size_t)r.head);
-    r.nvec = (V - r.head) / 8;
-    r.tail0 = r.head + r.nvec * 8;
-    return r;
+    int v = (int)x;
+    v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, false);  // row_shr:1
+    v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, false);  // row_shr:2
+    v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, false);  // row_shr:4
+    v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, false);  // row_shr:8
+    v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false);  // row_bcast:15
+    v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false);  // row_bcast:31
+    return (uint32_t)v;
 }
 
-__device__ inline uint32_t pattern_at(const char *row, int id)
-{
-    return reinterpret_cast<const uint16_t *>(row)[id];
-}
-
-__device__ inline uint32_t wave_sum_u32(uint32_t v)
-{
-    int x = (int)v;
-    x += lane_xch<0>(x);
-    x += lane_xch<1>(x);
-    x += lane_xch<2>(x);
-    x += lane_xch<3>(x);
-    x += lane_xch<4>(x);
-    x += lane_xch<5>(x);
-    return (uint32_t)x;
-}
-
-__device__ inline uint32_t wave_scan_u32(uint32_t v)
-{
-    const int lane = threadIdx.x & 63;
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-        const uint32_t u = (uint32_t)__shfl_up((int)v, o);
-        if (lane >= o)
-            v += u;
-    }
-    return v;
-}
-
-// A tile's lane: its value, its count, and its bin (-1 outside the window).
-__device__ inline void tile_entry(int tile, const uint32_t *hist, const CutLds &c, float &x,
-                                  uint32_t &n, int &bin)
-{
-    const int lane = threadIdx.x & 63;
-    if (tile == 0 || tile == TILE_ZERO) {
-        x = c.xval[tile != 0][lane];
-        n = c.xcnt[tile != 0][lane];
-        bin = -1;
-        return;
-    }
-    const bool neg = tile > TILE_ZERO;
-    const int mag = neg ? (tile - TILE_ZERO - 1) * 64 + lane : HMAG - 1 - ((tile - 1) * 64 + lane);
-    bin = 2 * mag + (int)neg;
-    n = hist[bin];
-    x = pattern_value(HLO + (uint32_t)mag + (neg ? 0x8000u : 0u));
-}
-
-// The values kept apart, in order, into tiles 0 and 65 (wave 0).
-__device__ inline void order_outside(CutLds &c)
+// The values kept apart, in order, into xval and xcnt (wave 0).
+__device__ __forceinline__ void order_outside(CutLds &c)
 {
     const int lane = threadIdx.x & 63;
     c.xcnt[0][lane] = c.xcnt[1][lane] = 0;
     c.xval[0][lane] = c.xval[1][lane] = 0.0f;
     const int n = (int)min(c.nx, (uint32_t)HX - 1);
-    // lane n stands for the zeros
-    const float x = lane < n ? pattern_value(c.xlist[lane]) : 0.0f;
-    const uint32_t mine = lane < n ? 1u : lane == n ? c.zeros : 0u;
-    const bool high = x >= 256.0f;
     if (n == 0) {
         if (lane == 0)
             c.xcnt[1][0] = c.zeros;
         return;
     }
+    // lane n stands for the zeros; of equal values the first stands for all
+    const float x = lane < n ? pattern_value(c.xlist[lane]) : 0.0f;
+    const uint32_t mine = lane < n ? 1u : lane == n ? c.zeros : 0u;
+    const bool high = x >= 256.0f;
     uint32_t cnt = 0;
     bool first = lane <= n;
     for (int j = 0; j <= n; ++j) {
@@ -437,26 +484,51 @@ __device__ inline void order_outside(CutLds &c)
         c.xcnt[!high][rank] = cnt;
         c.xval[!high][rank] = x;
     }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
 }
 
-// What top-k leaves of a tile's counts: nothing past the first k ids.
-__device__ inline uint32_t clip_counts(uint32_t n, uint32_t before, uint32_t tile_count, int k)
+// The thread's four positions of an order row: counts, values and first bin (-1 outside the
+// window; positive bins descend from it, negative ones ascend).
+template <int WGT>
+__device__ __forceinline__ void order_entry(int row, const uint32_t *hist, const CutLds &c, uint32_t (&n)[4],
+                                   float (&x)[4], int &bin)
 {
-    if (before >= (uint32_t)k)
-        return 0;
-    if (before + tile_count <= (uint32_t)k)
-        return n;
-    const uint32_t b = before + wave_scan_u32(n) - n;
-    return b >= (uint32_t)k ? 0u : min(n, (uint32_t)k - b);
+    constexpr int PR = HMAG / (4 * WGT);
+    const int t = threadIdx.x;
+    if (row == 0 || row == PR + 1) {
+        const bool in = t < 64;
+        n[0] = in ? c.xcnt[row != 0][t & 63] : 0u;
+        x[0] = in ? c.xval[row != 0][t & 63] : 0.0f;
+        n[1] = n[2] = n[3] = 0;
+        x[1] = x[2] = x[3] = 0.0f;
+        bin = -1;
+        return;
+    }
+    const bool neg = row > PR + 1;
+    const int at = 4 * ((neg ? row - PR - 2 : row - 1) * WGT + t);
+    bin = neg ? HMAG + at : HMAG - 1 - at;
+    const uint4 q = *reinterpret_cast<const uint4 *>(hist + (neg ? bin : bin - 3));
+    n[0] = neg ? q.x : q.w;
+    n[1] = neg ? q.y : q.z;
+    n[2] = neg ? q.z : q.y;
+    n[3] = neg ? q.w : q.x;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        x[i] = pattern_value(bin_pattern(neg ? bin + i : bin - i));
 }
 
-// The cut from the counts.  NW waves; on return c.cut holds the result for all.  With `table`,
-// table[bin] receives the weight of every bin that occurs among the first k ids.
-template <int NW>
-__device__ void cut_from_counts(const uint32_t *hist, CutLds &c, const Outside &o, const Params &q,
+// The cut from the counts, by a workgroup of WGT threads; on return c.cut holds it.  Top-k, top-p
+// and min-p each leave a prefix of the order, so the cut lies in the first of the three places
+// (order row, thread) where theirs end, and there position by position.  With `table`,
+// table[bin] receives the weight of every bin that occurs and is kept, and 0 of every bin that
+// occurs and is not.
+template <int WGT>
+__device__ __forceinline__ void cut_from_counts(const uint32_t *hist, CutLds &c, const Outside &o, const Params &q,
                                 int V, double *table)
 {
-    const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
+    constexpr int NW = WGT / 64, R = order_rows(WGT);
+    static_assert(R * NW <= 64, "a lane for every order row and wave");
+    const int t = threadIdx.x, lane = t & 63, wv = t >> 6;
     if (o.zeros)
         atomicAdd(&c.zeros, o.zeros);
     if (o.low)
@@ -466,203 +538,200 @@ __device__ void cut_from_counts(const uint32_t *hist, CutLds &c, const Outside &
     __syncthreads();
     if (wv == 0)
         order_outside(c);
-    __syncthreads();
-    for (int t = wv; t < NTILES; t += NW) {
-        float x;
-        uint32_t n;
+    // wave 0 alone reads what it has just written there
+    uint32_t cnt[R], before[R];
+    unroll<0, R>([&](auto r) SV_INLINE {
+        uint32_t n[4];
+        float x[4];
         int bin;
-        tile_entry(t, hist, c, x, n, bin);
-        const uint32_t s = __ballot(n != 0) ? wave_sum_u32(n) : 0u;
-        if (lane == 0)
-            c.count[t] = s;
-    }
+        order_entry<WGT>(r, hist, c, n, x, bin);
+        cnt[r] = n[0] + n[1] + n[2] + n[3];
+        const unsigned long long has = __ballot(cnt[r] != 0);
+        uint32_t inc = 0;
+        if (has) {
+            inc = wave_scan_u32(cnt[r]);
+            if (lane == __ffsll(has) - 1)
+                c.first[r * NW + wv] = n[0] ? x[0] : n[1] ? x[1] : n[2] ? x[2] : x[3];
+        }
+        before[r] = inc - cnt[r];
+        if (lane == 63)
+            c.count[r * NW + wv] = inc;
+    });
     __syncthreads();
-    if (wv == 0) {
-        // three tiles to a lane
-        uint32_t a[3], s = 0;
-#pragma unroll
-        for (int i = 0; i < 3; ++i) {
-            a[i] = lane * 3 + i < NTILES ? c.count[lane * 3 + i] : 0u;
-            s += a[i];
-        }
-        const uint32_t inc = wave_scan_u32(s);
-        uint32_t b = inc - s;
-        int first = NTILES;
-#pragma unroll
-        for (int i = 0; i < 3; ++i) {
-            if (lane * 3 + i < NTILES)
-                c.before[lane * 3 + i] = b;
-            if (a[i] && first == NTILES)
-                first = lane * 3 + i;
-            b += a[i];
-        }
-        const unsigned long long any = __ballot(first != NTILES);
-        const int t0 = any ? __shfl(first, __ffsll(any) - 1) : 0;
-        float x;
-        uint32_t n;
-        int bin;
-        tile_entry(t0, hist, c, x, n, bin);
-        const unsigned long long has = __ballot(n != 0);
-        x = __shfl(x, has ? __ffsll(has) - 1 : 0);
-        const int total = __shfl((int)inc, 63);
-        if (lane == 0) {
-            c.total = total;
-            c.first = t0;
-            c.max = x;
-            RowCut r;
-            r.z = 0.0;
-            r.c = q.c;
-            r.max = x;
-            r.cut = KEY_NEG_INF;
-            r.tie = V;
-            r.state = CUT_READY;
-            if (!q.ok || c.bad || (total == 0 && c.low == 0)) {
-                r.state = CUT_NONE;
-            } else if (c.nx >= HX || total == 0) {
-                r.state = CUT_EXACT;
-            } else if (c.low) {
-                // the low values count if one of them could be kept with a weight that matters
-                const double w = weight(key_value(c.low), x, q.c);
-                if (w > 0.0 && (w >= 0x1p-80 || (q.k < V && q.k > total) || (q.m > 0.0 && w >= q.m)))
-                    r.state = CUT_EXACT;
-            }
-            c.cut = r;
-        }
+    const uint32_t mine = lane < R * NW ? c.count[lane] : 0u;
+    const uint32_t inc = wave_scan_u32(mine);
+    const uint32_t total = (uint32_t)lane_value((int)inc, 63);
+    const unsigned long long some = __ballot(mine != 0);
+    const float M = some ? c.first[__ffsll(some) - 1] : 0.0f;
+    unroll<0, R>([&](auto r) SV_INLINE {
+        before[r] += (uint32_t)lane_value((int)(inc - mine), r * NW + __builtin_amdgcn_readfirstlane(wv));
+    });
+    RowCut cut;
+    cut.z = 0.0;
+    cut.c = q.c;
+    cut.max = M;
+    cut.cut = KEY_NEG_INF;
+    cut.tie = V;
+    cut.state = CUT_READY;
+    if (!q.ok || c.bad || (total == 0 && c.low == 0)) {
+        cut.state = CUT_NONE;
+    } else if (c.nx >= HX || total == 0) {
+        cut.state = CUT_EXACT;
+    } else if (c.low) {
+        // the low values count if one of them could be kept with a weight that matters
+        const double w = weight(key_value(c.low), M, q.c);
+        if (w > 0.0 && (w >= 0x1p-80 || (q.k < V && q.k > (int)total) || (q.m > 0.0 && w >= q.m)))
+            cut.state = CUT_EXACT;
     }
-    __syncthreads();
-    if (c.cut.state != CUT_READY)
+    if (cut.state != CUT_READY) {
+        if (t == 0)
+            c.cut = cut;
+        __syncthreads();
         return;
-    const float M = c.max;
-    const int total = c.total, k = min(q.k, total);
-    for (int t = wv; t < NTILES; t += NW) {
-        const uint32_t cnt = c.count[t], b = c.before[t];
-        double s = 0.0, sm = 0.0;
-        if (cnt && b < (uint32_t)k) {
-            float x;
-            uint32_t n;
-            int bin;
-            tile_entry(t, hist, c, x, n, bin);
-            const uint32_t left = clip_counts(n, b, cnt, k);
-            const double w = left ? weight(x, M, q.c) : 0.0;
-            if (table && left && bin >= 0)
-                table[bin] = w;
-            s = wave_sum((double)left * w);
-            sm = q.m > 0.0 ? wave_sum(w >= q.m ? (double)left * w : 0.0) : s;
-        }
-        if (lane == 0) {
-            c.sum[t] = s;
-            c.sum_m[t] = sm;
-        }
     }
+    const uint32_t k = min((uint32_t)q.k, total);
+    double sum[R];
+    uint32_t passes = 0;       // bit r: min-p leaves something of the thread's positions in row r
+    unroll<0, R>([&](auto r) SV_INLINE {
+        sum[r] = 0.0;
+        const bool in = cnt[r] != 0 && before[r] < k;
+        if (__ballot(cnt[r] != 0) == 0) {
+            if (lane == 63)
+                c.sum[r * NW + wv] = 0.0;
+            return;
+        }
+        if (__ballot(in) != 0) {
+            uint32_t n[4];
+            float x[4];
+            int bin;
+            order_entry<WGT>(r, hist, c, n, x, bin);
+            uint32_t b = before[r];
+            double w[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t left = b >= k ? 0u : min(n[i], k - b);
+                b += n[i];
+                w[i] = left ? weight(x[i], M, q.c) : 0.0;
+                sum[r] += (double)left * w[i];
+                passes |= (uint32_t)(left && w[i] >= q.m) << r;
+            }
+            if (table && bin >= 0 && cnt[r] != 0) {
+                const bool neg = bin >= HMAG;
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    table[neg ? bin + i : bin - i] = w[i];
+            }
+        } else if (table && cnt[r] != 0) {
+            // occurs, but past the first k
+            uint32_t n[4];
+            float x[4];
+            int bin;
+            order_entry<WGT>(r, hist, c, n, x, bin);
+            if (bin >= 0)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    table[bin >= HMAG ? bin + i : bin - i] = 0.0;
+        }
+        const double s = wave_incl_scan(sum[r]);
+        if (lane == 63)
+            c.sum[r * NW + wv] = s;
+        sum[r] = wave_excl_from_incl(s);       // from here on: what lies before the thread
+    });
     __syncthreads();
-    if (wv == 0) {
-        double a[3], am[3], s = 0.0, sm = 0.0;
-#pragma unroll
-        for (int i = 0; i < 3; ++i) {
-            const bool in = lane * 3 + i < NTILES;
-            a[i] = in ? c.sum[lane * 3 + i] : 0.0;
-            am[i] = in ? c.sum_m[lane * 3 + i] : 0.0;
-            s += a[i];
-            sm += am[i];
+    const double wmine = lane < R * NW ? c.sum[lane] : 0.0, winc = wave_incl_scan(wmine);
+    const double zk = lane_value(winc, 63), wexc = wave_excl_from_incl(winc);
+    const double goal = q.p < 1.0 ? q.p * zk : INFINITY;
+    int last[3] = {-1, -1, -1};
+    unroll<0, R>([&](auto r) SV_INLINE {
+        sum[r] += lane_value(wexc, r * NW + __builtin_amdgcn_readfirstlane(wv));
+        const bool in = cnt[r] != 0 && before[r] < k;
+        const unsigned long long a = __ballot(in);
+        const unsigned long long b = __ballot(in && (sum[r] < goal || before[r] == 0));
+        const unsigned long long m = __ballot(passes >> r & 1);
+        if (a)
+            last[0] = r * WGT + wv * 64 + 63 - __clzll(a);
+        if (b)
+            last[1] = r * WGT + wv * 64 + 63 - __clzll(b);
+        if (m)
+            last[2] = r * WGT + wv * 64 + 63 - __clzll(m);
+    });
+    const int mylast = lane == 0 ? last[0] : lane == 1 ? last[1] : last[2];
+    if (lane < 3 && mylast >= 0)
+        atomicMax(&c.last[lane], mylast);
+    __syncthreads();
+    const int owner = min(c.last[0], min(c.last[1], c.last[2]));
+    const bool all = q.p >= 1.0 && k == total && q.m <= 0.0;
+    if (all) {
+        if (t == 0) {
+            cut.z = zk;
+            c.cut = cut;
         }
-        const double inc = wave_incl_scan(s), before = wave_excl_from_incl(inc);
-        const double zk = lane_value(inc, 63), zm = wave_sum(sm);
-        // the tile of the cut and, in it, what comes before
-        int tile = -1;
-        double base = 0.0;
-        const double goal = q.p < 1.0 ? q.p * zk : INFINITY;
-        if (q.p < 1.0 || k < total) {
-            double b = before;
+    } else {
+        unroll<0, R>([&](auto r) SV_INLINE {
+            const int me = r * WGT + t;
+            if (me < owner || cnt[r] == 0 || (me > owner && !table))
+                return;
+            uint32_t n[4];
+            float x[4];
+            int bin;
+            order_entry<WGT>(r, hist, c, n, x, bin);
+            int keep_to = -1;              // the last of the four positions kept
+            if (me == owner) {
+                uint32_t b = before[r];
+                double run = sum[r];
+                bool go = true;
 #pragma unroll
-            for (int i = 0; i < 3; ++i) {
-                const int t = lane * 3 + i;
-                if (t < NTILES && c.count[t] && c.before[t] < (uint32_t)k && (b < goal || t == c.first)) {
-                    tile = t;
-                    base = b;
+                for (int i = 0; i < 4; ++i) {
+                    const uint32_t left = b >= k ? 0u : min(n[i], k - b);
+                    const double w = left ? weight(x[i], M, q.c) : 0.0;
+                    if (go && left) {
+                        go = (run < goal || b == 0) && w >= q.m;
+                        if (go) {
+                            uint32_t keep = left;
+                            if (q.p < 1.0) {
+                                const double f = ceil((goal - run) / w);
+                                keep = f < 1.0 ? 1u : f > (double)left ? left : (uint32_t)f;
+                            }
+                            keep_to = i;
+                            cut.cut = order_key(x[i]);
+                            cut.z = run + (double)keep * w;
+                            cut.state = keep < n[i] ? CUT_TIES : CUT_READY;
+                            cut.tie = keep < n[i] ? (int)keep : V;
+                        }
+                    }
+                    b += n[i];
+                    run += (double)left * w;
                 }
-                b += a[i];
+                c.cut = cut;
             }
-            const unsigned long long has = __ballot(tile >= 0);
-            const int l = 63 - __clzll(has);
-            tile = __shfl(tile, l);
-            base = lane_value(base, l);
-        }
-        RowCut r = c.cut;
-        r.z = zk;
-        double wcut = 0.0;
-        if (tile >= 0) {
-            float x;
-            uint32_t n;
-            int bin;
-            tile_entry(tile, hist, c, x, n, bin);
-            const uint32_t left = clip_counts(n, c.before[tile], c.count[tile], k);
-            const double w = left ? weight(x, M, q.c) : 0.0;
-            const double in = wave_incl_scan((double)left * w);
-            const double bef = base + wave_excl_from_incl(in);
-            unsigned long long has = __ballot(left && bef < goal);
-            if (!has)
-                has = __ballot(left != 0) & -__ballot(left != 0);   // p = 0: the first alone
-            const int l = 63 - __clzll(has);
-            const double bl = lane_value(bef, l), wl = lane_value(w, l);
-            const uint32_t nl = (uint32_t)__shfl((int)n, l), ll = (uint32_t)__shfl((int)left, l);
-            uint32_t keep = ll;
-            if (q.p < 1.0) {
-                const double m = ceil((goal - bl) / wl);
-                keep = m < 1.0 ? 1u : m > (double)ll ? ll : (uint32_t)m;
-            }
-            wcut = wl;
-            r.cut = order_key(__shfl(x, l));
-            r.z = q.p < 1.0 ? bl + (double)keep * wl : zk;
-            r.state = keep < nl ? CUT_TIES : CUT_READY;
-            r.tie = keep < nl ? (int)keep : V;
-        }
-        if (q.m > 0.0 && wcut < q.m) {
-            // min-p is the tighter: the last value that passes it
-            int mt = -1;
+            if (table && bin >= 0)
 #pragma unroll
-            for (int i = 0; i < 3; ++i)
-                if (am[i] > 0.0)
-                    mt = lane * 3 + i;
-            const int l = 63 - __clzll(__ballot(mt >= 0));
-            mt = __shfl(mt, l);
-            float x;
-            uint32_t n;
-            int bin;
-            tile_entry(mt, hist, c, x, n, bin);
-            const uint32_t left = clip_counts(n, c.before[mt], c.count[mt], k);
-            const double w = left ? weight(x, M, q.c) : 0.0;
-            const unsigned long long has = __ballot(left && w >= q.m);
-            const int ll = 63 - __clzll(has);
-            const uint32_t nl = (uint32_t)__shfl((int)n, ll), fl = (uint32_t)__shfl((int)left, ll);
-            r.cut = order_key(__shfl(x, ll));
-            r.z = zm;
-            r.state = fl < nl ? CUT_TIES : CUT_READY;
-            r.tie = fl < nl ? (int)fl : V;
-        }
-        if (lane == 0)
-            c.cut = r;
+                for (int i = 0; i < 4; ++i)
+                    if (i > keep_to)
+                        table[bin >= HMAG ? bin + i : bin - i] = 0.0;
+        });
     }
     __syncthreads();
 }
 
-// Counts a whole row straight from memory, eight vectors of a thread in flight.
+// Counts a whole row straight from memory, four vectors of a thread in flight.
 template <int WGT>
-__device__ void count_row(const RowSpan &r, int V, uint32_t *hist, CutLds &c, Outside &o)
+__device__ __forceinline__ void count_row(const Groups<1> &gr, uint32_t *hist, CutLds &c, Outside &o)
 {
-    const int t = threadIdx.x;
     constexpr int U = 4;
+    const int t = threadIdx.x;
     uint4 v[U];
-    int i = t;
-    if (i + (U - 1) * WGT < r.nvec) {
+    int g = t;
+    if (g + (U - 1) * WGT < gr.whole) {
 #pragma unroll
         for (int k = 0; k < U; ++k)
-            v[k] = load_stream(reinterpret_cast<const char *>(r.vec + i + k * WGT));
-        i += U * WGT;
-        for (; i + (U - 1) * WGT < r.nvec; i += U * WGT) {
+            v[k] = gr.load_whole(g + k * WGT);
+        g += U * WGT;
+        for (; g + (U - 1) * WGT < gr.whole; g += U * WGT) {
             uint4 nx[U];
 #pragma unroll
             for (int k = 0; k < U; ++k)
-                nx[k] = load_stream(reinterpret_cast<const char *>(r.vec + i + k * WGT));
+                nx[k] = gr.load_whole(g + k * WGT);
 #pragma unroll
             for (int k = 0; k < U; ++k)
                 count_vec(v[k], hist, c, o);
@@ -674,15 +743,11 @@ __device__ void count_row(const RowSpan &r, int V, uint32_t *hist, CutLds &c, Ou
         for (int k = 0; k < U; ++k)
             count_vec(v[k], hist, c, o);
     }
-    for (; i < r.nvec; i += WGT)
-        count_vec(load_stream(reinterpret_cast<const char *>(r.vec + i)), hist, c, o);
-    if (t < r.head)
-        count_one(pattern_at(r.row, t), hist, c, o);
-    if (r.tail0 + t < V)
-        count_one(pattern_at(r.row, r.tail0 + t), hist, c, o);
+    for (; g * 8 < gr.V; g += WGT)
+        count_vec(gr.load(g), hist, c, o);
 }
 
-template <int WGT> __device__ void clear_hist(uint32_t *hist)
+template <int WGT> __device__ __forceinline__ void clear_hist(uint32_t *hist)
 {
     for (int i = threadIdx.x; i < HBINS / 4; i += WGT)
         reinterpret_cast<uint4 *>(hist)[i] = make_uint4(0, 0, 0, 0);
@@ -705,66 +770,21 @@ __global__ __launch_bounds__(RWG, 8) void k_filter_rows_bf16(const char *tgt, co
     cut_lds_clear(c);
     __syncthreads();
     Outside o;
-    count_row<RWG>(row_span(row, V), V, hist, c, o);
-    cut_from_counts<RWG / 64>(hist, c, o, q, V, nullptr);
+    count_row<RWG>(Groups<1>(row, V), hist, c, o);
+    cut_from_counts<RWG>(hist, c, o, q, V, nullptr);
     if (threadIdx.x == 0)
         cuts[n] = c.cut;
 }
 
 // ------------------------------------------------------------------ the inverse-CDF draw
 //
-// A row is read in groups of one 16-byte vector, group 0 being the ids before the first aligned
-// vector and the last group those after the last whole one.  Each of a workgroup's waves takes a
-// contiguous range of groups, 64 at a time (a unit); a unit's kept weight is summed in a fixed
-// order and noted in LDS.  The draw then finds the wave, the unit, the lane and the id whose
-// cumulative weight passes u * total, reading again only that unit.
+// Each of a workgroup's waves takes a contiguous range of a row's groups, 64 at a time (a unit);
+// a unit's kept weight is summed in a fixed order and noted in LDS.  The draw then finds the wave,
+// the unit, the lane and the id whose cumulative weight passes u * total, looking again only at
+// that unit.
 
-template <int DT> struct Groups {
-    static constexpr int E = Elt<DT>::EPV;
-    const char *row;
-    int V, head, count, per_wave;      // ids before the first vector; groups; units per wave
-
-    __device__ Groups(const char *r, int v) : row(r), V(v)
-    {
-        const int mis = (int)(reinterpret_cast<uintptr_t>(r) & 15);
-        head = min(v, mis ? (16 - mis) / Elt<DT>::BYTES : 0);
-        count = (v - head) / E + 2;
-        per_wave = (count + FWAVES * 64 - 1) / (FWAVES * 64);
-    }
-    __device__ int first_id(int g) const { return head + (g - 1) * E; }
-    __device__ int group_of(int wave, int unit, int lane) const
-    {
-        return (wave * per_wave + unit) * 64 + lane;
-    }
-    // the group's logits; -inf where it has no id
-    __device__ uint4 load(int g) const
-    {
-        if (g > 0 && g < count - 1)
-            return load_plain(row + (ptrdiff_t)first_id(g) * Elt<DT>::BYTES);
-        uint32_t w[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            w[i] = DT == 1 ? 0xff80ff80u : 0xff800000u;
-        if (g == 0 || g == count - 1) {
-            const int i0 = first_id(g), end = g == 0 ? head : V;
-#pragma unroll
-            for (int k = 0; k < E; ++k) {
-                if (i0 + k < 0 || i0 + k >= end)
-                    continue;
-                if constexpr (DT == 1) {
-                    const uint32_t p = pattern_at(row, i0 + k);
-                    w[k / 2] = k & 1 ? (w[k / 2] & 0xffffu) | p << 16 : (w[k / 2] & 0xffff0000u) | p;
-                } else {
-                    w[k] = __float_as_uint(Elt<DT>::one(row, i0 + k));
-                }
-            }
-        }
-        return make_uint4(w[0], w[1], w[2], w[3]);
-    }
-};
-
-constexpr int MAX_UNITS_BF16 = (MAX_VOCAB / 8 + 2 + 63) / 64 + FWAVES;
-constexpr int MAX_UNITS_F32 = (MAX_VOCAB / 4 + 2 + 63) / 64 + FWAVES;
+constexpr int MAX_UNITS_BF16 = (MAX_VOCAB / 8 + 63) / 64 + FWAVES;
+constexpr int MAX_UNITS_F32 = (MAX_VOCAB / 4 + 63) / 64 + FWAVES;
 template <int DT> constexpr int max_units() { return DT == 1 ? MAX_UNITS_BF16 : MAX_UNITS_F32; }
 
 struct DrawLds {
@@ -773,11 +793,24 @@ struct DrawLds {
     int id;
 };
 
-// units[w * per_wave + i] hold the sums of all units (written by their waves); weights(g, vec, x)
-// gives the E weights of a group.  Returns the drawn id in every thread, -1 if all weights are 0.
-template <int DT, typename W>
-__device__ int draw_from_units(const Groups<DT> &gr, const double *units, double u, DrawLds &lds,
-                               W weights)
+// One unit's kept weight into units[]; vec is the lane's group of it.
+template <int DT, typename A, typename W>
+__device__ __forceinline__ void sum_unit(const Groups<DT> &gr, int i, double *units, const uint4 &vec, A may,
+                                const W &law)
+{
+    const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
+    double s = 0.0;
+    if (__ballot(may(vec)) != 0)
+        s = wave_incl_scan(law.sum(gr.group_of(wv, i, lane), vec));
+    if (lane == 63)
+        units[wv * gr.per_wave + i] = s;
+}
+
+// The draw from the units' sums.  law.weights(g, vec, x) gives the E weights of a group, fetch(i)
+// the lane's group of the wave's unit i.  Returns the id in every thread, -1 if all weights are 0.
+template <int DT, typename F, typename W>
+__device__ __forceinline__ int draw_from_units(const Groups<DT> &gr, const double *units, double u, DrawLds &lds,
+                               F fetch, const W &law)
 {
     constexpr int E = Elt<DT>::EPV;
     const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
@@ -785,29 +818,19 @@ __device__ int draw_from_units(const Groups<DT> &gr, const double *units, double
     double s = 0.0;
     for (int i = lane; i < gr.per_wave; i += 64)
         s += mine[i];
-    s = wave_sum(s);
-    if (lane == 0)
+    s = wave_incl_scan(s);
+    if (lane == 63)
         lds.wave[wv] = s;
     if (threadIdx.x == 0)
         lds.id = -1;
     __syncthreads();
-    double total = 0.0;
-    for (int i = 0; i < FWAVES; ++i)
-        total += lds.wave[i];
-    double goal = u * total;
-    int pick = -1;
-    double base = 0.0, run = 0.0;
-    for (int i = 0; i < FWAVES; ++i) {
-        const double x = lds.wave[i];
-        if (x > 0.0) {
-            pick = i;
-            base = run;
-            run += x;
-            if (run > goal)
-                break;
-        }
-    }
+    // lane w: wave w's sum
+    const double ws = lane < FWAVES ? lds.wave[lane] : 0.0, wi = wave_incl_scan(ws);
+    double goal = u * lane_value(wi, 63);
+    const unsigned long long wpos = __ballot(ws > 0.0), wover = __ballot(ws > 0.0 && wi > goal);
+    const int pick = wover ? __ffsll(wover) - 1 : wpos ? 63 - __clzll(wpos) : -1;
     if (wv == pick) {
+        double base = lane_value(wave_excl_from_incl(wi), pick);
         int unit = -1, last = 0;
         for (int i0 = 0; i0 < gr.per_wave && unit < 0; i0 += 64) {
             const double x = i0 + lane < gr.per_wave ? mine[i0 + lane] : 0.0;
@@ -830,7 +853,7 @@ __device__ int draw_from_units(const Groups<DT> &gr, const double *units, double
         }
         const int g = gr.group_of(wv, unit, lane);
         double x[E], sum = 0.0;
-        weights(g, gr.load(g), x);
+        law.weights(g, fetch(unit), x);
 #pragma unroll
         for (int k = 0; k < E; ++k)
             sum += x[k];
@@ -841,13 +864,14 @@ __device__ int draw_from_units(const Groups<DT> &gr, const double *units, double
         if (lane == l) {
             int id = -1;
             double r = before;
+            bool done = false;
 #pragma unroll
-            for (int k = 0; k < E; ++k) {
-                if (x[k] > 0.0 && !(id >= 0 && r > goal)) {
+            for (int k = 0; k < E; ++k)
+                if (x[k] > 0.0 && !done) {
                     r += x[k];
-                    id = gr.first_id(g) + k;
+                    id = g * E + k;
+                    done = over && r > goal;
                 }
-            }
             lds.id = id;
         }
     }
@@ -855,51 +879,106 @@ __device__ int draw_from_units(const Groups<DT> &gr, const double *units, double
     return lds.id;
 }
 
-// Sums the kept weight of each of the wave's units; vec(i, g) is unit i's group g.
-template <int DT, typename V, typename A, typename W>
-__device__ void sum_unit(const Groups<DT> &gr, int i, double *units, V vec, A any, W weights)
+constexpr int RES = 16;    // units whose groups a wave keeps in registers: 131072 bfloat16 ids
+
+template <int DT> __device__ __forceinline__ void hold(const Groups<DT> &gr, uint4 (&held)[RES])
 {
-    constexpr int E = Elt<DT>::EPV;
     const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
-    double s = 0.0;
-    if (__ballot(any(vec)) != 0) {
-        double x[E];
-        weights(gr.group_of(wv, i, lane), vec, x);
-#pragma unroll
-        for (int k = 0; k < E; ++k)
-            s += x[k];
-        s = wave_sum(s);
+    unroll<0, RES>([&](auto i) SV_INLINE {
+        if (i < gr.per_wave)
+            held[i] = gr.load(gr.group_of(wv, i, lane));
+    });
+}
+
+// The lane's group of unit i, the same unit in all lanes.
+template <int DT>
+__device__ __forceinline__ uint4 held_unit(const Groups<DT> &gr, const uint4 (&held)[RES], int unit)
+{
+    uint4 v = make_uint4(0, 0, 0, 0);
+    if (unit >= RES)
+        return gr.load(gr.group_of(threadIdx.x >> 6, unit, threadIdx.x & 63));
+    unroll<0, RES>([&](auto i) SV_INLINE {
+        if (i == unit)
+            v = held[i];
+    });
+    return v;
+}
+
+// Runs f(i, vec) over the wave's units: the first RES from registers, the rest four loads at a
+// time.  One body for all units; where it is short, unrolled costs less than choosing registers.
+template <bool SHORT, int DT, typename F>
+__device__ __forceinline__ void each_unit(const Groups<DT> &gr, const uint4 (&held)[RES], F f)
+{
+    const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
+    if constexpr (SHORT) {
+        unroll<0, RES>([&](auto i) SV_INLINE {
+            if (i < gr.per_wave)
+                f((int)i, held[i]);
+        });
+    } else {
+#pragma nounroll
+        for (int i = 0; i < min(RES, gr.per_wave); ++i)
+            f(i, held_unit(gr, held, i));
     }
-    if (lane == 0)
-        units[wv * gr.per_wave + i] = s;
+    for (int i0 = RES; i0 < gr.per_wave; i0 += 4) {
+        uint4 v[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            v[j] = gr.load(gr.group_of(wv, i0 + j, lane));
+        unroll<0, 4>([&](auto j) SV_INLINE {
+            if (i0 + j < gr.per_wave)
+                f(i0 + j, v[j]);
+        });
+    }
+}
+
+// Runs f(i, vec) over the wave's units of a row that is not held, eight loads at a time.
+template <int DT, typename F> __device__ __forceinline__ void each_unit(const Groups<DT> &gr, F f)
+{
+    const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
+    for (int i0 = 0; i0 < gr.per_wave; i0 += 8) {
+        uint4 v[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            v[j] = gr.load(gr.group_of(wv, i0 + j, lane));
+        unroll<0, 8>([&](auto j) SV_INLINE {
+            if (i0 + j < gr.per_wave)
+                f(i0 + j, v[j]);
+        });
+    }
+}
+
+// Bit k: the k-th logit of the group equals y.
+template <int DT> __device__ __forceinline__ uint32_t equal_mask(const uint4 &v, float y)
+{
+    float x[Elt<DT>::EPV];
+    Elt<DT>::unpack(v, x);
+    uint32_t m = 0;
+#pragma unroll
+    for (int k = 0; k < Elt<DT>::EPV; ++k)
+        m |= (uint32_t)(x[k] == y) << k;
+    return m;
 }
 
 // The last kept id among those equal to the cut, the n-th of them: equals per unit, then the wave,
-// the unit, the lane and the id.
+// the unit, the lane and the id.  each(f) runs f over the wave's units.
 template <int DT, typename F>
-__device__ int nth_equal(const Groups<DT> &gr, uint32_t cut, int n, uint32_t *units, DrawLds &lds,
-                         F vec)
+__device__ __forceinline__ int nth_equal(const Groups<DT> &gr, uint32_t cut, int n, uint32_t *units, DrawLds &lds,
+                         F each)
 {
     constexpr int E = Elt<DT>::EPV;
     const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
-    auto equals = [&](const uint4 &v) {
-        float x[E];
-        Elt<DT>::unpack(v, x);
-        const float y = key_value(cut);
-        uint32_t m = 0;
-#pragma unroll
-        for (int k = 0; k < E; ++k)
-            m |= (uint32_t)(x[k] == y) << k;
-        return m;
-    };
+    const float y = key_value(cut);
     uint32_t all = 0;
-    for (int i = 0; i < gr.per_wave; ++i) {
-        const uint32_t m = equals(vec(i));
-        const uint32_t s = __ballot(m != 0) ? wave_sum_u32(__popc(m)) : 0u;
-        if (lane == 0)
+    each([&](int i, const uint4 &v) {
+        const uint32_t m = equal_mask<DT>(v, y);
+        uint32_t s = 0;
+        if (__ballot(m != 0) != 0)
+            s = (uint32_t)lane_value((int)wave_scan_u32(__popc(m)), 63);
+        if (lane == 63)
             units[wv * gr.per_wave + i] = s;
         all += s;
-    }
+    });
     if (lane == 0)
         lds.ties[wv] = all;
     if (threadIdx.x == 0)
@@ -912,94 +991,200 @@ __device__ int nth_equal(const Groups<DT> &gr, uint32_t cut, int n, uint32_t *un
         const uint32_t *mine = units + wv * gr.per_wave;
         int unit = -1;
         for (int i0 = 0; i0 < gr.per_wave && unit < 0; i0 += 64) {
-            const int x = i0 + lane < gr.per_wave ? (int)mine[i0 + lane] : 0;
-            const int inc = (int)wave_scan_u32((uint32_t)x);
+            const uint32_t x = i0 + lane < gr.per_wave ? mine[i0 + lane] : 0u;
+            const int inc = (int)wave_scan_u32(x);
             const unsigned long long here = __ballot(before + inc >= n);
             if (here) {
                 const int l = __ffsll(here) - 1;
                 unit = i0 + l;
-                before += __shfl(inc - x, l);
+                before += __shfl(inc - (int)x, l);
             } else {
                 before += __shfl(inc, 63);
             }
         }
         const int g = gr.group_of(wv, unit, lane);
-        uint32_t m = equals(gr.load(g));
+        uint32_t m = equal_mask<DT>(gr.load(g), y);
         const int c = __popc(m), b = before + (int)wave_scan_u32((uint32_t)c) - c;
         if (b < n && n <= b + c) {
             for (int skip = n - b - 1; skip > 0; --skip)
                 m &= m - 1;
-            lds.id = gr.first_id(g) + __ffs(m) - 1;
+            lds.id = g * E + __ffs(m) - 1;
         }
     }
     __syncthreads();
-    return lds.id;
+    const int id = lds.id;
+    __syncthreads();
+    return id;
 }
 
-// Weights of a group under a cut law, computed from the logits: w / z.
+// How many ids below x equal y.
+template <int DT>
+__device__ __forceinline__ int equals_below(const Groups<DT> &gr, int x, float y, RedLds &red)
+{
+    constexpr int E = Elt<DT>::EPV;
+    const int last = x / E;
+    int n = 0;
+    for (int g0 = threadIdx.x; g0 <= last; g0 += 8 * FWG) {
+        uint4 v[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            v[j] = gr.load(min(g0 + j * FWG, last));
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int g = g0 + j * FWG;
+            uint32_t m = equal_mask<DT>(v[j], y);
+            if (g == last)
+                m &= (1u << (x % E)) - 1;
+            n += g <= last ? __popc(m) : 0;
+        }
+    }
+    return block_sum(n, red.i);
+}
+
+// The logits of a group one after another: the first of w[], which moves on.
+template <int DT> __device__ __forceinline__ float next_logit(uint32_t (&w)[4])
+{
+    float x;
+    if constexpr (DT == 1) {
+        x = pattern_value(w[0] & 0xffffu);
+        w[0] = __builtin_amdgcn_alignbit(w[1], w[0], 16);
+        w[1] = __builtin_amdgcn_alignbit(w[2], w[1], 16);
+        w[2] = __builtin_amdgcn_alignbit(w[3], w[2], 16);
+        w[3] >>= 16;
+    } else {
+        x = __uint_as_float(w[0]);
+        w[0] = w[1];
+        w[1] = w[2];
+        w[2] = w[3];
+    }
+    return x;
+}
+
+// Weights under a cut law, w / z, computed from the logits.
 template <int DT> struct DirectLaw {
-    const Groups<DT> &gr;
-    const RowCut &r;
+    static constexpr int E = Elt<DT>::EPV;
+    RowCut r;
     double z;
-    __device__ void operator()(int g, const uint4 &v, double (&x)[Elt<DT>::EPV]) const
+    __device__ __forceinline__ double one(float y, int id) const
     {
-        float y[Elt<DT>::EPV];
+        return kept(order_key(y), id, r) && y != -INFINITY ? weight(y, r.max, r.c) / z : 0.0;
+    }
+    __device__ __forceinline__ void weights(int g, const uint4 &v, double (&x)[E]) const
+    {
+        float y[E];
         Elt<DT>::unpack(v, y);
 #pragma unroll
-        for (int k = 0; k < Elt<DT>::EPV; ++k) {
-            x[k] = 0.0;
-            if (kept(order_key(y[k]), gr.first_id(g) + k, r) && y[k] != -INFINITY)
-                x[k] = weight(y[k], r.max, r.c) / z;
-        }
+        for (int k = 0; k < E; ++k)
+            x[k] = one(y[k], g * E + k);
+    }
+    __device__ __forceinline__ double sum(int g, const uint4 &v) const
+    {
+        uint32_t w[4] = {v.x, v.y, v.z, v.w};
+        double s = 0.0;
+#pragma nounroll
+        for (int k = 0; k < E; ++k)
+            s += one(next_logit<DT>(w), g * E + k);
+        return s;
     }
 };
 
 // The same from a table of w / z by bin, 0 for what the cut leaves out.
 struct TableLaw {
-    const Groups<1> &gr;
-    const RowCut &r;
+    RowCut r;
     double z;
     const double *table;
-    __device__ double at(uint32_t off) const
+    __device__ __forceinline__ double at(uint32_t off) const
     {
         return *reinterpret_cast<const double *>(reinterpret_cast<const char *>(table) + 2 * off);
     }
-    __device__ double one(uint32_t p, int id) const
+    __device__ __forceinline__ double one(float y, int id) const
     {
-        const uint32_t t = (p - HLO) & 0xffffu;
-        const float y = pattern_value(p);
-        if ((t & 0x7000u) == 0) {
-            const double w = table[((t & 0xfffu) << 1) | (t >> 15)];
-            return order_key(y) == r.cut && id > r.tie ? 0.0 : w;
-        }
-        if ((p & 0x7fffu) >= 0x7f80u || !kept(order_key(y), id, r))
-            return 0.0;
-        return weight(y, r.max, r.c) / z;
+        const uint32_t p = __float_as_uint(y) >> 16, t = window_words(p) & 0xffffu;
+        if ((t & 0x7000u) == 0)
+            return y == key_value(r.cut) && id > r.tie ? 0.0 : at(bin_offsets(t) & 0xffffu);
+        return kept(order_key(y), id, r) && y != -INFINITY ? weight(y, r.max, r.c) / z : 0.0;
     }
-    __device__ void operator()(int g, const uint4 &v, double (&x)[8]) const
+    // Ids past the last kept tie are looked at one by one, since a tie may be among them, and so
+    // are groups with a logit outside the window.
+    __device__ __forceinline__ bool by_table(int g, const uint4 &v, uint32_t (&t)[4]) const
     {
-        uint32_t t[4], out = 0;
+        uint32_t out = 0;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             t[i] = window_words(vec_word(v, i));
             out |= t[i] & 0x70007000u;
         }
-        // ids past the last kept tie are looked at one by one only where a tie may be among them
-        if (__ballot(out != 0 || gr.first_id(g) + 7 > r.tie) == 0) {
+        return __ballot(out != 0 || g * 8 + 7 > r.tie) == 0;
+    }
+    __device__ __forceinline__ void weights(int g, const uint4 &v, double (&x)[8]) const
+    {
+        float y[8];
+        Elt<1>::unpack(v, y);
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            x[k] = one(y[k], g * 8 + k);
+    }
+    __device__ __forceinline__ double sum(int g, const uint4 &v) const
+    {
+        uint32_t t[4];
+        double s = 0.0;
+        if (by_table(g, v, t)) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const uint32_t b = bin_offsets(t[i]);
-                x[2 * i] = at(b & 0xffffu);
-                x[2 * i + 1] = at(b >> 16);
+                s += at(b & 0xffffu);
+                s += at(b >> 16);
             }
         } else {
-            const int id = gr.first_id(g);
+            uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma nounroll
+            for (int k = 0; k < 8; ++k)
+                s += one(next_logit<1>(w), g * 8 + k);
+        }
+        return s;
+    }
+};
+
+// max(0, p - q) of two laws' weights.  q's groups are read where they are needed, in a draw's
+// last step; sum() is given them.
+template <int DT, typename P> struct ResidualLaw {
+    static constexpr int E = Elt<DT>::EPV;
+    P p, q;
+    Groups<DT> gq;
+    __device__ __forceinline__ void weights(int g, const uint4 &v, double (&x)[E]) const
+    {
+        double y[E];
+        p.weights(g, v, x);
+        q.weights(g, gq.load(g), y);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                x[2 * i] = one(vec_word(v, i) & 0xffffu, id + 2 * i);
-                x[2 * i + 1] = one(vec_word(v, i) >> 16, id + 2 * i + 1);
+        for (int k = 0; k < E; ++k)
+            x[k] = fmax(x[k] - y[k], 0.0);
+    }
+    __device__ __forceinline__ double sum(int g, const uint4 &pv, const uint4 &qv) const
+    {
+        double s = 0.0;
+        if constexpr (DT == 1) {
+            uint32_t tp[4], tq[4];
+            const bool a = p.by_table(g, pv, tp), b = q.by_table(g, qv, tq);
+            if (a && b) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const uint32_t op = bin_offsets(tp[i]), oq = bin_offsets(tq[i]);
+                    s += fmax(p.at(op & 0xffffu) - q.at(oq & 0xffffu), 0.0);
+                    s += fmax(p.at(op >> 16) - q.at(oq >> 16), 0.0);
+                }
+                return s;
             }
         }
+        uint32_t wp[4] = {pv.x, pv.y, pv.z, pv.w}, wq[4] = {qv.x, qv.y, qv.z, qv.w};
+#pragma nounroll
+        for (int k = 0; k < E; ++k) {
+            const float yp = next_logit<DT>(wp), yq = next_logit<DT>(wq);
+            const double x = p.one(yp, g * E + k);
+            if (x > 0.0)
+                s += fmax(x - q.one(yq, g * E + k), 0.0);
+        }
+        return s;
     }
 };
 
@@ -1007,14 +1192,14 @@ struct TableLaw {
 // integers, two at a time.
 template <int DT> struct MayKeep {
     uint32_t below;      // the largest pattern, twice, below the cut; 0: any group may
-    __device__ explicit MayKeep(const RowCut &r)
+    __device__ __forceinline__ explicit MayKeep(const RowCut &r)
     {
         const float y = key_value(r.cut);
         below = 0;
         if (DT == 1 && y > 0.0f)
             below = ((__float_as_uint(y) >> 16) - 1) * 0x10001u;
     }
-    __device__ bool operator()(const uint4 &v) const
+    __device__ __forceinline__ bool operator()(const uint4 &v) const
     {
         if (DT != 1 || below == 0)
             return true;
@@ -1030,15 +1215,13 @@ template <int DT> struct MayKeep {
 };
 
 // table[bin] = w / z for the bins that r keeps, 0 for the others.
-__device__ void fill_table(const RowCut &r, double *table)
+__device__ __forceinline__ void fill_table(const RowCut &r, double *table)
 {
     for (int b = threadIdx.x; b < HBINS; b += FWG) {
-        const float x = pattern_value(HLO + (uint32_t)(b >> 1) + (b & 1 ? 0x8000u : 0u));
+        const float x = pattern_value(bin_pattern(b));
         table[b] = order_key(x) >= r.cut && x <= r.max ? weight(x, r.max, r.c) / r.z : 0.0;
     }
 }
-
-constexpr int RES = 16;    // vectors of its row that a thread keeps in registers: 131072 ids
 
 // One row: its cut by counting, then the draw from the same registers.
 __global__ __launch_bounds__(FWG, 4) void k_filter_sample_bf16(const char *logits, int V,
@@ -1047,72 +1230,43 @@ __global__ __launch_bounds__(FWG, 4) void k_filter_sample_bf16(const char *logit
                                                                float *prob)
 {
     __shared__ __align__(16) uint32_t hist[HBINS];
-    __shared__ double table[HBINS];
+    __shared__ __align__(16) double table[HBINS];
     __shared__ CutLds c;
     __shared__ DrawLds dl;
     __shared__ RedLds red;
     double *units = reinterpret_cast<double *>(hist);
     static_assert(sizeof(hist) >= MAX_UNITS_BF16 * sizeof(double), "units fit where the counts were");
-    const int n = blockIdx.x, lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
+    const int n = blockIdx.x;
     const char *row = logits + (size_t)n * stride * 2;
     const Groups<1> gr(row, V);
     uint4 v[RES];
-#pragma unroll
-    for (int i = 0; i < RES; ++i)
-        if (i < gr.per_wave)
-            v[i] = gr.load(gr.group_of(wv, i, lane));
+    hold(gr, v);
     const Params q = load_params(f, n, V);
     clear_hist<FWG>(hist);
     cut_lds_clear(c);
     __syncthreads();
     Outside o;
-#pragma unroll
-    for (int i = 0; i < RES; ++i)
-        if (i < gr.per_wave)
-            count_vec(v[i], hist, c, o);
-    for (int i = RES; i < gr.per_wave; ++i)
-        count_vec(gr.load(gr.group_of(wv, i, lane)), hist, c, o);
-    cut_from_counts<FWAVES>(hist, c, o, q, V, table);
+    each_unit<true>(gr, v, [&](int, const uint4 &x) SV_INLINE { count_vec(x, hist, c, o); });
+    cut_from_counts<FWG>(hist, c, o, q, V, table);
     RowCut r = c.cut;
     const bool counted = r.state != CUT_EXACT;
     if (!counted)
         r = cut_by_bisection<1>(row, V, q, red);
-    if (r.state == CUT_NONE) {
-        if (threadIdx.x == 0) {
-            tok[n] = -1;
-            if (prob)
-                prob[n] = NAN;
-        }
-        return;
-    }
-    auto held = [&](int i) { return gr.load(gr.group_of(wv, i, lane)); };
-    if (r.state == CUT_TIES) {
-        r.tie = nth_equal(gr, r.cut, r.tie, reinterpret_cast<uint32_t *>(hist), dl, held);
-        __syncthreads();
-    }
-    const MayKeep<1> may(r);
-    int id;
-    if (counted) {
-        // the table holds the weights of the bins that occur; those below the cut go to 0
-        for (int b = threadIdx.x; b < HBINS; b += FWG)
-            if (order_key(pattern_value(HLO + (uint32_t)(b >> 1) + (b & 1 ? 0x8000u : 0u))) < r.cut)
-                table[b] = 0.0;
-        __syncthreads();
-        const TableLaw law{gr, r, 1.0, table};
-#pragma unroll
-        for (int i = 0; i < RES; ++i)
-            if (i < gr.per_wave)
-                sum_unit(gr, i, units, v[i], may, law);
-        for (int i = RES; i < gr.per_wave; ++i)
-            sum_unit(gr, i, units, held(i), may, law);
-        __syncthreads();
-        id = draw_from_units(gr, units, (double)unif[n], dl, law);
-    } else {
-        const DirectLaw<1> law{gr, r, 1.0};
-        for (int i = 0; i < gr.per_wave; ++i)
-            sum_unit(gr, i, units, held(i), may, law);
-        __syncthreads();
-        id = draw_from_units(gr, units, (double)unif[n], dl, law);
+    int id = -1;
+    if (r.state != CUT_NONE) {
+        if (r.state == CUT_TIES)
+            r.tie = nth_equal(gr, r.cut, r.tie, reinterpret_cast<uint32_t *>(hist), dl,
+                              [&](auto g) SV_INLINE { each_unit<false>(gr, v, g); });
+        const MayKeep<1> may(r);
+        auto draw = [&](auto law) SV_INLINE {
+            each_unit<false>(gr, v, [&](int i, const uint4 &x) SV_INLINE {
+                sum_unit(gr, i, units, x, may, law);
+            });
+            __syncthreads();
+            return draw_from_units(gr, units, (double)unif[n], dl,
+                                   [&](int i) SV_INLINE { return held_unit(gr, v, i); }, law);
+        };
+        id = counted ? draw(TableLaw{r, 1.0, table}) : draw(DirectLaw<1>{r, 1.0});
     }
     if (threadIdx.x == 0) {
         tok[n] = id;
@@ -1135,11 +1289,11 @@ __global__ __launch_bounds__(FWG) void k_filter_sample_f32(const char *logits, i
     if (r.state == CUT_READY) {
         const Groups<0> gr(row, V);
         const MayKeep<0> may(r);
-        const DirectLaw<0> law{gr, r, 1.0};
-        for (int i = 0; i < gr.per_wave; ++i)
-            sum_unit(gr, i, units, gr.load(gr.group_of(wv, i, lane)), may, law);
+        const DirectLaw<0> law{r, 1.0};
+        each_unit(gr, [&](int i, const uint4 &x) { sum_unit(gr, i, units, x, may, law); });
         __syncthreads();
-        id = draw_from_units(gr, units, (double)unif[n], dl, law);
+        id = draw_from_units(gr, units, (double)unif[n], dl,
+                             [&](int i) { return gr.load(gr.group_of(wv, i, lane)); }, law);
     }
     if (threadIdx.x == 0) {
         tok[n] = id;
@@ -1164,21 +1318,13 @@ __global__ __launch_bounds__(FWG) void k_filter_rows_f32(const char *tgt, const 
         cuts[n] = r;
 }
 
-// The law's value at one id.
-template <int DT>
-__device__ inline double law_at(const char *row, int id, const RowCut &r)
-{
-    const float x = Elt<DT>::one(row, id);
-    return kept(order_key(x), id, r) ? weight(x, r.max, r.c) / r.z : 0.0;
-}
-
 constexpr int MAX_POS = 63;
 
 struct VerifyLds {
-    RowCut cut[2 * MAX_POS + 1];      // target rows 0..K, then draft rows 0..K-1
+    RowCut cut[2 * MAX_POS + 1];          // target rows 0..K, then draft rows 0..K-1
     double P[MAX_POS + 1], Q[MAX_POS + 1];
+    unsigned long long look_p, look_q;    // positions whose draft id equals a partly kept cut
     int L;
-    unsigned long long look;
 };
 
 // Accept tests, first rejection and the replacement or bonus draw of one sequence.
@@ -1189,7 +1335,6 @@ __global__ __launch_bounds__(FWG, 4) void k_filter_verify(const char *tgt, const
                                                           const RowCut *cuts, int *acc, int *out,
                                                           float *probs)
 {
-    constexpr int E = Elt<DT>::EPV;
     __shared__ double tables[DT == 1 ? 2 : 1][DT == 1 ? HBINS : 1];
     __shared__ double units[max_units<DT>()];
     __shared__ VerifyLds s;
@@ -1203,17 +1348,16 @@ __global__ __launch_bounds__(FWG, 4) void k_filter_verify(const char *tgt, const
         s.cut[t] = t <= K ? cuts[(size_t)b * (K + 1) + t]
                           : cuts[(size_t)B * (K + 1) + (size_t)b * K + (t - K - 1)];
     __syncthreads();
-    if (DT == 1)
-        for (int i = 0; i < 2 * K + 1; ++i)
-            if (s.cut[i].state == CUT_EXACT) {
-                const RowCut r = cut_by_bisection<DT>(row_of(i), V, load_params(i <= K ? ft : fd, b, V), red);
-                __syncthreads();
-                if (t == 0)
-                    s.cut[i] = r;
-                __syncthreads();
-            }
-    // lane j: position j.  A draft id equal to a cut that keeps some of its ties is looked up
-    // below; until then it counts as kept.
+    for (int i = 0; i < 2 * K + 1; ++i)
+        if (s.cut[i].state == CUT_EXACT) {
+            const RowCut r = cut_by_bisection<DT>(row_of(i), V, load_params(i <= K ? ft : fd, b, V), red);
+            __syncthreads();
+            if (t == 0)
+                s.cut[i] = r;
+            __syncthreads();
+        }
+    // lane j: position j.  A draft id equal to a cut that keeps some of its ties counts as kept
+    // until its rank among them is known.
     if (t < 64) {
         bool ok = t <= K ? s.cut[t].state != CUT_NONE : true;
         bool lookp = false, lookq = false;
@@ -1234,32 +1378,22 @@ __global__ __launch_bounds__(FWG, 4) void k_filter_verify(const char *tgt, const
             s.Q[t] = Q;
         }
         const bool good = __ballot(!ok) == 0;
-        const unsigned long long lp = __ballot(good && lookp), lq = __ballot(good && lookq);
+        const unsigned long long lp = __ballot(lookp), lq = __ballot(lookq);
         if (t == 0) {
             s.L = good ? 0 : -1;
-            s.look = lp;
-            dl.wave[0] = __longlong_as_double((long long)lq);
+            s.look_p = good ? lp : 0;
+            s.look_q = good ? lq : 0;
         }
     }
     __syncthreads();
-    const unsigned long long lp = s.look, lq = (unsigned long long)__double_as_longlong(dl.wave[0]);
-    __syncthreads();
-    for (int i = 0; i < 2 * K + 1; ++i) {
-        const bool is_t = i < K;
-        const int j = is_t ? i : i - K - 1;
-        if (i == K || !((is_t ? lp : lq) >> j & 1))
-            continue;
-        // how many ids below the draft's equal the cut
-        const char *row = row_of(i);
-        const int x = tokens[(size_t)b * K + j];
-        const float y = key_value(s.cut[i].cut);
-        int n = 0;
-        for (int id = t; id < x; id += FWG)
-            n += Elt<DT>::one(row, id) == y;
-        n = block_sum(n, red.i);
-        if (t == 0 && n >= s.cut[i].tie)
-            (is_t ? s.P : s.Q)[j] = 0.0;
-    }
+    for (int side = 0; side < 2; ++side)
+        for (unsigned long long m = side ? s.look_q : s.look_p; m; m &= m - 1) {
+            const int j = __ffsll(m) - 1, i = side ? K + 1 + j : j;
+            const int n = equals_below(Groups<DT>(row_of(i), V), tokens[(size_t)b * K + j],
+                                       key_value(s.cut[i].cut), red);
+            if (t == 0 && n >= s.cut[i].tie)
+                (side ? s.Q : s.P)[j] = 0.0;
+        }
     __syncthreads();
     if (t < 64) {
         const bool good = s.L >= 0;
@@ -1278,64 +1412,77 @@ __global__ __launch_bounds__(FWG, 4) void k_filter_verify(const char *tgt, const
     int id = -1;
     if (L >= 0) {
         const Groups<DT> gp(row_of(L), V);
-        RowCut rp = s.cut[L], rq = rp;
-        auto vp = [&](int i) { return gp.load(gp.group_of(wv, i, lane)); };
+        uint4 held[RES];
+        hold(gp, held);
+        auto fetch = [&](int i) SV_INLINE { return held_unit(gp, held, i); };
+        RowCut rp = s.cut[L];
         uint32_t *counts = reinterpret_cast<uint32_t *>(units);
-        if (rp.state == CUT_TIES) {
-            rp.tie = nth_equal(gp, rp.cut, rp.tie, counts, dl, vp);
-            __syncthreads();
-        }
-        const double u = (double)unif[(size_t)b * (K + 1) + K];
-        const MayKeep<DT> may(rp);
         if constexpr (DT == 1)
             fill_table(rp, tables[0]);
-        auto draw = [&](auto &weights) {
-            for (int i = 0; i < gp.per_wave; ++i)
-                sum_unit(gp, i, units, vp(i), may, weights);
-            __syncthreads();
-            return draw_from_units(gp, units, u, dl, weights);
-        };
-        auto with_law = [&](auto &p) {
+        if (rp.state == CUT_TIES)
+            rp.tie = nth_equal(gp, rp.cut, rp.tie, counts, dl,
+                               [&](auto f) SV_INLINE { each_unit<false>(gp, held, f); });
+        const double u = (double)unif[(size_t)b * (K + 1) + K];
+        const MayKeep<DT> may(rp);
+        auto with_law = [&](auto p, auto q_of) SV_INLINE {
             if (L < K) {
                 const Groups<DT> gq(row_of(K + 1 + L), V);
-                rq = s.cut[K + 1 + L];
-                if (rq.state == CUT_TIES) {
-                    rq.tie = nth_equal(gq, rq.cut, rq.tie, counts, dl,
-                                       [&](int i) { return gq.load(gq.group_of(wv, i, lane)); });
-                    __syncthreads();
-                }
+                RowCut rq = s.cut[K + 1 + L];
                 if constexpr (DT == 1)
-                    fill_table(rq, tables[1]);
+                    fill_table(rq, tables[DT == 1]);
+                if (rq.state == CUT_TIES)
+                    rq.tie = nth_equal(gq, rq.cut, rq.tie, counts, dl,
+                                       [&](auto f) { each_unit(gq, f); });
                 __syncthreads();
-                // max(0, p - q); q is looked at only where p > 0
-                auto residual = [&](int g, const uint4 &v, double (&x)[E]) {
-                    p(g, v, x);
+                const ResidualLaw<DT, decltype(p)> residual{p, q_of(rq), gq};
+                // four units at a time, so that their reads of q overlap
+#pragma nounroll
+                for (int i0 = 0; i0 < gp.per_wave; i0 += 4) {
+                    uint4 pv[4], qv[4];
+                    bool any[4];
+                    if (i0 < RES) {
+                        unroll<0, RES / 4>([&](auto h) SV_INLINE {
+                            if (h * 4 == i0)
+                                unroll<0, 4>([&](auto j) SV_INLINE { pv[j] = held[h * 4 + j]; });
+                        });
+                    } else {
 #pragma unroll
-                    for (int k = 0; k < E; ++k)
-                        if (x[k] > 0.0) {
-                            const int i = gp.first_id(g) + k;
-                            double y;
-                            if constexpr (DT == 1)
-                                y = TableLaw{gq, rq, rq.z, tables[DT == 1]}.one(pattern_at(gq.row, i), i);
-                            else
-                                y = law_at<DT>(gq.row, i, rq);
-                            x[k] = fmax(x[k] - y, 0.0);
-                        }
-                };
-                id = draw(residual);
+                        for (int j = 0; j < 4; ++j)
+                            pv[j] = gp.load(gp.group_of(wv, i0 + j, lane));
+                    }
+                    unroll<0, 4>([&](auto j) SV_INLINE {
+                        any[j] = i0 + j < gp.per_wave && __ballot(may(pv[j])) != 0;
+                        if (any[j])
+                            qv[j] = gq.load(gq.group_of(wv, i0 + j, lane));
+                    });
+                    unroll<0, 4>([&](auto j) SV_INLINE {
+                        if (i0 + j >= gp.per_wave)
+                            return;
+                        double sum = 0.0;
+                        if (any[j])
+                            sum = wave_incl_scan(
+                                residual.sum(gp.group_of(wv, i0 + j, lane), pv[j], qv[j]));
+                        if (lane == 63)
+                            units[wv * gp.per_wave + i0 + j] = sum;
+                    });
+                }
                 __syncthreads();
+                id = draw_from_units(gp, units, u, dl, fetch, residual);
             }
             __syncthreads();
-            if (id < 0)                     // the bonus draw, or nothing left of p - q
-                id = draw(p);
+            if (id < 0) {                   // the bonus draw, or nothing left of p - q
+                each_unit<false>(gp, held, [&](int i, const uint4 &v) SV_INLINE {
+                    sum_unit(gp, i, units, v, may, p);
+                });
+                __syncthreads();
+                id = draw_from_units(gp, units, u, dl, fetch, p);
+            }
         };
-        if constexpr (DT == 1) {
-            TableLaw p{gp, rp, rp.z, tables[0]};
-            with_law(p);
-        } else {
-            DirectLaw<DT> p{gp, rp, rp.z};
-            with_law(p);
-        }
+        if constexpr (DT == 1)
+            with_law(TableLaw{rp, rp.z, tables[0]},
+                     [&](const RowCut &r) { return TableLaw{r, r.z, tables[DT == 1]}; });
+        else
+            with_law(DirectLaw<DT>{rp, rp.z}, [&](const RowCut &r) { return DirectLaw<DT>{r, r.z}; });
     }
     if (t <= K) {
         const size_t o = (size_t)b * (K + 1) + t;
