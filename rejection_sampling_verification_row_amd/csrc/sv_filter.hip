@@ -261,6 +261,7 @@ typedef unsigned int u32x4_any __attribute__((ext_vector_type(4), aligned(2)));
 
 template <int DT> struct Groups {
     static constexpr int E = Elt<DT>::EPV;
+    static constexpr uint32_t EMPTY = DT == 1 ? 0xff80ff80u : 0xff800000u;   // -inf
     const char *row;
     int V, whole, per_wave;    // whole groups; units of 64 groups that each wave takes in a draw
 
@@ -274,6 +275,12 @@ template <int DT> struct Groups {
     }
     __device__ __forceinline__ uint4 load_whole(int g) const
     {
+        const u32x4_any v = *reinterpret_cast<const u32x4_any *>(row + (size_t)g * 16);
+        return make_uint4(v.x, v.y, v.z, v.w);
+    }
+    // past the caches, for what is read once
+    __device__ __forceinline__ uint4 load_once(int g) const
+    {
         const u32x4_any v =
             __builtin_nontemporal_load(reinterpret_cast<const u32x4_any *>(row + (size_t)g * 16));
         return make_uint4(v.x, v.y, v.z, v.w);
@@ -286,7 +293,7 @@ template <int DT> struct Groups {
         uint32_t w[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-            w[i] = DT == 1 ? 0xff80ff80u : 0xff800000u;
+            w[i] = EMPTY;
         if (g == whole) {
 #pragma unroll
             for (int k = 0; k < E; ++k) {
@@ -366,6 +373,7 @@ struct CutLds {
     uint32_t xlist[HX];            // patterns outside the window as they were met
     uint32_t nx, zeros, low, bad;  // how many; zeros; largest order key <= -2^8; NaN or +inf met
     int last[3];                   // last place that top-k, top-p, min-p leave something of
+    uint32_t rth[FWAVES], top[FWAVES];  // per wave: a value that enough of its ids reach; its largest
     RowCut cut;
 };
 
@@ -375,6 +383,8 @@ __device__ __forceinline__ void cut_lds_clear(CutLds &c)
         c.nx = c.zeros = c.low = c.bad = 0;
         c.last[0] = c.last[1] = c.last[2] = -1;
     }
+    if (threadIdx.x < FWAVES)
+        c.rth[threadIdx.x] = c.top[threadIdx.x] = 0;
 }
 
 // What a thread meets outside the window.
@@ -450,6 +460,104 @@ __device__ __forceinline__ uint32_t wave_scan_u32(uint32_t x)
     return (uint32_t)v;
 }
 
+// What need not be counted.  With top-k, an id cannot matter once k others are known to be above
+// it; with min-p and neither of the others, once it lies too far below a maximum.  Each wave notes
+// in LDS the r-th largest of its lanes' maxima so far, r = ceil(k / waves): the waves' least is a
+// value that at least k ids reach.  Groups below it cost two instructions for a pair of logits, in
+// place of two LDS adds, and after the first part of a row nearly all are.  Only floors above zero
+// are used, where patterns compare as signed integers.  Notes of different age may be mixed: all
+// are lower bounds.
+typedef short s16x2 __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ s16x2 as_s16x2(uint32_t v) { return __builtin_bit_cast(s16x2, v); }
+__device__ __forceinline__ uint32_t max_i16(uint32_t a, uint32_t b)
+{
+    return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(as_s16x2(a), as_s16x2(b)));
+}
+__device__ __forceinline__ uint32_t max_u16(uint32_t a, uint32_t b)
+{
+    return as_u32(__builtin_elementwise_max(as_u16x2(a), as_u16x2(b)));
+}
+__device__ __forceinline__ uint32_t group_max(const uint4 &v)
+{
+    return max_i16(max_i16(v.x, v.y), max_i16(v.z, v.w));
+}
+
+struct Floor {
+    bool by_k, by_m;
+    int r;
+    float drop;              // T ln m, a little lower
+    uint32_t top = 0x80008000u, most = 0;    // the lane's largest: signed, and as unsigned patterns
+    uint32_t below = 0;      // the largest pattern, twice, that need not be counted; 0: none
+
+    __device__ __forceinline__ Floor(const Params &q, int V, int waves)
+    {
+        by_k = q.k < V && q.k <= 64 * waves;
+        by_m = q.p >= 1.0 && q.m > 0.0 && (q.k >= V || by_k);
+        r = (q.k + waves - 1) / waves;
+        drop = by_m ? (float)(log2(q.m) / q.c * 1.00001) - 1e-30f : 0.0f;
+    }
+    __device__ __forceinline__ bool active() const { return by_k || by_m; }
+    __device__ __forceinline__ void see(const uint4 &v)
+    {
+        top = max_i16(top, group_max(v));
+        most = max_u16(most, max_u16(max_u16(v.x, v.y), max_u16(v.z, v.w)));
+    }
+    // notes the wave's bounds
+    __device__ __forceinline__ void note(CutLds &c) const
+    {
+        const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
+        const int a = (int)(short)(top & 0xffffu), b = (int)(short)(top >> 16), m = max(max(a, b), 0);
+        int t = 0, mx = 0;
+#pragma unroll
+        for (int bit = 14; bit >= 0; --bit) {
+            const int u = t | 1 << bit, w = mx | 1 << bit;
+            if (__popcll(__ballot(m >= u)) >= r)
+                t = u;
+            if (__ballot(m >= w) != 0)
+                mx = w;
+        }
+        if (lane == 0) {
+            c.rth[wv] = (uint32_t)t;
+            c.top[wv] = (uint32_t)mx;
+        }
+    }
+    template <int NW> __device__ __forceinline__ void update(const CutLds &c)
+    {
+        const int lane = threadIdx.x & (NW - 1);
+        int k = (int)*(const volatile uint32_t *)&c.rth[lane];
+        int m = (int)*(const volatile uint32_t *)&c.top[lane];
+        k = min(k, lane_xch<0>(k));
+        m = max(m, lane_xch<0>(m));
+        k = min(k, lane_xch<1>(k));
+        m = max(m, lane_xch<1>(m));
+        k = min(k, lane_xch<2>(k));
+        m = max(m, lane_xch<2>(m));
+        if (NW > 8) {
+            k = min(k, lane_xch<3>(k));
+            m = max(m, lane_xch<3>(m));
+        }
+        static_assert(NW == 8 || NW == 16, "lanes exchanged over the waves' notes");
+        uint32_t f = by_k ? (uint32_t)k : 0;
+        if (by_m) {
+            const float y = pattern_value((uint32_t)m) + drop;
+            if (m < 0x7f80 && y > 0.0f)
+                f = max(f, __float_as_uint(y) >> 16);
+        }
+        // NaN and +inf are counted, so that they are seen
+        f = min(f, 0x7f80u);
+        below = __builtin_amdgcn_readfirstlane(f > 1 ? (f - 1) * 0x10001u : 0);
+    }
+    __device__ __forceinline__ bool matters(const uint4 &v) const
+    {
+        return below == 0 || max_i16(group_max(v), below) != below;
+    }
+    // a NaN of negative sign lies below any floor
+    __device__ __forceinline__ uint32_t bad() const
+    {
+        return (most & 0xffffu) > 0xff80u || most >> 16 > 0xff80u;
+    }
+};
+
 // The values kept apart, in order, into xval and xcnt (wave 0).
 __device__ __forceinline__ void order_outside(CutLds &c)
 {
@@ -521,10 +629,10 @@ __device__ __forceinline__ void order_entry(int row, const uint32_t *hist, const
 // and min-p each leave a prefix of the order, so the cut lies in the first of the three places
 // (order row, thread) where theirs end, and there position by position.  With `table`,
 // table[bin] receives the weight of every bin that occurs and is kept, and 0 of every bin that
-// occurs and is not.
+// occurs and is not.  `whole`: every id was counted, not just those that matter.
 template <int WGT>
-__device__ __forceinline__ void cut_from_counts(const uint32_t *hist, CutLds &c, const Outside &o, const Params &q,
-                                int V, double *table)
+__device__ __forceinline__ void cut_from_counts(const uint32_t *hist, CutLds &c, const Outside &o,
+                                                const Params &q, int V, bool whole, double *table)
 {
     constexpr int NW = WGT / 64, R = order_rows(WGT);
     static_assert(R * NW <= 64, "a lane for every order row and wave");
@@ -660,91 +768,108 @@ __device__ __forceinline__ void cut_from_counts(const uint32_t *hist, CutLds &c,
         atomicMax(&c.last[lane], mylast);
     __syncthreads();
     const int owner = min(c.last[0], min(c.last[1], c.last[2]));
-    const bool all = q.p >= 1.0 && k == total && q.m <= 0.0;
+    const bool all = whole && q.p >= 1.0 && k == total && q.m <= 0.0;
     if (all) {
         if (t == 0) {
             cut.z = zk;
             c.cut = cut;
         }
     } else {
+        // the owner's row, the same in all threads
+        const int at = __builtin_amdgcn_readfirstlane(owner / WGT);
+        uint32_t b0 = 0;
+        double run = 0.0;
         unroll<0, R>([&](auto r) SV_INLINE {
-            const int me = r * WGT + t;
-            if (me < owner || cnt[r] == 0 || (me > owner && !table))
-                return;
+            b0 = r == at ? before[r] : b0;
+            run = r == at ? sum[r] : run;
+            // the bins past the owner's
+            if (table && cnt[r] != 0 && r * WGT + t > owner && r != 0 && r != R / 2) {
+                constexpr bool neg = r > R / 2;
+                const int p = 4 * ((neg ? r - R / 2 - 1 : r - 1) * WGT + t);
+                double2 *q = reinterpret_cast<double2 *>(table + (neg ? HMAG + p : HMAG - 4 - p));
+                q[0] = q[1] = make_double2(0.0, 0.0);
+            }
+        });
+        if (at * WGT + t == owner) {
             uint32_t n[4];
             float x[4];
-            int bin;
-            order_entry<WGT>(r, hist, c, n, x, bin);
-            int keep_to = -1;              // the last of the four positions kept
-            if (me == owner) {
-                uint32_t b = before[r];
-                double run = sum[r];
-                bool go = true;
+            int bin, keep_to = -1;         // the last of the four positions kept
+            order_entry<WGT>(at, hist, c, n, x, bin);
+            uint32_t b = b0;
+            bool go = true;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const uint32_t left = b >= k ? 0u : min(n[i], k - b);
-                    const double w = left ? weight(x[i], M, q.c) : 0.0;
-                    if (go && left) {
-                        go = (run < goal || b == 0) && w >= q.m;
-                        if (go) {
-                            uint32_t keep = left;
-                            if (q.p < 1.0) {
-                                const double f = ceil((goal - run) / w);
-                                keep = f < 1.0 ? 1u : f > (double)left ? left : (uint32_t)f;
-                            }
-                            keep_to = i;
-                            cut.cut = order_key(x[i]);
-                            cut.z = run + (double)keep * w;
-                            cut.state = keep < n[i] ? CUT_TIES : CUT_READY;
-                            cut.tie = keep < n[i] ? (int)keep : V;
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t left = b >= k ? 0u : min(n[i], k - b);
+                const double w = left ? weight(x[i], M, q.c) : 0.0;
+                if (go && left) {
+                    go = (run < goal || b == 0) && w >= q.m;
+                    if (go) {
+                        uint32_t keep = left;
+                        if (q.p < 1.0) {
+                            const double f = ceil((goal - run) / w);
+                            keep = f < 1.0 ? 1u : f > (double)left ? left : (uint32_t)f;
                         }
+                        keep_to = i;
+                        cut.cut = order_key(x[i]);
+                        cut.z = run + (double)keep * w;
+                        cut.state = keep < n[i] ? CUT_TIES : CUT_READY;
+                        cut.tie = keep < n[i] ? (int)keep : V;
                     }
-                    b += n[i];
-                    run += (double)left * w;
                 }
-                c.cut = cut;
+                b += n[i];
+                run += (double)left * w;
             }
+            c.cut = cut;
             if (table && bin >= 0)
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
                     if (i > keep_to)
                         table[bin >= HMAG ? bin + i : bin - i] = 0.0;
-        });
+        }
     }
     __syncthreads();
 }
 
-// Counts a whole row straight from memory, four vectors of a thread in flight.
+// Counts a row straight from memory, COUNT_LOADS vectors of a thread in flight; the other waves of
+// the compute unit count meanwhile.
+constexpr int COUNT_LOADS = 4;
+
 template <int WGT>
-__device__ __forceinline__ void count_row(const Groups<1> &gr, uint32_t *hist, CutLds &c, Outside &o)
+__device__ __forceinline__ void count_row(const Groups<1> &gr, Floor &fl, uint32_t *hist, CutLds &c,
+                                          Outside &o)
 {
-    constexpr int U = 4;
+    constexpr int U = COUNT_LOADS, NW = WGT / 64;
     const int t = threadIdx.x;
-    uint4 v[U];
-    int g = t;
-    if (g + (U - 1) * WGT < gr.whole) {
-#pragma unroll
-        for (int k = 0; k < U; ++k)
-            v[k] = gr.load_whole(g + k * WGT);
-        g += U * WGT;
-        for (; g + (U - 1) * WGT < gr.whole; g += U * WGT) {
-            uint4 nx[U];
-#pragma unroll
-            for (int k = 0; k < U; ++k)
-                nx[k] = gr.load_whole(g + k * WGT);
-#pragma unroll
-            for (int k = 0; k < U; ++k)
-                count_vec(v[k], hist, c, o);
-#pragma unroll
-            for (int k = 0; k < U; ++k)
-                v[k] = nx[k];
+#pragma nounroll
+    for (int i = 0; i * U * WGT < gr.whole; ++i) {
+        const int g = i * U * WGT + t;
+        uint4 v[U];
+        unroll<0, U>([&](auto k) SV_INLINE {
+            v[k] = make_uint4(gr.EMPTY, gr.EMPTY, gr.EMPTY, gr.EMPTY);
+            if (g + k * WGT < gr.whole)
+                v[k] = gr.load_once(g + k * WGT);
+        });
+        if (fl.active()) {
+            unroll<0, U>([&](auto k) SV_INLINE { fl.see(v[k]); });
+            if ((i & (i + 1)) == 0) {
+                fl.note(c);
+                if (i == 0)
+                    __syncthreads();
+                fl.template update<NW>(c);
+            }
         }
-#pragma unroll
-        for (int k = 0; k < U; ++k)
-            count_vec(v[k], hist, c, o);
+        unroll<0, U>([&](auto k) SV_INLINE {
+            if (g + k * WGT < gr.whole && fl.matters(v[k]))
+                count_vec(v[k], hist, c, o);
+        });
     }
-    for (; g * 8 < gr.V; g += WGT)
-        count_vec(gr.load(g), hist, c, o);
+    if (t == 0 && gr.whole * 8 < gr.V) {
+        const uint4 x = gr.load(gr.whole);
+        fl.see(x);
+        count_vec(x, hist, c, o);
+    }
+    if (fl.active())
+        o.bad |= fl.bad();
 }
 
 template <int WGT> __device__ __forceinline__ void clear_hist(uint32_t *hist)
@@ -770,182 +895,223 @@ __global__ __launch_bounds__(RWG, 8) void k_filter_rows_bf16(const char *tgt, co
     cut_lds_clear(c);
     __syncthreads();
     Outside o;
-    count_row<RWG>(Groups<1>(row, V), hist, c, o);
-    cut_from_counts<RWG>(hist, c, o, q, V, nullptr);
+    Floor fl(q, V, RWG / 64);
+    count_row<RWG>(Groups<1>(row, V), fl, hist, c, o);
+    cut_from_counts<RWG>(hist, c, o, q, V, !fl.active(), nullptr);
     if (threadIdx.x == 0)
         cuts[n] = c.cut;
 }
 
 // ------------------------------------------------------------------ the inverse-CDF draw
 //
-// Each of a workgroup's waves takes a contiguous range of a row's groups, 64 at a time (a unit);
-// a unit's kept weight is summed in a fixed order and noted in LDS.  The draw then finds the wave,
-// the unit, the lane and the id whose cumulative weight passes u * total, looking again only at
-// that unit.
-
-constexpr int MAX_UNITS_BF16 = (MAX_VOCAB / 8 + 63) / 64 + FWAVES;
-constexpr int MAX_UNITS_F32 = (MAX_VOCAB / 4 + 63) / 64 + FWAVES;
-template <int DT> constexpr int max_units() { return DT == 1 ? MAX_UNITS_BF16 : MAX_UNITS_F32; }
+// Each of a workgroup's waves takes a contiguous range of a row's groups, 64 at a time (a unit).
+// The waves' kept weights decide which of them holds the id whose cumulative weight passes
+// u * total, and that wave goes over its units again, in order, to the unit, the lane and the id.
+// All sums have a fixed order.
 
 struct DrawLds {
+    double batch[FWAVES][64];
     double wave[FWAVES];
     uint32_t ties[FWAVES];
     int id;
 };
 
-// One unit's kept weight into units[]; vec is the lane's group of it.
-template <int DT, typename A, typename W>
-__device__ __forceinline__ void sum_unit(const Groups<DT> &gr, int i, double *units, const uint4 &vec, A may,
-                                const W &law)
+// One of N vectors, the same in all lanes.
+template <int N> __device__ __forceinline__ uint4 choose(const uint4 (&v)[N], int i)
 {
-    const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
-    double s = 0.0;
-    if (__ballot(may(vec)) != 0)
-        s = wave_incl_scan(law.sum(gr.group_of(wv, i, lane), vec));
-    if (lane == 63)
-        units[wv * gr.per_wave + i] = s;
+    uint4 x = v[0];
+    unroll<1, N>([&](auto j) SV_INLINE {
+        if (j == i) {
+            x = v[j];
+            // keeps the choice a branch and four moves: merged, it would be an indexed read of an
+            // array, which lives in memory
+            asm volatile("" : "+v"(x.x), "+v"(x.y), "+v"(x.z), "+v"(x.w));
+        }
+    });
+    return x;
 }
 
-// The draw from the units' sums.  law.weights(g, vec, x) gives the E weights of a group, fetch(i)
-// the lane's group of the wave's unit i.  Returns the id in every thread, -1 if all weights are 0.
-template <int DT, typename F, typename W>
-__device__ __forceinline__ int draw_from_units(const Groups<DT> &gr, const double *units, double u, DrawLds &lds,
-                               F fetch, const W &law)
+// A wave's units are read four at a time (a batch), all four loads in flight.  A wave notes in
+// a bit per batch where there was something for it, and later passes read only those.
+constexpr int BATCH = 4;
+static_assert((MAX_VOCAB / 4 + FWAVES * 64 - 1) / (FWAVES * 64) <= 64 * BATCH, "a bit for every batch");
+
+template <int DT>
+__device__ __forceinline__ void load_batch(const Groups<DT> &gr, int i0, uint4 (&v)[BATCH])
+{
+    const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    unroll<0, BATCH>([&](auto j) SV_INLINE {
+        const int g = gr.group_of(wv, i0 + j, lane);
+        v[j] = make_uint4(gr.EMPTY, gr.EMPTY, gr.EMPTY, gr.EMPTY);
+        if (i0 + j < gr.per_wave && g < gr.whole)
+            v[j] = gr.load_whole(g);
+    });
+    if (gr.whole * gr.E < gr.V) {
+        const int at = gr.whole / 64 - wv * gr.per_wave - i0;      // the partial group's unit
+        if (at >= 0 && at < BATCH && i0 + at < gr.per_wave && (gr.whole & 63) == lane) {
+            const uint4 last = gr.load(gr.whole);
+            unroll<0, BATCH>([&](auto j) SV_INLINE {
+                if (j == at)
+                    v[j] = last;
+            });
+        }
+    }
+}
+
+template <int DT> __device__ __forceinline__ uint64_t all_batches(const Groups<DT> &gr)
+{
+    const int n = (gr.per_wave + BATCH - 1) / BATCH;
+    return n >= 64 ? ~0ull : (1ull << n) - 1;
+}
+
+// f(i, vec, aux(g)) for the units of the noted batches that may() something in, one body for all;
+// then done(b) for the batch b, if it had such units.  AHEAD: the next batch is on its way
+// meanwhile.  Returns the batches that had such units.
+template <bool AHEAD, int DT, typename A, typename X, typename F, typename D>
+__device__ __forceinline__ uint64_t walk(const Groups<DT> &gr, uint64_t batches, A may, X aux, F f, D done)
+{
+    const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
+    uint64_t with = 0;
+    uint4 nx[BATCH];
+    if (AHEAD && batches)
+        load_batch(gr, __builtin_ctzll(batches) * BATCH, nx);
+#pragma nounroll
+    while (batches) {
+        const int b = __builtin_ctzll(batches), i0 = b * BATCH;
+        uint4 v[BATCH], x[BATCH];
+        if constexpr (AHEAD)
+            unroll<0, BATCH>([&](auto j) SV_INLINE { v[j] = nx[j]; });
+        else
+            load_batch(gr, i0, v);
+        batches &= batches - 1;
+        if (AHEAD && batches)
+            load_batch(gr, __builtin_ctzll(batches) * BATCH, nx);
+        uint32_t mask = 0;
+        unroll<0, BATCH>([&](auto j) SV_INLINE {
+            if (i0 + j < gr.per_wave && __ballot(may(v[j])) != 0) {
+                mask |= 1u << j;
+                x[j] = aux(gr.group_of(wv, i0 + j, lane));
+            }
+        });
+        mask = __builtin_amdgcn_readfirstlane(mask);
+        if (!mask)
+            continue;
+        with |= 1ull << b;
+#pragma nounroll
+        for (; mask; mask &= mask - 1) {
+            const int j = __builtin_ctz(mask);
+            f(i0 + j, choose(v, j), choose(x, j));
+        }
+        done(b);
+    }
+    return with;
+}
+
+// The draw.  First every wave sums its batches, then the wave that holds the id goes over the
+// batch that holds it; both by the same code, which is then at hand.  law.sum(g, vec, law.aux(g))
+// is the weight of a group, law.one(logit, id) that of one id.  Returns the id in every thread, -1 if
+// all weights are 0.
+template <int DT, typename A, typename W>
+__device__ __forceinline__ int draw_row(const Groups<DT> &gr, uint64_t batches, A may, double u,
+                                        DrawLds &lds, const W &law)
 {
     constexpr int E = Elt<DT>::EPV;
     const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
-    const double *mine = units + wv * gr.per_wave;
-    double s = 0.0;
-    for (int i = lane; i < gr.per_wave; i += 64)
-        s += mine[i];
-    s = wave_incl_scan(s);
-    if (lane == 63)
-        lds.wave[wv] = s;
     if (threadIdx.x == 0)
         lds.id = -1;
-    __syncthreads();
-    // lane w: wave w's sum
-    const double ws = lane < FWAVES ? lds.wave[lane] : 0.0, wi = wave_incl_scan(ws);
-    double goal = u * lane_value(wi, 63);
-    const unsigned long long wpos = __ballot(ws > 0.0), wover = __ballot(ws > 0.0 && wi > goal);
-    const int pick = wover ? __ffsll(wover) - 1 : wpos ? 63 - __clzll(wpos) : -1;
-    if (wv == pick) {
-        double base = lane_value(wave_excl_from_incl(wi), pick);
-        int unit = -1, last = 0;
-        for (int i0 = 0; i0 < gr.per_wave && unit < 0; i0 += 64) {
-            const double x = i0 + lane < gr.per_wave ? mine[i0 + lane] : 0.0;
-            const double inc = wave_incl_scan(x), exc = wave_excl_from_incl(inc);
-            const unsigned long long pos = __ballot(x > 0.0);
-            const unsigned long long over = __ballot(x > 0.0 && base + inc > goal);
-            if (over) {
-                const int l = __ffsll(over) - 1;
-                unit = i0 + l;
-                base += lane_value(exc, l);
-            } else {
-                if (pos)
-                    last = i0 + 63 - __clzll(pos);
-                base += lane_value(inc, 63);
+    double base = 0.0, goal = INFINITY, mine = 0.0, all = 0.0;
+    int unit = -1, last = -1;
+    bool search = false;
+#pragma nounroll
+    for (int pass = 0; pass < 2; ++pass) {
+        batches = walk<W::AHEAD>(
+            gr, batches, may, [&](int g) SV_INLINE { return law.aux(g); },
+            [&](int i, const uint4 &v, const uint4 &x4) SV_INLINE {
+                const double s = law.sum(gr.group_of(wv, i, lane), v, x4);
+                if (!search) {
+                    mine += s;
+                } else if (unit < 0) {
+                    const double x = lane_value(wave_incl_scan(s), 63);
+                    if (x > 0.0) {
+                        last = i;
+                        if (base + x > goal)
+                            unit = i;
+                        else
+                            base += x;
+                    }
+                }
+            },
+            [&](int b) SV_INLINE {
+                const double s = lane_value(wave_incl_scan(mine), 63);
+                mine = 0.0;
+                all += s;
+                if (!search && lane == 0)
+                    lds.batch[wv][b] = s;
+            });
+        if (search)
+            break;
+        if (lane == 0)
+            lds.wave[wv] = all;
+        __syncthreads();
+        // lane w: wave w's sum
+        const double ws = lane < FWAVES ? lds.wave[lane] : 0.0, wi = wave_incl_scan(ws);
+        goal = u * lane_value(wi, 63);
+        const unsigned long long pos = __ballot(ws > 0.0), over = __ballot(ws > 0.0 && wi > goal);
+        const int pick = over ? __ffsll(over) - 1 : pos ? 63 - __clzll(pos) : -1;
+        if (__builtin_amdgcn_readfirstlane(wv) != pick)
+            break;
+        base = lane_value(wave_excl_from_incl(wi), pick);
+        search = true;
+        // the batch; where rounding leaves none, here or below, the last of positive weight
+        if (!over)
+            goal = INFINITY;
+        uint64_t m = batches;
+        double lastbase = base;
+        bool found = false;
+        int at = 0;
+#pragma nounroll
+        for (; m && !found; m &= m - 1) {
+            const int b = __builtin_ctzll(m);
+            const double x = lds.batch[wv][b];
+            if (x > 0.0) {
+                at = b;
+                lastbase = base;
+                found = base + x > goal;
+                base += x;
             }
         }
-        if (unit < 0) {                      // rounding left none: the last id of positive weight
+        if (!found)
+            goal = INFINITY;
+        base = lastbase;
+        batches = 1ull << at;
+    }
+    if (search) {
+        if (unit < 0) {
             unit = last;
             goal = INFINITY;
         }
         const int g = gr.group_of(wv, unit, lane);
-        double x[E], sum = 0.0;
-        law.weights(g, fetch(unit), x);
-#pragma unroll
-        for (int k = 0; k < E; ++k)
-            sum += x[k];
-        const double inc = wave_incl_scan(sum), before = base + wave_excl_from_incl(inc);
-        const unsigned long long pos = __ballot(sum > 0.0);
-        const unsigned long long over = __ballot(sum > 0.0 && base + inc > goal);
+        const uint4 v = gr.load(g);
+        const double s = law.sum(g, v, law.aux(g)), inc = wave_incl_scan(s);
+        const unsigned long long pos = __ballot(s > 0.0);
+        const unsigned long long over = __ballot(s > 0.0 && base + inc > goal);
         const int l = over ? __ffsll(over) - 1 : 63 - __clzll(pos);
-        if (lane == l) {
-            int id = -1;
-            double r = before;
-            bool done = false;
-#pragma unroll
-            for (int k = 0; k < E; ++k)
-                if (x[k] > 0.0 && !done) {
-                    r += x[k];
-                    id = g * E + k;
-                    done = over && r > goal;
-                }
+        base += lane_value(wave_excl_from_incl(inc), l);
+        // lane k: the group's k-th id
+        uint32_t w[4] = {(uint32_t)lane_value((int)v.x, l), (uint32_t)lane_value((int)v.y, l),
+                         (uint32_t)lane_value((int)v.z, l), (uint32_t)lane_value((int)v.w, l)};
+        const int k = lane % E, id = gr.group_of(wv, unit, l) * E + k;
+        const int word = DT == 1 ? k / 2 : k;
+        const uint32_t b = word == 0 ? w[0] : word == 1 ? w[1] : word == 2 ? w[2] : w[3];
+        const float y = DT == 1 ? pattern_value(k & 1 ? b >> 16 : b & 0xffffu) : __uint_as_float(b);
+        const double x = lane < E && id < gr.V ? law.one(y, id) : 0.0, xi = wave_incl_scan(x);
+        const unsigned long long xpos = __ballot(x > 0.0);
+        const unsigned long long xover = __ballot(x > 0.0 && over && base + xi > goal);
+        if (lane == (xover ? __ffsll(xover) - 1 : 63 - __clzll(xpos)))
             lds.id = id;
-        }
     }
     __syncthreads();
     return lds.id;
-}
-
-constexpr int RES = 16;    // units whose groups a wave keeps in registers: 131072 bfloat16 ids
-
-template <int DT> __device__ __forceinline__ void hold(const Groups<DT> &gr, uint4 (&held)[RES])
-{
-    const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
-    unroll<0, RES>([&](auto i) SV_INLINE {
-        if (i < gr.per_wave)
-            held[i] = gr.load(gr.group_of(wv, i, lane));
-    });
-}
-
-// The lane's group of unit i, the same unit in all lanes.
-template <int DT>
-__device__ __forceinline__ uint4 held_unit(const Groups<DT> &gr, const uint4 (&held)[RES], int unit)
-{
-    uint4 v = make_uint4(0, 0, 0, 0);
-    if (unit >= RES)
-        return gr.load(gr.group_of(threadIdx.x >> 6, unit, threadIdx.x & 63));
-    unroll<0, RES>([&](auto i) SV_INLINE {
-        if (i == unit)
-            v = held[i];
-    });
-    return v;
-}
-
-// Runs f(i, vec) over the wave's units: the first RES from registers, the rest four loads at a
-// time.  One body for all units; where it is short, unrolled costs less than choosing registers.
-template <bool SHORT, int DT, typename F>
-__device__ __forceinline__ void each_unit(const Groups<DT> &gr, const uint4 (&held)[RES], F f)
-{
-    const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
-    if constexpr (SHORT) {
-        unroll<0, RES>([&](auto i) SV_INLINE {
-            if (i < gr.per_wave)
-                f((int)i, held[i]);
-        });
-    } else {
-#pragma nounroll
-        for (int i = 0; i < min(RES, gr.per_wave); ++i)
-            f(i, held_unit(gr, held, i));
-    }
-    for (int i0 = RES; i0 < gr.per_wave; i0 += 4) {
-        uint4 v[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-            v[j] = gr.load(gr.group_of(wv, i0 + j, lane));
-        unroll<0, 4>([&](auto j) SV_INLINE {
-            if (i0 + j < gr.per_wave)
-                f(i0 + j, v[j]);
-        });
-    }
-}
-
-// Runs f(i, vec) over the wave's units of a row that is not held, eight loads at a time.
-template <int DT, typename F> __device__ __forceinline__ void each_unit(const Groups<DT> &gr, F f)
-{
-    const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
-    for (int i0 = 0; i0 < gr.per_wave; i0 += 8) {
-        uint4 v[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-            v[j] = gr.load(gr.group_of(wv, i0 + j, lane));
-        unroll<0, 8>([&](auto j) SV_INLINE {
-            if (i0 + j < gr.per_wave)
-                f(i0 + j, v[j]);
-        });
-    }
 }
 
 // Bit k: the k-th logit of the group equals y.
@@ -960,55 +1126,86 @@ template <int DT> __device__ __forceinline__ uint32_t equal_mask(const uint4 &v,
     return m;
 }
 
-// The last kept id among those equal to the cut, the n-th of them: equals per unit, then the wave,
-// the unit, the lane and the id.  each(f) runs f over the wave's units.
-template <int DT, typename F>
-__device__ __forceinline__ int nth_equal(const Groups<DT> &gr, uint32_t cut, int n, uint32_t *units, DrawLds &lds,
-                         F each)
+// How many logits of the group equal y; bfloat16 two at a time, as patterns (the zeros without
+// their sign).
+template <int DT> __device__ __forceinline__ uint32_t equal_count(const uint4 &v, float y)
+{
+    if constexpr (DT == 1) {
+        const uint32_t keep = y == 0.0f ? 0x7fff7fffu : 0xffffffffu;
+        const uint32_t p = (__float_as_uint(y) >> 16) * 0x10001u & keep;
+        const u16x2 one = {1, 1};
+        u16x2 n = {0, 0};
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            n += __builtin_elementwise_min(as_u16x2((vec_word(v, i) & keep) ^ p), one);
+        return 8u - n.x - n.y;
+    } else {
+        return __popc(equal_mask<DT>(v, y));
+    }
+}
+
+// The last kept id among those equal to the cut, the n-th of them: equals per wave, then the
+// unit, the lane and the id.
+template <int DT>
+__device__ __forceinline__ int nth_equal(const Groups<DT> &gr, uint64_t batches, uint32_t cut, int n,
+                                         DrawLds &lds)
 {
     constexpr int E = Elt<DT>::EPV;
     const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
     const float y = key_value(cut);
-    uint32_t all = 0;
-    each([&](int i, const uint4 &v) {
-        const uint32_t m = equal_mask<DT>(v, y);
-        uint32_t s = 0;
-        if (__ballot(m != 0) != 0)
-            s = (uint32_t)lane_value((int)wave_scan_u32(__popc(m)), 63);
-        if (lane == 63)
-            units[wv * gr.per_wave + i] = s;
-        all += s;
-    });
-    if (lane == 0)
-        lds.ties[wv] = all;
+    auto may = [&](const uint4 &v) SV_INLINE { return equal_count<DT>(v, y) != 0; };
+    auto none = [](int) SV_INLINE { return make_uint4(0, 0, 0, 0); };
+    uint32_t mine = 0;
+    int before = 0, all = 0;
+    bool search = false;
     if (threadIdx.x == 0)
         lds.id = 0x7fffffff;
-    __syncthreads();
-    int before = 0;
-    for (int w = 0; w < wv; ++w)
-        before += (int)lds.ties[w];
-    if (before < n && n <= before + (int)all) {
-        const uint32_t *mine = units + wv * gr.per_wave;
-        int unit = -1;
-        for (int i0 = 0; i0 < gr.per_wave && unit < 0; i0 += 64) {
-            const uint32_t x = i0 + lane < gr.per_wave ? mine[i0 + lane] : 0u;
-            const int inc = (int)wave_scan_u32(x);
-            const unsigned long long here = __ballot(before + inc >= n);
-            if (here) {
-                const int l = __ffsll(here) - 1;
-                unit = i0 + l;
-                before += __shfl(inc - (int)x, l);
-            } else {
-                before += __shfl(inc, 63);
-            }
-        }
-        const int g = gr.group_of(wv, unit, lane);
-        uint32_t m = equal_mask<DT>(gr.load(g), y);
-        const int c = __popc(m), b = before + (int)wave_scan_u32((uint32_t)c) - c;
-        if (b < n && n <= b + c) {
-            for (int skip = n - b - 1; skip > 0; --skip)
-                m &= m - 1;
-            lds.id = g * E + __ffs(m) - 1;
+#pragma nounroll
+    for (int pass = 0; pass < 2; ++pass) {
+        batches = walk<true>(
+            gr, batches, may, none,
+            [&](int i, const uint4 &v, const uint4 &) SV_INLINE {
+                uint32_t m = equal_mask<DT>(v, y);
+                const int c = __popc(m);
+                if (!search) {
+                    mine += c;
+                    return;
+                }
+                const int inc = before + (int)wave_scan_u32((uint32_t)c), b = inc - c;
+                if (b < n && n <= inc) {
+                    for (int skip = n - b - 1; skip > 0; --skip)
+                        m &= m - 1;
+                    lds.id = gr.group_of(wv, i, lane) * E + __ffs(m) - 1;
+                }
+                before = lane_value(inc, 63);
+            },
+            [&](int b) SV_INLINE {
+                const int s = lane_value((int)wave_scan_u32(mine), 63);
+                mine = 0;
+                all += s;
+                if (!search && lane == 0)
+                    lds.batch[wv][b] = (double)s;
+            });
+        if (search)
+            break;
+        if (lane == 0)
+            lds.ties[wv] = all;
+        __syncthreads();
+        const int w = lane < FWAVES ? (int)lds.ties[lane] : 0, wi = (int)wave_scan_u32((uint32_t)w);
+        const int me = __builtin_amdgcn_readfirstlane(wv);
+        before = lane_value(wi - w, me);
+        if (!(before < n && n <= before + all))
+            break;
+        search = true;
+        uint64_t m = batches;
+        batches = 0;
+#pragma nounroll
+        for (; m && !batches; m &= m - 1) {
+            const int b = __builtin_ctzll(m), s = (int)lds.batch[wv][b];
+            if (before + s >= n)
+                batches = 1ull << b;
+            else
+                before += s;
         }
     }
     __syncthreads();
@@ -1060,24 +1257,18 @@ template <int DT> __device__ __forceinline__ float next_logit(uint32_t (&w)[4])
     return x;
 }
 
-// Weights under a cut law, w / z, computed from the logits.
+// Weights under a cut law times a scale, computed from the logits.
 template <int DT> struct DirectLaw {
     static constexpr int E = Elt<DT>::EPV;
+    static constexpr bool AHEAD = true;
     RowCut r;
-    double z;
+    double scale;
     __device__ __forceinline__ double one(float y, int id) const
     {
-        return kept(order_key(y), id, r) && y != -INFINITY ? weight(y, r.max, r.c) / z : 0.0;
+        return kept(order_key(y), id, r) && y != -INFINITY ? weight(y, r.max, r.c) * scale : 0.0;
     }
-    __device__ __forceinline__ void weights(int g, const uint4 &v, double (&x)[E]) const
-    {
-        float y[E];
-        Elt<DT>::unpack(v, y);
-#pragma unroll
-        for (int k = 0; k < E; ++k)
-            x[k] = one(y[k], g * E + k);
-    }
-    __device__ __forceinline__ double sum(int g, const uint4 &v) const
+    __device__ __forceinline__ uint4 aux(int) const { return make_uint4(0, 0, 0, 0); }
+    __device__ __forceinline__ double sum(int g, const uint4 &v, const uint4 &) const
     {
         uint32_t w[4] = {v.x, v.y, v.z, v.w};
         double s = 0.0;
@@ -1088,11 +1279,21 @@ template <int DT> struct DirectLaw {
     }
 };
 
-// The same from a table of w / z by bin, 0 for what the cut leaves out.
+// The same from a table by bin, 0 for what the cut leaves out.
 struct TableLaw {
+    static constexpr bool AHEAD = true;
     RowCut r;
-    double z;
+    double scale;
     const double *table;
+    uint32_t cut_off;        // where some of the cut's ties are left out: its offset, if it has one
+
+    __device__ __forceinline__ TableLaw(const RowCut &c, int V, double sc, const double *tab)
+        : r(c), scale(sc), table(tab), cut_off(~0u)
+    {
+        const uint32_t t = window_words(__float_as_uint(key_value(c.cut)) >> 16) & 0xffffu;
+        if (c.tie < V && (t & 0x7000u) == 0)
+            cut_off = bin_offsets(t) & 0xffffu;
+    }
     __device__ __forceinline__ double at(uint32_t off) const
     {
         return *reinterpret_cast<const double *>(reinterpret_cast<const char *>(table) + 2 * off);
@@ -1102,10 +1303,10 @@ struct TableLaw {
         const uint32_t p = __float_as_uint(y) >> 16, t = window_words(p) & 0xffffu;
         if ((t & 0x7000u) == 0)
             return y == key_value(r.cut) && id > r.tie ? 0.0 : at(bin_offsets(t) & 0xffffu);
-        return kept(order_key(y), id, r) && y != -INFINITY ? weight(y, r.max, r.c) / z : 0.0;
+        return kept(order_key(y), id, r) && y != -INFINITY ? weight(y, r.max, r.c) * scale : 0.0;
     }
-    // Ids past the last kept tie are looked at one by one, since a tie may be among them, and so
-    // are groups with a logit outside the window.
+    // Whether a unit's groups can be looked up whole: no logit outside the window, and not the
+    // group in which the kept ties end.
     __device__ __forceinline__ bool by_table(int g, const uint4 &v, uint32_t (&t)[4]) const
     {
         uint32_t out = 0;
@@ -1114,26 +1315,27 @@ struct TableLaw {
             t[i] = window_words(vec_word(v, i));
             out |= t[i] & 0x70007000u;
         }
-        return __ballot(out != 0 || g * 8 + 7 > r.tie) == 0;
+        return __ballot(out != 0 || (g * 8 <= r.tie && g * 8 + 7 > r.tie)) == 0;
     }
-    __device__ __forceinline__ void weights(int g, const uint4 &v, double (&x)[8]) const
+    // what a group past the last kept tie must not look up
+    __device__ __forceinline__ uint32_t left_out(int g) const { return g * 8 > r.tie ? cut_off : ~0u; }
+    __device__ __forceinline__ double at(uint32_t off, uint32_t without) const
     {
-        float y[8];
-        Elt<1>::unpack(v, y);
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-            x[k] = one(y[k], g * 8 + k);
+        const double x = at(off);
+        return off == without ? 0.0 : x;
     }
-    __device__ __forceinline__ double sum(int g, const uint4 &v) const
+    __device__ __forceinline__ uint4 aux(int) const { return make_uint4(0, 0, 0, 0); }
+    __device__ __forceinline__ double sum(int g, const uint4 &v, const uint4 &) const
     {
         uint32_t t[4];
         double s = 0.0;
         if (by_table(g, v, t)) {
+            const uint32_t no = left_out(g);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const uint32_t b = bin_offsets(t[i]);
-                s += at(b & 0xffffu);
-                s += at(b >> 16);
+                s += at(b & 0xffffu, no);
+                s += at(b >> 16, no);
             }
         } else {
             uint32_t w[4] = {v.x, v.y, v.z, v.w};
@@ -1145,21 +1347,18 @@ struct TableLaw {
     }
 };
 
-// max(0, p - q) of two laws' weights.  q's groups are read where they are needed, in a draw's
-// last step; sum() is given them.
+// max(0, p - q) of two laws' weights; the second operand of sum() is q's group.
 template <int DT, typename P> struct ResidualLaw {
     static constexpr int E = Elt<DT>::EPV;
+    static constexpr bool AHEAD = false;     // two rows: the registers hold one batch of each
     P p, q;
     Groups<DT> gq;
-    __device__ __forceinline__ void weights(int g, const uint4 &v, double (&x)[E]) const
+    __device__ __forceinline__ double one(float y, int id) const
     {
-        double y[E];
-        p.weights(g, v, x);
-        q.weights(g, gq.load(g), y);
-#pragma unroll
-        for (int k = 0; k < E; ++k)
-            x[k] = fmax(x[k] - y[k], 0.0);
+        const double x = p.one(y, id);
+        return x > 0.0 ? fmax(x - q.one(Elt<DT>::one(gq.row, id), id), 0.0) : 0.0;
     }
+    __device__ __forceinline__ uint4 aux(int g) const { return gq.load(g); }
     __device__ __forceinline__ double sum(int g, const uint4 &pv, const uint4 &qv) const
     {
         double s = 0.0;
@@ -1167,11 +1366,12 @@ template <int DT, typename P> struct ResidualLaw {
             uint32_t tp[4], tq[4];
             const bool a = p.by_table(g, pv, tp), b = q.by_table(g, qv, tq);
             if (a && b) {
+                const uint32_t np = p.left_out(g), nq = q.left_out(g);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const uint32_t op = bin_offsets(tp[i]), oq = bin_offsets(tq[i]);
-                    s += fmax(p.at(op & 0xffffu) - q.at(oq & 0xffffu), 0.0);
-                    s += fmax(p.at(op >> 16) - q.at(oq >> 16), 0.0);
+                    s += fmax(p.at(op & 0xffffu, np) - q.at(oq & 0xffffu, nq), 0.0);
+                    s += fmax(p.at(op >> 16, np) - q.at(oq >> 16, nq), 0.0);
                 }
                 return s;
             }
@@ -1215,15 +1415,16 @@ template <int DT> struct MayKeep {
 };
 
 // table[bin] = w / z for the bins that r keeps, 0 for the others.
-__device__ __forceinline__ void fill_table(const RowCut &r, double *table)
+__device__ __forceinline__ void fill_table(const RowCut &r, double scale, double *table)
 {
+    const float low = key_value(r.cut);
     for (int b = threadIdx.x; b < HBINS; b += FWG) {
         const float x = pattern_value(bin_pattern(b));
-        table[b] = order_key(x) >= r.cut && x <= r.max ? weight(x, r.max, r.c) / r.z : 0.0;
+        table[b] = x >= low && x <= r.max ? weight(x, r.max, r.c) * scale : 0.0;
     }
 }
 
-// One row: its cut by counting, then the draw from the same registers.
+// One row: its cut by counting, then the draw.
 __global__ __launch_bounds__(FWG, 4) void k_filter_sample_bf16(const char *logits, int V,
                                                                int64_t stride, FilterPtrs f,
                                                                const float *unif, int *tok,
@@ -1234,39 +1435,58 @@ __global__ __launch_bounds__(FWG, 4) void k_filter_sample_bf16(const char *logit
     __shared__ CutLds c;
     __shared__ DrawLds dl;
     __shared__ RedLds red;
-    double *units = reinterpret_cast<double *>(hist);
-    static_assert(sizeof(hist) >= MAX_UNITS_BF16 * sizeof(double), "units fit where the counts were");
     const int n = blockIdx.x;
     const char *row = logits + (size_t)n * stride * 2;
     const Groups<1> gr(row, V);
-    uint4 v[RES];
-    hold(gr, v);
+    uint4 nx[BATCH];
+    load_batch(gr, 0, nx);
     const Params q = load_params(f, n, V);
+    Outside o;
+    Floor fl(q, V, FWAVES);
     clear_hist<FWG>(hist);
+    if (fl.active())                       // what is not counted is looked up all the same
+        for (int b = threadIdx.x; b < HBINS / 2; b += FWG)
+            reinterpret_cast<double2 *>(table)[b] = make_double2(0.0, 0.0);
     cut_lds_clear(c);
     __syncthreads();
-    Outside o;
-    each_unit<true>(gr, v, [&](int, const uint4 &x) SV_INLINE { count_vec(x, hist, c, o); });
-    cut_from_counts<FWG>(hist, c, o, q, V, table);
+    uint64_t batches = 0;
+#pragma nounroll
+    for (int b = 0; b * BATCH < gr.per_wave; ++b) {
+        uint4 v[BATCH];
+        unroll<0, BATCH>([&](auto j) SV_INLINE { v[j] = nx[j]; });
+        if ((b + 1) * BATCH < gr.per_wave)
+            load_batch(gr, (b + 1) * BATCH, nx);
+        if (fl.active()) {
+            unroll<0, BATCH>([&](auto j) SV_INLINE { fl.see(v[j]); });
+            fl.note(c);
+            if (b == 0)
+                __syncthreads();
+            fl.update<FWAVES>(c);
+        }
+        bool any = false;
+        unroll<0, BATCH>([&](auto j) SV_INLINE {
+            if (b * BATCH + j < gr.per_wave && fl.matters(v[j])) {
+                any = true;
+                count_vec(v[j], hist, c, o);
+            }
+        });
+        if (__ballot(any) != 0)
+            batches |= 1ull << b;
+    }
+    if (fl.active())
+        o.bad |= fl.bad();
+    cut_from_counts<FWG>(hist, c, o, q, V, !fl.active(), table);
     RowCut r = c.cut;
-    const bool counted = r.state != CUT_EXACT;
-    if (!counted)
-        r = cut_by_bisection<1>(row, V, q, red);
     int id = -1;
-    if (r.state != CUT_NONE) {
+    const double u = (double)unif[n];
+    if (r.state == CUT_EXACT) {
+        r = cut_by_bisection<1>(row, V, q, red);
+        if (r.state == CUT_READY)
+            id = draw_row(gr, all_batches(gr), MayKeep<1>(r), u, dl, DirectLaw<1>{r, 1.0});
+    } else if (r.state != CUT_NONE) {
         if (r.state == CUT_TIES)
-            r.tie = nth_equal(gr, r.cut, r.tie, reinterpret_cast<uint32_t *>(hist), dl,
-                              [&](auto g) SV_INLINE { each_unit<false>(gr, v, g); });
-        const MayKeep<1> may(r);
-        auto draw = [&](auto law) SV_INLINE {
-            each_unit<false>(gr, v, [&](int i, const uint4 &x) SV_INLINE {
-                sum_unit(gr, i, units, x, may, law);
-            });
-            __syncthreads();
-            return draw_from_units(gr, units, (double)unif[n], dl,
-                                   [&](int i) SV_INLINE { return held_unit(gr, v, i); }, law);
-        };
-        id = counted ? draw(TableLaw{r, 1.0, table}) : draw(DirectLaw<1>{r, 1.0});
+            r.tie = nth_equal(gr, batches, r.cut, r.tie, dl);
+        id = draw_row(gr, batches, MayKeep<1>(r), u, dl, TableLaw(r, V, 1.0, table));
     }
     if (threadIdx.x == 0) {
         tok[n] = id;
@@ -1281,19 +1501,13 @@ __global__ __launch_bounds__(FWG) void k_filter_sample_f32(const char *logits, i
 {
     __shared__ RedLds red;
     __shared__ DrawLds dl;
-    __shared__ double units[MAX_UNITS_F32];
-    const int n = blockIdx.x, lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
+    const int n = blockIdx.x;
     const char *row = logits + (size_t)n * stride * 4;
     const RowCut r = cut_by_bisection<0>(row, V, load_params(f, n, V), red);
     int id = -1;
     if (r.state == CUT_READY) {
         const Groups<0> gr(row, V);
-        const MayKeep<0> may(r);
-        const DirectLaw<0> law{r, 1.0};
-        each_unit(gr, [&](int i, const uint4 &x) { sum_unit(gr, i, units, x, may, law); });
-        __syncthreads();
-        id = draw_from_units(gr, units, (double)unif[n], dl,
-                             [&](int i) { return gr.load(gr.group_of(wv, i, lane)); }, law);
+        id = draw_row(gr, all_batches(gr), MayKeep<0>(r), (double)unif[n], dl, DirectLaw<0>{r, 1.0});
     }
     if (threadIdx.x == 0) {
         tok[n] = id;
@@ -1336,11 +1550,10 @@ __global__ __launch_bounds__(FWG, 4) void k_filter_verify(const char *tgt, const
                                                           float *probs)
 {
     __shared__ double tables[DT == 1 ? 2 : 1][DT == 1 ? HBINS : 1];
-    __shared__ double units[max_units<DT>()];
     __shared__ VerifyLds s;
     __shared__ DrawLds dl;
     __shared__ RedLds red;
-    const int b = blockIdx.x, t = threadIdx.x, lane = t & 63, wv = t >> 6;
+    const int b = blockIdx.x, t = threadIdx.x;
     const size_t rb = (size_t)V * Elt<DT>::BYTES;
     const char *trow = tgt + (size_t)b * (K + 1) * rb, *drow = drf + (size_t)b * K * rb;
     auto row_of = [&](int i) { return i <= K ? trow + i * rb : drow + (i - K - 1) * rb; };
@@ -1412,77 +1625,35 @@ __global__ __launch_bounds__(FWG, 4) void k_filter_verify(const char *tgt, const
     int id = -1;
     if (L >= 0) {
         const Groups<DT> gp(row_of(L), V);
-        uint4 held[RES];
-        hold(gp, held);
-        auto fetch = [&](int i) SV_INLINE { return held_unit(gp, held, i); };
+        uint64_t batches = all_batches(gp);
         RowCut rp = s.cut[L];
-        uint32_t *counts = reinterpret_cast<uint32_t *>(units);
         if constexpr (DT == 1)
-            fill_table(rp, tables[0]);
+            fill_table(rp, 1.0 / rp.z, tables[0]);
         if (rp.state == CUT_TIES)
-            rp.tie = nth_equal(gp, rp.cut, rp.tie, counts, dl,
-                               [&](auto f) SV_INLINE { each_unit<false>(gp, held, f); });
+            rp.tie = nth_equal(gp, batches, rp.cut, rp.tie, dl);
         const double u = (double)unif[(size_t)b * (K + 1) + K];
         const MayKeep<DT> may(rp);
-        auto with_law = [&](auto p, auto q_of) SV_INLINE {
+        const Groups<DT> gq(row_of(L < K ? K + 1 + L : L), V);
+        RowCut rq = s.cut[L < K ? K + 1 + L : L];
+        auto draw = [&](auto p, auto q) SV_INLINE {
             if (L < K) {
-                const Groups<DT> gq(row_of(K + 1 + L), V);
-                RowCut rq = s.cut[K + 1 + L];
-                if constexpr (DT == 1)
-                    fill_table(rq, tables[DT == 1]);
-                if (rq.state == CUT_TIES)
-                    rq.tie = nth_equal(gq, rq.cut, rq.tie, counts, dl,
-                                       [&](auto f) { each_unit(gq, f); });
+                id = draw_row(gp, batches, may, u, dl, ResidualLaw<DT, decltype(p)>{p, q, gq});
                 __syncthreads();
-                const ResidualLaw<DT, decltype(p)> residual{p, q_of(rq), gq};
-                // four units at a time, so that their reads of q overlap
-#pragma nounroll
-                for (int i0 = 0; i0 < gp.per_wave; i0 += 4) {
-                    uint4 pv[4], qv[4];
-                    bool any[4];
-                    if (i0 < RES) {
-                        unroll<0, RES / 4>([&](auto h) SV_INLINE {
-                            if (h * 4 == i0)
-                                unroll<0, 4>([&](auto j) SV_INLINE { pv[j] = held[h * 4 + j]; });
-                        });
-                    } else {
-#pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            pv[j] = gp.load(gp.group_of(wv, i0 + j, lane));
-                    }
-                    unroll<0, 4>([&](auto j) SV_INLINE {
-                        any[j] = i0 + j < gp.per_wave && __ballot(may(pv[j])) != 0;
-                        if (any[j])
-                            qv[j] = gq.load(gq.group_of(wv, i0 + j, lane));
-                    });
-                    unroll<0, 4>([&](auto j) SV_INLINE {
-                        if (i0 + j >= gp.per_wave)
-                            return;
-                        double sum = 0.0;
-                        if (any[j])
-                            sum = wave_incl_scan(
-                                residual.sum(gp.group_of(wv, i0 + j, lane), pv[j], qv[j]));
-                        if (lane == 63)
-                            units[wv * gp.per_wave + i0 + j] = sum;
-                    });
-                }
-                __syncthreads();
-                id = draw_from_units(gp, units, u, dl, fetch, residual);
             }
-            __syncthreads();
-            if (id < 0) {                   // the bonus draw, or nothing left of p - q
-                each_unit<false>(gp, held, [&](int i, const uint4 &v) SV_INLINE {
-                    sum_unit(gp, i, units, v, may, p);
-                });
-                __syncthreads();
-                id = draw_from_units(gp, units, u, dl, fetch, p);
-            }
+            if (id < 0)                     // the bonus draw, or nothing left of p - q
+                id = draw_row(gp, batches, may, u, dl, p);
         };
+        if (L < K) {
+            if constexpr (DT == 1)
+                fill_table(rq, 1.0 / rq.z, tables[DT == 1]);
+            if (rq.state == CUT_TIES)
+                rq.tie = nth_equal(gq, batches, rq.cut, rq.tie, dl);
+        }
+        __syncthreads();
         if constexpr (DT == 1)
-            with_law(TableLaw{rp, rp.z, tables[0]},
-                     [&](const RowCut &r) { return TableLaw{r, r.z, tables[DT == 1]}; });
+            draw(TableLaw(rp, V, 1.0 / rp.z, tables[0]), TableLaw(rq, V, 1.0 / rq.z, tables[DT == 1]));
         else
-            with_law(DirectLaw<DT>{rp, rp.z}, [&](const RowCut &r) { return DirectLaw<DT>{r, r.z}; });
+            draw(DirectLaw<DT>{rp, 1.0 / rp.z}, DirectLaw<DT>{rq, 1.0 / rq.z});
     }
     if (t <= K) {
         const size_t o = (size_t)b * (K + 1) + t;
