@@ -285,30 +285,35 @@ template <int DT> struct Groups {
             __builtin_nontemporal_load(reinterpret_cast<const u32x4_any *>(row + (size_t)g * 16));
         return make_uint4(v.x, v.y, v.z, v.w);
     }
+    // the last, partial group; -inf where it has no id
+    __device__ __forceinline__ uint4 load_partial() const
+    {
+        uint32_t w0 = EMPTY, w1 = EMPTY, w2 = EMPTY, w3 = EMPTY;
+#pragma nounroll
+        for (int id = V - 1; id >= whole * E; --id) {
+            if constexpr (DT == 1) {
+                w3 = __builtin_amdgcn_alignbit(w3, w2, 16);
+                w2 = __builtin_amdgcn_alignbit(w2, w1, 16);
+                w1 = __builtin_amdgcn_alignbit(w1, w0, 16);
+                w0 = w0 << 16 | reinterpret_cast<const uint16_t *>(row)[id];
+            } else {
+                w3 = w2;
+                w2 = w1;
+                w1 = w0;
+                w0 = reinterpret_cast<const uint32_t *>(row)[id];
+            }
+        }
+        return make_uint4(w0, w1, w2, w3);
+    }
     // the group's logits; -inf where it has no id
     __device__ __forceinline__ uint4 load(int g) const
     {
+        uint4 v = make_uint4(EMPTY, EMPTY, EMPTY, EMPTY);
         if (g < whole)
-            return load_whole(g);
-        uint32_t w[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            w[i] = EMPTY;
-        if (g == whole) {
-#pragma unroll
-            for (int k = 0; k < E; ++k) {
-                const int id = g * E + k;
-                if (id >= V)
-                    continue;
-                if constexpr (DT == 1) {
-                    const uint32_t p = reinterpret_cast<const uint16_t *>(row)[id];
-                    w[k / 2] = k & 1 ? (w[k / 2] & 0xffffu) | p << 16 : (w[k / 2] & 0xffff0000u) | p;
-                } else {
-                    w[k] = reinterpret_cast<const uint32_t *>(row)[id];
-                }
-            }
-        }
-        return make_uint4(w[0], w[1], w[2], w[3]);
+            v = load_whole(g);
+        else if (g == whole && whole * E < V)
+            v = load_partial();
+        return v;
     }
 };
 
@@ -909,11 +914,34 @@ __global__ __launch_bounds__(RWG, 8) void k_filter_rows_bf16(const char *tgt, co
 // u * total, and that wave goes over its units again, in order, to the unit, the lane and the id.
 // All sums have a fixed order.
 
+constexpr int LIST = 256;  // groups that matter in a wave's range, if they are so few
+
 struct DrawLds {
     double batch[FWAVES][64];
     double wave[FWAVES];
     uint32_t ties[FWAVES];
+    uint16_t list[FWAVES][LIST];
     int id;
+};
+
+constexpr int NO_GROUP = 0x7fffffff;
+
+// A wave's groups, in order and 64 to a unit: all of its range, or a list of those that matter.
+template <int DT> struct Units {
+    const Groups<DT> &gr;
+    const uint16_t *list;
+    int n;                 // length of the list, -1 for the whole range
+
+    __device__ __forceinline__ int count() const { return n < 0 ? gr.per_wave : (n + 63) / 64; }
+    // the lane's group of unit i, past the row where it has none
+    __device__ __forceinline__ int group(int i) const
+    {
+        const int lane = threadIdx.x & 63, g0 = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) * gr.per_wave * 64;
+        const int at = i * 64 + lane;
+        if (n < 0)
+            return i < gr.per_wave ? g0 + at : NO_GROUP;
+        return at < n ? g0 + list[at] : NO_GROUP;
+    }
 };
 
 // One of N vectors, the same in all lanes.
@@ -937,30 +965,33 @@ constexpr int BATCH = 4;
 static_assert((MAX_VOCAB / 4 + FWAVES * 64 - 1) / (FWAVES * 64) <= 64 * BATCH, "a bit for every batch");
 
 template <int DT>
-__device__ __forceinline__ void load_batch(const Groups<DT> &gr, int i0, uint4 (&v)[BATCH])
+__device__ __forceinline__ void load_batch(const Units<DT> &un, int i0, uint4 (&v)[BATCH])
 {
-    const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const Groups<DT> &gr = un.gr;
+    const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+    const int g0 = (wv * gr.per_wave + i0) * 64;
+    if (un.n < 0 && i0 + BATCH <= gr.per_wave && g0 + BATCH * 64 <= gr.whole) {
+        unroll<0, BATCH>([&](auto j) SV_INLINE { v[j] = gr.load_whole(g0 + j * 64 + lane); });
+        return;
+    }
     unroll<0, BATCH>([&](auto j) SV_INLINE {
-        const int g = gr.group_of(wv, i0 + j, lane);
+        const int g = un.group(i0 + j);
         v[j] = make_uint4(gr.EMPTY, gr.EMPTY, gr.EMPTY, gr.EMPTY);
-        if (i0 + j < gr.per_wave && g < gr.whole)
+        if (g < gr.whole)
             v[j] = gr.load_whole(g);
     });
     if (gr.whole * gr.E < gr.V) {
-        const int at = gr.whole / 64 - wv * gr.per_wave - i0;      // the partial group's unit
-        if (at >= 0 && at < BATCH && i0 + at < gr.per_wave && (gr.whole & 63) == lane) {
-            const uint4 last = gr.load(gr.whole);
-            unroll<0, BATCH>([&](auto j) SV_INLINE {
-                if (j == at)
-                    v[j] = last;
-            });
-        }
+        const uint4 last = gr.load_partial();
+        unroll<0, BATCH>([&](auto j) SV_INLINE {
+            if (un.group(i0 + j) == gr.whole)
+                v[j] = last;
+        });
     }
 }
 
-template <int DT> __device__ __forceinline__ uint64_t all_batches(const Groups<DT> &gr)
+template <int DT> __device__ __forceinline__ uint64_t all_batches(const Units<DT> &un)
 {
-    const int n = (gr.per_wave + BATCH - 1) / BATCH;
+    const int n = (un.count() + BATCH - 1) / BATCH;
     return n >= 64 ? ~0ull : (1ull << n) - 1;
 }
 
@@ -968,13 +999,12 @@ template <int DT> __device__ __forceinline__ uint64_t all_batches(const Groups<D
 // then done(b) for the batch b, if it had such units.  AHEAD: the next batch is on its way
 // meanwhile.  Returns the batches that had such units.
 template <bool AHEAD, int DT, typename A, typename X, typename F, typename D>
-__device__ __forceinline__ uint64_t walk(const Groups<DT> &gr, uint64_t batches, A may, X aux, F f, D done)
+__device__ __forceinline__ uint64_t walk(const Units<DT> &un, uint64_t batches, A may, X aux, F f, D done)
 {
-    const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
     uint64_t with = 0;
     uint4 nx[BATCH];
     if (AHEAD && batches)
-        load_batch(gr, __builtin_ctzll(batches) * BATCH, nx);
+        load_batch(un, __builtin_ctzll(batches) * BATCH, nx);
 #pragma nounroll
     while (batches) {
         const int b = __builtin_ctzll(batches), i0 = b * BATCH;
@@ -982,18 +1012,18 @@ __device__ __forceinline__ uint64_t walk(const Groups<DT> &gr, uint64_t batches,
         if constexpr (AHEAD)
             unroll<0, BATCH>([&](auto j) SV_INLINE { v[j] = nx[j]; });
         else
-            load_batch(gr, i0, v);
+            load_batch(un, i0, v);
         batches &= batches - 1;
         if (AHEAD && batches)
-            load_batch(gr, __builtin_ctzll(batches) * BATCH, nx);
+            load_batch(un, __builtin_ctzll(batches) * BATCH, nx);
         uint32_t mask = 0;
         unroll<0, BATCH>([&](auto j) SV_INLINE {
-            if (i0 + j < gr.per_wave && __ballot(may(v[j])) != 0) {
+            if (__ballot(may(v[j])) != 0) {
                 mask |= 1u << j;
-                x[j] = aux(gr.group_of(wv, i0 + j, lane));
+                x[j] = aux(un.group(i0 + j));
             }
         });
-        mask = __builtin_amdgcn_readfirstlane(mask);
+        mask = __builtin_amdgcn_readfirstlane(mask) & ((2u << min(un.count() - 1 - i0, BATCH - 1)) - 1);
         if (!mask)
             continue;
         with |= 1ull << b;
@@ -1012,11 +1042,12 @@ __device__ __forceinline__ uint64_t walk(const Groups<DT> &gr, uint64_t batches,
 // is the weight of a group, law.one(logit, id) that of one id.  Returns the id in every thread, -1 if
 // all weights are 0.
 template <int DT, typename A, typename W>
-__device__ __forceinline__ int draw_row(const Groups<DT> &gr, uint64_t batches, A may, double u,
-                                        DrawLds &lds, const W &law)
+__device__ __forceinline__ int draw_row(const Units<DT> &un, A may, double u, DrawLds &lds,
+                                        const W &law)
 {
     constexpr int E = Elt<DT>::EPV;
     const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
+    uint64_t batches = all_batches(un);
     if (threadIdx.x == 0)
         lds.id = -1;
     double base = 0.0, goal = INFINITY, mine = 0.0, all = 0.0;
@@ -1025,9 +1056,9 @@ __device__ __forceinline__ int draw_row(const Groups<DT> &gr, uint64_t batches, 
 #pragma nounroll
     for (int pass = 0; pass < 2; ++pass) {
         batches = walk<W::AHEAD>(
-            gr, batches, may, [&](int g) SV_INLINE { return law.aux(g); },
+            un, batches, may, [&](int g) SV_INLINE { return law.aux(g); },
             [&](int i, const uint4 &v, const uint4 &x4) SV_INLINE {
-                const double s = law.sum(gr.group_of(wv, i, lane), v, x4);
+                const double s = law.sum(un.group(i), v, x4);
                 if (!search) {
                     mine += s;
                 } else if (unit < 0) {
@@ -1090,8 +1121,8 @@ __device__ __forceinline__ int draw_row(const Groups<DT> &gr, uint64_t batches, 
             unit = last;
             goal = INFINITY;
         }
-        const int g = gr.group_of(wv, unit, lane);
-        const uint4 v = gr.load(g);
+        const int g = un.group(unit);
+        const uint4 v = un.gr.load(g);
         const double s = law.sum(g, v, law.aux(g)), inc = wave_incl_scan(s);
         const unsigned long long pos = __ballot(s > 0.0);
         const unsigned long long over = __ballot(s > 0.0 && base + inc > goal);
@@ -1100,11 +1131,11 @@ __device__ __forceinline__ int draw_row(const Groups<DT> &gr, uint64_t batches, 
         // lane k: the group's k-th id
         uint32_t w[4] = {(uint32_t)lane_value((int)v.x, l), (uint32_t)lane_value((int)v.y, l),
                          (uint32_t)lane_value((int)v.z, l), (uint32_t)lane_value((int)v.w, l)};
-        const int k = lane % E, id = gr.group_of(wv, unit, l) * E + k;
+        const int k = lane % E, id = lane_value(g, l) * E + k;
         const int word = DT == 1 ? k / 2 : k;
         const uint32_t b = word == 0 ? w[0] : word == 1 ? w[1] : word == 2 ? w[2] : w[3];
         const float y = DT == 1 ? pattern_value(k & 1 ? b >> 16 : b & 0xffffu) : __uint_as_float(b);
-        const double x = lane < E && id < gr.V ? law.one(y, id) : 0.0, xi = wave_incl_scan(x);
+        const double x = lane < E && id < un.gr.V ? law.one(y, id) : 0.0, xi = wave_incl_scan(x);
         const unsigned long long xpos = __ballot(x > 0.0);
         const unsigned long long xover = __ballot(x > 0.0 && over && base + xi > goal);
         if (lane == (xover ? __ffsll(xover) - 1 : 63 - __clzll(xpos)))
@@ -1147,9 +1178,9 @@ template <int DT> __device__ __forceinline__ uint32_t equal_count(const uint4 &v
 // The last kept id among those equal to the cut, the n-th of them: equals per wave, then the
 // unit, the lane and the id.
 template <int DT>
-__device__ __forceinline__ int nth_equal(const Groups<DT> &gr, uint64_t batches, uint32_t cut, int n,
-                                         DrawLds &lds)
+__device__ __forceinline__ int nth_equal(const Units<DT> &un, uint32_t cut, int n, DrawLds &lds)
 {
+    uint64_t batches = all_batches(un);
     constexpr int E = Elt<DT>::EPV;
     const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
     const float y = key_value(cut);
@@ -1163,7 +1194,7 @@ __device__ __forceinline__ int nth_equal(const Groups<DT> &gr, uint64_t batches,
 #pragma nounroll
     for (int pass = 0; pass < 2; ++pass) {
         batches = walk<true>(
-            gr, batches, may, none,
+            un, batches, may, none,
             [&](int i, const uint4 &v, const uint4 &) SV_INLINE {
                 uint32_t m = equal_mask<DT>(v, y);
                 const int c = __popc(m);
@@ -1175,7 +1206,7 @@ __device__ __forceinline__ int nth_equal(const Groups<DT> &gr, uint64_t batches,
                 if (b < n && n <= inc) {
                     for (int skip = n - b - 1; skip > 0; --skip)
                         m &= m - 1;
-                    lds.id = gr.group_of(wv, i, lane) * E + __ffs(m) - 1;
+                    lds.id = un.group(i) * E + __ffs(m) - 1;
                 }
                 before = lane_value(inc, 63);
             },
@@ -1312,13 +1343,13 @@ struct TableLaw {
         uint32_t out = 0;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            t[i] = window_words(vec_word(v, i));
+            t[i] = g == NO_GROUP ? 0u : window_words(vec_word(v, i));
             out |= t[i] & 0x70007000u;
         }
-        return __ballot(out != 0 || (g * 8 <= r.tie && g * 8 + 7 > r.tie)) == 0;
+        return __ballot(out != 0 || g == r.tie / 8) == 0;
     }
     // what a group past the last kept tie must not look up
-    __device__ __forceinline__ uint32_t left_out(int g) const { return g * 8 > r.tie ? cut_off : ~0u; }
+    __device__ __forceinline__ uint32_t left_out(int g) const { return g > r.tie / 8 ? cut_off : ~0u; }
     __device__ __forceinline__ double at(uint32_t off, uint32_t without) const
     {
         const double x = at(off);
@@ -1337,6 +1368,7 @@ struct TableLaw {
                 s += at(b & 0xffffu, no);
                 s += at(b >> 16, no);
             }
+            s = g == NO_GROUP ? 0.0 : s;       // whatever bin 0 holds
         } else {
             uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma nounroll
@@ -1353,15 +1385,21 @@ template <int DT, typename P> struct ResidualLaw {
     static constexpr bool AHEAD = false;     // two rows: the registers hold one batch of each
     P p, q;
     Groups<DT> gq;
+    bool both;                     // false: p alone
     __device__ __forceinline__ double one(float y, int id) const
     {
         const double x = p.one(y, id);
-        return x > 0.0 ? fmax(x - q.one(Elt<DT>::one(gq.row, id), id), 0.0) : 0.0;
+        return x > 0.0 && !both ? x : x > 0.0 ? fmax(x - q.one(Elt<DT>::one(gq.row, id), id), 0.0) : 0.0;
     }
-    __device__ __forceinline__ uint4 aux(int g) const { return gq.load(g); }
+    __device__ __forceinline__ uint4 aux(int g) const
+    {
+        return both ? gq.load(g) : make_uint4(0, 0, 0, 0);
+    }
     __device__ __forceinline__ double sum(int g, const uint4 &pv, const uint4 &qv) const
     {
         double s = 0.0;
+        if (!both)
+            return p.sum(g, pv, qv);
         if constexpr (DT == 1) {
             uint32_t tp[4], tq[4];
             const bool a = p.by_table(g, pv, tp), b = q.by_table(g, qv, tq);
@@ -1373,7 +1411,7 @@ template <int DT, typename P> struct ResidualLaw {
                     s += fmax(p.at(op & 0xffffu, np) - q.at(oq & 0xffffu, nq), 0.0);
                     s += fmax(p.at(op >> 16, np) - q.at(oq >> 16, nq), 0.0);
                 }
-                return s;
+                return g == NO_GROUP ? 0.0 : s;
             }
         }
         uint32_t wp[4] = {pv.x, pv.y, pv.z, pv.w}, wq[4] = {qv.x, qv.y, qv.z, qv.w};
@@ -1437,9 +1475,11 @@ __global__ __launch_bounds__(FWG, 4) void k_filter_sample_bf16(const char *logit
     __shared__ RedLds red;
     const int n = blockIdx.x;
     const char *row = logits + (size_t)n * stride * 2;
+    const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
     const Groups<1> gr(row, V);
+    const Units<1> all{gr, nullptr, -1};
     uint4 nx[BATCH];
-    load_batch(gr, 0, nx);
+    load_batch(all, 0, nx);
     const Params q = load_params(f, n, V);
     Outside o;
     Floor fl(q, V, FWAVES);
@@ -1449,29 +1489,33 @@ __global__ __launch_bounds__(FWG, 4) void k_filter_sample_bf16(const char *logit
             reinterpret_cast<double2 *>(table)[b] = make_double2(0.0, 0.0);
     cut_lds_clear(c);
     __syncthreads();
-    uint64_t batches = 0;
+    int listed = 0;
 #pragma nounroll
-    for (int b = 0; b * BATCH < gr.per_wave; ++b) {
+    for (int i0 = 0; i0 < gr.per_wave; i0 += BATCH) {
         uint4 v[BATCH];
         unroll<0, BATCH>([&](auto j) SV_INLINE { v[j] = nx[j]; });
-        if ((b + 1) * BATCH < gr.per_wave)
-            load_batch(gr, (b + 1) * BATCH, nx);
+        if (i0 + BATCH < gr.per_wave)
+            load_batch(all, i0 + BATCH, nx);
         if (fl.active()) {
             unroll<0, BATCH>([&](auto j) SV_INLINE { fl.see(v[j]); });
             fl.note(c);
-            if (b == 0)
+            if (i0 == 0)
                 __syncthreads();
             fl.update<FWAVES>(c);
         }
-        bool any = false;
         unroll<0, BATCH>([&](auto j) SV_INLINE {
-            if (b * BATCH + j < gr.per_wave && fl.matters(v[j])) {
-                any = true;
-                count_vec(v[j], hist, c, o);
+            const bool m = i0 + j < gr.per_wave && fl.matters(v[j]);
+            const unsigned long long who = __ballot(m);
+            if (who) {
+                const int at = listed + (int)__builtin_amdgcn_mbcnt_hi(
+                                   (uint32_t)(who >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)who, 0));
+                listed += __popcll(who);
+                if (m && listed <= LIST)
+                    dl.list[wv][at] = (uint16_t)((i0 + j) * 64 + lane);
+                if (m)
+                    count_vec(v[j], hist, c, o);
             }
         });
-        if (__ballot(any) != 0)
-            batches |= 1ull << b;
     }
     if (fl.active())
         o.bad |= fl.bad();
@@ -1482,11 +1526,12 @@ __global__ __launch_bounds__(FWG, 4) void k_filter_sample_bf16(const char *logit
     if (r.state == CUT_EXACT) {
         r = cut_by_bisection<1>(row, V, q, red);
         if (r.state == CUT_READY)
-            id = draw_row(gr, all_batches(gr), MayKeep<1>(r), u, dl, DirectLaw<1>{r, 1.0});
+            id = draw_row(all, MayKeep<1>(r), u, dl, DirectLaw<1>{r, 1.0});
     } else if (r.state != CUT_NONE) {
+        const Units<1> few{gr, dl.list[wv], listed <= LIST ? __builtin_amdgcn_readfirstlane(listed) : -1};
         if (r.state == CUT_TIES)
-            r.tie = nth_equal(gr, batches, r.cut, r.tie, dl);
-        id = draw_row(gr, batches, MayKeep<1>(r), u, dl, TableLaw(r, V, 1.0, table));
+            r.tie = nth_equal(few, r.cut, r.tie, dl);
+        id = draw_row(few, MayKeep<1>(r), u, dl, TableLaw(r, V, 1.0, table));
     }
     if (threadIdx.x == 0) {
         tok[n] = id;
@@ -1507,7 +1552,7 @@ __global__ __launch_bounds__(FWG) void k_filter_sample_f32(const char *logits, i
     int id = -1;
     if (r.state == CUT_READY) {
         const Groups<0> gr(row, V);
-        id = draw_row(gr, all_batches(gr), MayKeep<0>(r), (double)unif[n], dl, DirectLaw<0>{r, 1.0});
+        id = draw_row(Units<0>{gr, nullptr, -1}, MayKeep<0>(r), (double)unif[n], dl, DirectLaw<0>{r, 1.0});
     }
     if (threadIdx.x == 0) {
         tok[n] = id;
@@ -1549,7 +1594,7 @@ __global__ __launch_bounds__(FWG, 4) void k_filter_verify(const char *tgt, const
                                                           const RowCut *cuts, int *acc, int *out,
                                                           float *probs)
 {
-    __shared__ double tables[DT == 1 ? 2 : 1][DT == 1 ? HBINS : 1];
+    __shared__ __align__(16) double tables[2][DT == 1 ? HBINS : 1];
     __shared__ VerifyLds s;
     __shared__ DrawLds dl;
     __shared__ RedLds red;
@@ -1624,34 +1669,36 @@ __global__ __launch_bounds__(FWG, 4) void k_filter_verify(const char *tgt, const
     const int L = s.L;
     int id = -1;
     if (L >= 0) {
-        const Groups<DT> gp(row_of(L), V);
-        uint64_t batches = all_batches(gp);
-        RowCut rp = s.cut[L];
-        if constexpr (DT == 1)
-            fill_table(rp, 1.0 / rp.z, tables[0]);
-        if (rp.state == CUT_TIES)
-            rp.tie = nth_equal(gp, batches, rp.cut, rp.tie, dl);
-        const double u = (double)unif[(size_t)b * (K + 1) + K];
-        const MayKeep<DT> may(rp);
-        const Groups<DT> gq(row_of(L < K ? K + 1 + L : L), V);
-        RowCut rq = s.cut[L < K ? K + 1 + L : L];
-        auto draw = [&](auto p, auto q) SV_INLINE {
-            if (L < K) {
-                id = draw_row(gp, batches, may, u, dl, ResidualLaw<DT, decltype(p)>{p, q, gq});
-                __syncthreads();
-            }
-            if (id < 0)                     // the bonus draw, or nothing left of p - q
-                id = draw_row(gp, batches, may, u, dl, p);
-        };
-        if (L < K) {
+        // p's row, and q's where there is one
+        const Groups<DT> gp(row_of(L), V), gq(row_of(L < K ? K + 1 + L : L), V);
+        const Units<DT> up{gp, nullptr, -1};
+        RowCut rp = s.cut[L], rq = s.cut[L < K ? K + 1 + L : L];
+#pragma nounroll
+        for (int side = 0; side < (L < K ? 2 : 1); ++side) {
+            RowCut r = side ? rq : rp;
             if constexpr (DT == 1)
-                fill_table(rq, 1.0 / rq.z, tables[DT == 1]);
-            if (rq.state == CUT_TIES)
-                rq.tie = nth_equal(gq, batches, rq.cut, rq.tie, dl);
+                fill_table(r, 1.0 / r.z, tables[side]);
+            if (r.state == CUT_TIES)
+                r.tie = nth_equal(Units<DT>{side ? gq : gp, nullptr, -1}, r.cut, r.tie, dl);
+            if (side)
+                rq = r;
+            else
+                rp = r;
         }
         __syncthreads();
+        const double u = (double)unif[(size_t)b * (K + 1) + K];
+        auto draw = [&](auto p, auto q) SV_INLINE {
+            // the residual; then, where nothing is left of p - q, p
+#pragma nounroll
+            for (bool both = L < K;; both = false) {
+                id = draw_row(up, MayKeep<DT>(rp), u, dl, ResidualLaw<DT, decltype(p)>{p, q, gq, both});
+                if (id >= 0 || !both)
+                    break;
+                __syncthreads();
+            }
+        };
         if constexpr (DT == 1)
-            draw(TableLaw(rp, V, 1.0 / rp.z, tables[0]), TableLaw(rq, V, 1.0 / rq.z, tables[DT == 1]));
+            draw(TableLaw(rp, V, 1.0 / rp.z, tables[0]), TableLaw(rq, V, 1.0 / rq.z, tables[1]));
         else
             draw(DirectLaw<DT>{rp, 1.0 / rp.z}, DirectLaw<DT>{rq, 1.0 / rq.z});
     }
