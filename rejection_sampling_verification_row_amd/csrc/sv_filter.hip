@@ -392,20 +392,16 @@ __device__ __forceinline__ void cut_lds_clear(CutLds &c)
         c.rth[threadIdx.x] = c.top[threadIdx.x] = 0;
 }
 
-// What a thread meets outside the window.
-struct Outside {
-    uint32_t zeros = 0, low = 0, bad = 0;
-};
-
-__device__ __forceinline__ void count_outside(uint32_t p, CutLds &c, Outside &o)
+__device__ __forceinline__ void count_outside(uint32_t p, CutLds &c)
 {
     const uint32_t a = p & 0x7fffu;
     if (a == 0) {
-        o.zeros++;
+        atomicAdd(&c.zeros, 1u);
     } else if (a >= 0x7f80u) {
-        o.bad |= p != 0xff80u;
+        if (p != 0xff80u)
+            atomicOr(&c.bad, 1u);
     } else if ((p & 0x8000u) && a >= HLO) {
-        o.low = max(o.low, order_key(pattern_value(p)));
+        atomicMax(&c.low, order_key(pattern_value(p)));
     } else {
         const uint32_t i = atomicAdd(&c.nx, 1u);
         if (i < HX)
@@ -420,7 +416,7 @@ __device__ __forceinline__ void bump(uint32_t *hist, uint32_t off)
 
 // Counts eight patterns.  The common case, all lanes inside the window, takes seven VALU
 // instructions for two patterns and one LDS add for each.
-__device__ __forceinline__ void count_vec(const uint4 &v, uint32_t *hist, CutLds &c, Outside &o)
+__device__ __forceinline__ void count_vec(const uint4 &v, uint32_t *hist, CutLds &c)
 {
     uint32_t t[4], out = 0;
 #pragma unroll
@@ -444,7 +440,7 @@ __device__ __forceinline__ void count_vec(const uint4 &v, uint32_t *hist, CutLds
             if ((u & 0x7000u) == 0)
                 bump(hist, bin_offsets(u) & 0xffffu);
             else
-                count_outside(p, c, o);
+                count_outside(p, c);
             w0 = __builtin_amdgcn_alignbit(w1, w0, 16);
             w1 = __builtin_amdgcn_alignbit(w2, w1, 16);
             w2 = __builtin_amdgcn_alignbit(w3, w2, 16);
@@ -636,18 +632,12 @@ __device__ __forceinline__ void order_entry(int row, const uint32_t *hist, const
 // table[bin] receives the weight of every bin that occurs and is kept, and 0 of every bin that
 // occurs and is not.  `whole`: every id was counted, not just those that matter.
 template <int WGT>
-__device__ __forceinline__ void cut_from_counts(const uint32_t *hist, CutLds &c, const Outside &o,
-                                                const Params &q, int V, bool whole, double *table)
+__device__ __forceinline__ void cut_from_counts(const uint32_t *hist, CutLds &c, const Params &q, int V,
+                                                bool whole, double *table)
 {
     constexpr int NW = WGT / 64, R = order_rows(WGT);
     static_assert(R * NW <= 64, "a lane for every order row and wave");
     const int t = threadIdx.x, lane = t & 63, wv = t >> 6;
-    if (o.zeros)
-        atomicAdd(&c.zeros, o.zeros);
-    if (o.low)
-        atomicMax(&c.low, o.low);
-    if (o.bad)
-        atomicOr(&c.bad, 1u);
     __syncthreads();
     if (wv == 0)
         order_outside(c);
@@ -840,8 +830,7 @@ __device__ __forceinline__ void cut_from_counts(const uint32_t *hist, CutLds &c,
 constexpr int COUNT_LOADS = 4;
 
 template <int WGT>
-__device__ __forceinline__ void count_row(const Groups<1> &gr, Floor &fl, uint32_t *hist, CutLds &c,
-                                          Outside &o)
+__device__ __forceinline__ void count_row(const Groups<1> &gr, Floor &fl, uint32_t *hist, CutLds &c)
 {
     constexpr int U = COUNT_LOADS, NW = WGT / 64;
     const int t = threadIdx.x;
@@ -849,11 +838,16 @@ __device__ __forceinline__ void count_row(const Groups<1> &gr, Floor &fl, uint32
     for (int i = 0; i * U * WGT < gr.whole; ++i) {
         const int g = i * U * WGT + t;
         uint4 v[U];
-        unroll<0, U>([&](auto k) SV_INLINE {
-            v[k] = make_uint4(gr.EMPTY, gr.EMPTY, gr.EMPTY, gr.EMPTY);
-            if (g + k * WGT < gr.whole)
-                v[k] = gr.load_once(g + k * WGT);
-        });
+        const bool full = (i + 1) * U * WGT <= gr.whole;
+        if (full) {
+            unroll<0, U>([&](auto k) SV_INLINE { v[k] = gr.load_once(g + k * WGT); });
+        } else {
+            unroll<0, U>([&](auto k) SV_INLINE {
+                v[k] = make_uint4(gr.EMPTY, gr.EMPTY, gr.EMPTY, gr.EMPTY);
+                if (g + k * WGT < gr.whole)
+                    v[k] = gr.load_once(g + k * WGT);
+            });
+        }
         if (fl.active()) {
             unroll<0, U>([&](auto k) SV_INLINE { fl.see(v[k]); });
             if ((i & (i + 1)) == 0) {
@@ -863,18 +857,22 @@ __device__ __forceinline__ void count_row(const Groups<1> &gr, Floor &fl, uint32
                 fl.template update<NW>(c);
             }
         }
-        unroll<0, U>([&](auto k) SV_INLINE {
-            if (g + k * WGT < gr.whole && fl.matters(v[k]))
-                count_vec(v[k], hist, c, o);
-        });
+        if (full && fl.below == 0) {
+            unroll<0, U>([&](auto k) SV_INLINE { count_vec(v[k], hist, c); });
+        } else {
+            unroll<0, U>([&](auto k) SV_INLINE {
+                if (g + k * WGT < gr.whole && fl.matters(v[k]))
+                    count_vec(v[k], hist, c);
+            });
+        }
     }
     if (t == 0 && gr.whole * 8 < gr.V) {
-        const uint4 x = gr.load(gr.whole);
+        const uint4 x = gr.load_partial();
         fl.see(x);
-        count_vec(x, hist, c, o);
+        count_vec(x, hist, c);
     }
-    if (fl.active())
-        o.bad |= fl.bad();
+    if (fl.active() && fl.bad())
+        atomicOr(&c.bad, 1u);
 }
 
 template <int WGT> __device__ __forceinline__ void clear_hist(uint32_t *hist)
@@ -899,10 +897,9 @@ __global__ __launch_bounds__(RWG, 8) void k_filter_rows_bf16(const char *tgt, co
     clear_hist<RWG>(hist);
     cut_lds_clear(c);
     __syncthreads();
-    Outside o;
     Floor fl(q, V, RWG / 64);
-    count_row<RWG>(Groups<1>(row, V), fl, hist, c, o);
-    cut_from_counts<RWG>(hist, c, o, q, V, !fl.active(), nullptr);
+    count_row<RWG>(Groups<1>(row, V), fl, hist, c);
+    cut_from_counts<RWG>(hist, c, q, V, !fl.active(), nullptr);
     if (threadIdx.x == 0)
         cuts[n] = c.cut;
 }
@@ -919,12 +916,10 @@ constexpr int LIST = 256;  // groups that matter in a wave's range, if they are 
 struct DrawLds {
     double batch[FWAVES][64];
     double wave[FWAVES];
-    uint32_t ties[FWAVES];
+    int ties[2][FWAVES], tie_id[2];
     uint16_t list[FWAVES][LIST];
     int id;
 };
-
-constexpr int NO_GROUP = 0x7fffffff;
 
 // A wave's groups, in order and 64 to a unit: all of its range, or a list of those that matter.
 template <int DT> struct Units {
@@ -932,15 +927,25 @@ template <int DT> struct Units {
     const uint16_t *list;
     int n;                 // length of the list, -1 for the whole range
 
-    __device__ __forceinline__ int count() const { return n < 0 ? gr.per_wave : (n + 63) / 64; }
-    // the lane's group of unit i, past the row where it has none
+    __device__ __forceinline__ int first() const
+    {
+        return __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) * gr.per_wave * 64;
+    }
+    // units that hold a group of the row
+    __device__ __forceinline__ int count() const
+    {
+        const int groups = (gr.V + gr.E - 1) / gr.E;
+        return n < 0 ? max(0, min(gr.per_wave, (groups - first() + 63) / 64)) : (n + 63) / 64;
+    }
+    // the lane's group of unit i; past the row or the list's end, one that holds() is false for
     __device__ __forceinline__ int group(int i) const
     {
-        const int lane = threadIdx.x & 63, g0 = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) * gr.per_wave * 64;
-        const int at = i * 64 + lane;
-        if (n < 0)
-            return i < gr.per_wave ? g0 + at : NO_GROUP;
-        return at < n ? g0 + list[at] : NO_GROUP;
+        const int at = i * 64 + (threadIdx.x & 63);
+        return n < 0 ? first() + at : first() + list[at < n ? at : i * 64];
+    }
+    __device__ __forceinline__ bool holds(int i) const
+    {
+        return n < 0 || i * 64 + (int)(threadIdx.x & 63) < n;
     }
 };
 
@@ -968,22 +973,23 @@ template <int DT>
 __device__ __forceinline__ void load_batch(const Units<DT> &un, int i0, uint4 (&v)[BATCH])
 {
     const Groups<DT> &gr = un.gr;
-    const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
-    const int g0 = (wv * gr.per_wave + i0) * 64;
-    if (un.n < 0 && i0 + BATCH <= gr.per_wave && g0 + BATCH * 64 <= gr.whole) {
+    const int units = un.count(), g0 = un.first() + i0 * 64, lane = threadIdx.x & 63;
+    if (un.n < 0 && i0 + BATCH <= units && g0 + BATCH * 64 <= gr.whole) {
         unroll<0, BATCH>([&](auto j) SV_INLINE { v[j] = gr.load_whole(g0 + j * 64 + lane); });
         return;
     }
     unroll<0, BATCH>([&](auto j) SV_INLINE {
-        const int g = un.group(i0 + j);
         v[j] = make_uint4(gr.EMPTY, gr.EMPTY, gr.EMPTY, gr.EMPTY);
-        if (g < gr.whole)
-            v[j] = gr.load_whole(g);
+        if (i0 + j < units) {
+            const int g = un.group(i0 + j);
+            if (g < gr.whole)
+                v[j] = gr.load_whole(g);
+        }
     });
     if (gr.whole * gr.E < gr.V) {
         const uint4 last = gr.load_partial();
         unroll<0, BATCH>([&](auto j) SV_INLINE {
-            if (un.group(i0 + j) == gr.whole)
+            if (i0 + j < units && un.group(i0 + j) == gr.whole)
                 v[j] = last;
         });
     }
@@ -995,150 +1001,130 @@ template <int DT> __device__ __forceinline__ uint64_t all_batches(const Units<DT
     return n >= 64 ? ~0ull : (1ull << n) - 1;
 }
 
-// f(i, vec, aux(g)) for the units of the noted batches that may() something in, one body for all;
-// then done(b) for the batch b, if it had such units.  AHEAD: the next batch is on its way
-// meanwhile.  Returns the batches that had such units.
-template <bool AHEAD, int DT, typename A, typename X, typename F, typename D>
-__device__ __forceinline__ uint64_t walk(const Units<DT> &un, uint64_t batches, A may, X aux, F f, D done)
+// The units of batch i0 that may() something in, as a mask, and their aux() groups.
+template <int DT, typename A, typename W>
+__device__ __forceinline__ uint32_t look(const Units<DT> &un, int i0, const uint4 (&v)[BATCH],
+                                         uint4 (&x)[BATCH], A may, const W &law)
 {
-    uint64_t with = 0;
-    uint4 nx[BATCH];
-    if (AHEAD && batches)
-        load_batch(un, __builtin_ctzll(batches) * BATCH, nx);
-#pragma nounroll
-    while (batches) {
-        const int b = __builtin_ctzll(batches), i0 = b * BATCH;
-        uint4 v[BATCH], x[BATCH];
-        if constexpr (AHEAD)
-            unroll<0, BATCH>([&](auto j) SV_INLINE { v[j] = nx[j]; });
-        else
-            load_batch(un, i0, v);
-        batches &= batches - 1;
-        if (AHEAD && batches)
-            load_batch(un, __builtin_ctzll(batches) * BATCH, nx);
-        uint32_t mask = 0;
-        unroll<0, BATCH>([&](auto j) SV_INLINE {
-            if (__ballot(may(v[j])) != 0) {
-                mask |= 1u << j;
-                x[j] = aux(un.group(i0 + j));
-            }
-        });
-        mask = __builtin_amdgcn_readfirstlane(mask) & ((2u << min(un.count() - 1 - i0, BATCH - 1)) - 1);
-        if (!mask)
-            continue;
-        with |= 1ull << b;
-#pragma nounroll
-        for (; mask; mask &= mask - 1) {
-            const int j = __builtin_ctz(mask);
-            f(i0 + j, choose(v, j), choose(x, j));
+    uint32_t mask = 0;
+    const int units = un.count();
+    unroll<0, BATCH>([&](auto j) SV_INLINE {
+        if (i0 + j < units && __ballot(may(v[j])) != 0) {
+            mask |= 1u << j;
+            x[j] = law.aux(un.group(i0 + j));
         }
-        done(b);
-    }
-    return with;
+    });
+    return __builtin_amdgcn_readfirstlane(mask);
 }
 
-// The draw.  First every wave sums its batches, then the wave that holds the id goes over the
-// batch that holds it; both by the same code, which is then at hand.  law.sum(g, vec, law.aux(g))
-// is the weight of a group, law.one(logit, id) that of one id.  Returns the id in every thread, -1 if
-// all weights are 0.
+// The draw.  Every wave sums its batches of units; the wave that holds the id then looks again at
+// the batch that holds it.  law.sum(g, vec, law.aux(g)) is the weight of a group, law.one(logit, id)
+// that of one id.  Returns the id in every thread, -1 if all weights are 0.
 template <int DT, typename A, typename W>
 __device__ __forceinline__ int draw_row(const Units<DT> &un, A may, double u, DrawLds &lds,
                                         const W &law)
 {
     constexpr int E = Elt<DT>::EPV;
-    const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
-    uint64_t batches = all_batches(un);
+    const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6, units = un.count();
     if (threadIdx.x == 0)
         lds.id = -1;
-    double base = 0.0, goal = INFINITY, mine = 0.0, all = 0.0;
-    int unit = -1, last = -1;
-    bool search = false;
+    uint64_t with = 0;             // batches with some weight
+    double all = 0.0;
+    uint4 nx[BATCH];
+    if (W::AHEAD)
+        load_batch(un, 0, nx);
 #pragma nounroll
-    for (int pass = 0; pass < 2; ++pass) {
-        batches = walk<W::AHEAD>(
-            un, batches, may, [&](int g) SV_INLINE { return law.aux(g); },
-            [&](int i, const uint4 &v, const uint4 &x4) SV_INLINE {
-                const double s = law.sum(un.group(i), v, x4);
-                if (!search) {
-                    mine += s;
-                } else if (unit < 0) {
-                    const double x = lane_value(wave_incl_scan(s), 63);
-                    if (x > 0.0) {
-                        last = i;
-                        if (base + x > goal)
-                            unit = i;
-                        else
-                            base += x;
-                    }
-                }
-            },
-            [&](int b) SV_INLINE {
-                const double s = lane_value(wave_incl_scan(mine), 63);
-                mine = 0.0;
-                all += s;
-                if (!search && lane == 0)
-                    lds.batch[wv][b] = s;
-            });
-        if (search)
-            break;
-        if (lane == 0)
-            lds.wave[wv] = all;
-        __syncthreads();
-        // lane w: wave w's sum
-        const double ws = lane < FWAVES ? lds.wave[lane] : 0.0, wi = wave_incl_scan(ws);
-        goal = u * lane_value(wi, 63);
-        const unsigned long long pos = __ballot(ws > 0.0), over = __ballot(ws > 0.0 && wi > goal);
-        const int pick = over ? __ffsll(over) - 1 : pos ? 63 - __clzll(pos) : -1;
-        if (__builtin_amdgcn_readfirstlane(wv) != pick)
-            break;
-        base = lane_value(wave_excl_from_incl(wi), pick);
-        search = true;
-        // the batch; where rounding leaves none, here or below, the last of positive weight
+    for (int i0 = 0; i0 < units; i0 += BATCH) {
+        uint4 v[BATCH], x[BATCH];
+        if constexpr (W::AHEAD) {
+            unroll<0, BATCH>([&](auto j) SV_INLINE { v[j] = nx[j]; });
+            if (i0 + BATCH < units)
+                load_batch(un, i0 + BATCH, nx);
+        } else {
+            load_batch(un, i0, v);
+        }
+        const uint32_t mask = look(un, i0, v, x, may, law);
+        if (!mask)
+            continue;
+        double mine = 0.0;
+        unroll<0, BATCH>([&](auto j) SV_INLINE {
+            if (mask >> j & 1) {
+                const double s = law.sum(un.group(i0 + j), v[j], x[j]);
+                mine += un.holds(i0 + j) ? s : 0.0;
+            }
+        });
+        const double s = lane_value(wave_incl_scan(mine), 63);
+        if (s > 0.0) {
+            with |= 1ull << i0 / BATCH;
+            all += s;
+            if (lane == 0)
+                lds.batch[wv][i0 / BATCH] = s;
+        }
+    }
+    if (lane == 0)
+        lds.wave[wv] = all;
+    __syncthreads();
+    // lane w: wave w's sum
+    const double ws = lane < FWAVES ? lds.wave[lane] : 0.0, wi = wave_incl_scan(ws);
+    double goal = u * lane_value(wi, 63);
+    const unsigned long long pos = __ballot(ws > 0.0), over = __ballot(ws > 0.0 && wi > goal);
+    const int pick = over ? __ffsll(over) - 1 : pos ? 63 - __clzll(pos) : -1;
+    if (__builtin_amdgcn_readfirstlane(wv) == pick) {
+        // where rounding leaves no batch, unit, lane or id above the goal: the last of positive weight
         if (!over)
             goal = INFINITY;
-        uint64_t m = batches;
-        double lastbase = base;
+        double base = lane_value(wave_excl_from_incl(wi), pick), before = base;
         bool found = false;
         int at = 0;
 #pragma nounroll
-        for (; m && !found; m &= m - 1) {
-            const int b = __builtin_ctzll(m);
-            const double x = lds.batch[wv][b];
-            if (x > 0.0) {
-                at = b;
-                lastbase = base;
-                found = base + x > goal;
-                base += x;
+        for (; with && !found; with &= with - 1) {
+            at = __builtin_ctzll(with);
+            const double s = lds.batch[wv][at];
+            before = base;
+            base += s;
+            found = base > goal;
+        }
+        if (!found)
+            goal = INFINITY;
+        base = before;
+        uint4 v[BATCH], x[BATCH], uv = make_uint4(0, 0, 0, 0);
+        load_batch(un, at * BATCH, v);
+        uint32_t mask = look(un, at * BATCH, v, x, may, law);
+        double us = 0.0;           // the unit's: lane sums, groups, what lies before
+        int ug = 0;
+        found = false;
+#pragma nounroll
+        for (; mask && !found; mask &= mask - 1) {
+            const int j = __builtin_ctz(mask), i = at * BATCH + j, g = un.group(i);
+            const uint4 w = choose(v, j);
+            const double s0 = law.sum(g, w, choose(x, j)), s = un.holds(i) ? s0 : 0.0;
+            const double sum = lane_value(wave_incl_scan(s), 63);
+            if (sum > 0.0) {
+                us = s;
+                ug = g;
+                uv = w;
+                before = base;
+                base += sum;
+                found = base > goal;
             }
         }
         if (!found)
             goal = INFINITY;
-        base = lastbase;
-        batches = 1ull << at;
-    }
-    if (search) {
-        if (unit < 0) {
-            unit = last;
-            goal = INFINITY;
-        }
-        const int g = un.group(unit);
-        const uint4 v = un.gr.load(g);
-        const double s = law.sum(g, v, law.aux(g)), inc = wave_incl_scan(s);
-        const unsigned long long pos = __ballot(s > 0.0);
-        const unsigned long long over = __ballot(s > 0.0 && base + inc > goal);
-        const int l = over ? __ffsll(over) - 1 : 63 - __clzll(pos);
-        base += lane_value(wave_excl_from_incl(inc), l);
+        const double inc = wave_incl_scan(us);
+        const unsigned long long lpos = __ballot(us > 0.0);
+        const unsigned long long lover = __ballot(us > 0.0 && before + inc > goal);
+        const int l = lover ? __ffsll(lover) - 1 : 63 - __clzll(lpos);
+        before += lane_value(wave_excl_from_incl(inc), l);
         // lane k: the group's k-th id
-        uint32_t w[4] = {(uint32_t)lane_value((int)v.x, l), (uint32_t)lane_value((int)v.y, l),
-                         (uint32_t)lane_value((int)v.z, l), (uint32_t)lane_value((int)v.w, l)};
-        const int k = lane % E, id = lane_value(g, l) * E + k;
-        const int word = DT == 1 ? k / 2 : k;
+        const uint32_t w[4] = {(uint32_t)lane_value((int)uv.x, l), (uint32_t)lane_value((int)uv.y, l),
+                               (uint32_t)lane_value((int)uv.z, l), (uint32_t)lane_value((int)uv.w, l)};
+        const int k = lane % E, id = lane_value(ug, l) * E + k, word = DT == 1 ? k / 2 : k;
         const uint32_t b = word == 0 ? w[0] : word == 1 ? w[1] : word == 2 ? w[2] : w[3];
         const float y = DT == 1 ? pattern_value(k & 1 ? b >> 16 : b & 0xffffu) : __uint_as_float(b);
-        const double x = lane < E && id < un.gr.V ? law.one(y, id) : 0.0, xi = wave_incl_scan(x);
-        const unsigned long long xpos = __ballot(x > 0.0);
-        const unsigned long long xover = __ballot(x > 0.0 && over && base + xi > goal);
-        if (lane == (xover ? __ffsll(xover) - 1 : 63 - __clzll(xpos)))
+        const double p = lane < E && id < un.gr.V ? law.one(y, id) : 0.0, pi = wave_incl_scan(p);
+        const unsigned long long ppos = __ballot(p > 0.0);
+        const unsigned long long pover = __ballot(p > 0.0 && lover && before + pi > goal);
+        if (lane == (pover ? __ffsll(pover) - 1 : 63 - __clzll(ppos)))
             lds.id = id;
     }
     __syncthreads();
@@ -1175,74 +1161,89 @@ template <int DT> __device__ __forceinline__ uint32_t equal_count(const uint4 &v
     }
 }
 
-// The last kept id among those equal to the cut, the n-th of them: equals per wave, then the
-// unit, the lane and the id.
+// Finds, for up to two rows at once, the last kept id among those equal to a cut, the n-th of
+// them: equals per batch and wave, then the unit, the lane and the id.  need: bit 0 p, bit 1 q.
 template <int DT>
-__device__ __forceinline__ int nth_equal(const Units<DT> &un, uint32_t cut, int n, DrawLds &lds)
+__device__ __forceinline__ void find_ties(const Units<DT> &up, const Units<DT> &uq, int need, RowCut &rp,
+                                          RowCut &rq, DrawLds &lds)
 {
-    uint64_t batches = all_batches(un);
     constexpr int E = Elt<DT>::EPV;
     const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
-    const float y = key_value(cut);
-    auto may = [&](const uint4 &v) SV_INLINE { return equal_count<DT>(v, y) != 0; };
-    auto none = [](int) SV_INLINE { return make_uint4(0, 0, 0, 0); };
-    uint32_t mine = 0;
-    int before = 0, all = 0;
-    bool search = false;
-    if (threadIdx.x == 0)
-        lds.id = 0x7fffffff;
+    const int units = max(need & 1 ? up.count() : 0, need & 2 ? uq.count() : 0);
+    const float yp = key_value(rp.cut), yq = key_value(rq.cut);
+    uint32_t *batch = reinterpret_cast<uint32_t *>(lds.batch[wv]);
+    int allp = 0, allq = 0;
+    // a batch holds at most 2048 ids: two counts to a word
 #pragma nounroll
-    for (int pass = 0; pass < 2; ++pass) {
-        batches = walk<true>(
-            un, batches, may, none,
-            [&](int i, const uint4 &v, const uint4 &) SV_INLINE {
-                uint32_t m = equal_mask<DT>(v, y);
-                const int c = __popc(m);
-                if (!search) {
-                    mine += c;
-                    return;
-                }
-                const int inc = before + (int)wave_scan_u32((uint32_t)c), b = inc - c;
-                if (b < n && n <= inc) {
-                    for (int skip = n - b - 1; skip > 0; --skip)
-                        m &= m - 1;
-                    lds.id = un.group(i) * E + __ffs(m) - 1;
-                }
-                before = lane_value(inc, 63);
-            },
-            [&](int b) SV_INLINE {
-                const int s = lane_value((int)wave_scan_u32(mine), 63);
-                mine = 0;
-                all += s;
-                if (!search && lane == 0)
-                    lds.batch[wv][b] = (double)s;
+    for (int i0 = 0; i0 < units; i0 += BATCH) {
+        uint4 p[BATCH], q[BATCH];
+        if (need & 1)
+            load_batch(up, i0, p);
+        if (need & 2)
+            load_batch(uq, i0, q);
+        uint32_t n = 0;
+        if (need & 1)
+            unroll<0, BATCH>([&](auto j) SV_INLINE {
+                n += i0 + j < up.count() && up.holds(i0 + j) ? equal_count<DT>(p[j], yp) : 0u;
             });
-        if (search)
-            break;
+        if (need & 2)
+            unroll<0, BATCH>([&](auto j) SV_INLINE {
+                n += (i0 + j < uq.count() && uq.holds(i0 + j) ? equal_count<DT>(q[j], yq) : 0u) << 16;
+            });
+        const uint32_t s = (uint32_t)lane_value((int)wave_scan_u32(n), 63);
+        allp += (int)(s & 0xffffu);
+        allq += (int)(s >> 16);
         if (lane == 0)
-            lds.ties[wv] = all;
-        __syncthreads();
-        const int w = lane < FWAVES ? (int)lds.ties[lane] : 0, wi = (int)wave_scan_u32((uint32_t)w);
-        const int me = __builtin_amdgcn_readfirstlane(wv);
-        before = lane_value(wi - w, me);
-        if (!(before < n && n <= before + all))
-            break;
-        search = true;
-        uint64_t m = batches;
-        batches = 0;
+            batch[i0 / BATCH] = s;
+    }
+    if (lane == 0) {
+        lds.ties[0][wv] = allp;
+        lds.ties[1][wv] = allq;
+    }
+    if (threadIdx.x < 2)
+        lds.tie_id[threadIdx.x] = 0x7fffffff;
+    __syncthreads();
 #pragma nounroll
-        for (; m && !batches; m &= m - 1) {
-            const int b = __builtin_ctzll(m), s = (int)lds.batch[wv][b];
+    for (int side = 0; side < 2; ++side) {
+        if (!(need >> side & 1))
+            continue;
+        const int n = side ? rq.tie : rp.tie;
+        const int w = lane < FWAVES ? lds.ties[side][lane] : 0, wi = (int)wave_scan_u32((uint32_t)w);
+        const int me = __builtin_amdgcn_readfirstlane(wv);
+        int before = lane_value(wi - w, me);
+        if (!(before < n && n <= lane_value(wi, me)))
+            continue;
+        int at = 0;
+        for (;; ++at) {                        // ends: the wave's batches hold the n-th
+            const int s = (int)(side ? batch[at] >> 16 : batch[at] & 0xffffu);
             if (before + s >= n)
-                batches = 1ull << b;
-            else
-                before += s;
+                break;
+            before += s;
+        }
+        const Units<DT> un{side ? uq.gr : up.gr, side ? uq.list : up.list, side ? uq.n : up.n};
+        uint4 v[BATCH];
+        load_batch(un, at * BATCH, v);
+#pragma nounroll
+        for (int j = 0; j < BATCH; ++j) {
+            const int i = at * BATCH + j;
+            if (i >= un.count())
+                break;
+            uint32_t m = un.holds(i) ? equal_mask<DT>(choose(v, j), side ? yq : yp) : 0u;
+            const int c = __popc(m), inc = before + (int)wave_scan_u32((uint32_t)c), b = inc - c;
+            if (b < n && n <= inc) {
+                for (int skip = n - b - 1; skip > 0; --skip)
+                    m &= m - 1;
+                lds.tie_id[side] = un.group(i) * E + __ffs(m) - 1;
+            }
+            before = lane_value(inc, 63);
         }
     }
     __syncthreads();
-    const int id = lds.id;
+    if (need & 1)
+        rp.tie = lds.tie_id[0];
+    if (need & 2)
+        rq.tie = lds.tie_id[1];
     __syncthreads();
-    return id;
 }
 
 // How many ids below x equal y.
@@ -1323,18 +1324,7 @@ struct TableLaw {
     {
         const uint32_t t = window_words(__float_as_uint(key_value(c.cut)) >> 16) & 0xffffu;
         if (c.tie < V && (t & 0x7000u) == 0)
-            cut_off = bin_offsets(t) & 0xffffu;
-    }
-    __device__ __forceinline__ double at(uint32_t off) const
-    {
-        return *reinterpret_cast<const double *>(reinterpret_cast<const char *>(table) + 2 * off);
-    }
-    __device__ __forceinline__ double one(float y, int id) const
-    {
-        const uint32_t p = __float_as_uint(y) >> 16, t = window_words(p) & 0xffffu;
-        if ((t & 0x7000u) == 0)
-            return y == key_value(r.cut) && id > r.tie ? 0.0 : at(bin_offsets(t) & 0xffffu);
-        return kept(order_key(y), id, r) && y != -INFINITY ? weight(y, r.max, r.c) * scale : 0.0;
+            cut_off = offsets(t) & 0xffffu;
     }
     // Whether a unit's groups can be looked up whole: no logit outside the window, and not the
     // group in which the kept ties end.
@@ -1343,10 +1333,20 @@ struct TableLaw {
         uint32_t out = 0;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            t[i] = g == NO_GROUP ? 0u : window_words(vec_word(v, i));
+            t[i] = window_words(vec_word(v, i));
             out |= t[i] & 0x70007000u;
         }
         return __ballot(out != 0 || g == r.tie / 8) == 0;
+    }
+    // 8 * bin of both halves
+    static __device__ __forceinline__ uint32_t offsets(uint32_t t)
+    {
+        const u16x2 three = {3, 3};
+        return as_u32(as_u16x2(t) << three) | (t & 0x80008000u);
+    }
+    __device__ __forceinline__ double at(uint32_t off) const
+    {
+        return *reinterpret_cast<const double *>(reinterpret_cast<const char *>(table) + off);
     }
     // what a group past the last kept tie must not look up
     __device__ __forceinline__ uint32_t left_out(int g) const { return g > r.tie / 8 ? cut_off : ~0u; }
@@ -1355,20 +1355,35 @@ struct TableLaw {
         const double x = at(off);
         return off == without ? 0.0 : x;
     }
+    __device__ __forceinline__ double one(float y, int id) const
+    {
+        const uint32_t p = __float_as_uint(y) >> 16, t = window_words(p) & 0xffffu;
+        if ((t & 0x7000u) == 0)
+            return y == key_value(r.cut) && id > r.tie ? 0.0 : at(offsets(t) & 0xffffu);
+        return kept(order_key(y), id, r) && y != -INFINITY ? weight(y, r.max, r.c) * scale : 0.0;
+    }
     __device__ __forceinline__ uint4 aux(int) const { return make_uint4(0, 0, 0, 0); }
     __device__ __forceinline__ double sum(int g, const uint4 &v, const uint4 &) const
     {
         uint32_t t[4];
         double s = 0.0;
         if (by_table(g, v, t)) {
-            const uint32_t no = left_out(g);
+            if (cut_off == ~0u) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const uint32_t b = bin_offsets(t[i]);
-                s += at(b & 0xffffu, no);
-                s += at(b >> 16, no);
+                for (int i = 0; i < 4; ++i) {
+                    const uint32_t b = offsets(t[i]);
+                    s += at(b & 0xffffu);
+                    s += at(b >> 16);
+                }
+            } else {
+                const uint32_t no = left_out(g);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const uint32_t b = offsets(t[i]);
+                    s += at(b & 0xffffu, no);
+                    s += at(b >> 16, no);
+                }
             }
-            s = g == NO_GROUP ? 0.0 : s;       // whatever bin 0 holds
         } else {
             uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma nounroll
@@ -1407,11 +1422,11 @@ template <int DT, typename P> struct ResidualLaw {
                 const uint32_t np = p.left_out(g), nq = q.left_out(g);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const uint32_t op = bin_offsets(tp[i]), oq = bin_offsets(tq[i]);
+                    const uint32_t op = P::offsets(tp[i]), oq = P::offsets(tq[i]);
                     s += fmax(p.at(op & 0xffffu, np) - q.at(oq & 0xffffu, nq), 0.0);
                     s += fmax(p.at(op >> 16, np) - q.at(oq >> 16, nq), 0.0);
                 }
-                return g == NO_GROUP ? 0.0 : s;
+                return s;
             }
         }
         uint32_t wp[4] = {pv.x, pv.y, pv.z, pv.w}, wq[4] = {qv.x, qv.y, qv.z, qv.w};
@@ -1481,7 +1496,6 @@ __global__ __launch_bounds__(FWG, 4) void k_filter_sample_bf16(const char *logit
     uint4 nx[BATCH];
     load_batch(all, 0, nx);
     const Params q = load_params(f, n, V);
-    Outside o;
     Floor fl(q, V, FWAVES);
     clear_hist<FWG>(hist);
     if (fl.active())                       // what is not counted is looked up all the same
@@ -1490,11 +1504,14 @@ __global__ __launch_bounds__(FWG, 4) void k_filter_sample_bf16(const char *logit
     cut_lds_clear(c);
     __syncthreads();
     int listed = 0;
+    const int units = all.count();
+    if (fl.active() && units == 0)         // the other waves wait below
+        __syncthreads();
 #pragma nounroll
-    for (int i0 = 0; i0 < gr.per_wave; i0 += BATCH) {
+    for (int i0 = 0; i0 < units; i0 += BATCH) {
         uint4 v[BATCH];
         unroll<0, BATCH>([&](auto j) SV_INLINE { v[j] = nx[j]; });
-        if (i0 + BATCH < gr.per_wave)
+        if (i0 + BATCH < units)
             load_batch(all, i0 + BATCH, nx);
         if (fl.active()) {
             unroll<0, BATCH>([&](auto j) SV_INLINE { fl.see(v[j]); });
@@ -1503,23 +1520,31 @@ __global__ __launch_bounds__(FWG, 4) void k_filter_sample_bf16(const char *logit
                 __syncthreads();
             fl.update<FWAVES>(c);
         }
-        unroll<0, BATCH>([&](auto j) SV_INLINE {
-            const bool m = i0 + j < gr.per_wave && fl.matters(v[j]);
-            const unsigned long long who = __ballot(m);
-            if (who) {
-                const int at = listed + (int)__builtin_amdgcn_mbcnt_hi(
-                                   (uint32_t)(who >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)who, 0));
-                listed += __popcll(who);
-                if (m && listed <= LIST)
-                    dl.list[wv][at] = (uint16_t)((i0 + j) * 64 + lane);
-                if (m)
-                    count_vec(v[j], hist, c, o);
-            }
-        });
+        if (fl.below == 0) {
+            listed = LIST + 1;
+            unroll<0, BATCH>([&](auto j) SV_INLINE {
+                if (i0 + j < units)
+                    count_vec(v[j], hist, c);
+            });
+        } else {
+            unroll<0, BATCH>([&](auto j) SV_INLINE {
+                const bool m = i0 + j < units && fl.matters(v[j]);
+                const unsigned long long who = __ballot(m);
+                if (who) {
+                    const int at = listed + (int)__builtin_amdgcn_mbcnt_hi(
+                                       (uint32_t)(who >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)who, 0));
+                    listed += __popcll(who);
+                    if (m && at < LIST)
+                        dl.list[wv][at] = (uint16_t)((i0 + j) * 64 + lane);
+                    if (m)
+                        count_vec(v[j], hist, c);
+                }
+            });
+        }
     }
-    if (fl.active())
-        o.bad |= fl.bad();
-    cut_from_counts<FWG>(hist, c, o, q, V, !fl.active(), table);
+    if (fl.active() && fl.bad())
+        atomicOr(&c.bad, 1u);
+    cut_from_counts<FWG>(hist, c, q, V, !fl.active(), table);
     RowCut r = c.cut;
     int id = -1;
     const double u = (double)unif[n];
@@ -1530,7 +1555,7 @@ __global__ __launch_bounds__(FWG, 4) void k_filter_sample_bf16(const char *logit
     } else if (r.state != CUT_NONE) {
         const Units<1> few{gr, dl.list[wv], listed <= LIST ? __builtin_amdgcn_readfirstlane(listed) : -1};
         if (r.state == CUT_TIES)
-            r.tie = nth_equal(few, r.cut, r.tie, dl);
+            find_ties(few, few, 1, r, r, dl);
         id = draw_row(few, MayKeep<1>(r), u, dl, TableLaw(r, V, 1.0, table));
     }
     if (threadIdx.x == 0) {
@@ -1673,18 +1698,13 @@ __global__ __launch_bounds__(FWG, 4) void k_filter_verify(const char *tgt, const
         const Groups<DT> gp(row_of(L), V), gq(row_of(L < K ? K + 1 + L : L), V);
         const Units<DT> up{gp, nullptr, -1};
         RowCut rp = s.cut[L], rq = s.cut[L < K ? K + 1 + L : L];
+        if constexpr (DT == 1)
 #pragma nounroll
-        for (int side = 0; side < (L < K ? 2 : 1); ++side) {
-            RowCut r = side ? rq : rp;
-            if constexpr (DT == 1)
-                fill_table(r, 1.0 / r.z, tables[side]);
-            if (r.state == CUT_TIES)
-                r.tie = nth_equal(Units<DT>{side ? gq : gp, nullptr, -1}, r.cut, r.tie, dl);
-            if (side)
-                rq = r;
-            else
-                rp = r;
-        }
+            for (int side = 0; side < (L < K ? 2 : 1); ++side)
+                fill_table(side ? rq : rp, 1.0 / (side ? rq : rp).z, tables[side]);
+        const int need = (rp.state == CUT_TIES ? 1 : 0) | (L < K && rq.state == CUT_TIES ? 2 : 0);
+        if (need)
+            find_ties(up, Units<DT>{gq, nullptr, -1}, need, rp, rq, dl);
         __syncthreads();
         const double u = (double)unif[(size_t)b * (K + 1) + K];
         auto draw = [&](auto p, auto q) SV_INLINE {
