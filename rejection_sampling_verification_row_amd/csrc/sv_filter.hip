@@ -839,15 +839,8 @@ __device__ __forceinline__ void count_row(const Groups<1> &gr, Floor &fl, uint32
         const int g = i * U * WGT + t;
         uint4 v[U];
         const bool full = (i + 1) * U * WGT <= gr.whole;
-        if (full) {
-            unroll<0, U>([&](auto k) SV_INLINE { v[k] = gr.load_once(g + k * WGT); });
-        } else {
-            unroll<0, U>([&](auto k) SV_INLINE {
-                v[k] = make_uint4(gr.EMPTY, gr.EMPTY, gr.EMPTY, gr.EMPTY);
-                if (g + k * WGT < gr.whole)
-                    v[k] = gr.load_once(g + k * WGT);
-            });
-        }
+        // threads past the end read the last group again and leave it
+        unroll<0, U>([&](auto k) SV_INLINE { v[k] = gr.load_once(min(g + k * WGT, gr.whole - 1)); });
         if (fl.active()) {
             unroll<0, U>([&](auto k) SV_INLINE { fl.see(v[k]); });
             if ((i & (i + 1)) == 0) {
