@@ -164,6 +164,7 @@ __device__ __forceinline__ RowCut cut_by_bisection(const char *row, int V, const
     mx = block_max(mx, lds.u);
     bad = block_sum(bad, lds.i);
     r.state = q.ok && !bad && mx > KEY_NEG_INF ? CUT_READY : CUT_NONE;
+    r.kept = V;
     r.max = key_value(mx);
     r.c = q.c;
     r.cut = KEY_NEG_INF;                            // no key lies below it: all ids
@@ -676,6 +677,7 @@ __device__ __forceinline__ void cut_from_counts(const uint32_t *hist, CutLds &c,
     cut.cut = KEY_NEG_INF;
     cut.tie = V;
     cut.state = CUT_READY;
+    cut.kept = V;
     if (!q.ok || c.bad || (total == 0 && c.low == 0)) {
         cut.state = CUT_NONE;
     } else if (c.nx >= HX || total == 0) {
@@ -809,6 +811,7 @@ __device__ __forceinline__ void cut_from_counts(const uint32_t *hist, CutLds &c,
                         cut.z = run + (double)keep * w;
                         cut.state = keep < n[i] ? CUT_TIES : CUT_READY;
                         cut.tie = keep < n[i] ? (int)keep : V;
+                        cut.kept = b + keep;
                     }
                 }
                 b += n[i];
@@ -839,8 +842,13 @@ __device__ __forceinline__ void count_row(const Groups<1> &gr, Floor &fl, uint32
         const int g = i * U * WGT + t;
         uint4 v[U];
         const bool full = (i + 1) * U * WGT <= gr.whole;
-        // threads past the end read the last group again and leave it
+        // threads past the end read the last group again and drop it
         unroll<0, U>([&](auto k) SV_INLINE { v[k] = gr.load_once(min(g + k * WGT, gr.whole - 1)); });
+        if (!full)
+            unroll<0, U>([&](auto k) SV_INLINE {
+                if (g + k * WGT >= gr.whole)
+                    v[k] = make_uint4(gr.EMPTY, gr.EMPTY, gr.EMPTY, gr.EMPTY);
+            });
         if (fl.active()) {
             unroll<0, U>([&](auto k) SV_INLINE { fl.see(v[k]); });
             if ((i & (i + 1)) == 0) {
@@ -992,6 +1000,20 @@ template <int DT> __device__ __forceinline__ uint64_t all_batches(const Units<DT
 {
     const int n = (un.count() + BATCH - 1) / BATCH;
     return n >= 64 ? ~0ull : (1ull << n) - 1;
+}
+
+// Adds the lanes' groups `at` for which m holds to a wave's list, in order, of which n are listed
+// already; past LIST they are only counted.
+__device__ __forceinline__ void list_groups(uint16_t *list, int &n, bool m, int at)
+{
+    const unsigned long long who = __ballot(m);
+    if (who) {
+        const int i = n + (int)__builtin_amdgcn_mbcnt_hi((uint32_t)(who >> 32),
+                                                         __builtin_amdgcn_mbcnt_lo((uint32_t)who, 0));
+        n += __popcll(who);
+        if (m && i < LIST)
+            list[i] = (uint16_t)at;
+    }
 }
 
 // The units of batch i0 that may() something in, as a mask, and their aux() groups.
@@ -1154,15 +1176,45 @@ template <int DT> __device__ __forceinline__ uint32_t equal_count(const uint4 &v
     }
 }
 
+// Whether a group can hold a kept id.  For a cut above zero patterns compare as signed 16-bit
+// integers, two at a time.
+template <int DT> struct MayKeep {
+    uint32_t below;      // the largest pattern, twice, below the cut; 0: any group may
+    __device__ __forceinline__ explicit MayKeep(const RowCut &r)
+    {
+        const float y = key_value(r.cut);
+        below = 0;
+        if (DT == 1 && y > 0.0f)
+            below = ((__float_as_uint(y) >> 16) - 1) * 0x10001u;
+    }
+    __device__ __forceinline__ bool operator()(const uint4 &v) const
+    {
+        if (DT != 1 || below == 0)
+            return true;
+        typedef short s16x2 __attribute__((ext_vector_type(2)));
+        const s16x2 b = __builtin_bit_cast(s16x2, below);
+        uint32_t d = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            d |= __builtin_bit_cast(uint32_t, __builtin_elementwise_max(
+                     __builtin_bit_cast(s16x2, vec_word(v, i)), b)) ^ below;
+        return d != 0;
+    }
+};
+
 // Finds, for up to two rows at once, the last kept id among those equal to a cut, the n-th of
-// them: equals per batch and wave, then the unit, the lane and the id.  need: bit 0 p, bit 1 q.
+// them: equals per batch and wave, then the unit, the lane and the id.  need: bit 0 p, bit 1 q,
+// bit 2: list the groups of p (all of its range) that can hold a kept id.  Returns the list's
+// length, -1 if it is too long or not asked for.
 template <int DT>
-__device__ __forceinline__ void find_ties(const Units<DT> &up, const Units<DT> &uq, int need, RowCut &rp,
-                                          RowCut &rq, DrawLds &lds)
+__device__ __forceinline__ int find_ties(const Units<DT> &up, const Units<DT> &uq, int need, RowCut &rp,
+                                         RowCut &rq, DrawLds &lds)
 {
+    const MayKeep<DT> may(rp);
+    int listed = 0;
     constexpr int E = Elt<DT>::EPV;
     const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
-    const int units = max(need & 1 ? up.count() : 0, need & 2 ? uq.count() : 0);
+    const int units = max(need & 5 ? up.count() : 0, need & 2 ? uq.count() : 0);
     const float yp = key_value(rp.cut), yq = key_value(rq.cut);
     uint32_t *batch = reinterpret_cast<uint32_t *>(lds.batch[wv]);
     int allp = 0, allq = 0;
@@ -1170,11 +1222,15 @@ __device__ __forceinline__ void find_ties(const Units<DT> &up, const Units<DT> &
 #pragma nounroll
     for (int i0 = 0; i0 < units; i0 += BATCH) {
         uint4 p[BATCH], q[BATCH];
-        if (need & 1)
+        if (need & 5)
             load_batch(up, i0, p);
         if (need & 2)
             load_batch(uq, i0, q);
         uint32_t n = 0;
+        if (need & 4)
+            unroll<0, BATCH>([&](auto j) SV_INLINE {
+                list_groups(lds.list[wv], listed, i0 + j < units && may(p[j]), (i0 + j) * 64 + lane);
+            });
         if (need & 1)
             unroll<0, BATCH>([&](auto j) SV_INLINE {
                 n += i0 + j < up.count() && up.holds(i0 + j) ? equal_count<DT>(p[j], yp) : 0u;
@@ -1237,6 +1293,7 @@ __device__ __forceinline__ void find_ties(const Units<DT> &up, const Units<DT> &
     if (need & 2)
         rq.tie = lds.tie_id[1];
     __syncthreads();
+    return need & 4 && listed <= LIST ? __builtin_amdgcn_readfirstlane(listed) : -1;
 }
 
 // How many ids below x equal y.
@@ -1434,32 +1491,6 @@ template <int DT, typename P> struct ResidualLaw {
     }
 };
 
-// Whether a group can hold a kept id.  For a cut above zero patterns compare as signed 16-bit
-// integers, two at a time.
-template <int DT> struct MayKeep {
-    uint32_t below;      // the largest pattern, twice, below the cut; 0: any group may
-    __device__ __forceinline__ explicit MayKeep(const RowCut &r)
-    {
-        const float y = key_value(r.cut);
-        below = 0;
-        if (DT == 1 && y > 0.0f)
-            below = ((__float_as_uint(y) >> 16) - 1) * 0x10001u;
-    }
-    __device__ __forceinline__ bool operator()(const uint4 &v) const
-    {
-        if (DT != 1 || below == 0)
-            return true;
-        typedef short s16x2 __attribute__((ext_vector_type(2)));
-        const s16x2 b = __builtin_bit_cast(s16x2, below);
-        uint32_t d = 0;
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            d |= __builtin_bit_cast(uint32_t, __builtin_elementwise_max(
-                     __builtin_bit_cast(s16x2, vec_word(v, i)), b)) ^ below;
-        return d != 0;
-    }
-};
-
 // table[bin] = w / z for the bins that r keeps, 0 for the others.
 __device__ __forceinline__ void fill_table(const RowCut &r, double scale, double *table)
 {
@@ -1522,16 +1553,9 @@ __global__ __launch_bounds__(FWG, 4) void k_filter_sample_bf16(const char *logit
         } else {
             unroll<0, BATCH>([&](auto j) SV_INLINE {
                 const bool m = i0 + j < units && fl.matters(v[j]);
-                const unsigned long long who = __ballot(m);
-                if (who) {
-                    const int at = listed + (int)__builtin_amdgcn_mbcnt_hi(
-                                       (uint32_t)(who >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)who, 0));
-                    listed += __popcll(who);
-                    if (m && at < LIST)
-                        dl.list[wv][at] = (uint16_t)((i0 + j) * 64 + lane);
-                    if (m)
-                        count_vec(v[j], hist, c);
-                }
+                list_groups(dl.list[wv], listed, m, (i0 + j) * 64 + lane);
+                if (m)
+                    count_vec(v[j], hist, c);
             });
         }
     }
@@ -1596,6 +1620,7 @@ __global__ __launch_bounds__(FWG) void k_filter_rows_f32(const char *tgt, const 
 }
 
 constexpr int MAX_POS = 63;
+constexpr uint32_t SPARSE = 2048;         // an eighth of the groups that the waves' lists hold
 
 struct VerifyLds {
     RowCut cut[2 * MAX_POS + 1];          // target rows 0..K, then draft rows 0..K-1
@@ -1689,15 +1714,36 @@ __global__ __launch_bounds__(FWG, 4) void k_filter_verify(const char *tgt, const
     if (L >= 0) {
         // p's row, and q's where there is one
         const Groups<DT> gp(row_of(L), V), gq(row_of(L < K ? K + 1 + L : L), V);
-        const Units<DT> up{gp, nullptr, -1};
+        const Units<DT> uq{gq, nullptr, -1};
+        Units<DT> up{gp, nullptr, -1};
         RowCut rp = s.cut[L], rq = s.cut[L < K ? K + 1 + L : L];
         if constexpr (DT == 1)
 #pragma nounroll
             for (int side = 0; side < (L < K ? 2 : 1); ++side)
                 fill_table(side ? rq : rp, 1.0 / (side ? rq : rp).z, tables[side]);
-        const int need = (rp.state == CUT_TIES ? 1 : 0) | (L < K && rq.state == CUT_TIES ? 2 : 0);
+        // Where p keeps few ids, one pass over p lists their groups and the rest looks at those
+        // alone.  q's last kept tie matters only if one of them has q's cut value.
+        const bool sparse = rp.kept <= SPARSE;
+        int need = (rp.state == CUT_TIES ? 1 : 0) | (L < K && rq.state == CUT_TIES ? 2 : 0);
+        if (sparse) {
+            up.n = find_ties(up, uq, (need & 1) | 4, rp, rq, dl);
+            up.list = dl.list[t >> 6];
+            if (need & 2) {
+                const MayKeep<DT> may(rp);
+                const float yq = key_value(rq.cut);
+                bool hit = false;
+                for (int i = 0; i < up.count(); ++i) {
+                    const int g = up.group(i);
+                    if (may(gp.load(g)))
+                        hit |= equal_count<DT>(gq.load(g), yq) != 0;
+                }
+                need = __syncthreads_or(hit) ? 2 : 0;
+            } else {
+                need = 0;
+            }
+        }
         if (need)
-            find_ties(up, Units<DT>{gq, nullptr, -1}, need, rp, rq, dl);
+            find_ties(up, uq, need, rp, rq, dl);
         __syncthreads();
         const double u = (double)unif[(size_t)b * (K + 1) + K];
         auto draw = [&](auto p, auto q) SV_INLINE {

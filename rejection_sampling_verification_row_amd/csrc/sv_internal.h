@@ -223,7 +223,8 @@ struct RowCut {
     float max;
     uint32_t cut;    // order key
     int tie;
-    int state;       // CutState
+    uint32_t state : 3;   // CutState
+    uint32_t kept : 29;   // ids kept, or more
 };
 static_assert(sizeof(RowCut) <= WAVES * sizeof(float2), "a row's record must fit its partials");
 
