@@ -917,6 +917,7 @@ constexpr int LIST = 256;  // groups that matter in a wave's range, if they are 
 struct DrawLds {
     double batch[FWAVES][64];
     double wave[FWAVES];
+    double total;              // the row's
     int ties[2][FWAVES], tie_id[2];
     uint16_t list[FWAVES][LIST];
     int id;
@@ -1082,6 +1083,8 @@ __device__ __forceinline__ int draw_row(const Units<DT> &un, A may, double u, Dr
     // lane w: wave w's sum
     const double ws = lane < FWAVES ? lds.wave[lane] : 0.0, wi = wave_incl_scan(ws);
     double goal = u * lane_value(wi, 63);
+    if (threadIdx.x == 0)
+        lds.total = lane_value(wi, 63);
     const unsigned long long pos = __ballot(ws > 0.0), over = __ballot(ws > 0.0 && wi > goal);
     const int pick = over ? __ffsll(over) - 1 : pos ? 63 - __clzll(pos) : -1;
     if (__builtin_amdgcn_readfirstlane(wv) == pick) {
@@ -1176,29 +1179,23 @@ template <int DT> __device__ __forceinline__ uint32_t equal_count(const uint4 &v
     }
 }
 
-// Whether a group can hold a kept id.  For a cut above zero patterns compare as signed 16-bit
-// integers, two at a time.
+// Whether a group can hold a kept id.  bfloat16: for a cut above zero patterns compare as signed
+// 16-bit integers, two at a time; else any group may.
 template <int DT> struct MayKeep {
-    uint32_t below;      // the largest pattern, twice, below the cut; 0: any group may
+    uint32_t below;      // bfloat16: the largest pattern, twice, below the cut; 0: any group may
+    float low;           // float32: the cut
     __device__ __forceinline__ explicit MayKeep(const RowCut &r)
     {
-        const float y = key_value(r.cut);
-        below = 0;
-        if (DT == 1 && y > 0.0f)
-            below = ((__float_as_uint(y) >> 16) - 1) * 0x10001u;
+        low = key_value(r.cut);
+        below = DT == 1 && low > 0.0f ? ((__float_as_uint(low) >> 16) - 1) * 0x10001u : 0;
     }
     __device__ __forceinline__ bool operator()(const uint4 &v) const
     {
-        if (DT != 1 || below == 0)
-            return true;
-        typedef short s16x2 __attribute__((ext_vector_type(2)));
-        const s16x2 b = __builtin_bit_cast(s16x2, below);
-        uint32_t d = 0;
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            d |= __builtin_bit_cast(uint32_t, __builtin_elementwise_max(
-                     __builtin_bit_cast(s16x2, vec_word(v, i)), b)) ^ below;
-        return d != 0;
+        if constexpr (DT == 1)
+            return below == 0 || max_i16(group_max(v), below) != below;
+        else
+            return fmaxf(fmaxf(__uint_as_float(v.x), __uint_as_float(v.y)),
+                         fmaxf(__uint_as_float(v.z), __uint_as_float(v.w))) >= low;
     }
 };
 
@@ -1352,11 +1349,17 @@ template <int DT> struct DirectLaw {
     __device__ __forceinline__ uint4 aux(int) const { return make_uint4(0, 0, 0, 0); }
     __device__ __forceinline__ double sum(int g, const uint4 &v, const uint4 &) const
     {
-        uint32_t w[4] = {v.x, v.y, v.z, v.w};
         double s = 0.0;
+        if constexpr (DT == 0) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                s += one(__uint_as_float(vec_word(v, k)), g * 4 + k);
+        } else {
+            uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma nounroll
-        for (int k = 0; k < E; ++k)
-            s += one(next_logit<DT>(w), g * E + k);
+            for (int k = 0; k < E; ++k)
+                s += one(next_logit<DT>(w), g * E + k);
+        }
         return s;
     }
 };
@@ -1582,39 +1585,468 @@ __global__ __launch_bounds__(FWG, 4) void k_filter_sample_bf16(const char *logit
     }
 }
 
-__global__ __launch_bounds__(FWG) void k_filter_sample_f32(const char *logits, int V, int64_t stride,
-                                                           FilterPtrs f, const float *unif, int *tok,
-                                                           float *prob)
+// ------------------------------------------------------------------ float32: the cut by counting
+//
+// The upper halves of float32 logits are counted in the bins of the bfloat16 path (truncated, which
+// keeps the order), with three more for what lies above, around zero and below.  The counts name
+// the bin of a cut; the few logits of that bin, or of it and all above, are then gathered and put
+// in order exactly.  For top-p the bins' weights are needed too: one more pass adds them up in
+// LDS, as integers so that their order does not matter, in units of 2^-47 (for vocabularies past
+// 2^15 coarser, 2^-41 at 2^20) of the weight at the bin's upper edge: half a unit is lost per logit,
+// relative to its bin.  A row whose bin holds more than GATHER logits goes to cut_by_bisection.
+
+constexpr int BIN_HIGH = HBINS, BIN_ZERO = HBINS + 1, BIN_LOW = HBINS + 2, FBINS = HBINS + 3;
+constexpr int GATHER = 1024;
+
+struct FloatLds {
+    __align__(16) uint32_t hist[FBINS + 1];
+    unsigned long long weight[FBINS];
+    unsigned long long list[GATHER], order[GATHER];   // order key, then ~id
+    double dwave[FWAVES];
+    double prefix;                 // what find_bin found
+    int bin, place;
+    uint32_t n;
+};
+
+// Which logits a bin holds: from low() to high().
+__device__ __forceinline__ float bin_low(int bin)
 {
-    __shared__ RedLds red;
+    if (bin >= HBINS)
+        return bin == BIN_HIGH ? 256.0f : bin == BIN_ZERO ? -__uint_as_float((HLO << 16) - 1) : -FLT_MAX;
+    const uint32_t p = bin_pattern(bin);
+    return __uint_as_float(p << 16 | (bin >= HMAG ? 0xffffu : 0u));
+}
+__device__ __forceinline__ float bin_high(int bin)
+{
+    if (bin >= HBINS)
+        return bin == BIN_HIGH ? FLT_MAX : bin == BIN_ZERO ? __uint_as_float((HLO << 16) - 1) : -256.0f;
+    const uint32_t p = bin_pattern(bin);
+    return __uint_as_float(p << 16 | (bin >= HMAG ? 0u : 0xffffu));
+}
+
+// The bin of a finite logit.
+__device__ __forceinline__ int float_bin(uint32_t bits)
+{
+    const uint32_t t = ((bits >> 16) - HLO) & 0xffffu;
+    if ((t & 0x7000u) == 0)
+        return (int)((t >> 15) * HMAG + (t & 0xfffu));
+    return (bits & 0x7fffffffu) < HLO << 16 ? BIN_ZERO : bits >> 31 ? BIN_LOW : BIN_HIGH;
+}
+
+// Upper halves of four float32 words, two to a word.
+__device__ __forceinline__ uint2 upper_halves(const uint4 &v)
+{
+    return make_uint2(__builtin_amdgcn_perm(v.y, v.x, 0x07060302u),
+                      __builtin_amdgcn_perm(v.w, v.z, 0x07060302u));
+}
+
+__device__ __forceinline__ void count_floats(const uint4 &v, const uint2 &h, FloatLds &f, CutLds &c)
+{
+    const uint32_t t0 = window_words(h.x), t1 = window_words(h.y);
+    if (__ballot(((t0 | t1) & 0x70007000u) != 0) == 0) {
+        const uint32_t a = bin_offsets(t0), b = bin_offsets(t1);
+        bump(f.hist, a & 0xffffu);
+        bump(f.hist, a >> 16);
+        bump(f.hist, b & 0xffffu);
+        bump(f.hist, b >> 16);
+    } else {
+        uint32_t w0 = v.x, w1 = v.y, w2 = v.z, w3 = v.w;
+#pragma nounroll
+        for (int i = 0; i < 4; ++i) {
+            if ((w0 & 0x7f800000u) != 0x7f800000u)
+                atomicAdd(&f.hist[float_bin(w0)], 1u);
+            else if (w0 != 0xff800000u)
+                atomicOr(&c.bad, 1u);
+            w0 = w1;
+            w1 = w2;
+            w2 = w3;
+        }
+    }
+}
+
+// The workgroup's inclusive scan in thread order; *total is the sum.
+__device__ __forceinline__ double block_scan(double v, double *lds, double *total)
+{
+    const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
+    v = wave_incl_scan(v);
+    __syncthreads();
+    if (lane == 63)
+        lds[wv] = v;
+    __syncthreads();
+    const double w = lane < FWAVES ? lds[lane] : 0.0, wi = wave_incl_scan(w);
+    *total = lane_value(wi, 63);
+    return lane_value(wave_excl_from_incl(wi), __builtin_amdgcn_readfirstlane(wv)) + v;
+}
+
+// The last bin, in order, that holds something and before which lies less than goal; f.bin and
+// f.prefix.  val(bin) is what a bin holds, goal_of(total) the goal.  Returns the total.  A thread
+// takes eight bins; those outside the window join the threads that they stand next to.
+template <typename W, typename G>
+__device__ __forceinline__ double find_bin(FloatLds &f, W val, G goal_of)
+{
+    const int t = threadIdx.x;
+    constexpr int PER = HBINS / FWG;
+    auto bin_of = [&](int i) SV_INLINE {       // i = 0: before the eight, 9: after them
+        if (i == 0)
+            return t == 0 ? BIN_HIGH : t == FWG / 2 ? BIN_ZERO : -1;
+        if (i == PER + 1)
+            return t == FWG - 1 ? BIN_LOW : -1;
+        const int o = t * PER + i - 1;
+        return o < HMAG ? HMAG - 1 - o : o;
+    };
+    double sum = 0.0, total, run = 0.0, goal = 0.0;
+    if (t == 0)
+        f.place = -1;
+    // the threads sum their bins; then the one that holds the goal goes over its own again
+#pragma nounroll
+    for (int pass = 0; pass < 2; ++pass) {
+#pragma nounroll
+        for (int i = 0; i <= PER + 1; ++i) {
+            const int b = bin_of(i);
+            const double n = b >= 0 ? val(b) : 0.0;
+            if (pass == 1 && n > 0.0 && run < goal) {
+                f.bin = b;
+                f.prefix = run;
+            }
+            run += n;
+        }
+        if (pass == 1)
+            break;
+        sum = run;
+        const double inc = block_scan(sum, f.dwave, &total);
+        goal = goal_of(total);
+        run = __shfl_up(inc, 1);               // what stands before the thread
+        if ((t & 63) == 0) {
+            run = 0.0;
+            for (int i = 0; i < t >> 6; ++i)
+                run += f.dwave[i];
+        }
+        if (sum > 0.0 && run < goal)
+            atomicMax(&f.place, t);
+        __syncthreads();
+        if (f.place != t)
+            break;
+    }
+    __syncthreads();
+    return total;
+}
+
+// Runs f(bits, id) over the logits of the wave's units.
+template <typename F> __device__ __forceinline__ void each_float(const Units<0> &un, F f)
+{
+    const int units = un.count();
+#pragma nounroll
+    for (int i0 = 0; i0 < units; i0 += BATCH) {
+        uint4 v[BATCH];
+        load_batch(un, i0, v);
+#pragma nounroll
+        for (int j = 0; j < BATCH && i0 + j < units; ++j) {
+            const uint4 x = choose(v, j);
+            const int id = un.group(i0 + j) * 4;
+            if (!un.holds(i0 + j))
+                continue;
+            f(x.x, id);
+            f(x.y, id + 1);
+            f(x.z, id + 2);
+            f(x.w, id + 3);
+        }
+    }
+}
+
+// The logits from lo to hi that r keeps, gathered and put in order: f.order[0 .. f.n).  False if
+// there are too many.
+__device__ __forceinline__ bool gather(const Units<0> &un, float lo, float hi, const RowCut &r, FloatLds &f)
+{
+    if (threadIdx.x == 0)
+        f.n = 0;
+    __syncthreads();
+    each_float(un, [&](uint32_t bits, int id) SV_INLINE {
+        const float x = __uint_as_float(bits);
+        if (x >= lo && x <= hi && kept(order_key(x), id, r)) {
+            const uint32_t at = atomicAdd(&f.n, 1u);
+            if (at < GATHER)
+                f.list[at] = (unsigned long long)order_key(x) << 32 | (uint32_t)~id;
+        }
+    });
+    __syncthreads();
+    const int n = (int)f.n;
+    if (n > GATHER)
+        return false;
+    if ((int)threadIdx.x < n) {
+        const unsigned long long me = f.list[threadIdx.x];
+        int rank = 0;
+#pragma unroll 4
+        for (int j = 0; j < n; ++j)
+            rank += f.list[j] > me;
+        f.order[rank] = me;
+    }
+    __syncthreads();
+    return true;
+}
+
+// How many of the ordered logits stay: those before which less than goal lies (counting `base`
+// before all of them), of weight at least m and among the first k.  Sets r's cut to the last, and
+// returns what lies before the first that goes; *sum is the sum over the first k.
+__device__ __forceinline__ void cut_in_order(RowCut &r, double base, int k, double p, double goal,
+                                             double m, FloatLds &f)
+{
+    const int t = threadIdx.x, n = min((int)f.n, k);
+    const double w = t < n ? weight(key_value((uint32_t)(f.order[t] >> 32)), r.max, r.c) : 0.0;
+    double total;
+    const double inc = block_scan(w, f.dwave, &total);
+    if (p < 1.0)
+        goal = p * total;
+    // the exclusive prefix as the sum of what stands before, not the difference with w
+    const double left = __shfl_up(inc, 1);
+    double before = left;
+    if ((t & 63) == 0) {
+        before = 0.0;
+        for (int i = 0; i < t >> 6; ++i)
+            before += f.dwave[i];
+    }
+    before += base;
+    const bool keep = t < n && (before < goal || t == 0) && w >= m;
+    const int stay = __syncthreads_count(keep);
+    if (t == stay - 1) {
+        f.place = (int)~(uint32_t)f.order[t];
+        f.dwave[0] = base + inc;
+    }
+    __syncthreads();
+    r.cut = (uint32_t)(f.order[stay - 1] >> 32);
+    r.tie = f.place;
+    r.z = f.dwave[0];
+    r.kept = stay;
+    __syncthreads();
+}
+
+// The lowest key of weight at least m, 64 at a time.
+__device__ __forceinline__ uint32_t key_of_weight(float M, double c, double m)
+{
+    uint32_t lo = KEY_NEG_INF, hi = order_key(M);     // weight(hi) >= m
+#pragma nounroll
+    while (lo < hi) {
+        const uint32_t step = (hi - lo) / 64 + 1, lane = threadIdx.x & 63;
+        const uint32_t key = hi - lo < lane * step ? hi : lo + lane * step;
+        const unsigned long long ok = __ballot(weight(key_value(key), M, c) >= m);
+        const int l = ok ? __ffsll(ok) - 1 : 64;       // the first of the probes that passes
+        const uint32_t up = l == 64 || hi - lo < (uint32_t)l * step ? hi : lo + (uint32_t)l * step;
+        lo = l == 0 ? lo : min(lo + (uint32_t)(l - 1) * step + 1, up);
+        hi = up;
+        if (l == 0)
+            break;
+    }
+    return hi;
+}
+
+// A float32 row's cut.  few receives the units that hold what matters.  z is left at 0 where only
+// a sum over the kept ids would give it.
+__device__ __forceinline__ RowCut cut_floats(const Units<0> &all, Units<0> &few, const Params &q, FloatLds &f,
+                                             CutLds &c, DrawLds &dl, RedLds &red)
+{
+    const int t = threadIdx.x, lane = t & 63, wv = t >> 6, V = all.gr.V, units = all.count();
+    for (int i = t; i < FBINS; i += FWG)
+        f.hist[i] = 0;
+    cut_lds_clear(c);
+    __syncthreads();
+    Floor fl(q, V, FWAVES);
+    float mx = -INFINITY;
+    uint32_t most = 0;             // as unsigned bits: a NaN of negative sign is above -inf
+    int listed = 0;
+    if (fl.active() && units == 0)
+        __syncthreads();
+#pragma nounroll
+    for (int i0 = 0; i0 < units; i0 += BATCH) {
+        uint4 v[BATCH];
+        uint2 h[BATCH];
+        load_batch(all, i0, v);
+        unroll<0, BATCH>([&](auto j) SV_INLINE {
+            h[j] = upper_halves(v[j]);
+            mx = fmaxf(fmaxf(mx, fmaxf(__uint_as_float(v[j].x), __uint_as_float(v[j].y))),
+                       fmaxf(__uint_as_float(v[j].z), __uint_as_float(v[j].w)));
+            most = max(max(most, max(v[j].x, v[j].y)), max(v[j].z, v[j].w));
+        });
+        if (fl.active()) {
+            unroll<0, BATCH / 2>([&](auto j) SV_INLINE {
+                fl.see(make_uint4(h[2 * j].x, h[2 * j].y, h[2 * j + 1].x, h[2 * j + 1].y));
+            });
+            fl.note(c);
+            if (i0 == 0)
+                __syncthreads();
+            fl.update<FWAVES>(c);
+        }
+        if (fl.below == 0) {
+            listed = LIST + 1;
+            unroll<0, BATCH>([&](auto j) SV_INLINE {
+                if (i0 + j < units)
+                    count_floats(v[j], h[j], f, c);
+            });
+        } else {
+            unroll<0, BATCH>([&](auto j) SV_INLINE {
+                const bool m = i0 + j < units && max_i16(max_i16(h[j].x, h[j].y), fl.below) != fl.below;
+                list_groups(dl.list[wv], listed, m, (i0 + j) * 64 + lane);
+                if (m)
+                    count_floats(v[j], h[j], f, c);
+            });
+        }
+    }
+    if (most > 0xff800000u)
+        atomicOr(&c.bad, 1u);
+    few.n = listed <= LIST ? __builtin_amdgcn_readfirstlane(listed) : -1;
+    few.list = dl.list[wv];
+    RowCut r;
+    r.max = key_value(block_max(order_key(mx), red.u));       // and the counts are complete
+    r.c = q.c;
+    r.cut = KEY_NEG_INF;
+    r.tie = V;
+    r.z = 0.0;
+    r.kept = V;
+    r.state = q.ok && !c.bad && r.max != -INFINITY ? CUT_READY : CUT_NONE;
+    if (r.state == CUT_NONE)
+        return r;
+    if (q.k < V) {
+        const double total = find_bin(f, [&](int b) SV_INLINE { return (double)f.hist[b]; },
+                                      [&](double) SV_INLINE { return (double)q.k; });
+        if (fl.active() || (double)q.k < total) {
+            const int bin = f.bin;
+            const uint32_t before = (uint32_t)f.prefix;
+            if (before + f.hist[bin] <= GATHER) {
+                // all that top-k can keep is in hand: the three cuts at once
+                gather(few, bin_low(bin), FLT_MAX, r, f);
+                cut_in_order(r, 0.0, q.k, q.p, INFINITY, q.m, f);
+                return r;
+            }
+            if (!gather(few, bin_low(bin), bin_high(bin), r, f)) {
+                r.state = CUT_EXACT;
+                return r;
+            }
+            const unsigned long long last = f.order[q.k - before - 1];
+            r.cut = (uint32_t)(last >> 32);
+            r.tie = (int)~(uint32_t)last;
+            __syncthreads();
+        }
+    }
+    if (q.p < 1.0) {
+        const double unit = ldexp(1.0, min(47, 62 - (32 - __clz(V))));
+        for (int i = t; i < FBINS; i += FWG)
+            f.weight[i] = 0;
+        __syncthreads();
+        // no edge lies above the maximum, so that its own weight is 1
+        auto edge = [&](int b) SV_INLINE { return fminf(bin_high(b), r.max); };
+        each_float(few, [&](uint32_t bits, int id) SV_INLINE {
+            const float x = __uint_as_float(bits);
+            if (x != -INFINITY && kept(order_key(x), id, r)) {
+                // w * unit to the nearest integer, in the low bits of the sum with 2^52
+                const int b = float_bin(bits);
+                const double w = fma(weight(x, edge(b), r.c), unit, 0x1p52);
+                atomicAdd(&f.weight[b],
+                          (unsigned long long)__double_as_longlong(w) & 0xfffffffffffffull);
+            }
+        });
+        __syncthreads();
+        double goal = 0.0;
+        find_bin(
+            f,
+            [&](int b) SV_INLINE {
+                const unsigned long long n = f.weight[b];
+                return n ? (double)n / unit * weight(edge(b), r.max, r.c) : 0.0;
+            },
+            [&](double z) SV_INLINE {
+                goal = q.p * z;
+                return fmax(goal, 0x1p-1074);  // the first bin at least
+            });
+        const int bin = f.bin;
+        const double base = f.prefix;
+        if (!gather(few, bin_low(bin), bin_high(bin), r, f)) {
+            r.state = CUT_EXACT;
+            return r;
+        }
+        cut_in_order(r, base, GATHER, 1.0, goal, 0.0, f);
+        r.kept = V;
+    }
+    if (q.m > 0.0 && weight(key_value(r.cut), r.max, r.c) < q.m) {
+        r.cut = key_of_weight(r.max, r.c, q.m);
+        r.tie = V;
+        r.z = 0.0;
+    }
+    return r;
+}
+
+// The kept weight of a whole row, the same bits in every thread.
+template <int DT, typename W>
+__device__ __forceinline__ double row_total(const Units<DT> &un, const MayKeep<DT> &may, const W &law,
+                                            RedLds &red)
+{
+    const int units = un.count();
+    double s = 0.0;
+#pragma nounroll
+    for (int i0 = 0; i0 < units; i0 += BATCH) {
+        uint4 v[BATCH], x[BATCH];
+        load_batch(un, i0, v);
+        const uint32_t mask = look(un, i0, v, x, may, law);
+        unroll<0, BATCH>([&](auto j) SV_INLINE {
+            if (mask >> j & 1) {
+                const double w = law.sum(un.group(i0 + j), v[j], x[j]);
+                s += un.holds(i0 + j) ? w : 0.0;
+            }
+        });
+    }
+    return block_sum(s, red.d);
+}
+
+__global__ __launch_bounds__(FWG, 4) void k_filter_sample_f32(const char *logits, int V,
+                                                              int64_t stride, FilterPtrs f,
+                                                              const float *unif, int *tok,
+                                                              float *prob)
+{
+    __shared__ FloatLds fl;
+    __shared__ CutLds c;
     __shared__ DrawLds dl;
+    __shared__ RedLds red;
     const int n = blockIdx.x;
     const char *row = logits + (size_t)n * stride * 4;
-    const RowCut r = cut_by_bisection<0>(row, V, load_params(f, n, V), red);
-    int id = -1;
-    if (r.state == CUT_READY) {
-        const Groups<0> gr(row, V);
-        id = draw_row(Units<0>{gr, nullptr, -1}, MayKeep<0>(r), (double)unif[n], dl, DirectLaw<0>{r, 1.0});
+    const Groups<0> gr(row, V);
+    const Units<0> all{gr, nullptr, -1};
+    Units<0> few = all;
+    const Params q = load_params(f, n, V);
+    RowCut r = cut_floats(all, few, q, fl, c, dl, red);
+    if (r.state == CUT_EXACT) {
+        r = cut_by_bisection<0>(row, V, q, red);
+        few.n = -1;
     }
+    int id = -1;
+    if (r.state == CUT_READY)
+        id = draw_row(few, MayKeep<0>(r), (double)unif[n], dl, DirectLaw<0>{r, 1.0});
     if (threadIdx.x == 0) {
         tok[n] = id;
-        if (prob)
-            prob[n] = id < 0 ? NAN : (float)(weight(Elt<0>::one(row, id), r.max, r.c) / r.z);
+        if (prob) {
+            const double z = r.z > 0.0 ? r.z : dl.total;
+            prob[n] = id < 0 ? NAN : (float)(weight(Elt<0>::one(row, id), r.max, r.c) / z);
+        }
     }
 }
 
 // The RowCut of every target and draft row of a float32 verify: the B (K+1) target rows, then the
 // B K draft rows.
-__global__ __launch_bounds__(FWG) void k_filter_rows_f32(const char *tgt, const char *drf, int B,
-                                                         int K, int V, FilterPtrs ft, FilterPtrs fd,
-                                                         RowCut *cuts)
+__global__ __launch_bounds__(FWG, 4) void k_filter_rows_f32(const char *tgt, const char *drf, int B,
+                                                            int K, int V, FilterPtrs ft,
+                                                            FilterPtrs fd, RowCut *cuts)
 {
+    __shared__ FloatLds fl;
+    __shared__ CutLds c;
+    __shared__ DrawLds dl;
     __shared__ RedLds red;
     const int n = blockIdx.x, nt = B * (K + 1);
     const bool is_t = n < nt;
     const char *row = is_t ? tgt + (size_t)n * V * 4 : drf + (size_t)(n - nt) * V * 4;
     const Params q = is_t ? load_params(ft, n / (K + 1), V) : load_params(fd, (n - nt) / K, V);
-    const RowCut r = cut_by_bisection<0>(row, V, q, red);
+    const Groups<0> gr(row, V);
+    const Units<0> all{gr, nullptr, -1};
+    Units<0> few = all;
+    RowCut r = cut_floats(all, few, q, fl, c, dl, red);
+    if (r.state == CUT_EXACT)
+        r = cut_by_bisection<0>(row, V, q, red);
+    else if (r.state == CUT_READY && r.z == 0.0)
+        r.z = row_total(few, MayKeep<0>(r), DirectLaw<0>{r, 1.0}, red);
     if (threadIdx.x == 0)
         cuts[n] = r;
 }
