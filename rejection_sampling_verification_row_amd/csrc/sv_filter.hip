@@ -1593,7 +1593,8 @@ __global__ __launch_bounds__(FWG, 4) void k_filter_sample_bf16(const char *logit
 // in order exactly.  For top-p the bins' weights are needed too: one more pass adds them up in
 // LDS, as integers so that their order does not matter, in units of 2^-47 (for vocabularies past
 // 2^15 coarser, 2^-41 at 2^20) of the weight at the bin's upper edge: half a unit is lost per logit,
-// relative to its bin.  A row whose bin holds more than GATHER logits goes to cut_by_bisection.
+// relative to its bin.  A bin of more than GATHER logits is counted once more by its next 13 bits.
+// A row in which even that leaves more, GATHER equal logits at its cut, goes to cut_by_bisection.
 
 constexpr int BIN_HIGH = HBINS, BIN_ZERO = HBINS + 1, BIN_LOW = HBINS + 2, FBINS = HBINS + 3;
 constexpr int GATHER = 1024;
@@ -1678,20 +1679,23 @@ __device__ __forceinline__ double block_scan(double v, double *lds, double *tota
     return lane_value(wave_excl_from_incl(wi), __builtin_amdgcn_readfirstlane(wv)) + v;
 }
 
-// The last bin, in order, that holds something and before which lies less than goal; f.bin and
-// f.prefix.  val(bin) is what a bin holds, goal_of(total) the goal.  Returns the total.  A thread
-// takes eight bins; those outside the window join the threads that they stand next to.
-template <typename W, typename G>
-__device__ __forceinline__ double find_bin(FloatLds &f, W val, G goal_of)
+// The last bin, in order, that holds something and before which (counting `base` before all) lies
+// less than goal; f.bin and f.prefix.  val(bin) is what a bin holds, goal_of(total) the goal.
+// Returns the total.  A thread takes eight bins; those outside the window join the threads that
+// they stand next to.  SUB: the bins are parts of one, by magnitude; `down`: the largest first.
+template <bool SUB, typename W, typename G>
+__device__ __forceinline__ double find_bin(FloatLds &f, double base, bool down, W val, G goal_of)
 {
     const int t = threadIdx.x;
     constexpr int PER = HBINS / FWG;
     auto bin_of = [&](int i) SV_INLINE {       // i = 0: before the eight, 9: after them
-        if (i == 0)
-            return t == 0 ? BIN_HIGH : t == FWG / 2 ? BIN_ZERO : -1;
-        if (i == PER + 1)
-            return t == FWG - 1 ? BIN_LOW : -1;
         const int o = t * PER + i - 1;
+        if (i == 0)
+            return SUB ? -1 : t == 0 ? BIN_HIGH : t == FWG / 2 ? BIN_ZERO : -1;
+        if (i == PER + 1)
+            return !SUB && t == FWG - 1 ? BIN_LOW : -1;
+        if (SUB)
+            return down ? HBINS - 1 - o : o;
         return o < HMAG ? HMAG - 1 - o : o;
     };
     double sum = 0.0, total, run = 0.0, goal = 0.0;
@@ -1721,6 +1725,7 @@ __device__ __forceinline__ double find_bin(FloatLds &f, W val, G goal_of)
             for (int i = 0; i < t >> 6; ++i)
                 run += f.dwave[i];
         }
+        run += base;
         if (sum > 0.0 && run < goal)
             atomicMax(&f.place, t);
         __syncthreads();
@@ -1782,6 +1787,30 @@ __device__ __forceinline__ bool gather(const Units<0> &un, float lo, float hi, c
     }
     __syncthreads();
     return true;
+}
+
+// What the logits from lo to hi, a bin's, that r keeps hold by their next 13 bits: of(x) each, in
+// f.weight.
+template <typename O>
+__device__ __forceinline__ void count_parts(const Units<0> &un, float lo, float hi, const RowCut &r,
+                                            FloatLds &f, O of)
+{
+    for (int i = threadIdx.x; i < HBINS; i += FWG)
+        f.weight[i] = 0;
+    __syncthreads();
+    each_float(un, [&](uint32_t bits, int id) SV_INLINE {
+        const float x = __uint_as_float(bits);
+        if (x >= lo && x <= hi && kept(order_key(x), id, r))
+            atomicAdd(&f.weight[(bits & 0xffffu) >> 3], of(x));
+    });
+    __syncthreads();
+}
+
+__device__ __forceinline__ void part_range(int bin, int part, float &lo, float &hi)
+{
+    const uint32_t p = bin_pattern(bin) << 16 | (uint32_t)part << 3;
+    lo = __uint_as_float(bin >= HMAG ? p | 7u : p);
+    hi = __uint_as_float(bin >= HMAG ? p : p | 7u);
 }
 
 // How many of the ordered logits stay: those before which less than goal lies (counting `base`
@@ -1904,18 +1933,28 @@ __device__ __forceinline__ RowCut cut_floats(const Units<0> &all, Units<0> &few,
     if (r.state == CUT_NONE)
         return r;
     if (q.k < V) {
-        const double total = find_bin(f, [&](int b) SV_INLINE { return (double)f.hist[b]; },
-                                      [&](double) SV_INLINE { return (double)q.k; });
+        const double total = find_bin<false>(f, 0.0, false,
+                                             [&](int b) SV_INLINE { return (double)f.hist[b]; },
+                                             [&](double) SV_INLINE { return (double)q.k; });
         if (fl.active() || (double)q.k < total) {
             const int bin = f.bin;
-            const uint32_t before = (uint32_t)f.prefix;
+            uint32_t before = (uint32_t)f.prefix;
+            float lo = bin_low(bin), hi = bin_high(bin);
             if (before + f.hist[bin] <= GATHER) {
                 // all that top-k can keep is in hand: the three cuts at once
-                gather(few, bin_low(bin), FLT_MAX, r, f);
+                gather(few, lo, FLT_MAX, r, f);
                 cut_in_order(r, 0.0, q.k, q.p, INFINITY, q.m, f);
                 return r;
             }
-            if (!gather(few, bin_low(bin), bin_high(bin), r, f)) {
+            if (f.hist[bin] > GATHER && bin < HBINS) {
+                const double was = f.prefix;
+                count_parts(few, lo, hi, r, f, [&](float) SV_INLINE { return 1ull; });
+                find_bin<true>(f, was, bin < HMAG, [&](int b) SV_INLINE { return (double)f.weight[b]; },
+                               [&](double) SV_INLINE { return (double)q.k; });
+                before = (uint32_t)f.prefix;
+                part_range(bin, f.bin, lo, hi);
+            }
+            if (!gather(few, lo, hi, r, f)) {
                 r.state = CUT_EXACT;
                 return r;
             }
@@ -1928,35 +1967,49 @@ __device__ __forceinline__ RowCut cut_floats(const Units<0> &all, Units<0> &few,
     if (q.p < 1.0) {
         const double unit = ldexp(1.0, min(47, 62 - (32 - __clz(V))));
         for (int i = t; i < FBINS; i += FWG)
-            f.weight[i] = 0;
+            f.weight[i] = f.hist[i] = 0;
         __syncthreads();
         // no edge lies above the maximum, so that its own weight is 1
         auto edge = [&](int b) SV_INLINE { return fminf(bin_high(b), r.max); };
+        // w * unit to the nearest integer, in the low bits of the sum with 2^52
+        auto units_of = [&](float x, float top) SV_INLINE {
+            const double w = fma(weight(x, top, r.c), unit, 0x1p52);
+            return (unsigned long long)__double_as_longlong(w) & 0xfffffffffffffull;
+        };
+        auto weight_of = [&](int b, float top) SV_INLINE {
+            const unsigned long long n = f.weight[b];
+            return n ? (double)n / unit * weight(top, r.max, r.c) : 0.0;
+        };
         each_float(few, [&](uint32_t bits, int id) SV_INLINE {
             const float x = __uint_as_float(bits);
             if (x != -INFINITY && kept(order_key(x), id, r)) {
-                // w * unit to the nearest integer, in the low bits of the sum with 2^52
                 const int b = float_bin(bits);
-                const double w = fma(weight(x, edge(b), r.c), unit, 0x1p52);
-                atomicAdd(&f.weight[b],
-                          (unsigned long long)__double_as_longlong(w) & 0xfffffffffffffull);
+                atomicAdd(&f.weight[b], units_of(x, edge(b)));
+                if (b < HBINS)
+                    atomicAdd(&f.hist[b], 1u);
             }
         });
         __syncthreads();
         double goal = 0.0;
-        find_bin(
-            f,
-            [&](int b) SV_INLINE {
-                const unsigned long long n = f.weight[b];
-                return n ? (double)n / unit * weight(edge(b), r.max, r.c) : 0.0;
-            },
+        find_bin<false>(
+            f, 0.0, false, [&](int b) SV_INLINE { return weight_of(b, edge(b)); },
             [&](double z) SV_INLINE {
                 goal = q.p * z;
                 return fmax(goal, 0x1p-1074);  // the first bin at least
             });
         const int bin = f.bin;
-        const double base = f.prefix;
-        if (!gather(few, bin_low(bin), bin_high(bin), r, f)) {
+        const float top = edge(bin);
+        double base = f.prefix;
+        float lo = bin_low(bin), hi = bin_high(bin);
+        if (bin < HBINS && f.hist[bin] > GATHER) {
+            __syncthreads();
+            count_parts(few, lo, hi, r, f, [&](float x) SV_INLINE { return units_of(x, top); });
+            find_bin<true>(f, base, bin < HMAG, [&](int b) SV_INLINE { return weight_of(b, top); },
+                           [&](double) SV_INLINE { return fmax(goal, 0x1p-1074); });
+            base = f.prefix;
+            part_range(bin, f.bin, lo, hi);
+        }
+        if (!gather(few, lo, hi, r, f)) {
             r.state = CUT_EXACT;
             return r;
         }
