@@ -76,6 +76,8 @@ def library_path() -> str:
 def load():
     """Load libspecverify.so, building it first only if it is missing."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -166,6 +168,20 @@ def _ptrs(*specs):
     return tuple(_ptr(x) for x, _, _, _ in specs)
 
 
+_KINDS = {}       # kind -> (accepted element types, their name), filled at the first tensor
+
+
+def _kinds():
+    import torch
+    _KINDS.update({
+        SPECVERIFY_F32: ((torch.float32,), "float32"),
+        SPECVERIFY_BF16: ((torch.bfloat16, torch.int16, torch.uint16),
+                          "bfloat16 (or its 16-bit patterns)"),
+        "i32": ((torch.int32,), "int32"), "f32": ((torch.float32,), "float32"),
+        "u8": ((torch.uint8, torch.bool), "uint8")})
+    return _KINDS
+
+
 def _arr(x, count: int, kind, name: str):
     """Check a tensor argument against the call's shape: its element type (kind: "i32", "f32",
     "u8", or a logits dtype SPECVERIFY_F32 / SPECVERIFY_BF16) and at least `count` elements,
@@ -173,17 +189,12 @@ def _arr(x, count: int, kind, name: str):
     extent is the caller's to guarantee."""
     if x is None or isinstance(x, int) or not hasattr(x, "data_ptr"):
         return
-    import torch
-    if kind in (SPECVERIFY_F32, SPECVERIFY_BF16):
-        ok = ({torch.float32} if kind == SPECVERIFY_F32
-              else {torch.bfloat16, torch.int16, torch.uint16})
-        what = "float32" if kind == SPECVERIFY_F32 else "bfloat16 (or its 16-bit patterns)"
-    else:
-        ok = {"i32": {torch.int32}, "f32": {torch.float32}, "u8": {torch.uint8, torch.bool}}[kind]
-        what = {"i32": "int32", "f32": "float32", "u8": "uint8"}[kind]
+    # any other logits dtype is checked as bfloat16 and refused by the library
+    kinds = _KINDS or _kinds()
+    ok, what = kinds.get(kind) or kinds[SPECVERIFY_BF16 if isinstance(kind, int) else kind]
     if x.dtype not in ok:
         raise ValueError("%s: expected %s elements, got %s" % (name, what, x.dtype))
-    if x.numel() < max(int(count), 0):
+    if x.numel() < count:
         raise ValueError("%s: needs at least %d elements for this call, has %d"
                          % (name, count, x.numel()))
 

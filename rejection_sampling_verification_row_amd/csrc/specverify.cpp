@@ -659,8 +659,11 @@ int specverify_cache_create(specverify_cache **out, int device, int num_pages, i
     const size_t b_pools = align_up((size_t)std::max(num_pools, 1) * sizeof(void *));
     const size_t b_both = align_up(both * sizeof(int));
     const size_t b_pages = align_up((size_t)num_pages * sizeof(int));
-    const size_t b_seqs = align_up((size_t)num_seqs * sizeof(int));
-    const size_t total = b_pools + 3 * b_both + 2 * b_pages + 2 * b_seqs + align_up(sizeof(int));
+    const size_t b_entries = align_up((size_t)num_seqs * sizeof(sv::CacheEntry));
+    const size_t b_stretches = align_up(
+        ((size_t)num_pages + sv::CACHE_STRETCH - 1) / sv::CACHE_STRETCH * sizeof(int));
+    const size_t b_one = align_up(sizeof(int));
+    const size_t total = b_pools + b_both + 4 * b_pages + b_entries + b_stretches + b_one;
     specverify_cache *c = new (std::nothrow) specverify_cache();
     if (!c)
         return SPECVERIFY_ENOMEM;
@@ -688,13 +691,13 @@ int specverify_cache_create(specverify_cache **out, int device, int num_pages, i
     char *dpools = take(b_pools);
     v.pools = reinterpret_cast<char *const *>(dpools);
     v.owner = reinterpret_cast<int *>(take(b_both));
-    v.src = reinterpret_cast<int *>(take(b_both));
-    v.dst = reinterpret_cast<int *>(take(b_both));
+    v.src = reinterpret_cast<int *>(take(b_pages));
+    v.dst = reinterpret_cast<int *>(take(b_pages));
     v.free_ids = reinterpret_cast<int *>(take(b_pages));
     v.map = reinterpret_cast<int *>(take(b_pages));
-    v.off = reinterpret_cast<int *>(take(b_seqs));
-    v.len = reinterpret_cast<int *>(take(b_seqs));
-    v.count = reinterpret_cast<int *>(take(align_up(sizeof(int))));
+    v.entries = reinterpret_cast<sv::CacheEntry *>(take(b_entries));
+    v.free_count = reinterpret_cast<int *>(take(b_stretches));
+    v.count = reinterpret_cast<int *>(take(b_one));
     c->device = device;
     c->num_cus = cus;
     c->bytes = total;

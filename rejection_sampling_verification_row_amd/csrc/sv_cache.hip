@@ -5,9 +5,13 @@
 // list whose order would depend on the history: a call that takes pages takes the lowest free
 // ids, in list order, so its result is a function of the state alone.
 //
-// A call that takes pages is a plan and an apply: one workgroup checks the list, prefix-sums what
-// each entry asks for and finds the free ids; then the whole chip writes the tables and copies
-// pages.  The plan keeps in scratch whatever an apply workgroup could find changed by another.
+// A call that takes pages is a plan and an apply.  The free pages are listed stretch by stretch of
+// the pool, a workgroup each; one workgroup checks the list and prefix-sums what its entries ask
+// for; then the whole chip writes the tables and copies pages.  The plan leaves for each entry one
+// record of all that its apply needs, since an apply workgroup may find the state changed by
+// another, and since a record is one trip to memory.
+#include <algorithm>
+
 #include "sv_device.h"
 #include "sv_internal.h"
 
@@ -56,29 +60,69 @@ __device__ inline int block_incl_scan(int v, int *lds, int *total)
     return before + inc;
 }
 
-// The first `want` free pages, ascending, into ids (fewer if there are fewer); returns how many.
-__device__ int find_free(const CacheView &c, int want, int *ids, int *lds)
+// The free pages of a stretch, ascending, into its part of free_ids.
+__device__ void list_free(const CacheView &c, int stretch, int *lds)
 {
-    int found = 0;
-    for (int p0 = 0; p0 < c.num_pages && found < want; p0 += CWG * 4) {
-        const int p = p0 + (int)threadIdx.x * 4;
-        int bits = 0;
+    const int p = stretch * CACHE_STRETCH + (int)threadIdx.x * 4;
+    static_assert(CACHE_STRETCH == CWG * 4, "four pages to a thread");
+    int bits = 0;
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-            if (p + k < c.num_pages && c.refs[p + k] == 0)
-                bits |= 1 << k;
+    for (int k = 0; k < 4; ++k)
+        if (p + k < c.num_pages && c.refs[p + k] == 0)
+            bits |= 1 << k;
+    int all;
+    int at = stretch * CACHE_STRETCH + block_incl_scan(__popc(bits), lds, &all) - __popc(bits);
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+        if (bits >> k & 1)
+            c.free_ids[at++] = p + k;
+    if (threadIdx.x == 0)
+        c.free_count[stretch] = all;
+}
+
+// Pools of more than one stretch list their free pages in a launch before the plan.
+__global__ __launch_bounds__(CWG) void k_list_free(CacheView c)
+{
+    __shared__ int lds[CWAVES];
+    list_free(c, blockIdx.x, lds);
+}
+
+// free_count becomes the free pages before each stretch, in LDS too as far as it holds them;
+// returns how many there are.
+constexpr int LDS_STRETCHES = 1024;
+
+__device__ int scan_free(const CacheView &c, int stretches, int *before, int *lds)
+{
+    int sum = 0;
+    for (int s0 = 0; s0 < stretches; s0 += CWG) {
+        const int s = s0 + threadIdx.x, n = s < stretches ? c.free_count[s] : 0;
         int all;
-        int at = found + block_incl_scan(__popc(bits), lds, &all) - __popc(bits);
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-            if (bits >> k & 1) {
-                if (at < want)
-                    ids[at] = p + k;
-                ++at;
-            }
-        found += all;
+        const int inc = block_incl_scan(n, lds, &all);
+        if (s < stretches) {
+            c.free_count[s] = sum + inc - n;
+            if (s < LDS_STRETCHES)
+                before[s] = sum + inc - n;
+        }
+        sum += all;
     }
-    return min(found, want);
+    __syncthreads();
+    return sum;
+}
+
+// The i-th free page: the last stretch with no more than i before it.
+__device__ int free_page(const CacheView &c, int stretches, const int *before, int i)
+{
+    const bool small = stretches <= LDS_STRETCHES;
+    int lo = 0, hi = stretches - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if ((small ? before[mid] : c.free_count[mid]) <= i)
+            lo = mid;
+        else
+            hi = mid - 1;
+    }
+    const int at = i - (small ? before[lo] : c.free_count[lo]);
+    return c.free_ids[lo * CACHE_STRETCH + at];
 }
 
 // The list entries that name a sequence first own it; later ones are refused.
@@ -103,48 +147,47 @@ __device__ void unclaim(const CacheView &c, int n, const int *seqs)
 }
 
 // an entry's sequence has a state that an operation may build on
-__device__ inline bool sound(const CacheView &c, int s)
+__device__ inline bool sound(const CacheView &c, int b, int l)
 {
-    const int b = c.blocks[s], l = c.lengths[s];
     return b >= 0 && b <= c.max_blocks && l >= 0 && l <= b * c.page_tokens;
 }
 
-// Gives the entries their places among the free pages.  ask(i) is what entry i asks for (-1: it
-// is refused); an entry is granted when all that is asked up to it exists.
+// Gives the entries their places among the free pages, and lists the pages taken in c.map.
+// ask(i, e) is what entry i asks for and fills in its record (-1: it is refused); an entry is
+// granted when all that is asked up to it exists.
 template <typename Ask>
 __device__ void grant(const CacheView &c, int n, int *status, int *lds, Ask ask)
 {
+    __shared__ int before[LDS_STRETCHES];
+    const int stretches = (c.num_pages + CACHE_STRETCH - 1) / CACHE_STRETCH;
+    if (stretches == 1) {
+        list_free(c, 0, lds);
+        __syncthreads();
+    }
+    const int found = scan_free(c, stretches, before, lds);
     int sum = 0;
     for (int i0 = 0; i0 < n; i0 += CWG) {
         const int i = i0 + threadIdx.x;
-        const int a = i < n ? ask(i) : 0;
+        CacheEntry e = {-1, -1, 0, 0, 0, 0, -1, -1};
+        const int a = i < n ? ask(i, e) : 0;
         int all;
         // no overflow: an entry asks for at most max_blocks + 1 pages, which is at most 2^20 + 1
         const int inc = block_incl_scan(max(a, 0), lds, &all);
-        if (i < n)
-            c.off[i] = a < 0 ? -1 : sum + inc - a;
+        if (i < n) {
+            const bool ok = a >= 0 && sum + inc <= found;
+            e.first = sum + inc - a;
+            if (!ok)
+                e.seq = -1;
+            else if (e.src >= 0)
+                e.dst = free_page(c, stretches, before, e.first++);
+            c.entries[i] = e;
+            if (status)
+                status[i] = ok ? 0 : -1;
+        }
         sum = min(sum + all, c.num_pages + 1);
     }
-    __syncthreads();
-    const int found = find_free(c, min(sum, c.num_pages), c.free_ids, lds);
-    __syncthreads();
-    for (int i = threadIdx.x; i < n; i += CWG) {
-        const int o = c.off[i];
-        const bool ok = o >= 0 && o + ask(i) <= found;
-        c.off[i] = ok ? o : -1;
-        if (status)
-            status[i] = ok ? 0 : -1;
-    }
-}
-
-// Reserve: entry i needs pages for lengths + counts tokens, and a page of its own where it will
-// write into a partly filled page that another holds too.
-__device__ inline bool needs_own(const CacheView &c, int s, int len)
-{
-    if (len % c.page_tokens == 0)
-        return false;
-    const int pg = c.tables[(size_t)s * c.max_blocks + len / c.page_tokens];
-    return in_range(pg, c.num_pages) && c.refs[pg] > 1;
+    for (int i = threadIdx.x; i < min(sum, found); i += CWG)
+        c.map[i] = free_page(c, stretches, before, i);
 }
 
 __global__ __launch_bounds__(CWG) void k_reserve_plan(CacheView c, int n, const int *seqs,
@@ -152,93 +195,122 @@ __global__ __launch_bounds__(CWG) void k_reserve_plan(CacheView c, int n, const 
 {
     __shared__ int lds[CWAVES];
     claim(c, n, seqs);
-    auto ask = [&](int i) {
-        const int s = seqs ? seqs[i] : i;
-        if (!in_range(s, c.num_seqs) || load_agent(&c.owner[s]) != i || !sound(c, s))
+    grant(c, n, status, lds, [&](int i, CacheEntry &e) {
+        const int s = seqs ? seqs[i] : i, cnt = counts[i];
+        if (!in_range(s, c.num_seqs) || load_agent(&c.owner[s]) != i)
             return -1;
-        const int len = c.lengths[s], cnt = counts[i];
-        if (cnt < 0 || cnt > c.max_blocks * c.page_tokens - len)
+        const int len = c.lengths[s], had = c.blocks[s];
+        if (!sound(c, had, len) || cnt < 0 || cnt > c.max_blocks * c.page_tokens - len)
             return -1;
+        e.seq = s;
+        e.had = e.want = had;
+        e.len = len;
         if (cnt == 0)
             return 0;
-        return max(0, ceil_div(len + cnt, c.page_tokens) - c.blocks[s]) + (int)needs_own(c, s, len);
-    };
-    grant(c, n, status, lds, ask);
-    __syncthreads();
-    for (int i = threadIdx.x; i < n; i += CWG) {
-        const int s = seqs ? seqs[i] : i;
-        int from = -1, to = -1;
-        if (c.off[i] >= 0 && counts[i] > 0 && needs_own(c, s, c.lengths[s])) {
-            from = c.tables[(size_t)s * c.max_blocks + c.lengths[s] / c.page_tokens];
-            to = c.free_ids[c.off[i]];
+        e.want = max(had, ceil_div(len + cnt, c.page_tokens));
+        if (len % c.page_tokens != 0) {
+            // a page of its own where it will write into one that another holds too
+            const int pg = c.tables[(size_t)s * c.max_blocks + len / c.page_tokens];
+            if (in_range(pg, c.num_pages) && c.refs[pg] > 1)
+                e.src = pg;
         }
-        c.src[i] = from;
-        c.dst[i] = to;
-    }
+        return e.want - had + (e.src >= 0);
+    });
     unclaim(c, n, seqs);
 }
 
-// Copies the planned pages in every pool.  A work item is 16 KiB of one page in one pool; the
-// workgroups take items at a stride.
+// Copies the planned pages in every pool: 16 KiB of a page to a workgroup, which stands at (part of
+// the page, pool, entries) and strides along each; pages(i, from, to) gives entry i's pages.  Few
+// entries copy anything, so a wave reads 64 of them at once, one a lane, and walks those that do.
 constexpr int COPY_WG = 256;
 constexpr int COPY_VECS = 4;
 constexpr int COPY_ITEM = COPY_WG * COPY_VECS * 16;
 
-__device__ void copy_pages(const CacheView &c, int n, const int *src, const int *dst)
+__device__ inline void copy_page(const CacheView &c, int from, int to)
 {
-    const int per = (int)((c.page_bytes + COPY_ITEM - 1) / COPY_ITEM);
-    const int64_t items = (int64_t)n * c.num_pools * per;
-    for (int64_t it = blockIdx.x; it < items; it += gridDim.x) {
-        const int part = (int)(it % per);
-        const int64_t rest = it / per;
-        const int pool = (int)(rest % c.num_pools), i = (int)(rest / c.num_pools);
-        const int from = src[i], to = dst[i];
-        if (!in_range(from, c.num_pages) || !in_range(to, c.num_pages))
-            continue;
+    for (int pool = blockIdx.y; pool < c.num_pools; pool += gridDim.y) {
         const char *a = c.pools[pool] + (int64_t)from * c.page_bytes;
         char *b = c.pools[pool] + (int64_t)to * c.page_bytes;
-        const int64_t o = (int64_t)part * COPY_ITEM + (int64_t)threadIdx.x * 16;
-        uint4 v[COPY_VECS];
+        for (int64_t o = (int64_t)blockIdx.x * COPY_ITEM + threadIdx.x * 16; o < c.page_bytes;
+             o += (int64_t)gridDim.x * COPY_ITEM) {
+            uint4 v[COPY_VECS];
 #pragma unroll
-        for (int k = 0; k < COPY_VECS; ++k)
-            if (o + k * COPY_WG * 16 < c.page_bytes)
-                v[k] = *reinterpret_cast<const uint4 *>(a + o + k * COPY_WG * 16);
+            for (int k = 0; k < COPY_VECS; ++k)
+                if (o + k * COPY_WG * 16 < c.page_bytes)
+                    v[k] = *reinterpret_cast<const uint4 *>(a + o + k * COPY_WG * 16);
 #pragma unroll
-        for (int k = 0; k < COPY_VECS; ++k)
-            if (o + k * COPY_WG * 16 < c.page_bytes)
-                *reinterpret_cast<uint4 *>(b + o + k * COPY_WG * 16) = v[k];
+            for (int k = 0; k < COPY_VECS; ++k)
+                if (o + k * COPY_WG * 16 < c.page_bytes)
+                    *reinterpret_cast<uint4 *>(b + o + k * COPY_WG * 16) = v[k];
+        }
     }
 }
 
-__global__ __launch_bounds__(COPY_WG) void k_reserve_apply(CacheView c, int n, const int *seqs,
-                                                           const int *counts)
+template <typename P> __device__ void copy_pages(const CacheView &c, int n, P pages)
 {
-    const int lane = threadIdx.x & 63, waves = gridDim.x * (COPY_WG / 64);
-    for (int i = blockIdx.x * (COPY_WG / 64) + (threadIdx.x >> 6); i < n; i += waves) {
-        int o = c.off[i];
-        if (o < 0 || counts[i] == 0)
-            continue;
-        const int s = seqs ? seqs[i] : i;
-        const int len = c.lengths[s], had = c.blocks[s];
-        const int want = ceil_div(len + counts[i], c.page_tokens);
-        int *row = c.tables + (size_t)s * c.max_blocks;
-        if (c.dst[i] >= 0) {
-            if (lane == 0) {
-                row[len / c.page_tokens] = c.dst[i];
-                c.refs[c.dst[i]] = 1;
-                atomicSub(&c.refs[c.src[i]], 1);
-            }
-            ++o;
+    const int lane = threadIdx.x & 63;
+    const int64_t step = 64 * (int64_t)gridDim.z;
+    for (int64_t i0 = blockIdx.z; i0 < n; i0 += step) {
+        const int64_t i = i0 + (int64_t)lane * gridDim.z;
+        int from = -1, to = -1;
+        if (i < n)
+            pages((int)i, from, to);
+        uint64_t copies = __ballot(in_range(from, c.num_pages) && in_range(to, c.num_pages));
+        while (copies) {
+            const int j = __builtin_ctzll(copies);
+            copies &= copies - 1;
+            copy_page(c, __shfl(from, j), __shfl(to, j));
         }
-        for (int j = had + lane; j < want; j += 64) {
-            const int pg = c.free_ids[o + j - had];
-            row[j] = pg;
-            c.refs[pg] = 1;
-        }
-        if (lane == 0 && want > had)
-            c.blocks[s] = want;
     }
-    copy_pages(c, n, c.src, c.dst);
+}
+
+__device__ void copy_entries(const CacheView &c, int n)
+{
+    copy_pages(c, n, [&](int i, int &from, int &to) {
+        from = c.entries[i].src;
+        to = c.entries[i].dst;
+    });
+}
+
+// Workgroups of a copy's launch, and this one among them.
+__device__ inline int copy_groups() { return gridDim.x * gridDim.y * gridDim.z; }
+__device__ inline int copy_group()
+{
+    return (blockIdx.z * gridDim.y + blockIdx.y) * gridDim.x + blockIdx.x;
+}
+
+// Pages had .. want of an entry, one lane each, and its copied page.
+__device__ inline void take_pages(const CacheView &c, const CacheEntry &e, int *row)
+{
+    const int lane = threadIdx.x & 63;
+    for (int j = e.had + lane; j < e.want; j += 64) {
+        const int pg = c.map[e.first + j - e.had];
+        row[j] = pg;
+        c.refs[pg] = 1;
+    }
+    if (lane == 0 && e.dst >= 0)
+        c.refs[e.dst] = 1;
+}
+
+__global__ __launch_bounds__(COPY_WG) void k_reserve_apply(CacheView c, int n)
+{
+    const int lane = threadIdx.x & 63, waves = copy_groups() * (COPY_WG / 64);
+    for (int i = copy_group() * (COPY_WG / 64) + (threadIdx.x >> 6); i < n; i += waves) {
+        const CacheEntry e = c.entries[i];
+        if (e.seq < 0)
+            continue;
+        int *row = c.tables + (size_t)e.seq * c.max_blocks;
+        take_pages(c, e, row);
+        if (lane == 0) {
+            if (e.dst >= 0) {
+                row[e.len / c.page_tokens] = e.dst;
+                atomicSub(&c.refs[e.src], 1);
+            }
+            if (e.want > e.had)
+                c.blocks[e.seq] = e.want;
+        }
+    }
+    copy_entries(c, n);
 }
 
 __device__ inline void release(const CacheView &c, int pg)
@@ -253,10 +325,10 @@ __global__ __launch_bounds__(CWG) void k_commit(CacheView c, int n, const int *s
     claim(c, n, seqs);
     for (int i = threadIdx.x; i < n; i += CWG) {
         const int s = seqs ? seqs[i] : i;
-        bool ok = in_range(s, c.num_seqs) && load_agent(&c.owner[s]) == i && sound(c, s);
+        bool ok = in_range(s, c.num_seqs) && load_agent(&c.owner[s]) == i;
         if (ok) {
             const int had = c.blocks[s], len = c.lengths[s], add = accepted[i];
-            ok = add >= -1 && add < had * c.page_tokens - len;
+            ok = sound(c, had, len) && add >= -1 && add < had * c.page_tokens - len;
             if (ok) {
                 const int left = ceil_div(len + add + 1, c.page_tokens);
                 int *row = c.tables + (size_t)s * c.max_blocks;
@@ -279,45 +351,41 @@ __global__ __launch_bounds__(CWG) void k_fork_plan(CacheView c, int n, const int
 {
     __shared__ int lds[CWAVES];
     claim(c, n, children);
-    auto ask = [&](int i) {
+    grant(c, n, status, lds, [&](int i, CacheEntry &e) {
         const int a = parents[i], b = children[i];
         if (!in_range(a, c.num_seqs) || !in_range(b, c.num_seqs) || a == b ||
-            load_agent(&c.owner[b]) != i || c.blocks[b] != 0 || c.lengths[b] != 0 || !sound(c, a))
+            load_agent(&c.owner[b]) != i || c.blocks[b] != 0 || c.lengths[b] != 0)
             return -1;
-        return (int)(c.lengths[a] % c.page_tokens != 0);
-    };
-    grant(c, n, status, lds, ask);
-    __syncthreads();
-    for (int i = threadIdx.x; i < n; i += CWG) {
-        int from = -1, to = -1;
-        if (c.off[i] >= 0) {
-            const int a = parents[i], len = c.lengths[a];
-            c.len[i] = len;
-            if (len % c.page_tokens != 0) {
-                from = c.tables[(size_t)a * c.max_blocks + len / c.page_tokens];
-                to = c.free_ids[c.off[i]];
-            }
-        }
-        c.src[i] = from;
-        c.dst[i] = to;
-    }
+        const int len = c.lengths[a];
+        if (!sound(c, c.blocks[a], len))
+            return -1;
+        e.seq = b;
+        e.from = a;
+        e.len = len;
+        e.had = e.want = ceil_div(len, c.page_tokens);
+        if (len % c.page_tokens == 0)
+            return 0;
+        // a partly filled page is replaced whatever the table names, out of range without contents
+        const int pg = c.tables[(size_t)a * c.max_blocks + e.had - 1];
+        e.src = pg >= 0 ? pg : c.num_pages;
+        return 1;
+    });
     unclaim(c, n, children);
 }
 
-__global__ __launch_bounds__(COPY_WG) void k_fork_apply(CacheView c, int n, const int *parents,
-                                                        const int *children)
+__global__ __launch_bounds__(COPY_WG) void k_fork_apply(CacheView c, int n)
 {
-    const int lane = threadIdx.x & 63, waves = gridDim.x * (COPY_WG / 64);
-    for (int i = blockIdx.x * (COPY_WG / 64) + (threadIdx.x >> 6); i < n; i += waves) {
-        if (c.off[i] < 0)
+    const int lane = threadIdx.x & 63, waves = copy_groups() * (COPY_WG / 64);
+    for (int i = copy_group() * (COPY_WG / 64) + (threadIdx.x >> 6); i < n; i += waves) {
+        const CacheEntry e = c.entries[i];
+        if (e.seq < 0)
             continue;
-        const int len = c.len[i], nb = ceil_div(len, c.page_tokens), to = c.dst[i];
-        const int *from = c.tables + (size_t)parents[i] * c.max_blocks;
-        int *row = c.tables + (size_t)children[i] * c.max_blocks;
-        for (int j = lane; j < nb; j += 64) {
-            if (to >= 0 && j == nb - 1) {
-                row[j] = to;
-                c.refs[to] = 1;
+        const int *from = c.tables + (size_t)e.from * c.max_blocks;
+        int *row = c.tables + (size_t)e.seq * c.max_blocks;
+        for (int j = lane; j < e.want; j += 64) {
+            if (e.dst >= 0 && j == e.want - 1) {
+                row[j] = e.dst;
+                c.refs[e.dst] = 1;
             } else {
                 const int pg = from[j];
                 row[j] = pg;
@@ -326,11 +394,11 @@ __global__ __launch_bounds__(COPY_WG) void k_fork_apply(CacheView c, int n, cons
             }
         }
         if (lane == 0) {
-            c.blocks[children[i]] = nb;
-            c.lengths[children[i]] = len;
+            c.blocks[e.seq] = e.want;
+            c.lengths[e.seq] = e.len;
         }
     }
-    copy_pages(c, n, c.src, c.dst);
+    copy_entries(c, n);
 }
 
 // One wave per entry.  The exchange lets only one of several entries that name a sequence see its
@@ -400,8 +468,8 @@ __global__ __launch_bounds__(CWG) void k_compact_plan(CacheView c, int *page_map
 __global__ __launch_bounds__(COPY_WG) void k_compact_apply(CacheView c)
 {
     const int n = *c.count;
-    const int64_t threads = (int64_t)gridDim.x * COPY_WG;
-    const int64_t t = (int64_t)blockIdx.x * COPY_WG + threadIdx.x;
+    const int64_t threads = (int64_t)copy_groups() * COPY_WG;
+    const int64_t t = (int64_t)copy_group() * COPY_WG + threadIdx.x;
     for (int64_t i = t; i < n; i += threads) {
         c.refs[c.dst[i]] = c.refs[c.src[i]];
         c.refs[c.src[i]] = 0;
@@ -412,7 +480,10 @@ __global__ __launch_bounds__(COPY_WG) void k_compact_apply(CacheView c)
             if (in_range(pg, c.num_pages) && c.map[pg] != pg)
                 c.tables[e] = c.map[pg];
         }
-    copy_pages(c, n, c.src, c.dst);
+    copy_pages(c, n, [&](int i, int &from, int &to) {
+        from = c.src[i];
+        to = c.dst[i];
+    });
 }
 
 // Copy: an entry is refused if a page is out of range, its destination is an earlier entry's, or
@@ -441,7 +512,10 @@ __global__ __launch_bounds__(CWG) void k_copy_plan(CacheView c, int n, const int
 
 __global__ __launch_bounds__(COPY_WG) void k_copy_apply(CacheView c, int n)
 {
-    copy_pages(c, n, c.src, c.dst);
+    copy_pages(c, n, [&](int i, int &from, int &to) {
+        from = c.src[i];
+        to = c.dst[i];
+    });
 }
 
 __global__ void k_cache_init(CacheView c)
@@ -451,15 +525,24 @@ __global__ void k_cache_init(CacheView c)
         c.owner[i] = CACHE_NO_OWNER;
 }
 
-// workgroups of an apply: one per copy item up to 8 per compute unit, and at least one wave per
-// four list entries
-int apply_grid(const CacheView &c, int cus, int64_t n)
+hipError_t list_stretches(hipStream_t st, const CacheView &c)
 {
-    const int64_t per = (c.page_bytes + COPY_ITEM - 1) / COPY_ITEM;
-    const int64_t items = n * c.num_pools * per;
-    const int64_t least = (n + COPY_WG / 64 - 1) / (COPY_WG / 64);
-    const int64_t g = items > least ? items : least;
-    return (int)(g < 8 * (int64_t)cus ? (g > 0 ? g : 1) : 8 * (int64_t)cus);
+    const int n = (c.num_pages + CACHE_STRETCH - 1) / CACHE_STRETCH;
+    if (n > 1)
+        k_list_free<<<n, CWG, 0, st>>>(c);
+    return hipGetLastError();
+}
+
+// The launch of an apply over n entries: a workgroup for every part of a page in every pool, and
+// entries until there are about 8 workgroups per compute unit.
+dim3 apply_grid(const CacheView &c, int cus, int64_t n)
+{
+    const int64_t most = 8 * (int64_t)cus;
+    const int64_t parts = std::max<int64_t>((c.page_bytes + COPY_ITEM - 1) / COPY_ITEM, 1);
+    const int64_t x = std::min(parts, most);
+    const int64_t y = std::min<int64_t>(std::max(c.num_pools, 1), most / x);
+    const int64_t z = std::min<int64_t>(std::max<int64_t>(n, 1), most / x / y);
+    return dim3((unsigned)x, (unsigned)y, (unsigned)z);
 }
 
 }  // namespace
@@ -474,11 +557,14 @@ hipError_t launch_cache_init(hipStream_t st, const CacheView &c)
 hipError_t launch_cache_reserve(hipStream_t st, const CacheView &c, int cus, int n, const int *seqs,
                                 const int *counts, int *status)
 {
-    k_reserve_plan<<<1, CWG, 0, st>>>(c, n, seqs, counts, status);
-    hipError_t e = hipGetLastError();
+    hipError_t e = list_stretches(st, c);
     if (e != hipSuccess)
         return e;
-    k_reserve_apply<<<apply_grid(c, cus, n), COPY_WG, 0, st>>>(c, n, seqs, counts);
+    k_reserve_plan<<<1, CWG, 0, st>>>(c, n, seqs, counts, status);
+    e = hipGetLastError();
+    if (e != hipSuccess)
+        return e;
+    k_reserve_apply<<<apply_grid(c, cus, n), COPY_WG, 0, st>>>(c, n);
     return hipGetLastError();
 }
 
@@ -492,11 +578,14 @@ hipError_t launch_cache_commit(hipStream_t st, const CacheView &c, int n, const 
 hipError_t launch_cache_fork(hipStream_t st, const CacheView &c, int cus, int n,
                              const int *parents, const int *children, int *status)
 {
-    k_fork_plan<<<1, CWG, 0, st>>>(c, n, parents, children, status);
-    hipError_t e = hipGetLastError();
+    hipError_t e = list_stretches(st, c);
     if (e != hipSuccess)
         return e;
-    k_fork_apply<<<apply_grid(c, cus, n), COPY_WG, 0, st>>>(c, n, parents, children);
+    k_fork_plan<<<1, CWG, 0, st>>>(c, n, parents, children, status);
+    e = hipGetLastError();
+    if (e != hipSuccess)
+        return e;
+    k_fork_apply<<<apply_grid(c, cus, n), COPY_WG, 0, st>>>(c, n);
     return hipGetLastError();
 }
 
@@ -514,7 +603,7 @@ hipError_t launch_cache_compact(hipStream_t st, const CacheView &c, int cus, int
     hipError_t e = hipGetLastError();
     if (e != hipSuccess)
         return e;
-    k_compact_apply<<<8 * cus, COPY_WG, 0, st>>>(c);
+    k_compact_apply<<<apply_grid(c, cus, c.num_pages), COPY_WG, 0, st>>>(c);
     return hipGetLastError();
 }
 

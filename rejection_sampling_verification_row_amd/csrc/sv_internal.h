@@ -238,6 +238,8 @@ hipError_t launch_filter_verify(const Launch &ln, const Workspace &ws, int dtype
                                 const void *drf, const int32_t *tokens, const float *unif,
                                 int32_t *acc, int32_t *out, float *probs);
 
+struct CacheEntry;
+
 // The pages of a key-value cache: the caller's state and the handle's scratch (device arrays).
 struct CacheView {
     int num_pages, page_tokens, num_seqs, max_blocks, num_pools;
@@ -249,13 +251,23 @@ struct CacheView {
     int *lengths;        // [num_seqs] tokens
     // scratch
     int *owner;          // [max(num_seqs, num_pages)] first list entry naming an id; INT_MAX between calls
-    int *free_ids;       // [num_pages] the free pages a call takes, ascending
-    int *off;            // [num_seqs] an entry's first place in free_ids, -1 refused
-    int *len;            // [num_seqs] an entry's length at the start of the call
-    int *src, *dst;      // [max(num_seqs, num_pages)] pages to copy, -1 none
-    int *map;            // [num_pages] a compaction's new page ids
+    int *free_ids;       // [num_pages] each stretch's free pages, ascending, from the stretch's start
+    int *free_count;     // [stretches] how many
+    CacheEntry *entries; // [num_seqs] what a plan leaves for its apply
+    int *src, *dst;      // [num_pages] pages to copy, -1 none
+    int *map;            // [num_pages] a compaction's new page ids, or the pages a plan takes
     int *count;          // number of src / dst entries of a compaction
 };
+
+// What an apply does for a list entry.
+struct CacheEntry {
+    int seq, from;       // the sequence (-1: nothing), and a fork's parent
+    int had, want;       // pages held and to be held
+    int len;             // a fork's tokens
+    int first;           // its place among the free pages taken
+    int src, dst;        // page to copy, -1 none
+};
+constexpr int CACHE_STRETCH = 4096;   // pages that one workgroup of a plan looks through
 
 constexpr int CACHE_NO_OWNER = 0x7fffffff;
 
