@@ -1698,40 +1698,33 @@ __device__ __forceinline__ double find_bin(FloatLds &f, double base, bool down, 
             return down ? HBINS - 1 - o : o;
         return o < HMAG ? HMAG - 1 - o : o;
     };
-    double sum = 0.0, total, run = 0.0, goal = 0.0;
+    double v[PER + 2], sum = 0.0, total;
     if (t == 0)
         f.place = -1;
-    // the threads sum their bins; then the one that holds the goal goes over its own again
-#pragma nounroll
-    for (int pass = 0; pass < 2; ++pass) {
-#pragma nounroll
-        for (int i = 0; i <= PER + 1; ++i) {
-            const int b = bin_of(i);
-            const double n = b >= 0 ? val(b) : 0.0;
-            if (pass == 1 && n > 0.0 && run < goal) {
-                f.bin = b;
+    unroll<0, PER + 2>([&](auto i) SV_INLINE {
+        const int b = bin_of(i);
+        v[i] = b >= 0 ? val(b) : 0.0;
+        sum += v[i];
+    });
+    const double inc = block_scan(sum, f.dwave, &total), goal = goal_of(total);
+    double run = __shfl_up(inc, 1);            // what stands before the thread
+    if ((t & 63) == 0) {
+        run = 0.0;
+        for (int i = 0; i < t >> 6; ++i)
+            run += f.dwave[i];
+    }
+    run += base;
+    if (sum > 0.0 && run < goal)
+        atomicMax(&f.place, t);
+    __syncthreads();
+    if (f.place == t)
+        unroll<0, PER + 2>([&](auto i) SV_INLINE {
+            if (v[i] > 0.0 && run < goal) {
+                f.bin = bin_of(i);
                 f.prefix = run;
             }
-            run += n;
-        }
-        if (pass == 1)
-            break;
-        sum = run;
-        const double inc = block_scan(sum, f.dwave, &total);
-        goal = goal_of(total);
-        run = __shfl_up(inc, 1);               // what stands before the thread
-        if ((t & 63) == 0) {
-            run = 0.0;
-            for (int i = 0; i < t >> 6; ++i)
-                run += f.dwave[i];
-        }
-        run += base;
-        if (sum > 0.0 && run < goal)
-            atomicMax(&f.place, t);
-        __syncthreads();
-        if (f.place != t)
-            break;
-    }
+            run += v[i];
+        });
     __syncthreads();
     return total;
 }
@@ -1976,10 +1969,18 @@ __device__ __forceinline__ RowCut cut_floats(const Units<0> &all, Units<0> &few,
             const double w = fma(weight(x, top, r.c), unit, 0x1p52);
             return (unsigned long long)__double_as_longlong(w) & 0xfffffffffffffull;
         };
-        auto weight_of = [&](int b, float top) SV_INLINE {
-            const unsigned long long n = f.weight[b];
-            return n ? (double)n / unit * weight(top, r.max, r.c) : 0.0;
+        // the sums in units to weights in place, each where its bin's neighbours are other threads'
+        auto weigh = [&](int bins, auto top) SV_INLINE {
+#pragma nounroll
+            for (int b = t; b < bins; b += FWG) {
+                const unsigned long long n = f.weight[b];
+                if (n)
+                    f.weight[b] = (unsigned long long)__double_as_longlong(
+                        (double)n * (1.0 / unit) * weight(top(b), r.max, r.c));
+            }
+            __syncthreads();
         };
+        auto weight_of = [&](int b) SV_INLINE { return __longlong_as_double((long long)f.weight[b]); };
         each_float(few, [&](uint32_t bits, int id) SV_INLINE {
             const float x = __uint_as_float(bits);
             if (x != -INFINITY && kept(order_key(x), id, r)) {
@@ -1990,9 +1991,10 @@ __device__ __forceinline__ RowCut cut_floats(const Units<0> &all, Units<0> &few,
             }
         });
         __syncthreads();
+        weigh(FBINS, edge);
         double goal = 0.0;
         find_bin<false>(
-            f, 0.0, false, [&](int b) SV_INLINE { return weight_of(b, edge(b)); },
+            f, 0.0, false, weight_of,
             [&](double z) SV_INLINE {
                 goal = q.p * z;
                 return fmax(goal, 0x1p-1074);  // the first bin at least
@@ -2004,7 +2006,8 @@ __device__ __forceinline__ RowCut cut_floats(const Units<0> &all, Units<0> &few,
         if (bin < HBINS && f.hist[bin] > GATHER) {
             __syncthreads();
             count_parts(few, lo, hi, r, f, [&](float x) SV_INLINE { return units_of(x, top); });
-            find_bin<true>(f, base, bin < HMAG, [&](int b) SV_INLINE { return weight_of(b, top); },
+            weigh(HBINS, [&](int) SV_INLINE { return top; });
+            find_bin<true>(f, base, bin < HMAG, weight_of,
                            [&](double) SV_INLINE { return fmax(goal, 0x1p-1074); });
             base = f.prefix;
             part_range(bin, f.bin, lo, hi);
