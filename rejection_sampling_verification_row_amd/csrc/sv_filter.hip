@@ -78,9 +78,46 @@ __device__ __forceinline__ double exp2_neg(double a)
     return ldexp(p, (int)n);
 }
 
+// 2^a for -1/4 <= a <= 0: Taylor to a^10, whose rest is below (ln 2 / 4)^11 / 11! = 2^-53.
+__device__ __forceinline__ double exp2_small(double a)
+{
+    double p = 7.0549116208011233299e-09;
+    p = fma(p, a, 1.0178086009239699728e-07);
+    p = fma(p, a, 1.3215486790144309488e-06);
+    p = fma(p, a, 1.5252733804059840280e-05);
+    p = fma(p, a, 1.5403530393381609954e-04);
+    p = fma(p, a, 1.3333558146428443423e-03);
+    p = fma(p, a, 9.6181291076284771620e-03);
+    p = fma(p, a, 5.5504108664821579953e-02);
+    p = fma(p, a, 2.4022650695910071233e-01);
+    p = fma(p, a, 6.9314718055994530942e-01);
+    return fma(p, a, 1.0);
+}
+
 __device__ __forceinline__ double weight(float x, float m, double c)
 {
     return exp2_neg(((double)x - (double)m) * c);
+}
+
+// Four at once: each constant is fetched once for all of them.
+__device__ __forceinline__ void exp2_neg4(const double (&a)[4], double (&w)[4])
+{
+    constexpr double C[14] = {1.3691488853904128881e-12, 2.5678435993488205142e-11, 4.4455382718708114976e-10,
+                              7.0549116208011233299e-09, 1.0178086009239699728e-07, 1.3215486790144309488e-06,
+                              1.5252733804059840280e-05, 1.5403530393381609954e-04, 1.3333558146428443423e-03,
+                              9.6181291076284771620e-03, 5.5504108664821579953e-02, 2.4022650695910071233e-01,
+                              6.9314718055994530942e-01, 1.0};
+    double n[4], r[4];
+    unroll<0, 4>([&](auto k) SV_INLINE {
+        const double b = fmax(a[k], -1100.0);
+        n[k] = rint(b);
+        r[k] = b - n[k];
+        w[k] = C[0];
+    });
+    unroll<1, 14>([&](auto i) SV_INLINE {
+        unroll<0, 4>([&](auto k) SV_INLINE { w[k] = fma(w[k], r[k], C[i]); });
+    });
+    unroll<0, 4>([&](auto k) SV_INLINE { w[k] = ldexp(w[k], (int)n[k]); });
 }
 
 struct Params {
@@ -1347,13 +1384,32 @@ template <int DT> struct DirectLaw {
         return kept(order_key(y), id, r) && y != -INFINITY ? weight(y, r.max, r.c) * scale : 0.0;
     }
     __device__ __forceinline__ uint4 aux(int) const { return make_uint4(0, 0, 0, 0); }
+    // float32: the weights of a group.  Its ids are all up to the last tie kept or all past it, so
+    // one comparison tells, but for the group in which the kept ties end.
+    __device__ __forceinline__ void four(int g, const uint4 &v, double (&w)[4]) const
+    {
+        const int id = g * 4;
+        const float least = key_value(id <= r.tie ? r.cut : r.cut + 1);
+        double a[4];
+        unroll<0, 4>([&](auto k) SV_INLINE {
+            const float x = __uint_as_float(vec_word(v, k));
+            a[k] = ((double)(x >= least ? x : -INFINITY) - (double)r.max) * r.c;
+        });
+        if (__ballot(id <= r.tie && id + 3 > r.tie) != 0)
+            unroll<0, 4>([&](auto k) SV_INLINE {
+                if (!kept(order_key(__uint_as_float(vec_word(v, k))), id + k, r))
+                    a[k] = -INFINITY;
+            });
+        exp2_neg4(a, w);
+        unroll<0, 4>([&](auto k) SV_INLINE { w[k] *= scale; });
+    }
     __device__ __forceinline__ double sum(int g, const uint4 &v, const uint4 &) const
     {
         double s = 0.0;
         if constexpr (DT == 0) {
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-                s += one(__uint_as_float(vec_word(v, k)), g * 4 + k);
+            double x[4];
+            four(g, v, x);
+            unroll<0, 4>([&](auto k) SV_INLINE { s += x[k]; });
         } else {
             uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma nounroll
@@ -1729,8 +1785,9 @@ __device__ __forceinline__ double find_bin(FloatLds &f, double base, bool down, 
     return total;
 }
 
-// Runs f(bits, id) over the logits of the wave's units.
-template <typename F> __device__ __forceinline__ void each_float(const Units<0> &un, F f)
+// Runs f(four logits' bits, the first's id) over the wave's units, -inf where there are none; all
+// lanes together.
+template <typename F> __device__ __forceinline__ void each_vec(const Units<0> &un, F f)
 {
     const int units = un.count();
 #pragma nounroll
@@ -1739,16 +1796,32 @@ template <typename F> __device__ __forceinline__ void each_float(const Units<0> 
         load_batch(un, i0, v);
 #pragma nounroll
         for (int j = 0; j < BATCH && i0 + j < units; ++j) {
-            const uint4 x = choose(v, j);
-            const int id = un.group(i0 + j) * 4;
+            uint4 x = choose(v, j);
             if (!un.holds(i0 + j))
-                continue;
-            f(x.x, id);
-            f(x.y, id + 1);
-            f(x.z, id + 2);
-            f(x.w, id + 3);
+                x = make_uint4(un.gr.EMPTY, un.gr.EMPTY, un.gr.EMPTY, un.gr.EMPTY);
+            f(x, un.group(i0 + j) * 4);
         }
     }
+}
+
+// Runs f(bits, id) over the logits from lo to hi that r keeps.
+template <typename F>
+__device__ __forceinline__ void each_between(const Units<0> &un, float lo, float hi, const RowCut &r, F f)
+{
+    each_vec(un, [&](const uint4 &v, int id) SV_INLINE {
+        auto in = [&](uint32_t w) SV_INLINE { return __uint_as_float(w) >= lo && __uint_as_float(w) <= hi; };
+        if (__ballot(in(v.x) || in(v.y) || in(v.z) || in(v.w)) == 0)
+            return;
+        uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma nounroll
+        for (int k = 0; k < 4; ++k) {
+            if (in(w[0]) && kept(order_key(__uint_as_float(w[0])), id + k, r))
+                f(w[0], id + k);
+            w[0] = w[1];
+            w[1] = w[2];
+            w[2] = w[3];
+        }
+    });
 }
 
 // The logits from lo to hi that r keeps, gathered and put in order: f.order[0 .. f.n).  False if
@@ -1758,13 +1831,10 @@ __device__ __forceinline__ bool gather(const Units<0> &un, float lo, float hi, c
     if (threadIdx.x == 0)
         f.n = 0;
     __syncthreads();
-    each_float(un, [&](uint32_t bits, int id) SV_INLINE {
-        const float x = __uint_as_float(bits);
-        if (x >= lo && x <= hi && kept(order_key(x), id, r)) {
-            const uint32_t at = atomicAdd(&f.n, 1u);
-            if (at < GATHER)
-                f.list[at] = (unsigned long long)order_key(x) << 32 | (uint32_t)~id;
-        }
+    each_between(un, lo, hi, r, [&](uint32_t bits, int id) SV_INLINE {
+        const uint32_t at = atomicAdd(&f.n, 1u);
+        if (at < GATHER)
+            f.list[at] = (unsigned long long)order_key(__uint_as_float(bits)) << 32 | (uint32_t)~id;
     });
     __syncthreads();
     const int n = (int)f.n;
@@ -1791,10 +1861,8 @@ __device__ __forceinline__ void count_parts(const Units<0> &un, float lo, float 
     for (int i = threadIdx.x; i < HBINS; i += FWG)
         f.weight[i] = 0;
     __syncthreads();
-    each_float(un, [&](uint32_t bits, int id) SV_INLINE {
-        const float x = __uint_as_float(bits);
-        if (x >= lo && x <= hi && kept(order_key(x), id, r))
-            atomicAdd(&f.weight[(bits & 0xffffu) >> 3], of(x));
+    each_between(un, lo, hi, r, [&](uint32_t bits, int) SV_INLINE {
+        atomicAdd(&f.weight[(bits & 0xffffu) >> 3], of(__uint_as_float(bits)));
     });
     __syncthreads();
 }
@@ -1959,16 +2027,21 @@ __device__ __forceinline__ RowCut cut_floats(const Units<0> &all, Units<0> &few,
     }
     if (q.p < 1.0) {
         const double unit = ldexp(1.0, min(47, 62 - (32 - __clz(V))));
-        for (int i = t; i < FBINS; i += FWG)
-            f.weight[i] = f.hist[i] = 0;
+        const bool cut = r.cut != KEY_NEG_INF;     // then the counts are those of the kept, once more
+        for (int i = t; i < FBINS; i += FWG) {
+            f.weight[i] = 0;
+            if (cut)
+                f.hist[i] = 0;
+        }
         __syncthreads();
         // no edge lies above the maximum, so that its own weight is 1
         auto edge = [&](int b) SV_INLINE { return fminf(bin_high(b), r.max); };
-        // w * unit to the nearest integer, in the low bits of the sum with 2^52
-        auto units_of = [&](float x, float top) SV_INLINE {
-            const double w = fma(weight(x, top, r.c), unit, 0x1p52);
-            return (unsigned long long)__double_as_longlong(w) & 0xfffffffffffffull;
+        // a weight, w * unit to the nearest integer, in the low bits of the sum with 2^52
+        auto to_units = [&](double w) SV_INLINE {
+            return (unsigned long long)__double_as_longlong(fma(w, unit, 0x1p52)) & 0xfffffffffffffull;
         };
+        const float small = (float)(-0.249 / r.c);      // in logits, what exp2_small takes
+        auto units_of = [&](float x, float top) SV_INLINE { return to_units(weight(x, top, r.c)); };
         // the sums in units to weights in place, each where its bin's neighbours are other threads'
         auto weigh = [&](int bins, auto top) SV_INLINE {
 #pragma nounroll
@@ -1981,13 +2054,46 @@ __device__ __forceinline__ RowCut cut_floats(const Units<0> &all, Units<0> &few,
             __syncthreads();
         };
         auto weight_of = [&](int b) SV_INLINE { return __longlong_as_double((long long)f.weight[b]); };
-        each_float(few, [&](uint32_t bits, int id) SV_INLINE {
-            const float x = __uint_as_float(bits);
-            if (x != -INFINITY && kept(order_key(x), id, r)) {
-                const int b = float_bin(bits);
-                atomicAdd(&f.weight[b], units_of(x, edge(b)));
-                if (b < HBINS)
-                    atomicAdd(&f.hist[b], 1u);
+        each_vec(few, [&](const uint4 &v, int id) SV_INLINE {
+            uint32_t w[4] = {v.x, v.y, v.z, v.w};
+            const uint32_t t0 = window_words(upper_halves(v).x), t1 = window_words(upper_halves(v).y);
+            if (__ballot(((t0 | t1) & 0x70007000u) != 0) == 0) {
+                // all in the window: an edge is the logit's own upper half, and their difference
+                // is exact, since they share an exponent
+                float d[4];
+                double a[4], p[4];
+                unroll<0, 4>([&](auto k) SV_INLINE {
+                    const uint32_t e = (w[k] & 0xffff0000u) | (~(uint32_t)((int32_t)w[k] >> 31) & 0xffffu);
+                    d[k] = __uint_as_float(w[k]) - fminf(__uint_as_float(e), r.max);
+                    a[k] = (double)d[k] * r.c;
+                });
+                if (__ballot(fminf(fminf(d[0], d[1]), fminf(d[2], d[3])) < small) == 0)
+                    unroll<0, 4>([&](auto k) SV_INLINE { p[k] = exp2_small(a[k]); });
+                else
+                    exp2_neg4(a, p);
+                const uint32_t b0 = bin_offsets(t0), b1 = bin_offsets(t1);
+                const uint32_t at[4] = {b0 & 0xffffu, b0 >> 16, b1 & 0xffffu, b1 >> 16};
+                unroll<0, 4>([&](auto k) SV_INLINE {
+                    if (cut && !kept(order_key(__uint_as_float(w[k])), id + k, r))
+                        return;
+                    atomicAdd(&f.weight[at[k] / 4], to_units(p[k]));
+                    if (cut)
+                        atomicAdd(&f.hist[at[k] / 4], 1u);
+                });
+            } else {
+#pragma nounroll
+                for (int k = 0; k < 4; ++k) {
+                    const float x = __uint_as_float(w[0]);
+                    if (x != -INFINITY && kept(order_key(x), id + k, r)) {
+                        const int b = float_bin(w[0]);
+                        atomicAdd(&f.weight[b], units_of(x, edge(b)));
+                        if (cut)
+                            atomicAdd(&f.hist[b], 1u);
+                    }
+                    w[0] = w[1];
+                    w[1] = w[2];
+                    w[2] = w[3];
+                }
             }
         });
         __syncthreads();
