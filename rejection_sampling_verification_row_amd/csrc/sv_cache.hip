@@ -165,17 +165,17 @@ __device__ void grant(const CacheView &c, int n, int *status, int *lds, Ask ask)
         __syncthreads();
     }
     const int found = scan_free(c, stretches, before, lds);
-    int sum = 0;
+    // unsigned: sum stays at found + 1, 2^30 at most, and a tile asks for at most 1024 (2^20 + 1)
+    uint32_t sum = 0;
     for (int i0 = 0; i0 < n; i0 += CWG) {
         const int i = i0 + threadIdx.x;
         CacheEntry e = {-1, -1, 0, 0, 0, 0, -1, -1};
         const int a = i < n ? ask(i, e) : 0;
         int all;
-        // no overflow: an entry asks for at most max_blocks + 1 pages, which is at most 2^20 + 1
         const int inc = block_incl_scan(max(a, 0), lds, &all);
         if (i < n) {
-            const bool ok = a >= 0 && sum + inc <= found;
-            e.first = sum + inc - a;
+            const bool ok = a >= 0 && sum + (uint32_t)inc <= (uint32_t)found;
+            e.first = (int)(sum + (uint32_t)(inc - a));
             if (!ok)
                 e.seq = -1;
             else if (e.src >= 0)
@@ -184,9 +184,9 @@ __device__ void grant(const CacheView &c, int n, int *status, int *lds, Ask ask)
             if (status)
                 status[i] = ok ? 0 : -1;
         }
-        sum = min(sum + all, c.num_pages + 1);
+        sum = min(sum + (uint32_t)all, (uint32_t)found + 1);
     }
-    for (int i = threadIdx.x; i < min(sum, found); i += CWG)
+    for (int i = threadIdx.x; i < (int)min(sum, (uint32_t)found); i += CWG)
         c.map[i] = free_page(c, stretches, before, i);
 }
 

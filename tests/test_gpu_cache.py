@@ -335,3 +335,55 @@ def test_a_served_round_of_the_operators_together():
     c.check()
     c.compact()
     sv.specverify_destroy(ctx)
+
+
+def test_a_pool_of_millions_of_pages():
+    """More stretches of the pool than a plan keeps in LDS, with few pages free among them."""
+    pages, seqs, blocks = 4096 * 1100 + 77, 40, 300
+    r = np.random.RandomState(8)
+    refs = np.ones(pages, np.int32)
+    free = np.sort(r.permutation(pages)[:9000]).astype(np.int32)
+    refs[free] = 0
+    dr = dev(refs)
+    tables = torch.full((seqs, blocks), -1, dtype=torch.int32, device="cuda")
+    zero = lambda: torch.zeros(seqs, dtype=torch.int32, device="cuda")
+    bl, ln, st = zero(), zero(), zero()
+    h = sv.specverify_cache_create(0, pages, 1, seqs, blocks, 0, [], dr, tables, bl, ln)
+    counts = r.randint(0, 300, seqs).astype(np.int32)
+    sv.specverify_cache_reserve(h, None, seqs, None, dev(counts), st)
+    torch.cuda.synchronize()
+    upto = np.cumsum(counts)
+    assert upto[-1] <= 9000 and st.tolist() == [0] * seqs and bl.tolist() == counts.tolist()
+    t = tables.cpu().numpy()
+    for i in range(seqs):
+        assert np.array_equal(t[i, :counts[i]], free[upto[i] - counts[i]: upto[i]])
+        assert np.all(t[i, counts[i]:] == -1)
+    refs[free[:upto[-1]]] = 1
+    assert np.array_equal(dr.cpu().numpy(), refs)
+    pm = torch.zeros(pages, dtype=torch.int32, device="cuda")
+    used = torch.zeros(1, dtype=torch.int32, device="cuda")
+    sv.specverify_cache_compact(h, None, pm, used)
+    torch.cuda.synchronize()
+    U = int((refs > 0).sum())
+    at = np.flatnonzero(refs > 0)
+    want = np.full(pages, -1, np.int64)
+    want[at] = at
+    want[at[at >= U]] = np.flatnonzero(refs == 0)[:(at >= U).sum()]
+    assert used.item() == U and np.array_equal(pm.cpu().numpy(), want)
+    for i in range(seqs):
+        assert np.array_equal(tables[i, :counts[i]].cpu().numpy(), want[t[i, :counts[i]]])
+    sv.specverify_cache_destroy(h)
+
+
+@pytest.mark.parametrize("pools,page_bytes", [(70, 32), (3, 33 * 16384 + 16), (1, 16 << 20)])
+def test_pages_and_pools_of_many_sizes_are_copied_whole(pools, page_bytes):
+    c = Cache(12, 4, 8, 3, pools, page_bytes)
+    c.call("reserve", [0, 1], [6, 7])
+    c.call("commit", [0, 1], [5, 6])
+    c.call("fork", [0, 1, 0], [2, 3, 4])
+    c.free([0, 3])
+    c.compact()
+    status = torch.zeros(2, dtype=torch.int32, device="cuda")
+    sv.specverify_cache_copy(c.h, None, 2, dev(np.array([0, 1], np.int32)), dev(np.array([11, 10], np.int32)), status)
+    c.m.moves = [(0, 11), (1, 10)]
+    c.check()
