@@ -216,6 +216,8 @@ def _stream(s):
         return s
     if s is None:
         import torch
+        if torch.cuda.is_initialized():      # the same handle without a Stream object around it
+            return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
         return torch.cuda.current_stream().cuda_stream
     return s.cuda_stream
 
@@ -375,6 +377,9 @@ def specverify_run_sampling_filtered(ctx, stream, dtype, B, K, V, target_filter,
            "specverify_run_sampling_filtered")
 
 
+_cache_pages = {}       # handle -> num_pages, which page maps are checked against
+
+
 def specverify_cache_create(device, num_pages, page_tokens, num_seqs, max_blocks, page_bytes, pools,
                             refs, tables, blocks, lengths) -> int:
     """Returns the handle (an int).  pools: a sequence of device tensors (or addresses) of
@@ -391,6 +396,7 @@ def specverify_cache_create(device, num_pages, page_tokens, num_seqs, max_blocks
     _check(load().specverify_cache_create(ctypes.byref(h), device, num_pages, page_tokens, num_seqs,
                                           max_blocks, len(pools), page_bytes, arr, *state),
            "specverify_cache_create")
+    _cache_pages[h.value] = num_pages
     return h.value
 
 
@@ -399,6 +405,7 @@ def specverify_cache_workspace_bytes(cache: int) -> int:
 
 
 def specverify_cache_destroy(cache) -> None:
+    _cache_pages.pop(cache, None)
     _check(load().specverify_cache_destroy(cache), "specverify_cache_destroy")
 
 
@@ -427,9 +434,9 @@ def specverify_cache_free(cache, stream, n, seqs=None, keep=None) -> None:
 
 
 def specverify_cache_compact(cache, stream, page_map=None, num_used=None) -> None:
-    """The arrays' sizes are the caller's to guarantee: num_pages and 1."""
     _check(load().specverify_cache_compact(cache, _stream(stream),
-                                           *_ptrs((page_map, 0, "i32", "page_map"),
+                                           *_ptrs((page_map, _cache_pages.get(cache, 0), "i32",
+                                                   "page_map"),
                                                   (num_used, 1, "i32", "num_used"))),
            "specverify_cache_compact")
 

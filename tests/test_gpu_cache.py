@@ -222,6 +222,8 @@ def test_argument_errors():
     assert status(sv.specverify_cache_copy, 1, None, i, i) == sv.SPECVERIFY_EINVAL
     assert status(sv.specverify_cache_free, 4, i) == sv.SPECVERIFY_ECAPACITY
     assert status(sv.specverify_cache_compact, i.data_ptr() + 1) == sv.SPECVERIFY_EINVAL
+    with pytest.raises(ValueError):
+        sv.specverify_cache_compact(c.h, None, i[:7])          # a map of 8 pages
     assert sv.specverify_cache_workspace_bytes(c.h) > 0
     c.check()
 
