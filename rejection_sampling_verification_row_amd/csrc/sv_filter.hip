@@ -120,6 +120,13 @@ __device__ __forceinline__ void exp2_neg4(const double (&a)[4], double (&w)[4])
     unroll<0, 4>([&](auto k) SV_INLINE { w[k] = ldexp(w[k], (int)n[k]); });
 }
 
+__device__ __forceinline__ void weight4(const float (&x)[4], float m, double c, double (&w)[4])
+{
+    double a[4];
+    unroll<0, 4>([&](auto k) SV_INLINE { a[k] = ((double)x[k] - (double)m) * c; });
+    exp2_neg4(a, w);
+}
+
 struct Params {
     double c;       // log2(e) / T
     double p, m;
@@ -749,11 +756,12 @@ __device__ __forceinline__ void cut_from_counts(const uint32_t *hist, CutLds &c,
             order_entry<WGT>(r, hist, c, n, x, bin);
             uint32_t b = before[r];
             double w[4];
+            weight4(x, M, q.c, w);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const uint32_t left = b >= k ? 0u : min(n[i], k - b);
                 b += n[i];
-                w[i] = left ? weight(x[i], M, q.c) : 0.0;
+                w[i] = left ? w[i] : 0.0;      // what does not occur may lie above M
                 sum[r] += (double)left * w[i];
                 passes |= (uint32_t)(left && w[i] >= q.m) << r;
             }
