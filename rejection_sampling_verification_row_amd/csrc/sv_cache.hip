@@ -223,8 +223,11 @@ __global__ __launch_bounds__(CWG) void k_reserve_plan(CacheView c, int n, const 
 // the page, pool, entries) and strides along each; pages(i, from, to) gives entry i's pages.  Few
 // entries copy anything, so a wave reads 64 of them at once, one a lane, and walks those that do.
 constexpr int COPY_WG = 256;
-constexpr int COPY_VECS = 4;
-constexpr int COPY_ITEM = COPY_WG * COPY_VECS * 16;
+constexpr int COPY_STEP = COPY_WG * 16;       // bytes that a workgroup loads at once
+constexpr int COPY_ITEM = 4 * COPY_STEP;
+
+__device__ inline uint4 load16(const char *p) { return *reinterpret_cast<const uint4 *>(p); }
+__device__ inline void store16(char *p, const uint4 &v) { *reinterpret_cast<uint4 *>(p) = v; }
 
 __device__ inline void copy_page(const CacheView &c, int from, int to)
 {
@@ -233,15 +236,20 @@ __device__ inline void copy_page(const CacheView &c, int from, int to)
         char *b = c.pools[pool] + (int64_t)to * c.page_bytes;
         for (int64_t o = (int64_t)blockIdx.x * COPY_ITEM + threadIdx.x * 16; o < c.page_bytes;
              o += (int64_t)gridDim.x * COPY_ITEM) {
-            uint4 v[COPY_VECS];
-#pragma unroll
-            for (int k = 0; k < COPY_VECS; ++k)
-                if (o + k * COPY_WG * 16 < c.page_bytes)
-                    v[k] = *reinterpret_cast<const uint4 *>(a + o + k * COPY_WG * 16);
-#pragma unroll
-            for (int k = 0; k < COPY_VECS; ++k)
-                if (o + k * COPY_WG * 16 < c.page_bytes)
-                    *reinterpret_cast<uint4 *>(b + o + k * COPY_WG * 16) = v[k];
+            // four variables: an array of them would live in LDS
+            const bool h1 = o + COPY_STEP < c.page_bytes, h2 = o + 2 * COPY_STEP < c.page_bytes,
+                       h3 = o + 3 * COPY_STEP < c.page_bytes;
+            const uint4 none = make_uint4(0, 0, 0, 0);
+            const uint4 v0 = load16(a + o), v1 = h1 ? load16(a + o + COPY_STEP) : none,
+                        v2 = h2 ? load16(a + o + 2 * COPY_STEP) : none,
+                        v3 = h3 ? load16(a + o + 3 * COPY_STEP) : none;
+            store16(b + o, v0);
+            if (h1)
+                store16(b + o + COPY_STEP, v1);
+            if (h2)
+                store16(b + o + 2 * COPY_STEP, v2);
+            if (h3)
+                store16(b + o + 3 * COPY_STEP, v3);
         }
     }
 }
