@@ -662,8 +662,8 @@ int specverify_cache_create(specverify_cache **out, int device, int num_pages, i
     const size_t b_entries = align_up((size_t)num_seqs * sizeof(sv::CacheEntry));
     const size_t b_stretches = align_up(
         ((size_t)num_pages + sv::CACHE_STRETCH - 1) / sv::CACHE_STRETCH * sizeof(int));
-    const size_t b_one = align_up(sizeof(int));
-    const size_t total = b_pools + b_both + 4 * b_pages + b_entries + b_stretches + b_one;
+    const size_t b_two = align_up(2 * sizeof(int));
+    const size_t total = b_pools + b_both + 4 * b_pages + b_entries + b_stretches + b_two;
     specverify_cache *c = new (std::nothrow) specverify_cache();
     if (!c)
         return SPECVERIFY_ENOMEM;
@@ -697,7 +697,7 @@ int specverify_cache_create(specverify_cache **out, int device, int num_pages, i
     v.map = reinterpret_cast<int *>(take(b_pages));
     v.entries = reinterpret_cast<sv::CacheEntry *>(take(b_entries));
     v.free_count = reinterpret_cast<int *>(take(b_stretches));
-    v.count = reinterpret_cast<int *>(take(b_one));
+    v.count = reinterpret_cast<int *>(take(b_two));
     c->device = device;
     c->num_cus = cus;
     c->bytes = total;

@@ -60,16 +60,23 @@ __device__ inline int block_incl_scan(int v, int *lds, int *total)
     return before + inc;
 }
 
+// Bit k: page p + k is below end and free.
+__device__ int free_bits(const CacheView &c, int p, int end)
+{
+    int bits = 0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+        if (p + k < end && c.refs[p + k] == 0)
+            bits |= 1 << k;
+    return bits;
+}
+
 // The free pages of a stretch, ascending, into its part of free_ids.
 __device__ void list_free(const CacheView &c, int stretch, int *lds)
 {
     const int p = stretch * CACHE_STRETCH + (int)threadIdx.x * 4;
     static_assert(CACHE_STRETCH == CWG * 4, "four pages to a thread");
-    int bits = 0;
-#pragma unroll
-    for (int k = 0; k < 4; ++k)
-        if (p + k < c.num_pages && c.refs[p + k] == 0)
-            bits |= 1 << k;
+    const int bits = free_bits(c, p, c.num_pages);
     int all;
     int at = stretch * CACHE_STRETCH + block_incl_scan(__popc(bits), lds, &all) - __popc(bits);
 #pragma unroll
@@ -433,44 +440,72 @@ __global__ __launch_bounds__(COPY_WG) void k_free(CacheView c, int n, const int 
     }
 }
 
-// Compaction: of U used pages, the i-th used page at or past U moves to the i-th free page below
-// U, so that the used pages become 0 .. U - 1 with the fewest moves.
+// Compaction: of U pages in use, the i-th at or past U moves to the i-th free page (of which h lie
+// below U, as many as there are pages to move), so that the pages in use become 0 .. U - 1 with
+// the fewest moves.  Where a page goes follows from the free pages before it alone, so every
+// stretch is mapped by a workgroup of its own.
+__device__ void map_stretch(const CacheView &c, int stretch, int stretches, const int *before, int base,
+                            int used, int holes, int *page_map, int *lds)
+{
+    const int p = stretch * CACHE_STRETCH + (int)threadIdx.x * 4, bits = free_bits(c, p, c.num_pages);
+    int all;
+    int free_before = base + block_incl_scan(__popc(bits), lds, &all) - __popc(bits);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        if (p + k >= c.num_pages)
+            break;
+        int to = -1;
+        if (bits >> k & 1) {
+            ++free_before;
+        } else if (p + k < used) {
+            to = p + k;
+        } else {
+            const int i = p + k - free_before - (used - holes);
+            to = free_page(c, stretches, before, i);
+            c.src[i] = p + k;
+            c.dst[i] = to;
+        }
+        c.map[p + k] = to;
+        if (page_map)
+            page_map[p + k] = to;
+    }
+}
+
+// Counts, and for a pool of one stretch the map as well.
 __global__ __launch_bounds__(CWG) void k_compact_plan(CacheView c, int *page_map, int *num_used)
 {
     __shared__ int lds[CWAVES];
-    int mine = 0, used = 0;
-    for (int p = threadIdx.x; p < c.num_pages; p += CWG)
-        mine += c.refs[p] > 0;
-    block_incl_scan(mine, lds, &used);
-    int holes = 0, movers = 0;
-    for (int p0 = 0; p0 < c.num_pages; p0 += CWG) {
-        const int p = p0 + threadIdx.x;
-        const bool there = p < c.num_pages, full = there && c.refs[p] > 0;
-        const bool hole = there && !full && p < used, mover = full && p >= used;
-        int h, m;
-        const int ih = holes + block_incl_scan(hole, lds, &h);
-        const int im = movers + block_incl_scan(mover, lds, &m);
-        if (hole)
-            c.dst[ih - 1] = p;
-        if (mover)
-            c.src[im - 1] = p;
-        if (there)
-            c.map[p] = full ? p : -1;
-        holes += h;
-        movers += m;
+    __shared__ int before[LDS_STRETCHES];
+    const int stretches = (c.num_pages + CACHE_STRETCH - 1) / CACHE_STRETCH;
+    if (stretches == 1) {
+        list_free(c, 0, lds);
+        __syncthreads();
     }
-    __syncthreads();
-    for (int i = threadIdx.x; i < movers; i += CWG)
-        c.map[c.src[i]] = c.dst[i];
-    __syncthreads();
-    if (page_map)
-        for (int p = threadIdx.x; p < c.num_pages; p += CWG)
-            page_map[p] = c.map[p];
+    const int used = c.num_pages - scan_free(c, stretches, before, lds);
+    const int at = min(used / CACHE_STRETCH, stretches - 1);
+    const int base = at < LDS_STRETCHES ? before[at] : c.free_count[at];
+    int holes;
+    block_incl_scan(__popc(free_bits(c, at * CACHE_STRETCH + (int)threadIdx.x * 4, used)), lds, &holes);
+    holes += base;
     if (threadIdx.x == 0) {
-        *c.count = movers;
+        c.count[0] = holes;
+        c.count[1] = used;
         if (num_used)
             *num_used = used;
     }
+    if (stretches == 1)
+        map_stretch(c, 0, 1, before, 0, used, holes, page_map, lds);
+}
+
+__global__ __launch_bounds__(CWG) void k_compact_map(CacheView c, int *page_map)
+{
+    __shared__ int lds[CWAVES];
+    __shared__ int before[LDS_STRETCHES];
+    const int stretches = gridDim.x;
+    for (int s = threadIdx.x; s < min(stretches, LDS_STRETCHES); s += CWG)
+        before[s] = c.free_count[s];
+    map_stretch(c, blockIdx.x, stretches, before, c.free_count[blockIdx.x], c.count[1], c.count[0], page_map,
+                lds);
 }
 
 __global__ __launch_bounds__(COPY_WG) void k_compact_apply(CacheView c)
@@ -607,10 +642,20 @@ hipError_t launch_cache_free(hipStream_t st, const CacheView &c, int n, const in
 hipError_t launch_cache_compact(hipStream_t st, const CacheView &c, int cus, int *page_map,
                                 int *num_used)
 {
-    k_compact_plan<<<1, CWG, 0, st>>>(c, page_map, num_used);
-    hipError_t e = hipGetLastError();
+    const int stretches = (c.num_pages + CACHE_STRETCH - 1) / CACHE_STRETCH;
+    hipError_t e = list_stretches(st, c);
     if (e != hipSuccess)
         return e;
+    k_compact_plan<<<1, CWG, 0, st>>>(c, page_map, num_used);
+    e = hipGetLastError();
+    if (e != hipSuccess)
+        return e;
+    if (stretches > 1) {
+        k_compact_map<<<stretches, CWG, 0, st>>>(c, page_map);
+        e = hipGetLastError();
+        if (e != hipSuccess)
+            return e;
+    }
     k_compact_apply<<<apply_grid(c, cus, c.num_pages), COPY_WG, 0, st>>>(c);
     return hipGetLastError();
 }

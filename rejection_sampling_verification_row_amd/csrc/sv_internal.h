@@ -256,7 +256,7 @@ struct CacheView {
     CacheEntry *entries; // [num_seqs] what a plan leaves for its apply
     int *src, *dst;      // [num_pages] pages to copy, -1 none
     int *map;            // [num_pages] a compaction's new page ids, or the pages a plan takes
-    int *count;          // number of src / dst entries of a compaction
+    int *count;          // a compaction's moved pages, and its pages in use
 };
 
 // What an apply does for a list entry.
