@@ -9,12 +9,21 @@
 // value plus the lowest ids among those equal to it.  A row is therefore described by (cut value,
 // last id kept at that value, Z), RowCut, and no row is ever sorted.
 //
-//   k_filter_sample   one 1024-thread workgroup per row: its RowCut, then the inverse-CDF draw
-//   k_filter_rows     the RowCut of every target and draft row of a verify
-//   k_filter_verify   one workgroup per sequence: accept tests, first rejection, residual draw
+//   k_filter_sample_bf16, _f32   one 1024-thread workgroup per row: its RowCut, then the
+//                                inverse-CDF draw; a decode step has a row per sequence, so this
+//                                fills the chip with one launch
+//   k_filter_rows_bf16, _f32     the RowCut of every target and draft row of a verify
+//   k_filter_verify              one workgroup per sequence: accept tests, first rejection and
+//                                the draw from p or from max(0, p - q)
 //
-// The cut has to be the exact one, because ids are compared for equality with the definition: all
-// weights and sums are fp64.
+// Ids are compared for equality with the definition, so weights and sums are fp64: an error of
+// 2^-24 per weight would move a draw between neighbouring ids once in about 10^2 rows of 128256.
+// The one place with less, float32 top-p's integer sums, says there what it loses.
+//
+// A row has to be read once; everything else here serves to keep the second look at it small.
+// Counting patterns turns the cuts into arithmetic on 8192 bins instead of passes over the row
+// (a bisection over values, the first kernels here, took 32 passes: 2929 us for 256 rows of
+// 128256 where counting takes 43).
 #include <float.h>
 
 #include <type_traits>
@@ -1568,7 +1577,12 @@ __device__ __forceinline__ void fill_table(const RowCut &r, double scale, double
     }
 }
 
-// One row: its cut by counting, then the draw.
+// One row: its cut by counting, then the draw.  256 rows of 128256 with mixed parameters take 43 us,
+// the time of a row that keeps everything: 10 us to read and count it (the rate of HBM), 5 for the
+// cut (barriers and scans, one after the other), 12 for a second reading through the table (an
+// 8-byte LDS lookup per logit, 12 clocks for a wave's, is what bounds it) and 4 to find the id.
+// Rows cut by top-k or min-p list the groups that can matter while they count, and need 26 us.
+// One row of 32000: 14 us, all of it latency.
 __global__ __launch_bounds__(FWG, 4) void k_filter_sample_bf16(const char *logits, int V,
                                                                int64_t stride, FilterPtrs f,
                                                                const float *unif, int *tok,
@@ -1662,6 +1676,12 @@ __global__ __launch_bounds__(FWG, 4) void k_filter_sample_bf16(const char *logit
 
 constexpr int BIN_HIGH = HBINS, BIN_ZERO = HBINS + 1, BIN_LOW = HBINS + 2, FBINS = HBINS + 3;
 constexpr int GATHER = 1024;
+// Where top-k keeps little, all of it is put in order at once instead of its last bin alone: that
+// spares the sum over the row that gives Z, and with top-p the weights' pass, but an order of n
+// costs n comparisons of each.  The cuts of 576 rows of 32000 in us, at once and by the bin: k = 20
+// 46.7 and 47.8, 50 49.9 and 48.9, 250 63 and 51; with top-p k = 50 50 and 74, 400 77 and 85, 800
+// 118 and 101.
+constexpr int AT_ONCE = 32, AT_ONCE_P = 512;
 
 struct FloatLds {
     __align__(16) uint32_t hist[FBINS + 1];
@@ -2009,7 +2029,7 @@ __device__ __forceinline__ RowCut cut_floats(const Units<0> &all, Units<0> &few,
             const int bin = f.bin;
             uint32_t before = (uint32_t)f.prefix;
             float lo = bin_low(bin), hi = bin_high(bin);
-            if (before + f.hist[bin] <= GATHER) {
+            if (before + f.hist[bin] <= (q.p < 1.0 ? AT_ONCE_P : AT_ONCE)) {
                 // all that top-k can keep is in hand: the three cuts at once
                 gather(few, lo, FLT_MAX, r, f);
                 cut_in_order(r, 0.0, q.k, q.p, INFINITY, q.m, f);
@@ -2030,6 +2050,7 @@ __device__ __forceinline__ RowCut cut_floats(const Units<0> &all, Units<0> &few,
             const unsigned long long last = f.order[q.k - before - 1];
             r.cut = (uint32_t)(last >> 32);
             r.tie = (int)~(uint32_t)last;
+            r.kept = q.k;          // at most: what a draw decides by
             __syncthreads();
         }
     }
@@ -2130,8 +2151,9 @@ __device__ __forceinline__ RowCut cut_floats(const Units<0> &all, Units<0> &few,
             r.state = CUT_EXACT;
             return r;
         }
+        const int kept_at_most = r.kept;
         cut_in_order(r, base, GATHER, 1.0, goal, 0.0, f);
-        r.kept = V;
+        r.kept = kept_at_most;
     }
     if (q.m > 0.0 && weight(key_value(r.cut), r.max, r.c) < q.m) {
         r.cut = key_of_weight(r.max, r.c, q.m);
@@ -2163,6 +2185,9 @@ __device__ __forceinline__ double row_total(const Units<DT> &un, const MayKeep<D
     return block_sum(s, red.d);
 }
 
+// One row.  64 rows of 32000 with top-p alone, which skips nothing, take 48 us: counting 5, the
+// weights' pass 12 (fp64 issue), the goal's bin 3, gathering and ordering its logits 7, the draw 5,
+// and the waves' waits for each other.  With top-k 21 us.
 __global__ __launch_bounds__(FWG, 4) void k_filter_sample_f32(const char *logits, int V,
                                                               int64_t stride, FilterPtrs f,
                                                               const float *unif, int *tok,
@@ -2196,7 +2221,9 @@ __global__ __launch_bounds__(FWG, 4) void k_filter_sample_f32(const char *logits
 }
 
 // The RowCut of every target and draft row of a float32 verify: the B (K+1) target rows, then the
-// B K draft rows.
+// B K draft rows.  The counts, weights and lists take 131 KB of LDS, so a compute unit holds one
+// workgroup and a row's phases wait for each other: 704 rows of 32000 with top-k take 52 us, three
+// rounds of 17, where the bytes need 13.
 __global__ __launch_bounds__(FWG, 4) void k_filter_rows_f32(const char *tgt, const char *drf, int B,
                                                             int K, int V, FilterPtrs ft,
                                                             FilterPtrs fd, RowCut *cuts)
@@ -2222,7 +2249,12 @@ __global__ __launch_bounds__(FWG, 4) void k_filter_rows_f32(const char *tgt, con
 }
 
 constexpr int MAX_POS = 63;
-constexpr uint32_t SPARSE = 2048;         // an eighth of the groups that the waves' lists hold
+// A target row that keeps no more ids than this is drawn from by lists of its groups: 11/16 of the
+// places that the waves' lists have, so that ids spread evenly do not overflow one.  256 sequences
+// of 128256 in bfloat16, with lists and without: k = 50 42 and 50 us, 1000 47 and 64, 3000 58 and
+// 63; 4000, where lists overflow, 79 and 66.  64 of 32000 in float32: k = 50 15 and 19, 3000 27 and
+// 42.
+constexpr uint32_t SPARSE = 2816;
 
 struct VerifyLds {
     RowCut cut[2 * MAX_POS + 1];          // target rows 0..K, then draft rows 0..K-1
@@ -2231,7 +2263,11 @@ struct VerifyLds {
     int L;
 };
 
-// Accept tests, first rejection and the replacement or bonus draw of one sequence.
+// Accept tests, first rejection and the replacement or bonus draw of one sequence.  256 sequences of
+// 128256 in bfloat16 take 62 us: 5 for the tests, 2 for the tables, then 16 (two lookups per id,
+// as in the sampler) where p keeps much, or 13 to list p's few groups and 3 to draw from them, and
+// 3 to 6 to find the id.  A chip has as many workgroups in flight as sequences, so a batch waits
+// for its slowest.
 template <int DT>
 __global__ __launch_bounds__(FWG, 4) void k_filter_verify(const char *tgt, const char *drf, int B,
                                                           int K, int V, FilterPtrs ft, FilterPtrs fd,
