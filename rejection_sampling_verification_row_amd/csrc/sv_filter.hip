@@ -2022,10 +2022,15 @@ __device__ __forceinline__ RowCut cut_floats(const Units<0> &all, Units<0> &few,
     if (r.state == CUT_NONE)
         return r;
     if (q.k < V) {
-        const double total = find_bin<false>(f, 0.0, false,
-                                             [&](int b) SV_INLINE { return (double)f.hist[b]; },
-                                             [&](double) SV_INLINE { return (double)q.k; });
+        // what min-p's floor passed over was not counted: then fewer than k may be left
+        double total = 0.0;
+        find_bin<false>(f, 0.0, false, [&](int b) SV_INLINE { return (double)f.hist[b]; },
+                        [&](double n) SV_INLINE {
+                            total = n;
+                            return fmin((double)q.k, n);
+                        });
         if (fl.active() || (double)q.k < total) {
+            const int k = (int)fmin((double)q.k, total);
             const int bin = f.bin;
             uint32_t before = (uint32_t)f.prefix;
             float lo = bin_low(bin), hi = bin_high(bin);
@@ -2039,7 +2044,7 @@ __device__ __forceinline__ RowCut cut_floats(const Units<0> &all, Units<0> &few,
                 const double was = f.prefix;
                 count_parts(few, lo, hi, r, f, [&](float) SV_INLINE { return 1ull; });
                 find_bin<true>(f, was, bin < HMAG, [&](int b) SV_INLINE { return (double)f.weight[b]; },
-                               [&](double) SV_INLINE { return (double)q.k; });
+                               [&](double) SV_INLINE { return (double)k; });
                 before = (uint32_t)f.prefix;
                 part_range(bin, f.bin, lo, hi);
             }
@@ -2047,10 +2052,10 @@ __device__ __forceinline__ RowCut cut_floats(const Units<0> &all, Units<0> &few,
                 r.state = CUT_EXACT;
                 return r;
             }
-            const unsigned long long last = f.order[q.k - before - 1];
+            const unsigned long long last = f.order[k - before - 1];
             r.cut = (uint32_t)(last >> 32);
             r.tie = (int)~(uint32_t)last;
-            r.kept = q.k;          // at most: what a draw decides by
+            r.kept = k;            // at most: what a draw decides by
             __syncthreads();
         }
     }

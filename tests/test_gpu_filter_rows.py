@@ -114,6 +114,21 @@ def test_sample_parameters_at_the_ends(ctx, dtype):
     assert all(g[i] == top[i] and gp[i] == 1 for i in (0, 1, 8, 11, 13))
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("k", [40, 300, 1500, 6000, 15000])
+def test_min_p_leaves_fewer_than_top_k(ctx, k, dtype):
+    """What lies below min-p's bound is not looked at, so that fewer than k ids may be seen."""
+    r = np.random.RandomState(k)
+    n, V = 24, 20011
+    q = plain(n)
+    q["k"][:] = k
+    q["m"][:] = 10.0 ** r.uniform(-6, -0.5, n)
+    q["T"][:] = r.uniform(0.3, 2.5, n)
+    check_sample(ctx, rows(r, n, V), dtype, q, r.rand(n).astype(np.float32))
+    f = {c: a[:8] for c, a in q.items()}
+    check_verify(ctx, workload(r, 8, 2, 5003, dtype, f, f), dtype, f, f, same=True)
+
+
 @pytest.mark.parametrize("bits", [0x7F800001, 0xFF800001, 0x7FC00000, 0xFFC00000, 0xFFFFFFFF])
 @pytest.mark.parametrize("kind", ["", "k", "p", "m"])
 def test_a_nan_of_any_sign_anywhere_ends_its_row(ctx, bits, kind):
