@@ -263,7 +263,12 @@ int specverify_quantile_cut(specverify_ctx *ctx, void *hip_stream, int P, int N,
  * A row has no law when it holds NaN or +inf or nothing finite, or when its parameters are out of
  * range (T finite and >= 0; p and m in [0, 1]; any k): see each call for what it returns then.
  * -inf entries are ids of zero weight.  Values lie in device memory, so none of this is checked on
- * the host.  All weights, sums and decisions are fp64 and every cut is the exact one.
+ * the host.  Weights, sums and decisions are fp64, and ids follow the definition wherever its
+ * comparisons differ by more than the rounding of the sums (V 2^-53 of a row's sum; with top-p on
+ * float32 rows, whose sums over close logits are integers, about 2^-47 up to 2^15 ids and 2^-41 at
+ * 2^20, at worst V/2 times that).  Integers are counted and added in any order, the rest in fixed
+ * orders; which small terms of a draw's sums are passed over as cut away may differ from run to
+ * run, and with it at most the grouping of the others, 2^-53 of a sum.
  */
 typedef struct specverify_filter {
     const float *temperature;
@@ -278,8 +283,8 @@ typedef struct specverify_filter {
  * positive weight if rounding leaves none); out_probs [N] float = its probability, or NULL.
  * logits: N rows of V ids (dtype), row n at element n * row_stride (row_stride >= V); `filter`
  * arrays [N]; uniforms [N] float in [0,1].  A row without a law gets token -1 and probability NaN.
- * One kernel, no workspace.  Errors as for specverify_sample, and EINVAL for row_stride < V,
- * ECAPACITY for N >= 2^22 (one 1024-thread workgroup per row).
+ * One kernel, nothing kept in the workspace.  Errors as for specverify_sample, and EINVAL for
+ * row_stride < V, ECAPACITY for N >= 2^22 (one 1024-thread workgroup per row).
  */
 int specverify_sample_filtered(specverify_ctx *ctx, void *hip_stream, int dtype, int N, int V,
                                int64_t row_stride, const specverify_filter *filter,

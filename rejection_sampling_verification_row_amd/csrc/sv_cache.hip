@@ -10,6 +10,12 @@
 // for; then the whole chip writes the tables and copies pages.  The plan leaves for each entry one
 // record of all that its apply needs, since an apply workgroup may find the state changed by
 // another, and since a record is one trip to memory.
+//
+// The calls read and write little but for the copies, so they are bound by launches and by trips to
+// memory in a row: a reserve and a commit of 512 sequences in a pool of 65536 pages take 4.6 us to
+// list the free pages, 6.5 to plan, 3 to apply and 3.9 to commit.  Copies run at the rate of a
+// large copy: a compaction of 3000 pages moves 340 MB in 70 us (4.9 TB/s); a fork of 480 children,
+// whose few sources stay in the caches, writes 67 MB in 13 us.
 #include <algorithm>
 
 #include "sv_device.h"
