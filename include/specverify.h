@@ -280,7 +280,8 @@ typedef struct specverify_filter {
 /*
  * Draft-token sampler with cut laws: one draw per row.  out_tokens[n] = the first id (ascending)
  * whose inclusive prefix sum of row n's kept w exceeds uniforms[n] times their sum (the last id of
- * positive weight if rounding leaves none); out_probs [N] float = its probability, or NULL.
+ * positive weight if rounding leaves none; logits <= -256 of weight below 2^-80 count as weightless
+ * there); out_probs [N] float = its probability, or NULL.
  * logits: N rows of V ids (dtype), row n at element n * row_stride (row_stride >= V); `filter`
  * arrays [N]; uniforms [N] float in [0,1].  A row without a law gets token -1 and probability NaN.
  * One kernel, nothing kept in the workspace.  Errors as for specverify_sample, and EINVAL for

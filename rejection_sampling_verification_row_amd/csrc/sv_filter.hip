@@ -377,6 +377,21 @@ __device__ __forceinline__ uint32_t vec_word(const uint4 &v, int i)
     return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
 }
 
+// One of N vectors, the same in all lanes.
+template <int N> __device__ __forceinline__ uint4 choose(const uint4 (&v)[N], int i)
+{
+    uint4 x = v[0];
+    unroll<1, N>([&](auto j) SV_INLINE {
+        if (j == i) {
+            x = v[j];
+            // keeps the choice a branch and four moves: merged, it would be an indexed read of an
+            // array, which lives in memory
+            asm volatile("" : "+v"(x.x), "+v"(x.y), "+v"(x.z), "+v"(x.w));
+        }
+    });
+    return x;
+}
+
 // ------------------------------------------------------------------ bfloat16: the cut by counting
 //
 // A bfloat16 row has few distinct values, so its cut comes from how often each occurs: one pass
@@ -414,6 +429,23 @@ __device__ __forceinline__ uint32_t bin_offsets(uint32_t t)
 }
 
 __device__ __forceinline__ float pattern_value(uint32_t p) { return __uint_as_float(p << 16); }
+
+// What masks write: values <= -2^8 and -inf.  As patterns less that of -2^8 they are the numbers up
+// to MASK_INF, largest value first; every other pattern gives a larger one.
+constexpr uint32_t MASK_TOP = 0xc380u, MASK_INF = 0xff80u - MASK_TOP;
+
+__device__ __forceinline__ uint32_t mask_words(uint32_t w)
+{
+    const u16x2 top = {(unsigned short)MASK_TOP, (unsigned short)MASK_TOP};
+    return as_u32(as_u16x2(w) - top);
+}
+// Not 0 where a half of window word t lies outside the window and, by mask word m, is not masked.
+__device__ __forceinline__ uint32_t rare_words(uint32_t t, uint32_t m)
+{
+    const u16x2 inf = {(unsigned short)MASK_INF, (unsigned short)MASK_INF};
+    return as_u32(__builtin_elementwise_min(__builtin_elementwise_sub_sat(as_u16x2(m), inf),
+                                            as_u16x2(t & 0x70007000u)));
+}
 __device__ __forceinline__ uint32_t bin_pattern(int bin)
 {
     return HLO + (uint32_t)(bin & (HMAG - 1)) + (bin >= HMAG ? 0x8000u : 0u);
@@ -455,8 +487,6 @@ __device__ __forceinline__ void count_outside(uint32_t p, CutLds &c)
     } else if (a >= 0x7f80u) {
         if (p != 0xff80u)
             atomicOr(&c.bad, 1u);
-    } else if ((p & 0x8000u) && a >= HLO) {
-        atomicMax(&c.low, order_key(pattern_value(p)));
     } else {
         const uint32_t i = atomicAdd(&c.nx, 1u);
         if (i < HX)
@@ -470,8 +500,11 @@ __device__ __forceinline__ void bump(uint32_t *hist, uint32_t off)
 }
 
 // Counts eight patterns.  The common case, all lanes inside the window, takes seven VALU
-// instructions for two patterns and one LDS add for each.
-__device__ __forceinline__ void count_vec(const uint4 &v, uint32_t *hist, CutLds &c)
+// instructions for two patterns and one LDS add for each.  Masked rows have -inf or low values
+// anywhere, so these cost little more: left out of the adds, with the largest kept in `low`, the
+// lane's least mask words.  (An LDS maximum for each of them took 500 us for a row of 152064 of
+// which 70% had the type's lowest value.)
+__device__ __forceinline__ void count_vec(const uint4 &v, uint32_t *hist, CutLds &c, uint32_t &low)
 {
     uint32_t t[4], out = 0;
 #pragma unroll
@@ -486,22 +519,46 @@ __device__ __forceinline__ void count_vec(const uint4 &v, uint32_t *hist, CutLds
             bump(hist, b & 0xffffu);
             bump(hist, b >> 16);
         }
-    } else {
-        // rare, so one body for all pairs
+        return;
+    }
+    uint32_t rare = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t b = bin_offsets(t[i]), m = mask_words(vec_word(v, i));
+        if ((t[i] & 0x7000u) == 0)
+            bump(hist, b & 0xffffu);
+        if ((t[i] & 0x70000000u) == 0)
+            bump(hist, b >> 16);
+        low = as_u32(__builtin_elementwise_min(as_u16x2(low), as_u16x2(m)));
+        rare |= rare_words(t[i], m);
+    }
+    if (__ballot(rare != 0) != 0) {
         uint32_t w0 = v.x, w1 = v.y, w2 = v.z, w3 = v.w;
 #pragma nounroll
         for (int i = 0; i < 8; ++i) {
-            const uint32_t p = w0 & 0xffffu, u = window_words(p) & 0xffffu;
-            if ((u & 0x7000u) == 0)
-                bump(hist, bin_offsets(u) & 0xffffu);
-            else
-                count_outside(p, c);
+            if (rare_words(window_words(w0), mask_words(w0)) & 0xffffu)
+                count_outside(w0 & 0xffffu, c);
             w0 = __builtin_amdgcn_alignbit(w1, w0, 16);
             w1 = __builtin_amdgcn_alignbit(w2, w1, 16);
             w2 = __builtin_amdgcn_alignbit(w3, w2, 16);
             w3 >>= 16;
         }
     }
+}
+
+constexpr uint32_t NO_LOW = 0xffffffffu;
+
+// The wave's largest value <= -2^8, if it met one.
+__device__ __forceinline__ void note_low(uint32_t low, CutLds &c)
+{
+    int m = (int)min(low & 0xffffu, low >> 16);
+    if (__ballot(m < (int)MASK_INF) == 0)
+        return;
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1)
+        m = min(m, __shfl_xor(m, o));
+    if ((threadIdx.x & 63) == 0)
+        atomicMax(&c.low, order_key(pattern_value(MASK_TOP + (uint32_t)m)));
 }
 
 __device__ __forceinline__ uint32_t wave_scan_u32(uint32_t x)
@@ -892,6 +949,7 @@ __device__ __forceinline__ void count_row(const Groups<1> &gr, Floor &fl, uint32
 {
     constexpr int U = COUNT_LOADS, NW = WGT / 64;
     const int t = threadIdx.x;
+    uint32_t low = NO_LOW;
 #pragma nounroll
     for (int i = 0; i * U * WGT < gr.whole; ++i) {
         const int g = i * U * WGT + t;
@@ -914,19 +972,20 @@ __device__ __forceinline__ void count_row(const Groups<1> &gr, Floor &fl, uint32
             }
         }
         if (full && fl.below == 0) {
-            unroll<0, U>([&](auto k) SV_INLINE { count_vec(v[k], hist, c); });
+            unroll<0, U>([&](auto k) SV_INLINE { count_vec(v[k], hist, c, low); });
         } else {
             unroll<0, U>([&](auto k) SV_INLINE {
                 if (g + k * WGT < gr.whole && fl.matters(v[k]))
-                    count_vec(v[k], hist, c);
+                    count_vec(v[k], hist, c, low);
             });
         }
     }
     if (t == 0 && gr.whole * 8 < gr.V) {
         const uint4 x = gr.load_partial();
         fl.see(x);
-        count_vec(x, hist, c);
+        count_vec(x, hist, c, low);
     }
+    note_low(low, c);
     if (fl.active() && fl.bad())
         atomicOr(&c.bad, 1u);
 }
@@ -1010,21 +1069,6 @@ template <int DT> struct Units {
         return n < 0 || i * 64 + (int)(threadIdx.x & 63) < n;
     }
 };
-
-// One of N vectors, the same in all lanes.
-template <int N> __device__ __forceinline__ uint4 choose(const uint4 (&v)[N], int i)
-{
-    uint4 x = v[0];
-    unroll<1, N>([&](auto j) SV_INLINE {
-        if (j == i) {
-            x = v[j];
-            // keeps the choice a branch and four moves: merged, it would be an indexed read of an
-            // array, which lives in memory
-            asm volatile("" : "+v"(x.x), "+v"(x.y), "+v"(x.z), "+v"(x.w));
-        }
-    });
-    return x;
-}
 
 // A wave's units are read four at a time (a batch), all four loads in flight.  A wave notes in
 // a bit per batch where there was something for it, and later passes read only those.
@@ -1450,17 +1494,20 @@ struct TableLaw {
     double scale;
     const double *table;
     uint32_t cut_off;        // where some of the cut's ties are left out: its offset, if it has one
+    bool low_counts;         // logits <= -2^8 may weigh something
 
     __device__ __forceinline__ TableLaw(const RowCut &c, int V, double sc, const double *tab)
-        : r(c), scale(sc), table(tab), cut_off(~0u)
+        : r(c), scale(sc), table(tab), cut_off(~0u), low_counts(weight(-256.0f, c.max, c.c) >= 0x1p-80)
     {
         const uint32_t t = window_words(__float_as_uint(key_value(c.cut)) >> 16) & 0xffffu;
         if (c.tie < V && (t & 0x7000u) == 0)
             cut_off = offsets(t) & 0xffffu;
     }
-    // Whether a unit's groups can be looked up whole: no logit outside the window, and not the
-    // group in which the kept ties end.
-    __device__ __forceinline__ bool by_table(int g, const uint4 &v, uint32_t (&t)[4]) const
+    // How a unit's groups can be looked up: whole (no logit outside the window), with masked logits
+    // left out, or id by id (rare values, low ones that count, and the group in which the kept ties
+    // end).
+    enum Way { WHOLE, MASKED, SINGLY };
+    __device__ __forceinline__ Way by_table(int g, const uint4 &v, uint32_t (&t)[4]) const
     {
         uint32_t out = 0;
 #pragma unroll
@@ -1468,7 +1515,13 @@ struct TableLaw {
             t[i] = window_words(vec_word(v, i));
             out |= t[i] & 0x70007000u;
         }
-        return __ballot(out != 0 || g == r.tie / 8) == 0;
+        if (__ballot(out != 0 || g == r.tie / 8) == 0)
+            return WHOLE;
+        uint32_t rare = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            rare |= rare_words(t[i], mask_words(vec_word(v, i)));
+        return __ballot(rare != 0 || low_counts || g == r.tie / 8) == 0 ? MASKED : SINGLY;
     }
     // 8 * bin of both halves
     static __device__ __forceinline__ uint32_t offsets(uint32_t t)
@@ -1487,19 +1540,33 @@ struct TableLaw {
         const double x = at(off);
         return off == without ? 0.0 : x;
     }
+    // the halves of window word t, 0 outside the window
+    __device__ __forceinline__ double low_half(uint32_t t, uint32_t without) const
+    {
+        const double x = at(offsets(t) & 0xffffu, without);
+        return (t & 0x7000u) == 0 ? x : 0.0;
+    }
+    __device__ __forceinline__ double high_half(uint32_t t, uint32_t without) const
+    {
+        const double x = at(offsets(t) >> 16, without);
+        return (t & 0x70000000u) == 0 ? x : 0.0;
+    }
     __device__ __forceinline__ double one(float y, int id) const
     {
         const uint32_t p = __float_as_uint(y) >> 16, t = window_words(p) & 0xffffu;
         if ((t & 0x7000u) == 0)
             return y == key_value(r.cut) && id > r.tie ? 0.0 : at(offsets(t) & 0xffffu);
-        return kept(order_key(y), id, r) && y != -INFINITY ? weight(y, r.max, r.c) * scale : 0.0;
+        return kept(order_key(y), id, r) && y > (low_counts ? -INFINITY : -256.0f)
+                   ? weight(y, r.max, r.c) * scale
+                   : 0.0;
     }
     __device__ __forceinline__ uint4 aux(int) const { return make_uint4(0, 0, 0, 0); }
     __device__ __forceinline__ double sum(int g, const uint4 &v, const uint4 &) const
     {
         uint32_t t[4];
         double s = 0.0;
-        if (by_table(g, v, t)) {
+        const Way way = by_table(g, v, t);
+        if (way == WHOLE) {
             if (cut_off == ~0u) {
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
@@ -1515,6 +1582,13 @@ struct TableLaw {
                     s += at(b & 0xffffu, no);
                     s += at(b >> 16, no);
                 }
+            }
+        } else if (way == MASKED) {
+            const uint32_t no = left_out(g);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                s += low_half(t[i], no);
+                s += high_half(t[i], no);
             }
         } else {
             uint32_t w[4] = {v.x, v.y, v.z, v.w};
@@ -1549,14 +1623,24 @@ template <int DT, typename P> struct ResidualLaw {
             return p.sum(g, pv, qv);
         if constexpr (DT == 1) {
             uint32_t tp[4], tq[4];
-            const bool a = p.by_table(g, pv, tp), b = q.by_table(g, qv, tq);
-            if (a && b) {
+            const auto a = p.by_table(g, pv, tp);
+            const auto b = q.by_table(g, qv, tq);
+            if (a == P::WHOLE && b == P::WHOLE) {
                 const uint32_t np = p.left_out(g), nq = q.left_out(g);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const uint32_t op = P::offsets(tp[i]), oq = P::offsets(tq[i]);
                     s += fmax(p.at(op & 0xffffu, np) - q.at(oq & 0xffffu, nq), 0.0);
                     s += fmax(p.at(op >> 16, np) - q.at(oq >> 16, nq), 0.0);
+                }
+                return s;
+            }
+            if (a != P::SINGLY && b != P::SINGLY) {
+                const uint32_t np = p.left_out(g), nq = q.left_out(g);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    s += fmax(p.low_half(tp[i], np) - q.low_half(tq[i], nq), 0.0);
+                    s += fmax(p.high_half(tp[i], np) - q.high_half(tq[i], nq), 0.0);
                 }
                 return s;
             }
@@ -1615,6 +1699,7 @@ __global__ __launch_bounds__(FWG, 4) void k_filter_sample_bf16(const char *logit
     cut_lds_clear(c);
     __syncthreads();
     int listed = 0;
+    uint32_t low = NO_LOW;
     const int units = all.count();
     if (fl.active() && units == 0)         // the other waves wait below
         __syncthreads();
@@ -1635,17 +1720,18 @@ __global__ __launch_bounds__(FWG, 4) void k_filter_sample_bf16(const char *logit
             listed = LIST + 1;
             unroll<0, BATCH>([&](auto j) SV_INLINE {
                 if (i0 + j < units)
-                    count_vec(v[j], hist, c);
+                    count_vec(v[j], hist, c, low);
             });
         } else {
             unroll<0, BATCH>([&](auto j) SV_INLINE {
                 const bool m = i0 + j < units && fl.matters(v[j]);
                 list_groups(dl.list[wv], listed, m, (i0 + j) * 64 + lane);
                 if (m)
-                    count_vec(v[j], hist, c);
+                    count_vec(v[j], hist, c, low);
             });
         }
     }
+    note_low(low, c);
     if (fl.active() && fl.bad())
         atomicOr(&c.bad, 1u);
     cut_from_counts<FWG>(hist, c, q, V, !fl.active(), table);
@@ -1732,23 +1818,47 @@ __device__ __forceinline__ uint2 upper_halves(const uint4 &v)
                       __builtin_amdgcn_perm(v.w, v.z, 0x07060302u));
 }
 
-__device__ __forceinline__ void count_floats(const uint4 &v, const uint2 &h, FloatLds &f, CutLds &c)
+// Masked logits are left out, the finite ones counted in `low` by each lane.
+__device__ __forceinline__ bool outside(const uint2 &h)
+{
+    return ((window_words(h.x) | window_words(h.y)) & 0x70007000u) != 0;
+}
+
+__device__ __forceinline__ void count_inside(const uint2 &h, uint32_t *hist)
+{
+    const uint32_t a = bin_offsets(window_words(h.x)), b = bin_offsets(window_words(h.y));
+    bump(hist, a & 0xffffu);
+    bump(hist, a >> 16);
+    bump(hist, b & 0xffffu);
+    bump(hist, b >> 16);
+}
+
+__device__ __forceinline__ void count_any(const uint4 &v, const uint2 &h, FloatLds &f, CutLds &c,
+                                          uint32_t &low)
 {
     const uint32_t t0 = window_words(h.x), t1 = window_words(h.y);
-    if (__ballot(((t0 | t1) & 0x70007000u) != 0) == 0) {
-        const uint32_t a = bin_offsets(t0), b = bin_offsets(t1);
+    const uint32_t a = bin_offsets(t0), b = bin_offsets(t1);
+    if ((t0 & 0x7000u) == 0)
         bump(f.hist, a & 0xffffu);
+    if ((t0 & 0x70000000u) == 0)
         bump(f.hist, a >> 16);
+    if ((t1 & 0x7000u) == 0)
         bump(f.hist, b & 0xffffu);
+    if ((t1 & 0x70000000u) == 0)
         bump(f.hist, b >> 16);
-    } else {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    unroll<0, 4>([&](auto k) SV_INLINE { low += w[k] - (MASK_TOP << 16) < MASK_INF << 16; });
+    if (__ballot((rare_words(t0, mask_words(h.x)) | rare_words(t1, mask_words(h.y))) != 0) != 0) {
         uint32_t w0 = v.x, w1 = v.y, w2 = v.z, w3 = v.w;
 #pragma nounroll
         for (int i = 0; i < 4; ++i) {
-            if ((w0 & 0x7f800000u) != 0x7f800000u)
-                atomicAdd(&f.hist[float_bin(w0)], 1u);
-            else if (w0 != 0xff800000u)
-                atomicOr(&c.bad, 1u);
+            const uint32_t u = w0 >> 16;
+            if (rare_words(window_words(u), mask_words(u)) & 0xffffu) {
+                if ((w0 & 0x7f800000u) != 0x7f800000u)
+                    atomicAdd(&f.hist[float_bin(w0)], 1u);
+                else
+                    atomicOr(&c.bad, 1u);
+            }
             w0 = w1;
             w1 = w2;
             w2 = w3;
@@ -1976,6 +2086,7 @@ __device__ __forceinline__ RowCut cut_floats(const Units<0> &all, Units<0> &few,
     Floor fl(q, V, FWAVES);
     float mx = -INFINITY;
     uint32_t most = 0;             // as unsigned bits: a NaN of negative sign is above -inf
+    uint32_t low = 0;              // finite logits <= -2^8
     int listed = 0;
     if (fl.active() && units == 0)
         __syncthreads();
@@ -1999,23 +2110,45 @@ __device__ __forceinline__ RowCut cut_floats(const Units<0> &all, Units<0> &few,
                 __syncthreads();
             fl.update<FWAVES>(c);
         }
+        uint32_t wait = 0;
+        auto matters = [&](const uint2 &x) SV_INLINE {
+            return max_i16(max_i16(x.x, x.y), fl.below) != fl.below;
+        };
         if (fl.below == 0) {
             listed = LIST + 1;
             unroll<0, BATCH>([&](auto j) SV_INLINE {
-                if (i0 + j < units)
-                    count_floats(v[j], h[j], f, c);
+                if (i0 + j < units) {
+                    if (__ballot(outside(h[j])) == 0)
+                        count_inside(h[j], f.hist);
+                    else
+                        wait |= 1u << j;
+                }
             });
         } else {
             unroll<0, BATCH>([&](auto j) SV_INLINE {
-                const bool m = i0 + j < units && max_i16(max_i16(h[j].x, h[j].y), fl.below) != fl.below;
+                const bool m = i0 + j < units && matters(h[j]);
                 list_groups(dl.list[wv], listed, m, (i0 + j) * 64 + lane);
-                if (m)
-                    count_floats(v[j], h[j], f, c);
+                if (__ballot(m && outside(h[j])) != 0)
+                    wait |= 1u << j;
+                else if (m)
+                    count_inside(h[j], f.hist);
             });
+        }
+#pragma nounroll
+        for (wait = __builtin_amdgcn_readfirstlane(wait); wait; wait &= wait - 1) {
+            const uint4 x = choose(v, __builtin_ctz(wait));
+            const uint2 y = upper_halves(x);
+            if (fl.below == 0 || matters(y))
+                count_any(x, y, f, c, low);
         }
     }
     if (most > 0xff800000u)
         atomicOr(&c.bad, 1u);
+    if (__ballot(low != 0) != 0) {
+        low = wave_scan_u32(low);
+        if (lane == 63)
+            atomicAdd(&f.hist[BIN_LOW], low);
+    }
     few.n = listed <= LIST ? __builtin_amdgcn_readfirstlane(listed) : -1;
     few.list = dl.list[wv];
     RowCut r;
@@ -2095,12 +2228,20 @@ __device__ __forceinline__ RowCut cut_floats(const Units<0> &all, Units<0> &few,
             __syncthreads();
         };
         auto weight_of = [&](int b) SV_INLINE { return __longlong_as_double((long long)f.weight[b]); };
+        // masked logits are passed over where even V of -2^8 would not be noticed
+        const bool low_counts = weight(edge(BIN_LOW), r.max, r.c) >= 0x1p-80;
         each_vec(few, [&](const uint4 &v, int id) SV_INLINE {
             uint32_t w[4] = {v.x, v.y, v.z, v.w};
-            const uint32_t t0 = window_words(upper_halves(v).x), t1 = window_words(upper_halves(v).y);
-            if (__ballot(((t0 | t1) & 0x70007000u) != 0) == 0) {
-                // all in the window: an edge is the logit's own upper half, and their difference
-                // is exact, since they share an exponent
+            const uint2 h = upper_halves(v);
+            const uint32_t t0 = window_words(h.x), t1 = window_words(h.y);
+            const uint32_t other = low_counts ? (t0 | t1) & 0x70007000u
+                                              : rare_words(t0, mask_words(h.x)) | rare_words(t1, mask_words(h.y));
+            if (__ballot(other != 0) == 0) {
+                // all in the window, or masked, whose weights come to nothing of use.  An edge is
+                // the logit's own upper half, and their difference is exact, since they share an
+                // exponent.
+                const bool whole = __ballot(((t0 | t1) & 0x70007000u) != 0) == 0;
+                const uint32_t out[4] = {t0 & 0x7000u, t0 & 0x70000000u, t1 & 0x7000u, t1 & 0x70000000u};
                 float d[4];
                 double a[4], p[4];
                 unroll<0, 4>([&](auto k) SV_INLINE {
@@ -2115,6 +2256,8 @@ __device__ __forceinline__ RowCut cut_floats(const Units<0> &all, Units<0> &few,
                 const uint32_t b0 = bin_offsets(t0), b1 = bin_offsets(t1);
                 const uint32_t at[4] = {b0 & 0xffffu, b0 >> 16, b1 & 0xffffu, b1 >> 16};
                 unroll<0, 4>([&](auto k) SV_INLINE {
+                    if (!whole && out[k] != 0)
+                        return;
                     if (cut && !kept(order_key(__uint_as_float(w[k])), id + k, r))
                         return;
                     atomicAdd(&f.weight[at[k] / 4], to_units(p[k]));
@@ -2125,7 +2268,7 @@ __device__ __forceinline__ RowCut cut_floats(const Units<0> &all, Units<0> &few,
 #pragma nounroll
                 for (int k = 0; k < 4; ++k) {
                     const float x = __uint_as_float(w[0]);
-                    if (x != -INFINITY && kept(order_key(x), id + k, r)) {
+                    if (x > (low_counts ? -INFINITY : -256.0f) && kept(order_key(x), id + k, r)) {
                         const int b = float_bin(w[0]);
                         atomicAdd(&f.weight[b], units_of(x, edge(b)));
                         if (cut)

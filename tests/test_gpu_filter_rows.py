@@ -115,6 +115,30 @@ def test_sample_parameters_at_the_ends(ctx, dtype):
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("low", [-np.inf, -3.3895313892515355e38, -1e9, -257.0])
+@pytest.mark.parametrize("T", [0.7, 90.0])
+def test_verify_masked_ids(ctx, low, T, dtype):
+    """Most ids masked in both models' rows; at T = 90 the low value -257 still weighs something."""
+    r = np.random.RandomState(int(T))
+    B, K, V = 8, 3, 4003
+    ft = params(r, B, "mixed")
+    ft["T"][ft["T"] > 0] *= T
+    gone = r.rand(B, 1, V) < 0.8
+    gone[:, :, 5] = False
+    t = rows(r, B * (K + 1), V).reshape(B, K + 1, V)
+    d = t[:, :K] + rows(r, B * K, V, 0.5).reshape(B, K, V)
+    t, d = np.where(gone, low, t).astype(np.float32), np.where(gone, low, d).astype(np.float32)
+    tb, tv = as_dtype(t, dtype)
+    db, dv = as_dtype(d, dtype)
+    x = np.zeros((B, K), np.int32)
+    for b in range(B):
+        for j in range(K):
+            q = model.law(dv[b, j], *(ft[c][b] for c in "Tkpm"))[0]
+            x[b, j] = r.choice(V, p=q / q.sum())
+    check_verify(ctx, (tb, tv, db, dv, x, r.rand(B, K + 1).astype(np.float32)), dtype, ft, ft, same=True)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
 @pytest.mark.parametrize("k", [40, 300, 1500, 6000, 15000])
 def test_min_p_leaves_fewer_than_top_k(ctx, k, dtype):
     """What lies below min-p's bound is not looked at, so that fewer than k ids may be seen."""
