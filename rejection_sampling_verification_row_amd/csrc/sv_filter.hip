@@ -1303,6 +1303,19 @@ template <int DT> struct MayKeep {
     }
 };
 
+// Values that are the same in all lanes, kept in scalar registers: the laws' parameters would else
+// take some 30 vector registers of a draw that has none to spare.
+__device__ __forceinline__ double uniform(double x) { return lane_value(x, 0); }
+__device__ __forceinline__ RowCut uniform(RowCut r)
+{
+    r.z = uniform(r.z);
+    r.c = uniform(r.c);
+    r.max = __int_as_float(__builtin_amdgcn_readfirstlane(__float_as_int(r.max)));
+    r.cut = (uint32_t)__builtin_amdgcn_readfirstlane((int)r.cut);
+    r.tie = __builtin_amdgcn_readfirstlane(r.tie);
+    return r;
+}
+
 // Finds, for up to two rows at once, the last kept id among those equal to a cut, the n-th of
 // them: equals per batch and wave, then the unit, the lane and the id.  need: bit 0 p, bit 1 q,
 // bit 2: list the groups of p (all of its range) that can hold a kept id.  Returns the list's
@@ -1497,11 +1510,12 @@ struct TableLaw {
     bool low_counts;         // logits <= -2^8 may weigh something
 
     __device__ __forceinline__ TableLaw(const RowCut &c, int V, double sc, const double *tab)
-        : r(c), scale(sc), table(tab), cut_off(~0u), low_counts(weight(-256.0f, c.max, c.c) >= 0x1p-80)
+        : r(uniform(c)), scale(uniform(sc)), table(tab), cut_off(~0u)
     {
-        const uint32_t t = window_words(__float_as_uint(key_value(c.cut)) >> 16) & 0xffffu;
-        if (c.tie < V && (t & 0x7000u) == 0)
+        const uint32_t t = window_words(__float_as_uint(key_value(r.cut)) >> 16) & 0xffffu;
+        if (r.tie < V && (t & 0x7000u) == 0)
             cut_off = offsets(t) & 0xffffu;
+        low_counts = __builtin_amdgcn_readfirstlane(weight(-256.0f, r.max, r.c) >= 0x1p-80);
     }
     // How a unit's groups can be looked up: whole (no logit outside the window), with masked logits
     // left out, or id by id (rare values, low ones that count, and the group in which the kept ties
@@ -2365,7 +2379,7 @@ __global__ __launch_bounds__(FWG, 4) void k_filter_sample_f32(const char *logits
     }
     int id = -1;
     if (r.state == CUT_READY)
-        id = draw_row(few, MayKeep<0>(r), (double)unif[n], dl, DirectLaw<0>{r, 1.0});
+        id = draw_row(few, MayKeep<0>(r), (double)unif[n], dl, DirectLaw<0>{uniform(r), 1.0});
     if (threadIdx.x == 0) {
         tok[n] = id;
         if (prob) {
@@ -2398,7 +2412,7 @@ __global__ __launch_bounds__(FWG, 4) void k_filter_rows_f32(const char *tgt, con
     if (r.state == CUT_EXACT)
         r = cut_by_bisection<0>(row, V, q, red);
     else if (r.state == CUT_READY && r.z == 0.0)
-        r.z = row_total(few, MayKeep<0>(r), DirectLaw<0>{r, 1.0}, red);
+        r.z = row_total(few, MayKeep<0>(r), DirectLaw<0>{uniform(r), 1.0}, red);
     if (threadIdx.x == 0)
         cuts[n] = r;
 }
@@ -2552,7 +2566,7 @@ __global__ __launch_bounds__(FWG, 4) void k_filter_verify(const char *tgt, const
         if constexpr (DT == 1)
             draw(TableLaw(rp, V, 1.0 / rp.z, tables[0]), TableLaw(rq, V, 1.0 / rq.z, tables[1]));
         else
-            draw(DirectLaw<DT>{rp, 1.0 / rp.z}, DirectLaw<DT>{rq, 1.0 / rq.z});
+            draw(DirectLaw<DT>{uniform(rp), uniform(1.0 / rp.z)}, DirectLaw<DT>{uniform(rq), uniform(1.0 / rq.z)});
     }
     if (t <= K) {
         const size_t o = (size_t)b * (K + 1) + t;
