@@ -1000,9 +1000,9 @@ constexpr int RWG = 512;   // threads per row of a bfloat16 verify: four workgro
 
 // The RowCut of every target and draft row of a bfloat16 verify.  Four workgroups of 35 KB to a
 // compute unit, so that one counts while another is at its cut's barriers: 4352 rows of 128256
-// (1.12 GB) take 170 us, 6.6 TB/s, where a bare streaming read of the same layout takes 161-164.
-// Counting is seven VALU instructions and two LDS adds for two logits: in those 170 us a SIMD issues
-// 62 thousand VALU instructions (250 thousand clocks) and a compute unit's LDS works for 116
+// (1.12 GB) take 171 us, 6.5 TB/s, where a bare streaming read of the same layout takes 161-164.
+// Counting is seven VALU instructions and two LDS adds for two logits: in those 171 us a SIMD issues
+// 65 thousand VALU instructions (260 thousand clocks) and a compute unit's LDS works for 116
 // thousand, so that the reads hide both, but not by much.
 __global__ __launch_bounds__(RWG, 8) void k_filter_rows_bf16(const char *tgt, const char *drf, int B,
                                                              int K, int V, FilterPtrs ft,
@@ -2433,7 +2433,7 @@ struct VerifyLds {
 };
 
 // Accept tests, first rejection and the replacement or bonus draw of one sequence.  256 sequences of
-// 128256 in bfloat16 take 62 us: 5 for the tests, 2 for the tables, then 16 (two lookups per id,
+// 128256 in bfloat16 take 60 us: 5 for the tests, 2 for the tables, then 16 (two lookups per id,
 // as in the sampler) where p keeps much, or 13 to list p's few groups and 3 to draw from them, and
 // 3 to 6 to find the id.  A chip has as many workgroups in flight as sequences, so a batch waits
 // for its slowest.
