@@ -2033,9 +2033,9 @@ __device__ __forceinline__ void part_range(int bin, int part, float &lo, float &
     hi = __uint_as_float(bin >= HMAG ? p : p | 7u);
 }
 
-// How many of the ordered logits stay: those before which less than goal lies (counting `base`
-// before all of them), of weight at least m and among the first k.  Sets r's cut to the last, and
-// returns what lies before the first that goes; *sum is the sum over the first k.
+// How many of the ordered logits, of which there is one at least, stay: those before which less than
+// goal lies (counting `base` before all of them), of weight at least m and among the first k; with
+// p < 1 the goal is p times the sum over the first k.  Sets r's cut to the last, and its z.
 __device__ __forceinline__ void cut_in_order(RowCut &r, double base, int k, double p, double goal,
                                              double m, FloatLds &f)
 {
@@ -2054,7 +2054,8 @@ __device__ __forceinline__ void cut_in_order(RowCut &r, double base, int k, doub
             before += f.dwave[i];
     }
     before += base;
-    const bool keep = t < n && (before < goal || t == 0) && w >= m;
+    // the first stays whatever the rounding: it is the row's largest, or m is 0
+    const bool keep = t < n && (t == 0 || (before < goal && w >= m));
     const int stay = __syncthreads_count(keep);
     if (t == stay - 1) {
         f.place = (int)~(uint32_t)f.order[t];
@@ -2188,27 +2189,36 @@ __device__ __forceinline__ RowCut cut_floats(const Units<0> &all, Units<0> &few,
             const int bin = f.bin;
             uint32_t before = (uint32_t)f.prefix;
             float lo = bin_low(bin), hi = bin_high(bin);
-            if (before + f.hist[bin] <= (q.p < 1.0 ? AT_ONCE_P : AT_ONCE)) {
+            // What min-p's floor passed over is not in the counts but may be met again below, where
+            // a wave has no list.  All of it lies below this bound, and nothing there is kept.
+            const float least = fl.by_m ? r.max + fl.drop : -INFINITY;
+            const bool some = hi >= least;
+            if (some && before + f.hist[bin] <= (q.p < 1.0 ? AT_ONCE_P : AT_ONCE)) {
                 // all that top-k can keep is in hand: the three cuts at once
-                gather(few, lo, FLT_MAX, r, f);
-                cut_in_order(r, 0.0, q.k, q.p, INFINITY, q.m, f);
+                if (gather(few, fmaxf(lo, least), FLT_MAX, r, f))
+                    cut_in_order(r, 0.0, q.k, q.p, INFINITY, q.m, f);
+                else
+                    r.state = CUT_EXACT;
                 return r;
             }
-            if (f.hist[bin] > GATHER && bin < HBINS) {
+            if (some && f.hist[bin] > GATHER && bin < HBINS) {
                 const double was = f.prefix;
-                count_parts(few, lo, hi, r, f, [&](float) SV_INLINE { return 1ull; });
+                count_parts(few, fmaxf(lo, least), hi, r, f, [&](float) SV_INLINE { return 1ull; });
                 find_bin<true>(f, was, bin < HMAG, [&](int b) SV_INLINE { return (double)f.weight[b]; },
                                [&](double) SV_INLINE { return (double)k; });
                 before = (uint32_t)f.prefix;
                 part_range(bin, f.bin, lo, hi);
             }
-            if (!gather(few, lo, hi, r, f)) {
+            if (some && !gather(few, fmaxf(lo, least), hi, r, f)) {
                 r.state = CUT_EXACT;
                 return r;
             }
-            const unsigned long long last = f.order[k - before - 1];
-            r.cut = (uint32_t)(last >> 32);
-            r.tie = (int)~(uint32_t)last;
+            // where the k-th lies below the bound, min-p alone cuts the row
+            if (some && k - (int)before <= (int)f.n) {
+                const unsigned long long last = f.order[k - before - 1];
+                r.cut = (uint32_t)(last >> 32);
+                r.tie = (int)~(uint32_t)last;
+            }
             r.kept = k;            // at most: what a draw decides by
             __syncthreads();
         }
