@@ -358,11 +358,11 @@ int specverify_cache_destroy(specverify_cache *cache);
 
 /*
  * Make room: sequence seqs[i] will hold pages for lengths + counts[i] tokens (K + 1 places before
- * a verify; the prompt's before a prefill), and if counts[i] > 0 and the partly filled page it
- * will write into has other holders, a page of its own with the same contents.  Lengths stay.
- * What is shared is decided by the state before the call: of two listed holders of one page each
- * gets a copy.  Refused besides: counts[i] < 0, more than max_blocks pages, or more pages asked
- * for up to this entry than are free.
+ * a verify; the prompt's before a prefill), and pages of its own in place of those among the
+ * counts[i] tokens that have other holders: a copy of the partly filled page, and for pages past
+ * the length, which hold nothing, new ones.  Lengths stay.  What is shared is decided by the state
+ * before the call: of two listed holders of one page each gets one.  Refused besides: counts[i] < 0,
+ * more than max_blocks pages, or more pages asked for up to this entry than are free.
  */
 int specverify_cache_reserve(specverify_cache *cache, void *hip_stream, int n, const int32_t *seqs,
                              const int32_t *counts, int32_t *status);

@@ -167,9 +167,10 @@ __device__ inline bool sound(const CacheView &c, int b, int l)
 
 // Gives the entries their places among the free pages, and lists the pages taken in c.map.
 // ask(i, e) is what entry i asks for and fills in its record (-1: it is refused); an entry is
-// granted when all that is asked up to it exists.
-template <typename Ask>
-__device__ void grant(const CacheView &c, int n, int *status, int *lds, Ask ask)
+// granted when all that is asked up to it exists.  placed(e) then sees its record, seq -1 where
+// nothing is granted.  Whole waves call both, past the list's end too.
+template <typename Ask, typename Placed>
+__device__ void grant(const CacheView &c, int n, int *status, int *lds, Ask ask, Placed placed)
 {
     __shared__ int before[LDS_STRETCHES];
     const int stretches = (c.num_pages + CACHE_STRETCH - 1) / CACHE_STRETCH;
@@ -178,12 +179,12 @@ __device__ void grant(const CacheView &c, int n, int *status, int *lds, Ask ask)
         __syncthreads();
     }
     const int found = scan_free(c, stretches, before, lds);
-    // unsigned: sum stays at found + 1, 2^30 at most, and a tile asks for at most 1024 (2^20 + 1)
+    // unsigned: sum stays at found + 1, 2^30 at most, and a tile asks for at most 1024 * 2^20
     uint32_t sum = 0;
     for (int i0 = 0; i0 < n; i0 += CWG) {
         const int i = i0 + threadIdx.x;
         CacheEntry e = {-1, -1, 0, 0, 0, 0, -1, -1};
-        const int a = i < n ? ask(i, e) : 0;
+        const int a = ask(i, e);
         int all;
         const int inc = block_incl_scan(max(a, 0), lds, &all);
         if (i < n) {
@@ -197,10 +198,36 @@ __device__ void grant(const CacheView &c, int n, int *status, int *lds, Ask ask)
             if (status)
                 status[i] = ok ? 0 : -1;
         }
+        placed(e);
         sum = min(sum + (uint32_t)all, (uint32_t)found + 1);
     }
     for (int i = threadIdx.x; i < (int)min(sum, (uint32_t)found); i += CWG)
         c.map[i] = free_page(c, stretches, before, i);
+}
+
+// How many of the blocks from .. to of a lane's sequence name a page that others hold too; with
+// first >= 0 they are listed in c.src from there on.  A wave walks its lanes' blocks together, one
+// lane's after another: few have any, since a commit leaves no page past the length.
+__device__ int shared_blocks(const CacheView &c, int seq, int from, int to, int first)
+{
+    const int lane = threadIdx.x & 63;
+    int mine = 0;
+    for (uint64_t who = __ballot(from < to); who; who &= who - 1) {
+        const int l = __builtin_ctzll(who), s = __shfl(seq, l), end = __shfl(to, l), at = __shfl(first, l);
+        const int *row = c.tables + (size_t)s * c.max_blocks;
+        int n = 0;
+        for (int j0 = __shfl(from, l); j0 < end; j0 += 64) {
+            const int j = j0 + lane, pg = j < end ? row[j] : -1;
+            const bool shared = in_range(pg, c.num_pages) && c.refs[pg] > 1;
+            const uint64_t all = __ballot(shared);
+            if (shared && at >= 0)
+                c.src[at + n + __popcll(all & ((1ull << lane) - 1))] = j;
+            n += __popcll(all);
+        }
+        if (lane == l)
+            mine = n;
+    }
+    return mine;
 }
 
 __global__ __launch_bounds__(CWG) void k_reserve_plan(CacheView c, int n, const int *seqs,
@@ -208,27 +235,43 @@ __global__ __launch_bounds__(CWG) void k_reserve_plan(CacheView c, int n, const 
 {
     __shared__ int lds[CWAVES];
     claim(c, n, seqs);
-    grant(c, n, status, lds, [&](int i, CacheEntry &e) {
-        const int s = seqs ? seqs[i] : i, cnt = counts[i];
-        if (!in_range(s, c.num_seqs) || load_agent(&c.owner[s]) != i)
-            return -1;
-        const int len = c.lengths[s], had = c.blocks[s];
-        if (!sound(c, had, len) || cnt < 0 || cnt > c.max_blocks * c.page_tokens - len)
-            return -1;
-        e.seq = s;
-        e.had = e.want = had;
-        e.len = len;
-        if (cnt == 0)
-            return 0;
-        e.want = max(had, ceil_div(len + cnt, c.page_tokens));
-        if (len % c.page_tokens != 0) {
-            // a page of its own where it will write into one that another holds too
-            const int pg = c.tables[(size_t)s * c.max_blocks + len / c.page_tokens];
-            if (in_range(pg, c.num_pages) && c.refs[pg] > 1)
-                e.src = pg;
-        }
-        return e.want - had + (e.src >= 0);
-    });
+    int past = 0, end = 0;         // the blocks held past the length that it will write into
+    grant(
+        c, n, status, lds,
+        [&](int i, CacheEntry &e) {
+            past = end = 0;
+            int a = i < n ? -1 : 0;
+            const int s = i < n ? (seqs ? seqs[i] : i) : -1, cnt = i < n ? counts[i] : 0;
+            if (in_range(s, c.num_seqs) && load_agent(&c.owner[s]) == i) {
+                const int len = c.lengths[s], had = c.blocks[s];
+                if (sound(c, had, len) && cnt >= 0 && cnt <= c.max_blocks * c.page_tokens - len) {
+                    e.seq = s;
+                    e.had = e.want = had;
+                    e.len = len;
+                    a = 0;
+                    if (cnt > 0) {
+                        const int need = ceil_div(len + cnt, c.page_tokens);
+                        e.want = max(had, need);
+                        past = ceil_div(len, c.page_tokens);
+                        end = min(had, need);
+                        if (len % c.page_tokens != 0) {
+                            // partly filled: a copy, where another holds it too
+                            const int pg = c.tables[(size_t)s * c.max_blocks + len / c.page_tokens];
+                            if (in_range(pg, c.num_pages) && c.refs[pg] > 1)
+                                e.src = pg;
+                        }
+                        a = e.want - had + (e.src >= 0);
+                    }
+                }
+            }
+            e.from = shared_blocks(c, s, past, end, -1);
+            return a + e.from;
+        },
+        [&](const CacheEntry &e) {
+            if (e.seq < 0 || e.from == 0)
+                end = past;
+            shared_blocks(c, e.seq, past, end, e.first);
+        });
     unclaim(c, n, seqs);
 }
 
@@ -300,17 +343,30 @@ __device__ inline int copy_group()
     return (blockIdx.z * gridDim.y + blockIdx.y) * gridDim.x + blockIdx.x;
 }
 
-// Pages had .. want of an entry, one lane each, and its copied page.
+__device__ inline void release(const CacheView &c, int pg)
+{
+    if (in_range(pg, c.num_pages) && atomicSub(&c.refs[pg], 1) <= 0)
+        atomicAdd(&c.refs[pg], 1);
+}
+
+// An entry's pages, one lane each: those in place of shared ones, then had .. want; and its copied
+// page.
 __device__ inline void take_pages(const CacheView &c, const CacheEntry &e, int *row)
 {
     const int lane = threadIdx.x & 63;
-    for (int j = e.had + lane; j < e.want; j += 64) {
-        const int pg = c.map[e.first + j - e.had];
+    for (int i = lane; i < e.from + e.want - e.had; i += 64) {
+        const int pg = c.map[e.first + i];
+        const int j = i < e.from ? c.src[e.first + i] : e.had + i - e.from;
+        if (i < e.from)
+            release(c, row[j]);
         row[j] = pg;
         c.refs[pg] = 1;
     }
-    if (lane == 0 && e.dst >= 0)
+    if (lane == 0 && e.dst >= 0) {
+        row[e.len / c.page_tokens] = e.dst;
         c.refs[e.dst] = 1;
+        release(c, e.src);
+    }
 }
 
 __global__ __launch_bounds__(COPY_WG) void k_reserve_apply(CacheView c, int n)
@@ -322,22 +378,10 @@ __global__ __launch_bounds__(COPY_WG) void k_reserve_apply(CacheView c, int n)
             continue;
         int *row = c.tables + (size_t)e.seq * c.max_blocks;
         take_pages(c, e, row);
-        if (lane == 0) {
-            if (e.dst >= 0) {
-                row[e.len / c.page_tokens] = e.dst;
-                atomicSub(&c.refs[e.src], 1);
-            }
-            if (e.want > e.had)
-                c.blocks[e.seq] = e.want;
-        }
+        if (lane == 0 && e.want > e.had)
+            c.blocks[e.seq] = e.want;
     }
     copy_entries(c, n);
-}
-
-__device__ inline void release(const CacheView &c, int pg)
-{
-    if (in_range(pg, c.num_pages) && atomicSub(&c.refs[pg], 1) <= 0)
-        atomicAdd(&c.refs[pg], 1);
 }
 
 __global__ __launch_bounds__(CWG) void k_commit(CacheView c, int n, const int *seqs,
@@ -372,7 +416,9 @@ __global__ __launch_bounds__(CWG) void k_fork_plan(CacheView c, int n, const int
 {
     __shared__ int lds[CWAVES];
     claim(c, n, children);
-    grant(c, n, status, lds, [&](int i, CacheEntry &e) {
+    auto ask = [&](int i, CacheEntry &e) {
+        if (i >= n)
+            return 0;
         const int a = parents[i], b = children[i];
         if (!in_range(a, c.num_seqs) || !in_range(b, c.num_seqs) || a == b ||
             load_agent(&c.owner[b]) != i || c.blocks[b] != 0 || c.lengths[b] != 0)
@@ -390,7 +436,8 @@ __global__ __launch_bounds__(CWG) void k_fork_plan(CacheView c, int n, const int
         const int pg = c.tables[(size_t)a * c.max_blocks + e.had - 1];
         e.src = pg >= 0 ? pg : c.num_pages;
         return 1;
-    });
+    };
+    grant(c, n, status, lds, ask, [](const CacheEntry &) {});
     unclaim(c, n, children);
 }
 

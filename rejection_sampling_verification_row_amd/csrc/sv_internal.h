@@ -254,14 +254,15 @@ struct CacheView {
     int *free_ids;       // [num_pages] each stretch's free pages, ascending, from the stretch's start
     int *free_count;     // [stretches] how many
     CacheEntry *entries; // [num_seqs] what a plan leaves for its apply
-    int *src, *dst;      // [num_pages] pages to copy, -1 none
+    int *src, *dst;      // [num_pages] pages to copy, -1 none; src: a reserve's replaced blocks
     int *map;            // [num_pages] a compaction's new page ids, or the pages a plan takes
     int *count;          // a compaction's moved pages, and its pages in use
 };
 
 // What an apply does for a list entry.
 struct CacheEntry {
-    int seq, from;       // the sequence (-1: nothing), and a fork's parent
+    int seq, from;       // the sequence (-1: nothing); a fork's parent, or the shared pages that a
+                         // reserve replaces
     int had, want;       // pages held and to be held
     int len;             // a fork's tokens
     int first;           // its place among the free pages taken
