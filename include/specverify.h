@@ -267,8 +267,7 @@ int specverify_quantile_cut(specverify_ctx *ctx, void *hip_stream, int P, int N,
  * comparisons differ by more than the rounding of the sums (V 2^-53 of a row's sum; with top-p on
  * float32 rows, whose sums over close logits are integers, about 2^-47 up to 2^15 ids and 2^-41 at
  * 2^20, at worst V/2 times that).  Integers are counted and added in any order, the rest in fixed
- * orders; which small terms of a draw's sums are passed over as cut away may differ from run to
- * run, and with it at most the grouping of the others, 2^-53 of a sum.
+ * orders: the same call gives the same bits.
  */
 typedef struct specverify_filter {
     const float *temperature;

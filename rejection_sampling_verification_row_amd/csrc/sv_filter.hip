@@ -465,7 +465,7 @@ struct CutLds {
     uint32_t xlist[HX];            // patterns outside the window as they were met
     uint32_t nx, zeros, low, bad;  // how many; zeros; largest order key <= -2^8; NaN or +inf met
     int last[3];                   // last place that top-k, top-p, min-p leave something of
-    uint32_t rth[FWAVES], top[FWAVES];  // per wave: a value that enough of its ids reach; its largest
+    uint32_t rth[2][FWAVES], top[2][FWAVES];  // per wave: a value that enough of its ids reach; its largest
     RowCut cut;
 };
 
@@ -475,8 +475,6 @@ __device__ __forceinline__ void cut_lds_clear(CutLds &c)
         c.nx = c.zeros = c.low = c.bad = 0;
         c.last[0] = c.last[1] = c.last[2] = -1;
     }
-    if (threadIdx.x < FWAVES)
-        c.rth[threadIdx.x] = c.top[threadIdx.x] = 0;
 }
 
 __device__ __forceinline__ void count_outside(uint32_t p, CutLds &c)
@@ -578,8 +576,8 @@ __device__ __forceinline__ uint32_t wave_scan_u32(uint32_t x)
 // in LDS the r-th largest of its lanes' maxima so far, r = ceil(k / waves): the waves' least is a
 // value that at least k ids reach.  Groups below it cost two instructions for a pair of logits, in
 // place of two LDS adds, and after the first part of a row nearly all are.  Only floors above zero
-// are used, where patterns compare as signed integers.  Notes of different age may be mixed: all
-// are lower bounds.
+// are used, where patterns compare as signed integers.  The waves wait for each other's notes, so
+// that what is counted and listed, and with it the grouping of every sum, is the same in each run.
 typedef short s16x2 __attribute__((ext_vector_type(2)));
 __device__ __forceinline__ s16x2 as_s16x2(uint32_t v) { return __builtin_bit_cast(s16x2, v); }
 __device__ __forceinline__ uint32_t max_i16(uint32_t a, uint32_t b)
@@ -615,30 +613,33 @@ struct Floor {
         top = max_i16(top, group_max(v));
         most = max_u16(most, max_u16(max_u16(v.x, v.y), max_u16(v.z, v.w)));
     }
-    // notes the wave's bounds
-    __device__ __forceinline__ void note(CutLds &c) const
+    // Notes the wave's bounds, and takes the floor from all waves' notes, in steps 0, 1, 3, 7, ... of
+    // the row: the later ones raise it little.  All waves of the workgroup come here in every step.
+    // Two sets of notes in turn: who writes one again has waited once more since it was read.
+    template <int NW> __device__ __forceinline__ void exchange(CutLds &c, int step)
     {
-        const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
-        const int a = (int)(short)(top & 0xffffu), b = (int)(short)(top >> 16), m = max(max(a, b), 0);
+        if ((step & (step + 1)) != 0)
+            return;
+        const int turn = __popc(step);
+        const int wv = threadIdx.x >> 6;
+        const int a = (int)(short)(top & 0xffffu), b = (int)(short)(top >> 16), best = max(max(a, b), 0);
         int t = 0, mx = 0;
 #pragma unroll
         for (int bit = 14; bit >= 0; --bit) {
             const int u = t | 1 << bit, w = mx | 1 << bit;
-            if (__popcll(__ballot(m >= u)) >= r)
+            if (__popcll(__ballot(best >= u)) >= r)
                 t = u;
-            if (__ballot(m >= w) != 0)
+            if (__ballot(best >= w) != 0)
                 mx = w;
         }
-        if (lane == 0) {
-            c.rth[wv] = (uint32_t)t;
-            c.top[wv] = (uint32_t)mx;
+        uint32_t *rth = c.rth[turn & 1], *tops = c.top[turn & 1];
+        if ((threadIdx.x & 63) == 0) {
+            rth[wv] = (uint32_t)t;
+            tops[wv] = (uint32_t)mx;
         }
-    }
-    template <int NW> __device__ __forceinline__ void update(const CutLds &c)
-    {
+        __syncthreads();
         const int lane = threadIdx.x & (NW - 1);
-        int k = (int)*(const volatile uint32_t *)&c.rth[lane];
-        int m = (int)*(const volatile uint32_t *)&c.top[lane];
+        int k = (int)rth[lane], m = (int)tops[lane];
         k = min(k, lane_xch<0>(k));
         m = max(m, lane_xch<0>(m));
         k = min(k, lane_xch<1>(k));
@@ -964,12 +965,7 @@ __device__ __forceinline__ void count_row(const Groups<1> &gr, Floor &fl, uint32
             });
         if (fl.active()) {
             unroll<0, U>([&](auto k) SV_INLINE { fl.see(v[k]); });
-            if ((i & (i + 1)) == 0) {
-                fl.note(c);
-                if (i == 0)
-                    __syncthreads();
-                fl.template update<NW>(c);
-            }
+            fl.template exchange<NW>(c, i);
         }
         if (full && fl.below == 0) {
             unroll<0, U>([&](auto k) SV_INLINE { count_vec(v[k], hist, c, low); });
@@ -1714,21 +1710,16 @@ __global__ __launch_bounds__(FWG, 4) void k_filter_sample_bf16(const char *logit
     __syncthreads();
     int listed = 0;
     uint32_t low = NO_LOW;
-    const int units = all.count();
-    if (fl.active() && units == 0)         // the other waves wait below
-        __syncthreads();
+    const int units = all.count(), trips = fl.active() ? gr.per_wave : units;
 #pragma nounroll
-    for (int i0 = 0; i0 < units; i0 += BATCH) {
+    for (int i0 = 0; i0 < trips; i0 += BATCH) {
         uint4 v[BATCH];
         unroll<0, BATCH>([&](auto j) SV_INLINE { v[j] = nx[j]; });
-        if (i0 + BATCH < units)
+        if (i0 + BATCH < trips)
             load_batch(all, i0 + BATCH, nx);
         if (fl.active()) {
             unroll<0, BATCH>([&](auto j) SV_INLINE { fl.see(v[j]); });
-            fl.note(c);
-            if (i0 == 0)
-                __syncthreads();
-            fl.update<FWAVES>(c);
+            fl.exchange<FWAVES>(c, i0 / BATCH);
         }
         if (fl.below == 0) {
             listed = LIST + 1;
@@ -2103,10 +2094,9 @@ __device__ __forceinline__ RowCut cut_floats(const Units<0> &all, Units<0> &few,
     uint32_t most = 0;             // as unsigned bits: a NaN of negative sign is above -inf
     uint32_t low = 0;              // finite logits <= -2^8
     int listed = 0;
-    if (fl.active() && units == 0)
-        __syncthreads();
+    const int trips = fl.active() ? all.gr.per_wave : units;
 #pragma nounroll
-    for (int i0 = 0; i0 < units; i0 += BATCH) {
+    for (int i0 = 0; i0 < trips; i0 += BATCH) {
         uint4 v[BATCH];
         uint2 h[BATCH];
         load_batch(all, i0, v);
@@ -2120,10 +2110,7 @@ __device__ __forceinline__ RowCut cut_floats(const Units<0> &all, Units<0> &few,
             unroll<0, BATCH / 2>([&](auto j) SV_INLINE {
                 fl.see(make_uint4(h[2 * j].x, h[2 * j].y, h[2 * j + 1].x, h[2 * j + 1].y));
             });
-            fl.note(c);
-            if (i0 == 0)
-                __syncthreads();
-            fl.update<FWAVES>(c);
+            fl.exchange<FWAVES>(c, i0 / BATCH);
         }
         uint32_t wait = 0;
         auto matters = [&](const uint2 &x) SV_INLINE {
