@@ -795,9 +795,12 @@ __device__ __forceinline__ void cut_from_counts(const uint32_t *hist, CutLds &c,
     } else if (c.nx >= HX || total == 0) {
         cut.state = CUT_EXACT;
     } else if (c.low) {
-        // the low values count if one of them could be kept with a weight that matters
+        // the low values count if one of them could be kept with a weight that matters; with p = 1
+        // none is that min-p leaves out, however few were counted above its floor
         const double w = weight(key_value(c.low), M, q.c);
-        if (w > 0.0 && (w >= 0x1p-80 || (q.k < V && q.k > (int)total) || (q.m > 0.0 && w >= q.m)))
+        const bool left_out = q.p >= 1.0 && w < q.m;
+        if (w > 0.0 && !left_out &&
+            (w >= 0x1p-80 || (q.k < V && q.k > (int)total) || (q.m > 0.0 && w >= q.m)))
             cut.state = CUT_EXACT;
     }
     if (cut.state != CUT_READY) {

@@ -5,7 +5,8 @@ import numpy as np
 import pytest
 
 import filter_model as model
-from test_gpu_filter import BF16, F32, as_dtype, check_sample, check_verify, ctx, rows  # noqa: F401
+from test_gpu_filter import (BF16, F32, PROB_RTOL, as_dtype, check_sample, check_verify, ctx,  # noqa: F401
+                             rows, run_sample)
 
 pytestmark = pytest.mark.gpu
 
@@ -87,3 +88,32 @@ def test_verify_a_block_of_ids_by_top_k_and_min_p(ctx, kind, dtype):
             q = model.law(dv[b, j], *(f[c][b] for c in "Tkpm"))[0]
             x[b, j] = r.choice(V, p=q / q.sum())
     check_verify(ctx, (tb, tv, db, dv, x, r.rand(B, K + 1).astype(np.float32)), dtype, f, f, same=True)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("low", [-257.0, -300.0, -700.0])
+def test_ids_masked_by_a_value_that_still_weighs_something(ctx, low, dtype):
+    """Fewer ids than top-k's above the mask, or above min-p's bound; the masked ones are kept where
+    top-k reaches them and min-p does not, and only there."""
+    r = np.random.RandomState(int(-low))
+    n, V = 48, 50257
+    x = np.full((n, V), low, np.float32)
+    for i in range(n):
+        at = r.choice(V, r.choice([5, 30, 400]), replace=False)
+        x[i, at] = rows(r, 1, len(at))[0]
+    q = cuts(r, n, [20, 50, 1000, 1025])
+    q["m"][:] = r.choice([0.0, 1e-20, 0.1], n)
+    q["T"][:] = r.choice([0.7, 1.5, 60.0], n)
+    u = r.rand(n).astype(np.float32)
+    bits, val = as_dtype(x, dtype)
+    tok, prob, mar = model.sample(val, u, q["T"], q["k"], q["p"], q["m"])
+    for i in np.flatnonzero(q["m"] == np.float32(1e-20)):
+        # the model's gap between a weight and m is absolute: here a relative one says how clear it is
+        v = val[i].astype(np.float64)
+        gap = np.abs(np.exp((v - v.max()) / float(q["T"][i])) / float(q["m"][i]) - 1).min()
+        mar[i] = min(gap, model.draw(model.law(val[i], q["T"][i], int(q["k"][i]), 1.0, q["m"][i])[0], u[i])[1])
+    clear = mar > model.CLEAR
+    assert clear.mean() > 0.9
+    g, gp = run_sample(ctx, bits, dtype, q, u)
+    assert np.array_equal(g[clear], tok[clear]), (np.flatnonzero(g != tok), g, tok)
+    np.testing.assert_allclose(gp[clear], prob[clear], rtol=PROB_RTOL, atol=2.0 ** -149)
