@@ -1001,7 +1001,7 @@ constexpr int RWG = 512;   // threads per row of a bfloat16 verify: four workgro
 // compute unit, so that one counts while another is at its cut's barriers: 4352 rows of 128256
 // (1.12 GB) take 171 us, 6.5 TB/s, where a bare streaming read of the same layout takes 161-164.
 // Counting is seven VALU instructions and two LDS adds for two logits: in those 171 us a SIMD issues
-// 65 thousand VALU instructions (260 thousand clocks) and a compute unit's LDS works for 116
+// 63 thousand VALU instructions (250 thousand clocks) and a compute unit's LDS works for 112
 // thousand, so that the reads hide both, but not by much.
 __global__ __launch_bounds__(RWG, 8) void k_filter_rows_bf16(const char *tgt, const char *drf, int B,
                                                              int K, int V, FilterPtrs ft,
@@ -1680,12 +1680,14 @@ __device__ __forceinline__ void fill_table(const RowCut &r, double scale, double
     }
 }
 
-// One row: its cut by counting, then the draw.  256 rows of 128256 with mixed parameters take 43 us,
-// the time of a row that keeps everything: 10 us to read and count it (the rate of HBM), 5 for the
-// cut (barriers and scans, one after the other), 12 for a second reading through the table (an
-// 8-byte LDS lookup per logit, 12 clocks for a wave's, is what bounds it) and 4 to find the id.
-// Rows cut by top-k or min-p list the groups that can matter while they count, and need 26 us.
-// One row of 32000: 14 us, all of it latency.
+// One row: its cut by counting, then the draw.  256 rows of 128256 take 35 us without a cut, 27 with
+// top-k or min-p, 47 with top-p and 43 with mixed parameters.  A workgroup's phases in us, the logits
+// from the last-level cache: without a cut 7 to count, 7 for the cut (barriers and scans, one after
+// the other), 13 for the sums, a second reading through the table (an 8-byte LDS lookup per logit,
+// 12 clocks for a wave's, is what bounds it), 3 to find the id.  The slowest rows of the mixed batch
+// are cut by top-p inside a run of equals and have no list: 6, 9, then 9 to find the last kept of
+// the equals (a reading of its own), 13 and 3.  Rows cut by top-k or min-p list the groups that can
+// matter while they count: 12, 5, up to 3, 2 and 2.  One row of 32000: 14 us, all of it latency.
 __global__ __launch_bounds__(FWG, 4) void k_filter_sample_bf16(const char *logits, int V,
                                                                int64_t stride, FilterPtrs f,
                                                                const float *unif, int *tok,
@@ -1772,8 +1774,9 @@ __global__ __launch_bounds__(FWG, 4) void k_filter_sample_bf16(const char *logit
 // LDS, as integers so that their order does not matter, in units of 2^-47 (for vocabularies past
 // 2^15 coarser, 2^-41 at 2^20) of the weight at the bin's upper edge.  Half a unit is lost per logit
 // at most, so V halves of a unit of a row's sum at worst: 2^-33 up to 2^15 ids, 2^-28 at 2^17.  The
-// errors of a row's logits have no sign in common, which leaves about one unit.  A bin of more than GATHER logits is counted once more by its next 13 bits.
-// A row in which even that leaves more, GATHER equal logits at its cut, goes to cut_by_bisection.
+// errors of a row's logits have no sign in common, which leaves about one unit.  A bin of more than
+// GATHER logits is counted once more by its next 13 bits.  A row in which even that leaves more,
+// GATHER equal logits at its cut, goes to cut_by_bisection.
 
 constexpr int BIN_HIGH = HBINS, BIN_ZERO = HBINS + 1, BIN_LOW = HBINS + 2, FBINS = HBINS + 3;
 constexpr int GATHER = 1024;
@@ -2354,9 +2357,10 @@ __device__ __forceinline__ double row_total(const Units<DT> &un, const MayKeep<D
     return block_sum(s, red.d);
 }
 
-// One row.  64 rows of 32000 with top-p alone, which skips nothing, take 48 us: counting 5, the
-// weights' pass 12 (fp64 issue), the goal's bin 3, gathering and ordering its logits 7, the draw 5,
-// and the waves' waits for each other.  With top-k 21 us.
+// One row.  64 rows of 32000 with top-p alone, which skips nothing, take 48 us, the time of the
+// slowest.  Its workgroup's phases in us: counting 3, the maximum 2, the weights' pass 13 (fp64
+// issue), the goal's bin 4, gathering and ordering its logits 9 (half of that in a median row), the
+// cut 2, the draw's sums 9 and its search 3.  With top-k 21 us.
 __global__ __launch_bounds__(FWG, 4) void k_filter_sample_f32(const char *logits, int V,
                                                               int64_t stride, FilterPtrs f,
                                                               const float *unif, int *tok,
@@ -2391,7 +2395,7 @@ __global__ __launch_bounds__(FWG, 4) void k_filter_sample_f32(const char *logits
 
 // The RowCut of every target and draft row of a float32 verify: the B (K+1) target rows, then the
 // B K draft rows.  The counts, weights and lists take 131 KB of LDS, so a compute unit holds one
-// workgroup and a row's phases wait for each other: 704 rows of 32000 with top-k take 52 us, three
+// workgroup and a row's phases wait for each other: 704 rows of 32000 with top-k take 51 us, three
 // rounds of 17, where the bytes need 13.
 __global__ __launch_bounds__(FWG, 4) void k_filter_rows_f32(const char *tgt, const char *drf, int B,
                                                             int K, int V, FilterPtrs ft,
@@ -2433,10 +2437,12 @@ struct VerifyLds {
 };
 
 // Accept tests, first rejection and the replacement or bonus draw of one sequence.  256 sequences of
-// 128256 in bfloat16 take 60 us: 5 for the tests, 2 for the tables, then 16 (two lookups per id,
-// as in the sampler) where p keeps much, or 13 to list p's few groups and 3 to draw from them, and
-// 3 to 6 to find the id.  A chip has as many workgroups in flight as sequences, so a batch waits
-// for its slowest.
+// 128256 in bfloat16 take 60 us with mixed parameters, since a chip has as many workgroups in flight
+// as sequences and a batch waits for its slowest.  Phases in us of such a one, whose p keeps much and
+// whose cuts fall inside runs of equals: 4 for the tests (a draft id equal to a partly kept cut adds a
+// reading of its row), 2 for the tables, 19 to find the last kept equals of both rows, 27 for the
+// sums of p - q (two lookups per id, as in the sampler), 6 to find the id.  The median sequence, whose
+// p keeps few: 4, 2, 11 to list p's groups, 4 and 3.
 template <int DT>
 __global__ __launch_bounds__(FWG, 4) void k_filter_verify(const char *tgt, const char *drf, int B,
                                                           int K, int V, FilterPtrs ft, FilterPtrs fd,
