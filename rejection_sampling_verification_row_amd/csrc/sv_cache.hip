@@ -13,7 +13,7 @@
 //
 // The calls read and write little but for the copies, so they are bound by launches and by trips to
 // memory in a row: a reserve and a commit of 512 sequences in a pool of 65536 pages take 4.6 us to
-// list the free pages, 6.8 to plan, 3.7 to apply and 3.6 to commit.  Copies run at the rate of a
+// list the free pages, 6.8 to plan, 3.7 to apply and 3.4 to commit.  Copies run at the rate of a
 // large copy: a compaction that moves 696 pages of 8 x 32 KiB, 365 MB read and written by the
 // counters, takes 69 us (5.3 TB/s); 2000 such pages copied, 1.05 GB, 203 us (5.2 TB/s); a fork of 480
 // children, whose few sources stay in the caches, writes 67 MB in 13 us.

@@ -613,14 +613,16 @@ struct Floor {
         top = max_i16(top, group_max(v));
         most = max_u16(most, max_u16(max_u16(v.x, v.y), max_u16(v.z, v.w)));
     }
-    // Notes the wave's bounds, and takes the floor from all waves' notes, in steps 0, 1, 3, 7, ... of
-    // the row: the later ones raise it little.  All waves of the workgroup come here in every step.
-    // Two sets of notes in turn: who writes one again has waited once more since it was read.
+    // Notes the wave's bounds, and takes the floor from all waves' notes, in steps 0, 3, 15 and 63 of
+    // the row: more of them raise it little and make the waves wait (in steps 0, 1, 3, 7, ... a verify
+    // B=64 K=5 V=32000 in float32 takes 68.4 us, so 65.3; B=17 K=3 V=50257 in bfloat16 44.8 and 43.5).
+    // All waves of the workgroup come here in every step.  Two sets of notes in turn: who writes one
+    // again has waited once more since it was read.
     template <int NW> __device__ __forceinline__ void exchange(CutLds &c, int step)
     {
-        if ((step & (step + 1)) != 0)
+        if ((step & (step + 1)) != 0 || (__popc(step) & 1) != 0)
             return;
-        const int turn = __popc(step);
+        const int turn = __popc(step) / 2;
         const int wv = threadIdx.x >> 6;
         const int a = (int)(short)(top & 0xffffu), b = (int)(short)(top >> 16), best = max(max(a, b), 0);
         int t = 0, mx = 0;
@@ -999,9 +1001,9 @@ constexpr int RWG = 512;   // threads per row of a bfloat16 verify: four workgro
 
 // The RowCut of every target and draft row of a bfloat16 verify.  Four workgroups of 35 KB to a
 // compute unit, so that one counts while another is at its cut's barriers: 4352 rows of 128256
-// (1.12 GB) take 171 us, 6.5 TB/s, where a bare streaming read of the same layout takes 161-164.
-// Counting is seven VALU instructions and two LDS adds for two logits: in those 171 us a SIMD issues
-// 63 thousand VALU instructions (250 thousand clocks) and a compute unit's LDS works for 112
+// (1.12 GB) take 170 us, 6.6 TB/s, where a bare streaming read of the same layout takes 161-164.
+// Counting is seven VALU instructions and two LDS adds for two logits: in those 170 us a SIMD issues
+// 62 thousand VALU instructions (246 thousand clocks) and a compute unit's LDS works for 113
 // thousand, so that the reads hide both, but not by much.
 __global__ __launch_bounds__(RWG, 8) void k_filter_rows_bf16(const char *tgt, const char *drf, int B,
                                                              int K, int V, FilterPtrs ft,
@@ -2395,8 +2397,8 @@ __global__ __launch_bounds__(FWG, 4) void k_filter_sample_f32(const char *logits
 
 // The RowCut of every target and draft row of a float32 verify: the B (K+1) target rows, then the
 // B K draft rows.  The counts, weights and lists take 131 KB of LDS, so a compute unit holds one
-// workgroup and a row's phases wait for each other: 704 rows of 32000 with top-k take 51 us, three
-// rounds of 17, where the bytes need 13.
+// workgroup and a row's phases wait for each other: 704 rows of 32000 with top-k take 48 us, three
+// rounds of 16, where the bytes need 13.
 __global__ __launch_bounds__(FWG, 4) void k_filter_rows_f32(const char *tgt, const char *drf, int B,
                                                             int K, int V, FilterPtrs ft,
                                                             FilterPtrs fd, RowCut *cuts)
