@@ -12,8 +12,8 @@
  *    (output distribution identical to the target's), which fixes the replacement law
  *    as the normalised residual max(0, p - q); the bonus token after K acceptances is
  *    the gamma+1 draw of the "Speculative Contrastive Decoding" review, SCD section.
- *  - Greedy blockwise verify (also with early exit): "Blockwise Parallel Decoding", section
- *    3.5 (Verify and Accept: longest prefix on which the target's argmax equals the proposals).
+ *  - Greedy blockwise verify (also with early exit, or of a drafted tree): "Blockwise Parallel
+ *    Decoding", section 3.5 (Verify and Accept: longest prefix on which the target's argmax equals the proposals).
  *  - Contrastive-target verify: "Speculative Contrastive Decoding" review, sections on
  *    contrastive decoding (large-model minus small-model distribution) and SCD.
  *  - Draft-token sampler: "推测性拒绝采样", step 1 (the draft model proposes its tokens one
@@ -193,6 +193,28 @@ int specverify_run_greedy_early_exit(specverify_ctx *ctx, void *hip_stream, int 
                                      int K, int V, const void *target_logits,
                                      const int32_t *proposals, int32_t *accepted_len,
                                      int32_t *out_tokens);
+
+/*
+ * Greedy verify of a drafted tree: specverify_run_greedy where several continuations are drafted.
+ * T nodes per sequence: node 0 is the token fed before the drafts, node i >= 1 a draft tokens[b][i]
+ * that follows node parents[b][i] < i; counts[b] (or NULL: T) of them are there.  target_logits
+ * [B][T][V] (dtype): row i scores the token after node i.  With g_i the lowest id among the maxima of
+ * row i, the walk starts at node 0 and goes on from node i to its lowest child c with tokens[b][c] ==
+ * g_i, over at most `depth` drafts.
+ * Outputs: accepted_len [B] = L, the drafts on the walk; path [B][depth+1] = its nodes n_0 = 0, n_1,
+ * ..., n_L, then -1; out_tokens [B][depth+1] = g of each (g_(n_L) is the emitted token after the
+ * accepted drafts), then -1.  A sequence with a count outside [1, T], or a node with an id outside
+ * [0, V) or a parent that is not below it, gets accepted_len -1 and all -1; what stands at node 0 is
+ * not read.  A chain (parents i - 1, depth T - 1) gives specverify_run_greedy's results.
+ * Rows off the walk need not be read: where reading all of them takes longer, the rows are read
+ * depth by depth, one a sequence.
+ * Errors as specverify_run_greedy, EINVAL also for T < 1, depth < 0 or depth >= T; T - 1 is limited
+ * by the context's max_k.
+ */
+int specverify_run_greedy_tree(specverify_ctx *ctx, void *hip_stream, int dtype, int B, int T, int V,
+                               int depth, const void *target_logits, const int32_t *tokens,
+                               const int32_t *parents, const int32_t *counts, int32_t *accepted_len,
+                               int32_t *path, int32_t *out_tokens);
 
 /*
  * Contrastive-target verify: as specverify_run_sampling with the target law
@@ -410,6 +432,126 @@ int specverify_cache_compact(specverify_cache *cache, void *hip_stream, int32_t 
  */
 int specverify_cache_copy(specverify_cache *cache, void *hip_stream, int n, const int32_t *src,
                           const int32_t *dst, int32_t *status);
+
+/*
+ * Move the accepted path of a drafted tree to the places right after the cached tokens: with L =
+ * accepted_len[i] and l = lengths[seqs[i]], the token at place l + path[i][j] of the sequence goes to
+ * place l + j for j = 1..L, in every pool; what stood there is lost, lengths and pages stay.  A
+ * specverify_cache_commit with the same accepted_len then keeps the path and releases the rest.
+ * path [n][max_count] is what specverify_run_greedy_tree wrote (max_count = depth + 1): ascending,
+ * path[i][0] = 0; entries past L are not read.  accepted_len -1 moves nothing.
+ * A token's bytes are page_bytes / page_tokens in a row.  The places' pages have to be the sequence's
+ * own, as after a reserve; a token whose page is out of range is not moved.
+ * Refused besides (status): accepted_len outside [-1, max_count), a path that does not start at 0
+ * and ascend, or places past the pages held.
+ * Errors: those of the other calls, EINVAL also for max_count < 1 or page_bytes not a multiple of
+ * page_tokens, ECAPACITY for max_count > SPECVERIFY_MAX_NODES.
+ */
+int specverify_cache_keep_path(specverify_cache *cache, void *hip_stream, int n, int max_count,
+                               const int32_t *seqs, const int32_t *accepted_len,
+                               const int32_t *path, int32_t *status);
+
+/*
+ * Attention over a cache.  A handle says how two pools of a cache hold keys and values: of each
+ * token kv_heads rows of head_dim elements of `dtype`, head after head, so that page_bytes is
+ * page_tokens * kv_heads * head_dim elements.  Query head h reads key head h / (q_heads / kv_heads).
+ *
+ * A step's tokens (nodes) are rows of the inputs.  Entry i is sequence s = seqs[i] with counts[i]
+ * nodes, node t in row starts[i] + t.  Node t's place in the sequence is lengths[s] + t, so that
+ * room for counts[i] tokens has to be reserved before.  Its parent is node parents[starts[i] + t],
+ * below t; node 0 (the token fed before the drafts) is the root, its parent is not read; without
+ * `parents` node t's parent is node t - 1.  Its position is lengths[s] + its depth, the root's 0.
+ * NULL arrays: seqs 0..n-1, starts i * max_count, counts max_count.
+ *
+ * Conventions are those of the cache's calls.  Only `status` says that an entry was refused (-1):
+ * a sequence outside [0, num_seqs), blocks and lengths that contradict each other, a count outside
+ * [0, max_count], rows outside [0, rows), places past the pages held, a parent that is not below its
+ * child; an append refuses a sequence that an earlier entry names too.  A refused entry's rows and
+ * places, and rows that no entry has, stay as they were.  Entries' rows must not overlap in what is
+ * written.  Strides are in elements from row to row, heads lie side by side; any alignment to the
+ * element size will do.
+ * Errors: EINVAL (NULL handle or required array, negative sizes, a pool outside the cache's, a
+ * stride below a row's elements or too large for 63-bit byte offsets, misaligned pointers),
+ * ECAPACITY (n above the handle's max_entries, for an append above the cache's num_seqs; max_count
+ * above max_nodes, for an append with `parents` above SPECVERIFY_MAX_NODES; more workgroups than a
+ * launch holds), EHIP.
+ */
+typedef struct specverify_attn specverify_attn;
+
+typedef struct specverify_nodes {
+    const int32_t *seqs;
+    const int32_t *starts;
+    const int32_t *counts;
+    const int32_t *parents;
+} specverify_nodes;
+
+/* Most nodes of a tree, and most tokens of an entry of specverify_attn_attend. */
+#define SPECVERIFY_MAX_NODES 64
+#define SPECVERIFY_MAX_HEAD_DIM 256
+#define SPECVERIFY_MAX_ENTRIES (1 << 16)
+
+/*
+ * Create a handle for attention over `cache`, which has to live while calls are made.  Allocates the
+ * handle's workspace on the cache's device (what parts of a sequence leave for their joining: at
+ * most some tens of MB) and synchronises it.
+ * Errors: EINVAL (NULL pointers, sizes < 1, q_heads not a multiple of kv_heads, head_dim elements
+ * not a multiple of 16 bytes, page_bytes other than said above), EUNSUPPORTED (dtype), ECAPACITY
+ * (head_dim, max_nodes or max_entries above the limits, q_heads above 2^16), EHIP, ENOMEM.
+ */
+int specverify_attn_create(specverify_attn **out, const specverify_cache *cache, int dtype,
+                           int q_heads, int kv_heads, int head_dim, int max_entries, int max_nodes);
+
+/* Bytes of device workspace the handle holds. */
+int64_t specverify_attn_workspace_bytes(const specverify_attn *attn);
+
+/* Release the handle and its workspace.  NULL-safe. */
+int specverify_attn_destroy(specverify_attn *attn);
+
+/*
+ * The rotation of positions: the first `dims` elements of a head (even, 0: none) are dims / 2 pairs,
+ * pair i being elements (i, i + dims / 2), or (2i, 2i + 1) when `interleaved`; (a, b) becomes
+ * (a cos f - b sin f, b cos f + a sin f) with f = position * inv_freq[i], formed and reduced in fp64.
+ * inv_freq [dims / 2] lies on the device.
+ */
+typedef struct specverify_rotation {
+    const float *inv_freq;
+    int dims;
+    int interleaved;
+} specverify_rotation;
+
+/*
+ * Write the nodes' keys and values to their places, a prompt's tokens likewise (a chain of any
+ * length): keys [rows][kv_heads][head_dim] rotated into pool key_pool, values as they are into pool
+ * value_pool.  queries (or NULL) [rows][q_heads][head_dim] are rotated into `rotated`, which may be
+ * the queries themselves, with the same stride.  rotation NULL rotates nothing.  Lengths stay: a
+ * commit moves them.
+ * Arithmetic in fp32, one rounding at the end.  The places' pages have to be the sequence's own, as
+ * after a reserve; a token whose page is out of range is not written.
+ */
+int specverify_attn_append(specverify_attn *attn, void *hip_stream, int key_pool, int value_pool,
+                           int n, int max_count, int rows, const specverify_nodes *nodes,
+                           const specverify_rotation *rotation, const void *keys,
+                           int64_t key_stride, const void *values, int64_t value_stride,
+                           const void *queries, int64_t query_stride, void *rotated,
+                           int64_t rotated_stride, int32_t *status);
+
+/*
+ * Attention of the nodes over the cached tokens of their sequence, their ancestors and themselves,
+ * whose keys and values have to be in place: with s_j = scale * <q, k_j> over the tokens seen,
+ * out = sum_j exp(s_j) v_j / sum_j exp(s_j) and lse (or NULL) [rows][q_heads] = log sum_j exp(s_j).
+ * window > 0: a token is seen only from positions less than `window` after its own.  Tokens whose
+ * page is out of range are not seen; a row that sees nothing, or nothing above -inf, gets zeros and
+ * -inf.  What a row does not see does not touch it, whatever its values.
+ * queries, out: [rows][q_heads][head_dim].  Scores, maxima and sums are fp32; for bfloat16 the
+ * weights exp(s_j - max) are rounded to bfloat16 for the product with the values (their sum is
+ * not), and the result once more at the end.  The order of the sums depends on the call's lengths
+ * only: the same call gives the same bits.
+ * EINVAL also for a scale that is not finite, window < 0.
+ */
+int specverify_attn_attend(specverify_attn *attn, void *hip_stream, int key_pool, int value_pool,
+                           int n, int max_count, int rows, const specverify_nodes *nodes,
+                           float scale, int window, const void *queries, int64_t query_stride,
+                           void *out, int64_t out_stride, float *lse, int32_t *status);
 
 /*
  * Test hook: flags that force draw paths which data rarely reaches, so that tests can compare

@@ -34,6 +34,9 @@ SPECVERIFY_MAX_SEQS = 1 << 20
 SPECVERIFY_MAX_BLOCKS = 1 << 20
 SPECVERIFY_MAX_POOLS = 1 << 16
 SPECVERIFY_MAX_PAGE_BYTES = 1 << 30
+SPECVERIFY_MAX_NODES = 64
+SPECVERIFY_MAX_HEAD_DIM = 256
+SPECVERIFY_MAX_ENTRIES = 1 << 16
 SPECVERIFY_TEST_CHUNK_FALLBACK = 1
 SPECVERIFY_TEST_EXACT_TWO_PASS = 2
 KERNEL_NAMES = ("row_stats", "accept_draw", "row_argmax", "greedy_emit", "quantile_cut",
@@ -56,6 +59,34 @@ class SpecVerifyFilter(ctypes.Structure):
         """The tensors' types and sizes against a call of `count` rows or sequences."""
         for name, t in self.tensors.items():
             _arr(t, count, "i32" if name == "top_k" else "f32", name)
+
+
+class SpecVerifyNodes(ctypes.Structure):
+    """A step's nodes: device tensors (or addresses), None for what the library fills in (see the
+    header).  The tensors are held for as long as the structure lives."""
+    _fields_ = [(name, ctypes.c_void_p) for name in ("seqs", "starts", "counts", "parents")]
+
+    def __init__(self, seqs=None, starts=None, counts=None, parents=None):
+        self.tensors = {"seqs": seqs, "starts": starts, "counts": counts, "parents": parents}
+        self.checked = None
+        super().__init__(*(_ptr(t) for t in self.tensors.values()))
+
+    def check(self, n: int, rows: int):
+        """The tensors' types and sizes against a call of n entries and `rows` rows."""
+        if self.checked != (n, rows):
+            for name, t in self.tensors.items():
+                _arr(t, rows if name == "parents" else n, "i32", name)
+            self.checked = (n, rows)
+
+
+class SpecVerifyRotation(ctypes.Structure):
+    """The rotation of positions: inv_freq [dims / 2] float32 on the device, held while this lives."""
+    _fields_ = [("inv_freq", ctypes.c_void_p), ("dims", ctypes.c_int), ("interleaved", ctypes.c_int)]
+
+    def __init__(self, inv_freq, dims, interleaved=False):
+        _arr(inv_freq, dims // 2, "f32", "inv_freq")
+        self.tensor = inv_freq
+        super().__init__(_ptr(inv_freq), dims, int(bool(interleaved)))
 
 
 class SpecVerifyError(RuntimeError):
@@ -126,6 +157,17 @@ def load():
         lib.specverify_cache_free.argtypes = [vp, vp, i, vp, vp]
         lib.specverify_cache_compact.argtypes = [vp, vp, vp, vp]
         lib.specverify_cache_copy.argtypes = [vp, vp, i, vp, vp, vp]
+        lib.specverify_run_greedy_tree.argtypes = [vp, vp, i, i, i, i, i, vp, vp, vp, vp, vp, vp, vp]
+        lib.specverify_cache_keep_path.argtypes = [vp, vp, i, i, vp, vp, vp, vp]
+        nodes, rotation = ctypes.POINTER(SpecVerifyNodes), ctypes.POINTER(SpecVerifyRotation)
+        lib.specverify_attn_create.argtypes = [ctypes.POINTER(vp), vp, i, i, i, i, i, i]
+        lib.specverify_attn_workspace_bytes.argtypes = [vp]
+        lib.specverify_attn_workspace_bytes.restype = i64
+        lib.specverify_attn_destroy.argtypes = [vp]
+        lib.specverify_attn_append.argtypes = [vp, vp, i, i, i, i, i, nodes, rotation, vp, i64, vp, i64,
+                                               vp, i64, vp, i64, vp]
+        lib.specverify_attn_attend.argtypes = [vp, vp, i, i, i, i, i, nodes, f, i, vp, i64, vp, i64, vp,
+                                               vp]
         lib.specverify_set_test_flags.argtypes = [vp, ctypes.c_uint]
         lib.specverify_set_test_flags.restype = i
         lib.specverify_destroy.argtypes = [vp]
@@ -444,6 +486,101 @@ def specverify_cache_compact(cache, stream, page_map=None, num_used=None) -> Non
 def specverify_cache_copy(cache, stream, n, src, dst, status=None) -> None:
     _cache_call("specverify_cache_copy", cache, stream, n, (src, n, "i32", "src"),
                 (dst, n, "i32", "dst"), (status, n, "i32", "status"))
+
+
+def specverify_run_greedy_tree(ctx, stream, dtype, B, T, V, depth, target_logits, tokens, parents,
+                               counts, accepted_len, path, out_tokens) -> None:
+    _check(load().specverify_run_greedy_tree(
+        ctx, _stream(stream), dtype, B, T, V, depth,
+        *_ptrs((target_logits, B * T * V, dtype, "target_logits"), (tokens, B * T, "i32", "tokens"),
+               (parents, B * T, "i32", "parents"), (counts, B, "i32", "counts"),
+               (accepted_len, B, "i32", "accepted_len"), (path, B * (depth + 1), "i32", "path"),
+               (out_tokens, B * (depth + 1), "i32", "out_tokens"))), "specverify_run_greedy_tree")
+
+
+def specverify_cache_keep_path(cache, stream, n, max_count, seqs, accepted_len, path,
+                               status=None) -> None:
+    _check(load().specverify_cache_keep_path(
+        cache, _stream(stream), n, max_count,
+        *_ptrs((seqs, n, "i32", "seqs"), (accepted_len, n, "i32", "accepted_len"),
+               (path, n * max_count, "i32", "path"), (status, n, "i32", "status"))),
+        "specverify_cache_keep_path")
+
+
+_attn_shapes = {}       # handle -> (dtype, query row elements, key row elements, query heads)
+
+
+def specverify_attn_create(cache, dtype, q_heads, kv_heads, head_dim, max_entries, max_nodes) -> int:
+    """Returns the handle (an int).  The cache has to live while calls are made."""
+    h = ctypes.c_void_p()
+    _check(load().specverify_attn_create(ctypes.byref(h), cache, dtype, q_heads, kv_heads, head_dim,
+                                         max_entries, max_nodes), "specverify_attn_create")
+    _attn_shapes[h.value] = (dtype, q_heads * head_dim, kv_heads * head_dim, q_heads)
+    return h.value
+
+
+def specverify_attn_workspace_bytes(attn: int) -> int:
+    return int(load().specverify_attn_workspace_bytes(attn))
+
+
+def specverify_attn_destroy(attn) -> None:
+    _attn_shapes.pop(attn, None)
+    _check(load().specverify_attn_destroy(attn), "specverify_attn_destroy")
+
+
+def _rows(x, dtype, rows, width, stride, name):
+    """The pointer of a row array: `rows` rows of `width` elements, `stride` apart.  A tensor is
+    contiguous, or its first dimension has that stride and the others lie side by side."""
+    if x is None or isinstance(x, int) or not hasattr(x, "data_ptr"):
+        return _ptr(x)
+    if x.is_contiguous():
+        _arr(x, (rows - 1) * stride + width if rows > 0 else 0, dtype, name)
+        return _ptr(x)
+    _arr(x, 0, dtype, name)
+    beside = 1
+    for size, step in zip(x.shape[:0:-1], x.stride()[:0:-1]):
+        if size != 1 and step != beside:
+            raise ValueError("%s: the elements of a row have to lie side by side" % name)
+        beside *= size
+    if x.dim() < 2 or x.shape[0] < rows or beside < width or (rows > 1 and x.stride(0) != stride):
+        raise ValueError("%s: expected %d rows of %d elements, %d apart, got %s with strides %s"
+                         % (name, rows, width, stride, tuple(x.shape), x.stride()))
+    if not x.is_cuda:
+        raise ValueError("expected a device tensor, got one on %s" % x.device)
+    return x.data_ptr()
+
+
+def _nodes(nodes, n, rows):
+    if nodes is None:
+        return None
+    nodes.check(n, rows)
+    return ctypes.byref(nodes)
+
+
+def specverify_attn_append(attn, stream, key_pool, value_pool, n, max_count, rows, nodes, rotation,
+                           keys, key_stride, values, value_stride, queries=None, query_stride=0,
+                           rotated=None, rotated_stride=0, status=None) -> None:
+    dtype, q, kv, _ = _attn_shapes.get(attn, (0, 0, 0, 0))
+    _arr(status, n, "i32", "status")
+    _check(load().specverify_attn_append(
+        attn, _stream(stream), key_pool, value_pool, n, max_count, rows, _nodes(nodes, n, rows),
+        None if rotation is None else ctypes.byref(rotation),
+        _rows(keys, dtype, rows, kv, key_stride, "keys"), key_stride,
+        _rows(values, dtype, rows, kv, value_stride, "values"), value_stride,
+        _rows(queries, dtype, rows, q, query_stride, "queries"), query_stride,
+        _rows(rotated, dtype, rows, q, rotated_stride, "rotated"), rotated_stride, _ptr(status)),
+        "specverify_attn_append")
+
+
+def specverify_attn_attend(attn, stream, key_pool, value_pool, n, max_count, rows, nodes, scale, window,
+                           queries, query_stride, out, out_stride, lse=None, status=None) -> None:
+    dtype, q, _, heads = _attn_shapes.get(attn, (0, 0, 0, 0))
+    lse, status = _ptrs((lse, rows * heads, "f32", "lse"), (status, n, "i32", "status"))
+    _check(load().specverify_attn_attend(
+        attn, _stream(stream), key_pool, value_pool, n, max_count, rows, _nodes(nodes, n, rows),
+        scale, window, _rows(queries, dtype, rows, q, query_stride, "queries"), query_stride,
+        _rows(out, dtype, rows, q, out_stride, "out"), out_stride, lse, status),
+        "specverify_attn_attend")
 
 
 def specverify_set_test_flags(ctx, flags: int) -> None:

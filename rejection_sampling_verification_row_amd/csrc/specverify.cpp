@@ -37,6 +37,15 @@ struct specverify_cache {
     sv::CacheView view;
 };
 
+struct specverify_attn {
+    int device;                           // the cache's, and its view: either handle may go first
+    sv::CacheView view;
+    int max_entries, max_nodes;
+    void *mem;
+    size_t bytes;
+    sv::AttnShape shape;
+};
+
 namespace {
 
 constexpr int NK = SPECVERIFY_NUM_KERNELS;
@@ -45,6 +54,10 @@ static_assert(SPECVERIFY_MAX_CUT_N == sv::MAX_CUT_N, "cut capacity out of step w
 static_assert(SPECVERIFY_MAX_VOCAB == sv::MAX_VOCAB, "vocabulary cap out of step with the header");
 static_assert(SPECVERIFY_STATIC_SCRATCH_BYTES == sv::STATIC_SCRATCH_BYTES,
               "scratch size out of step with the header");
+static_assert(SPECVERIFY_MAX_NODES == sv::MAX_NODES && SPECVERIFY_MAX_NODES == SPECVERIFY_MAX_K + 1 &&
+                  SPECVERIFY_MAX_HEAD_DIM == sv::ATTN_MAX_HEAD_DIM &&
+                  SPECVERIFY_MAX_ENTRIES == sv::ATTN_MAX_ENTRIES,
+              "attention limits out of step with the header");
 static_assert(SPECVERIFY_TEST_CHUNK_FALLBACK == sv::TEST_CHUNK_FALLBACK &&
                   SPECVERIFY_TEST_EXACT_TWO_PASS == sv::TEST_EXACT_TWO_PASS,
               "test flags out of step with the header");
@@ -200,12 +213,38 @@ int cache_check(const specverify_cache *cache, int n, int most)
     return n == 0 ? 1 : SPECVERIFY_OK;
 }
 
-template <typename F> int cache_launch(const specverify_cache *cache, F f)
+template <typename H, typename F> int cache_launch(const H *handle, F f)
 {
-    DeviceGuard g(cache->device);
+    DeviceGuard g(handle->device);
     if (g.err != hipSuccess)
         return SPECVERIFY_EHIP;
     return f() == hipSuccess ? SPECVERIFY_OK : SPECVERIFY_EHIP;
+}
+
+// A step's nodes as a call gives them; false when a pointer is misaligned.
+bool nodes_view(const specverify_nodes *nodes, int n, int max_count, int rows, sv::NodesView *v)
+{
+    *v = {n, max_count, rows, nullptr, nullptr, nullptr, nullptr};
+    if (nodes) {
+        v->seqs = nodes->seqs;
+        v->starts = nodes->starts;
+        v->counts = nodes->counts;
+        v->parents = nodes->parents;
+    }
+    return aligned_to(v->seqs, 4) && aligned_to(v->starts, 4) && aligned_to(v->counts, 4) &&
+           aligned_to(v->parents, 4);
+}
+
+// A row array: elements from row to row, at least `least` of them, so that every byte offset fits.
+bool bad_rows(const void *p, int64_t stride, int64_t least, int rows, size_t es)
+{
+    return !p || !aligned_to(p, es) || stride < least || stride > INT64_MAX / 8 / ((int64_t)rows + 1);
+}
+
+bool bad_pools(const specverify_attn *attn, int key_pool, int value_pool)
+{
+    const int n = attn->view.num_pools;
+    return key_pool < 0 || key_pool >= n || value_pool < 0 || value_pool >= n;
 }
 
 }  // namespace
@@ -366,6 +405,35 @@ int specverify_run_sampling_static(void *hip_stream, int dtype, int B, int K, in
     const hipError_t e = sv::launch_sampling(ln, ws, sv::SAMPLING, dtype, B, K, V, sc, sc,
                                              target_logits, draft_logits, draft_tokens, uniforms,
                                              accepted_len, out_tokens, out_probs, nullptr);
+    return e == hipSuccess ? SPECVERIFY_OK : SPECVERIFY_EHIP;
+}
+
+int specverify_run_greedy_tree(specverify_ctx *ctx, void *hip_stream, int dtype, int B, int T, int V,
+                               int depth, const void *target_logits, const int32_t *tokens,
+                               const int32_t *parents, const int32_t *counts, int32_t *accepted_len,
+                               int32_t *path, int32_t *out_tokens)
+{
+    if (ctx && (T < 1 || depth < 0 || depth >= T))
+        return SPECVERIFY_EINVAL;
+    const int rc = check_common(ctx, dtype, B, T - 1, V);
+    if (rc != SPECVERIFY_OK)
+        return rc;
+    if (B == 0)
+        return SPECVERIFY_OK;
+    const size_t es = dtype == SPECVERIFY_BF16 ? 2 : 4;
+    if (!target_logits || !accepted_len || !path || !out_tokens || (T > 1 && (!tokens || !parents)) ||
+        !aligned_to(target_logits, es) || !aligned_to(tokens, 4) || !aligned_to(parents, 4) ||
+        !aligned_to(counts, 4) || !aligned_to(accepted_len, 4) || !aligned_to(path, 4) ||
+        !aligned_to(out_tokens, 4))
+        return SPECVERIFY_EINVAL;
+    DeviceGuard g(ctx->device);
+    if (g.err != hipSuccess)
+        return SPECVERIFY_EHIP;
+    hipEvent_t *ev = next_events(ctx);
+    sv::Launch ln{static_cast<hipStream_t>(hip_stream), ev, ctx->prof_mask};
+    const hipError_t e = sv::launch_greedy_tree(ln, ctx->ws, dtype, B, T, V, depth, target_logits, tokens,
+                                                parents, counts, accepted_len, path, out_tokens);
+    note_call(ctx, ev, (1u << sv::KIND_ARGMAX) | (1u << sv::KIND_GREEDY_EMIT));
     return e == hipSuccess ? SPECVERIFY_OK : SPECVERIFY_EHIP;
 }
 
@@ -810,6 +878,181 @@ int specverify_cache_copy(specverify_cache *cache, void *hip_stream, int n, cons
     return cache_launch(cache, [&] {
         return sv::launch_cache_copy(static_cast<hipStream_t>(hip_stream), cache->view,
                                      cache->num_cus, n, src, dst, status);
+    });
+}
+
+int specverify_cache_keep_path(specverify_cache *cache, void *hip_stream, int n, int max_count,
+                               const int32_t *seqs, const int32_t *accepted_len,
+                               const int32_t *path, int32_t *status)
+{
+    if (cache && (max_count < 1 || cache->view.page_bytes % cache->view.page_tokens != 0))
+        return SPECVERIFY_EINVAL;
+    if (cache && n >= 0 && max_count > SPECVERIFY_MAX_NODES)
+        return SPECVERIFY_ECAPACITY;
+    const int rc = cache_check(cache, n, cache ? cache->view.num_seqs : 0);
+    if (rc != SPECVERIFY_OK)
+        return rc == 1 ? SPECVERIFY_OK : rc;
+    if (!accepted_len || !path || !aligned_to(seqs, 4) || !aligned_to(accepted_len, 4) ||
+        !aligned_to(path, 4) || !aligned_to(status, 4))
+        return SPECVERIFY_EINVAL;
+    return cache_launch(cache, [&] {
+        return sv::launch_keep_path(static_cast<hipStream_t>(hip_stream), cache->view, n, max_count,
+                                    seqs, accepted_len, path, status);
+    });
+}
+
+int specverify_attn_create(specverify_attn **out, const specverify_cache *cache, int dtype,
+                           int q_heads, int kv_heads, int head_dim, int max_entries, int max_nodes)
+{
+    if (!out)
+        return SPECVERIFY_EINVAL;
+    *out = nullptr;
+    if (!cache)
+        return SPECVERIFY_EINVAL;
+    if (dtype != SPECVERIFY_F32 && dtype != SPECVERIFY_BF16)
+        return SPECVERIFY_EUNSUPPORTED;
+    const int es = dtype == SPECVERIFY_BF16 ? 2 : 4;
+    if (q_heads < 1 || kv_heads < 1 || head_dim < 1 || max_entries < 1 || max_nodes < 1 ||
+        q_heads % kv_heads != 0 || head_dim * (int64_t)es % 16 != 0)
+        return SPECVERIFY_EINVAL;
+    if (head_dim > SPECVERIFY_MAX_HEAD_DIM || max_nodes > SPECVERIFY_MAX_NODES || q_heads > (1 << 16) ||
+        max_entries > SPECVERIFY_MAX_ENTRIES)
+        return SPECVERIFY_ECAPACITY;
+    const sv::CacheView &v = cache->view;
+    if (v.num_pools < 1 || v.page_bytes != (int64_t)v.page_tokens * kv_heads * head_dim * es)
+        return SPECVERIFY_EINVAL;
+    DeviceGuard g(cache->device);
+    if (g.err != hipSuccess)
+        return SPECVERIFY_EHIP;
+
+    const int group = q_heads / kv_heads;
+    // the most rows that parts of any call leave: twice the parts that fill the chip, for each tile
+    int64_t rows = 0;
+    for (int m = 1; m <= max_nodes; ++m) {
+        const int tiles = sv::attend_row_tiles(dtype, head_dim, m * group);
+        rows = std::max<int64_t>(rows, 2ll * sv::attend_units(cache->num_cus, tiles) * 16 * tiles);
+    }
+    const size_t b_plan = align_up((size_t)max_entries * sizeof(sv::AttnPlan));
+    const size_t b_ml = align_up((size_t)rows * sizeof(float2));
+    const size_t b_o = align_up((size_t)rows * head_dim * sizeof(float));
+    specverify_attn *a = new (std::nothrow) specverify_attn();
+    if (!a)
+        return SPECVERIFY_ENOMEM;
+    a->bytes = b_plan + b_ml + b_o;
+    if (hipMalloc(&a->mem, a->bytes) != hipSuccess) {
+        delete a;
+        return SPECVERIFY_ENOMEM;
+    }
+    if (hipMemset(a->mem, 0, b_plan) != hipSuccess || hipDeviceSynchronize() != hipSuccess) {
+        (void)hipFree(a->mem);
+        delete a;
+        return SPECVERIFY_EHIP;
+    }
+    char *p = static_cast<char *>(a->mem);
+    a->device = cache->device;
+    a->view = v;
+    a->max_entries = max_entries;
+    a->max_nodes = max_nodes;
+    a->shape = {dtype, q_heads, kv_heads, head_dim, group, sv::fast_div(group),
+                sv::fast_div(v.page_tokens), cache->num_cus, reinterpret_cast<sv::AttnPlan *>(p),
+                reinterpret_cast<float2 *>(p + b_plan), reinterpret_cast<float *>(p + b_plan + b_ml)};
+    *out = a;
+    return SPECVERIFY_OK;
+}
+
+int64_t specverify_attn_workspace_bytes(const specverify_attn *attn)
+{
+    return attn ? (int64_t)attn->bytes : 0;
+}
+
+int specverify_attn_destroy(specverify_attn *attn)
+{
+    if (!attn)
+        return SPECVERIFY_OK;
+    {
+        DeviceGuard g(attn->device);
+        if (attn->mem)
+            (void)hipFree(attn->mem);
+    }
+    delete attn;
+    return SPECVERIFY_OK;
+}
+
+int specverify_attn_append(specverify_attn *attn, void *hip_stream, int key_pool, int value_pool,
+                           int n, int max_count, int rows, const specverify_nodes *nodes,
+                           const specverify_rotation *rotation, const void *keys,
+                           int64_t key_stride, const void *values, int64_t value_stride,
+                           const void *queries, int64_t query_stride, void *rotated,
+                           int64_t rotated_stride, int32_t *status)
+{
+    if (!attn || n < 0 || max_count < 0 || rows < 0 || bad_pools(attn, key_pool, value_pool))
+        return SPECVERIFY_EINVAL;
+    const sv::AttnShape &s = attn->shape;
+    sv::RotationView rot = {nullptr, 0, 0};
+    if (rotation) {
+        rot = {rotation->inv_freq, rotation->dims, rotation->interleaved != 0};
+        if (rot.dims < 0 || rot.dims > s.head_dim || rot.dims % 2 != 0 ||
+            (rot.dims > 0 && (!rot.inv_freq || !aligned_to(rot.inv_freq, 4))))
+            return SPECVERIFY_EINVAL;
+    }
+    sv::NodesView nv;
+    if (!nodes_view(nodes, n, max_count, rows, &nv) || !aligned_to(status, 4))
+        return SPECVERIFY_EINVAL;
+    if (n > attn->view.num_seqs || (nv.parents && max_count > SPECVERIFY_MAX_NODES))
+        return SPECVERIFY_ECAPACITY;
+    // a workgroup for every four tokens at most, as the launch does it
+    if ((int64_t)n * ((int64_t)max_count + 3) / 4 > (int64_t)(MAX_ITEMS / sv::ATTN_WG) - n)
+        return SPECVERIFY_ECAPACITY;
+    if (n == 0)
+        return SPECVERIFY_OK;
+    const size_t es = s.dtype == SPECVERIFY_BF16 ? 2 : 4;
+    if (rows > 0) {
+        const int64_t kv = (int64_t)s.kv_heads * s.head_dim, qw = (int64_t)s.q_heads * s.head_dim;
+        if (bad_rows(keys, key_stride, kv, rows, es) || bad_rows(values, value_stride, kv, rows, es))
+            return SPECVERIFY_EINVAL;
+        if (queries && (bad_rows(queries, query_stride, qw, rows, es) ||
+                        bad_rows(rotated, rotated_stride, qw, rows, es) ||
+                        (queries == rotated && query_stride != rotated_stride)))
+            return SPECVERIFY_EINVAL;
+    }
+    return cache_launch(attn, [&] {
+        return sv::launch_append(static_cast<hipStream_t>(hip_stream), attn->view, s, nv, rot,
+                                 key_pool, value_pool, keys, key_stride, values, value_stride, queries,
+                                 query_stride, rotated, rotated_stride, status);
+    });
+}
+
+int specverify_attn_attend(specverify_attn *attn, void *hip_stream, int key_pool, int value_pool,
+                           int n, int max_count, int rows, const specverify_nodes *nodes,
+                           float scale, int window, const void *queries, int64_t query_stride,
+                           void *out, int64_t out_stride, float *lse, int32_t *status)
+{
+    if (!attn || n < 0 || max_count < 0 || rows < 0 || bad_pools(attn, key_pool, value_pool) ||
+        !isfinite(scale) || window < 0)
+        return SPECVERIFY_EINVAL;
+    const sv::AttnShape &s = attn->shape;
+    sv::NodesView nv;
+    if (!nodes_view(nodes, n, max_count, rows, &nv) || !aligned_to(status, 4) || !aligned_to(lse, 4))
+        return SPECVERIFY_EINVAL;
+    if (n > attn->max_entries || max_count > attn->max_nodes)
+        return SPECVERIFY_ECAPACITY;
+    // a workgroup for each key head and 16 rows of an entry besides those that fill the chip, and a
+    // wave for each row and head of the join
+    const int64_t parts = (int64_t)n * s.kv_heads * (((int64_t)max_count * s.group + 15) / 16);
+    if (parts + sv::ATTN_MAX_UNITS + 8 > (int64_t)(MAX_ITEMS / sv::ATTN_WG) ||
+        (int64_t)n * max_count * s.q_heads > (int64_t)(MAX_ITEMS / 64) - 4)
+        return SPECVERIFY_ECAPACITY;
+    if (n == 0)
+        return SPECVERIFY_OK;
+    const size_t es = s.dtype == SPECVERIFY_BF16 ? 2 : 4;
+    const int64_t wide = (int64_t)s.q_heads * s.head_dim;
+    if (rows > 0 && (bad_rows(queries, query_stride, wide, rows, es) ||
+                     bad_rows(out, out_stride, wide, rows, es)))
+        return SPECVERIFY_EINVAL;
+    return cache_launch(attn, [&] {
+        return sv::launch_attend(static_cast<hipStream_t>(hip_stream), attn->view, s, nv,
+                                 key_pool, value_pool, scale, window, queries, query_stride, out,
+                                 out_stride, lse, status);
     });
 }
 

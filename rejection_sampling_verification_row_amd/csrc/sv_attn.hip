@@ -1,0 +1,1021 @@
+// Attention of a verify step's nodes over a paged cache, and the append of their keys and values
+// (gfx950).
+//
+// A node is a row; it sees the cached tokens of its sequence, its ancestors and itself.  A workgroup
+// of k_attend has one key head of one entry, up to 64 rows of it (query heads of the key head times
+// nodes: they read the same keys) and a stretch of the tokens, which its four waves take tile by
+// tile.  Per tile S^T = K Q^T comes first: in the accumulator layout of a 16x16 matrix instruction a
+// lane then holds scores of one row, so that the maximum and the sum of a softmax stay in the lane
+// but for two exchanges, and the weights are, as they lie, the right operand of O^T = V^T P^T: the
+// order in which a product runs over the tokens is free as long as V^T is read in the same.  K is
+// read from memory straight into the left operand's layout; V too, with lanes along the head, and
+// for 16-bit values pairs of tokens are joined by byte permutes.  Nothing passes through LDS but the
+// places of the tokens.
+//
+// The work is cut into as many parts as fill the chip, from the lengths, which only the device knows:
+// every workgroup adds them up and finds its own part.  Parts of a split segment leave sums that
+// k_attend_join adds in the parts' order.
+#include <algorithm>
+
+#include "sv_device.h"
+#include "sv_internal.h"
+
+namespace sv {
+
+namespace {
+
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+
+constexpr float LOG2E = 1.4426950408889634f;
+constexpr float LN2 = 0.6931471805599453f;
+
+__device__ inline bool in_range(int i, int n) { return (unsigned)i < (unsigned)n; }
+
+// a value that all lanes have
+__device__ inline int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+
+__device__ inline int divide(int j, const FastDiv &f)
+{
+    return f.s < 0 ? j : (int)(__umulhi((uint32_t)j, f.m) >> f.s);
+}
+
+// ------------------------------------------------------------------ entries and nodes
+
+struct Entry {
+    int seq, start, count, len;      // count < 0: refused
+};
+
+__device__ inline Entry load_entry(const CacheView &c, const NodesView &nv, int i)
+{
+    Entry e = {-1, 0, -1, 0};
+    const int s = nv.seqs ? nv.seqs[i] : i;
+    if (!in_range(s, c.num_seqs))
+        return e;
+    const int64_t start = nv.starts ? nv.starts[i] : (int64_t)i * nv.max_count;
+    const int cnt = nv.counts ? nv.counts[i] : nv.max_count;
+    const int had = c.blocks[s], len = c.lengths[s];
+    if (had < 0 || had > c.max_blocks || len < 0 || len > had * c.page_tokens)
+        return e;
+    if (cnt < 0 || cnt > nv.max_count || cnt > had * c.page_tokens - len || start < 0 ||
+        start + cnt > nv.rows)
+        return e;
+    e.seq = s;
+    e.start = (int)start;
+    e.count = cnt;
+    e.len = len;
+    return e;
+}
+
+// Lane t's node: its ancestors and itself as bits, and its depth; false when a parent is not below
+// its child.  Of `window` depths only, if that is above 0.  Whole waves call it.  Ancestors are
+// joined over 1, 2, 4, ... 32 steps at a time.
+__device__ inline bool lane_node(const int *parents, int count, int window, uint64_t &seen, int &depth)
+{
+    const int t = threadIdx.x & 63;
+    int up = t < count ? t - 1 : -1;
+    if (parents && t > 0 && t < count)
+        up = parents[t];
+    const bool bad = t > 0 && t < count && (up < 0 || up >= t);
+    if (__ballot(bad) != 0)
+        return false;
+    seen = 1ull << t;
+#pragma unroll
+    for (int k = 0; k < 6; ++k) {
+        const uint64_t more = __shfl((unsigned long long)seen, max(up, 0));
+        const int far = __shfl(up, max(up, 0));
+        if (up >= 0) {
+            seen |= more;
+            up = far;
+        }
+    }
+    depth = __popcll(seen) - 1;
+    if (window > 0 && window < MAX_NODES) {
+        uint64_t near = 0;
+        for (int a = 0; a < count; ++a)
+            if (depth - __shfl(depth, a) < window)
+                near |= 1ull << a;
+        seen &= near;
+    }
+    return true;
+}
+
+// ------------------------------------------------------------------ attention
+
+struct AttnArgs {
+    CacheView c;
+    AttnShape a;
+    NodesView nv;
+    int key_pool, value_pool;
+    float c1;            // |scale| log2(e), 1 for scale 0
+    float q_sign;        // the queries' factor: scale's sign
+    int window;
+    const char *q;
+    int64_t q_stride;    // bytes
+    char *out;
+    int64_t out_stride;  // bytes
+    float *lse;
+    int *status;
+    int units;           // parts that fill the chip
+};
+
+__device__ inline int64_t block_sum(int64_t v, int64_t *lds)
+{
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1)
+        v += __shfl_xor((long long)v, o);
+    __syncthreads();
+    if ((threadIdx.x & 63) == 0)
+        lds[threadIdx.x >> 6] = v;
+    __syncthreads();
+    return lds[0] + lds[1] + lds[2] + lds[3];
+}
+
+// Inclusive over the workgroup's threads; *all is the sum.
+__device__ inline int64_t block_scan(int64_t v, int64_t *lds, int64_t *all)
+{
+    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+        const int64_t u = __shfl_up((long long)v, o);
+        if (lane >= o)
+            v += u;
+    }
+    __syncthreads();
+    if (lane == 63)
+        lds[w] = v;
+    __syncthreads();
+    int64_t before = 0;
+    for (int i = 0; i < w; ++i)
+        before += lds[i];
+    *all = lds[0] + lds[1] + lds[2] + lds[3];
+    return before + v;
+}
+
+// An entry's work: segments (key heads times tiles of rows) and tiles of KT tokens from `low` on.
+struct Work {
+    int tiles_of_rows, segments, low, tiles;
+};
+
+template <int KT> __device__ inline Work entry_work(const AttnArgs &a, const Entry &e, int rows_per_tile)
+{
+    Work w = {0, 0, 0, 0};
+    if (e.count <= 0)
+        return w;
+    w.tiles_of_rows = (e.count * a.a.group + rows_per_tile - 1) / rows_per_tile;
+    w.segments = w.tiles_of_rows * a.a.kv_heads;
+    // the root is the first to see least far back
+    w.low = a.window > 0 ? max(e.len - a.window + 1, 0) / KT : 0;
+    w.tiles = (int)(((unsigned)e.len + e.count + KT - 1) / KT) - w.low;
+    return w;
+}
+
+struct Part {
+    int entry, local, chunks, kept;      // entry < 0: none
+};
+
+// This workgroup's part.  Workgroup 0 also leaves the plan for the join, and the status of entries
+// that have no part.
+template <int KT> __device__ Part find_part(const AttnArgs &a, int rows_per_tile, int least)
+{
+    __shared__ int64_t lds[4];
+    __shared__ Part found;
+    const int n = a.nv.n, t = threadIdx.x;
+    Entry e0 = {-1, 0, -1, 0};
+    if (t < n)
+        e0 = load_entry(a.c, a.nv, t);
+    const Work w0 = entry_work<KT>(a, e0, rows_per_tile);
+    auto work = [&](int i, Entry &e) {
+        if (i < ATTN_WG) {
+            e = e0;
+            return w0;
+        }
+        e = load_entry(a.c, a.nv, i);
+        return entry_work<KT>(a, e, rows_per_tile);
+    };
+    int64_t sum = 0;
+    for (int i = t; i < n; i += ATTN_WG) {
+        Entry e;
+        const Work w = work(i, e);
+        sum += (int64_t)w.segments * w.tiles;
+    }
+    sum = block_sum(sum, lds);
+    const int per = (int)max((sum + a.units - 1) / a.units, (int64_t)least);   // tiles of a part
+    if (t == 0)
+        found = {-1, 0, 0, 0};
+    int64_t total = 0;
+    for (int i = t; i < n; i += ATTN_WG) {
+        Entry e;
+        const Work w = work(i, e);
+        total += (int64_t)w.segments * ((w.tiles + per - 1) / per);
+    }
+    total = block_sum(total, lds);
+    // neighbours, which read the same tokens, on one of the 8 dies, to which workgroups go in turn
+    const int64_t each = (total + 7) / 8;
+    const int64_t mine = (int64_t)(blockIdx.x & 7) * each + (blockIdx.x >> 3);
+    const bool none = (int64_t)(blockIdx.x >> 3) >= each || mine >= total;
+    if (none && blockIdx.x != 0)
+        return {-1, 0, 0, 0};
+    int64_t base = 0;                    // parts in the upper half, kept ones in the lower
+    for (int i0 = 0; i0 < n; i0 += ATTN_WG) {
+        const int i = i0 + t;
+        Entry e = {-1, 0, -1, 0};
+        Work w = {0, 0, 0, 0};
+        if (i < n)
+            w = work(i, e);
+        const int chunks = (w.tiles + per - 1) / per, parts = w.segments * chunks;
+        const int kept = chunks > 1 ? parts : 0;
+        int64_t all;
+        const int64_t inc = base + block_scan(((int64_t)parts << 32) + kept, lds, &all);
+        const int64_t first = (inc >> 32) - parts;
+        const int at = (int)(inc & 0xffffffff) - kept;
+        if (i < n && !none && mine >= first && mine < first + parts)
+            found = {i, (int)(mine - first), chunks, at};
+        if (blockIdx.x == 0 && i < n) {
+            a.a.plan[i].chunks = parts > 0 ? chunks : 0;
+            a.a.plan[i].part = at;
+            a.a.plan[i].tiles = w.tiles_of_rows;
+            if (a.status && parts == 0)
+                a.status[i] = e.count < 0 ? -1 : 0;
+        }
+        base += all;
+    }
+    __syncthreads();
+    return {uniform(found.entry), uniform(found.local), uniform(found.chunks), uniform(found.kept)};
+}
+
+template <int DT> struct Tile;
+template <> struct Tile<1> {
+    static constexpr int ES = 2, KT = 32;     // bytes of an element, tokens of a tile
+    typedef bf16x8 vec;
+};
+template <> struct Tile<0> {
+    static constexpr int ES = 4, KT = 16;
+    typedef f32x4 vec;
+};
+
+template <int BYTES> struct Chunk;
+template <> struct Chunk<16> { typedef u32x4 type; };
+template <> struct Chunk<8> { typedef u32x2 type; };
+
+// any element of a word (two bfloat16, or a float) infinite or NaN
+template <int DT> __device__ inline bool odd_word(uint32_t w)
+{
+    if constexpr (DT == 1)
+        return (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u;
+    else
+        return (w & 0x7f800000u) == 0x7f800000u;
+}
+
+__device__ inline float row_max(float v)
+{
+    v = fmaxf(v, xch<4>(v));
+    return fmaxf(v, xch<5>(v));
+}
+__device__ inline float row_sum(float v)
+{
+    v += xch<4>(v);
+    return v + xch<5>(v);
+}
+
+// DP: head_dim or more; VW: elements of a value row that a lane loads at once, 16 lanes side by
+// side; R: tiles of 16 rows.  Left operands of the products: row lane % 16, 16 bytes (4 for float32)
+// of the axis summed over to each of the four groups lane / 16; right ones likewise with columns;
+// results: column lane % 16, rows 4 (lane / 16) + r.
+template <int DT, int DP, int VW, int R, int OCC>
+__global__ __launch_bounds__(ATTN_WG, OCC) void k_attend(AttnArgs a)
+{
+    typedef Tile<DT> TL;
+    constexpr int ES = TL::ES, KT = TL::KT, SUB = KT / 16, KPL = KT / 4;
+    constexpr int KS = DP * ES / 64;              // 16-byte pieces of a key row to a lane
+    constexpr int NB = DP / (16 * VW);            // pieces of a value row to a lane
+    constexpr int NT = DP / 16;
+    constexpr int ROWS = 16 * R, PITCH = DP + 4;
+    typedef typename Chunk<VW * ES>::type vchunk;
+
+    __shared__ float s_o[4][ROWS][PITCH];
+    __shared__ float2 s_ml[4][ROWS];
+    __shared__ int64_t s_off[4][2][KT];
+
+    const int lane = threadIdx.x & 63, w = uniform(threadIdx.x >> 6), col = lane & 15, grp = lane >> 4;
+    const Part part = find_part<KT>(a, ROWS, 128 / KT);
+    if (part.entry < 0)
+        return;
+    const Entry e = load_entry(a.c, a.nv, part.entry);
+    const Work work = entry_work<KT>(a, e, ROWS);
+    uint64_t lane_seen;
+    int lane_depth;
+    const bool ok = lane_node(a.nv.parents ? a.nv.parents + e.start : nullptr, e.count, a.window, lane_seen,
+                              lane_depth);
+    if (part.local == 0 && threadIdx.x == 0) {
+        a.a.plan[part.entry].ok = ok;
+        if (a.status)
+            a.status[part.entry] = ok ? 0 : -1;
+    }
+    if (!ok)
+        return;
+    const int mt = part.local % work.tiles_of_rows, hc = part.local / work.tiles_of_rows;
+    const int head = hc % a.a.kv_heads, chunk = hc / a.a.kv_heads;
+    const int t0 = work.low + (int)((int64_t)work.tiles * chunk / part.chunks);
+    const int t1 = work.low + (int)((int64_t)work.tiles * (chunk + 1) / part.chunks);
+    const int D = a.a.head_dim, G = a.a.group, rows = e.count * G;
+    const int len = e.len, total = len + e.count;
+
+    // the rows of this lane's columns: what they see, and their queries
+    uint64_t seen[R];
+    int low[R];
+    typename TL::vec q[R][KS];
+    int low_most = 0;
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        const int row = mt * ROWS + r * 16 + col;
+        const int node = row < rows ? divide(row, a.a.by_group) : 0;
+        seen[r] = __shfl((unsigned long long)lane_seen, node);
+        const int depth = __shfl(lane_depth, node);
+        low[r] = a.window > 0 ? max(len - a.window + 1 + depth, 0) : 0;
+        low_most = max(low_most, low[r]);
+        const char *qp = a.q + (int64_t)(e.start + node) * a.q_stride +
+                         (int64_t)(head * G + row - node * G) * D * ES;
+        const bool al = aligned16(qp);
+#pragma unroll
+        for (int s = 0; s < KS; ++s) {
+            const int d = (s * 64 + grp * 16) / ES;
+            uint4 v = make_uint4(0, 0, 0, 0);
+            if (row < rows && d < D) {
+                if (al) {
+                    v = load_plain(qp + d * ES);
+                } else if constexpr (DT == 1) {
+                    const uint16_t *p = reinterpret_cast<const uint16_t *>(qp) + d;
+                    v = make_uint4(p[0] | (uint32_t)p[1] << 16, p[2] | (uint32_t)p[3] << 16,
+                                   p[4] | (uint32_t)p[5] << 16, p[6] | (uint32_t)p[7] << 16);
+                } else {
+                    const uint32_t *p = reinterpret_cast<const uint32_t *>(qp) + d;
+                    v = make_uint4(p[0], p[1], p[2], p[3]);
+                }
+            }
+            if (a.q_sign == 0.0f) {
+                v = make_uint4(0, 0, 0, 0);
+            } else if (a.q_sign < 0.0f) {
+                const uint32_t f = DT == 1 ? 0x80008000u : 0x80000000u;
+                v = make_uint4(v.x ^ f, v.y ^ f, v.z ^ f, v.w ^ f);
+            }
+            q[r][s] = __builtin_bit_cast(typename TL::vec, v);
+        }
+    }
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1)
+        low_most = max(low_most, __shfl_xor(low_most, o));
+    low_most = uniform(low_most);
+
+    const int *table = a.c.tables + (size_t)e.seq * a.c.max_blocks;
+    const int64_t row_bytes = (int64_t)a.a.kv_heads * D * ES;
+    const char *kp = a.c.pools[a.key_pool] + (int64_t)head * D * ES;
+    const char *vp = a.c.pools[a.value_pool] + (int64_t)head * D * ES;
+
+    // a tile's page ids, one token to a lane, then the tokens' places; bits of what has no place
+    auto page_of = [&](int tile) {
+        const int j = (int)min((unsigned)tile * KT + (lane & (KT - 1)), (unsigned)total - 1);
+        return load_global<int>(table + divide(j, a.a.by_page));
+    };
+    auto put_places = [&](int tile, int pg, int buf) {
+        const int j = (int)min((unsigned)tile * KT + (lane & (KT - 1)), (unsigned)total - 1);
+        const int b = divide(j, a.a.by_page);
+        const bool good = in_range(pg, a.c.num_pages);
+        const int64_t at = (int64_t)(good ? pg : 0) * a.c.page_tokens + (j - b * a.c.page_tokens);
+        if (lane < KT)
+            s_off[w][buf][lane] = at * row_bytes;
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+        return (uint32_t)(__ballot(!good) & ((1ull << KT) - 1));
+    };
+
+    u32x4 kr[SUB][KS];
+    vchunk vr[KPL][NB];
+    auto load_keys = [&](int buf) {
+#pragma unroll
+        for (int s = 0; s < SUB; ++s) {
+            const char *p = kp + s_off[w][buf][s * 16 + col];
+#pragma unroll
+            for (int k = 0; k < KS; ++k) {
+                const int b = k * 64 + grp * 16;
+                kr[s][k] = load_global<u32x4>(p + (b < D * ES ? b : 0));
+            }
+        }
+    };
+    auto load_values = [&](int buf) {
+#pragma unroll
+        for (int k = 0; k < KPL; ++k) {
+            const char *p = vp + s_off[w][buf][(k / 4) * 16 + grp * 4 + (k & 3)];
+#pragma unroll
+            for (int b = 0; b < NB; ++b) {
+                const int at = (b * 16 + col) * VW * ES;
+                vr[k][b] = load_global<vchunk>(p + (at < D * ES ? at : 0));
+            }
+        }
+    };
+
+    f32x4 o[R][NT];
+    float m[R], l[R];                    // maximum of the raw scores, this lane's part of the sum
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        m[r] = -INFINITY;
+        l[r] = 0.0f;
+#pragma unroll
+        for (int i = 0; i < NT; ++i)
+            o[r][i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    }
+
+    int t = t0 + w, buf = 0, next_page = 0;
+    const int last = t1 - 1 - (t1 - 1 - t0 - w & 3);     // this wave's last tile
+    uint32_t lost = 0;
+    if (t < t1) {
+        lost = put_places(t, page_of(t), 0);
+        load_keys(0);
+        load_values(0);
+        next_page = page_of(min(t + 4, last));
+    }
+    for (; t < t1; t += 4, buf ^= 1) {
+        f32x4 s[R][SUB];
+        if (DP != D) {
+            // elements past the head's end: the queries are 0 there, the keys must be finite
+#pragma unroll
+            for (int x = 0; x < SUB; ++x)
+#pragma unroll
+                for (int k = 0; k < KS; ++k)
+                    if (k * 64 + grp * 16 >= D * ES)
+                        kr[x][k] = u32x4{0, 0, 0, 0};
+        }
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+#pragma unroll
+            for (int x = 0; x < SUB; ++x) {
+                s[r][x] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                for (int k = 0; k < KS; ++k) {
+                    const typename TL::vec kv = __builtin_bit_cast(typename TL::vec, kr[x][k]);
+                    if constexpr (DT == 1) {
+                        s[r][x] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kv, q[r][k], s[r][x], 0, 0, 0);
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            s[r][x] = __builtin_amdgcn_mfma_f32_16x16x4f32(kv[i], q[r][k][i], s[r][x], 0, 0, 0);
+                    }
+                }
+            }
+        // the next tile's loads are made in any case (the last tile's again): a branch around them
+        // would let every wait for older ones wait for all
+        const uint32_t next_lost = put_places(min(t + 4, last), next_page, buf ^ 1);
+        next_page = page_of(min(t + 8, last));
+        load_keys(buf ^ 1);
+        const unsigned j0 = (unsigned)t * KT;
+        const bool masked = j0 + KT > (unsigned)len || lost != 0 || (int)j0 < low_most;
+        uint32_t vis[R];                 // the tile's tokens that a row sees, as bits
+        if (masked) {
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                const int back = len - (int)j0, from = low[r] - (int)j0;
+                uint32_t v = back >= 32 ? ~0u : back > 0 ? (1u << back) - 1 : 0;
+                v = from >= 32 ? 0 : from > 0 ? v & (~0u << from) : v;
+                if (back <= 0)
+                    v |= back > -64 ? (uint32_t)(seen[r] >> -back) : 0;
+                else if (back < 32)
+                    v |= (uint32_t)seen[r] << back;
+                vis[r] = v & ~lost;
+#pragma unroll
+                for (int x = 0; x < SUB; ++x)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        s[r][x][i] = vis[r] >> (grp * 4) & (1u << (x * 16 + i)) ? s[r][x][i] : -INFINITY;
+            }
+        }
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            float top = s[r][0][0];
+#pragma unroll
+            for (int x = 0; x < SUB; ++x)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    top = fmaxf(top, s[r][x][i]);
+            if (__ballot(top > m[r]) != 0) {
+                const float was = m[r];
+                m[r] = fmaxf(was, row_max(top));
+                const float f = m[r] == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f((was - m[r]) * a.c1);
+                l[r] *= f;
+#pragma unroll
+                for (int i = 0; i < NT; ++i)
+                    o[r][i] *= f;
+            }
+            const float ref = m[r] == -INFINITY ? 0.0f : m[r] * a.c1;
+#pragma unroll
+            for (int x = 0; x < SUB; ++x)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    s[r][x][i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[r][x][i], a.c1, -ref));
+                    l[r] += s[r][x][i];
+                }
+        }
+        if (masked) {
+            // What a row does not see may be anything: rows of values with an infinity or a NaN are left
+            // out of the product and added to the rows that see them, one by one.
+            uint32_t odd = 0;
+#pragma unroll
+            for (int k = 0; k < KPL; ++k) {
+                bool mine = false;
+#pragma unroll
+                for (int x = 0; x < NB; ++x)
+#pragma unroll
+                    for (int i = 0; i < VW * ES / 4; ++i)
+                        mine |= odd_word<DT>(vr[k][x][i]);
+                const uint64_t all = __ballot(mine);
+                if (all == 0)
+                    continue;
+#pragma unroll
+                for (int g = 0; g < 4; ++g)
+                    odd |= all >> (g * 16) & 0xffff ? 1u << ((k / 4) * 16 + g * 4 + (k & 3)) : 0;
+                if (all >> (grp * 16) & 0xffff)
+#pragma unroll
+                    for (int x = 0; x < NB; ++x)
+                        vr[k][x] = vchunk{};
+            }
+#pragma unroll 1
+            for (; odd != 0; odd &= odd - 1) {
+                const int key = __builtin_ctz(odd);
+                const char *p = vp + s_off[w][buf][key];
+#pragma unroll
+                for (int r = 0; r < R; ++r) {
+                    float pr = 0.0f;
+#pragma unroll
+                    for (int x = 0; x < SUB; ++x)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            pr = key / 16 == x && (key & 3) == i ? s[r][x][i] : pr;
+                    pr = __shfl(pr, (key >> 2 & 3) * 16 + col);
+                    const bool sees = vis[r] >> key & 1;
+#pragma unroll
+                    for (int x = 0; x < NT; ++x)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int d = (x / VW) * 16 * VW + (grp * 4 + i) * VW + x % VW;
+                            const char *at = p + (d < D ? d : 0) * ES;
+                            float v;
+                            if constexpr (DT == 1)
+                                v = __uint_as_float((uint32_t)load_global<uint16_t>(at) << 16);
+                            else
+                                v = load_global<float>(at);
+                            o[r][x][i] = sees ? o[r][x][i] + pr * v : o[r][x][i];
+                        }
+                }
+            }
+        }
+        if constexpr (DT == 1) {
+            bf16x8 p[R];
+#pragma unroll
+            for (int r = 0; r < R; ++r)
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    p[r][i] = (__bf16)s[r][i / 4][i & 3];
+#pragma unroll
+            for (int b = 0; b < NB; ++b)
+#pragma unroll
+                for (int x = 0; x < VW; ++x) {
+                    uint32_t u[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        u[i] = __builtin_amdgcn_perm(vr[2 * i + 1][b][x / 2], vr[2 * i][b][x / 2],
+                                                     x & 1 ? 0x07060302u : 0x05040100u);
+                    const bf16x8 vt = __builtin_bit_cast(bf16x8, make_uint4(u[0], u[1], u[2], u[3]));
+#pragma unroll
+                    for (int r = 0; r < R; ++r)
+                        o[r][b * VW + x] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vt, p[r], o[r][b * VW + x],
+                                                                                   0, 0, 0);
+                }
+        } else {
+#pragma unroll
+            for (int k = 0; k < KPL; ++k)
+#pragma unroll
+                for (int b = 0; b < NB; ++b)
+#pragma unroll
+                    for (int x = 0; x < VW; ++x)
+#pragma unroll
+                        for (int r = 0; r < R; ++r)
+                            o[r][b * VW + x] = __builtin_amdgcn_mfma_f32_16x16x4f32(
+                                __uint_as_float(vr[k][b][x]), s[r][0][k], o[r][b * VW + x], 0, 0, 0);
+        }
+        load_values(buf ^ 1);
+        lost = next_lost;
+    }
+
+    // the four waves' sums, joined
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        const float sum = row_sum(l[r]);
+        if (grp == 0)
+            s_ml[w][r * 16 + col] = make_float2(m[r] == -INFINITY ? -INFINITY : m[r] * a.c1, sum);
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int x = 0; x < VW; ++x)
+                    s_o[w][r * 16 + col][b * 16 * VW + (grp * 4 + i) * VW + x] = o[r][b * VW + x][i];
+    }
+    __syncthreads();
+    const int here = min(rows - mt * ROWS, ROWS);
+    const int64_t kept = part.kept + part.local;
+    for (int i = threadIdx.x; i < here * (D / 4); i += ATTN_WG) {
+        const int row = i / (D / 4), d = (i - row * (D / 4)) * 4;
+        float top = -INFINITY;
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            top = fmaxf(top, s_ml[k][row].x);
+        float z = 0.0f, acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const float2 ml = s_ml[k][row];
+            const float f = ml.x == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(ml.x - top);
+            z += f * ml.y;
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+                acc[x] += f * s_o[k][row][d + x];
+        }
+        if (part.chunks > 1) {
+            float *to = a.a.part_o + (kept * ROWS + row) * (int64_t)D + d;
+            *reinterpret_cast<float4 *>(to) = make_float4(acc[0], acc[1], acc[2], acc[3]);
+            if (d == 0)
+                a.a.part_ml[kept * ROWS + row] = make_float2(top, z);
+            continue;
+        }
+        const int gr = mt * ROWS + row, node = divide(gr, a.a.by_group);
+        const int qh = head * G + gr - node * G;
+        char *to = a.out + (int64_t)(e.start + node) * a.out_stride + ((int64_t)qh * D + d) * ES;
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+            const float v = z == 0.0f ? 0.0f : acc[x] / z;
+            if constexpr (DT == 1)
+                reinterpret_cast<__bf16 *>(to)[x] = (__bf16)v;
+            else
+                reinterpret_cast<float *>(to)[x] = v;
+        }
+        if (a.lse && d == 0)
+            a.lse[(int64_t)(e.start + node) * a.a.q_heads + qh] =
+                z == 0.0f ? -INFINITY : (top + log2f(z)) * LN2;
+    }
+}
+
+// A wave joins the parts of one row: weights of 64 parts at once, a lane each.
+template <int DT> __global__ __launch_bounds__(ATTN_WG) void k_attend_join(AttnArgs a, int rows_per_tile)
+{
+    constexpr int ES = Tile<DT>::ES;
+    const int lane = threadIdx.x & 63;
+    const int per = a.nv.max_count * a.a.q_heads;
+    const int64_t at = (int64_t)blockIdx.x * (ATTN_WG / 64) + (threadIdx.x >> 6);
+    const int i = (int)(at / per), rest = (int)(at - (int64_t)i * per);
+    if (i >= a.nv.n)
+        return;
+    const AttnPlan p = a.a.plan[i];
+    if (p.chunks < 2 || !p.ok)
+        return;
+    const Entry e = load_entry(a.c, a.nv, i);
+    const int node = rest / a.a.q_heads, qh = rest - node * a.a.q_heads;
+    if (node >= e.count)
+        return;
+    const int D = a.a.head_dim, G = a.a.group, head = qh / G;
+    const int gr = node * G + qh - head * G, mt = gr / rows_per_tile, row = gr - mt * rows_per_tile;
+    auto kept = [&](int c) {
+        return ((int64_t)p.part + ((int64_t)c * a.a.kv_heads + head) * p.tiles + mt) * rows_per_tile + row;
+    };
+    float top = -INFINITY;
+    for (int c = lane; c < p.chunks; c += 64)
+        top = fmaxf(top, a.a.part_ml[kept(c)].x);
+    top = wave_max(top);
+    float z = 0.0f, acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    for (int c0 = 0; c0 < p.chunks; c0 += 64) {
+        float f = 0.0f, part = 0.0f;
+        if (c0 + lane < p.chunks) {
+            const float2 ml = a.a.part_ml[kept(c0 + lane)];
+            f = ml.x == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(ml.x - top);
+            part = f * ml.y;
+        }
+#pragma unroll
+        for (int s = 32; s > 0; s >>= 1)
+            part += __shfl_xor(part, s);
+        z += part;
+        const int most = min(p.chunks - c0, 64);
+#pragma unroll 8
+        for (int c = 0; c < most; ++c) {
+            const float fc = __shfl(f, c);
+            if (lane * 4 < D) {
+                const float4 v = *reinterpret_cast<const float4 *>(a.a.part_o + kept(c0 + c) * D + lane * 4);
+                acc[0] += fc * v.x;
+                acc[1] += fc * v.y;
+                acc[2] += fc * v.z;
+                acc[3] += fc * v.w;
+            }
+        }
+    }
+    char *to = a.out + (int64_t)(e.start + node) * a.out_stride + ((int64_t)qh * D + lane * 4) * ES;
+    if (lane * 4 < D)
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+            const float v = z == 0.0f ? 0.0f : acc[x] / z;
+            if constexpr (DT == 1)
+                reinterpret_cast<__bf16 *>(to)[x] = (__bf16)v;
+            else
+                reinterpret_cast<float *>(to)[x] = v;
+        }
+    if (a.lse && lane == 0)
+        a.lse[(int64_t)(e.start + node) * a.a.q_heads + qh] =
+            z == 0.0f ? -INFINITY : (top + log2f(z)) * LN2;
+}
+
+template <int DT, int DP, int VW, int R, int OCC>
+hipError_t attend_with(hipStream_t st, const AttnArgs &a)
+{
+    const int64_t segments = (int64_t)a.nv.n * a.a.kv_heads *
+                             ((a.nv.max_count * a.a.group + 16 * R - 1) / (16 * R));
+    // workgroups stand by dies, each of which may have one part more than its share
+    const unsigned grid = (unsigned)(a.units + segments + 8);
+    k_attend<DT, DP, VW, R, OCC><<<grid, ATTN_WG, 0, st>>>(a);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess)
+        return e;
+    const int64_t rows = (int64_t)a.nv.n * a.nv.max_count * a.a.q_heads;
+    k_attend_join<DT><<<(unsigned)((rows + 3) / 4), ATTN_WG, 0, st>>>(a, 16 * R);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+int attend_row_tiles(int dtype, int head_dim, int rows)
+{
+    if (rows <= 16 || (dtype == 0 && head_dim > 128))
+        return 1;
+    return rows <= 32 || dtype == 0 || head_dim > 128 ? 2 : 4;
+}
+
+int attend_units(int num_cus, int row_tiles) { return std::min(num_cus * (row_tiles == 4 ? 1 : 2), ATTN_MAX_UNITS); }
+
+hipError_t launch_attend(hipStream_t st, const CacheView &c, const AttnShape &s, const NodesView &nodes,
+                         int key_pool, int value_pool, float scale, int window, const void *q,
+                         int64_t q_stride, void *out, int64_t out_stride, float *lse, int *status)
+{
+    const int D = s.head_dim, R = attend_row_tiles(s.dtype, D, nodes.max_count * s.group);
+    const int es = s.dtype == 1 ? 2 : 4;
+    AttnArgs a = {c, s, nodes, key_pool, value_pool, scale == 0.0f ? 1.0f : fabsf(scale) * LOG2E,
+                  scale > 0.0f ? 1.0f : scale < 0.0f ? -1.0f : 0.0f, window, static_cast<const char *>(q),
+                  q_stride * es, static_cast<char *>(out), out_stride * es, lse, status,
+                  attend_units(s.num_cus, R)};
+    if (s.dtype == 1) {
+        if (D <= 64)
+            return R == 1 ? attend_with<1, 64, 4, 1, 2>(st, a)
+                 : R == 2 ? attend_with<1, 64, 4, 2, 2>(st, a) : attend_with<1, 64, 4, 4, 1>(st, a);
+        if (D <= 128)
+            return R == 1 ? attend_with<1, 128, 8, 1, 2>(st, a)
+                 : R == 2 ? attend_with<1, 128, 8, 2, 2>(st, a) : attend_with<1, 128, 8, 4, 1>(st, a);
+        return R == 1 ? attend_with<1, 256, 8, 1, 1>(st, a) : attend_with<1, 256, 8, 2, 1>(st, a);
+    }
+    if (D <= 64)
+        return R == 1 ? attend_with<0, 64, 4, 1, 2>(st, a) : attend_with<0, 64, 4, 2, 2>(st, a);
+    if (D <= 128)
+        return R == 1 ? attend_with<0, 128, 4, 1, 2>(st, a) : attend_with<0, 128, 4, 2, 2>(st, a);
+    return attend_with<0, 256, 4, 1, 1>(st, a);
+}
+
+// ------------------------------------------------------------------ append
+
+namespace {
+
+// cos and sin of position * inv_freq: the angle in turns in fp64, what is left of whole turns in fp32.
+__device__ inline float2 turn(int position, float inv_freq)
+{
+    const double x = (double)position * (double)inv_freq * 0.15915494309189533577;
+    const float h = 2.0f * (float)(x - rint(x));
+    float s, c;
+    sincospif(h, &s, &c);
+    return make_float2(c, s);
+}
+
+constexpr int APPEND_TOKENS = 4;                   // of an entry to a workgroup
+constexpr int APPEND_PAIRS = ATTN_MAX_HEAD_DIM / 2;
+
+struct AppendArgs {
+    CacheView c;
+    AttnShape a;
+    NodesView nv;
+    RotationView rot;
+    int key_pool, value_pool;
+    const char *k, *v, *q;
+    char *rotated;
+    int64_t k_stride, v_stride, q_stride, rotated_stride;   // bytes
+    int *status;
+    int tokens;          // of an entry to a group of workgroups
+    int split;           // workgroups of a group
+    FastDiv by_group;    // groups of an entry, times split
+    FastDiv by_token;    // pieces of a token
+    FastDiv by_head;     // pieces of a rotated head
+};
+
+template <int DT, int N> __device__ inline void load_piece(const char *p, float (&x)[N])
+{
+    if constexpr (N == Elt<DT>::EPV) {
+        Elt<DT>::unpack(load_plain(p), x);
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            x[i] = Elt<DT>::one(p, i);
+    }
+}
+
+template <int DT, int N> __device__ inline void store_piece(char *p, const float (&x)[N])
+{
+    if constexpr (DT == 0 && N == 4) {
+        *reinterpret_cast<float4 *>(p) = make_float4(x[0], x[1], x[2], x[3]);
+    } else if constexpr (DT == 1 && N == 8) {
+        bf16x8 v;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            v[i] = (__bf16)x[i];
+        *reinterpret_cast<bf16x8 *>(p) = v;
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            if constexpr (DT == 1)
+                reinterpret_cast<__bf16 *>(p)[i] = (__bf16)x[i];
+            else
+                reinterpret_cast<float *>(p)[i] = x[i];
+    }
+}
+
+template <int DT, bool VEC> __device__ inline void copy_piece(char *to, const char *from)
+{
+    if constexpr (VEC)
+        *reinterpret_cast<uint4 *>(to) = load_plain(from);
+    else if constexpr (DT == 1)
+        *reinterpret_cast<uint16_t *>(to) = *reinterpret_cast<const uint16_t *>(from);
+    else
+        *reinterpret_cast<uint32_t *>(to) = *reinterpret_cast<const uint32_t *>(from);
+}
+
+// A rotated piece holds 16 bytes of both halves of a head (of neighbouring pairs: 16 bytes), the
+// others 16 bytes; without VEC, where something is not aligned to 16 bytes, one pair and one
+// element.  A token's pieces: its query heads', its key heads', its values'.
+template <int DT, bool VEC, bool INTER>
+__global__ __launch_bounds__(ATTN_WG) void k_append(AppendArgs a)
+{
+    constexpr int ES = Elt<DT>::BYTES, N = VEC ? Elt<DT>::EPV : 1;
+    constexpr int PAIRS = INTER && VEC ? N / 2 : N;      // pairs of a rotated piece
+    __shared__ float2 cs[APPEND_TOKENS][APPEND_PAIRS];
+    __shared__ int64_t place[APPEND_TOKENS];
+    __shared__ int depth_of[MAX_NODES];
+    const int group = divide((int)blockIdx.x, a.by_group);
+    const int within = (int)blockIdx.x - group * (int)a.by_group.d;
+    const int first = within / a.split * a.tokens, part = within - within / a.split * a.split;
+    const int t = threadIdx.x, i = group;
+
+    const Entry e = load_entry(a.c, a.nv, i);
+    bool ok = e.count >= 0;
+    if (ok && a.nv.parents) {
+        uint64_t seen;
+        int depth;
+        ok = lane_node(a.nv.parents + e.start, e.count, 0, seen, depth);
+        if (ok && t < MAX_NODES)
+            depth_of[t] = depth;
+    }
+    if (ok && a.nv.seqs) {
+        bool named = false;
+        for (int j = t; j < i; j += ATTN_WG)
+            named |= a.nv.seqs[j] == e.seq;
+        ok = !__syncthreads_or(named);
+    }
+    if (a.status && within == 0 && t == 0)
+        a.status[i] = ok ? 0 : -1;
+    if (!ok || first >= e.count)
+        return;
+    __syncthreads();
+    const int tokens = min(a.tokens, e.count - first), dims = a.rot.dims, half = dims / 2;
+    const int D = a.a.head_dim, Hk = a.a.kv_heads, Hq = a.q ? a.a.q_heads : 0;
+    const int64_t row_bytes = (int64_t)Hk * D * ES;
+    if (t < tokens) {
+        const int j = e.len + first + t, b = divide(j, a.a.by_page);
+        const int pg = a.c.tables[(size_t)e.seq * a.c.max_blocks + b];
+        place[t] = in_range(pg, a.c.num_pages)
+                       ? ((int64_t)pg * a.c.page_tokens + (j - b * a.c.page_tokens)) * row_bytes
+                       : -1;
+    }
+    for (int x = t; x < tokens * half; x += ATTN_WG) {
+        const int tk = x / half, p = x - tk * half;
+        const int depth = a.nv.parents ? depth_of[first + tk] : first + tk;
+        cs[tk][p] = turn(e.len + depth, a.rot.inv_freq[p]);
+    }
+    __syncthreads();
+
+    char *kp = a.c.pools[a.key_pool], *vp = a.c.pools[a.value_pool];
+    const int per_token = (int)a.by_token.d, per_head = (int)a.by_head.d, turned = half / PAIRS;
+    for (int x = part * ATTN_WG + t; x < tokens * per_token; x += a.split * ATTN_WG) {
+        const int tk = divide(x, a.by_token), y = x - tk * per_token;
+        const int64_t row = e.start + first + tk;
+        const int64_t at = place[tk];
+        if (y >= (Hq + Hk) * per_head) {
+            const int64_t o = (int64_t)(y - (Hq + Hk) * per_head) * N * ES;
+            if (at >= 0)
+                copy_piece<DT, VEC>(vp + at + o, a.v + row * a.v_stride + o);
+            continue;
+        }
+        int h = divide(y, a.by_head);
+        const int u = y - h * per_head;
+        const char *from;
+        char *to;
+        if (h < Hq) {
+            from = a.q + row * a.q_stride;
+            to = a.rotated + row * a.rotated_stride;
+        } else {
+            h -= Hq;
+            if (at < 0)
+                continue;
+            from = a.k + row * a.k_stride;
+            to = kp + at;
+        }
+        from += (int64_t)h * D * ES;
+        to += (int64_t)h * D * ES;
+        if (u >= turned) {
+            const int64_t o = (int64_t)(dims + (u - turned) * N) * ES;
+            copy_piece<DT, VEC>(to + o, from + o);
+        } else if constexpr (INTER) {
+            float v[2 * PAIRS];
+            const int64_t o = (int64_t)u * 2 * PAIRS * ES;
+            load_piece<DT>(from + o, v);
+#pragma unroll
+            for (int p = 0; p < PAIRS; ++p) {
+                const float2 f = cs[tk][u * PAIRS + p];
+                const float g = v[2 * p], b = v[2 * p + 1];
+                v[2 * p] = __builtin_fmaf(g, f.x, -(b * f.y));
+                v[2 * p + 1] = __builtin_fmaf(b, f.x, g * f.y);
+            }
+            store_piece<DT>(to + o, v);
+        } else {
+            float v[N], z[N];
+            const int64_t o = (int64_t)u * N * ES, far = (int64_t)half * ES;
+            load_piece<DT>(from + o, v);
+            load_piece<DT>(from + o + far, z);
+#pragma unroll
+            for (int p = 0; p < N; ++p) {
+                const float2 f = cs[tk][u * N + p];
+                const float g = v[p], b = z[p];
+                v[p] = __builtin_fmaf(g, f.x, -(b * f.y));
+                z[p] = __builtin_fmaf(b, f.x, g * f.y);
+            }
+            store_piece<DT>(to + o, v);
+            store_piece<DT>(to + o + far, z);
+        }
+    }
+}
+
+template <int DT> hipError_t append_with(hipStream_t st, AppendArgs &a, bool vec)
+{
+    const int n_el = vec ? Elt<DT>::EPV : 1, D = a.a.head_dim, dims = a.rot.dims, Hk = a.a.kv_heads;
+    const int turned = dims / 2 / (a.rot.interleaved && vec ? n_el / 2 : n_el);
+    const int per_head = turned + (D - dims) / n_el;
+    const int per_token = ((a.q ? a.a.q_heads : 0) + Hk) * per_head + Hk * D / n_el;
+    a.by_head = fast_div(per_head);
+    a.by_token = fast_div(per_token);
+    a.tokens = std::min(APPEND_TOKENS, a.nv.max_count);
+    const int64_t groups = (a.nv.max_count + a.tokens - 1) / a.tokens;
+    // a piece to a thread where there are few tokens
+    const int64_t want = 2 * (int64_t)a.a.num_cus / std::max<int64_t>(1, groups * a.nv.n);
+    const int64_t most = ((int64_t)a.tokens * per_token + ATTN_WG - 1) / ATTN_WG;
+    a.split = (int)std::max<int64_t>(1, std::min(want, most));
+    const int64_t per_entry = groups * a.split;
+    if (per_entry * a.nv.n * ATTN_WG > 0xffffffffll)
+        return hipErrorInvalidConfiguration;
+    a.by_group = fast_div((int)per_entry);
+    const unsigned grid = (unsigned)(per_entry * a.nv.n);
+    if (vec)
+        a.rot.interleaved ? k_append<DT, true, true><<<grid, ATTN_WG, 0, st>>>(a)
+                          : k_append<DT, true, false><<<grid, ATTN_WG, 0, st>>>(a);
+    else
+        a.rot.interleaved ? k_append<DT, false, true><<<grid, ATTN_WG, 0, st>>>(a)
+                          : k_append<DT, false, false><<<grid, ATTN_WG, 0, st>>>(a);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_append(hipStream_t st, const CacheView &c, const AttnShape &s, const NodesView &nodes,
+                         const RotationView &rot, int key_pool, int value_pool, const void *k,
+                         int64_t k_stride, const void *v, int64_t v_stride, const void *q,
+                         int64_t q_stride, void *rotated, int64_t rotated_stride, int *status)
+{
+    const int es = s.dtype == 1 ? 2 : 4, epv = 16 / es;
+    AppendArgs a = {c, s, nodes, rot, key_pool, value_pool, static_cast<const char *>(k),
+                    static_cast<const char *>(v), static_cast<const char *>(q),
+                    static_cast<char *>(rotated), k_stride * es, v_stride * es, q_stride * es,
+                    rotated_stride * es, status, 0, 0, {}, {}, {}};
+    const uintptr_t bits = reinterpret_cast<uintptr_t>(k) | reinterpret_cast<uintptr_t>(v) |
+                           reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(rotated) |
+                           (uintptr_t)a.k_stride | (uintptr_t)a.v_stride |
+                           (q ? (uintptr_t)a.q_stride | (uintptr_t)a.rotated_stride : 0);
+    const bool vec = bits % 16 == 0 && (rot.interleaved ? rot.dims : rot.dims / 2) % epv == 0;
+    return s.dtype == 1 ? append_with<1>(st, a, vec) : append_with<0>(st, a, vec);
+}
+
+}  // namespace sv

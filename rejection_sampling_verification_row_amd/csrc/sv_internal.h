@@ -286,6 +286,89 @@ hipError_t launch_cache_compact(hipStream_t st, const CacheView &c, int cus, int
 hipError_t launch_cache_copy(hipStream_t st, const CacheView &c, int cus, int n, const int *src,
                              const int *dst, int *status);
 
+// ------------------------------------------------------------------ attention over a cache
+
+constexpr int MAX_NODES = 64;         // nodes of a tree: one lane each, one bit each of an ancestor mask
+constexpr int ATTN_WG = 256;
+constexpr int ATTN_MAX_HEAD_DIM = 256;
+constexpr int ATTN_MAX_ENTRIES = 1 << 16;
+constexpr int ATTN_MAX_UNITS = 1024;  // parts that a call's work is cut into, at most (but for a part
+                                      // for each key head and tile of rows of an entry)
+
+// j / d for 0 <= j < 2^31: (j m) >> (31 + s), with m = floor(2^(31 + s) / d) + 1 < 2^32 and
+// 2^(s-1) < d <= 2^s: m d exceeds 2^(31 + s) by at most d, so that the quotient is exact.
+struct FastDiv {
+    uint32_t d, m;
+    int s;               // shift after the upper half of the product, -1 for d = 1
+};
+inline FastDiv fast_div(int d)
+{
+    FastDiv f = {(uint32_t)d, 0, -1};
+    if (d > 1) {
+        int s = 0;
+        while ((1ll << s) < d)
+            ++s;
+        f.m = (uint32_t)((1ull << (31 + s)) / (uint64_t)d + 1);
+        f.s = s - 1;
+    }
+    return f;
+}
+
+// The nodes of a step, as the caller gives them.
+struct NodesView {
+    int n, max_count, rows;
+    const int *seqs, *starts, *counts, *parents;
+};
+
+// What the parts of an entry's work leave for their joining: the number of parts of a segment (a
+// key head and a tile of rows), where they are kept, and the rows of a tile.
+struct AttnPlan {
+    int chunks;          // 0: refused, or nothing to do
+    int part;            // first kept part (chunks > 1)
+    int tiles;           // tiles of rows
+    int ok;              // the parents are sound; written by the entry's first part
+};
+
+struct AttnShape {
+    int dtype, q_heads, kv_heads, head_dim, group;
+    FastDiv by_group, by_page;
+    int num_cus;
+    AttnPlan *plan;      // [max_entries]
+    float2 *part_ml;     // [2 units][rows of a tile] maximum (times scale, in powers of 2) and sum
+    float *part_o;       // [2 units][rows of a tile][head_dim] sums of weighted values
+};
+
+// Tiles of 16 rows that a workgroup of k_attend has, by type, head size and rows per key head; the
+// parts that fill the chip.
+int attend_row_tiles(int dtype, int head_dim, int rows);
+int attend_units(int num_cus, int row_tiles);
+
+hipError_t launch_attend(hipStream_t st, const CacheView &c, const AttnShape &a, const NodesView &nodes,
+                         int key_pool, int value_pool, float scale, int window, const void *q,
+                         int64_t q_stride, void *out, int64_t out_stride, float *lse, int *status);
+
+struct RotationView {
+    const float *inv_freq;
+    int dims, interleaved;
+};
+
+hipError_t launch_append(hipStream_t st, const CacheView &c, const AttnShape &a, const NodesView &nodes,
+                         const RotationView &rot, int key_pool, int value_pool, const void *k,
+                         int64_t k_stride, const void *v, int64_t v_stride, const void *q,
+                         int64_t q_stride, void *rotated, int64_t rotated_stride, int *status);
+
+hipError_t launch_keep_path(hipStream_t st, const CacheView &c, int n, int max_count, const int *seqs,
+                            const int *accepted, const int *path, int *status);
+
+// greedy verify of a drafted tree, rows read all at once or depth by depth
+hipError_t launch_greedy_tree(const Launch &ln, const Workspace &ws, int dtype, int B, int T, int V,
+                              int depth, const void *tgt, const int32_t *tokens,
+                              const int32_t *parents, const int32_t *counts, int32_t *acc_len,
+                              int32_t *path, int32_t *out_tokens);
+// k_argmax over `rows` rows in a row: the chunks' partials in ws.part
+hipError_t launch_argmax_rows(const Launch &ln, const Workspace &ws, int dtype, size_t rows, int V,
+                              const void *tgt);
+
 // The workspace of the entry point that allocates nothing: a file-scope device array of
 // STATIC_SCRATCH_BYTES per device (see static_scratch in the kernels' source).
 constexpr size_t STATIC_SCRATCH_BYTES = size_t(4) << 20;

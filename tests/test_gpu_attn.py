@@ -1,0 +1,598 @@
+"""Attention over a paged cache and its append on the GPU, against models in 64 bits.
+
+Tolerances.  e = 2^-24, S = the largest scale * sum |q| |k| of a call, n = the tokens seen.  A score's
+D products and sums in fp32 are off by at most (D + 6) e S with the scaling and the exponential's
+argument, so that a weight is off by (2 (D + 6) S + 16) e relative to the maximum's, and sums of n
+weights by n e more; the result is off by that times sum w |v| / sum w.  bfloat16 adds half a step
+(2^-8) for each weight, so 2^-8 sum w |v| / sum w, and half a step of the result.
+A rotation's cos and sin are off by half an ulp of the angle in half turns (pi 2^-25) and two ulps
+of sincospif (2^-23), below 2.2e-7 together, its two products and sum by three roundings: 4e-7 (|a| + |b|).
+"""
+import numpy as np
+import pytest
+import torch
+
+import attn_model as model
+from gpu_support import dev
+from rejection_sampling_verification_row_amd import binding as sv
+
+pytestmark = pytest.mark.gpu
+
+E = 2.0 ** -24
+TD = {"bf16": torch.bfloat16, "f32": torch.float32}
+HALF = {"bf16": 2.0 ** -8, "f32": 2.0 ** -24}
+
+
+def i32(x):
+    return None if x is None else dev(np.asarray(x, np.int32))
+
+
+def values(r, shape, dt):
+    """Values of the type, and as float64."""
+    x = torch.from_numpy(r.standard_normal(shape).astype(np.float32)).to(TD[dt])
+    return x, x.double().numpy()
+
+
+def tree(r, m):
+    return [-1] + [int(r.randint(0, t)) if r.rand() < 0.6 else t - 1 for t in range(1, m)]
+
+
+class Setup:
+    """A cache whose sequences hold tokens in shuffled pages, and a step's nodes."""
+
+    def __init__(self, dt, H, Hk, D, pt, lens, counts, seed=0, parents=True, extra_seqs=1, extra_pages=2,
+                 shuffle=True, max_count=None, pad=0, given=True):
+        r = self.r = np.random.RandomState(seed)
+        self.dt, self.H, self.Hk, self.D, self.pt = dt, H, Hk, D, pt
+        n, S = len(lens), len(lens) + extra_seqs
+        seqs = r.permutation(S)[:n] if given else np.arange(n)
+        need = [-(-(ln + m) // pt) for ln, m in zip(lens, counts)]
+        self.mb = max(max(need), 1) + 1
+        self.P = sum(need) + extra_pages
+        pages = r.permutation(self.P) if shuffle else np.arange(self.P)
+        self.tables = np.full((S, self.mb), -1, np.int32)
+        self.blocks = np.zeros(S, np.int32)
+        self.lengths = np.zeros(S, np.int32)
+        self.refs = np.zeros(self.P, np.int32)
+        at = 0
+        for s, ln, b in zip(seqs, lens, need):
+            self.tables[s, :b] = pages[at:at + b]
+            self.refs[pages[at:at + b]] = 1
+            self.blocks[s], self.lengths[s] = b, ln
+            at += b
+        self.max_count = max(counts) if max_count is None else max_count
+        starts, self.rows = [], 0
+        for i, m in enumerate(counts):
+            starts.append(self.rows if given else i * self.max_count)
+            self.rows = starts[-1] + (m if given else self.max_count) + (i % 2 if given else 0)
+        par = np.full(self.rows, -5, np.int32)
+        for a, m in zip(starts, counts):
+            par[a:a + m] = tree(r, m)[:m]
+        self.n = n
+        self.given = dict(seqs=seqs, starts=starts, counts=counts) if given else \
+            dict(seqs=None, starts=None, counts=None if min(counts) == self.max_count else counts)
+        self.given["parents"] = par if parents else None
+        self.pad = pad
+        self.pools = [values(r, (self.P, pt, Hk, D), dt) for _ in range(2)]
+        self.q, self.q64 = values(r, (self.rows, H, D), dt)
+        self.k, self.k64 = values(r, (self.rows, Hk, D), dt)
+        self.v, self.v64 = values(r, (self.rows, Hk, D), dt)
+
+    def step(self):
+        return model.Step(self.pt, self.P, self.tables, self.blocks, self.lengths, self.n, self.max_count,
+                          self.rows, **self.given)
+
+    def device(self, max_nodes=64):
+        self.state = [dev(a) for a in (self.refs, self.tables, self.blocks, self.lengths)]
+        self.dpools = [p[0].cuda() for p in self.pools]
+        es = 2 if self.dt == "bf16" else 4
+        self.cache = sv.specverify_cache_create(0, self.P, self.pt, len(self.blocks), self.mb,
+                                                self.pt * self.Hk * self.D * es, self.dpools, *self.state)
+        self.h = sv.specverify_attn_create(self.cache, sv.SPECVERIFY_BF16 if self.dt == "bf16" else
+                                           sv.SPECVERIFY_F32, self.H, self.Hk, self.D, max(self.n, 1),
+                                           max_nodes)
+        self.nodes = sv.SpecVerifyNodes(**{k: i32(x) for k, x in self.given.items()})
+        # rows `pad` elements further apart than they are wide, from an odd place on
+        w = self.H * self.D + 2 * self.Hk * self.D + self.pad
+        buf = torch.zeros(max(self.rows, 1) * w + self.pad, dtype=TD[self.dt], device="cuda")
+        self.x = buf[self.pad:].view(-1, w)[:self.rows] if self.pad % w else buf.view(-1, w)
+        a, b = self.H * self.D, (self.H + self.Hk) * self.D
+        self.wide = w
+        self.dq = self.x[:, :a].unflatten(1, (self.H, self.D))
+        self.dk = self.x[:, a:b].unflatten(1, (self.Hk, self.D))
+        self.dv = self.x[:, b:b + self.Hk * self.D].unflatten(1, (self.Hk, self.D))
+        for to, x in ((self.dq, self.q), (self.dk, self.k), (self.dv, self.v)):
+            to.copy_(x)
+        return self
+
+    def attend(self, scale, window=0, stream=None):
+        out = torch.full((self.rows, self.H, self.D), 7.0, dtype=TD[self.dt], device="cuda")
+        lse = torch.full((self.rows, self.H), 7.0, device="cuda")
+        status = torch.full((max(self.n, 1),), -7, dtype=torch.int32, device="cuda")
+        torch.cuda.synchronize()
+        sv.specverify_attn_attend(self.h, stream, 0, 1, self.n, self.max_count, self.rows, self.nodes, scale,
+                                  window, self.dq, self.wide, out, self.H * self.D, lse, status)
+        torch.cuda.synchronize()
+        return out, lse, status
+
+    def check_attend(self, scale=None, window=0):
+        scale = self.D ** -0.5 if scale is None else scale
+        got, lse, status = self.attend(scale, window)
+        kp, vp = (p[1].reshape(-1, self.Hk, self.D) for p in self.pools)
+        out, want_lse, want_status, rows, size = model.attend(self.step(), kp, vp, self.q64, scale, window,
+                                                              self.Hk)
+        assert status.tolist()[:self.n] == want_status
+        got, lse = got.double().cpu().numpy(), lse.double().cpu().numpy()
+        rest = np.setdiff1d(np.arange(self.rows), rows)
+        assert np.all(got[rest] == 7) and np.all(lse[rest] == 7), "rows of no entry"
+        assert len(set(rows)) == len(rows)
+        fin = np.abs(kp[np.isfinite(kp)]).max(initial=0)
+        S = abs(scale) * np.abs(self.q64).sum(2).max(initial=0) * fin
+        n = int(self.lengths.max(initial=0)) + self.max_count
+        rel = (2 * (self.D + 6) * S + 16 + n) * E
+        g, o, z = got[rows], out[rows], size[rows]
+        assert np.array_equal(np.isnan(g), np.isnan(o))
+        ok = np.isfinite(o)
+        assert np.array_equal(g[~ok & ~np.isnan(o)], o[~ok & ~np.isnan(o)])
+        tol = (rel + (HALF["bf16"] if self.dt == "bf16" else 0)) * z + HALF[self.dt] * np.abs(o) * 1.01 + 1e-30
+        with np.errstate(invalid="ignore"):
+            off = np.where(ok, np.abs(g - o) / tol, 0)
+        assert off.max(initial=0) <= 1, off.max()
+        a, b = lse[rows], want_lse[rows]
+        assert np.array_equal(np.isneginf(a), np.isneginf(b)) and np.array_equal(np.isnan(a), np.isnan(b))
+        ok = np.isfinite(b)
+        assert np.all(np.abs(a[ok] - b[ok]) <= rel + 4 * E * np.abs(b[ok]))
+        return got
+
+    def __del__(self):
+        if hasattr(self, "h"):
+            sv.specverify_attn_destroy(self.h)
+        if hasattr(self, "cache"):
+            sv.specverify_cache_destroy(self.cache)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("H,Hk,D,pt", [(4, 4, 64, 16), (8, 2, 128, 16), (6, 2, 80, 5), (3, 1, 8, 1), (14, 2, 256, 7),
+                                       (5, 5, 192, 100), (40, 2, 32, 64), (2, 1, 112, 3)])
+@pytest.mark.parametrize("lens,counts", [([0], [1]), ([300], [1]), ([17, 0, 130], [5, 1, 9]), ([31, 32, 33], [3, 2, 1]),
+                                         ([260, 0], [64, 64]), ([95], [33])])
+def test_attend_shapes(dt, H, Hk, D, pt, lens, counts):
+    Setup(dt, H, Hk, D, pt, lens, counts, seed=len(lens) * H + D, parents=D != 64).device().check_attend()
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("pad", [1, 2, 8])
+@pytest.mark.parametrize("given", [True, False])
+def test_attend_strides_and_lists(dt, pad, given):
+    """Rows at any element, entries in any order or as the library fills them in."""
+    Setup(dt, 4, 2, 64, 16, [40, 7, 100], [6, 6, 6], pad=pad, given=given).device().check_attend()
+    Setup(dt, 4, 2, 64, 16, [40, 7, 100], [6, 2, 0], pad=pad, given=given, max_count=9).device().check_attend()
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("window", [1, 2, 5, 33, 64, 100, 5000])
+def test_attend_window(dt, window):
+    Setup(dt, 4, 2, 64, 8, [0, 3, 64, 257], [9, 30, 64, 5], seed=window).device().check_attend(window=window)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("scale", [0.0, -0.3, 1e-4, 3.0, 40.0])
+def test_attend_scales(dt, scale):
+    """Zero: means; negative; so large that one token takes all."""
+    s = Setup(dt, 4, 2, 64, 8, [70, 9], [5, 12]).device()
+    if scale == 40.0:
+        # bounds of rounded scores leave nothing: the token of the largest score, with a clear lead
+        got, lse, _ = s.attend(scale)
+        assert torch.isfinite(got.float()).all() and torch.isfinite(lse[:5]).all()
+        return
+    s.check_attend(scale)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("D", [64, 80, 128, 256])
+def test_what_is_not_seen_does_not_count(dt, D):
+    """NaN and infinities in siblings, behind the last token, before the window and in other pages."""
+    s = Setup(dt, 4, 2, D, 16, [40, 3, 100], [9, 20, 3], seed=3)
+    r = np.random.RandomState(5)
+    st = s.step()
+    # a node of each entry holds something odd, its descendants do too: compared as they are
+    for i, odd in enumerate((np.nan, np.inf, -np.inf)):
+        q, a, m, ln, par = st.entry(i)
+        leafs = [t for t in range(m) if t not in par] if m > 2 else [m - 1]
+        at = st.slot(q, ln + leafs[0])
+        for x, (t, f) in enumerate(s.pools):
+            f.reshape(-1, 2, D)[at, :, r.randint(0, D, 3)] = odd
+            t.view(-1, 2, D)[at] = torch.from_numpy(f.reshape(-1, 2, D)[at]).to(TD[dt])
+        # the page's places behind the last token
+        b = int(s.blocks[q])
+        for j in range(ln + m, b * s.pt):
+            at = st.slot(q, j)
+            for t, f in s.pools:
+                f.reshape(-1, 2, D)[at] = odd
+                t.view(-1, 2, D)[at] = odd
+    s.device().check_attend()
+    # cached tokens that no row's window reaches: seen by none
+    s = Setup(dt, 4, 2, D, 16, [100], [4], seed=4, parents=False)
+    st = s.step()
+    for j in range(0, 100 - 20 + 1):
+        at = st.slot(st.entry(0)[0], j)
+        for t, f in s.pools:
+            f.reshape(-1, 2, D)[at] = np.nan
+            t.view(-1, 2, D)[at] = float("nan")
+    s.device().check_attend(window=20)
+    # one that the first row's window reaches and the others' do not
+    s = Setup(dt, 4, 2, D, 16, [100], [4], seed=4, parents=False)
+    st = s.step()
+    at = st.slot(st.entry(0)[0], 81)
+    for t, f in s.pools:
+        f.reshape(-1, 2, D)[at, :, ::3] = np.inf
+        t.view(-1, 2, D)[at, :, ::3] = float("inf")
+    got = s.device().attend(D ** -0.5, 20)[0]
+    a = st.entry(0)[1]
+    assert not torch.isfinite(got[a].float()).all() and torch.isfinite(got[a + 1:a + 4].float()).all()
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_low_values_and_rows_of_nothing(dt):
+    """Keys of -inf give no weight; of the type's lowest value, finite scores or -inf; all -inf: zeros."""
+    s = Setup(dt, 2, 2, 64, 4, [50, 6], [3, 2], seed=8, parents=False)
+    st = s.step()
+    # queries positive in element 0, keys -inf there
+    for t, f in ((s.q, s.q64),):
+        f[:, :, 0] = 1.0
+        t[:, :, 0] = 1.0
+    q0 = st.entry(0)[0]
+    for j in range(10, 30):
+        at = st.slot(q0, j)
+        for t, f in s.pools[:1]:
+            f.reshape(-1, 2, 64)[at, :, 0] = -np.inf
+            t.view(-1, 2, 64)[at, :, 0] = float("-inf")
+    q1 = st.entry(1)[0]
+    for j in range(0, 8):
+        at = st.slot(q1, j)
+        for t, f in s.pools[:1]:
+            f.reshape(-1, 2, 64)[at, :, 0] = -np.inf
+            t.view(-1, 2, 64)[at, :, 0] = float("-inf")
+    got = s.device().check_attend()
+    a = st.entry(1)[1]
+    assert np.all(got[a:a + 2] == 0)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_pages_out_of_range_are_not_seen(dt):
+    s = Setup(dt, 4, 2, 64, 8, [100, 20, 9], [5, 4, 3], seed=2)
+    seqs = s.given["seqs"]
+    s.tables[seqs[0], 3] = -1
+    s.tables[seqs[0], 7] = s.P
+    s.tables[seqs[0], 8] = 2 ** 31 - 1
+    s.tables[seqs[2], :] = -7          # nothing at all
+    got = s.device().check_attend()
+    a = s.given["starts"][2]
+    assert np.all(got[a:a + 3] == 0)
+
+
+def test_refused_entries_leave_their_rows():
+    for spoil in range(9):
+        s = Setup("bf16", 4, 2, 64, 8, [30, 20, 9], [5, 4, 3], seed=spoil)
+        g, q = s.given, s.given["seqs"][1]
+        if spoil == 0:
+            g["seqs"][1] = -1
+        elif spoil == 1:
+            g["seqs"][1] = len(s.blocks)
+        elif spoil == 2:
+            g["counts"][1] = -1
+        elif spoil == 3:
+            g["counts"][1] = 6             # above max_count
+        elif spoil == 4:
+            s.lengths[q] = s.blocks[q] * 8 - 3
+        elif spoil == 5:
+            s.blocks[q] = s.mb + 1
+        elif spoil == 6:
+            g["starts"][1] = -1
+        elif spoil == 7:
+            g["starts"][1] = s.rows - 3
+        else:
+            g["parents"][g["starts"][1] + 2] = 2
+        s.max_count = 5
+        s.device()
+        s.check_attend()
+        assert s.attend(0.1)[2].tolist() == [0, -1, 0]
+        check_append(s, 32, 0)
+
+
+def test_a_sequence_named_twice_and_no_entries():
+    s = Setup("bf16", 4, 2, 64, 8, [30, 20], [5, 4], seed=1)
+    s.given["seqs"][:] = s.given["seqs"][0]
+    s.device().check_attend()             # two sets of nodes on one sequence: read alike
+    check_append(s, 64, 0, want=[0, -1])
+    s.n = 0
+    out = s.attend(0.1)
+    assert torch.all(out[0] == 7)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("D,H,Hk,m", [(64, 2, 1, 5), (128, 8, 1, 4), (256, 2, 1, 1), (128, 16, 1, 16)])
+def test_attend_split_over_long_sequences(dt, D, H, Hk, m):
+    """One long sequence in many parts beside short ones."""
+    Setup(dt, H, Hk, D, 16, [9000, 5, 700], [m, 1, m], seed=D).device().check_attend()
+
+
+def test_attend_of_more_entries_than_a_workgroup():
+    r = np.random.RandomState(1)
+    Setup("bf16", 2, 1, 64, 4, list(r.randint(0, 60, 700)), list(r.randint(0, 4, 700)), seed=9).device().check_attend()
+
+
+def test_attend_repeats_bit_for_bit():
+    s = Setup("bf16", 8, 2, 128, 16, [3000, 100, 900], [7, 30, 64], seed=4).device()
+    a = s.attend(0.09)
+    for _ in range(20):
+        b = s.attend(0.09)
+        assert all(torch.equal(x, y) for x, y in zip(a, b))
+
+
+def test_tokens_past_four_gigabytes():
+    """Pages whose byte offsets pass 2^32."""
+    Hk, D, pt, P = 8, 128, 64, 40000            # 131072 bytes a page, 5.2 GB a pool
+    pools = [torch.zeros(P, pt, Hk, D, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    tables = np.full((1, 4), -1, np.int32)
+    tables[0, :3] = [P - 1, 3, P - 7]
+    refs = np.zeros(P, np.int32)
+    refs[tables[0, :3]] = 1
+    state = [dev(refs), dev(tables), i32([3]), i32([150])]
+    cache = sv.specverify_cache_create(0, P, pt, 1, 4, pt * Hk * D * 2, pools, *state)
+    h = sv.specverify_attn_create(cache, sv.SPECVERIFY_BF16, 8, Hk, D, 1, 8)
+    r = np.random.RandomState(0)
+    small = [values(r, (3, pt, Hk, D), "bf16") for _ in range(2)]
+    for p, (t, _) in zip(pools, small):
+        p[tables[0, :3].tolist()] = t.cuda()
+    q, q64 = values(r, (5, 8, D), "bf16")
+    k, k64 = values(r, (5, Hk, D), "bf16")
+    v, v64 = values(r, (5, Hk, D), "bf16")
+    out, status = torch.zeros(5, 8, D, dtype=torch.bfloat16, device="cuda"), i32([9])
+    w = 8 * D
+    sv.specverify_attn_append(h, None, 0, 1, 1, 5, 5, None, None, k.cuda(), w, v.cuda(), w, status=status)
+    sv.specverify_attn_attend(h, None, 0, 1, 1, 5, 5, None, 0.09, 0, q.cuda(), w, out, w)
+    torch.cuda.synchronize()
+    kp, vp = (f.reshape(-1, Hk, D) for _, f in small)
+    st = model.Step(pt, 3, np.array([[0, 1, 2, -1]]), np.array([3]), np.array([150]), 1, 5, 5)
+    model.append(st, kp, vp, k64, v64, None, None, 0, False)
+    for p, f in zip(pools, (kp, vp)):
+        assert np.array_equal(p[tables[0, :3].tolist()].double().cpu().numpy().reshape(-1, Hk, D), f)
+    want, _, _, _, size = model.attend(st, kp, vp, q64, 0.09, 0, Hk)
+    assert status.tolist() == [0]
+    assert np.all(np.abs(out.double().cpu().numpy() - want) <= (2.0 ** -8 + 1e-4) * (size + np.abs(want)))
+    sv.specverify_attn_destroy(h)
+    sv.specverify_cache_destroy(cache)
+
+
+# ---------------------------------------------------------------------------------- append
+
+def check_append(s, dims, inter, queries=True, in_place=False, want=None, base=10000.0, stream=None):
+    """A device step's append against the model; the setup's pools become what they are then."""
+    half = dims // 2
+    freq = (base ** (-np.arange(half) / max(half, 1))).astype(np.float32)
+    rot = sv.SpecVerifyRotation(dev(freq), dims, inter) if dims else None
+    out = s.dq if in_place else torch.full((s.rows, s.H, s.D), 7.0, dtype=TD[s.dt], device="cuda")
+    status = torch.full((s.n,), -7, dtype=torch.int32, device="cuda")
+    more = (s.dq, s.wide, out, s.wide if in_place else s.H * s.D) if queries else ()
+    torch.cuda.synchronize()
+    sv.specverify_attn_append(s.h, stream, 0, 1, s.n, s.max_count, s.rows, s.nodes, rot, s.dk, s.wide, s.dv,
+                              s.wide, *more, status=status)
+    torch.cuda.synchronize()
+    st = s.step()
+    kp, vp = (p[1].reshape(-1, s.Hk, s.D) for p in s.pools)
+    old = kp.copy()
+    q, want_status = model.append(st, kp, vp, s.k64, s.v64, s.q64, freq, dims, inter)
+    assert status.tolist() == want_status and (want is None or want_status == want)
+    gk, gv = (p.double().cpu().numpy().reshape(-1, s.Hk, s.D) for p in s.dpools)
+    assert np.array_equal(gv, vp)
+    same = np.all(kp == old, axis=(1, 2))
+    assert np.array_equal(gk[same], old[same])
+    big = 4e-7 * 2 * np.abs(s.k64).max(initial=0)
+    assert np.all(np.abs(gk - kp) <= big + HALF[s.dt] * 1.01 * np.abs(kp))
+    kp[:] = gk                       # the pool holds rounded keys
+    if queries:
+        got = out.double().cpu().numpy()
+        rows = [e[1] + t for e in (st.entry(i, once=True) for i in range(s.n)) if e for t in range(e[2])]
+        big = 4e-7 * 2 * np.abs(s.q64).max(initial=0)
+        assert np.all(np.abs(got[rows] - q[rows]) <= big + HALF[s.dt] * 1.01 * np.abs(q[rows]))
+        rest = np.setdiff1d(np.arange(s.rows), rows)
+        assert np.all(got[rest] == (s.q64[rest] if in_place else 7))
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("inter", [0, 1])
+@pytest.mark.parametrize("H,Hk,D,dims,pad", [(4, 2, 64, 64, 0), (8, 8, 128, 64, 0), (3, 1, 80, 80, 0), (6, 2, 80, 24, 1),
+                                             (2, 1, 256, 256, 8), (4, 2, 64, 2, 0), (4, 2, 64, 0, 3), (1, 1, 8, 8, 0)])
+@pytest.mark.parametrize("lens,counts", [([0], [1]), ([17, 1000, 5], [9, 1, 64]), ([300, 2], [4, 5])])
+def test_append_shapes(dt, inter, H, Hk, D, dims, pad, lens, counts):
+    s = Setup(dt, H, Hk, D, 7, lens, counts, seed=D + dims + pad, pad=pad).device()
+    check_append(s, dims, inter, queries=dims != 2, in_place=dims == 24)
+
+
+@pytest.mark.parametrize("given", [True, False])
+@pytest.mark.parametrize("counts", [[700, 65, 1], [200, 200, 200]])
+def test_append_prompts(given, counts):
+    check_append(Setup("bf16", 4, 2, 64, 16, [0, 30, 5], counts, parents=False, given=given).device(), 64, 0)
+
+
+@pytest.mark.parametrize("base", [10000.0, 1e6])
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_append_far_positions(dt, base):
+    """Angles of a million radians are reduced in 64 bits; only the last pages are there."""
+    s = Setup(dt, 2, 1, 64, 1024, [0], [40])
+    S = len(s.blocks)
+    q = s.given["seqs"][0]
+    s.mb = 1100
+    tables = np.full((S, s.mb), -1, np.int32)
+    tables[q, 1099], tables[q, 1098] = s.tables[q, 0], (s.tables[q, 0] + 1) % s.P
+    s.tables = tables
+    s.blocks[q], s.lengths[q] = 1100, 1099 * 1024 - 10
+    check_append(s.device(), 64, 0, base=base)
+
+
+def test_append_without_pages_writes_nothing_there():
+    s = Setup("bf16", 4, 2, 64, 8, [30, 20], [12, 4], seed=1)
+    q = s.given["seqs"][0]
+    s.tables[q, 4] = s.P + 3
+    check_append(s.device(), 64, 0)
+
+
+def test_append_copies_bits():
+    """Values and what is not rotated keep their bits, NaN's among them."""
+    s = Setup("bf16", 2, 2, 64, 8, [3], [5], parents=False)
+    bits = torch.randint(-2 ** 15, 2 ** 15, (s.rows, 2, 64), dtype=torch.int16)
+    s.v = bits.view(torch.bfloat16)
+    s.device()
+    sv.specverify_attn_append(s.h, None, 0, 1, s.n, s.max_count, s.rows, s.nodes, None, s.dk, s.wide, s.dv,
+                              s.wide)
+    torch.cuda.synchronize()
+    st = s.step()
+    q, a, m, ln, _ = st.entry(0)
+    at = [st.slot(q, ln + t) for t in range(m)]
+    assert torch.equal(s.dpools[1].view(torch.int16).view(-1, 2, 64)[at].cpu(), bits[a:a + m])
+
+
+# ---------------------------------------------------------------------------------- streams and graphs
+
+def test_another_stream_and_a_replayed_graph():
+    s = Setup("bf16", 8, 2, 128, 16, [700, 90], [8, 5], seed=6).device()
+    freq = dev((10000.0 ** (-np.arange(64) / 64)).astype(np.float32))
+    rot = sv.SpecVerifyRotation(freq, 128)
+    out = torch.zeros(s.rows, 8, 128, dtype=torch.bfloat16, device="cuda")
+    turned = torch.zeros_like(out)
+
+    def both(stream):
+        sv.specverify_attn_append(s.h, stream, 0, 1, s.n, s.max_count, s.rows, s.nodes, rot, s.dk, s.wide, s.dv,
+                                  s.wide, s.dq, s.wide, turned, 1024)
+        sv.specverify_attn_attend(s.h, stream, 0, 1, s.n, s.max_count, s.rows, s.nodes, 0.09, 0, turned, 1024,
+                                  out, 1024)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    both(side)
+    torch.cuda.synchronize()
+    first = out.clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        both(side)
+    for i in range(4):
+        # other inputs and lengths in the same places, eager work between the replays
+        s.dk.copy_(torch.randn_like(s.dk))
+        s.dq.copy_(torch.randn_like(s.dq))
+        s.state[3].sub_(torch.tensor([7], dtype=torch.int32, device="cuda") * (s.state[3] > 7))
+        out.zero_()
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        got = out.clone()
+        out.zero_()
+        both(None)
+        torch.cuda.synchronize()
+        assert torch.equal(got, out) and not torch.equal(got, first)
+
+
+def test_two_handles_on_two_streams():
+    a = Setup("bf16", 8, 2, 128, 16, [5000], [8], seed=1).device()
+    b = Setup("bf16", 8, 2, 128, 16, [4000, 100], [5, 9], seed=2).device()
+    want = [x.attend(0.09)[0] for x in (a, b)]
+    sides = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(10):
+        outs = [torch.zeros(x.rows, 8, 128, dtype=torch.bfloat16, device="cuda") for x in (a, b)]
+        torch.cuda.synchronize()
+        for x, o, st in zip((a, b), outs, sides):
+            sv.specverify_attn_attend(x.h, st, 0, 1, x.n, x.max_count, x.rows, x.nodes, 0.09, 0, x.dq, x.wide,
+                                      o, 1024)
+        torch.cuda.synchronize()
+        for x, o, w in zip((a, b), outs, want):
+            rows = [e[1] + t for e in (x.step().entry(i) for i in range(x.n)) for t in range(e[2])]
+            assert torch.equal(o[rows], w[rows])
+
+
+def test_the_cache_may_go_first():
+    s = Setup("f32", 2, 1, 64, 8, [9], [2]).device()
+    s.check_attend()
+    sv.specverify_cache_destroy(s.cache)
+    del s.cache
+    sv.specverify_attn_destroy(s.h)
+    del s.h
+    torch.cuda.synchronize()
+
+
+# ---------------------------------------------------------------------------------- refusals
+
+def test_host_refusals_touch_nothing():
+    s = Setup("bf16", 4, 2, 64, 8, [9, 5], [2, 3]).device(max_nodes=5)
+    lib, byref = sv.load(), sv.ctypes.byref
+    I, C = sv.SPECVERIFY_EINVAL, sv.SPECVERIFY_ECAPACITY
+    out = torch.full((s.rows, 4, 64), 7.0, dtype=torch.bfloat16, device="cuda")
+    nodes = byref(s.nodes)
+    q, k, v, o = (x.data_ptr() for x in (s.dq, s.dk, s.dv, out))
+    good = dict(kp=0, vp=1, n=2, m=3, rows=s.rows, nodes=nodes, scale=1.0, window=0, q=q, qs=s.wide, o=o, os=256, lse=None,
+                st=None)
+
+    def attend(**kw):
+        a = dict(good, **kw)
+        return lib.specverify_attn_attend(s.h, None, a["kp"], a["vp"], a["n"], a["m"], a["rows"], a["nodes"],
+                                          a["scale"], a["window"], a["q"], a["qs"], a["o"], a["os"], a["lse"], a["st"])
+
+    for kw, want in ((dict(kp=2), I), (dict(vp=-1), I), (dict(n=-1), I), (dict(m=-1), I), (dict(rows=-1), I),
+                     (dict(scale=float("nan")), I), (dict(scale=float("inf")), I), (dict(window=-1), I),
+                     (dict(q=None), I), (dict(q=q + 1), I), (dict(qs=255), I), (dict(qs=2 ** 62), I), (dict(o=None), I),
+                     (dict(o=o + 1), I), (dict(os=255), I), (dict(lse=o + 2), I), (dict(st=o + 2), I), (dict(n=3), C),
+                     (dict(m=6), C), (dict(n=0, q=None), 0), (dict(nodes=byref(sv.SpecVerifyNodes(starts=256 + 2))), I)):
+        assert attend(**kw) == want, kw
+
+    rot = lambda f, d: byref(sv.SpecVerifyRotation(f, d))  # noqa: E731
+    good2 = dict(n=2, m=3, rows=s.rows, nodes=nodes, rot=None, k=k, ks=s.wide, v=v, vs=s.wide, q=q, qs=s.wide, o=o, os=256,
+                 st=None, kp=0, vp=1)
+
+    def append(**kw):
+        a = dict(good2, **kw)
+        return lib.specverify_attn_append(s.h, None, a["kp"], a["vp"], a["n"], a["m"], a["rows"], a["nodes"], a["rot"],
+                                          a["k"], a["ks"], a["v"], a["vs"], a["q"], a["qs"], a["o"], a["os"], a["st"])
+
+    for kw, want in ((dict(kp=-1), I), (dict(vp=9), I), (dict(n=-1), I), (dict(n=4), C), (dict(m=65), C),
+                     (dict(rot=rot(256, 66)), I), (dict(rot=rot(256, 3)), I), (dict(rot=rot(256, -2)), I),
+                     (dict(rot=rot(None, 8)), I), (dict(rot=rot(258, 8)), I), (dict(k=None), I), (dict(k=k + 1), I),
+                     (dict(ks=127), I), (dict(v=None), I), (dict(vs=0), I), (dict(o=None), I), (dict(os=255), I),
+                     (dict(o=q, os=s.wide + 8), I), (dict(st=o + 1), I), (dict(n=2, m=2 ** 31 - 1, nodes=None), C)):
+        assert append(**kw) == want, kw
+    assert lib.specverify_cache_keep_path(s.cache, None, 2, 0, None, 256, 256, None) == I
+    assert lib.specverify_cache_keep_path(s.cache, None, 2, 65, None, 256, 256, None) == C
+    assert lib.specverify_cache_keep_path(s.cache, None, 9, 2, None, 256, 256, None) == C
+    assert lib.specverify_cache_keep_path(s.cache, None, 2, 2, None, None, 256, None) == I
+    assert lib.specverify_cache_keep_path(s.cache, None, 2, 2, None, 256, 257, None) == I
+    h = sv.ctypes.c_void_p()
+    create = lambda dt=1, H=4, Hk=2, D=64, n=2, m=4: lib.specverify_attn_create(  # noqa: E731
+        byref(h), s.cache, dt, H, Hk, D, n, m)
+    for kw, want in ((dict(dt=2), sv.SPECVERIFY_EUNSUPPORTED), (dict(H=5), I), (dict(H=0), I), (dict(Hk=0), I), (dict(D=0), I),
+                     (dict(D=60), I), (dict(D=32), I), (dict(Hk=1), I), (dict(dt=0), I), (dict(n=0), I), (dict(m=0), I),
+                     (dict(D=264), C), (dict(m=65), C), (dict(n=2 ** 16 + 1), C), (dict(H=2 ** 17), C)):
+        assert create(**kw) == want and not h.value, kw
+    torch.cuda.synchronize()
+    assert torch.all(out == 7)
+    for p, d in zip(s.pools, s.dpools):
+        assert torch.equal(p[0], d.cpu())
+    # a page that is not a whole number of tokens moves nothing
+    refs, tab, one = (torch.zeros(k, dtype=torch.int32, device="cuda") for k in (4, 4, 2))
+    c = sv.specverify_cache_create(0, 4, 3, 2, 2, 16, [torch.zeros(64, dtype=torch.uint8, device="cuda")], refs, tab, one,
+                                   one)
+    assert lib.specverify_cache_keep_path(c, None, 1, 2, None, 256, 256, None) == I
+    assert lib.specverify_attn_create(byref(h), c, 1, 1, 1, 8, 1, 1) == I
+    sv.specverify_cache_destroy(c)
+
+
+def test_greedy_tree_refusals():
+    lib = sv.load()
+    ctx = sv.specverify_create(0, 2, 7, 100)
+    x = torch.zeros(2 * 8 * 100, dtype=torch.bfloat16, device="cuda").data_ptr()
+    f = lambda dt=1, B=2, T=8, V=100, d=3, p=x, t=x, par=x, c=None, o=x: lib.specverify_run_greedy_tree(  # noqa: E731
+        ctx, None, dt, B, T, V, d, p, t, par, c, o, o, o)
+    I, C = sv.SPECVERIFY_EINVAL, sv.SPECVERIFY_ECAPACITY
+    for kw, want in ((dict(T=0), I), (dict(d=-1), I), (dict(d=8), I), (dict(T=9), C), (dict(B=3), C), (dict(V=101), C),
+                     (dict(B=-1), I), (dict(dt=5), sv.SPECVERIFY_EUNSUPPORTED), (dict(p=None), I), (dict(t=None), I),
+                     (dict(par=None), I), (dict(o=None), I), (dict(o=x + 2), I), (dict(p=x + 1), I), (dict(c=x + 1), I),
+                     (dict(B=0, p=None), 0)):
+        assert f(**kw) == want, kw
+    sv.specverify_destroy(ctx)
