@@ -926,12 +926,7 @@ int specverify_attn_create(specverify_attn **out, const specverify_cache *cache,
         return SPECVERIFY_EHIP;
 
     const int group = q_heads / kv_heads;
-    // the most rows that parts of any call leave: twice the parts that fill the chip, for each tile
-    int64_t rows = 0;
-    for (int m = 1; m <= max_nodes; ++m) {
-        const int tiles = sv::attend_row_tiles(dtype, head_dim, m * group);
-        rows = std::max<int64_t>(rows, 2ll * sv::attend_units(cache->num_cus, tiles) * 16 * tiles);
-    }
+    const int64_t rows = sv::attend_kept_rows(cache->num_cus);
     const size_t b_plan = align_up((size_t)max_entries * sizeof(sv::AttnPlan));
     const size_t b_ml = align_up((size_t)rows * sizeof(float2));
     const size_t b_o = align_up((size_t)rows * head_dim * sizeof(float));

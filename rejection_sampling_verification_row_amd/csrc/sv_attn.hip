@@ -26,6 +26,7 @@ namespace {
 
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
 
 constexpr float LOG2E = 1.4426950408889634f;
 constexpr float LN2 = 0.6931471805599453f;
@@ -119,7 +120,7 @@ struct AttnArgs {
     int units;           // parts that fill the chip
 };
 
-__device__ inline int64_t block_sum(int64_t v, int64_t *lds)
+template <int WG_SIZE> __device__ inline int64_t block_sum(int64_t v, int64_t *lds)
 {
 #pragma unroll
     for (int o = 32; o > 0; o >>= 1)
@@ -128,11 +129,14 @@ __device__ inline int64_t block_sum(int64_t v, int64_t *lds)
     if ((threadIdx.x & 63) == 0)
         lds[threadIdx.x >> 6] = v;
     __syncthreads();
-    return lds[0] + lds[1] + lds[2] + lds[3];
+    int64_t all = 0;
+    for (int i = 0; i < WG_SIZE / 64; ++i)
+        all += lds[i];
+    return all;
 }
 
 // Inclusive over the workgroup's threads; *all is the sum.
-__device__ inline int64_t block_scan(int64_t v, int64_t *lds, int64_t *all)
+template <int WG_SIZE> __device__ inline int64_t block_scan(int64_t v, int64_t *lds, int64_t *all)
 {
     const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
 #pragma unroll
@@ -145,10 +149,12 @@ __device__ inline int64_t block_scan(int64_t v, int64_t *lds, int64_t *all)
     if (lane == 63)
         lds[w] = v;
     __syncthreads();
-    int64_t before = 0;
-    for (int i = 0; i < w; ++i)
-        before += lds[i];
-    *all = lds[0] + lds[1] + lds[2] + lds[3];
+    int64_t before = 0, sum = 0;
+    for (int i = 0; i < WG_SIZE / 64; ++i) {
+        before += i < w ? lds[i] : 0;
+        sum += lds[i];
+    }
+    *all = sum;
     return before + v;
 }
 
@@ -176,9 +182,9 @@ struct Part {
 
 // This workgroup's part.  Workgroup 0 also leaves the plan for the join, and the status of entries
 // that have no part.
-template <int KT> __device__ Part find_part(const AttnArgs &a, int rows_per_tile, int least)
+template <int WG_SIZE, int KT> __device__ Part find_part(const AttnArgs &a, int rows_per_tile, int least)
 {
-    __shared__ int64_t lds[4];
+    __shared__ int64_t lds[WG_SIZE / 64];
     __shared__ Part found;
     const int n = a.nv.n, t = threadIdx.x;
     Entry e0 = {-1, 0, -1, 0};
@@ -186,7 +192,7 @@ template <int KT> __device__ Part find_part(const AttnArgs &a, int rows_per_tile
         e0 = load_entry(a.c, a.nv, t);
     const Work w0 = entry_work<KT>(a, e0, rows_per_tile);
     auto work = [&](int i, Entry &e) {
-        if (i < ATTN_WG) {
+        if (i < WG_SIZE) {
             e = e0;
             return w0;
         }
@@ -194,22 +200,22 @@ template <int KT> __device__ Part find_part(const AttnArgs &a, int rows_per_tile
         return entry_work<KT>(a, e, rows_per_tile);
     };
     int64_t sum = 0;
-    for (int i = t; i < n; i += ATTN_WG) {
+    for (int i = t; i < n; i += WG_SIZE) {
         Entry e;
         const Work w = work(i, e);
         sum += (int64_t)w.segments * w.tiles;
     }
-    sum = block_sum(sum, lds);
+    sum = block_sum<WG_SIZE>(sum, lds);
     const int per = (int)max((sum + a.units - 1) / a.units, (int64_t)least);   // tiles of a part
     if (t == 0)
         found = {-1, 0, 0, 0};
     int64_t total = 0;
-    for (int i = t; i < n; i += ATTN_WG) {
+    for (int i = t; i < n; i += WG_SIZE) {
         Entry e;
         const Work w = work(i, e);
         total += (int64_t)w.segments * ((w.tiles + per - 1) / per);
     }
-    total = block_sum(total, lds);
+    total = block_sum<WG_SIZE>(total, lds);
     // neighbours, which read the same tokens, on one of the 8 dies, to which workgroups go in turn
     const int64_t each = (total + 7) / 8;
     const int64_t mine = (int64_t)(blockIdx.x & 7) * each + (blockIdx.x >> 3);
@@ -217,7 +223,7 @@ template <int KT> __device__ Part find_part(const AttnArgs &a, int rows_per_tile
     if (none && blockIdx.x != 0)
         return {-1, 0, 0, 0};
     int64_t base = 0;                    // parts in the upper half, kept ones in the lower
-    for (int i0 = 0; i0 < n; i0 += ATTN_WG) {
+    for (int i0 = 0; i0 < n; i0 += WG_SIZE) {
         const int i = i0 + t;
         Entry e = {-1, 0, -1, 0};
         Work w = {0, 0, 0, 0};
@@ -226,7 +232,7 @@ template <int KT> __device__ Part find_part(const AttnArgs &a, int rows_per_tile
         const int chunks = (w.tiles + per - 1) / per, parts = w.segments * chunks;
         const int kept = chunks > 1 ? parts : 0;
         int64_t all;
-        const int64_t inc = base + block_scan(((int64_t)parts << 32) + kept, lds, &all);
+        const int64_t inc = base + block_scan<WG_SIZE>(((int64_t)parts << 32) + kept, lds, &all);
         const int64_t first = (inc >> 32) - parts;
         const int at = (int)(inc & 0xffffffff) - kept;
         if (i < n && !none && mine >= first && mine < first + parts)
@@ -278,70 +284,75 @@ __device__ inline float row_sum(float v)
     return v + xch<5>(v);
 }
 
-// DP: head_dim or more; VW: elements of a value row that a lane loads at once, 16 lanes side by
-// side; R: tiles of 16 rows.  Left operands of the products: row lane % 16, 16 bytes (4 for float32)
-// of the axis summed over to each of the four groups lane / 16; right ones likewise with columns;
-// results: column lane % 16, rows 4 (lane / 16) + r.
-template <int DT, int DP, int VW, int R, int OCC>
-__global__ __launch_bounds__(ATTN_WG, OCC) void k_attend(AttnArgs a)
-{
-    typedef Tile<DT> TL;
-    constexpr int ES = TL::ES, KT = TL::KT, SUB = KT / 16, KPL = KT / 4;
-    constexpr int KS = DP * ES / 64;              // 16-byte pieces of a key row to a lane
-    constexpr int NB = DP / (16 * VW);            // pieces of a value row to a lane
-    constexpr int NT = DP / 16;
-    constexpr int ROWS = 16 * R, PITCH = DP + 4;
-    typedef typename Chunk<VW * ES>::type vchunk;
-
-    __shared__ float s_o[4][ROWS][PITCH];
-    __shared__ float2 s_ml[4][ROWS];
-    __shared__ int64_t s_off[4][2][KT];
-
-    const int lane = threadIdx.x & 63, w = uniform(threadIdx.x >> 6), col = lane & 15, grp = lane >> 4;
-    const Part part = find_part<KT>(a, ROWS, 128 / KT);
-    if (part.entry < 0)
-        return;
-    const Entry e = load_entry(a.c, a.nv, part.entry);
-    const Work work = entry_work<KT>(a, e, ROWS);
-    uint64_t lane_seen;
+// What a workgroup works on: a segment's rows, and the tiles t0 .. t1 of its tokens.
+struct Job {
+    Entry e;
+    int head, mt, t0, t1, rows, total, chunks;
+    int64_t kept;                        // its place among the kept parts
+    bool ok;
+    uint64_t lane_seen;                  // lane_node of the entry's nodes
     int lane_depth;
-    const bool ok = lane_node(a.nv.parents ? a.nv.parents + e.start : nullptr, e.count, a.window, lane_seen,
-                              lane_depth);
-    if (part.local == 0 && threadIdx.x == 0) {
-        a.a.plan[part.entry].ok = ok;
-        if (a.status)
-            a.status[part.entry] = ok ? 0 : -1;
-    }
-    if (!ok)
-        return;
-    const int mt = part.local % work.tiles_of_rows, hc = part.local / work.tiles_of_rows;
-    const int head = hc % a.a.kv_heads, chunk = hc / a.a.kv_heads;
-    const int t0 = work.low + (int)((int64_t)work.tiles * chunk / part.chunks);
-    const int t1 = work.low + (int)((int64_t)work.tiles * (chunk + 1) / part.chunks);
-    const int D = a.a.head_dim, G = a.a.group, rows = e.count * G;
-    const int len = e.len, total = len + e.count;
+};
 
-    // the rows of this lane's columns: what they see, and their queries
+template <int WG_SIZE, int KT> __device__ inline Job take_job(const AttnArgs &a, int rows_per_tile, int least)
+{
+    Job j;
+    const Part part = find_part<WG_SIZE, KT>(a, rows_per_tile, least);
+    j.ok = false;
+    if (part.entry < 0)
+        return j;
+    j.e = load_entry(a.c, a.nv, part.entry);
+    const Work work = entry_work<KT>(a, j.e, rows_per_tile);
+    j.ok = lane_node(a.nv.parents ? a.nv.parents + j.e.start : nullptr, j.e.count, a.window, j.lane_seen,
+                     j.lane_depth);
+    if (part.local == 0 && threadIdx.x == 0) {
+        a.a.plan[part.entry].ok = j.ok;
+        if (a.status)
+            a.status[part.entry] = j.ok ? 0 : -1;
+    }
+    const int hc = part.local / work.tiles_of_rows, chunk = hc / a.a.kv_heads;
+    j.mt = part.local - hc * work.tiles_of_rows;
+    j.head = hc - chunk * a.a.kv_heads;
+    j.t0 = work.low + (int)((int64_t)work.tiles * chunk / part.chunks);
+    j.t1 = work.low + (int)((int64_t)work.tiles * (chunk + 1) / part.chunks);
+    j.rows = j.e.count * a.a.group;
+    j.total = j.e.len + j.e.count;
+    j.chunks = part.chunks;
+    j.kept = part.kept + part.local;
+    return j;
+}
+
+// The rows of a lane's columns: what they see, and from where on.
+template <int R> struct Rows {
     uint64_t seen[R];
     int low[R];
-    typename TL::vec q[R][KS];
-    int low_most = 0;
+    int low_most;
+};
+
+// A wave's R tiles of rows from `first` on, with their queries as right operands.
+template <int DT, int KS, int R>
+__device__ inline void load_rows(const AttnArgs &a, const Job &j, int first, Rows<R> &rows,
+                                 typename Tile<DT>::vec (&q)[R][KS])
+{
+    constexpr int ES = Tile<DT>::ES;
+    const int col = threadIdx.x & 15, grp = threadIdx.x >> 4 & 3, D = a.a.head_dim, G = a.a.group;
+    rows.low_most = 0;
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-        const int row = mt * ROWS + r * 16 + col;
-        const int node = row < rows ? divide(row, a.a.by_group) : 0;
-        seen[r] = __shfl((unsigned long long)lane_seen, node);
-        const int depth = __shfl(lane_depth, node);
-        low[r] = a.window > 0 ? max(len - a.window + 1 + depth, 0) : 0;
-        low_most = max(low_most, low[r]);
-        const char *qp = a.q + (int64_t)(e.start + node) * a.q_stride +
-                         (int64_t)(head * G + row - node * G) * D * ES;
+        const int row = first + r * 16 + col;
+        const int node = row < j.rows ? divide(row, a.a.by_group) : 0;
+        rows.seen[r] = __shfl((unsigned long long)j.lane_seen, node);
+        const int depth = __shfl(j.lane_depth, node);
+        rows.low[r] = a.window > 0 ? max(j.e.len - a.window + 1 + depth, 0) : 0;
+        rows.low_most = max(rows.low_most, rows.low[r]);
+        const char *qp = a.q + (int64_t)(j.e.start + node) * a.q_stride +
+                         (int64_t)(j.head * G + row - node * G) * D * ES;
         const bool al = aligned16(qp);
 #pragma unroll
         for (int s = 0; s < KS; ++s) {
             const int d = (s * 64 + grp * 16) / ES;
             uint4 v = make_uint4(0, 0, 0, 0);
-            if (row < rows && d < D) {
+            if (row < j.rows && d < D) {
                 if (al) {
                     v = load_plain(qp + d * ES);
                 } else if constexpr (DT == 1) {
@@ -359,18 +370,141 @@ __global__ __launch_bounds__(ATTN_WG, OCC) void k_attend(AttnArgs a)
                 const uint32_t f = DT == 1 ? 0x80008000u : 0x80000000u;
                 v = make_uint4(v.x ^ f, v.y ^ f, v.z ^ f, v.w ^ f);
             }
-            q[r][s] = __builtin_bit_cast(typename TL::vec, v);
+            q[r][s] = __builtin_bit_cast(typename Tile<DT>::vec, v);
         }
     }
 #pragma unroll
     for (int o = 8; o > 0; o >>= 1)
-        low_most = max(low_most, __shfl_xor(low_most, o));
-    low_most = uniform(low_most);
+        rows.low_most = max(rows.low_most, __shfl_xor(rows.low_most, o));
+    rows.low_most = uniform(rows.low_most);
+}
 
-    const int *table = a.c.tables + (size_t)e.seq * a.c.max_blocks;
+// Which of the 32 tokens from j0 on a row sees, as bits.
+__device__ inline uint32_t visible(int len, int low, uint64_t seen, int j0, uint32_t lost)
+{
+    const int back = len - j0, from = low - j0;
+    uint32_t v = back >= 32 ? ~0u : back > 0 ? (1u << back) - 1 : 0;
+    v = from >= 32 ? 0 : from > 0 ? v & (~0u << from) : v;
+    if (back <= 0)
+        v |= back > -64 ? (uint32_t)(seen >> -back) : 0;
+    else if (back < 32)
+        v |= (uint32_t)seen << back;
+    return v & ~lost;
+}
+
+// Scores of a tile become weights against the running maximum m (of the raw scores); what was summed
+// before is scaled where the maximum grew.
+template <int SUB, int NT>
+__device__ inline void weigh(f32x4 (&s)[SUB], f32x4 (&o)[NT], float &m, float &l, float c1)
+{
+    float top = s[0][0];
+#pragma unroll
+    for (int x = 0; x < SUB; ++x)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            top = fmaxf(top, s[x][i]);
+    if (__ballot(top > m) != 0) {
+        const float was = m;
+        m = fmaxf(was, row_max(top));
+        const float f = m == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f((was - m) * c1);
+        l *= f;
+#pragma unroll
+        for (int i = 0; i < NT; ++i)
+            o[i] *= f;
+    }
+    const float ref = m == -INFINITY ? 0.0f : m * c1;
+#pragma unroll
+    for (int x = 0; x < SUB; ++x)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            s[x][i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[x][i], c1, -ref));
+            l += s[x][i];
+        }
+}
+
+// The sums of `waves` waves over one tile of rows, joined, to the output or to the kept parts: row i
+// at o[wave * wave_step + i], its maximum and sum at ml of the same index; rows is how many are there.
+template <int DT, int WG_SIZE, int PITCH>
+__device__ inline void finish(const AttnArgs &a, const Job &j, int first, int rows, int rows_per_tile,
+                              const float (*o)[PITCH], const float2 *ml, int waves, int wave_step, int thread,
+                              int threads)
+{
+    constexpr int ES = Tile<DT>::ES;
+    const int D = a.a.head_dim, G = a.a.group;
+    for (int i = thread; i < rows * (D / 4); i += threads) {
+        const int row = i / (D / 4), d = (i - row * (D / 4)) * 4;
+        float top = -INFINITY;
+        for (int k = 0; k < waves; ++k)
+            top = fmaxf(top, ml[k * wave_step + row].x);
+        float z = 0.0f, acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        for (int k = 0; k < waves; ++k) {
+            const float2 p = ml[k * wave_step + row];
+            const float f = p.x == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(p.x - top);
+            z += f * p.y;
+            const float4 v = *reinterpret_cast<const float4 *>(&o[k * wave_step + row][d]);
+            acc[0] += f * v.x;
+            acc[1] += f * v.y;
+            acc[2] += f * v.z;
+            acc[3] += f * v.w;
+        }
+        if (j.chunks > 1) {
+            const int64_t at = j.kept * rows_per_tile + first - j.mt * rows_per_tile + row;
+            *reinterpret_cast<float4 *>(a.a.part_o + at * D + d) = make_float4(acc[0], acc[1], acc[2], acc[3]);
+            if (d == 0)
+                a.a.part_ml[at] = make_float2(top, z);
+            continue;
+        }
+        const int gr = first + row, node = divide(gr, a.a.by_group), qh = j.head * G + gr - node * G;
+        char *to = a.out + (int64_t)(j.e.start + node) * a.out_stride + ((int64_t)qh * D + d) * ES;
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+            const float v = z == 0.0f ? 0.0f : acc[x] / z;
+            if constexpr (DT == 1)
+                reinterpret_cast<__bf16 *>(to)[x] = (__bf16)v;
+            else
+                reinterpret_cast<float *>(to)[x] = v;
+        }
+        if (a.lse && d == 0)
+            a.lse[(int64_t)(j.e.start + node) * a.a.q_heads + qh] =
+                z == 0.0f ? -INFINITY : (top + log2f(z)) * LN2;
+    }
+}
+
+// Few rows: each of four waves has tiles of tokens of its own, whose keys and values it loads into
+// registers a tile ahead.
+//
+// DP: head_dim or more; VW: elements of a value row that a lane loads at once, 16 lanes side by
+// side; R: tiles of 16 rows.  Left operands of the products: row lane % 16, 16 bytes (4 for float32)
+// of the axis summed over to each of the four groups lane / 16; right ones likewise with columns;
+// results: column lane % 16, rows 4 (lane / 16) + r.
+template <int DT, int DP, int VW, int R, int OCC>
+__global__ __launch_bounds__(ATTN_WG, OCC) void k_attend(AttnArgs a)
+{
+    typedef Tile<DT> TL;
+    constexpr int ES = TL::ES, KT = TL::KT, SUB = KT / 16, KPL = KT / 4;
+    constexpr int KS = DP * ES / 64;              // 16-byte pieces of a key row to a lane
+    constexpr int NB = DP / (16 * VW);            // pieces of a value row to a lane
+    constexpr int NT = DP / 16;
+    constexpr int ROWS = 16 * R, PITCH = DP + 4;
+    typedef typename Chunk<VW * ES>::type vchunk;
+
+    __shared__ float s_o[4 * ROWS][PITCH];
+    __shared__ float2 s_ml[4 * ROWS];
+    __shared__ int64_t s_off[4][2][KT];
+
+    const int lane = threadIdx.x & 63, w = uniform(threadIdx.x >> 6), col = lane & 15, grp = lane >> 4;
+    const Job job = take_job<ATTN_WG, KT>(a, ROWS, 128 / KT);
+    if (!job.ok)
+        return;
+    const int D = a.a.head_dim, len = job.e.len, total = job.total, t1 = job.t1;
+    Rows<R> rows;
+    typename TL::vec q[R][KS];
+    load_rows<DT, KS, R>(a, job, job.mt * ROWS, rows, q);
+
+    const int *table = a.c.tables + (size_t)job.e.seq * a.c.max_blocks;
     const int64_t row_bytes = (int64_t)a.a.kv_heads * D * ES;
-    const char *kp = a.c.pools[a.key_pool] + (int64_t)head * D * ES;
-    const char *vp = a.c.pools[a.value_pool] + (int64_t)head * D * ES;
+    const char *kp = a.c.pools[a.key_pool] + (int64_t)job.head * D * ES;
+    const char *vp = a.c.pools[a.value_pool] + (int64_t)job.head * D * ES;
 
     // a tile's page ids, one token to a lane, then the tokens' places; bits of what has no place
     auto page_of = [&](int tile) {
@@ -425,8 +559,8 @@ __global__ __launch_bounds__(ATTN_WG, OCC) void k_attend(AttnArgs a)
             o[r][i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     }
 
-    int t = t0 + w, buf = 0, next_page = 0;
-    const int last = t1 - 1 - (t1 - 1 - t0 - w & 3);     // this wave's last tile
+    int t = job.t0 + w, buf = 0, next_page = 0;
+    const int last = t1 - 1 - (t1 - 1 - t & 3);          // this wave's last tile
     uint32_t lost = 0;
     if (t < t1) {
         lost = put_places(t, page_of(t), 0);
@@ -468,19 +602,12 @@ __global__ __launch_bounds__(ATTN_WG, OCC) void k_attend(AttnArgs a)
         next_page = page_of(min(t + 8, last));
         load_keys(buf ^ 1);
         const unsigned j0 = (unsigned)t * KT;
-        const bool masked = j0 + KT > (unsigned)len || lost != 0 || (int)j0 < low_most;
-        uint32_t vis[R];                 // the tile's tokens that a row sees, as bits
+        const bool masked = j0 + KT > (unsigned)len || lost != 0 || (int)j0 < rows.low_most;
+        uint32_t vis[R];                 // the tile's tokens that a row sees
         if (masked) {
 #pragma unroll
             for (int r = 0; r < R; ++r) {
-                const int back = len - (int)j0, from = low[r] - (int)j0;
-                uint32_t v = back >= 32 ? ~0u : back > 0 ? (1u << back) - 1 : 0;
-                v = from >= 32 ? 0 : from > 0 ? v & (~0u << from) : v;
-                if (back <= 0)
-                    v |= back > -64 ? (uint32_t)(seen[r] >> -back) : 0;
-                else if (back < 32)
-                    v |= (uint32_t)seen[r] << back;
-                vis[r] = v & ~lost;
+                vis[r] = visible(len, rows.low[r], rows.seen[r], (int)j0, lost);
 #pragma unroll
                 for (int x = 0; x < SUB; ++x)
 #pragma unroll
@@ -489,31 +616,8 @@ __global__ __launch_bounds__(ATTN_WG, OCC) void k_attend(AttnArgs a)
             }
         }
 #pragma unroll
-        for (int r = 0; r < R; ++r) {
-            float top = s[r][0][0];
-#pragma unroll
-            for (int x = 0; x < SUB; ++x)
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    top = fmaxf(top, s[r][x][i]);
-            if (__ballot(top > m[r]) != 0) {
-                const float was = m[r];
-                m[r] = fmaxf(was, row_max(top));
-                const float f = m[r] == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f((was - m[r]) * a.c1);
-                l[r] *= f;
-#pragma unroll
-                for (int i = 0; i < NT; ++i)
-                    o[r][i] *= f;
-            }
-            const float ref = m[r] == -INFINITY ? 0.0f : m[r] * a.c1;
-#pragma unroll
-            for (int x = 0; x < SUB; ++x)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    s[r][x][i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[r][x][i], a.c1, -ref));
-                    l[r] += s[r][x][i];
-                }
-        }
+        for (int r = 0; r < R; ++r)
+            weigh<SUB, NT>(s[r], o[r], m[r], l[r], a.c1);
         if (masked) {
             // What a row does not see may be anything: rows of values with an infinity or a NaN are left
             // out of the product and added to the rows that see them, one by one.
@@ -605,61 +709,266 @@ __global__ __launch_bounds__(ATTN_WG, OCC) void k_attend(AttnArgs a)
         lost = next_lost;
     }
 
-    // the four waves' sums, joined
 #pragma unroll
     for (int r = 0; r < R; ++r) {
         const float sum = row_sum(l[r]);
+        const int at = w * ROWS + r * 16 + col;
         if (grp == 0)
-            s_ml[w][r * 16 + col] = make_float2(m[r] == -INFINITY ? -INFINITY : m[r] * a.c1, sum);
+            s_ml[at] = make_float2(m[r] == -INFINITY ? -INFINITY : m[r] * a.c1, sum);
 #pragma unroll
         for (int b = 0; b < NB; ++b)
 #pragma unroll
             for (int i = 0; i < 4; ++i)
 #pragma unroll
                 for (int x = 0; x < VW; ++x)
-                    s_o[w][r * 16 + col][b * 16 * VW + (grp * 4 + i) * VW + x] = o[r][b * VW + x][i];
+                    s_o[at][b * 16 * VW + (grp * 4 + i) * VW + x] = o[r][b * VW + x][i];
     }
     __syncthreads();
-    const int here = min(rows - mt * ROWS, ROWS);
-    const int64_t kept = part.kept + part.local;
-    for (int i = threadIdx.x; i < here * (D / 4); i += ATTN_WG) {
-        const int row = i / (D / 4), d = (i - row * (D / 4)) * 4;
-        float top = -INFINITY;
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-            top = fmaxf(top, s_ml[k][row].x);
-        float z = 0.0f, acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const float2 ml = s_ml[k][row];
-            const float f = ml.x == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(ml.x - top);
-            z += f * ml.y;
-#pragma unroll
-            for (int x = 0; x < 4; ++x)
-                acc[x] += f * s_o[k][row][d + x];
+    finish<DT, ATTN_WG, PITCH>(a, job, job.mt * ROWS, min(job.rows - job.mt * ROWS, ROWS), ROWS, s_o, s_ml, 4, ROWS,
+                               threadIdx.x, ATTN_WG);
+}
+
+// The order of a row's 16-byte pieces in LDS: piece p of row r is at p ^ order(r).  Keys: 8 rows'
+// equal pieces in different banks; values: 4 rows' equal pairs of pieces.  (64 banks of 4 bytes: rows
+// of 128 bytes come in pairs.)
+template <int DP> __device__ inline int key_order(int row)
+{
+    return DP == 64 ? row >> 1 & 7 : row & 15;
+}
+template <int DP> __device__ inline int value_order(int row)
+{
+    return DP == 64 ? (row >> 1 & 3) * 2 : (row & 7) * 2;
+}
+
+// More rows, bfloat16: eight waves, WR of them side by side over the rows (16 R each) and 8 / WR
+// over the tokens, share what a stage of tokens brings from memory straight into LDS, DEPTH stages
+// ahead.  KB: blocks of 32 tokens that a wave has in a stage.
+//
+// LDS holds a token's row of a stage in 16-byte pieces in an order of the row's own, so that 16
+// lanes that read the same piece of 16 rows (keys), or 32 bytes of 4 rows (values, which the LDS
+// transposes on the way), touch all banks alike.
+template <int DP, int R, int WR, int KB, int STAGES>
+__global__ __launch_bounds__(ATTN_WIDE_WG, 1) void k_attend_wide(AttnArgs a)
+{
+    constexpr int WAVES8 = ATTN_WIDE_WG / 64, KG = WAVES8 / WR, TK = KG * KB * 32;
+    constexpr int KS = DP / 32, NT = DP / 16, PIECES = DP / 8, ROW = DP * 2;
+    constexpr int ROWS = 16 * R * WR, PITCH = DP + 4, DEPTH = STAGES - 1;
+    constexpr int HALF = TK * ROW, LOADS = HALF / 1024 / WAVES8;      // bytes of keys in a stage; a wave's loads
+    constexpr int PAGE_AHEAD = 2 * DEPTH + 1;
+    static_assert(LOADS * 1024 * WAVES8 == HALF && DEPTH <= 3 && TK <= ATTN_WIDE_WG, "whole loads, rings of 4 stages");
+    constexpr int MERGE = WAVES8 * 16 * R * PITCH * 4;
+    __shared__ __attribute__((aligned(1024))) char mem[MERGE > STAGES * 2 * HALF ? MERGE : STAGES * 2 * HALF];
+    __shared__ float2 s_ml[WAVES8 * 16 * R];
+    __shared__ int64_t s_off[4][TK];
+    __shared__ int s_page[4][TK < 64 ? 64 : TK];
+    __shared__ uint32_t s_lost[8][TK / 32];
+
+    const int t = threadIdx.x, lane = t & 63, w = uniform(t >> 6), col = lane & 15, grp = lane >> 4;
+    const int rw = w % WR, kg = w / WR;
+    const Job job = take_job<ATTN_WIDE_WG, TK>(a, ROWS, 1);
+    if (!job.ok)
+        return;
+    const int D = a.a.head_dim, len = job.e.len, total = job.total, stages = job.t1 - job.t0;
+    const int first = job.mt * ROWS + rw * 16 * R;
+    Rows<R> rows;
+    bf16x8 q[R][KS];
+    load_rows<1, KS, R>(a, job, first, rows, q);
+
+    const int *table = a.c.tables + (size_t)job.e.seq * a.c.max_blocks;
+    const int64_t row_bytes = (int64_t)a.a.kv_heads * D * 2;
+    const char *kp = a.c.pools[a.key_pool] + (int64_t)job.head * D * 2;
+    const char *vp = a.c.pools[a.value_pool] + (int64_t)job.head * D * 2;
+
+    auto token_of = [&](int stage, int i) {
+        return (int)min((unsigned)(job.t0 + stage) * TK + i, (unsigned)total - 1);
+    };
+    // from a stage's page ids the places of its tokens, and which have none
+    auto put_places = [&](int stage, int pg) {
+        if (t < TK) {
+            const int j = token_of(stage, t), b = divide(j, a.a.by_page);
+            const bool good = in_range(pg, a.c.num_pages);
+            s_off[stage & 3][t] = ((int64_t)(good ? pg : 0) * a.c.page_tokens + (j - b * a.c.page_tokens)) * row_bytes;
+            const uint64_t bad = __ballot(!good);
+            if ((lane & 31) == 0)
+                s_lost[stage & 7][t / 32] = (uint32_t)(bad >> (lane & 32));
         }
-        if (part.chunks > 1) {
-            float *to = a.a.part_o + (kept * ROWS + row) * (int64_t)D + d;
-            *reinterpret_cast<float4 *>(to) = make_float4(acc[0], acc[1], acc[2], acc[3]);
-            if (d == 0)
-                a.a.part_ml[kept * ROWS + row] = make_float2(top, z);
-            continue;
-        }
-        const int gr = mt * ROWS + row, node = divide(gr, a.a.by_group);
-        const int qh = head * G + gr - node * G;
-        char *to = a.out + (int64_t)(e.start + node) * a.out_stride + ((int64_t)qh * D + d) * ES;
+    };
+    // page ids of a stage, one load of every wave (waves past the stage's tokens repeat others')
+    auto load_pages = [&](int stage) {
+        const int part = w * 64 % (TK < 64 ? 64 : TK), i = (part + lane) % TK;
+        const int *p = table + divide(token_of(min(stage, stages - 1), i), a.a.by_page);
+        __builtin_amdgcn_global_load_lds((const SV_GLOBAL void *)p,
+                                         (__attribute__((address_space(3))) void *)&s_page[stage & 3][part], 4, 0, 0);
+    };
+    auto load_stage = [&](int stage) {
+        char *to = mem + stage % STAGES * 2 * HALF;
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
-            const float v = z == 0.0f ? 0.0f : acc[x] / z;
-            if constexpr (DT == 1)
-                reinterpret_cast<__bf16 *>(to)[x] = (__bf16)v;
-            else
-                reinterpret_cast<float *>(to)[x] = v;
+        for (int i = 0; i < LOADS; ++i) {
+            const int at = (i * WAVES8 + w) * 1024, row = (at + lane * 16) / ROW, slot = (at + lane * 16) % ROW / 16;
+            const int64_t off = s_off[stage & 3][row];
+            const int ck = slot ^ key_order<DP>(row), cv = slot ^ value_order<DP>(row);
+            const char *k = kp + off + (ck * 8 < D ? ck * 16 : 0), *v = vp + off + (cv * 8 < D ? cv * 16 : 0);
+            __builtin_amdgcn_global_load_lds((const SV_GLOBAL void *)k,
+                                             (__attribute__((address_space(3))) void *)(to + at), 16, 0, 0);
+            __builtin_amdgcn_global_load_lds((const SV_GLOBAL void *)v,
+                                             (__attribute__((address_space(3))) void *)(to + HALF + at), 16, 0, 0);
         }
-        if (a.lse && d == 0)
-            a.lse[(int64_t)(e.start + node) * a.a.q_heads + qh] =
-                z == 0.0f ? -INFINITY : (top + log2f(z)) * LN2;
+    };
+
+    f32x4 o[R][NT];
+    float m[R], l[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        m[r] = -INFINITY;
+        l[r] = 0.0f;
+#pragma unroll
+        for (int i = 0; i < NT; ++i)
+            o[r][i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     }
+    for (int s = 0; s <= DEPTH && s < stages; ++s)
+        if (t < TK)
+            put_places(s, load_global<int>(table + divide(token_of(s, t), a.a.by_page)));
+    __syncthreads();
+    for (int s = 0; s < DEPTH; ++s) {
+        load_pages(s + DEPTH + 1);
+        if (s < stages)
+            load_stage(s);
+    }
+
+    for (int i = 0; i < stages; ++i) {
+        // stage i and the page ids loaded with it are there; what came after may be under way
+        if (i + DEPTH <= stages)
+            asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"((DEPTH - 1) * (2 * LOADS + 1)) : "memory");
+        else
+            asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+        load_pages(i + PAGE_AHEAD);
+        if (i + DEPTH < stages)
+            load_stage(i + DEPTH);
+        if (i + DEPTH + 1 < stages && t < TK)
+            put_places(i + DEPTH + 1, s_page[i + DEPTH + 1 & 3][t]);
+        const char *keys = mem + i % STAGES * 2 * HALF, *vals = keys + HALF;
+#pragma unroll 1
+        for (int kb = 0; kb < KB; ++kb) {
+            const int b0 = (kg * KB + kb) * 32;
+            const unsigned j0 = (unsigned)(job.t0 + i) * TK + b0;
+            if (j0 >= (unsigned)total)
+                break;
+            f32x4 s[R][2];
+#pragma unroll
+            for (int r = 0; r < R; ++r)
+                s[r][0] = s[r][1] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int k = 0; k < KS; ++k)
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    const int row = b0 + x * 16 + col;
+                    u32x4 kv = *reinterpret_cast<const u32x4 *>(keys + row * ROW +
+                                                                ((k * 4 + grp) ^ key_order<DP>(row)) * 16);
+                    if (DP != D && (k * 4 + grp) * 8 >= D)
+                        kv = u32x4{0, 0, 0, 0};
+#pragma unroll
+                    for (int r = 0; r < R; ++r)
+                        s[r][x] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, kv), q[r][k],
+                                                                          s[r][x], 0, 0, 0);
+                }
+            const uint32_t lost = (uint32_t)uniform((int)s_lost[i & 7][b0 / 32]);
+            const bool masked = j0 + 32 > (unsigned)len || lost != 0 || (int)j0 < rows.low_most;
+            uint32_t vis[R], odd = 0;
+            if (masked) {
+#pragma unroll
+                for (int r = 0; r < R; ++r) {
+                    vis[r] = visible(len, rows.low[r], rows.seen[r], (int)j0, lost);
+#pragma unroll
+                    for (int x = 0; x < 2; ++x)
+#pragma unroll
+                        for (int y = 0; y < 4; ++y)
+                            s[r][x][y] = vis[r] >> (grp * 4) & (1u << (x * 16 + y)) ? s[r][x][y] : -INFINITY;
+                }
+            }
+#pragma unroll
+            for (int r = 0; r < R; ++r)
+                weigh<2, NT>(s[r], o[r], m[r], l[r], a.c1);
+            if (masked) {
+                // as in k_attend: rows of values with an infinity or a NaN are added one by one
+                for (int x = 0; x < 32 * PIECES / 64; ++x) {
+                    const int p = x * 64 + lane, row = p / PIECES;
+                    const u32x4 v = *reinterpret_cast<const u32x4 *>(vals + b0 * ROW + p * 16);
+                    const bool mine = odd_word<1>(v[0]) || odd_word<1>(v[1]) || odd_word<1>(v[2]) || odd_word<1>(v[3]);
+                    for (uint64_t all = __ballot(mine); all != 0; all &= all - 1)
+                        odd |= 1u << uniform(__shfl(row, __builtin_ctzll(all)));
+                }
+#pragma unroll 1
+                for (uint32_t left = odd; left != 0; left &= left - 1) {
+                    const int key = __builtin_ctz(left), row = b0 + key;
+#pragma unroll
+                    for (int r = 0; r < R; ++r) {
+                        float pr = 0.0f;
+#pragma unroll
+                        for (int x = 0; x < 2; ++x)
+#pragma unroll
+                            for (int y = 0; y < 4; ++y)
+                                pr = key / 16 == x && (key & 3) == y ? s[r][x][y] : pr;
+                        pr = __shfl(pr, (key >> 2 & 3) * 16 + col);
+                        const bool sees = vis[r] >> key & 1;
+#pragma unroll
+                        for (int x = 0; x < NT; ++x)
+#pragma unroll
+                            for (int y = 0; y < 4; ++y) {
+                                const int d = x * 16 + grp * 4 + y;
+                                const char *at = vals + row * ROW + ((d / 8) ^ value_order<DP>(row)) * 16 + (d & 7) * 2;
+                                const float v = __uint_as_float((uint32_t) * reinterpret_cast<const uint16_t *>(at) << 16);
+                                o[r][x][y] = sees ? o[r][x][y] + pr * v : o[r][x][y];
+                            }
+                    }
+                }
+            }
+            bf16x8 p[R];
+#pragma unroll
+            for (int r = 0; r < R; ++r)
+#pragma unroll
+                for (int y = 0; y < 8; ++y)
+                    p[r][y] = (__bf16)s[r][y / 4][y & 3];
+#pragma unroll
+            for (int x = 0; x < NT; ++x) {
+                s16x4 v[2];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int row = b0 + h * 16 + grp * 4 + (col >> 2);
+                    const char *at = vals + row * ROW + ((x * 2 + (col >> 1 & 1)) ^ value_order<DP>(row)) * 16 + (col & 1) * 8;
+                    v[h] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                        (__attribute__((address_space(3))) s16x4 *)at);
+                }
+                if (odd != 0)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+#pragma unroll
+                        for (int y = 0; y < 4; ++y)
+                            v[h][y] = odd >> (h * 16 + grp * 4 + y) & 1 ? (short)0 : v[h][y];
+                const bf16x8 vt = __builtin_bit_cast(
+                    bf16x8, __builtin_shufflevector(v[0], v[1], 0, 1, 2, 3, 4, 5, 6, 7));
+#pragma unroll
+                for (int r = 0; r < R; ++r)
+                    o[r][x] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vt, p[r], o[r][x], 0, 0, 0);
+            }
+        }
+    }
+    // nothing is under way to LDS, and all have read it
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    float(*s_o)[PITCH] = reinterpret_cast<float(*)[PITCH]>(mem);
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        const float sum = row_sum(l[r]);
+        const int at = w * 16 * R + r * 16 + col;
+        if (grp == 0)
+            s_ml[at] = make_float2(m[r] == -INFINITY ? -INFINITY : m[r] * a.c1, sum);
+#pragma unroll
+        for (int x = 0; x < NT; ++x)
+            *reinterpret_cast<f32x4 *>(&s_o[at][x * 16 + grp * 4]) = o[r][x];
+    }
+    __syncthreads();
+    // waves rw, rw + WR, ... hold the same rows
+    finish<1, ATTN_WIDE_WG, PITCH>(a, job, job.mt * ROWS, min(job.rows - job.mt * ROWS, ROWS), ROWS, s_o, s_ml, KG,
+                                   WR * 16 * R, t, ATTN_WIDE_WG);
 }
 
 // A wave joins the parts of one row: weights of 64 parts at once, a lane each.
@@ -728,57 +1037,57 @@ template <int DT> __global__ __launch_bounds__(ATTN_WG) void k_attend_join(AttnA
             z == 0.0f ? -INFINITY : (top + log2f(z)) * LN2;
 }
 
-template <int DT, int DP, int VW, int R, int OCC>
-hipError_t attend_with(hipStream_t st, const AttnArgs &a)
+// The launch of a form for tiles of `rows` rows.
+template <typename K> hipError_t attend_with(hipStream_t st, K kernel, AttnArgs a, int threads, int rows, int per_cu)
 {
-    const int64_t segments = (int64_t)a.nv.n * a.a.kv_heads *
-                             ((a.nv.max_count * a.a.group + 16 * R - 1) / (16 * R));
+    a.units = std::min(a.a.num_cus * per_cu, ATTN_MAX_UNITS);
+    const int64_t segments = (int64_t)a.nv.n * a.a.kv_heads * ((a.nv.max_count * a.a.group + rows - 1) / rows);
     // workgroups stand by dies, each of which may have one part more than its share
     const unsigned grid = (unsigned)(a.units + segments + 8);
-    k_attend<DT, DP, VW, R, OCC><<<grid, ATTN_WG, 0, st>>>(a);
+    kernel<<<grid, threads, 0, st>>>(a);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess)
         return e;
-    const int64_t rows = (int64_t)a.nv.n * a.nv.max_count * a.a.q_heads;
-    k_attend_join<DT><<<(unsigned)((rows + 3) / 4), ATTN_WG, 0, st>>>(a, 16 * R);
+    const int64_t joined = (int64_t)a.nv.n * a.nv.max_count * a.a.q_heads;
+    const unsigned groups = (unsigned)((joined + 3) / 4);
+    a.a.dtype == 1 ? k_attend_join<1><<<groups, ATTN_WG, 0, st>>>(a, rows)
+                   : k_attend_join<0><<<groups, ATTN_WG, 0, st>>>(a, rows);
     return hipGetLastError();
 }
 
 }  // namespace
 
-int attend_row_tiles(int dtype, int head_dim, int rows)
-{
-    if (rows <= 16 || (dtype == 0 && head_dim > 128))
-        return 1;
-    return rows <= 32 || dtype == 0 || head_dim > 128 ? 2 : 4;
-}
-
-int attend_units(int num_cus, int row_tiles) { return std::min(num_cus * (row_tiles == 4 ? 1 : 2), ATTN_MAX_UNITS); }
+int64_t attend_kept_rows(int num_cus) { return 2 * std::max<int64_t>(ATTN_MAX_UNITS * 32, num_cus * 256); }
 
 hipError_t launch_attend(hipStream_t st, const CacheView &c, const AttnShape &s, const NodesView &nodes,
                          int key_pool, int value_pool, float scale, int window, const void *q,
                          int64_t q_stride, void *out, int64_t out_stride, float *lse, int *status)
 {
-    const int D = s.head_dim, R = attend_row_tiles(s.dtype, D, nodes.max_count * s.group);
-    const int es = s.dtype == 1 ? 2 : 4;
+    const int D = s.head_dim, M = nodes.max_count * s.group, es = s.dtype == 1 ? 2 : 4;
     AttnArgs a = {c, s, nodes, key_pool, value_pool, scale == 0.0f ? 1.0f : fabsf(scale) * LOG2E,
                   scale > 0.0f ? 1.0f : scale < 0.0f ? -1.0f : 0.0f, window, static_cast<const char *>(q),
-                  q_stride * es, static_cast<char *>(out), out_stride * es, lse, status,
-                  attend_units(s.num_cus, R)};
-    if (s.dtype == 1) {
+                  q_stride * es, static_cast<char *>(out), out_stride * es, lse, status, 0};
+#define NARROW(DT, DP, VW, R, OCC) attend_with(st, k_attend<DT, DP, VW, R, OCC>, a, ATTN_WG, 16 * R, 2)
+#define WIDE(DP, R, WR, KB, STAGES) \
+    attend_with(st, k_attend_wide<DP, R, WR, KB, STAGES>, a, ATTN_WIDE_WG, 16 * R * WR, 1)
+    if (s.dtype == 0) {
         if (D <= 64)
-            return R == 1 ? attend_with<1, 64, 4, 1, 2>(st, a)
-                 : R == 2 ? attend_with<1, 64, 4, 2, 2>(st, a) : attend_with<1, 64, 4, 4, 1>(st, a);
+            return M <= 16 ? NARROW(0, 64, 4, 1, 2) : NARROW(0, 64, 4, 2, 2);
         if (D <= 128)
-            return R == 1 ? attend_with<1, 128, 8, 1, 2>(st, a)
-                 : R == 2 ? attend_with<1, 128, 8, 2, 2>(st, a) : attend_with<1, 128, 8, 4, 1>(st, a);
-        return R == 1 ? attend_with<1, 256, 8, 1, 1>(st, a) : attend_with<1, 256, 8, 2, 1>(st, a);
+            return M <= 16 ? NARROW(0, 128, 4, 1, 2) : NARROW(0, 128, 4, 2, 1);
+        return NARROW(0, 256, 4, 1, 1);
     }
+    if (M <= 16)
+        return D <= 64 ? NARROW(1, 64, 4, 1, 2) : D <= 128 ? NARROW(1, 128, 8, 1, 2) : NARROW(1, 256, 8, 1, 1);
     if (D <= 64)
-        return R == 1 ? attend_with<0, 64, 4, 1, 2>(st, a) : attend_with<0, 64, 4, 2, 2>(st, a);
+        return M <= 32 ? WIDE(64, 1, 2, 1, 4) : M <= 64 ? WIDE(64, 2, 2, 1, 4)
+             : M <= 128 ? WIDE(64, 2, 4, 2, 4) : WIDE(64, 2, 8, 2, 4);
     if (D <= 128)
-        return R == 1 ? attend_with<0, 128, 4, 1, 2>(st, a) : attend_with<0, 128, 4, 2, 2>(st, a);
-    return attend_with<0, 256, 4, 1, 1>(st, a);
+        return M <= 32 ? WIDE(128, 1, 2, 1, 2) : M <= 64 ? WIDE(128, 2, 2, 1, 2)
+             : M <= 128 ? WIDE(128, 2, 4, 1, 4) : WIDE(128, 2, 8, 2, 4);
+    return M <= 64 ? WIDE(256, 1, 4, 1, 2) : WIDE(256, 1, 8, 2, 2);
+#undef NARROW
+#undef WIDE
 }
 
 // ------------------------------------------------------------------ append

@@ -290,6 +290,7 @@ hipError_t launch_cache_copy(hipStream_t st, const CacheView &c, int cus, int n,
 
 constexpr int MAX_NODES = 64;         // nodes of a tree: one lane each, one bit each of an ancestor mask
 constexpr int ATTN_WG = 256;
+constexpr int ATTN_WIDE_WG = 512;
 constexpr int ATTN_MAX_HEAD_DIM = 256;
 constexpr int ATTN_MAX_ENTRIES = 1 << 16;
 constexpr int ATTN_MAX_UNITS = 1024;  // parts that a call's work is cut into, at most (but for a part
@@ -338,10 +339,9 @@ struct AttnShape {
     float *part_o;       // [2 units][rows of a tile][head_dim] sums of weighted values
 };
 
-// Tiles of 16 rows that a workgroup of k_attend has, by type, head size and rows per key head; the
-// parts that fill the chip.
-int attend_row_tiles(int dtype, int head_dim, int rows);
-int attend_units(int num_cus, int row_tiles);
+// Rows that the parts of any call leave at most: twice the parts that fill the chip (an entry that is
+// split at all is split into at most twice its share), with the rows of each.
+int64_t attend_kept_rows(int num_cus);
 
 hipError_t launch_attend(hipStream_t st, const CacheView &c, const AttnShape &a, const NodesView &nodes,
                          int key_pool, int value_pool, float scale, int window, const void *q,
