@@ -928,29 +928,33 @@ int specverify_attn_create(specverify_attn **out, const specverify_cache *cache,
     const int group = q_heads / kv_heads;
     const int64_t rows = sv::attend_kept_rows(cache->num_cus);
     const size_t b_plan = align_up((size_t)max_entries * sizeof(sv::AttnPlan));
+    const size_t b_sound = align_up((size_t)max_entries * sizeof(int));
+    const size_t b_share = align_up(sizeof(int64_t));
     const size_t b_ml = align_up((size_t)rows * sizeof(float2));
     const size_t b_o = align_up((size_t)rows * head_dim * sizeof(float));
     specverify_attn *a = new (std::nothrow) specverify_attn();
     if (!a)
         return SPECVERIFY_ENOMEM;
-    a->bytes = b_plan + b_ml + b_o;
+    a->bytes = b_plan + b_sound + b_share + b_ml + b_o;
     if (hipMalloc(&a->mem, a->bytes) != hipSuccess) {
         delete a;
         return SPECVERIFY_ENOMEM;
     }
-    if (hipMemset(a->mem, 0, b_plan) != hipSuccess || hipDeviceSynchronize() != hipSuccess) {
-        (void)hipFree(a->mem);
-        delete a;
-        return SPECVERIFY_EHIP;
-    }
     char *p = static_cast<char *>(a->mem);
+    auto take = [&](size_t n) {
+        char *q = p;
+        p += n;
+        return q;
+    };
     a->device = cache->device;
     a->view = v;
     a->max_entries = max_entries;
     a->max_nodes = max_nodes;
     a->shape = {dtype, q_heads, kv_heads, head_dim, group, sv::fast_div(group),
-                sv::fast_div(v.page_tokens), cache->num_cus, reinterpret_cast<sv::AttnPlan *>(p),
-                reinterpret_cast<float2 *>(p + b_plan), reinterpret_cast<float *>(p + b_plan + b_ml)};
+                sv::fast_div(v.page_tokens), cache->num_cus,
+                reinterpret_cast<sv::AttnPlan *>(take(b_plan)), reinterpret_cast<int *>(take(b_sound)),
+                reinterpret_cast<int64_t *>(take(b_share)), reinterpret_cast<float2 *>(take(b_ml)),
+                reinterpret_cast<float *>(take(b_o))};
     *out = a;
     return SPECVERIFY_OK;
 }
@@ -1031,11 +1035,8 @@ int specverify_attn_attend(specverify_attn *attn, void *hip_stream, int key_pool
         return SPECVERIFY_EINVAL;
     if (n > attn->max_entries || max_count > attn->max_nodes)
         return SPECVERIFY_ECAPACITY;
-    // a workgroup for each key head and 16 rows of an entry besides those that fill the chip, and a
-    // wave for each row and head of the join
-    const int64_t parts = (int64_t)n * s.kv_heads * (((int64_t)max_count * s.group + 15) / 16);
-    if (parts + sv::ATTN_MAX_UNITS + 8 > (int64_t)(MAX_ITEMS / sv::ATTN_WG) ||
-        (int64_t)n * max_count * s.q_heads > (int64_t)(MAX_ITEMS / 64) - 4)
+    // at most a wave for each row and head of the join; tiles are counted in 63 bits
+    if ((int64_t)n * max_count * s.q_heads > (int64_t)(MAX_ITEMS / 64) - 64)
         return SPECVERIFY_ECAPACITY;
     if (n == 0)
         return SPECVERIFY_OK;

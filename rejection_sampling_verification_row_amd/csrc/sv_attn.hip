@@ -16,6 +16,7 @@
 // every workgroup adds them up and finds its own part.  Parts of a split segment leave sums that
 // k_attend_join adds in the parts' order.
 #include <algorithm>
+#include <type_traits>
 
 #include "sv_device.h"
 #include "sv_internal.h"
@@ -35,6 +36,15 @@ __device__ inline bool in_range(int i, int n) { return (unsigned)i < (unsigned)n
 
 // a value that all lanes have
 __device__ inline int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+__device__ inline int64_t uniform(int64_t v)
+{
+    return (int64_t)(uint32_t)uniform((int)v) | (int64_t)uniform((int)(v >> 32)) << 32;
+}
+
+__device__ inline int64_t quotient(int64_t a, int64_t b)
+{
+    return a >> 32 || b >> 32 ? a / b : (int64_t)((uint32_t)a / (uint32_t)b);
+}
 
 __device__ inline int divide(int j, const FastDiv &f)
 {
@@ -117,7 +127,7 @@ struct AttnArgs {
     int64_t out_stride;  // bytes
     float *lse;
     int *status;
-    int units;           // parts that fill the chip
+    int units;           // workgroups that fill the chip
 };
 
 template <int WG_SIZE> __device__ inline int64_t block_sum(int64_t v, int64_t *lds)
@@ -176,78 +186,128 @@ template <int KT> __device__ inline Work entry_work(const AttnArgs &a, const Ent
     return w;
 }
 
-struct Part {
-    int entry, local, chunks, kept;      // entry < 0: none
+// All tiles stand in a row, entry by entry and in an entry segment by segment, and every workgroup
+// takes the same number of them: `share`, the mine-th ones.
+struct Stretch {
+    int64_t at, end;
+    int mine;                            // < 0: none
 };
 
-// This workgroup's part.  Workgroup 0 also leaves the plan for the join, and the status of entries
-// that have no part.
-template <int WG_SIZE, int KT> __device__ Part find_part(const AttnArgs &a, int rows_per_tile, int least)
+// What a workgroup works on: tiles t0 .. t1 of a segment's tokens.
+struct Job {
+    int entry;
+    int64_t base;                        // its first tile among all
+    Entry e;
+    Work w;
+    bool ok;                             // the parents are sound
+    uint64_t lane_seen;                  // lane_node of the entry's nodes
+    int lane_depth;
+    int head, mt, t0, t1, rows, total;
+    bool whole;                          // else the sums go to this slot of the kept ones:
+    int slot;
+};
+
+// This workgroup's stretch and the entry that it begins in.  Workgroup 0 also leaves the plan for the
+// join, and the status of entries that have no work.
+template <int WG_SIZE, int KT>
+__device__ Stretch find_stretch(const AttnArgs &a, int rows_per_tile, int least, Job &job)
 {
-    __shared__ int64_t lds[WG_SIZE / 64];
-    __shared__ Part found;
+    __shared__ int64_t lds[WG_SIZE / 64], found_base;
+    __shared__ Entry found;
+    __shared__ int found_entry;
     const int n = a.nv.n, t = threadIdx.x;
     Entry e0 = {-1, 0, -1, 0};
     if (t < n)
         e0 = load_entry(a.c, a.nv, t);
-    const Work w0 = entry_work<KT>(a, e0, rows_per_tile);
-    auto work = [&](int i, Entry &e) {
-        if (i < WG_SIZE) {
-            e = e0;
-            return w0;
-        }
-        e = load_entry(a.c, a.nv, i);
-        return entry_work<KT>(a, e, rows_per_tile);
-    };
     int64_t sum = 0;
     for (int i = t; i < n; i += WG_SIZE) {
-        Entry e;
-        const Work w = work(i, e);
+        const Work w = entry_work<KT>(a, i < WG_SIZE ? e0 : load_entry(a.c, a.nv, i), rows_per_tile);
         sum += (int64_t)w.segments * w.tiles;
     }
-    sum = block_sum<WG_SIZE>(sum, lds);
-    const int per = (int)max((sum + a.units - 1) / a.units, (int64_t)least);   // tiles of a part
-    if (t == 0)
-        found = {-1, 0, 0, 0};
-    int64_t total = 0;
-    for (int i = t; i < n; i += WG_SIZE) {
-        Entry e;
-        const Work w = work(i, e);
-        total += (int64_t)w.segments * ((w.tiles + per - 1) / per);
-    }
-    total = block_sum<WG_SIZE>(total, lds);
+    sum = uniform(block_sum<WG_SIZE>(sum, lds));
+    const int64_t share = max(quotient(sum + a.units - 1, a.units), (int64_t)least);
     // neighbours, which read the same tokens, on one of the 8 dies, to which workgroups go in turn
-    const int64_t each = (total + 7) / 8;
-    const int64_t mine = (int64_t)(blockIdx.x & 7) * each + (blockIdx.x >> 3);
-    const bool none = (int64_t)(blockIdx.x >> 3) >= each || mine >= total;
-    if (none && blockIdx.x != 0)
-        return {-1, 0, 0, 0};
-    int64_t base = 0;                    // parts in the upper half, kept ones in the lower
+    const int active = (int)quotient(sum + share - 1, share), each = (active + 7) / 8;
+    Stretch st;
+    st.mine = (int)(blockIdx.x & 7) * each + (int)(blockIdx.x >> 3);
+    if ((int)(blockIdx.x >> 3) >= each || st.mine >= active)
+        st.mine = -1;
+    st.at = st.mine * share;
+    st.end = min(st.at + share, sum);
+    if (st.mine < 0 && blockIdx.x != 0)
+        return st;
+    int64_t base = 0;
     for (int i0 = 0; i0 < n; i0 += WG_SIZE) {
         const int i = i0 + t;
         Entry e = {-1, 0, -1, 0};
-        Work w = {0, 0, 0, 0};
         if (i < n)
-            w = work(i, e);
-        const int chunks = (w.tiles + per - 1) / per, parts = w.segments * chunks;
-        const int kept = chunks > 1 ? parts : 0;
+            e = i0 == 0 ? e0 : load_entry(a.c, a.nv, i);
+        const Work w = entry_work<KT>(a, e, rows_per_tile);
+        const int64_t work = (int64_t)w.segments * w.tiles;
         int64_t all;
-        const int64_t inc = base + block_scan<WG_SIZE>(((int64_t)parts << 32) + kept, lds, &all);
-        const int64_t first = (inc >> 32) - parts;
-        const int at = (int)(inc & 0xffffffff) - kept;
-        if (i < n && !none && mine >= first && mine < first + parts)
-            found = {i, (int)(mine - first), chunks, at};
+        const int64_t first = base + block_scan<WG_SIZE>(work, lds, &all) - work;
+        if (st.mine >= 0 && st.at >= first && st.at < first + work) {
+            found = e;
+            found_entry = i;
+            found_base = first;
+        }
         if (blockIdx.x == 0 && i < n) {
-            a.a.plan[i].chunks = parts > 0 ? chunks : 0;
-            a.a.plan[i].part = at;
-            a.a.plan[i].tiles = w.tiles_of_rows;
-            if (a.status && parts == 0)
+            a.a.plan[i] = {first, w.tiles, w.tiles_of_rows, e.start, max(e.count, 0)};
+            if (a.status && work == 0)
                 a.status[i] = e.count < 0 ? -1 : 0;
         }
         base += all;
     }
+    if (blockIdx.x == 0 && t == 0)
+        *a.a.share = share;
     __syncthreads();
-    return {uniform(found.entry), uniform(found.local), uniform(found.chunks), uniform(found.kept)};
+    if (st.mine >= 0) {
+        job.entry = uniform(found_entry);
+        job.base = uniform(found_base);
+        job.e = {uniform(found.seq), uniform(found.start), uniform(found.count), uniform(found.len)};
+        job.w = entry_work<KT>(a, job.e, rows_per_tile);
+    }
+    return st;
+}
+
+// The entry's nodes; the workgroup that has its first tile says whether they are sound.
+__device__ inline void open_entry(const AttnArgs &a, const Stretch &st, Job &job)
+{
+    job.ok = lane_node(a.nv.parents ? a.nv.parents + job.e.start : nullptr, job.e.count, a.window, job.lane_seen,
+                       job.lane_depth);
+    if (st.at == job.base && threadIdx.x == 0) {
+        a.a.sound[job.entry] = job.ok;
+        if (a.status)
+            a.status[job.entry] = job.ok ? 0 : -1;
+    }
+    job.rows = job.e.count * a.a.group;
+    job.total = job.e.len + job.e.count;
+}
+
+// The next job of the stretch, from where it stands on; false at its end.
+template <int KT>
+__device__ inline bool next_job(const AttnArgs &a, int rows_per_tile, Stretch &st, Job &job)
+{
+    if (st.mine < 0 || st.at >= st.end)
+        return false;
+    while (st.at >= job.base + (int64_t)job.w.segments * job.w.tiles) {
+        job.base += (int64_t)job.w.segments * job.w.tiles;
+        job.e = load_entry(a.c, a.nv, ++job.entry);
+        job.w = entry_work<KT>(a, job.e, rows_per_tile);
+        if (job.w.tiles > 0)
+            open_entry(a, st, job);
+    }
+    const int64_t rel = st.at - job.base, segment = quotient(rel, job.w.tiles);
+    const int off = (int)(rel - segment * job.w.tiles);
+    const int take = (int)min((int64_t)(job.w.tiles - off), st.end - st.at);
+    job.head = (int)segment / job.w.tiles_of_rows;
+    job.mt = (int)segment - job.head * job.w.tiles_of_rows;
+    job.t0 = job.w.low + off;
+    job.t1 = job.t0 + take;
+    job.whole = take == job.w.tiles;
+    job.slot = 2 * st.mine + (off == 0);
+    st.at += take;
+    return true;
 }
 
 template <int DT> struct Tile;
@@ -284,43 +344,9 @@ __device__ inline float row_sum(float v)
     return v + xch<5>(v);
 }
 
-// What a workgroup works on: a segment's rows, and the tiles t0 .. t1 of its tokens.
-struct Job {
-    Entry e;
-    int head, mt, t0, t1, rows, total, chunks;
-    int64_t kept;                        // its place among the kept parts
-    bool ok;
-    uint64_t lane_seen;                  // lane_node of the entry's nodes
-    int lane_depth;
-};
-
-template <int WG_SIZE, int KT> __device__ inline Job take_job(const AttnArgs &a, int rows_per_tile, int least)
-{
-    Job j;
-    const Part part = find_part<WG_SIZE, KT>(a, rows_per_tile, least);
-    j.ok = false;
-    if (part.entry < 0)
-        return j;
-    j.e = load_entry(a.c, a.nv, part.entry);
-    const Work work = entry_work<KT>(a, j.e, rows_per_tile);
-    j.ok = lane_node(a.nv.parents ? a.nv.parents + j.e.start : nullptr, j.e.count, a.window, j.lane_seen,
-                     j.lane_depth);
-    if (part.local == 0 && threadIdx.x == 0) {
-        a.a.plan[part.entry].ok = j.ok;
-        if (a.status)
-            a.status[part.entry] = j.ok ? 0 : -1;
-    }
-    const int hc = part.local / work.tiles_of_rows, chunk = hc / a.a.kv_heads;
-    j.mt = part.local - hc * work.tiles_of_rows;
-    j.head = hc - chunk * a.a.kv_heads;
-    j.t0 = work.low + (int)((int64_t)work.tiles * chunk / part.chunks);
-    j.t1 = work.low + (int)((int64_t)work.tiles * (chunk + 1) / part.chunks);
-    j.rows = j.e.count * a.a.group;
-    j.total = j.e.len + j.e.count;
-    j.chunks = part.chunks;
-    j.kept = part.kept + part.local;
-    return j;
-}
+// What stands for elements past a head's end (head_dim below a kernel's size): the queries are 0
+// there, and so must the keys be, whatever follows them in memory.
+__device__ const uint4 past_the_head = {0, 0, 0, 0};
 
 // The rows of a lane's columns: what they see, and from where on.
 template <int R> struct Rows {
@@ -422,16 +448,16 @@ __device__ inline void weigh(f32x4 (&s)[SUB], f32x4 (&o)[NT], float &m, float &l
         }
 }
 
-// The sums of `waves` waves over one tile of rows, joined, to the output or to the kept parts: row i
-// at o[wave * wave_step + i], its maximum and sum at ml of the same index; rows is how many are there.
+// The sums of `waves` waves over a tile of rows, joined, to the output or to the kept ones: row i at
+// o[wave * wave_step + i], its maximum and sum at ml of the same index.
 template <int DT, int WG_SIZE, int PITCH>
-__device__ inline void finish(const AttnArgs &a, const Job &j, int first, int rows, int rows_per_tile,
-                              const float (*o)[PITCH], const float2 *ml, int waves, int wave_step, int thread,
-                              int threads)
+__device__ inline void finish(const AttnArgs &a, const Job &j, int rows_per_tile, const float (*o)[PITCH],
+                              const float2 *ml, int waves, int wave_step)
 {
     constexpr int ES = Tile<DT>::ES;
-    const int D = a.a.head_dim, G = a.a.group;
-    for (int i = thread; i < rows * (D / 4); i += threads) {
+    const int D = a.a.head_dim, G = a.a.group, first = j.mt * rows_per_tile;
+    const int rows = min(j.rows - first, rows_per_tile);
+    for (int i = threadIdx.x; i < rows * (D / 4); i += WG_SIZE) {
         const int row = i / (D / 4), d = (i - row * (D / 4)) * 4;
         float top = -INFINITY;
         for (int k = 0; k < waves; ++k)
@@ -447,8 +473,8 @@ __device__ inline void finish(const AttnArgs &a, const Job &j, int first, int ro
             acc[2] += f * v.z;
             acc[3] += f * v.w;
         }
-        if (j.chunks > 1) {
-            const int64_t at = j.kept * rows_per_tile + first - j.mt * rows_per_tile + row;
+        if (!j.whole) {
+            const int64_t at = (int64_t)j.slot * rows_per_tile + row;
             *reinterpret_cast<float4 *>(a.a.part_o + at * D + d) = make_float4(acc[0], acc[1], acc[2], acc[3]);
             if (d == 0)
                 a.a.part_ml[at] = make_float2(top, z);
@@ -492,10 +518,15 @@ __global__ __launch_bounds__(ATTN_WG, OCC) void k_attend(AttnArgs a)
     __shared__ float2 s_ml[4 * ROWS];
     __shared__ int64_t s_off[4][2][KT];
 
-    const int lane = threadIdx.x & 63, w = uniform(threadIdx.x >> 6), col = lane & 15, grp = lane >> 4;
-    const Job job = take_job<ATTN_WG, KT>(a, ROWS, 128 / KT);
-    if (!job.ok)
+    const int lane = threadIdx.x & 63, w = uniform((int)(threadIdx.x >> 6)), col = lane & 15, grp = lane >> 4;
+    Job job;
+    Stretch stretch = find_stretch<ATTN_WG, KT>(a, ROWS, 128 / KT, job);
+    if (stretch.mine < 0)
         return;
+    open_entry(a, stretch, job);
+    while (next_job<KT>(a, ROWS, stretch, job)) {
+    if (!job.ok)
+        continue;
     const int D = a.a.head_dim, len = job.e.len, total = job.total, t1 = job.t1;
     Rows<R> rows;
     typename TL::vec q[R][KS];
@@ -505,6 +536,7 @@ __global__ __launch_bounds__(ATTN_WG, OCC) void k_attend(AttnArgs a)
     const int64_t row_bytes = (int64_t)a.a.kv_heads * D * ES;
     const char *kp = a.c.pools[a.key_pool] + (int64_t)job.head * D * ES;
     const char *vp = a.c.pools[a.value_pool] + (int64_t)job.head * D * ES;
+    const char *zeros = reinterpret_cast<const char *>(&past_the_head);
 
     // a tile's page ids, one token to a lane, then the tokens' places; bits of what has no place
     auto page_of = [&](int tile) {
@@ -532,7 +564,7 @@ __global__ __launch_bounds__(ATTN_WG, OCC) void k_attend(AttnArgs a)
 #pragma unroll
             for (int k = 0; k < KS; ++k) {
                 const int b = k * 64 + grp * 16;
-                kr[s][k] = load_global<u32x4>(p + (b < D * ES ? b : 0));
+                kr[s][k] = load_global<u32x4>(b < D * ES ? p + b : zeros);
             }
         }
     };
@@ -570,15 +602,6 @@ __global__ __launch_bounds__(ATTN_WG, OCC) void k_attend(AttnArgs a)
     }
     for (; t < t1; t += 4, buf ^= 1) {
         f32x4 s[R][SUB];
-        if (DP != D) {
-            // elements past the head's end: the queries are 0 there, the keys must be finite
-#pragma unroll
-            for (int x = 0; x < SUB; ++x)
-#pragma unroll
-                for (int k = 0; k < KS; ++k)
-                    if (k * 64 + grp * 16 >= D * ES)
-                        kr[x][k] = u32x4{0, 0, 0, 0};
-        }
 #pragma unroll
         for (int r = 0; r < R; ++r)
 #pragma unroll
@@ -724,8 +747,9 @@ __global__ __launch_bounds__(ATTN_WG, OCC) void k_attend(AttnArgs a)
                     s_o[at][b * 16 * VW + (grp * 4 + i) * VW + x] = o[r][b * VW + x][i];
     }
     __syncthreads();
-    finish<DT, ATTN_WG, PITCH>(a, job, job.mt * ROWS, min(job.rows - job.mt * ROWS, ROWS), ROWS, s_o, s_ml, 4, ROWS,
-                               threadIdx.x, ATTN_WG);
+    finish<DT, ATTN_WG, PITCH>(a, job, ROWS, s_o, s_ml, 4, ROWS);
+    __syncthreads();
+    }
 }
 
 // The order of a row's 16-byte pieces in LDS: piece p of row r is at p ^ order(r).  Keys: 8 rows'
@@ -738,6 +762,22 @@ template <int DP> __device__ inline int key_order(int row)
 template <int DP> __device__ inline int value_order(int row)
 {
     return DP == 64 ? (row >> 1 & 3) * 2 : (row & 7) * 2;
+}
+
+// A load of 16 (4) bytes a lane from memory to LDS, at `to` plus the lane's place; a wave's `to` is
+// uniform.  Nothing waits for it but what says so: the compiler, which cannot tell the stages
+// apart, would let every read of LDS wait for all of them.
+__device__ inline uint32_t lds_address(const void *p)
+{
+    return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) void *)p;
+}
+__device__ inline void load_to_lds16(const char *from, uint32_t to)
+{
+    asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(from), "{m0}"(to) : "memory");
+}
+__device__ inline void load_to_lds4(const void *from, uint32_t to)
+{
+    asm volatile("s_nop 0\n\tglobal_load_lds_dword %0, off" ::"v"(from), "{m0}"(to) : "memory");
 }
 
 // More rows, bfloat16: eight waves, WR of them side by side over the rows (16 R each) and 8 / WR
@@ -763,11 +803,16 @@ __global__ __launch_bounds__(ATTN_WIDE_WG, 1) void k_attend_wide(AttnArgs a)
     __shared__ int s_page[4][TK < 64 ? 64 : TK];
     __shared__ uint32_t s_lost[8][TK / 32];
 
-    const int t = threadIdx.x, lane = t & 63, w = uniform(t >> 6), col = lane & 15, grp = lane >> 4;
+    const int t = threadIdx.x, lane = t & 63, w = uniform((int)(t >> 6)), col = lane & 15, grp = lane >> 4;
     const int rw = w % WR, kg = w / WR;
-    const Job job = take_job<ATTN_WIDE_WG, TK>(a, ROWS, 1);
-    if (!job.ok)
+    Job job;
+    Stretch stretch = find_stretch<ATTN_WIDE_WG, TK>(a, ROWS, 1, job);
+    if (stretch.mine < 0)
         return;
+    open_entry(a, stretch, job);
+    while (next_job<TK>(a, ROWS, stretch, job)) {
+    if (!job.ok)
+        continue;
     const int D = a.a.head_dim, len = job.e.len, total = job.total, stages = job.t1 - job.t0;
     const int first = job.mt * ROWS + rw * 16 * R;
     Rows<R> rows;
@@ -778,6 +823,7 @@ __global__ __launch_bounds__(ATTN_WIDE_WG, 1) void k_attend_wide(AttnArgs a)
     const int64_t row_bytes = (int64_t)a.a.kv_heads * D * 2;
     const char *kp = a.c.pools[a.key_pool] + (int64_t)job.head * D * 2;
     const char *vp = a.c.pools[a.value_pool] + (int64_t)job.head * D * 2;
+    const char *zeros = reinterpret_cast<const char *>(&past_the_head);
 
     auto token_of = [&](int stage, int i) {
         return (int)min((unsigned)(job.t0 + stage) * TK + i, (unsigned)total - 1);
@@ -797,21 +843,18 @@ __global__ __launch_bounds__(ATTN_WIDE_WG, 1) void k_attend_wide(AttnArgs a)
     auto load_pages = [&](int stage) {
         const int part = w * 64 % (TK < 64 ? 64 : TK), i = (part + lane) % TK;
         const int *p = table + divide(token_of(min(stage, stages - 1), i), a.a.by_page);
-        __builtin_amdgcn_global_load_lds((const SV_GLOBAL void *)p,
-                                         (__attribute__((address_space(3))) void *)&s_page[stage & 3][part], 4, 0, 0);
+        load_to_lds4(p, lds_address(&s_page[stage & 3][part]));
     };
     auto load_stage = [&](int stage) {
-        char *to = mem + stage % STAGES * 2 * HALF;
+        const uint32_t to = lds_address(mem) + stage % STAGES * 2 * HALF;
 #pragma unroll
         for (int i = 0; i < LOADS; ++i) {
             const int at = (i * WAVES8 + w) * 1024, row = (at + lane * 16) / ROW, slot = (at + lane * 16) % ROW / 16;
             const int64_t off = s_off[stage & 3][row];
             const int ck = slot ^ key_order<DP>(row), cv = slot ^ value_order<DP>(row);
-            const char *k = kp + off + (ck * 8 < D ? ck * 16 : 0), *v = vp + off + (cv * 8 < D ? cv * 16 : 0);
-            __builtin_amdgcn_global_load_lds((const SV_GLOBAL void *)k,
-                                             (__attribute__((address_space(3))) void *)(to + at), 16, 0, 0);
-            __builtin_amdgcn_global_load_lds((const SV_GLOBAL void *)v,
-                                             (__attribute__((address_space(3))) void *)(to + HALF + at), 16, 0, 0);
+            const char *k = ck * 8 < D ? kp + off + ck * 16 : zeros, *v = cv * 8 < D ? vp + off + cv * 16 : zeros;
+            load_to_lds16(k, to + at);
+            load_to_lds16(v, to + HALF + at);
         }
     };
 
@@ -835,6 +878,12 @@ __global__ __launch_bounds__(ATTN_WIDE_WG, 1) void k_attend_wide(AttnArgs a)
             load_stage(s);
     }
 
+    // This lane's bytes of the first block: piece `grp` of key row `col`, and 8 bytes of value row
+    // 4 grp + col / 4; other pieces of the rows differ in bits of the offset, since orders are xors.
+    const int key_at = col * ROW + (grp ^ key_order<DP>(col)) * 16;
+    const int value_row = grp * 4 + (col >> 2);
+    const int value_at = value_row * ROW + ((col >> 1 & 1) ^ value_order<DP>(value_row)) * 16 + (col & 1) * 8;
+
     for (int i = 0; i < stages; ++i) {
         // stage i and the page ids loaded with it are there; what came after may be under way
         if (i + DEPTH <= stages)
@@ -846,13 +895,15 @@ __global__ __launch_bounds__(ATTN_WIDE_WG, 1) void k_attend_wide(AttnArgs a)
             load_stage(i + DEPTH);
         if (i + DEPTH + 1 < stages && t < TK)
             put_places(i + DEPTH + 1, s_page[i + DEPTH + 1 & 3][t]);
-        const char *keys = mem + i % STAGES * 2 * HALF, *vals = keys + HALF;
+        const int stage_at = i % STAGES * 2 * HALF;
+        const char *vals = mem + stage_at + HALF;
 #pragma unroll 1
         for (int kb = 0; kb < KB; ++kb) {
             const int b0 = (kg * KB + kb) * 32;
             const unsigned j0 = (unsigned)(job.t0 + i) * TK + b0;
             if (j0 >= (unsigned)total)
                 break;
+            const int lost_here = (int)s_lost[i & 7][b0 / 32];
             f32x4 s[R][2];
 #pragma unroll
             for (int r = 0; r < R; ++r)
@@ -861,17 +912,14 @@ __global__ __launch_bounds__(ATTN_WIDE_WG, 1) void k_attend_wide(AttnArgs a)
             for (int k = 0; k < KS; ++k)
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
-                    const int row = b0 + x * 16 + col;
-                    u32x4 kv = *reinterpret_cast<const u32x4 *>(keys + row * ROW +
-                                                                ((k * 4 + grp) ^ key_order<DP>(row)) * 16);
-                    if (DP != D && (k * 4 + grp) * 8 >= D)
-                        kv = u32x4{0, 0, 0, 0};
+                    const u32x4 kv = *reinterpret_cast<const u32x4 *>(
+                        mem + ((key_at + stage_at + b0 * ROW) ^ k * 64) + x * 16 * ROW);
 #pragma unroll
                     for (int r = 0; r < R; ++r)
                         s[r][x] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, kv), q[r][k],
                                                                           s[r][x], 0, 0, 0);
                 }
-            const uint32_t lost = (uint32_t)uniform((int)s_lost[i & 7][b0 / 32]);
+            const uint32_t lost = (uint32_t)uniform(lost_here);
             const bool masked = j0 + 32 > (unsigned)len || lost != 0 || (int)j0 < rows.low_most;
             uint32_t vis[R], odd = 0;
             if (masked) {
@@ -928,28 +976,31 @@ __global__ __launch_bounds__(ATTN_WIDE_WG, 1) void k_attend_wide(AttnArgs a)
 #pragma unroll
                 for (int y = 0; y < 8; ++y)
                     p[r][y] = (__bf16)s[r][y / 4][y & 3];
+            auto add_values = [&](auto some_odd) {
 #pragma unroll
-            for (int x = 0; x < NT; ++x) {
-                s16x4 v[2];
+                for (int x = 0; x < NT; ++x) {
+                    s16x4 v[2];
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int row = b0 + h * 16 + grp * 4 + (col >> 2);
-                    const char *at = vals + row * ROW + ((x * 2 + (col >> 1 & 1)) ^ value_order<DP>(row)) * 16 + (col & 1) * 8;
-                    v[h] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                        (__attribute__((address_space(3))) s16x4 *)at);
+                    for (int h = 0; h < 2; ++h) {
+                        const char *at = mem + ((value_at + stage_at + b0 * ROW) ^ x * 32) + HALF + h * 16 * ROW;
+                        v[h] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                            (__attribute__((address_space(3))) s16x4 *)at);
+                        if constexpr (decltype(some_odd)::value)
+#pragma unroll
+                            for (int y = 0; y < 4; ++y)
+                                v[h][y] = odd >> (h * 16 + grp * 4 + y) & 1 ? (short)0 : v[h][y];
+                    }
+                    const bf16x8 vt =
+                        __builtin_bit_cast(bf16x8, __builtin_shufflevector(v[0], v[1], 0, 1, 2, 3, 4, 5, 6, 7));
+#pragma unroll
+                    for (int r = 0; r < R; ++r)
+                        o[r][x] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vt, p[r], o[r][x], 0, 0, 0);
                 }
-                if (odd != 0)
-#pragma unroll
-                    for (int h = 0; h < 2; ++h)
-#pragma unroll
-                        for (int y = 0; y < 4; ++y)
-                            v[h][y] = odd >> (h * 16 + grp * 4 + y) & 1 ? (short)0 : v[h][y];
-                const bf16x8 vt = __builtin_bit_cast(
-                    bf16x8, __builtin_shufflevector(v[0], v[1], 0, 1, 2, 3, 4, 5, 6, 7));
-#pragma unroll
-                for (int r = 0; r < R; ++r)
-                    o[r][x] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vt, p[r], o[r][x], 0, 0, 0);
-            }
+            };
+            if (odd != 0)
+                add_values(std::true_type());
+            else
+                add_values(std::false_type());
         }
     }
     // nothing is under way to LDS, and all have read it
@@ -967,62 +1018,71 @@ __global__ __launch_bounds__(ATTN_WIDE_WG, 1) void k_attend_wide(AttnArgs a)
     }
     __syncthreads();
     // waves rw, rw + WR, ... hold the same rows
-    finish<1, ATTN_WIDE_WG, PITCH>(a, job, job.mt * ROWS, min(job.rows - job.mt * ROWS, ROWS), ROWS, s_o, s_ml, KG,
-                                   WR * 16 * R, t, ATTN_WIDE_WG);
+    finish<1, ATTN_WIDE_WG, PITCH>(a, job, ROWS, s_o, s_ml, KG, ROWS);
+    __syncthreads();
+    }
 }
 
-// A wave joins the parts of one row: weights of 64 parts at once, a lane each.
-template <int DT> __global__ __launch_bounds__(ATTN_WG) void k_attend_join(AttnArgs a, int rows_per_tile)
+// LG lanes join what the parts of one row left, 4 elements each, weights of LG parts at once.
+template <int DT, int LG> __global__ __launch_bounds__(ATTN_WG) void k_attend_join(AttnArgs a, int rows_per_tile)
 {
     constexpr int ES = Tile<DT>::ES;
-    const int lane = threadIdx.x & 63;
+    const int lane = threadIdx.x & (LG - 1);
     const int per = a.nv.max_count * a.a.q_heads;
-    const int64_t at = (int64_t)blockIdx.x * (ATTN_WG / 64) + (threadIdx.x >> 6);
-    const int i = (int)(at / per), rest = (int)(at - (int64_t)i * per);
+    const int64_t at = (int64_t)blockIdx.x * (ATTN_WG / LG) + threadIdx.x / LG;
+    const int i = (int)quotient(at, per), rest = (int)(at - (int64_t)i * per);
     if (i >= a.nv.n)
         return;
     const AttnPlan p = a.a.plan[i];
-    if (p.chunks < 2 || !p.ok)
-        return;
-    const Entry e = load_entry(a.c, a.nv, i);
     const int node = rest / a.a.q_heads, qh = rest - node * a.a.q_heads;
-    if (node >= e.count)
+    if (node >= p.count)
         return;
-    const int D = a.a.head_dim, G = a.a.group, head = qh / G;
-    const int gr = node * G + qh - head * G, mt = gr / rows_per_tile, row = gr - mt * rows_per_tile;
-    auto kept = [&](int c) {
-        return ((int64_t)p.part + ((int64_t)c * a.a.kv_heads + head) * p.tiles + mt) * rows_per_tile + row;
-    };
+    const int64_t share = *a.a.share;
+    const int D = a.a.head_dim, head = divide(qh, a.a.by_group);
+    const int gr = node * a.a.group + qh - head * a.a.group, mt = gr / rows_per_tile, row = gr - mt * rows_per_tile;
+    const int64_t base = p.base + ((int64_t)head * p.tiles_of_rows + mt) * p.tiles;
+    const int64_t w0 = quotient(base, share);
+    const int parts = (int)(quotient(base + p.tiles - 1, share) - w0) + 1;
+    if (parts < 2 || !a.a.sound[i])
+        return;
+    auto kept = [&](int c) { return (2 * (w0 + c) + (c == 0)) * rows_per_tile + row; };
     float top = -INFINITY;
-    for (int c = lane; c < p.chunks; c += 64)
+    for (int c = lane; c < parts; c += LG)
         top = fmaxf(top, a.a.part_ml[kept(c)].x);
-    top = wave_max(top);
+#pragma unroll
+    for (int s = LG / 2; s > 0; s >>= 1)
+        top = fmaxf(top, __shfl_xor(top, s, LG));
     float z = 0.0f, acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    for (int c0 = 0; c0 < p.chunks; c0 += 64) {
+    for (int c0 = 0; c0 < parts; c0 += LG) {
         float f = 0.0f, part = 0.0f;
-        if (c0 + lane < p.chunks) {
+        if (c0 + lane < parts) {
             const float2 ml = a.a.part_ml[kept(c0 + lane)];
             f = ml.x == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(ml.x - top);
             part = f * ml.y;
         }
 #pragma unroll
-        for (int s = 32; s > 0; s >>= 1)
-            part += __shfl_xor(part, s);
+        for (int s = LG / 2; s > 0; s >>= 1)
+            part += __shfl_xor(part, s, LG);
         z += part;
-        const int most = min(p.chunks - c0, 64);
-#pragma unroll 8
-        for (int c = 0; c < most; ++c) {
-            const float fc = __shfl(f, c);
-            if (lane * 4 < D) {
-                const float4 v = *reinterpret_cast<const float4 *>(a.a.part_o + kept(c0 + c) * D + lane * 4);
-                acc[0] += fc * v.x;
-                acc[1] += fc * v.y;
-                acc[2] += fc * v.z;
-                acc[3] += fc * v.w;
+        const int most = min(parts - c0, LG);
+        for (int c1 = 0; c1 < most; c1 += 8) {
+            float4 v[8];
+#pragma unroll
+            for (int c = 0; c < 8; ++c)
+                v[c] = c1 + c < most && lane * 4 < D
+                           ? *reinterpret_cast<const float4 *>(a.a.part_o + kept(c0 + c1 + c) * D + lane * 4)
+                           : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+            for (int c = 0; c < 8; ++c) {
+                const float fc = __shfl(f, min(c1 + c, most - 1), LG);
+                acc[0] += fc * v[c].x;
+                acc[1] += fc * v[c].y;
+                acc[2] += fc * v[c].z;
+                acc[3] += fc * v[c].w;
             }
         }
     }
-    char *to = a.out + (int64_t)(e.start + node) * a.out_stride + ((int64_t)qh * D + lane * 4) * ES;
+    char *to = a.out + (int64_t)(p.start + node) * a.out_stride + ((int64_t)qh * D + lane * 4) * ES;
     if (lane * 4 < D)
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
@@ -1033,31 +1093,31 @@ template <int DT> __global__ __launch_bounds__(ATTN_WG) void k_attend_join(AttnA
                 reinterpret_cast<float *>(to)[x] = v;
         }
     if (a.lse && lane == 0)
-        a.lse[(int64_t)(e.start + node) * a.a.q_heads + qh] =
+        a.lse[(int64_t)(p.start + node) * a.a.q_heads + qh] =
             z == 0.0f ? -INFINITY : (top + log2f(z)) * LN2;
 }
 
 // The launch of a form for tiles of `rows` rows.
 template <typename K> hipError_t attend_with(hipStream_t st, K kernel, AttnArgs a, int threads, int rows, int per_cu)
 {
-    a.units = std::min(a.a.num_cus * per_cu, ATTN_MAX_UNITS);
-    const int64_t segments = (int64_t)a.nv.n * a.a.kv_heads * ((a.nv.max_count * a.a.group + rows - 1) / rows);
-    // workgroups stand by dies, each of which may have one part more than its share
-    const unsigned grid = (unsigned)(a.units + segments + 8);
-    kernel<<<grid, threads, 0, st>>>(a);
-    hipError_t e = hipGetLastError();
+    a.units = (std::min(a.a.num_cus * per_cu, ATTN_MAX_UNITS) + 7) / 8 * 8;
+    kernel<<<a.units, threads, 0, st>>>(a);
+    const hipError_t e = hipGetLastError();
     if (e != hipSuccess)
         return e;
-    const int64_t joined = (int64_t)a.nv.n * a.nv.max_count * a.a.q_heads;
-    const unsigned groups = (unsigned)((joined + 3) / 4);
-    a.a.dtype == 1 ? k_attend_join<1><<<groups, ATTN_WG, 0, st>>>(a, rows)
-                   : k_attend_join<0><<<groups, ATTN_WG, 0, st>>>(a, rows);
+    const int lanes = a.a.head_dim <= 64 ? 16 : a.a.head_dim <= 128 ? 32 : 64;
+    const int64_t joined = (int64_t)a.nv.n * a.nv.max_count * a.a.q_heads, each = ATTN_WG / lanes;
+    const unsigned groups = (unsigned)((joined + each - 1) / each);
+    auto join = a.a.dtype == 1 ? (lanes == 16 ? k_attend_join<1, 16> : lanes == 32 ? k_attend_join<1, 32> : k_attend_join<1, 64>)
+                               : (lanes == 16 ? k_attend_join<0, 16> : lanes == 32 ? k_attend_join<0, 32> : k_attend_join<0, 64>);
+    if (groups > 0)
+        join<<<groups, ATTN_WG, 0, st>>>(a, rows);
     return hipGetLastError();
 }
 
 }  // namespace
 
-int64_t attend_kept_rows(int num_cus) { return 2 * std::max<int64_t>(ATTN_MAX_UNITS * 32, num_cus * 256); }
+int64_t attend_kept_rows(int num_cus) { return 2 * std::max<int64_t>(ATTN_MAX_UNITS * 32, (num_cus + 7) / 8 * 8 * 256); }
 
 hipError_t launch_attend(hipStream_t st, const CacheView &c, const AttnShape &s, const NodesView &nodes,
                          int key_pool, int value_pool, float scale, int window, const void *q,
@@ -1287,8 +1347,8 @@ template <int DT> hipError_t append_with(hipStream_t st, AppendArgs &a, bool vec
     const int per_token = ((a.q ? a.a.q_heads : 0) + Hk) * per_head + Hk * D / n_el;
     a.by_head = fast_div(per_head);
     a.by_token = fast_div(per_token);
-    a.tokens = std::min(APPEND_TOKENS, a.nv.max_count);
-    const int64_t groups = (a.nv.max_count + a.tokens - 1) / a.tokens;
+    a.tokens = std::max(std::min(APPEND_TOKENS, a.nv.max_count), 1);
+    const int64_t groups = std::max<int64_t>(((int64_t)a.nv.max_count + a.tokens - 1) / a.tokens, 1);
     // a piece to a thread where there are few tokens
     const int64_t want = 2 * (int64_t)a.a.num_cus / std::max<int64_t>(1, groups * a.nv.n);
     const int64_t most = ((int64_t)a.tokens * per_token + ATTN_WG - 1) / ATTN_WG;

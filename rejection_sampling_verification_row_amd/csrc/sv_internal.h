@@ -293,8 +293,7 @@ constexpr int ATTN_WG = 256;
 constexpr int ATTN_WIDE_WG = 512;
 constexpr int ATTN_MAX_HEAD_DIM = 256;
 constexpr int ATTN_MAX_ENTRIES = 1 << 16;
-constexpr int ATTN_MAX_UNITS = 1024;  // parts that a call's work is cut into, at most (but for a part
-                                      // for each key head and tile of rows of an entry)
+constexpr int ATTN_MAX_UNITS = 1024;  // workgroups of a call
 
 // j / d for 0 <= j < 2^31: (j m) >> (31 + s), with m = floor(2^(31 + s) / d) + 1 < 2^32 and
 // 2^(s-1) < d <= 2^s: m d exceeds 2^(31 + s) by at most d, so that the quotient is exact.
@@ -321,13 +320,11 @@ struct NodesView {
     const int *seqs, *starts, *counts, *parents;
 };
 
-// What the parts of an entry's work leave for their joining: the number of parts of a segment (a
-// key head and a tile of rows), where they are kept, and the rows of a tile.
+// An entry's work, for the joining of its parts: its first tile among all, the tiles of tokens of a
+// segment (a key head and a tile of rows), the tiles of rows, its rows.
 struct AttnPlan {
-    int chunks;          // 0: refused, or nothing to do
-    int part;            // first kept part (chunks > 1)
-    int tiles;           // tiles of rows
-    int ok;              // the parents are sound; written by the entry's first part
+    int64_t base;
+    int tiles, tiles_of_rows, start, count;
 };
 
 struct AttnShape {
@@ -335,12 +332,14 @@ struct AttnShape {
     FastDiv by_group, by_page;
     int num_cus;
     AttnPlan *plan;      // [max_entries]
-    float2 *part_ml;     // [2 units][rows of a tile] maximum (times scale, in powers of 2) and sum
-    float *part_o;       // [2 units][rows of a tile][head_dim] sums of weighted values
+    int *sound;          // [max_entries] the parents are; written by the entry's first workgroup
+    int64_t *share;      // tiles to a workgroup
+    float2 *part_ml;     // [2 workgroups][rows of a tile] maximum (times scale, in powers of 2) and sum
+    float *part_o;       // [2 workgroups][rows of a tile][head_dim] sums of weighted values
 };
 
-// Rows that the parts of any call leave at most: twice the parts that fill the chip (an entry that is
-// split at all is split into at most twice its share), with the rows of each.
+// Rows that the parts of any call leave at most: a workgroup may have two segments that it shares with
+// others, the first and the last.
 int64_t attend_kept_rows(int num_cus);
 
 hipError_t launch_attend(hipStream_t st, const CacheView &c, const AttnShape &a, const NodesView &nodes,

@@ -305,6 +305,9 @@ def test_a_sequence_named_twice_and_no_entries():
     s.given["seqs"][:] = s.given["seqs"][0]
     s.device().check_attend()             # two sets of nodes on one sequence: read alike
     check_append(s, 64, 0, want=[0, -1])
+    s.max_count = 0                      # nothing may come: entries with nodes are refused
+    assert s.attend(0.1)[2].tolist() == [-1, -1]
+    check_append(s, 64, 0, want=[-1, -1])
     s.n = 0
     out = s.attend(0.1)
     assert torch.all(out[0] == 7)
