@@ -187,34 +187,26 @@ template <int KT> __device__ inline Work entry_work(const AttnArgs &a, const Ent
 }
 
 // All tiles stand in a row, entry by entry and in an entry segment by segment, and every workgroup
-// takes the same number of them: `share`, the mine-th ones.
-struct Stretch {
-    int64_t at, end;
-    int mine;                            // < 0: none
-};
-
-// What a workgroup works on: tiles t0 .. t1 of a segment's tokens.
+// takes the same number of them.  What it works on, in LDS, so that it takes no registers while it
+// works: tiles t0 .. t1 of a segment's tokens, then from `at` on.
 struct Job {
+    int64_t at, end;                     // its stretch of all tiles, what is left of it
+    int64_t base;                        // the entry's first tile among all
+    int mine;                            // the stretch's number; < 0: none, or nothing left
     int entry;
-    int64_t base;                        // its first tile among all
     Entry e;
-    Work w;
-    bool ok;                             // the parents are sound
-    uint64_t lane_seen;                  // lane_node of the entry's nodes
-    int lane_depth;
-    int head, mt, t0, t1, rows, total;
-    bool whole;                          // else the sums go to this slot of the kept ones:
+    int head, mt, t0, t1;
+    int opens;                           // this is the entry's first tile
+    int whole;                           // all of the segment; else the sums go to this slot of the kept ones:
     int slot;
 };
 
 // This workgroup's stretch and the entry that it begins in.  Workgroup 0 also leaves the plan for the
-// join, and the status of entries that have no work.
+// join, and the status of entries that have no work.  False: there is no stretch for it.
 template <int WG_SIZE, int KT>
-__device__ Stretch find_stretch(const AttnArgs &a, int rows_per_tile, int least, Job &job)
+__device__ bool find_stretch(const AttnArgs &a, int rows_per_tile, int least, Job &job)
 {
-    __shared__ int64_t lds[WG_SIZE / 64], found_base;
-    __shared__ Entry found;
-    __shared__ int found_entry;
+    __shared__ int64_t lds[WG_SIZE / 64];
     const int n = a.nv.n, t = threadIdx.x;
     Entry e0 = {-1, 0, -1, 0};
     if (t < n)
@@ -228,14 +220,12 @@ __device__ Stretch find_stretch(const AttnArgs &a, int rows_per_tile, int least,
     const int64_t share = max(quotient(sum + a.units - 1, a.units), (int64_t)least);
     // neighbours, which read the same tokens, on one of the 8 dies, to which workgroups go in turn
     const int active = (int)quotient(sum + share - 1, share), each = (active + 7) / 8;
-    Stretch st;
-    st.mine = (int)(blockIdx.x & 7) * each + (int)(blockIdx.x >> 3);
-    if ((int)(blockIdx.x >> 3) >= each || st.mine >= active)
-        st.mine = -1;
-    st.at = st.mine * share;
-    st.end = min(st.at + share, sum);
-    if (st.mine < 0 && blockIdx.x != 0)
-        return st;
+    int mine = (int)(blockIdx.x & 7) * each + (int)(blockIdx.x >> 3);
+    if ((int)(blockIdx.x >> 3) >= each || mine >= active)
+        mine = -1;
+    const int64_t at = mine * share;
+    if (mine < 0 && blockIdx.x != 0)
+        return false;
     int64_t base = 0;
     for (int i0 = 0; i0 < n; i0 += WG_SIZE) {
         const int i = i0 + t;
@@ -246,10 +236,13 @@ __device__ Stretch find_stretch(const AttnArgs &a, int rows_per_tile, int least,
         const int64_t work = (int64_t)w.segments * w.tiles;
         int64_t all;
         const int64_t first = base + block_scan<WG_SIZE>(work, lds, &all) - work;
-        if (st.mine >= 0 && st.at >= first && st.at < first + work) {
-            found = e;
-            found_entry = i;
-            found_base = first;
+        if (mine >= 0 && at >= first && at < first + work) {
+            job.at = at;
+            job.end = min(at + share, sum);
+            job.base = first;
+            job.mine = mine;
+            job.entry = i;
+            job.e = e;
         }
         if (blockIdx.x == 0 && i < n) {
             a.a.plan[i] = {first, w.tiles, w.tiles_of_rows, e.start, max(e.count, 0)};
@@ -261,53 +254,61 @@ __device__ Stretch find_stretch(const AttnArgs &a, int rows_per_tile, int least,
     if (blockIdx.x == 0 && t == 0)
         *a.a.share = share;
     __syncthreads();
-    if (st.mine >= 0) {
-        job.entry = uniform(found_entry);
-        job.base = uniform(found_base);
-        job.e = {uniform(found.seq), uniform(found.start), uniform(found.count), uniform(found.len)};
-        job.w = entry_work<KT>(a, job.e, rows_per_tile);
-    }
-    return st;
+    return mine >= 0;
 }
 
-// The entry's nodes; the workgroup that has its first tile says whether they are sound.
-__device__ inline void open_entry(const AttnArgs &a, const Stretch &st, Job &job)
+// The next job of the stretch, found by the first wave; false at its end.
+template <int KT> __device__ inline bool next_job(const AttnArgs &a, int rows_per_tile, Job &job)
 {
-    job.ok = lane_node(a.nv.parents ? a.nv.parents + job.e.start : nullptr, job.e.count, a.window, job.lane_seen,
-                       job.lane_depth);
-    if (st.at == job.base && threadIdx.x == 0) {
-        a.a.sound[job.entry] = job.ok;
+    if (threadIdx.x < 64) {
+        const int64_t at = uniform(job.at), end = uniform(job.end);
+        if (at >= end) {
+            if (threadIdx.x == 0)
+                job.mine = -1;
+        } else {
+            int64_t base = uniform(job.base);
+            int entry = uniform(job.entry);
+            Entry e = {uniform(job.e.seq), uniform(job.e.start), uniform(job.e.count), uniform(job.e.len)};
+            Work w = entry_work<KT>(a, e, rows_per_tile);
+            while (at >= base + (int64_t)w.segments * w.tiles) {
+                base += (int64_t)w.segments * w.tiles;
+                e = load_entry(a.c, a.nv, ++entry);
+                w = entry_work<KT>(a, e, rows_per_tile);
+            }
+            const int64_t rel = at - base, segment = quotient(rel, w.tiles);
+            const int off = (int)(rel - segment * w.tiles);
+            const int take = (int)min((int64_t)(w.tiles - off), end - at);
+            if (threadIdx.x == 0) {
+                job.at = at + take;
+                job.base = base;
+                job.entry = entry;
+                job.e = e;
+                job.head = (int)segment / w.tiles_of_rows;
+                job.mt = (int)segment - job.head * w.tiles_of_rows;
+                job.t0 = w.low + off;
+                job.t1 = w.low + off + take;
+                job.opens = rel == 0;
+                job.whole = take == w.tiles;
+                job.slot = 2 * job.mine + (off == 0);
+            }
+        }
+    }
+    __syncthreads();
+    return uniform(job.mine) >= 0;
+}
+
+// Whether the parents of the job's entry are sound, and if so what a lane's node sees; the workgroup
+// that has the entry's first tile says it.
+__device__ inline bool open_job(const AttnArgs &a, const Job &job, uint64_t &seen, int &depth)
+{
+    const int start = uniform(job.e.start), count = uniform(job.e.count);
+    const bool ok = lane_node(a.nv.parents ? a.nv.parents + start : nullptr, count, a.window, seen, depth);
+    if (uniform(job.opens) && threadIdx.x == 0) {
+        a.a.sound[job.entry] = ok;
         if (a.status)
-            a.status[job.entry] = job.ok ? 0 : -1;
+            a.status[job.entry] = ok ? 0 : -1;
     }
-    job.rows = job.e.count * a.a.group;
-    job.total = job.e.len + job.e.count;
-}
-
-// The next job of the stretch, from where it stands on; false at its end.
-template <int KT>
-__device__ inline bool next_job(const AttnArgs &a, int rows_per_tile, Stretch &st, Job &job)
-{
-    if (st.mine < 0 || st.at >= st.end)
-        return false;
-    while (st.at >= job.base + (int64_t)job.w.segments * job.w.tiles) {
-        job.base += (int64_t)job.w.segments * job.w.tiles;
-        job.e = load_entry(a.c, a.nv, ++job.entry);
-        job.w = entry_work<KT>(a, job.e, rows_per_tile);
-        if (job.w.tiles > 0)
-            open_entry(a, st, job);
-    }
-    const int64_t rel = st.at - job.base, segment = quotient(rel, job.w.tiles);
-    const int off = (int)(rel - segment * job.w.tiles);
-    const int take = (int)min((int64_t)(job.w.tiles - off), st.end - st.at);
-    job.head = (int)segment / job.w.tiles_of_rows;
-    job.mt = (int)segment - job.head * job.w.tiles_of_rows;
-    job.t0 = job.w.low + off;
-    job.t1 = job.t0 + take;
-    job.whole = take == job.w.tiles;
-    job.slot = 2 * st.mine + (off == 0);
-    st.at += take;
-    return true;
+    return ok;
 }
 
 template <int DT> struct Tile;
@@ -348,61 +349,63 @@ __device__ inline float row_sum(float v)
 // there, and so must the keys be, whatever follows them in memory.
 __device__ const uint4 past_the_head = {0, 0, 0, 0};
 
-// The rows of a lane's columns: what they see, and from where on.
-template <int R> struct Rows {
-    uint64_t seen[R];
-    int low[R];
-    int low_most;
-};
-
-// A wave's R tiles of rows from `first` on, with their queries as right operands.
+// A wave's R tiles of rows from `first` on, with their queries as right operands.  What a row sees and
+// from which token on go to LDS, the least token that all see is returned.
 template <int DT, int KS, int R>
-__device__ inline void load_rows(const AttnArgs &a, const Job &j, int first, Rows<R> &rows,
-                                 typename Tile<DT>::vec (&q)[R][KS])
+__device__ inline int load_rows(const AttnArgs &a, const Job &job, uint64_t lane_seen, int lane_depth, int first,
+                                uint64_t *seen, int *low, typename Tile<DT>::vec (&q)[R][KS])
 {
     constexpr int ES = Tile<DT>::ES;
     const int col = threadIdx.x & 15, grp = threadIdx.x >> 4 & 3, D = a.a.head_dim, G = a.a.group;
-    rows.low_most = 0;
+    const int start = uniform(job.e.start), len = uniform(job.e.len), rows = uniform(job.e.count) * G;
+    const char *base = a.q + (int64_t)start * a.q_stride + (int64_t)uniform(job.head) * G * D * ES;
+    const bool aligned = (reinterpret_cast<uintptr_t>(a.q) | (uintptr_t)a.q_stride) % 16 == 0;
+    int most = 0;
+    u32x4 v[R][KS];
 #pragma unroll
     for (int r = 0; r < R; ++r) {
         const int row = first + r * 16 + col;
-        const int node = row < j.rows ? divide(row, a.a.by_group) : 0;
-        rows.seen[r] = __shfl((unsigned long long)j.lane_seen, node);
-        const int depth = __shfl(j.lane_depth, node);
-        rows.low[r] = a.window > 0 ? max(j.e.len - a.window + 1 + depth, 0) : 0;
-        rows.low_most = max(rows.low_most, rows.low[r]);
-        const char *qp = a.q + (int64_t)(j.e.start + node) * a.q_stride +
-                         (int64_t)(j.head * G + row - node * G) * D * ES;
-        const bool al = aligned16(qp);
+        const int node = row < rows ? divide(row, a.a.by_group) : 0;
+        const uint64_t sees = __shfl((unsigned long long)lane_seen, node);
+        const int depth = __shfl(lane_depth, node), from = a.window > 0 ? max(len - a.window + 1 + depth, 0) : 0;
+        most = max(most, from);
+        if (grp == 0) {
+            seen[r * 16 + col] = sees;
+            low[r * 16 + col] = from;
+        }
+        const char *qp = base + node * a.q_stride + (row - node * G) * D * ES;
 #pragma unroll
         for (int s = 0; s < KS; ++s) {
             const int d = (s * 64 + grp * 16) / ES;
-            uint4 v = make_uint4(0, 0, 0, 0);
-            if (row < j.rows && d < D) {
-                if (al) {
-                    v = load_plain(qp + d * ES);
+            v[r][s] = u32x4{0, 0, 0, 0};
+            if (row < rows && d < D) {
+                if (aligned) {
+                    v[r][s] = load_global<u32x4>(qp + d * ES);
                 } else if constexpr (DT == 1) {
-                    const uint16_t *p = reinterpret_cast<const uint16_t *>(qp) + d;
-                    v = make_uint4(p[0] | (uint32_t)p[1] << 16, p[2] | (uint32_t)p[3] << 16,
-                                   p[4] | (uint32_t)p[5] << 16, p[6] | (uint32_t)p[7] << 16);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        v[r][s][i] = load_global<uint16_t>(qp + (d + 2 * i) * ES) |
+                                     (uint32_t)load_global<uint16_t>(qp + (d + 2 * i + 1) * ES) << 16;
                 } else {
-                    const uint32_t *p = reinterpret_cast<const uint32_t *>(qp) + d;
-                    v = make_uint4(p[0], p[1], p[2], p[3]);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        v[r][s][i] = load_global<uint32_t>(qp + (d + i) * ES);
                 }
             }
-            if (a.q_sign == 0.0f) {
-                v = make_uint4(0, 0, 0, 0);
-            } else if (a.q_sign < 0.0f) {
-                const uint32_t f = DT == 1 ? 0x80008000u : 0x80000000u;
-                v = make_uint4(v.x ^ f, v.y ^ f, v.z ^ f, v.w ^ f);
-            }
-            q[r][s] = __builtin_bit_cast(typename Tile<DT>::vec, v);
         }
     }
+    // scale's sign
+    const uint32_t keep = a.q_sign == 0.0f ? 0u : ~0u;
+    const uint32_t flip = a.q_sign < 0.0f ? (DT == 1 ? 0x80008000u : 0x80000000u) : 0u;
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int s = 0; s < KS; ++s)
+            q[r][s] = __builtin_bit_cast(typename Tile<DT>::vec, (v[r][s] & keep) ^ flip);
 #pragma unroll
     for (int o = 8; o > 0; o >>= 1)
-        rows.low_most = max(rows.low_most, __shfl_xor(rows.low_most, o));
-    rows.low_most = uniform(rows.low_most);
+        most = max(most, __shfl_xor(most, o));
+    return uniform(most);
 }
 
 // Which of the 32 tokens from j0 on a row sees, as bits.
@@ -419,33 +422,47 @@ __device__ inline uint32_t visible(int len, int low, uint64_t seen, int j0, uint
 }
 
 // Scores of a tile become weights against the running maximum m (of the raw scores); what was summed
-// before is scaled where the maximum grew.
-template <int SUB, int NT>
-__device__ inline void weigh(f32x4 (&s)[SUB], f32x4 (&o)[NT], float &m, float &l, float c1)
+// before is scaled where a maximum grew.
+template <int SUB, int NT, int R>
+__device__ inline void weigh(f32x4 (&s)[R][SUB], f32x4 (&o)[R][NT], float (&m)[R], float (&l)[R], float c1)
 {
-    float top = s[0][0];
+    float top[R];
+    bool grew = false;
 #pragma unroll
-    for (int x = 0; x < SUB; ++x)
+    for (int r = 0; r < R; ++r) {
+        top[r] = s[r][0][0];
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            top = fmaxf(top, s[x][i]);
-    if (__ballot(top > m) != 0) {
-        const float was = m;
-        m = fmaxf(was, row_max(top));
-        const float f = m == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f((was - m) * c1);
-        l *= f;
+        for (int x = 0; x < SUB; ++x)
 #pragma unroll
-        for (int i = 0; i < NT; ++i)
-            o[i] *= f;
+            for (int i = 0; i < 4; ++i)
+                top[r] = fmaxf(top[r], s[r][x][i]);
+        grew |= top[r] > m[r];
     }
-    const float ref = m == -INFINITY ? 0.0f : m * c1;
+    if (__ballot(grew) != 0) {
 #pragma unroll
-    for (int x = 0; x < SUB; ++x)
+        for (int r = 0; r < R; ++r) {
+            const float was = m[r];
+            m[r] = fmaxf(was, row_max(top[r]));
+            const float f = m[r] == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f((was - m[r]) * c1);
+            l[r] *= f;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            s[x][i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[x][i], c1, -ref));
-            l += s[x][i];
+            for (int i = 0; i < NT; ++i)
+                o[r][i] *= f;
         }
+    }
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        const float ref = m[r] == -INFINITY ? 0.0f : m[r] * c1;
+        float sum[SUB];
+#pragma unroll
+        for (int x = 0; x < SUB; ++x) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                s[r][x][i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[r][x][i], c1, -ref));
+            sum[x] = (s[r][x][0] + s[r][x][1]) + (s[r][x][2] + s[r][x][3]);
+        }
+        l[r] += SUB == 2 ? sum[0] + sum[SUB - 1] : sum[0];
+    }
 }
 
 // The sums of `waves` waves over a tile of rows, joined, to the output or to the kept ones: row i at
@@ -456,7 +473,7 @@ __device__ inline void finish(const AttnArgs &a, const Job &j, int rows_per_tile
 {
     constexpr int ES = Tile<DT>::ES;
     const int D = a.a.head_dim, G = a.a.group, first = j.mt * rows_per_tile;
-    const int rows = min(j.rows - first, rows_per_tile);
+    const int rows = min(j.e.count * G - first, rows_per_tile);
     for (int i = threadIdx.x; i < rows * (D / 4); i += WG_SIZE) {
         const int row = i / (D / 4), d = (i - row * (D / 4)) * 4;
         float top = -INFINITY;
@@ -517,25 +534,32 @@ __global__ __launch_bounds__(ATTN_WG, OCC) void k_attend(AttnArgs a)
     __shared__ float s_o[4 * ROWS][PITCH];
     __shared__ float2 s_ml[4 * ROWS];
     __shared__ int64_t s_off[4][2][KT];
+    __shared__ uint64_t s_seen[ROWS];
+    __shared__ int s_low[ROWS];
+    __shared__ Job job;
 
     const int lane = threadIdx.x & 63, w = uniform((int)(threadIdx.x >> 6)), col = lane & 15, grp = lane >> 4;
-    Job job;
-    Stretch stretch = find_stretch<ATTN_WG, KT>(a, ROWS, 128 / KT, job);
-    if (stretch.mine < 0)
+    if (!find_stretch<ATTN_WG, KT>(a, ROWS, 128 / KT, job))
         return;
-    open_entry(a, stretch, job);
-    while (next_job<KT>(a, ROWS, stretch, job)) {
-    if (!job.ok)
-        continue;
-    const int D = a.a.head_dim, len = job.e.len, total = job.total, t1 = job.t1;
-    Rows<R> rows;
+    while (next_job<KT>(a, ROWS, job)) {
+    uint64_t lane_seen;
+    int lane_depth;
+    const bool ok = open_job(a, job, lane_seen, lane_depth);
+    const int D = a.a.head_dim, len = uniform(job.e.len), total = len + uniform(job.e.count);
+    const int t0 = uniform(job.t0), t1 = uniform(job.t1), head = uniform(job.head);
     typename TL::vec q[R][KS];
-    load_rows<DT, KS, R>(a, job, job.mt * ROWS, rows, q);
+    // all waves write the same rows
+    const int low_most =
+        ok ? load_rows<DT, KS, R>(a, job, lane_seen, lane_depth, uniform(job.mt) * ROWS, s_seen, s_low, q) : 0;
+    if (!ok) {
+        __syncthreads();
+        continue;
+    }
 
-    const int *table = a.c.tables + (size_t)job.e.seq * a.c.max_blocks;
+    const int *table = a.c.tables + (size_t)uniform(job.e.seq) * a.c.max_blocks;
     const int64_t row_bytes = (int64_t)a.a.kv_heads * D * ES;
-    const char *kp = a.c.pools[a.key_pool] + (int64_t)job.head * D * ES;
-    const char *vp = a.c.pools[a.value_pool] + (int64_t)job.head * D * ES;
+    const char *kp = a.c.pools[a.key_pool] + (int64_t)head * D * ES;
+    const char *vp = a.c.pools[a.value_pool] + (int64_t)head * D * ES;
     const char *zeros = reinterpret_cast<const char *>(&past_the_head);
 
     // a tile's page ids, one token to a lane, then the tokens' places; bits of what has no place
@@ -591,7 +615,7 @@ __global__ __launch_bounds__(ATTN_WG, OCC) void k_attend(AttnArgs a)
             o[r][i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     }
 
-    int t = job.t0 + w, buf = 0, next_page = 0;
+    int t = t0 + w, buf = 0, next_page = 0;
     const int last = t1 - 1 - (t1 - 1 - t & 3);          // this wave's last tile
     uint32_t lost = 0;
     if (t < t1) {
@@ -625,12 +649,12 @@ __global__ __launch_bounds__(ATTN_WG, OCC) void k_attend(AttnArgs a)
         next_page = page_of(min(t + 8, last));
         load_keys(buf ^ 1);
         const unsigned j0 = (unsigned)t * KT;
-        const bool masked = j0 + KT > (unsigned)len || lost != 0 || (int)j0 < rows.low_most;
+        const bool masked = j0 + KT > (unsigned)len || lost != 0 || (int)j0 < low_most;
         uint32_t vis[R];                 // the tile's tokens that a row sees
         if (masked) {
 #pragma unroll
             for (int r = 0; r < R; ++r) {
-                vis[r] = visible(len, rows.low[r], rows.seen[r], (int)j0, lost);
+                vis[r] = visible(len, s_low[r * 16 + col], s_seen[r * 16 + col], (int)j0, lost);
 #pragma unroll
                 for (int x = 0; x < SUB; ++x)
 #pragma unroll
@@ -638,9 +662,7 @@ __global__ __launch_bounds__(ATTN_WG, OCC) void k_attend(AttnArgs a)
                         s[r][x][i] = vis[r] >> (grp * 4) & (1u << (x * 16 + i)) ? s[r][x][i] : -INFINITY;
             }
         }
-#pragma unroll
-        for (int r = 0; r < R; ++r)
-            weigh<SUB, NT>(s[r], o[r], m[r], l[r], a.c1);
+        weigh<SUB, NT, R>(s, o, m, l, a.c1);
         if (masked) {
             // What a row does not see may be anything: rows of values with an infinity or a NaN are left
             // out of the product and added to the rows that see them, one by one.
@@ -795,6 +817,7 @@ __global__ __launch_bounds__(ATTN_WIDE_WG, 1) void k_attend_wide(AttnArgs a)
     constexpr int ROWS = 16 * R * WR, PITCH = DP + 4, DEPTH = STAGES - 1;
     constexpr int HALF = TK * ROW, LOADS = HALF / 1024 / WAVES8;      // bytes of keys in a stage; a wave's loads
     constexpr int PAGE_AHEAD = 2 * DEPTH + 1;
+    constexpr int EARLY = NT < 8 ? NT : 8;        // pieces of values read before the weights are there
     static_assert(LOADS * 1024 * WAVES8 == HALF && DEPTH <= 3 && TK <= ATTN_WIDE_WG, "whole loads, rings of 4 stages");
     constexpr int MERGE = WAVES8 * 16 * R * PITCH * 4;
     __shared__ __attribute__((aligned(1024))) char mem[MERGE > STAGES * 2 * HALF ? MERGE : STAGES * 2 * HALF];
@@ -802,193 +825,226 @@ __global__ __launch_bounds__(ATTN_WIDE_WG, 1) void k_attend_wide(AttnArgs a)
     __shared__ int64_t s_off[4][TK];
     __shared__ int s_page[4][TK < 64 ? 64 : TK];
     __shared__ uint32_t s_lost[8][TK / 32];
+    __shared__ uint64_t s_seen[ROWS];
+    __shared__ int s_low[ROWS];
+    __shared__ Job job;
 
     const int t = threadIdx.x, lane = t & 63, w = uniform((int)(t >> 6)), col = lane & 15, grp = lane >> 4;
     const int rw = w % WR, kg = w / WR;
-    Job job;
-    Stretch stretch = find_stretch<ATTN_WIDE_WG, TK>(a, ROWS, 1, job);
-    if (stretch.mine < 0)
+    if (!find_stretch<ATTN_WIDE_WG, TK>(a, ROWS, 1, job))
         return;
-    open_entry(a, stretch, job);
-    while (next_job<TK>(a, ROWS, stretch, job)) {
-    if (!job.ok)
-        continue;
-    const int D = a.a.head_dim, len = job.e.len, total = job.total, stages = job.t1 - job.t0;
-    const int first = job.mt * ROWS + rw * 16 * R;
-    Rows<R> rows;
-    bf16x8 q[R][KS];
-    load_rows<1, KS, R>(a, job, first, rows, q);
-
-    const int *table = a.c.tables + (size_t)job.e.seq * a.c.max_blocks;
-    const int64_t row_bytes = (int64_t)a.a.kv_heads * D * 2;
-    const char *kp = a.c.pools[a.key_pool] + (int64_t)job.head * D * 2;
-    const char *vp = a.c.pools[a.value_pool] + (int64_t)job.head * D * 2;
-    const char *zeros = reinterpret_cast<const char *>(&past_the_head);
-
-    auto token_of = [&](int stage, int i) {
-        return (int)min((unsigned)(job.t0 + stage) * TK + i, (unsigned)total - 1);
-    };
-    // from a stage's page ids the places of its tokens, and which have none
-    auto put_places = [&](int stage, int pg) {
-        if (t < TK) {
-            const int j = token_of(stage, t), b = divide(j, a.a.by_page);
-            const bool good = in_range(pg, a.c.num_pages);
-            s_off[stage & 3][t] = ((int64_t)(good ? pg : 0) * a.c.page_tokens + (j - b * a.c.page_tokens)) * row_bytes;
-            const uint64_t bad = __ballot(!good);
-            if ((lane & 31) == 0)
-                s_lost[stage & 7][t / 32] = (uint32_t)(bad >> (lane & 32));
+    while (next_job<TK>(a, ROWS, job)) {
+        uint64_t lane_seen;
+        int lane_depth;
+        const bool ok = open_job(a, job, lane_seen, lane_depth);
+        if (!ok) {
+            __syncthreads();
+            continue;
         }
-    };
-    // page ids of a stage, one load of every wave (waves past the stage's tokens repeat others')
-    auto load_pages = [&](int stage) {
-        const int part = w * 64 % (TK < 64 ? 64 : TK), i = (part + lane) % TK;
-        const int *p = table + divide(token_of(min(stage, stages - 1), i), a.a.by_page);
-        load_to_lds4(p, lds_address(&s_page[stage & 3][part]));
-    };
-    auto load_stage = [&](int stage) {
-        const uint32_t to = lds_address(mem) + stage % STAGES * 2 * HALF;
+        bf16x8 q[R][KS];
+        // waves of the same rows write the same
+        const int low_most = load_rows<1, KS, R>(a, job, lane_seen, lane_depth, uniform(job.mt) * ROWS + rw * 16 * R,
+                                                 s_seen + rw * 16 * R, s_low + rw * 16 * R, q);
+        const int D = a.a.head_dim, len = uniform(job.e.len), total = len + uniform(job.e.count);
+        const int t0 = uniform(job.t0), stages = uniform(job.t1) - t0, head = uniform(job.head);
+        const int *table = a.c.tables + (size_t)uniform(job.e.seq) * a.c.max_blocks;
+        const int64_t row_bytes = (int64_t)a.a.kv_heads * D * 2;
+        const char *kp = a.c.pools[a.key_pool] + (int64_t)head * D * 2;
+        const char *vp = a.c.pools[a.value_pool] + (int64_t)head * D * 2;
+        const char *zeros = reinterpret_cast<const char *>(&past_the_head);
+
+        auto token_of = [&](int stage, int i) {
+            return (int)min((unsigned)(t0 + stage) * TK + i, (unsigned)total - 1);
+        };
+        // from a stage's page ids the places of its tokens, and which have none
+        auto put_places = [&](int stage, int pg) {
+            if (t < TK) {
+                const int j = token_of(stage, t), b = divide(j, a.a.by_page);
+                const bool good = in_range(pg, a.c.num_pages);
+                s_off[stage & 3][t] =
+                    ((int64_t)(good ? pg : 0) * a.c.page_tokens + (j - b * a.c.page_tokens)) * row_bytes;
+                const uint64_t bad = __ballot(!good);
+                if ((lane & 31) == 0)
+                    s_lost[stage & 7][t / 32] = (uint32_t)(bad >> (lane & 32));
+            }
+        };
+        // page ids of a stage, one load of every wave (waves past the stage's tokens repeat others')
+        auto load_pages = [&](int stage) {
+            const int part = w * 64 % (TK < 64 ? 64 : TK), i = (part + lane) % TK;
+            const int *p = table + divide(token_of(min(stage, stages - 1), i), a.a.by_page);
+            load_to_lds4(p, lds_address(&s_page[stage & 3][part]));
+        };
+        auto load_stage = [&](int stage) {
+            const uint32_t to = lds_address(mem) + stage % STAGES * 2 * HALF;
 #pragma unroll
-        for (int i = 0; i < LOADS; ++i) {
-            const int at = (i * WAVES8 + w) * 1024, row = (at + lane * 16) / ROW, slot = (at + lane * 16) % ROW / 16;
-            const int64_t off = s_off[stage & 3][row];
-            const int ck = slot ^ key_order<DP>(row), cv = slot ^ value_order<DP>(row);
-            const char *k = ck * 8 < D ? kp + off + ck * 16 : zeros, *v = cv * 8 < D ? vp + off + cv * 16 : zeros;
-            load_to_lds16(k, to + at);
-            load_to_lds16(v, to + HALF + at);
+            for (int i = 0; i < LOADS; ++i) {
+                const int at = (i * WAVES8 + w) * 1024, row = (at + lane * 16) / ROW;
+                const int slot = (at + lane * 16) % ROW / 16;
+                const int64_t off = s_off[stage & 3][row];
+                const int ck = slot ^ key_order<DP>(row), cv = slot ^ value_order<DP>(row);
+                const char *k = ck * 8 < D ? kp + off + ck * 16 : zeros, *v = cv * 8 < D ? vp + off + cv * 16 : zeros;
+                load_to_lds16(k, to + at);
+                load_to_lds16(v, to + HALF + at);
+            }
+        };
+
+        f32x4 o[R][NT];
+        float m[R], l[R];
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            m[r] = -INFINITY;
+            l[r] = 0.0f;
+#pragma unroll
+            for (int i = 0; i < NT; ++i)
+                o[r][i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
         }
-    };
+        for (int s = 0; s <= DEPTH && s < stages; ++s)
+            if (t < TK)
+                put_places(s, load_global<int>(table + divide(token_of(s, t), a.a.by_page)));
+        __syncthreads();
+        for (int s = 0; s < DEPTH; ++s) {
+            load_pages(s + DEPTH + 1);
+            if (s < stages)
+                load_stage(s);
+        }
 
-    f32x4 o[R][NT];
-    float m[R], l[R];
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-        m[r] = -INFINITY;
-        l[r] = 0.0f;
-#pragma unroll
-        for (int i = 0; i < NT; ++i)
-            o[r][i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    }
-    for (int s = 0; s <= DEPTH && s < stages; ++s)
-        if (t < TK)
-            put_places(s, load_global<int>(table + divide(token_of(s, t), a.a.by_page)));
-    __syncthreads();
-    for (int s = 0; s < DEPTH; ++s) {
-        load_pages(s + DEPTH + 1);
-        if (s < stages)
-            load_stage(s);
-    }
+        // This lane's bytes of the first block: piece `grp` of key row `col`, and 8 bytes of value row
+        // 4 grp + col / 4; other pieces of the rows differ in bits of the offset, since orders are xors.
+        const int key_at = col * ROW + (grp ^ key_order<DP>(col)) * 16;
+        const int value_row = grp * 4 + (col >> 2);
+        const int value_at = value_row * ROW + ((col >> 1 & 1) ^ value_order<DP>(value_row)) * 16 + (col & 1) * 8;
 
-    // This lane's bytes of the first block: piece `grp` of key row `col`, and 8 bytes of value row
-    // 4 grp + col / 4; other pieces of the rows differ in bits of the offset, since orders are xors.
-    const int key_at = col * ROW + (grp ^ key_order<DP>(col)) * 16;
-    const int value_row = grp * 4 + (col >> 2);
-    const int value_at = value_row * ROW + ((col >> 1 & 1) ^ value_order<DP>(value_row)) * 16 + (col & 1) * 8;
-
-    for (int i = 0; i < stages; ++i) {
-        // stage i and the page ids loaded with it are there; what came after may be under way
-        if (i + DEPTH <= stages)
-            asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"((DEPTH - 1) * (2 * LOADS + 1)) : "memory");
-        else
-            asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-        load_pages(i + PAGE_AHEAD);
-        if (i + DEPTH < stages)
-            load_stage(i + DEPTH);
-        if (i + DEPTH + 1 < stages && t < TK)
-            put_places(i + DEPTH + 1, s_page[i + DEPTH + 1 & 3][t]);
-        const int stage_at = i % STAGES * 2 * HALF;
-        const char *vals = mem + stage_at + HALF;
+        for (int i = 0; i < stages; ++i) {
+            // stage i and the page ids loaded with it are there; what came after may be under way
+            if (i + DEPTH <= stages)
+                asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"((DEPTH - 1) * (2 * LOADS + 1))
+                             : "memory");
+            else
+                asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+            load_pages(i + PAGE_AHEAD);
+            if (i + DEPTH < stages)
+                load_stage(i + DEPTH);
+            if (i + DEPTH + 1 < stages && t < TK)
+                put_places(i + DEPTH + 1, s_page[i + DEPTH + 1 & 3][t]);
+            const int stage_at = i % STAGES * 2 * HALF;
 #pragma unroll 1
-        for (int kb = 0; kb < KB; ++kb) {
-            const int b0 = (kg * KB + kb) * 32;
-            const unsigned j0 = (unsigned)(job.t0 + i) * TK + b0;
-            if (j0 >= (unsigned)total)
-                break;
-            const int lost_here = (int)s_lost[i & 7][b0 / 32];
-            f32x4 s[R][2];
+            for (int kb = 0; kb < KB; ++kb) {
+                const int b0 = (kg * KB + kb) * 32;
+                const unsigned j0 = (unsigned)(t0 + i) * TK + b0;
+                if (j0 >= (unsigned)total)
+                    break;
+                const int lost_here = (int)s_lost[i & 7][b0 / 32];
+                u32x4 kf[KS][2];
 #pragma unroll
-            for (int r = 0; r < R; ++r)
-                s[r][0] = s[r][1] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+                for (int k = 0; k < KS; ++k)
 #pragma unroll
-            for (int k = 0; k < KS; ++k)
+                    for (int x = 0; x < 2; ++x)
+                        kf[k][x] = *reinterpret_cast<const u32x4 *>(
+                            mem + ((key_at + stage_at + b0 * ROW) ^ k * 64) + x * 16 * ROW);
+                auto read_value = [&](int x, int h) {
+                    const char *at = mem + ((value_at + stage_at + b0 * ROW) ^ x * 32) + HALF + h * 16 * ROW;
+                    return __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4 *)at);
+                };
+                s16x4 vf[EARLY][2];
 #pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    const u32x4 kv = *reinterpret_cast<const u32x4 *>(
-                        mem + ((key_at + stage_at + b0 * ROW) ^ k * 64) + x * 16 * ROW);
+                for (int x = 0; x < EARLY; ++x)
 #pragma unroll
-                    for (int r = 0; r < R; ++r)
-                        s[r][x] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, kv), q[r][k],
-                                                                          s[r][x], 0, 0, 0);
-                }
-            const uint32_t lost = (uint32_t)uniform(lost_here);
-            const bool masked = j0 + 32 > (unsigned)len || lost != 0 || (int)j0 < rows.low_most;
-            uint32_t vis[R], odd = 0;
-            if (masked) {
+                    for (int h = 0; h < 2; ++h)
+                        vf[x][h] = read_value(x, h);
+                f32x4 s[R][2];
 #pragma unroll
-                for (int r = 0; r < R; ++r) {
-                    vis[r] = visible(len, rows.low[r], rows.seen[r], (int)j0, lost);
+                for (int r = 0; r < R; ++r)
+                    s[r][0] = s[r][1] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                for (int k = 0; k < KS; ++k)
 #pragma unroll
                     for (int x = 0; x < 2; ++x)
 #pragma unroll
-                        for (int y = 0; y < 4; ++y)
-                            s[r][x][y] = vis[r] >> (grp * 4) & (1u << (x * 16 + y)) ? s[r][x][y] : -INFINITY;
-                }
-            }
-#pragma unroll
-            for (int r = 0; r < R; ++r)
-                weigh<2, NT>(s[r], o[r], m[r], l[r], a.c1);
-            if (masked) {
-                // as in k_attend: rows of values with an infinity or a NaN are added one by one
-                for (int x = 0; x < 32 * PIECES / 64; ++x) {
-                    const int p = x * 64 + lane, row = p / PIECES;
-                    const u32x4 v = *reinterpret_cast<const u32x4 *>(vals + b0 * ROW + p * 16);
-                    const bool mine = odd_word<1>(v[0]) || odd_word<1>(v[1]) || odd_word<1>(v[2]) || odd_word<1>(v[3]);
-                    for (uint64_t all = __ballot(mine); all != 0; all &= all - 1)
-                        odd |= 1u << uniform(__shfl(row, __builtin_ctzll(all)));
-                }
-#pragma unroll 1
-                for (uint32_t left = odd; left != 0; left &= left - 1) {
-                    const int key = __builtin_ctz(left), row = b0 + key;
+                        for (int r = 0; r < R; ++r)
+                            s[r][x] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                                __builtin_bit_cast(bf16x8, kf[k][x]), q[r][k], s[r][x], 0, 0, 0);
+                const uint32_t lost = (uint32_t)uniform(lost_here);
+                const bool masked = j0 + 32 > (unsigned)len || lost != 0 || (int)j0 < low_most;
+                uint32_t odd = 0;
+                if (masked) {
+                    uint32_t vis[R];
 #pragma unroll
                     for (int r = 0; r < R; ++r) {
-                        float pr = 0.0f;
+                        vis[r] = visible(len, s_low[rw * 16 * R + r * 16 + col], s_seen[rw * 16 * R + r * 16 + col],
+                                         (int)j0, lost);
 #pragma unroll
                         for (int x = 0; x < 2; ++x)
 #pragma unroll
                             for (int y = 0; y < 4; ++y)
-                                pr = key / 16 == x && (key & 3) == y ? s[r][x][y] : pr;
-                        pr = __shfl(pr, (key >> 2 & 3) * 16 + col);
-                        const bool sees = vis[r] >> key & 1;
-#pragma unroll
-                        for (int x = 0; x < NT; ++x)
-#pragma unroll
-                            for (int y = 0; y < 4; ++y) {
-                                const int d = x * 16 + grp * 4 + y;
-                                const char *at = vals + row * ROW + ((d / 8) ^ value_order<DP>(row)) * 16 + (d & 7) * 2;
-                                const float v = __uint_as_float((uint32_t) * reinterpret_cast<const uint16_t *>(at) << 16);
-                                o[r][x][y] = sees ? o[r][x][y] + pr * v : o[r][x][y];
-                            }
+                                s[r][x][y] = vis[r] >> (grp * 4) & (1u << (x * 16 + y)) ? s[r][x][y] : -INFINITY;
+                    }
+                    // as in k_attend: rows of values with an infinity or a NaN are added one by one
+                    for (int x = 0; x < 32 * PIECES / 64; ++x) {
+                        const int p = x * 64 + lane, row = p / PIECES;
+                        const u32x4 v = *reinterpret_cast<const u32x4 *>(mem + stage_at + HALF + b0 * ROW + p * 16);
+                        const bool mine =
+                            odd_word<1>(v[0]) || odd_word<1>(v[1]) || odd_word<1>(v[2]) || odd_word<1>(v[3]);
+                        for (uint64_t all = __ballot(mine); all != 0; all &= all - 1)
+                            odd |= 1u << uniform(__shfl(row, __builtin_ctzll(all)));
                     }
                 }
-            }
-            bf16x8 p[R];
+                weigh<2, NT, R>(s, o, m, l, a.c1);
+                if (odd != 0) {
+#pragma unroll 1
+                    for (uint32_t left = odd; left != 0; left &= left - 1) {
+                        const int key = __builtin_ctz(left), row = b0 + key;
 #pragma unroll
-            for (int r = 0; r < R; ++r)
+                        for (int r = 0; r < R; ++r) {
+                            float pr = 0.0f;
 #pragma unroll
-                for (int y = 0; y < 8; ++y)
-                    p[r][y] = (__bf16)s[r][y / 4][y & 3];
-            auto add_values = [&](auto some_odd) {
+                            for (int x = 0; x < 2; ++x)
+#pragma unroll
+                                for (int y = 0; y < 4; ++y)
+                                    pr = key / 16 == x && (key & 3) == y ? s[r][x][y] : pr;
+                            pr = __shfl(pr, (key >> 2 & 3) * 16 + col);
+                            const bool sees = visible(len, s_low[rw * 16 * R + r * 16 + col],
+                                                      s_seen[rw * 16 * R + r * 16 + col], (int)j0, lost) >> key & 1;
+#pragma unroll
+                            for (int x = 0; x < NT; ++x)
+#pragma unroll
+                                for (int y = 0; y < 4; ++y) {
+                                    const int d = x * 16 + grp * 4 + y;
+                                    const char *at = mem + stage_at + HALF + row * ROW +
+                                                     ((d / 8) ^ value_order<DP>(row)) * 16 + (d & 7) * 2;
+                                    const float v = __uint_as_float(
+                                        (uint32_t) * reinterpret_cast<const uint16_t *>(at) << 16);
+                                    o[r][x][y] = sees ? o[r][x][y] + pr * v : o[r][x][y];
+                                }
+                        }
+                    }
+#pragma unroll
+                    for (int x = 0; x < EARLY; ++x)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h)
+#pragma unroll
+                            for (int y = 0; y < 4; ++y)
+                                vf[x][h][y] = odd >> (h * 16 + grp * 4 + y) & 1 ? (short)0 : vf[x][h][y];
+                }
+                bf16x8 p[R];
+#pragma unroll
+                for (int r = 0; r < R; ++r)
+#pragma unroll
+                    for (int y = 0; y < 8; ++y)
+                        p[r][y] = (__bf16)s[r][y / 4][y & 3];
 #pragma unroll
                 for (int x = 0; x < NT; ++x) {
                     s16x4 v[2];
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
-                        const char *at = mem + ((value_at + stage_at + b0 * ROW) ^ x * 32) + HALF + h * 16 * ROW;
-                        v[h] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                            (__attribute__((address_space(3))) s16x4 *)at);
-                        if constexpr (decltype(some_odd)::value)
+                        if (x < EARLY) {
+                            v[h] = vf[x < EARLY ? x : 0][h];
+                        } else {
+                            v[h] = read_value(x, h);
+                            if (odd != 0)
 #pragma unroll
-                            for (int y = 0; y < 4; ++y)
-                                v[h][y] = odd >> (h * 16 + grp * 4 + y) & 1 ? (short)0 : v[h][y];
+                                for (int y = 0; y < 4; ++y)
+                                    v[h][y] = odd >> (h * 16 + grp * 4 + y) & 1 ? (short)0 : v[h][y];
+                        }
                     }
                     const bf16x8 vt =
                         __builtin_bit_cast(bf16x8, __builtin_shufflevector(v[0], v[1], 0, 1, 2, 3, 4, 5, 6, 7));
@@ -996,30 +1052,25 @@ __global__ __launch_bounds__(ATTN_WIDE_WG, 1) void k_attend_wide(AttnArgs a)
                     for (int r = 0; r < R; ++r)
                         o[r][x] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vt, p[r], o[r][x], 0, 0, 0);
                 }
-            };
-            if (odd != 0)
-                add_values(std::true_type());
-            else
-                add_values(std::false_type());
+            }
         }
-    }
-    // nothing is under way to LDS, and all have read it
-    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-    float(*s_o)[PITCH] = reinterpret_cast<float(*)[PITCH]>(mem);
+        // nothing is under way to LDS, and all have read it
+        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+        float(*s_o)[PITCH] = reinterpret_cast<float(*)[PITCH]>(mem);
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-        const float sum = row_sum(l[r]);
-        const int at = w * 16 * R + r * 16 + col;
-        if (grp == 0)
-            s_ml[at] = make_float2(m[r] == -INFINITY ? -INFINITY : m[r] * a.c1, sum);
+        for (int r = 0; r < R; ++r) {
+            const float sum = row_sum(l[r]);
+            const int at = w * 16 * R + r * 16 + col;
+            if (grp == 0)
+                s_ml[at] = make_float2(m[r] == -INFINITY ? -INFINITY : m[r] * a.c1, sum);
 #pragma unroll
-        for (int x = 0; x < NT; ++x)
-            *reinterpret_cast<f32x4 *>(&s_o[at][x * 16 + grp * 4]) = o[r][x];
-    }
-    __syncthreads();
-    // waves rw, rw + WR, ... hold the same rows
-    finish<1, ATTN_WIDE_WG, PITCH>(a, job, ROWS, s_o, s_ml, KG, ROWS);
-    __syncthreads();
+            for (int x = 0; x < NT; ++x)
+                *reinterpret_cast<f32x4 *>(&s_o[at][x * 16 + grp * 4]) = o[r][x];
+        }
+        __syncthreads();
+        // waves rw, rw + WR, ... hold the same rows
+        finish<1, ATTN_WIDE_WG, PITCH>(a, job, ROWS, s_o, s_ml, KG, ROWS);
+        __syncthreads();
     }
 }
 
