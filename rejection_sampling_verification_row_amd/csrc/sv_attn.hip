@@ -31,6 +31,9 @@ typedef short s16x4 __attribute__((ext_vector_type(4)));
 
 constexpr float LOG2E = 1.4426950408889634f;
 constexpr float LN2 = 0.6931471805599453f;
+// How far, in powers of 2, scores may exceed the running maximum before it follows: weights up to 2^8
+// lose nothing in fp32 sums or in bfloat16, and most rows' maxima need to follow once.
+constexpr float LAG = 8.0f;
 
 __device__ inline bool in_range(int i, int n) { return (unsigned)i < (unsigned)n; }
 
@@ -39,6 +42,14 @@ __device__ inline int uniform(int v) { return __builtin_amdgcn_readfirstlane(v);
 __device__ inline int64_t uniform(int64_t v)
 {
     return (int64_t)(uint32_t)uniform((int)v) | (int64_t)uniform((int)(v >> 32)) << 32;
+}
+
+// The same value, of which the compiler knows nothing: what is computed from it stays where it is
+// written, and takes no registers elsewhere.
+__device__ inline int afresh(int v)
+{
+    asm volatile("" : "+v"(v));
+    return v;
 }
 
 __device__ inline int64_t quotient(int64_t a, int64_t b)
@@ -421,35 +432,37 @@ __device__ inline uint32_t visible(int len, int low, uint64_t seen, int j0, uint
     return v & ~lost;
 }
 
-// Scores of a tile become weights against the running maximum m (of the raw scores); what was summed
-// before is scaled where a maximum grew.
-template <int SUB, int NT, int R>
-__device__ inline void weigh(f32x4 (&s)[R][SUB], f32x4 (&o)[R][NT], float (&m)[R], float (&l)[R], float c1)
+template <int SUB> __device__ inline float tile_max(const f32x4 (&s)[SUB])
 {
-    float top[R];
-    bool grew = false;
+    float top = s[0][0];
+#pragma unroll
+    for (int x = 0; x < SUB; ++x)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            top = fmaxf(top, s[x][i]);
+    return top;
+}
+
+// The running maxima m (of raw scores) follow a tile's; what was summed before is scaled.
+template <int SUB, int NT, int R>
+__device__ inline void follow(const f32x4 (&s)[R][SUB], f32x4 (&o)[R][NT], float (&m)[R], float (&l)[R], float c1)
+{
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-        top[r] = s[r][0][0];
+        const float was = m[r];
+        m[r] = fmaxf(was, row_max(tile_max<SUB>(s[r])));
+        const float f = m[r] == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f((was - m[r]) * c1);
+        l[r] *= f;
 #pragma unroll
-        for (int x = 0; x < SUB; ++x)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                top[r] = fmaxf(top[r], s[r][x][i]);
-        grew |= top[r] > m[r];
+        for (int i = 0; i < NT; ++i)
+            o[r][i] *= f;
     }
-    if (__ballot(grew) != 0) {
-#pragma unroll
-        for (int r = 0; r < R; ++r) {
-            const float was = m[r];
-            m[r] = fmaxf(was, row_max(top[r]));
-            const float f = m[r] == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f((was - m[r]) * c1);
-            l[r] *= f;
-#pragma unroll
-            for (int i = 0; i < NT; ++i)
-                o[r][i] *= f;
-        }
-    }
+}
+
+// Scores of a tile become weights against the maxima, and are summed.
+template <int SUB, int R>
+__device__ inline void weigh(f32x4 (&s)[R][SUB], const float (&m)[R], float (&l)[R], float c1)
+{
 #pragma unroll
     for (int r = 0; r < R; ++r) {
         const float ref = m[r] == -INFINITY ? 0.0f : m[r] * c1;
@@ -662,7 +675,13 @@ __global__ __launch_bounds__(ATTN_WG, OCC) void k_attend(AttnArgs a)
                         s[r][x][i] = vis[r] >> (grp * 4) & (1u << (x * 16 + i)) ? s[r][x][i] : -INFINITY;
             }
         }
-        weigh<SUB, NT, R>(s, o, m, l, a.c1);
+        bool grew = false;
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+            grew |= tile_max<SUB>(s[r]) > m[r];
+        if (__ballot(grew) != 0)
+            follow<SUB, NT, R>(s, o, m, l, a.c1);
+        weigh<SUB, R>(s, m, l, a.c1);
         if (masked) {
             // What a row does not see may be anything: rows of values with an infinity or a NaN are left
             // out of the product and added to the rows that see them, one by one.
@@ -704,6 +723,8 @@ __global__ __launch_bounds__(ATTN_WG, OCC) void k_attend(AttnArgs a)
                     for (int x = 0; x < NT; ++x)
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
+                            // one after another: all at once would take more registers than there are
+                            __builtin_amdgcn_sched_barrier(0);
                             const int d = (x / VW) * 16 * VW + (grp * 4 + i) * VW + x % VW;
                             const char *at = p + (d < D ? d : 0) * ES;
                             float v;
@@ -870,16 +891,16 @@ __global__ __launch_bounds__(ATTN_WIDE_WG, 1) void k_attend_wide(AttnArgs a)
         };
         // page ids of a stage, one load of every wave (waves past the stage's tokens repeat others')
         auto load_pages = [&](int stage) {
-            const int part = w * 64 % (TK < 64 ? 64 : TK), i = (part + lane) % TK;
+            const int part = w * 64 % (TK < 64 ? 64 : TK), i = (part + afresh(lane)) % TK;
             const int *p = table + divide(token_of(min(stage, stages - 1), i), a.a.by_page);
             load_to_lds4(p, lds_address(&s_page[stage & 3][part]));
         };
         auto load_stage = [&](int stage) {
             const uint32_t to = lds_address(mem) + stage % STAGES * 2 * HALF;
+            const int l16 = afresh(lane) * 16;
 #pragma unroll
             for (int i = 0; i < LOADS; ++i) {
-                const int at = (i * WAVES8 + w) * 1024, row = (at + lane * 16) / ROW;
-                const int slot = (at + lane * 16) % ROW / 16;
+                const int at = (i * WAVES8 + w) * 1024, row = (at + l16) / ROW, slot = (at + l16) % ROW / 16;
                 const int64_t off = s_off[stage & 3][row];
                 const int ck = slot ^ key_order<DP>(row), cv = slot ^ value_order<DP>(row);
                 const char *k = ck * 8 < D ? kp + off + ck * 16 : zeros, *v = cv * 8 < D ? vp + off + cv * 16 : zeros;
@@ -914,8 +935,9 @@ __global__ __launch_bounds__(ATTN_WIDE_WG, 1) void k_attend_wide(AttnArgs a)
         const int value_row = grp * 4 + (col >> 2);
         const int value_at = value_row * ROW + ((col >> 1 & 1) ^ value_order<DP>(value_row)) * 16 + (col & 1) * 8;
 
-        for (int i = 0; i < stages; ++i) {
-            // stage i and the page ids loaded with it are there; what came after may be under way
+        // Stage i and the page ids loaded with it are there (what came after may be under way), and all
+        // waves have read what they need of stage i - 1.
+        auto begin_stage = [&](int i) {
             if (i + DEPTH <= stages)
                 asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"((DEPTH - 1) * (2 * LOADS + 1))
                              : "memory");
@@ -926,132 +948,160 @@ __global__ __launch_bounds__(ATTN_WIDE_WG, 1) void k_attend_wide(AttnArgs a)
                 load_stage(i + DEPTH);
             if (i + DEPTH + 1 < stages && t < TK)
                 put_places(i + DEPTH + 1, s_page[i + DEPTH + 1 & 3][t]);
-            const int stage_at = i % STAGES * 2 * HALF;
-#pragma unroll 1
-            for (int kb = 0; kb < KB; ++kb) {
-                const int b0 = (kg * KB + kb) * 32;
-                const unsigned j0 = (unsigned)(t0 + i) * TK + b0;
-                if (j0 >= (unsigned)total)
-                    break;
-                const int lost_here = (int)s_lost[i & 7][b0 / 32];
-                u32x4 kf[KS][2];
+        };
+        u32x4 kf[KS][2];
+        int lost_here;
+        auto read_keys = [&](int i, int kb) {
+            const int b0 = (kg * KB + kb) * 32, at = key_at + i % STAGES * 2 * HALF + b0 * ROW;
+            lost_here = (int)s_lost[i & 7][b0 / 32];
 #pragma unroll
-                for (int k = 0; k < KS; ++k)
+            for (int k = 0; k < KS; ++k)
 #pragma unroll
-                    for (int x = 0; x < 2; ++x)
-                        kf[k][x] = *reinterpret_cast<const u32x4 *>(
-                            mem + ((key_at + stage_at + b0 * ROW) ^ k * 64) + x * 16 * ROW);
-                auto read_value = [&](int x, int h) {
-                    const char *at = mem + ((value_at + stage_at + b0 * ROW) ^ x * 32) + HALF + h * 16 * ROW;
-                    return __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4 *)at);
-                };
-                s16x4 vf[EARLY][2];
+                for (int x = 0; x < 2; ++x)
+                    kf[k][x] = *reinterpret_cast<const u32x4 *>(mem + (at ^ k * 64) + x * 16 * ROW);
+        };
+        f32x4 sc[R][2];
+        s16x4 vf[EARLY][2];
+        auto read_value = [&](int block_at, int x, int h) {
+            const char *at = mem + ((value_at + block_at) ^ x * 32) + HALF + h * 16 * ROW;
+            return __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4 *)at);
+        };
+        // scores of the block whose keys are in kf, and the first of its values
+        auto score = [&](int block_at) {
 #pragma unroll
-                for (int x = 0; x < EARLY; ++x)
+            for (int x = 0; x < EARLY; ++x)
 #pragma unroll
-                    for (int h = 0; h < 2; ++h)
-                        vf[x][h] = read_value(x, h);
-                f32x4 s[R][2];
+                for (int h = 0; h < 2; ++h)
+                    vf[x][h] = read_value(block_at, x, h);
 #pragma unroll
-                for (int r = 0; r < R; ++r)
-                    s[r][0] = s[r][1] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+            for (int r = 0; r < R; ++r)
+                sc[r][0] = sc[r][1] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-                for (int k = 0; k < KS; ++k)
+            for (int k = 0; k < KS; ++k)
 #pragma unroll
-                    for (int x = 0; x < 2; ++x)
-#pragma unroll
-                        for (int r = 0; r < R; ++r)
-                            s[r][x] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                                __builtin_bit_cast(bf16x8, kf[k][x]), q[r][k], s[r][x], 0, 0, 0);
-                const uint32_t lost = (uint32_t)uniform(lost_here);
-                const bool masked = j0 + 32 > (unsigned)len || lost != 0 || (int)j0 < low_most;
-                uint32_t odd = 0;
-                if (masked) {
-                    uint32_t vis[R];
-#pragma unroll
-                    for (int r = 0; r < R; ++r) {
-                        vis[r] = visible(len, s_low[rw * 16 * R + r * 16 + col], s_seen[rw * 16 * R + r * 16 + col],
-                                         (int)j0, lost);
-#pragma unroll
-                        for (int x = 0; x < 2; ++x)
-#pragma unroll
-                            for (int y = 0; y < 4; ++y)
-                                s[r][x][y] = vis[r] >> (grp * 4) & (1u << (x * 16 + y)) ? s[r][x][y] : -INFINITY;
-                    }
-                    // as in k_attend: rows of values with an infinity or a NaN are added one by one
-                    for (int x = 0; x < 32 * PIECES / 64; ++x) {
-                        const int p = x * 64 + lane, row = p / PIECES;
-                        const u32x4 v = *reinterpret_cast<const u32x4 *>(mem + stage_at + HALF + b0 * ROW + p * 16);
-                        const bool mine =
-                            odd_word<1>(v[0]) || odd_word<1>(v[1]) || odd_word<1>(v[2]) || odd_word<1>(v[3]);
-                        for (uint64_t all = __ballot(mine); all != 0; all &= all - 1)
-                            odd |= 1u << uniform(__shfl(row, __builtin_ctzll(all)));
-                    }
-                }
-                weigh<2, NT, R>(s, o, m, l, a.c1);
-                if (odd != 0) {
-#pragma unroll 1
-                    for (uint32_t left = odd; left != 0; left &= left - 1) {
-                        const int key = __builtin_ctz(left), row = b0 + key;
-#pragma unroll
-                        for (int r = 0; r < R; ++r) {
-                            float pr = 0.0f;
-#pragma unroll
-                            for (int x = 0; x < 2; ++x)
-#pragma unroll
-                                for (int y = 0; y < 4; ++y)
-                                    pr = key / 16 == x && (key & 3) == y ? s[r][x][y] : pr;
-                            pr = __shfl(pr, (key >> 2 & 3) * 16 + col);
-                            const bool sees = visible(len, s_low[rw * 16 * R + r * 16 + col],
-                                                      s_seen[rw * 16 * R + r * 16 + col], (int)j0, lost) >> key & 1;
-#pragma unroll
-                            for (int x = 0; x < NT; ++x)
-#pragma unroll
-                                for (int y = 0; y < 4; ++y) {
-                                    const int d = x * 16 + grp * 4 + y;
-                                    const char *at = mem + stage_at + HALF + row * ROW +
-                                                     ((d / 8) ^ value_order<DP>(row)) * 16 + (d & 7) * 2;
-                                    const float v = __uint_as_float(
-                                        (uint32_t) * reinterpret_cast<const uint16_t *>(at) << 16);
-                                    o[r][x][y] = sees ? o[r][x][y] + pr * v : o[r][x][y];
-                                }
-                        }
-                    }
-#pragma unroll
-                    for (int x = 0; x < EARLY; ++x)
-#pragma unroll
-                        for (int h = 0; h < 2; ++h)
-#pragma unroll
-                            for (int y = 0; y < 4; ++y)
-                                vf[x][h][y] = odd >> (h * 16 + grp * 4 + y) & 1 ? (short)0 : vf[x][h][y];
-                }
-                bf16x8 p[R];
-#pragma unroll
-                for (int r = 0; r < R; ++r)
-#pragma unroll
-                    for (int y = 0; y < 8; ++y)
-                        p[r][y] = (__bf16)s[r][y / 4][y & 3];
-#pragma unroll
-                for (int x = 0; x < NT; ++x) {
-                    s16x4 v[2];
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        if (x < EARLY) {
-                            v[h] = vf[x < EARLY ? x : 0][h];
-                        } else {
-                            v[h] = read_value(x, h);
-                            if (odd != 0)
-#pragma unroll
-                                for (int y = 0; y < 4; ++y)
-                                    v[h][y] = odd >> (h * 16 + grp * 4 + y) & 1 ? (short)0 : v[h][y];
-                        }
-                    }
-                    const bf16x8 vt =
-                        __builtin_bit_cast(bf16x8, __builtin_shufflevector(v[0], v[1], 0, 1, 2, 3, 4, 5, 6, 7));
+                for (int x = 0; x < 2; ++x)
 #pragma unroll
                     for (int r = 0; r < R; ++r)
-                        o[r][x] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vt, p[r], o[r][x], 0, 0, 0);
+                        sc[r][x] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, kf[k][x]), q[r][k],
+                                                                           sc[r][x], 0, 0, 0);
+        };
+        // the weights' product with the values, of which rows that `odd` names count as 0
+        auto add_values = [&](auto some_odd, int block_at, uint32_t odd) {
+            bf16x8 p[R];
+#pragma unroll
+            for (int r = 0; r < R; ++r)
+#pragma unroll
+                for (int y = 0; y < 8; ++y)
+                    p[r][y] = (__bf16)sc[r][y / 4][y & 3];
+#pragma unroll
+            for (int x = 0; x < NT; ++x) {
+                s16x4 v[2];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    v[h] = x < EARLY ? vf[x < EARLY ? x : 0][h] : read_value(block_at, x, h);
+                    if constexpr (decltype(some_odd)::value)
+#pragma unroll
+                        for (int y = 0; y < 4; ++y)
+                            v[h][y] = odd >> (h * 16 + grp * 4 + y) & 1 ? (short)0 : v[h][y];
                 }
+                const bf16x8 vt =
+                    __builtin_bit_cast(bf16x8, __builtin_shufflevector(v[0], v[1], 0, 1, 2, 3, 4, 5, 6, 7));
+#pragma unroll
+                for (int r = 0; r < R; ++r)
+                    o[r][x] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vt, p[r], o[r][x], 0, 0, 0);
+            }
+        };
+        // A block that some row does not see all of, or whose maximum the running one must follow.
+        auto slow_block = [&](int block_at, int j0, uint32_t lost) {
+            score(block_at);
+            uint32_t odd = 0;
+            // as in k_attend: rows of values with an infinity or a NaN are added one by one
+            if (j0 + 32 > len || lost != 0 || j0 < low_most) {
+#pragma unroll 1
+                for (int x = 0; x < 32 * PIECES / 64; ++x) {
+                    const int p = x * 64 + lane, row = p / PIECES;
+                    const u32x4 v = *reinterpret_cast<const u32x4 *>(mem + block_at + HALF + p * 16);
+                    const bool mine = odd_word<1>(v[0]) || odd_word<1>(v[1]) || odd_word<1>(v[2]) || odd_word<1>(v[3]);
+                    for (uint64_t all = __ballot(mine); all != 0; all &= all - 1)
+                        odd |= 1u << uniform(__shfl(row, __builtin_ctzll(all)));
+                }
+            }
+            uint32_t vis[R];
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                const int row = rw * 16 * R + r * 16 + col;
+                vis[r] = visible(len, s_low[row], s_seen[row], j0, lost);
+#pragma unroll
+                for (int x = 0; x < 2; ++x)
+#pragma unroll
+                    for (int y = 0; y < 4; ++y)
+                        sc[r][x][y] = vis[r] >> (grp * 4) & (1u << (x * 16 + y)) ? sc[r][x][y] : -INFINITY;
+            }
+            follow<2, NT, R>(sc, o, m, l, a.c1);
+            weigh<2, R>(sc, m, l, a.c1);
+#pragma unroll 1
+            for (uint32_t left = odd; left != 0; left &= left - 1) {
+                const int key = __builtin_ctz(left);
+#pragma unroll
+                for (int r = 0; r < R; ++r) {
+                    float pr = 0.0f;
+#pragma unroll
+                    for (int x = 0; x < 2; ++x)
+#pragma unroll
+                        for (int y = 0; y < 4; ++y)
+                            pr = key / 16 == x && (key & 3) == y ? sc[r][x][y] : pr;
+                    pr = __shfl(pr, (key >> 2 & 3) * 16 + col);
+                    const bool sees = vis[r] >> key & 1;
+#pragma unroll
+                    for (int x = 0; x < NT; ++x) {
+                        const u32x2 four = *reinterpret_cast<const u32x2 *>(
+                            mem + block_at + HALF + key * ROW + ((x * 2 + grp / 2) ^ value_order<DP>(key)) * 16 +
+                            (grp & 1) * 8);
+#pragma unroll
+                        for (int y = 0; y < 4; ++y) {
+                            const float v = __uint_as_float(y & 1 ? four[y / 2] & 0xffff0000u : four[y / 2] << 16);
+                            o[r][x][y] = sees ? o[r][x][y] + pr * v : o[r][x][y];
+                        }
+                        // one after another: all at once would take more registers than there are
+                        __builtin_amdgcn_sched_barrier(0);
+                    }
+                }
+            }
+            add_values(std::true_type(), block_at, odd);
+        };
+
+        // The loop over blocks leaves those that need more than the plain steps to slow_block, so that
+        // its registers are changed in place.
+        const float slack = LAG / a.c1;
+        const int blocks = stages * KB;
+        int begun = -1;
+        for (int b = 0; b < blocks; ++b) {
+            int block_at = 0, j0 = 0;
+            for (; b < blocks; ++b) {
+                const int i = b / KB, kb = b - i * KB;
+                if (begun != i) {
+                    begun = i;
+                    begin_stage(i);
+                }
+                const int b0 = (kg * KB + kb) * 32;
+                j0 = (t0 + i) * TK + b0;
+                block_at = i % STAGES * 2 * HALF + b0 * ROW;
+                if ((unsigned)j0 + 32 > (unsigned)len || j0 < low_most)
+                    break;
+                read_keys(i, kb);
+                score(block_at);
+                bool grew = uniform(lost_here) != 0;
+#pragma unroll
+                for (int r = 0; r < R; ++r)
+                    grew |= tile_max<2>(sc[r]) > (m[r] == -INFINITY ? m[r] : m[r] + slack);
+                if (__ballot(grew) != 0)
+                    break;
+                weigh<2, R>(sc, m, l, a.c1);
+                add_values(std::false_type(), block_at, 0);
+            }
+            if (b < blocks && (unsigned)j0 < (unsigned)total) {
+                read_keys(b / KB, b % KB);
+                slow_block(block_at, j0, (uint32_t)uniform(lost_here));
             }
         }
         // nothing is under way to LDS, and all have read it
