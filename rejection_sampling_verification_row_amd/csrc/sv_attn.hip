@@ -1077,16 +1077,17 @@ __global__ __launch_bounds__(ATTN_WIDE_WG, 1) void k_attend_wide(AttnArgs a)
         int begun = -1;
         for (int b = 0; b < blocks; ++b) {
             int block_at = 0, j0 = 0;
-            for (; b < blocks; ++b) {
+            // every way out is before the sums change
+            for (;; ++b) {
                 const int i = b / KB, kb = b - i * KB;
-                if (begun != i) {
+                if (b < blocks && begun != i) {
                     begun = i;
                     begin_stage(i);
                 }
                 const int b0 = (kg * KB + kb) * 32;
                 j0 = (t0 + i) * TK + b0;
                 block_at = i % STAGES * 2 * HALF + b0 * ROW;
-                if ((unsigned)j0 + 32 > (unsigned)len || j0 < low_most)
+                if (b >= blocks || (unsigned)j0 + 32 > (unsigned)len || j0 < low_most)
                     break;
                 read_keys(i, kb);
                 score(block_at);
