@@ -601,7 +601,7 @@ __global__ __launch_bounds__(ATTN_WG, OCC) void k_attend(AttnArgs a)
 #pragma unroll
             for (int k = 0; k < KS; ++k) {
                 const int b = k * 64 + grp * 16;
-                kr[s][k] = load_global<u32x4>(b < D * ES ? p + b : zeros);
+                kr[s][k] = load_once<u32x4>(b < D * ES ? p + b : zeros);
             }
         }
     };
@@ -612,7 +612,7 @@ __global__ __launch_bounds__(ATTN_WG, OCC) void k_attend(AttnArgs a)
 #pragma unroll
             for (int b = 0; b < NB; ++b) {
                 const int at = (b * 16 + col) * VW * ES;
-                vr[k][b] = load_global<vchunk>(p + (at < D * ES ? at : 0));
+                vr[k][b] = load_once<vchunk>(p + (at < D * ES ? at : 0));
             }
         }
     };
@@ -814,9 +814,14 @@ __device__ inline uint32_t lds_address(const void *p)
 {
     return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) void *)p;
 }
-__device__ inline void load_to_lds16(const char *from, uint32_t to)
+// ONCE: no other workgroup reads the same (it need not stay in the caches; attend over 250001 tokens
+// 202 -> 184 us).
+template <bool ONCE> __device__ inline void load_to_lds16(const char *from, uint32_t to)
 {
-    asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(from), "{m0}"(to) : "memory");
+    if constexpr (ONCE)
+        asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %0, off nt" ::"v"(from), "{m0}"(to) : "memory");
+    else
+        asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(from), "{m0}"(to) : "memory");
 }
 __device__ inline void load_to_lds4(const void *from, uint32_t to)
 {
@@ -904,8 +909,8 @@ __global__ __launch_bounds__(ATTN_WIDE_WG, 1) void k_attend_wide(AttnArgs a)
                 const int64_t off = s_off[stage & 3][row];
                 const int ck = slot ^ key_order<DP>(row), cv = slot ^ value_order<DP>(row);
                 const char *k = ck * 8 < D ? kp + off + ck * 16 : zeros, *v = cv * 8 < D ? vp + off + cv * 16 : zeros;
-                load_to_lds16(k, to + at);
-                load_to_lds16(v, to + HALF + at);
+                load_to_lds16<(WR < 8)>(k, to + at);
+                load_to_lds16<(WR < 8)>(v, to + HALF + at);
             }
         };
 
@@ -966,13 +971,14 @@ __global__ __launch_bounds__(ATTN_WIDE_WG, 1) void k_attend_wide(AttnArgs a)
             const char *at = mem + ((value_at + block_at) ^ x * 32) + HALF + h * 16 * ROW;
             return __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4 *)at);
         };
-        // scores of the block whose keys are in kf, and the first of its values
-        auto score = [&](int block_at) {
+        // scores of the block whose keys are in kf, and in the plain loop the first of its values
+        auto score = [&](auto plain, int block_at) {
+            if constexpr (decltype(plain)::value)
 #pragma unroll
-            for (int x = 0; x < EARLY; ++x)
+                for (int x = 0; x < EARLY; ++x)
 #pragma unroll
-                for (int h = 0; h < 2; ++h)
-                    vf[x][h] = read_value(block_at, x, h);
+                    for (int h = 0; h < 2; ++h)
+                        vf[x][h] = read_value(block_at, x, h);
 #pragma unroll
             for (int r = 0; r < R; ++r)
                 sc[r][0] = sc[r][1] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
@@ -985,8 +991,9 @@ __global__ __launch_bounds__(ATTN_WIDE_WG, 1) void k_attend_wide(AttnArgs a)
                         sc[r][x] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, kf[k][x]), q[r][k],
                                                                            sc[r][x], 0, 0, 0);
         };
-        // the weights' product with the values, of which rows that `odd` names count as 0
-        auto add_values = [&](auto some_odd, int block_at, uint32_t odd) {
+        // the weights' product with the values; out of the plain loop rows that `odd` names count as 0
+        auto add_values = [&](auto plain, int block_at, uint32_t odd) {
+            constexpr bool PLAIN = decltype(plain)::value;
             bf16x8 p[R];
 #pragma unroll
             for (int r = 0; r < R; ++r)
@@ -998,8 +1005,8 @@ __global__ __launch_bounds__(ATTN_WIDE_WG, 1) void k_attend_wide(AttnArgs a)
                 s16x4 v[2];
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    v[h] = x < EARLY ? vf[x < EARLY ? x : 0][h] : read_value(block_at, x, h);
-                    if constexpr (decltype(some_odd)::value)
+                    v[h] = PLAIN && x < EARLY ? vf[x < EARLY ? x : 0][h] : read_value(block_at, x, h);
+                    if constexpr (!PLAIN)
 #pragma unroll
                         for (int y = 0; y < 4; ++y)
                             v[h][y] = odd >> (h * 16 + grp * 4 + y) & 1 ? (short)0 : v[h][y];
@@ -1009,11 +1016,14 @@ __global__ __launch_bounds__(ATTN_WIDE_WG, 1) void k_attend_wide(AttnArgs a)
 #pragma unroll
                 for (int r = 0; r < R; ++r)
                     o[r][x] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vt, p[r], o[r][x], 0, 0, 0);
+                // one after another: all at once would take more registers than there are
+                if constexpr (!PLAIN)
+                    __builtin_amdgcn_sched_barrier(0);
             }
         };
         // A block that some row does not see all of, or whose maximum the running one must follow.
         auto slow_block = [&](int block_at, int j0, uint32_t lost) {
-            score(block_at);
+            score(std::false_type(), block_at);
             uint32_t odd = 0;
             // as in k_attend: rows of values with an infinity or a NaN are added one by one
             if (j0 + 32 > len || lost != 0 || j0 < low_most) {
@@ -1062,12 +1072,11 @@ __global__ __launch_bounds__(ATTN_WIDE_WG, 1) void k_attend_wide(AttnArgs a)
                             const float v = __uint_as_float(y & 1 ? four[y / 2] & 0xffff0000u : four[y / 2] << 16);
                             o[r][x][y] = sees ? o[r][x][y] + pr * v : o[r][x][y];
                         }
-                        // one after another: all at once would take more registers than there are
                         __builtin_amdgcn_sched_barrier(0);
                     }
                 }
             }
-            add_values(std::true_type(), block_at, odd);
+            add_values(std::false_type(), block_at, odd);
         };
 
         // The loop over blocks leaves those that need more than the plain steps to slow_block, so that
@@ -1090,7 +1099,7 @@ __global__ __launch_bounds__(ATTN_WIDE_WG, 1) void k_attend_wide(AttnArgs a)
                 if (b >= blocks || (unsigned)j0 + 32 > (unsigned)len || j0 < low_most)
                     break;
                 read_keys(i, kb);
-                score(block_at);
+                score(std::true_type(), block_at);
                 bool grew = uniform(lost_here) != 0;
 #pragma unroll
                 for (int r = 0; r < R; ++r)
@@ -1098,7 +1107,7 @@ __global__ __launch_bounds__(ATTN_WIDE_WG, 1) void k_attend_wide(AttnArgs a)
                 if (__ballot(grew) != 0)
                     break;
                 weigh<2, R>(sc, m, l, a.c1);
-                add_values(std::false_type(), block_at, 0);
+                add_values(std::true_type(), block_at, 0);
             }
             if (b < blocks && (unsigned)j0 < (unsigned)total) {
                 read_keys(b / KB, b % KB);

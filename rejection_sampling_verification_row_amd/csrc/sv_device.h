@@ -43,6 +43,10 @@ template <typename T> __device__ inline T load_global(const void *p)
 {
     return *(const SV_GLOBAL T *)p;
 }
+template <typename T> __device__ inline T load_once(const void *p)       // streams past the caches
+{
+    return __builtin_nontemporal_load((const SV_GLOBAL T *)p);
+}
 template <typename T> __device__ inline void store_global(void *p, T v) { *(SV_GLOBAL T *)p = v; }
 
 __device__ inline uint4 load_plain(const char *p) { return *reinterpret_cast<const uint4 *>(p); }
