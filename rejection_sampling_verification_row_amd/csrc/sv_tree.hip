@@ -83,6 +83,127 @@ __global__ __launch_bounds__(64) void k_tree_walk(const int *tokens, const int *
         acc[b] = L;
 }
 
+// 16 bytes of a row from id e on, at any address of the element's alignment.
+typedef u32x4 u32x4_any __attribute__((aligned(2)));
+template <int DT> __device__ inline u32x4 load_group(const char *row, int e)
+{
+    return load_once<u32x4_any>(row + (size_t)e * Elt<DT>::BYTES);
+}
+template <int DT> __device__ inline u32x4 low_group()
+{
+    const uint32_t low = DT == 1 ? 0xff80ff80u : 0xff800000u;
+    return u32x4{low, low, low, low};
+}
+// The group that holds the row's last id.
+template <int DT> __device__ inline u32x4 end_group(const char *row, int e, int V)
+{
+    u32x4 v = low_group<DT>();
+#pragma unroll
+    for (int k = 0; k < Elt<DT>::EPV; ++k)
+        if (e + k < V) {
+            const uint32_t x = __float_as_uint(Elt<DT>::one(row, e + k));
+            if constexpr (DT == 0)
+                v[k] = x;
+            else
+                v[k / 2] = k & 1 ? (v[k / 2] & 0xffffu) | x : (v[k / 2] & 0xffff0000u) | x >> 16;
+        }
+    return v;
+}
+
+// What decides between all rows at once and depth by depth.
+constexpr double TREE_RATE = 6e6;        // bytes a microsecond
+constexpr double TREE_ALL_US = 9.0, TREE_LEVEL_US = 4.5;
+
+// One depth of every walk, `groups` workgroups to a sequence.  Workgroup (b, c): the node that the walk stands on after the `level`
+// tokens before (from the row that the launch before reduced), and chunk c of its row.  The sequence's
+// first workgroup writes what is known.  Partials alternate between two halves, since others of the
+// sequence may still read those before.
+template <int DT>
+__global__ __launch_bounds__(WG) void k_tree_level(const char *__restrict__ tgt, const int *tokens,
+                                                   const int *parents, const int *counts, int T, int V, int depth,
+                                                   int level, int groups, int nch, const float2 *before,
+                                                   float2 *part, int *acc, int *path, int *out)
+{
+    constexpr int E = Elt<DT>::EPV;
+    const int b = blockIdx.x / groups, c = blockIdx.x - b * groups, t = threadIdx.x, lane = t & 63, w = t >> 6;
+    int *p = path + (size_t)b * (depth + 1), *o = out + (size_t)b * (depth + 1);
+    const Nodes n = load_nodes(tokens, parents, counts, b, T, V);
+    const bool first = c == 0 && t == 0;
+    int at = n.sound ? 0 : -1;
+    if (level > 0) {
+        const int prev = p[level - 1];
+        int g = -1;
+        at = -1;
+        if (prev >= 0) {
+            g = merge_partials(before + (size_t)b * nch * WAVES, nch * WAVES);
+            at = level <= depth ? child_of(n, prev, g) : -1;
+        }
+        if (first) {
+            o[level - 1] = g;
+            if (prev >= 0 && at < 0)
+                acc[b] = level - 1;
+        }
+    } else if (first && at < 0) {
+        acc[b] = -1;
+    }
+    if (first && level <= depth)
+        p[level] = at;
+    if (at < 0)
+        return;
+    const char *row = tgt + ((size_t)b * T + at) * (size_t)V * Elt<DT>::BYTES;
+    const int base = c * WG * NV_ARGMAX * E;
+    u32x4 raw[NV_ARGMAX];
+    if (base + WG * NV_ARGMAX * E <= V) {
+#pragma unroll
+        for (int i = 0; i < NV_ARGMAX; ++i)
+            raw[i] = load_group<DT>(row, base + (i * WG + t) * E);
+    } else {
+        // the row's end: what is past it reads as -inf
+#pragma unroll
+        for (int i = 0; i < NV_ARGMAX; ++i) {
+            const int e = base + (i * WG + t) * E;
+            raw[i] = e + E <= V ? load_group<DT>(row, e) : low_group<DT>();
+            if (e < V && e + E > V)
+                raw[i] = end_group<DT>(row, e, V);
+        }
+    }
+    float bv = -INFINITY;
+    int bi = base + t * E < V ? base + t * E : INT_MAX;
+#pragma unroll
+    for (int i = 0; i < NV_ARGMAX; ++i) {
+        float x[E];
+        Elt<DT>::unpack(make_uint4(raw[i][0], raw[i][1], raw[i][2], raw[i][3]), x);
+#pragma unroll
+        for (int k = 0; k < E; ++k)
+            if (x[k] > bv) {
+                bv = x[k];
+                bi = base + (i * WG + t) * E + k;
+            }
+    }
+    wave_argmax(bv, bi);
+    if (lane == 0)
+        part[(size_t)blockIdx.x * WAVES + w] = make_float2(bv, __int_as_float(bi));
+}
+
+template <int DT>
+hipError_t tree_by_levels(const Launch &ln, const Workspace &ws, int B, int T, int V, int depth, const char *tgt,
+                          const int *tokens, const int *parents, const int *counts, int *acc, int *path, int *out)
+{
+    const int nch = num_chunks(NV_ARGMAX, DT, V);
+    float2 *half[2] = {ws.part, ws.part + (size_t)B * nch * WAVES};
+    const Launch plain = {ln.stream, nullptr, 0};
+    for (int level = 0; level <= depth + 1; ++level) {
+        // the last one finishes the walks that went all the way down
+        const bool end = level > depth;
+        const int groups = end ? 1 : nch;
+        const Launch &l = level == 0 || end ? ln : plain;
+        SV_LAUNCH(l, end ? KIND_GREEDY_EMIT : KIND_ARGMAX, k_tree_level<DT>, dim3((unsigned)((size_t)B * groups)),
+                  dim3(WG), 0, tgt, tokens, parents, counts, T, V, depth, level, groups, nch, half[(level + 1) & 1],
+                  half[level & 1], acc, path, out);
+    }
+    return hipGetLastError();
+}
+
 }  // namespace
 
 hipError_t launch_greedy_tree(const Launch &ln, const Workspace &ws, int dtype, int B, int T, int V,
@@ -90,6 +211,12 @@ hipError_t launch_greedy_tree(const Launch &ln, const Workspace &ws, int dtype, 
                               const int32_t *parents, const int32_t *counts, int32_t *acc_len,
                               int32_t *path, int32_t *out_tokens)
 {
+    const double row = (double)V * (dtype == 1 ? 2 : 4), us_all = TREE_ALL_US + B * T * row / TREE_RATE,
+                 us_levels = (depth + 2) * TREE_LEVEL_US + (depth + 1) * B * row / TREE_RATE;
+    if (us_levels < us_all)
+        return (dtype == 1 ? tree_by_levels<1> : tree_by_levels<0>)(ln, ws, B, T, V, depth,
+                                                                  static_cast<const char *>(tgt), tokens, parents,
+                                                                  counts, acc_len, path, out_tokens);
     const int np = num_chunks(NV_ARGMAX, dtype, V) * WAVES;
     const hipError_t e = launch_argmax_rows(ln, ws, dtype, (size_t)B * T, V, tgt);
     if (e != hipSuccess)
@@ -104,11 +231,10 @@ hipError_t launch_greedy_tree(const Launch &ln, const Workspace &ws, int dtype, 
 namespace {
 
 constexpr int KEEP_WG = 256;
-constexpr int KEEP_BATCH = 4;
 
-// A thread has 4 * W bytes of a token in one pool and moves them for every node of the path in
+// A thread has sizeof(V) bytes of a token in one pool and moves them for every node of the path in
 // turn, so that a place is read before the thread writes it: places ascend, and a node moves down
-// or stays.  KEEP_BATCH loads are under way at once: the places that a batch writes are below those
+// or stays.  Four loads are under way at once: the places that they are stored to are below those
 // that later ones read.
 template <typename V> __global__ __launch_bounds__(KEEP_WG) void k_keep_path(CacheView c, int n, int max_count,
                                                                             int groups, const int *seqs,
@@ -165,16 +291,23 @@ template <typename V> __global__ __launch_bounds__(KEEP_WG) void k_keep_path(Cac
     for (int64_t x = (int64_t)group * KEEP_WG + t; x < (int64_t)cols * c.num_pools; x += (int64_t)groups * KEEP_WG) {
         const int pool = (int)(x / cols);
         char *p = c.pools[pool] + (x - (int64_t)pool * cols) * (int64_t)sizeof(V);
-        for (int j = 0; j < most; j += KEEP_BATCH) {
-            V v[KEEP_BATCH];
-#pragma unroll
-            for (int k = 0; k < KEEP_BATCH; ++k)
-                if (j + k < most)
-                    v[k] = *reinterpret_cast<const V *>(p + from[j + k]);
-#pragma unroll
-            for (int k = 0; k < KEEP_BATCH; ++k)
-                if (j + k < most)
-                    *reinterpret_cast<V *>(p + to[j + k]) = v[k];
+        for (int j = 0; j < most; j += 4) {
+            // four variables: an array of them would live in LDS
+            const bool h1 = j + 1 < most, h2 = j + 2 < most, h3 = j + 3 < most;
+            V v0 = load_global<V>(p + from[j]), v1 = v0, v2 = v0, v3 = v0;
+            if (h1)
+                v1 = load_global<V>(p + from[j + 1]);
+            if (h2)
+                v2 = load_global<V>(p + from[j + 2]);
+            if (h3)
+                v3 = load_global<V>(p + from[j + 3]);
+            store_global<V>(p + to[j], v0);
+            if (h1)
+                store_global<V>(p + to[j + 1], v1);
+            if (h2)
+                store_global<V>(p + to[j + 2], v2);
+            if (h3)
+                store_global<V>(p + to[j + 3], v3);
         }
     }
 }
@@ -198,7 +331,7 @@ hipError_t launch_keep_path(hipStream_t st, const CacheView &c, int n, int max_c
 {
     const int64_t token = c.page_bytes / c.page_tokens;
     if (token % 16 == 0)
-        return keep_with<uint4>(st, c, n, max_count, seqs, accepted, path, status);
+        return keep_with<u32x4>(st, c, n, max_count, seqs, accepted, path, status);
     if (token % 4 == 0)
         return keep_with<uint32_t>(st, c, n, max_count, seqs, accepted, path, status);
     return keep_with<uint8_t>(st, c, n, max_count, seqs, accepted, path, status);
