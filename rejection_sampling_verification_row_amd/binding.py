@@ -205,9 +205,23 @@ _ITEMSIZE = {"i32": 4, "f32": 4, "u8": 1}
 def _ptrs(*specs):
     """The pointers of a call's array arguments, each spec (x, count, kind, name): every tensor
     is first checked against the call's shape (_arr), then converted (_ptr)."""
+    kinds, out = _KINDS or _kinds(), []
     for x, count, kind, name in specs:
-        _arr(x, count, kind, name)
-    return tuple(_ptr(x) for x, _, _, _ in specs)
+        if x is None or type(x) is int:
+            out.append(x)
+            continue
+        # what passes needs no second look; anything else is checked in order, for the right error
+        try:
+            fine = (x.is_cuda and x.dtype in kinds[kind][0] and x.numel() >= count
+                    and x.is_contiguous())
+        except (AttributeError, KeyError):
+            fine = False
+        if not fine:
+            for y, n, k, what in specs:
+                _arr(y, n, k, what)
+            return tuple(_ptr(y) for y, _, _, _ in specs)
+        out.append(x.data_ptr())
+    return out
 
 
 _KINDS = {}       # kind -> (accepted element types, their name), filled at the first tensor
@@ -524,7 +538,8 @@ def specverify_attn_workspace_bytes(attn: int) -> int:
 
 
 def specverify_attn_destroy(attn) -> None:
-    _attn_shapes.pop(attn, None)
+    if _attn_shapes is not None:          # the module's names may be gone at the interpreter's end
+        _attn_shapes.pop(attn, None)
     _check(load().specverify_attn_destroy(attn), "specverify_attn_destroy")
 
 
@@ -534,15 +549,18 @@ def _rows(x, dtype, rows, width, stride, name):
     if x is None or isinstance(x, int) or not hasattr(x, "data_ptr"):
         return _ptr(x)
     if x.is_contiguous():
-        _arr(x, (rows - 1) * stride + width if rows > 0 else 0, dtype, name)
-        return _ptr(x)
+        return _ptrs((x, (rows - 1) * stride + width if rows > 0 else 0, dtype, name))[0]
+    shape, steps, beside = x.shape, x.stride(), 1
+    if (len(steps) == 2 and steps[1] == 1 and steps[0] == stride and shape[0] >= rows
+            and shape[1] >= width and x.is_cuda and dtype in (0, 1)
+            and x.dtype in (_KINDS or _kinds())[dtype][0]):
+        return x.data_ptr()
     _arr(x, 0, dtype, name)
-    beside = 1
-    for size, step in zip(x.shape[:0:-1], x.stride()[:0:-1]):
+    for size, step in zip(shape[:0:-1], steps[:0:-1]):
         if size != 1 and step != beside:
             raise ValueError("%s: the elements of a row have to lie side by side" % name)
         beside *= size
-    if x.dim() < 2 or x.shape[0] < rows or beside < width or (rows > 1 and x.stride(0) != stride):
+    if len(shape) < 2 or shape[0] < rows or beside < width or (rows > 1 and steps[0] != stride):
         raise ValueError("%s: expected %d rows of %d elements, %d apart, got %s with strides %s"
                          % (name, rows, width, stride, tuple(x.shape), x.stride()))
     if not x.is_cuda:
@@ -561,14 +579,14 @@ def specverify_attn_append(attn, stream, key_pool, value_pool, n, max_count, row
                            keys, key_stride, values, value_stride, queries=None, query_stride=0,
                            rotated=None, rotated_stride=0, status=None) -> None:
     dtype, q, kv, _ = _attn_shapes.get(attn, (0, 0, 0, 0))
-    _arr(status, n, "i32", "status")
+    status, = _ptrs((status, n, "i32", "status"))
     _check(load().specverify_attn_append(
         attn, _stream(stream), key_pool, value_pool, n, max_count, rows, _nodes(nodes, n, rows),
         None if rotation is None else ctypes.byref(rotation),
         _rows(keys, dtype, rows, kv, key_stride, "keys"), key_stride,
         _rows(values, dtype, rows, kv, value_stride, "values"), value_stride,
         _rows(queries, dtype, rows, q, query_stride, "queries"), query_stride,
-        _rows(rotated, dtype, rows, q, rotated_stride, "rotated"), rotated_stride, _ptr(status)),
+        _rows(rotated, dtype, rows, q, rotated_stride, "rotated"), rotated_stride, status),
         "specverify_attn_append")
 
 

@@ -370,7 +370,6 @@ __device__ inline int load_rows(const AttnArgs &a, const Job &job, uint64_t lane
     const int col = threadIdx.x & 15, grp = threadIdx.x >> 4 & 3, D = a.a.head_dim, G = a.a.group;
     const int start = uniform(job.e.start), len = uniform(job.e.len), rows = uniform(job.e.count) * G;
     const char *base = a.q + (int64_t)start * a.q_stride + (int64_t)uniform(job.head) * G * D * ES;
-    const bool aligned = (reinterpret_cast<uintptr_t>(a.q) | (uintptr_t)a.q_stride) % 16 == 0;
     int most = 0;
     u32x4 v[R][KS];
 #pragma unroll
@@ -389,20 +388,8 @@ __device__ inline int load_rows(const AttnArgs &a, const Job &job, uint64_t lane
         for (int s = 0; s < KS; ++s) {
             const int d = (s * 64 + grp * 16) / ES;
             v[r][s] = u32x4{0, 0, 0, 0};
-            if (row < rows && d < D) {
-                if (aligned) {
-                    v[r][s] = load_global<u32x4>(qp + d * ES);
-                } else if constexpr (DT == 1) {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        v[r][s][i] = load_global<uint16_t>(qp + (d + 2 * i) * ES) |
-                                     (uint32_t)load_global<uint16_t>(qp + (d + 2 * i + 1) * ES) << 16;
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        v[r][s][i] = load_global<uint32_t>(qp + (d + i) * ES);
-                }
-            }
+            if (row < rows && d < D)
+                v[r][s] = load_global<u32x4_any>(qp + d * ES);
         }
     }
     // scale's sign
@@ -1134,7 +1121,7 @@ __global__ __launch_bounds__(ATTN_WIDE_WG, 1) void k_attend_wide(AttnArgs a)
     }
 }
 
-// LG lanes join what the parts of one row left, 4 elements each, weights of LG parts at once.
+// LG lanes join what the parts of one row left, 4 elements each; eight parts' loads under way at once.
 template <int DT, int LG> __global__ __launch_bounds__(ATTN_WG) void k_attend_join(AttnArgs a, int rows_per_tile)
 {
     constexpr int ES = Tile<DT>::ES;
@@ -1145,67 +1132,60 @@ template <int DT, int LG> __global__ __launch_bounds__(ATTN_WG) void k_attend_jo
     if (i >= a.nv.n)
         return;
     const AttnPlan p = a.a.plan[i];
+    const int sound = a.a.sound[i];
+    const int64_t share = *a.a.share;
     const int node = rest / a.a.q_heads, qh = rest - node * a.a.q_heads;
     if (node >= p.count)
         return;
-    const int64_t share = *a.a.share;
     const int D = a.a.head_dim, head = divide(qh, a.a.by_group);
     const int gr = node * a.a.group + qh - head * a.a.group, mt = gr / rows_per_tile, row = gr - mt * rows_per_tile;
     const int64_t base = p.base + ((int64_t)head * p.tiles_of_rows + mt) * p.tiles;
     const int64_t w0 = quotient(base, share);
     const int parts = (int)(quotient(base + p.tiles - 1, share) - w0) + 1;
-    if (parts < 2 || !a.a.sound[i])
+    if (parts < 2 || !sound || lane * 4 >= D)
         return;
-    auto kept = [&](int c) { return (2 * (w0 + c) + (c == 0)) * rows_per_tile + row; };
-    float top = -INFINITY;
-    for (int c = lane; c < parts; c += LG)
-        top = fmaxf(top, a.a.part_ml[kept(c)].x);
+    float top = -INFINITY, z = 0.0f, acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    for (int c0 = 0; c0 < parts; c0 += 8) {
+        float2 ml[8];
+        f32x4 v[8];
 #pragma unroll
-    for (int s = LG / 2; s > 0; s >>= 1)
-        top = fmaxf(top, __shfl_xor(top, s, LG));
-    float z = 0.0f, acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    for (int c0 = 0; c0 < parts; c0 += LG) {
-        float f = 0.0f, part = 0.0f;
-        if (c0 + lane < parts) {
-            const float2 ml = a.a.part_ml[kept(c0 + lane)];
-            f = ml.x == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(ml.x - top);
-            part = f * ml.y;
+        for (int c = 0; c < 8; ++c) {
+            // the last part again where there is none, without weight
+            const int part = min(c0 + c, parts - 1);
+            const int64_t kept = (2 * (w0 + part) + (part == 0)) * rows_per_tile + row;
+            ml[c] = a.a.part_ml[kept];
+            v[c] = load_global<f32x4>(a.a.part_o + kept * D + lane * 4);
         }
+        const float was = top;
 #pragma unroll
-        for (int s = LG / 2; s > 0; s >>= 1)
-            part += __shfl_xor(part, s, LG);
-        z += part;
-        const int most = min(parts - c0, LG);
-        for (int c1 = 0; c1 < most; c1 += 8) {
-            float4 v[8];
+        for (int c = 0; c < 8; ++c)
+            top = fmaxf(top, ml[c].x);
+        const float old = was == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(was - top);
+        z *= old;
 #pragma unroll
-            for (int c = 0; c < 8; ++c)
-                v[c] = c1 + c < most && lane * 4 < D
-                           ? *reinterpret_cast<const float4 *>(a.a.part_o + kept(c0 + c1 + c) * D + lane * 4)
-                           : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        for (int x = 0; x < 4; ++x)
+            acc[x] *= old;
 #pragma unroll
-            for (int c = 0; c < 8; ++c) {
-                const float fc = __shfl(f, min(c1 + c, most - 1), LG);
-                acc[0] += fc * v[c].x;
-                acc[1] += fc * v[c].y;
-                acc[2] += fc * v[c].z;
-                acc[3] += fc * v[c].w;
+        for (int c = 0; c < 8; ++c)
+            if (c0 + c < parts) {
+                const float f = ml[c].x == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(ml[c].x - top);
+                z += f * ml[c].y;
+#pragma unroll
+                for (int x = 0; x < 4; ++x)
+                    acc[x] += f * v[c][x];
             }
-        }
     }
     char *to = a.out + (int64_t)(p.start + node) * a.out_stride + ((int64_t)qh * D + lane * 4) * ES;
-    if (lane * 4 < D)
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
-            const float v = z == 0.0f ? 0.0f : acc[x] / z;
-            if constexpr (DT == 1)
-                reinterpret_cast<__bf16 *>(to)[x] = (__bf16)v;
-            else
-                reinterpret_cast<float *>(to)[x] = v;
-        }
+    for (int x = 0; x < 4; ++x) {
+        const float o = z == 0.0f ? 0.0f : acc[x] / z;
+        if constexpr (DT == 1)
+            reinterpret_cast<__bf16 *>(to)[x] = (__bf16)o;
+        else
+            reinterpret_cast<float *>(to)[x] = o;
+    }
     if (a.lse && lane == 0)
-        a.lse[(int64_t)(p.start + node) * a.a.q_heads + qh] =
-            z == 0.0f ? -INFINITY : (top + log2f(z)) * LN2;
+        a.lse[(int64_t)(p.start + node) * a.a.q_heads + qh] = z == 0.0f ? -INFINITY : (top + log2f(z)) * LN2;
 }
 
 // The launch of a form for tiles of `rows` rows.
@@ -1298,47 +1278,52 @@ struct AppendArgs {
 template <int DT, int N> __device__ inline void load_piece(const char *p, float (&x)[N])
 {
     if constexpr (N == Elt<DT>::EPV) {
-        Elt<DT>::unpack(load_plain(p), x);
+        const u32x4 v = load_global<u32x4_any>(p);
+        Elt<DT>::unpack(make_uint4(v[0], v[1], v[2], v[3]), x);
     } else {
 #pragma unroll
         for (int i = 0; i < N; ++i)
-            x[i] = Elt<DT>::one(p, i);
+            if constexpr (DT == 1)
+                x[i] = __uint_as_float((uint32_t)load_global<uint16_t>(p + 2 * i) << 16);
+            else
+                x[i] = load_global<float>(p + 4 * i);
     }
 }
 
 template <int DT, int N> __device__ inline void store_piece(char *p, const float (&x)[N])
 {
     if constexpr (DT == 0 && N == 4) {
-        *reinterpret_cast<float4 *>(p) = make_float4(x[0], x[1], x[2], x[3]);
+        store_global<u32x4_any>(p, u32x4{__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]),
+                                         __float_as_uint(x[3])});
     } else if constexpr (DT == 1 && N == 8) {
         bf16x8 v;
 #pragma unroll
         for (int i = 0; i < 8; ++i)
             v[i] = (__bf16)x[i];
-        *reinterpret_cast<bf16x8 *>(p) = v;
+        store_global<u32x4_any>(p, __builtin_bit_cast(u32x4, v));
     } else {
 #pragma unroll
         for (int i = 0; i < N; ++i)
             if constexpr (DT == 1)
-                reinterpret_cast<__bf16 *>(p)[i] = (__bf16)x[i];
+                store_global<__bf16>(p + 2 * i, (__bf16)x[i]);
             else
-                reinterpret_cast<float *>(p)[i] = x[i];
+                store_global<float>(p + 4 * i, x[i]);
     }
 }
 
 template <int DT, bool VEC> __device__ inline void copy_piece(char *to, const char *from)
 {
     if constexpr (VEC)
-        *reinterpret_cast<uint4 *>(to) = load_plain(from);
+        store_global<u32x4_any>(to, load_global<u32x4_any>(from));
     else if constexpr (DT == 1)
-        *reinterpret_cast<uint16_t *>(to) = *reinterpret_cast<const uint16_t *>(from);
+        store_global<uint16_t>(to, load_global<uint16_t>(from));
     else
-        *reinterpret_cast<uint32_t *>(to) = *reinterpret_cast<const uint32_t *>(from);
+        store_global<uint32_t>(to, load_global<uint32_t>(from));
 }
 
 // A rotated piece holds 16 bytes of both halves of a head (of neighbouring pairs: 16 bytes), the
-// others 16 bytes; without VEC, where something is not aligned to 16 bytes, one pair and one
-// element.  A token's pieces: its query heads', its key heads', its values'.
+// others 16 bytes, at any address of the element's alignment; without VEC, where the rotated part is
+// no whole number of them, one pair and one element.  A token's pieces: its query heads', its key heads', its values'.
 template <int DT, bool VEC, bool INTER>
 __global__ __launch_bounds__(ATTN_WG) void k_append(AppendArgs a)
 {
@@ -1490,11 +1475,7 @@ hipError_t launch_append(hipStream_t st, const CacheView &c, const AttnShape &s,
                     static_cast<const char *>(v), static_cast<const char *>(q),
                     static_cast<char *>(rotated), k_stride * es, v_stride * es, q_stride * es,
                     rotated_stride * es, status, 0, 0, {}, {}, {}};
-    const uintptr_t bits = reinterpret_cast<uintptr_t>(k) | reinterpret_cast<uintptr_t>(v) |
-                           reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(rotated) |
-                           (uintptr_t)a.k_stride | (uintptr_t)a.v_stride |
-                           (q ? (uintptr_t)a.q_stride | (uintptr_t)a.rotated_stride : 0);
-    const bool vec = bits % 16 == 0 && (rot.interleaved ? rot.dims : rot.dims / 2) % epv == 0;
+    const bool vec = (rot.interleaved ? rot.dims : rot.dims / 2) % epv == 0;
     return s.dtype == 1 ? append_with<1>(st, a, vec) : append_with<0>(st, a, vec);
 }
 

@@ -43,6 +43,7 @@ template <typename T> __device__ inline T load_global(const void *p)
 {
     return *(const SV_GLOBAL T *)p;
 }
+typedef u32x4 u32x4_any __attribute__((aligned(2)));    // 16 bytes at any element's address
 template <typename T> __device__ inline T load_once(const void *p)       // streams past the caches
 {
     return __builtin_nontemporal_load((const SV_GLOBAL T *)p);

@@ -84,7 +84,6 @@ __global__ __launch_bounds__(64) void k_tree_walk(const int *tokens, const int *
 }
 
 // 16 bytes of a row from id e on, at any address of the element's alignment.
-typedef u32x4 u32x4_any __attribute__((aligned(2)));
 template <int DT> __device__ inline u32x4 load_group(const char *row, int e)
 {
     return load_once<u32x4_any>(row + (size_t)e * Elt<DT>::BYTES);
