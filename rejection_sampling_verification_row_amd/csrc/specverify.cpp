@@ -929,7 +929,7 @@ int specverify_attn_create(specverify_attn **out, const specverify_cache *cache,
     const int64_t rows = sv::attend_kept_rows(cache->num_cus);
     const size_t b_plan = align_up((size_t)max_entries * sizeof(sv::AttnPlan));
     const size_t b_sound = align_up((size_t)max_entries * sizeof(int));
-    const size_t b_share = align_up(sizeof(int64_t));
+    const size_t b_share = align_up(sizeof(double));
     const size_t b_ml = align_up((size_t)rows * sizeof(float2));
     const size_t b_o = align_up((size_t)rows * head_dim * sizeof(float));
     specverify_attn *a = new (std::nothrow) specverify_attn();
@@ -953,7 +953,7 @@ int specverify_attn_create(specverify_attn **out, const specverify_cache *cache,
     a->shape = {dtype, q_heads, kv_heads, head_dim, group, sv::fast_div(group),
                 sv::fast_div(v.page_tokens), cache->num_cus,
                 reinterpret_cast<sv::AttnPlan *>(take(b_plan)), reinterpret_cast<int *>(take(b_sound)),
-                reinterpret_cast<int64_t *>(take(b_share)), reinterpret_cast<float2 *>(take(b_ml)),
+                reinterpret_cast<double *>(take(b_share)), reinterpret_cast<float2 *>(take(b_ml)),
                 reinterpret_cast<float *>(take(b_o))};
     *out = a;
     return SPECVERIFY_OK;

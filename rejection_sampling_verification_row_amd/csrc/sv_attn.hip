@@ -39,9 +39,9 @@ __device__ inline bool in_range(int i, int n) { return (unsigned)i < (unsigned)n
 
 // a value that all lanes have
 __device__ inline int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
-__device__ inline int64_t uniform(int64_t v)
+__device__ inline double uniform(double v)
 {
-    return (int64_t)(uint32_t)uniform((int)v) | (int64_t)uniform((int)(v >> 32)) << 32;
+    return __hiloint2double(uniform(__double2hiint(v)), uniform(__double2loint(v)));
 }
 
 // The same value, of which the compiler knows nothing: what is computed from it stays where it is
@@ -50,11 +50,6 @@ __device__ inline int afresh(int v)
 {
     asm volatile("" : "+v"(v));
     return v;
-}
-
-__device__ inline int64_t quotient(int64_t a, int64_t b)
-{
-    return a >> 32 || b >> 32 ? a / b : (int64_t)((uint32_t)a / (uint32_t)b);
 }
 
 __device__ inline int divide(int j, const FastDiv &f)
@@ -141,47 +136,30 @@ struct AttnArgs {
     int units;           // workgroups that fill the chip
 };
 
-template <int WG_SIZE> __device__ inline int64_t block_sum(int64_t v, int64_t *lds)
+// Inclusive sum over the workgroup's threads; *all is the whole.  Counts of tiles are doubles: exact
+// up to 2^53, and sums and quotients of them take few instructions.
+template <int WG_SIZE> __device__ inline double block_scan(double v, double *lds, double *all)
 {
+    const int w = threadIdx.x >> 6;
+    const double inc = wave_incl_scan(v);
+    __syncthreads();
+    if ((threadIdx.x & 63) == 63)
+        lds[w] = inc;
+    __syncthreads();
+    double before = 0.0, sum = 0.0;
 #pragma unroll
-    for (int o = 32; o > 0; o >>= 1)
-        v += __shfl_xor((long long)v, o);
-    __syncthreads();
-    if ((threadIdx.x & 63) == 0)
-        lds[threadIdx.x >> 6] = v;
-    __syncthreads();
-    int64_t all = 0;
-    for (int i = 0; i < WG_SIZE / 64; ++i)
-        all += lds[i];
-    return all;
-}
-
-// Inclusive over the workgroup's threads; *all is the sum.
-template <int WG_SIZE> __device__ inline int64_t block_scan(int64_t v, int64_t *lds, int64_t *all)
-{
-    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-        const int64_t u = __shfl_up((long long)v, o);
-        if (lane >= o)
-            v += u;
-    }
-    __syncthreads();
-    if (lane == 63)
-        lds[w] = v;
-    __syncthreads();
-    int64_t before = 0, sum = 0;
     for (int i = 0; i < WG_SIZE / 64; ++i) {
-        before += i < w ? lds[i] : 0;
+        before += i < w ? lds[i] : 0.0;
         sum += lds[i];
     }
-    *all = sum;
-    return before + v;
+    *all = uniform(sum);
+    return before + inc;
 }
 
 // An entry's work: segments (key heads times tiles of rows) and tiles of KT tokens from `low` on.
 struct Work {
     int tiles_of_rows, segments, low, tiles;
+    __device__ double all() const { return (double)segments * (double)tiles; }
 };
 
 template <int KT> __device__ inline Work entry_work(const AttnArgs &a, const Entry &e, int rows_per_tile)
@@ -201,8 +179,8 @@ template <int KT> __device__ inline Work entry_work(const AttnArgs &a, const Ent
 // takes the same number of them.  What it works on, in LDS, so that it takes no registers while it
 // works: tiles t0 .. t1 of a segment's tokens, then from `at` on.
 struct Job {
-    int64_t at, end;                     // its stretch of all tiles, what is left of it
-    int64_t base;                        // the entry's first tile among all
+    double at, end;                      // its stretch of all tiles, what is left of it
+    double base;                         // the entry's first tile among all
     int mine;                            // the stretch's number; < 0: none, or nothing left
     int entry;
     Entry e;
@@ -217,39 +195,46 @@ struct Job {
 template <int WG_SIZE, int KT>
 __device__ bool find_stretch(const AttnArgs &a, int rows_per_tile, int least, Job &job)
 {
-    __shared__ int64_t lds[WG_SIZE / 64];
+    __shared__ double lds[WG_SIZE / 64];
     const int n = a.nv.n, t = threadIdx.x;
-    Entry e0 = {-1, 0, -1, 0};
+    Entry e = {-1, 0, -1, 0};
     if (t < n)
-        e0 = load_entry(a.c, a.nv, t);
-    int64_t sum = 0;
-    for (int i = t; i < n; i += WG_SIZE) {
-        const Work w = entry_work<KT>(a, i < WG_SIZE ? e0 : load_entry(a.c, a.nv, i), rows_per_tile);
-        sum += (int64_t)w.segments * w.tiles;
+        e = load_entry(a.c, a.nv, t);
+    Work w = entry_work<KT>(a, e, rows_per_tile);
+    double sum, first = block_scan<WG_SIZE>(w.all(), lds, &sum) - w.all();
+    const double part = sum;             // of the first WG_SIZE entries
+    for (int i0 = WG_SIZE; i0 < n; i0 += WG_SIZE) {
+        const int i = i0 + t;
+        double more = 0.0, all;
+        if (i < n)
+            more = entry_work<KT>(a, load_entry(a.c, a.nv, i), rows_per_tile).all();
+        block_scan<WG_SIZE>(more, lds, &all);
+        sum += all;
     }
-    sum = uniform(block_sum<WG_SIZE>(sum, lds));
-    const int64_t share = max(quotient(sum + a.units - 1, a.units), (int64_t)least);
+    const double share = fmax(floor(sum / a.units) + 1.0, (double)least);
     // neighbours, which read the same tokens, on one of the 8 dies, to which workgroups go in turn
-    const int active = (int)quotient(sum + share - 1, share), each = (active + 7) / 8;
+    const int active = (int)ceil(sum / share), each = (active + 7) / 8;
     int mine = (int)(blockIdx.x & 7) * each + (int)(blockIdx.x >> 3);
-    if ((int)(blockIdx.x >> 3) >= each || mine >= active)
+    const double at = mine * share;
+    if ((int)(blockIdx.x >> 3) >= each || at >= sum)
         mine = -1;
-    const int64_t at = mine * share;
     if (mine < 0 && blockIdx.x != 0)
         return false;
-    int64_t base = 0;
+    double base = part;
     for (int i0 = 0; i0 < n; i0 += WG_SIZE) {
         const int i = i0 + t;
-        Entry e = {-1, 0, -1, 0};
-        if (i < n)
-            e = i0 == 0 ? e0 : load_entry(a.c, a.nv, i);
-        const Work w = entry_work<KT>(a, e, rows_per_tile);
-        const int64_t work = (int64_t)w.segments * w.tiles;
-        int64_t all;
-        const int64_t first = base + block_scan<WG_SIZE>(work, lds, &all) - work;
-        if (mine >= 0 && at >= first && at < first + work) {
+        if (i0 > 0) {
+            e = {-1, 0, -1, 0};
+            if (i < n)
+                e = load_entry(a.c, a.nv, i);
+            w = entry_work<KT>(a, e, rows_per_tile);
+            double all;
+            first = base + block_scan<WG_SIZE>(w.all(), lds, &all) - w.all();
+            base += all;
+        }
+        if (mine >= 0 && at >= first && at < first + w.all()) {
             job.at = at;
-            job.end = min(at + share, sum);
+            job.end = fmin(at + share, sum);
             job.base = first;
             job.mine = mine;
             job.entry = i;
@@ -257,10 +242,9 @@ __device__ bool find_stretch(const AttnArgs &a, int rows_per_tile, int least, Jo
         }
         if (blockIdx.x == 0 && i < n) {
             a.a.plan[i] = {first, w.tiles, w.tiles_of_rows, e.start, max(e.count, 0)};
-            if (a.status && work == 0)
+            if (a.status && w.segments == 0)
                 a.status[i] = e.count < 0 ? -1 : 0;
         }
-        base += all;
     }
     if (blockIdx.x == 0 && t == 0)
         *a.a.share = share;
@@ -272,23 +256,23 @@ __device__ bool find_stretch(const AttnArgs &a, int rows_per_tile, int least, Jo
 template <int KT> __device__ inline bool next_job(const AttnArgs &a, int rows_per_tile, Job &job)
 {
     if (threadIdx.x < 64) {
-        const int64_t at = uniform(job.at), end = uniform(job.end);
+        const double at = uniform(job.at), end = uniform(job.end);
         if (at >= end) {
             if (threadIdx.x == 0)
                 job.mine = -1;
         } else {
-            int64_t base = uniform(job.base);
+            double base = uniform(job.base);
             int entry = uniform(job.entry);
             Entry e = {uniform(job.e.seq), uniform(job.e.start), uniform(job.e.count), uniform(job.e.len)};
             Work w = entry_work<KT>(a, e, rows_per_tile);
-            while (at >= base + (int64_t)w.segments * w.tiles) {
-                base += (int64_t)w.segments * w.tiles;
+            while (at >= base + w.all()) {
+                base += w.all();
                 e = load_entry(a.c, a.nv, ++entry);
                 w = entry_work<KT>(a, e, rows_per_tile);
             }
-            const int64_t rel = at - base, segment = quotient(rel, w.tiles);
+            const double rel = at - base, segment = floor(rel / w.tiles);
             const int off = (int)(rel - segment * w.tiles);
-            const int take = (int)min((int64_t)(w.tiles - off), end - at);
+            const int take = (int)fmin((double)(w.tiles - off), end - at);
             if (threadIdx.x == 0) {
                 job.at = at + take;
                 job.base = base;
@@ -298,7 +282,7 @@ template <int KT> __device__ inline bool next_job(const AttnArgs &a, int rows_pe
                 job.mt = (int)segment - job.head * w.tiles_of_rows;
                 job.t0 = w.low + off;
                 job.t1 = w.low + off + take;
-                job.opens = rel == 0;
+                job.opens = rel == 0.0;
                 job.whole = take == w.tiles;
                 job.slot = 2 * job.mine + (off == 0);
             }
@@ -1126,22 +1110,21 @@ template <int DT, int LG> __global__ __launch_bounds__(ATTN_WG) void k_attend_jo
 {
     constexpr int ES = Tile<DT>::ES;
     const int lane = threadIdx.x & (LG - 1);
-    const int per = a.nv.max_count * a.a.q_heads;
-    const int64_t at = (int64_t)blockIdx.x * (ATTN_WG / LG) + threadIdx.x / LG;
-    const int i = (int)quotient(at, per), rest = (int)(at - (int64_t)i * per);
+    const uint32_t per = (uint32_t)a.nv.max_count * a.a.q_heads;       // the launch's work-items fit 32 bits
+    const uint32_t at = blockIdx.x * (ATTN_WG / LG) + threadIdx.x / LG;
+    const int i = (int)(at / per), rest = (int)(at - i * per);
     if (i >= a.nv.n)
         return;
     const AttnPlan p = a.a.plan[i];
     const int sound = a.a.sound[i];
-    const int64_t share = *a.a.share;
+    const double share = *a.a.share;
     const int node = rest / a.a.q_heads, qh = rest - node * a.a.q_heads;
     if (node >= p.count)
         return;
     const int D = a.a.head_dim, head = divide(qh, a.a.by_group);
     const int gr = node * a.a.group + qh - head * a.a.group, mt = gr / rows_per_tile, row = gr - mt * rows_per_tile;
-    const int64_t base = p.base + ((int64_t)head * p.tiles_of_rows + mt) * p.tiles;
-    const int64_t w0 = quotient(base, share);
-    const int parts = (int)(quotient(base + p.tiles - 1, share) - w0) + 1;
+    const double base = p.base + (double)(head * p.tiles_of_rows + mt) * p.tiles;
+    const int w0 = (int)(base / share), parts = (int)((base + (p.tiles - 1)) / share) - w0 + 1;
     if (parts < 2 || !sound || lane * 4 >= D)
         return;
     float top = -INFINITY, z = 0.0f, acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
@@ -1152,7 +1135,7 @@ template <int DT, int LG> __global__ __launch_bounds__(ATTN_WG) void k_attend_jo
         for (int c = 0; c < 8; ++c) {
             // the last part again where there is none, without weight
             const int part = min(c0 + c, parts - 1);
-            const int64_t kept = (2 * (w0 + part) + (part == 0)) * rows_per_tile + row;
+            const int64_t kept = (int64_t)(2 * (w0 + part) + (part == 0)) * rows_per_tile + row;
             ml[c] = a.a.part_ml[kept];
             v[c] = load_global<f32x4>(a.a.part_o + kept * D + lane * 4);
         }

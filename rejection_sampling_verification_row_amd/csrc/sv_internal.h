@@ -323,7 +323,7 @@ struct NodesView {
 // An entry's work, for the joining of its parts: its first tile among all, the tiles of tokens of a
 // segment (a key head and a tile of rows), the tiles of rows, its rows.
 struct AttnPlan {
-    int64_t base;
+    double base;
     int tiles, tiles_of_rows, start, count;
 };
 
@@ -333,7 +333,7 @@ struct AttnShape {
     int num_cus;
     AttnPlan *plan;      // [max_entries]
     int *sound;          // [max_entries] the parents are; written by the entry's first workgroup
-    int64_t *share;      // tiles to a workgroup
+    double *share;       // tiles to a workgroup
     float2 *part_ml;     // [2 workgroups][rows of a tile] maximum (times scale, in powers of 2) and sum
     float *part_o;       // [2 workgroups][rows of a tile][head_dim] sums of weighted values
 };
