@@ -1035,7 +1035,7 @@ int specverify_attn_attend(specverify_attn *attn, void *hip_stream, int key_pool
         return SPECVERIFY_EINVAL;
     if (n > attn->max_entries || max_count > attn->max_nodes)
         return SPECVERIFY_ECAPACITY;
-    // at most a wave for each row and head of the join; tiles are counted in 63 bits
+    // at most a wave for each row and head of the join; tiles are counted exactly in doubles
     if ((int64_t)n * max_count * s.q_heads > (int64_t)(MAX_ITEMS / 64) - 64)
         return SPECVERIFY_ECAPACITY;
     if (n == 0)

@@ -1201,18 +1201,18 @@ hipError_t launch_attend(hipStream_t st, const CacheView &c, const AttnShape &s,
     AttnArgs a = {c, s, nodes, key_pool, value_pool, scale == 0.0f ? 1.0f : fabsf(scale) * LOG2E,
                   scale > 0.0f ? 1.0f : scale < 0.0f ? -1.0f : 0.0f, window, static_cast<const char *>(q),
                   q_stride * es, static_cast<char *>(out), out_stride * es, lse, status, 0};
-#define NARROW(DT, DP, VW, R, OCC) attend_with(st, k_attend<DT, DP, VW, R, OCC>, a, ATTN_WG, 16 * R, 2)
+#define NARROW(DT, DP, VW, R, OCC) attend_with(st, k_attend<DT, DP, VW, R, OCC>, a, ATTN_WG, 16 * R, OCC < 2 ? 2 : OCC)
 #define WIDE(DP, R, WR, KB, STAGES) \
     attend_with(st, k_attend_wide<DP, R, WR, KB, STAGES>, a, ATTN_WIDE_WG, 16 * R * WR, 1)
     if (s.dtype == 0) {
         if (D <= 64)
-            return M <= 16 ? NARROW(0, 64, 4, 1, 2) : NARROW(0, 64, 4, 2, 2);
+            return M <= 16 ? NARROW(0, 64, 4, 1, 3) : NARROW(0, 64, 4, 2, 2);
         if (D <= 128)
             return M <= 16 ? NARROW(0, 128, 4, 1, 2) : NARROW(0, 128, 4, 2, 1);
         return NARROW(0, 256, 4, 1, 1);
     }
     if (M <= 16)
-        return D <= 64 ? NARROW(1, 64, 4, 1, 2) : D <= 128 ? NARROW(1, 128, 8, 1, 2) : NARROW(1, 256, 8, 1, 1);
+        return D <= 64 ? NARROW(1, 64, 4, 1, 3) : D <= 128 ? NARROW(1, 128, 8, 1, 2) : NARROW(1, 256, 8, 1, 1);
     if (D <= 64)
         return M <= 32 ? WIDE(64, 1, 2, 1, 4) : M <= 64 ? WIDE(64, 2, 2, 1, 4)
              : M <= 128 ? WIDE(64, 2, 4, 2, 4) : WIDE(64, 2, 8, 2, 4);
