@@ -811,7 +811,8 @@ __global__ __launch_bounds__(ATTN_WIDE_WG, 1) void k_attend_wide(AttnArgs a)
 {
     constexpr int WAVES8 = ATTN_WIDE_WG / 64, KG = WAVES8 / WR, TK = KG * KB * 32;
     constexpr int KS = DP / 32, NT = DP / 16, PIECES = DP / 8, ROW = DP * 2;
-    constexpr int ROWS = 16 * R * WR, PITCH = DP + 4, DEPTH = STAGES - 1;
+    constexpr bool SHIFT = STAGES == 4;
+    constexpr int ROWS = 16 * R * WR, PITCH = DP + 4, DEPTH = SHIFT ? STAGES - 2 : STAGES - 1;
     constexpr int HALF = TK * ROW, LOADS = HALF / 1024 / WAVES8;      // bytes of keys in a stage; a wave's loads
     constexpr int PAGE_AHEAD = 2 * DEPTH + 1;
     constexpr int EARLY = NT < 8 ? NT : 8;        // pieces of values read before the weights are there
@@ -871,7 +872,7 @@ __global__ __launch_bounds__(ATTN_WIDE_WG, 1) void k_attend_wide(AttnArgs a)
             const int *p = table + divide(token_of(min(stage, stages - 1), i), a.a.by_page);
             load_to_lds4(p, lds_address(&s_page[stage & 3][part]));
         };
-        auto load_stage = [&](int stage) {
+        auto load_rows_of = [&](int stage, auto all) {
             const uint32_t to = lds_address(mem) + stage % STAGES * 2 * HALF;
             const int l16 = afresh(lane) * 16;
 #pragma unroll
@@ -879,10 +880,16 @@ __global__ __launch_bounds__(ATTN_WIDE_WG, 1) void k_attend_wide(AttnArgs a)
                 const int at = (i * WAVES8 + w) * 1024, row = (at + l16) / ROW, slot = (at + l16) % ROW / 16;
                 const int64_t off = s_off[stage & 3][row];
                 const int ck = slot ^ key_order<DP>(row), cv = slot ^ value_order<DP>(row);
-                const char *k = ck * 8 < D ? kp + off + ck * 16 : zeros, *v = cv * 8 < D ? vp + off + cv * 16 : zeros;
-                load_to_lds16<(WR < 8)>(k, to + at);
-                load_to_lds16<(WR < 8)>(v, to + HALF + at);
+                const bool key = decltype(all)::value || ck * 8 < D, value = decltype(all)::value || cv * 8 < D;
+                load_to_lds16<(WR < 8)>(key ? kp + off + ck * 16 : zeros, to + at);
+                load_to_lds16<(WR < 8)>(vp + off + (value ? cv * 16 : 0), to + HALF + at);
             }
+        };
+        auto load_stage = [&](int stage) {
+            if (D == DP)
+                load_rows_of(stage, std::true_type());
+            else
+                load_rows_of(stage, std::false_type());
         };
 
         f32x4 o[R][NT];
@@ -943,13 +950,15 @@ __global__ __launch_bounds__(ATTN_WIDE_WG, 1) void k_attend_wide(AttnArgs a)
             return __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4 *)at);
         };
         // scores of the block whose keys are in kf, and in the plain loop the first of its values
-        auto score = [&](auto plain, int block_at) {
-            if constexpr (decltype(plain)::value)
+        auto read_early = [&](int block_at) {
 #pragma unroll
-                for (int x = 0; x < EARLY; ++x)
+            for (int x = 0; x < EARLY; ++x)
 #pragma unroll
-                    for (int h = 0; h < 2; ++h)
-                        vf[x][h] = read_value(block_at, x, h);
+                for (int h = 0; h < 2; ++h)
+                    vf[x][h] = read_value(block_at, x, h);
+        };
+        auto score = [&] {
+            __builtin_amdgcn_s_setprio(1);
 #pragma unroll
             for (int r = 0; r < R; ++r)
                 sc[r][0] = sc[r][1] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
@@ -961,10 +970,12 @@ __global__ __launch_bounds__(ATTN_WIDE_WG, 1) void k_attend_wide(AttnArgs a)
                     for (int r = 0; r < R; ++r)
                         sc[r][x] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, kf[k][x]), q[r][k],
                                                                            sc[r][x], 0, 0, 0);
+            __builtin_amdgcn_s_setprio(0);
         };
         // the weights' product with the values; out of the plain loop rows that `odd` names count as 0
         auto add_values = [&](auto plain, int block_at, uint32_t odd) {
             constexpr bool PLAIN = decltype(plain)::value;
+            __builtin_amdgcn_s_setprio(1);
             bf16x8 p[R];
 #pragma unroll
             for (int r = 0; r < R; ++r)
@@ -994,7 +1005,7 @@ __global__ __launch_bounds__(ATTN_WIDE_WG, 1) void k_attend_wide(AttnArgs a)
         };
         // A block that some row does not see all of, or whose maximum the running one must follow.
         auto slow_block = [&](int block_at, int j0, uint32_t lost) {
-            score(std::false_type(), block_at);
+            score();
             uint32_t odd = 0;
             // as in k_attend: rows of values with an infinity or a NaN are added one by one
             if (j0 + 32 > len || lost != 0 || j0 < low_most) {
@@ -1054,6 +1065,7 @@ __global__ __launch_bounds__(ATTN_WIDE_WG, 1) void k_attend_wide(AttnArgs a)
         // its registers are changed in place.
         const float slack = LAG / a.c1;
         const int blocks = stages * KB;
+        const bool late = w >= WAVES8 / 2;
         int begun = -1;
         for (int b = 0; b < blocks; ++b) {
             int block_at = 0, j0 = 0;
@@ -1070,13 +1082,21 @@ __global__ __launch_bounds__(ATTN_WIDE_WG, 1) void k_attend_wide(AttnArgs a)
                 if (b >= blocks || (unsigned)j0 + 32 > (unsigned)len || j0 < low_most)
                     break;
                 read_keys(i, kb);
-                score(std::true_type(), block_at);
+                if constexpr (!SHIFT)
+                    read_early(block_at);
+                score();
                 bool grew = uniform(lost_here) != 0;
 #pragma unroll
                 for (int r = 0; r < R; ++r)
                     grew |= tile_max<2>(sc[r]) > (m[r] == -INFINITY ? m[r] : m[r] + slack);
                 if (__ballot(grew) != 0)
                     break;
+                if (SHIFT && late && kb == KB - 1 && i + 1 < stages) {
+                    begun = i + 1;
+                    begin_stage(i + 1);
+                }
+                if constexpr (SHIFT)
+                    read_early(block_at);
                 weigh<2, R>(sc, m, l, a.c1);
                 add_values(std::true_type(), block_at, 0);
             }
