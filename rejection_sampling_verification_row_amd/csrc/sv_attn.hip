@@ -136,6 +136,17 @@ struct AttnArgs {
     int units;           // workgroups that fill the chip
 };
 
+// The arguments read again: what comes from them is not kept in registers, or computed ahead, over a
+// whole kernel.
+__device__ inline AttnArgs args_afresh()
+{
+    auto p = __builtin_amdgcn_kernarg_segment_ptr();
+    asm volatile("" : "+s"(p));
+    AttnArgs a;
+    __builtin_memcpy(&a, p, sizeof a);
+    return a;
+}
+
 // Inclusive sum over the workgroup's threads; *all is the whole.  Counts of tiles are doubles: exact
 // up to 2^53, and sums and quotients of them take few instructions.
 template <int WG_SIZE> __device__ inline double block_scan(double v, double *lds, double *all)
@@ -505,7 +516,7 @@ __device__ inline void finish(const AttnArgs &a, const Job &j, int rows_per_tile
 // of the axis summed over to each of the four groups lane / 16; right ones likewise with columns;
 // results: column lane % 16, rows 4 (lane / 16) + r.
 template <int DT, int DP, int VW, int R, int OCC>
-__global__ __launch_bounds__(ATTN_WG, OCC) void k_attend(AttnArgs a)
+__global__ __launch_bounds__(ATTN_WG, OCC) void k_attend(AttnArgs args)
 {
     typedef Tile<DT> TL;
     constexpr int ES = TL::ES, KT = TL::KT, SUB = KT / 16, KPL = KT / 4;
@@ -522,10 +533,11 @@ __global__ __launch_bounds__(ATTN_WG, OCC) void k_attend(AttnArgs a)
     __shared__ int s_low[ROWS];
     __shared__ Job job;
 
-    const int lane = threadIdx.x & 63, w = uniform((int)(threadIdx.x >> 6)), col = lane & 15, grp = lane >> 4;
-    if (!find_stretch<ATTN_WG, KT>(a, ROWS, 128 / KT, job))
+    if (!find_stretch<ATTN_WG, KT>(args, ROWS, 128 / KT, job))
         return;
-    while (next_job<KT>(a, ROWS, job)) {
+    while (next_job<KT>(args_afresh(), ROWS, job)) {
+    const AttnArgs a = args_afresh();
+    const int t_ = afresh(threadIdx.x), lane = t_ & 63, w = uniform(t_ >> 6), col = lane & 15, grp = lane >> 4;
     uint64_t lane_seen;
     int lane_depth;
     const bool ok = open_job(a, job, lane_seen, lane_depth);
@@ -678,7 +690,7 @@ __global__ __launch_bounds__(ATTN_WG, OCC) void k_attend(AttnArgs a)
             }
 #pragma unroll 1
             for (; odd != 0; odd &= odd - 1) {
-                const int key = __builtin_ctz(odd);
+                const int key = __builtin_ctz(odd), g4 = afresh(grp * 4);
                 const char *p = vp + s_off[w][buf][key];
 #pragma unroll
                 for (int r = 0; r < R; ++r) {
@@ -696,7 +708,7 @@ __global__ __launch_bounds__(ATTN_WG, OCC) void k_attend(AttnArgs a)
                         for (int i = 0; i < 4; ++i) {
                             // one after another: all at once would take more registers than there are
                             __builtin_amdgcn_sched_barrier(0);
-                            const int d = (x / VW) * 16 * VW + (grp * 4 + i) * VW + x % VW;
+                            const int d = (x / VW) * 16 * VW + (g4 + i) * VW + x % VW;
                             const char *at = p + (d < D ? d : 0) * ES;
                             float v;
                             if constexpr (DT == 1)
@@ -827,7 +839,7 @@ __global__ __launch_bounds__(ATTN_WIDE_WG, 1) void k_attend_wide(AttnArgs a)
     __shared__ int s_low[ROWS];
     __shared__ Job job;
 
-    const int t = threadIdx.x, lane = t & 63, w = uniform((int)(t >> 6)), col = lane & 15, grp = lane >> 4;
+    const int t = threadIdx.x, lane = t & 63, w = uniform(t >> 6), col = lane & 15, grp = lane >> 4;
     const int rw = w % WR, kg = w / WR;
     if (!find_stretch<ATTN_WIDE_WG, TK>(a, ROWS, 1, job))
         return;
