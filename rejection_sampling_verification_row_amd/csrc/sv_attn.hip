@@ -1247,11 +1247,11 @@ hipError_t launch_attend(hipStream_t st, const CacheView &c, const AttnShape &s,
         return D <= 64 ? NARROW(1, 64, 4, 1, 3) : D <= 128 ? NARROW(1, 128, 8, 1, 2) : NARROW(1, 256, 8, 1, 1);
     if (D <= 64)
         return M <= 32 ? WIDE(64, 1, 2, 1, 4) : M <= 64 ? WIDE(64, 2, 2, 1, 4)
-             : M <= 128 ? WIDE(64, 2, 4, 2, 4) : WIDE(64, 2, 8, 2, 4);
+             : M <= 128 ? WIDE(64, 2, 4, 2, 4) : WIDE(64, 2, 8, 4, 4);
     if (D <= 128)
-        return M <= 32 ? WIDE(128, 1, 2, 1, 2) : M <= 64 ? WIDE(128, 2, 2, 1, 2)
+        return M <= 32 ? WIDE(128, 1, 2, 1, 2) : M <= 64 ? WIDE(128, 1, 4, 1, 4)
              : M <= 128 ? WIDE(128, 2, 4, 1, 4) : WIDE(128, 2, 8, 2, 4);
-    return M <= 64 ? WIDE(256, 1, 4, 1, 2) : WIDE(256, 1, 8, 2, 2);
+    return M <= 64 ? WIDE(256, 1, 4, 1, 2) : WIDE(256, 1, 8, 1, 4);
 #undef NARROW
 #undef WIDE
 }
