@@ -1,20 +1,31 @@
 // Attention of a verify step's nodes over a paged cache, and the append of their keys and values
 // (gfx950).
 //
-// A node is a row; it sees the cached tokens of its sequence, its ancestors and itself.  A workgroup
-// of k_attend has one key head of one entry, up to 64 rows of it (query heads of the key head times
-// nodes: they read the same keys) and a stretch of the tokens, which its four waves take tile by
-// tile.  Per tile S^T = K Q^T comes first: in the accumulator layout of a 16x16 matrix instruction a
-// lane then holds scores of one row, so that the maximum and the sum of a softmax stay in the lane
-// but for two exchanges, and the weights are, as they lie, the right operand of O^T = V^T P^T: the
-// order in which a product runs over the tokens is free as long as V^T is read in the same.  K is
-// read from memory straight into the left operand's layout; V too, with lanes along the head, and
-// for 16-bit values pairs of tokens are joined by byte permutes.  Nothing passes through LDS but the
-// places of the tokens.
+// A row is a query head of a node.  With x_j = scale q . k_j over the tokens j that the node sees (the
+// sequence's cached tokens, its ancestors and itself, the last `window` of them) and m = max_j x_j,
 //
-// The work is cut into as many parts as fill the chip, from the lengths, which only the device knows:
-// every workgroup adds them up and finds its own part.  Parts of a split segment leave sums that
-// k_attend_join adds in the parts' order.
+//     out = sum_j exp(x_j - m) v_j / sum_j exp(x_j - m),    lse = m + log(sum_j exp(x_j - m)).
+//
+// One pass over the tokens: m is a running maximum, and what was summed under an older one is scaled
+// by exp(old - new).  Scores, maxima and sums are fp32, and so is the product with the values, whose
+// right side, the weights, is rounded to bfloat16 in bfloat16 pools: a weight is off by at most 2^-8 of
+// itself, as the values and the output already are.  exp is computed as a power of 2.
+//
+// All rows of a key head and an entry read the same keys, so that they are the columns of one matrix:
+// S^T = K Q^T, then O^T = V^T P^T.  In the accumulator layout of a 16x16 matrix instruction a lane then
+// holds scores of one row, so that a row's maximum and sum stay in the lane but for two exchanges at
+// the end, and the weights are, as they lie, the right operand of the second product: the order in
+// which a product runs over the tokens is free as long as V^T is read in the same.
+//
+// Up to 16 rows are bound by memory: k_attend reads keys and values into registers, from where
+// they are used once.  More rows in bfloat16 share them: k_attend_wide brings them into LDS.  Which
+// form has how many rows, and why, is said at launch_attend.
+//
+// The lengths are known on the device only.  All tiles of tokens of all entries stand in a row, and
+// every workgroup adds the lengths up and takes an equal stretch of it, whatever segments of tokens
+// (an entry's, for a key head and a tile of rows) begin or end there.  What a stretch has of a split
+// segment is left in the workspace in fp32, and k_attend_join adds the parts in the tokens' order, so
+// that results do not depend on which workgroup is done first.
 #include <algorithm>
 #include <type_traits>
 
@@ -31,8 +42,8 @@ typedef short s16x4 __attribute__((ext_vector_type(4)));
 
 constexpr float LOG2E = 1.4426950408889634f;
 constexpr float LN2 = 0.6931471805599453f;
-// How far, in powers of 2, scores may exceed the running maximum before it follows: weights up to 2^8
-// lose nothing in fp32 sums or in bfloat16, and most rows' maxima need to follow once.
+// How far, in powers of 2, scores may exceed the running maximum before k_attend_wide lets it follow:
+// weights up to 2^8 lose nothing in fp32 sums or in bfloat16, and most rows' maxima need to follow once.
 constexpr float LAG = 8.0f;
 
 __device__ inline bool in_range(int i, int n) { return (unsigned)i < (unsigned)n; }
@@ -509,7 +520,16 @@ __device__ inline void finish(const AttnArgs &a, const Job &j, int rows_per_tile
 }
 
 // Few rows: each of four waves has tiles of tokens of its own, whose keys and values it loads into
-// registers a tile ahead.
+// registers a tile ahead, keys straight in the left operand's layout, values with lanes along the
+// head, of which for 16-bit values pairs of tokens are joined by byte permutes.  Waves meet only at a
+// segment's end.
+//
+// Bound by memory, for one sequence by the way to the first load: 64 sequences of 300 to 8200 tokens,
+// 8 key heads of 128 in bfloat16, 4 rows each: 211 us, 5.3 TB/s (values brought through LDS: 212 us);
+// float32, 4 key heads of 128: 197 us, 5.7 TB/s; one sequence of 1000 tokens: 9 us and 4 us of the join.  Of those
+// 9 us the loop is 2; what comes before it is short because it is not kept in registers from one job
+// to the next (args_afresh: 14.5 -> 12.9 us) and because stretches are counted in doubles (64-bit
+// integer division: 15.4 -> 14.6 us).
 //
 // DP: head_dim or more; VW: elements of a value row that a lane loads at once, 16 lanes side by
 // side; R: tiles of 16 rows.  Left operands of the products: row lane % 16, 16 bytes (4 for float32)
@@ -536,245 +556,246 @@ __global__ __launch_bounds__(ATTN_WG, OCC) void k_attend(AttnArgs args)
     if (!find_stretch<ATTN_WG, KT>(args, ROWS, 128 / KT, job))
         return;
     while (next_job<KT>(args_afresh(), ROWS, job)) {
-    const AttnArgs a = args_afresh();
-    const int t_ = afresh(threadIdx.x), lane = t_ & 63, w = uniform(t_ >> 6), col = lane & 15, grp = lane >> 4;
-    uint64_t lane_seen;
-    int lane_depth;
-    const bool ok = open_job(a, job, lane_seen, lane_depth);
-    const int D = a.a.head_dim, len = uniform(job.e.len), total = len + uniform(job.e.count);
-    const int t0 = uniform(job.t0), t1 = uniform(job.t1), head = uniform(job.head);
-    typename TL::vec q[R][KS];
-    // all waves write the same rows
-    const int low_most =
-        ok ? load_rows<DT, KS, R>(a, job, lane_seen, lane_depth, uniform(job.mt) * ROWS, s_seen, s_low, q) : 0;
-    if (!ok) {
-        __syncthreads();
-        continue;
-    }
-
-    const int *table = a.c.tables + (size_t)uniform(job.e.seq) * a.c.max_blocks;
-    const int64_t row_bytes = (int64_t)a.a.kv_heads * D * ES;
-    const char *kp = a.c.pools[a.key_pool] + (int64_t)head * D * ES;
-    const char *vp = a.c.pools[a.value_pool] + (int64_t)head * D * ES;
-    const char *zeros = reinterpret_cast<const char *>(&past_the_head);
-
-    // a tile's page ids, one token to a lane, then the tokens' places; bits of what has no place
-    auto page_of = [&](int tile) {
-        const int j = (int)min((unsigned)tile * KT + (lane & (KT - 1)), (unsigned)total - 1);
-        return load_global<int>(table + divide(j, a.a.by_page));
-    };
-    auto put_places = [&](int tile, int pg, int buf) {
-        const int j = (int)min((unsigned)tile * KT + (lane & (KT - 1)), (unsigned)total - 1);
-        const int b = divide(j, a.a.by_page);
-        const bool good = in_range(pg, a.c.num_pages);
-        const int64_t at = (int64_t)(good ? pg : 0) * a.c.page_tokens + (j - b * a.c.page_tokens);
-        if (lane < KT)
-            s_off[w][buf][lane] = at * row_bytes;
-        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-        __builtin_amdgcn_wave_barrier();
-        return (uint32_t)(__ballot(!good) & ((1ull << KT) - 1));
-    };
-
-    u32x4 kr[SUB][KS];
-    vchunk vr[KPL][NB];
-    auto load_keys = [&](int buf) {
-#pragma unroll
-        for (int s = 0; s < SUB; ++s) {
-            const char *p = kp + s_off[w][buf][s * 16 + col];
-#pragma unroll
-            for (int k = 0; k < KS; ++k) {
-                const int b = k * 64 + grp * 16;
-                kr[s][k] = load_once<u32x4>(b < D * ES ? p + b : zeros);
-            }
+        const AttnArgs a = args_afresh();
+        const int thread = afresh(threadIdx.x), lane = thread & 63, w = uniform(thread >> 6);
+        const int col = lane & 15, grp = lane >> 4;
+        uint64_t lane_seen;
+        int lane_depth;
+        const bool ok = open_job(a, job, lane_seen, lane_depth);
+        const int D = a.a.head_dim, len = uniform(job.e.len), total = len + uniform(job.e.count);
+        const int t0 = uniform(job.t0), t1 = uniform(job.t1), head = uniform(job.head);
+        typename TL::vec q[R][KS];
+        // all waves write the same rows
+        const int low_most =
+            ok ? load_rows<DT, KS, R>(a, job, lane_seen, lane_depth, uniform(job.mt) * ROWS, s_seen, s_low, q) : 0;
+        if (!ok) {
+            __syncthreads();
+            continue;
         }
-    };
-    auto load_values = [&](int buf) {
-#pragma unroll
-        for (int k = 0; k < KPL; ++k) {
-            const char *p = vp + s_off[w][buf][(k / 4) * 16 + grp * 4 + (k & 3)];
-#pragma unroll
-            for (int b = 0; b < NB; ++b) {
-                const int at = (b * 16 + col) * VW * ES;
-                vr[k][b] = load_once<vchunk>(p + (at < D * ES ? at : 0));
-            }
-        }
-    };
 
-    f32x4 o[R][NT];
-    float m[R], l[R];                    // maximum of the raw scores, this lane's part of the sum
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-        m[r] = -INFINITY;
-        l[r] = 0.0f;
-#pragma unroll
-        for (int i = 0; i < NT; ++i)
-            o[r][i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    }
+        const int *table = a.c.tables + (size_t)uniform(job.e.seq) * a.c.max_blocks;
+        const int64_t row_bytes = (int64_t)a.a.kv_heads * D * ES;
+        const char *kp = a.c.pools[a.key_pool] + (int64_t)head * D * ES;
+        const char *vp = a.c.pools[a.value_pool] + (int64_t)head * D * ES;
+        const char *zeros = reinterpret_cast<const char *>(&past_the_head);
 
-    int t = t0 + w, buf = 0, next_page = 0;
-    const int last = t1 - 1 - (t1 - 1 - t & 3);          // this wave's last tile
-    uint32_t lost = 0;
-    if (t < t1) {
-        lost = put_places(t, page_of(t), 0);
-        load_keys(0);
-        load_values(0);
-        next_page = page_of(min(t + 4, last));
-    }
-    for (; t < t1; t += 4, buf ^= 1) {
-        f32x4 s[R][SUB];
+        // a tile's page ids, one token to a lane, then the tokens' places; bits of what has no place
+        auto page_of = [&](int tile) {
+            const int j = (int)min((unsigned)tile * KT + (lane & (KT - 1)), (unsigned)total - 1);
+            return load_global<int>(table + divide(j, a.a.by_page));
+        };
+        auto put_places = [&](int tile, int pg, int buf) {
+            const int j = (int)min((unsigned)tile * KT + (lane & (KT - 1)), (unsigned)total - 1);
+            const int b = divide(j, a.a.by_page);
+            const bool good = in_range(pg, a.c.num_pages);
+            const int64_t at = (int64_t)(good ? pg : 0) * a.c.page_tokens + (j - b * a.c.page_tokens);
+            if (lane < KT)
+                s_off[w][buf][lane] = at * row_bytes;
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+            __builtin_amdgcn_wave_barrier();
+            return (uint32_t)(__ballot(!good) & ((1ull << KT) - 1));
+        };
+
+        u32x4 kr[SUB][KS];
+        vchunk vr[KPL][NB];
+        auto load_keys = [&](int buf) {
 #pragma unroll
-        for (int r = 0; r < R; ++r)
-#pragma unroll
-            for (int x = 0; x < SUB; ++x) {
-                s[r][x] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+            for (int s = 0; s < SUB; ++s) {
+                const char *p = kp + s_off[w][buf][s * 16 + col];
 #pragma unroll
                 for (int k = 0; k < KS; ++k) {
-                    const typename TL::vec kv = __builtin_bit_cast(typename TL::vec, kr[x][k]);
-                    if constexpr (DT == 1) {
-                        s[r][x] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kv, q[r][k], s[r][x], 0, 0, 0);
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            s[r][x] = __builtin_amdgcn_mfma_f32_16x16x4f32(kv[i], q[r][k][i], s[r][x], 0, 0, 0);
-                    }
+                    const int b = k * 64 + grp * 16;
+                    kr[s][k] = load_once<u32x4>(b < D * ES ? p + b : zeros);
                 }
             }
-        // the next tile's loads are made in any case (the last tile's again): a branch around them
-        // would let every wait for older ones wait for all
-        const uint32_t next_lost = put_places(min(t + 4, last), next_page, buf ^ 1);
-        next_page = page_of(min(t + 8, last));
-        load_keys(buf ^ 1);
-        const unsigned j0 = (unsigned)t * KT;
-        const bool masked = j0 + KT > (unsigned)len || lost != 0 || (int)j0 < low_most;
-        uint32_t vis[R];                 // the tile's tokens that a row sees
-        if (masked) {
-#pragma unroll
-            for (int r = 0; r < R; ++r) {
-                vis[r] = visible(len, s_low[r * 16 + col], s_seen[r * 16 + col], (int)j0, lost);
-#pragma unroll
-                for (int x = 0; x < SUB; ++x)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        s[r][x][i] = vis[r] >> (grp * 4) & (1u << (x * 16 + i)) ? s[r][x][i] : -INFINITY;
-            }
-        }
-        bool grew = false;
-#pragma unroll
-        for (int r = 0; r < R; ++r)
-            grew |= tile_max<SUB>(s[r]) > m[r];
-        if (__ballot(grew) != 0)
-            follow<SUB, NT, R>(s, o, m, l, a.c1);
-        weigh<SUB, R>(s, m, l, a.c1);
-        if (masked) {
-            // What a row does not see may be anything: rows of values with an infinity or a NaN are left
-            // out of the product and added to the rows that see them, one by one.
-            uint32_t odd = 0;
+        };
+        auto load_values = [&](int buf) {
 #pragma unroll
             for (int k = 0; k < KPL; ++k) {
-                bool mine = false;
+                const char *p = vp + s_off[w][buf][(k / 4) * 16 + grp * 4 + (k & 3)];
 #pragma unroll
-                for (int x = 0; x < NB; ++x)
-#pragma unroll
-                    for (int i = 0; i < VW * ES / 4; ++i)
-                        mine |= odd_word<DT>(vr[k][x][i]);
-                const uint64_t all = __ballot(mine);
-                if (all == 0)
-                    continue;
-#pragma unroll
-                for (int g = 0; g < 4; ++g)
-                    odd |= all >> (g * 16) & 0xffff ? 1u << ((k / 4) * 16 + g * 4 + (k & 3)) : 0;
-                if (all >> (grp * 16) & 0xffff)
-#pragma unroll
-                    for (int x = 0; x < NB; ++x)
-                        vr[k][x] = vchunk{};
+                for (int b = 0; b < NB; ++b) {
+                    const int at = (b * 16 + col) * VW * ES;
+                    vr[k][b] = load_once<vchunk>(p + (at < D * ES ? at : 0));
+                }
             }
-#pragma unroll 1
-            for (; odd != 0; odd &= odd - 1) {
-                const int key = __builtin_ctz(odd), g4 = afresh(grp * 4);
-                const char *p = vp + s_off[w][buf][key];
+        };
+
+        f32x4 o[R][NT];
+        float m[R], l[R];                    // maximum of the raw scores, this lane's part of the sum
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            m[r] = -INFINITY;
+            l[r] = 0.0f;
+#pragma unroll
+            for (int i = 0; i < NT; ++i)
+                o[r][i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        }
+
+        int t = t0 + w, buf = 0, next_page = 0;
+        const int last = t1 - 1 - (t1 - 1 - t & 3);          // this wave's last tile
+        uint32_t lost = 0;
+        if (t < t1) {
+            lost = put_places(t, page_of(t), 0);
+            load_keys(0);
+            load_values(0);
+            next_page = page_of(min(t + 4, last));
+        }
+        for (; t < t1; t += 4, buf ^= 1) {
+            f32x4 s[R][SUB];
+#pragma unroll
+            for (int r = 0; r < R; ++r)
+#pragma unroll
+                for (int x = 0; x < SUB; ++x) {
+                    s[r][x] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                    for (int k = 0; k < KS; ++k) {
+                        const typename TL::vec kv = __builtin_bit_cast(typename TL::vec, kr[x][k]);
+                        if constexpr (DT == 1) {
+                            s[r][x] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kv, q[r][k], s[r][x], 0, 0, 0);
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                s[r][x] = __builtin_amdgcn_mfma_f32_16x16x4f32(kv[i], q[r][k][i], s[r][x], 0, 0, 0);
+                        }
+                    }
+                }
+            // the next tile's loads are made in any case (the last tile's again): a branch around them
+            // would let every wait for older ones wait for all
+            const uint32_t next_lost = put_places(min(t + 4, last), next_page, buf ^ 1);
+            next_page = page_of(min(t + 8, last));
+            load_keys(buf ^ 1);
+            const unsigned j0 = (unsigned)t * KT;
+            const bool masked = j0 + KT > (unsigned)len || lost != 0 || (int)j0 < low_most;
+            uint32_t vis[R];                 // the tile's tokens that a row sees
+            if (masked) {
 #pragma unroll
                 for (int r = 0; r < R; ++r) {
-                    float pr = 0.0f;
+                    vis[r] = visible(len, s_low[r * 16 + col], s_seen[r * 16 + col], (int)j0, lost);
 #pragma unroll
                     for (int x = 0; x < SUB; ++x)
 #pragma unroll
                         for (int i = 0; i < 4; ++i)
-                            pr = key / 16 == x && (key & 3) == i ? s[r][x][i] : pr;
-                    pr = __shfl(pr, (key >> 2 & 3) * 16 + col);
-                    const bool sees = vis[r] >> key & 1;
-#pragma unroll
-                    for (int x = 0; x < NT; ++x)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            // one after another: all at once would take more registers than there are
-                            __builtin_amdgcn_sched_barrier(0);
-                            const int d = (x / VW) * 16 * VW + (g4 + i) * VW + x % VW;
-                            const char *at = p + (d < D ? d : 0) * ES;
-                            float v;
-                            if constexpr (DT == 1)
-                                v = __uint_as_float((uint32_t)load_global<uint16_t>(at) << 16);
-                            else
-                                v = load_global<float>(at);
-                            o[r][x][i] = sees ? o[r][x][i] + pr * v : o[r][x][i];
-                        }
+                            s[r][x][i] = vis[r] >> (grp * 4) & (1u << (x * 16 + i)) ? s[r][x][i] : -INFINITY;
                 }
             }
-        }
-        if constexpr (DT == 1) {
-            bf16x8 p[R];
+            bool grew = false;
 #pragma unroll
             for (int r = 0; r < R; ++r)
+                grew |= tile_max<SUB>(s[r]) > m[r];
+            if (__ballot(grew) != 0)
+                follow<SUB, NT, R>(s, o, m, l, a.c1);
+            weigh<SUB, R>(s, m, l, a.c1);
+            if (masked) {
+                // What a row does not see may be anything: rows of values with an infinity or a NaN are left
+                // out of the product and added to the rows that see them, one by one.
+                uint32_t odd = 0;
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    p[r][i] = (__bf16)s[r][i / 4][i & 3];
+                for (int k = 0; k < KPL; ++k) {
+                    bool mine = false;
 #pragma unroll
-            for (int b = 0; b < NB; ++b)
+                    for (int x = 0; x < NB; ++x)
 #pragma unroll
-                for (int x = 0; x < VW; ++x) {
-                    uint32_t u[4];
+                        for (int i = 0; i < VW * ES / 4; ++i)
+                            mine |= odd_word<DT>(vr[k][x][i]);
+                    const uint64_t all = __ballot(mine);
+                    if (all == 0)
+                        continue;
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        u[i] = __builtin_amdgcn_perm(vr[2 * i + 1][b][x / 2], vr[2 * i][b][x / 2],
-                                                     x & 1 ? 0x07060302u : 0x05040100u);
-                    const bf16x8 vt = __builtin_bit_cast(bf16x8, make_uint4(u[0], u[1], u[2], u[3]));
+                    for (int g = 0; g < 4; ++g)
+                        odd |= all >> (g * 16) & 0xffff ? 1u << ((k / 4) * 16 + g * 4 + (k & 3)) : 0;
+                    if (all >> (grp * 16) & 0xffff)
 #pragma unroll
-                    for (int r = 0; r < R; ++r)
-                        o[r][b * VW + x] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vt, p[r], o[r][b * VW + x],
-                                                                                   0, 0, 0);
+                        for (int x = 0; x < NB; ++x)
+                            vr[k][x] = vchunk{};
                 }
-        } else {
+#pragma unroll 1
+                for (; odd != 0; odd &= odd - 1) {
+                    const int key = __builtin_ctz(odd), g4 = afresh(grp * 4);
+                    const char *p = vp + s_off[w][buf][key];
 #pragma unroll
-            for (int k = 0; k < KPL; ++k)
+                    for (int r = 0; r < R; ++r) {
+                        float pr = 0.0f;
+#pragma unroll
+                        for (int x = 0; x < SUB; ++x)
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                pr = key / 16 == x && (key & 3) == i ? s[r][x][i] : pr;
+                        pr = __shfl(pr, (key >> 2 & 3) * 16 + col);
+                        const bool sees = vis[r] >> key & 1;
+#pragma unroll
+                        for (int x = 0; x < NT; ++x)
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                // one after another: all at once would take more registers than there are
+                                __builtin_amdgcn_sched_barrier(0);
+                                const int d = (x / VW) * 16 * VW + (g4 + i) * VW + x % VW;
+                                const char *at = p + (d < D ? d : 0) * ES;
+                                float v;
+                                if constexpr (DT == 1)
+                                    v = __uint_as_float((uint32_t)load_global<uint16_t>(at) << 16);
+                                else
+                                    v = load_global<float>(at);
+                                o[r][x][i] = sees ? o[r][x][i] + pr * v : o[r][x][i];
+                            }
+                    }
+                }
+            }
+            if constexpr (DT == 1) {
+                bf16x8 p[R];
+#pragma unroll
+                for (int r = 0; r < R; ++r)
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        p[r][i] = (__bf16)s[r][i / 4][i & 3];
 #pragma unroll
                 for (int b = 0; b < NB; ++b)
 #pragma unroll
-                    for (int x = 0; x < VW; ++x)
+                    for (int x = 0; x < VW; ++x) {
+                        uint32_t u[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            u[i] = __builtin_amdgcn_perm(vr[2 * i + 1][b][x / 2], vr[2 * i][b][x / 2],
+                                                         x & 1 ? 0x07060302u : 0x05040100u);
+                        const bf16x8 vt = __builtin_bit_cast(bf16x8, make_uint4(u[0], u[1], u[2], u[3]));
 #pragma unroll
                         for (int r = 0; r < R; ++r)
-                            o[r][b * VW + x] = __builtin_amdgcn_mfma_f32_16x16x4f32(
-                                __uint_as_float(vr[k][b][x]), s[r][0][k], o[r][b * VW + x], 0, 0, 0);
+                            o[r][b * VW + x] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vt, p[r], o[r][b * VW + x],
+                                                                                       0, 0, 0);
+                    }
+            } else {
+#pragma unroll
+                for (int k = 0; k < KPL; ++k)
+#pragma unroll
+                    for (int b = 0; b < NB; ++b)
+#pragma unroll
+                        for (int x = 0; x < VW; ++x)
+#pragma unroll
+                            for (int r = 0; r < R; ++r)
+                                o[r][b * VW + x] = __builtin_amdgcn_mfma_f32_16x16x4f32(
+                                    __uint_as_float(vr[k][b][x]), s[r][0][k], o[r][b * VW + x], 0, 0, 0);
+            }
+            load_values(buf ^ 1);
+            lost = next_lost;
         }
-        load_values(buf ^ 1);
-        lost = next_lost;
-    }
 
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-        const float sum = row_sum(l[r]);
-        const int at = w * ROWS + r * 16 + col;
-        if (grp == 0)
-            s_ml[at] = make_float2(m[r] == -INFINITY ? -INFINITY : m[r] * a.c1, sum);
+        for (int r = 0; r < R; ++r) {
+            const float sum = row_sum(l[r]);
+            const int at = w * ROWS + r * 16 + col;
+            if (grp == 0)
+                s_ml[at] = make_float2(m[r] == -INFINITY ? -INFINITY : m[r] * a.c1, sum);
 #pragma unroll
-        for (int b = 0; b < NB; ++b)
+            for (int b = 0; b < NB; ++b)
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+                for (int i = 0; i < 4; ++i)
 #pragma unroll
-                for (int x = 0; x < VW; ++x)
-                    s_o[at][b * 16 * VW + (grp * 4 + i) * VW + x] = o[r][b * VW + x][i];
-    }
-    __syncthreads();
-    finish<DT, ATTN_WG, PITCH>(a, job, ROWS, s_o, s_ml, 4, ROWS);
-    __syncthreads();
+                    for (int x = 0; x < VW; ++x)
+                        s_o[at][b * 16 * VW + (grp * 4 + i) * VW + x] = o[r][b * VW + x][i];
+        }
+        __syncthreads();
+        finish<DT, ATTN_WG, PITCH>(a, job, ROWS, s_o, s_ml, 4, ROWS);
+        __syncthreads();
     }
 }
 
@@ -817,7 +838,19 @@ __device__ inline void load_to_lds4(const void *from, uint32_t to)
 //
 // LDS holds a token's row of a stage in 16-byte pieces in an order of the row's own, so that 16
 // lanes that read the same piece of 16 rows (keys), or 32 bytes of 4 rows (values, which the LDS
-// transposes on the way), touch all banks alike.
+// transposes on the way), touch all banks alike: 0.07% of the LDS's active cycles are conflicts.
+//
+// A block of 32 rows and 32 tokens of heads of 128 is 32 matrix instructions (512 cycles) and some
+// 120 others with 16 exponentials (about 630 cycles), which overlap only if the two waves of a SIMD do
+// different things.  So with four stages the upper half of the waves meets the stage's barrier between
+// its scores and its weights, when the lower half begins with scores, and matrix instructions have
+// priority: 16 sequences of 64 nodes, 64 query and 8 key heads, 8000 to 16000 tokens: 531 -> 520 us,
+// 711 TFLOP/s, where a large library product reaches 1352 TFLOP/s.  The matrix units are busy 36% of the time;
+// waves wait for barriers and LDS 29% of theirs and for their turn to issue 27%.  Not kept: the next block's
+// keys read, or its scores computed, before the weights of this one (no registers are left, 2 times slower).
+//
+// Fewer rows are bound by memory: 64 sequences of 300 to 8200 tokens with 8 key heads of 128: 32 rows
+// 236 us (4.75 TB/s), 64 rows 270 us, 128 rows 375 us.
 template <int DP, int R, int WR, int KB, int STAGES>
 __global__ __launch_bounds__(ATTN_WIDE_WG, 1) void k_attend_wide(AttnArgs a)
 {
@@ -1138,6 +1171,8 @@ __global__ __launch_bounds__(ATTN_WIDE_WG, 1) void k_attend_wide(AttnArgs a)
 }
 
 // LG lanes join what the parts of one row left, 4 elements each; eight parts' loads under way at once.
+// Rows of one part are done.  Bound by memory where many rows are split (65536 rows of 128 in two
+// parts: 28 us for 84 MB), by the launch else (4 us).
 template <int DT, int LG> __global__ __launch_bounds__(ATTN_WG) void k_attend_join(AttnArgs a, int rows_per_tile)
 {
     constexpr int ES = Tile<DT>::ES;
@@ -1214,16 +1249,24 @@ template <typename K> hipError_t attend_with(hipStream_t st, K kernel, AttnArgs 
     const int lanes = a.a.head_dim <= 64 ? 16 : a.a.head_dim <= 128 ? 32 : 64;
     const int64_t joined = (int64_t)a.nv.n * a.nv.max_count * a.a.q_heads, each = ATTN_WG / lanes;
     const unsigned groups = (unsigned)((joined + each - 1) / each);
-    auto join = a.a.dtype == 1 ? (lanes == 16 ? k_attend_join<1, 16> : lanes == 32 ? k_attend_join<1, 32> : k_attend_join<1, 64>)
-                               : (lanes == 16 ? k_attend_join<0, 16> : lanes == 32 ? k_attend_join<0, 32> : k_attend_join<0, 64>);
-    if (groups > 0)
+    if (groups > 0) {
+        auto join = a.a.dtype == 1 ? k_attend_join<1, 64> : k_attend_join<0, 64>;
+        if (lanes == 16)
+            join = a.a.dtype == 1 ? k_attend_join<1, 16> : k_attend_join<0, 16>;
+        else if (lanes == 32)
+            join = a.a.dtype == 1 ? k_attend_join<1, 32> : k_attend_join<0, 32>;
         join<<<groups, ATTN_WG, 0, st>>>(a, rows);
+    }
     return hipGetLastError();
 }
 
 }  // namespace
 
-int64_t attend_kept_rows(int num_cus) { return 2 * std::max<int64_t>(ATTN_MAX_UNITS * 32, (num_cus + 7) / 8 * 8 * 256); }
+// Two tiles of rows to each workgroup of a launch: 32 rows of k_attend, 256 of k_attend_wide.
+int64_t attend_kept_rows(int num_cus)
+{
+    return 2 * std::max<int64_t>(ATTN_MAX_UNITS * 32, (num_cus + 7) / 8 * 8 * 256);
+}
 
 hipError_t launch_attend(hipStream_t st, const CacheView &c, const AttnShape &s, const NodesView &nodes,
                          int key_pool, int value_pool, float scale, int window, const void *q,
@@ -1233,6 +1276,21 @@ hipError_t launch_attend(hipStream_t st, const CacheView &c, const AttnShape &s,
     AttnArgs a = {c, s, nodes, key_pool, value_pool, scale == 0.0f ? 1.0f : fabsf(scale) * LOG2E,
                   scale > 0.0f ? 1.0f : scale < 0.0f ? -1.0f : 0.0f, window, static_cast<const char *>(q),
                   q_stride * es, static_cast<char *>(out), out_stride * es, lse, status, 0};
+    // Forms with tiles of as many rows as there are, or the largest.  Up to 16 rows k_attend is as fast
+    // as k_attend_wide or faster (heads of 128: one sequence 12.9 against 15.3 us, 64 of them 211 and 212 us;
+    // of 64: 227 and 252; of 256: 215 and 234).  It has as many workgroups on a compute unit as its
+    // registers allow (float32 heads of 64: 3, 70 us; 2, 79 us; 4, 100 us for spills); float32 has no other
+    // form, since its matrix instructions are 8 times slower than the bfloat16 ones and decide.
+    // k_attend_wide has what its registers and 160 KB of LDS allow, and of that the fastest, in us for 64 sequences
+    // of 300 to 8200 tokens (waves over the rows, rows of a wave, tokens and number of stages):
+    //   heads of 64:  32 rows  2 x 16, 128 x 4: 272;  x 2: 290
+    //                 64 rows  2 x 32, 128 x 4: 338;  4 x 16, 64 x 4: 348
+    //                128 rows  4 x 32, 128 x 4: 450;  64 x 4: 485;  8 x 16, 64 x 4: 534
+    //                256 rows  8 x 32, 128 x 4: 362;  64 x 4: 378  (half the heads)
+    //   of 128:       64 rows  4 x 16,  64 x 4: 271;  2 x 32, 128 x 2: 308
+    //                128 rows  4 x 32,  64 x 4: 375;  8 x 16, 64 x 4: 389;  32 x 4: 409
+    //                256 rows  8 x 32,  64 x 4: 519;  32 x 4: 541  (16 sequences of 512 rows)
+    //   of 256:      128 rows  8 x 16,  32 x 4: 349;  64 x 2: 389
 #define NARROW(DT, DP, VW, R, OCC) attend_with(st, k_attend<DT, DP, VW, R, OCC>, a, ATTN_WG, 16 * R, OCC < 2 ? 2 : OCC)
 #define WIDE(DP, R, WR, KB, STAGES) \
     attend_with(st, k_attend_wide<DP, R, WR, KB, STAGES>, a, ATTN_WIDE_WG, 16 * R * WR, 1)
@@ -1336,9 +1394,15 @@ template <int DT, bool VEC> __device__ inline void copy_piece(char *to, const ch
         store_global<uint32_t>(to, load_global<uint32_t>(from));
 }
 
-// A rotated piece holds 16 bytes of both halves of a head (of neighbouring pairs: 16 bytes), the
-// others 16 bytes, at any address of the element's alignment; without VEC, where the rotated part is
-// no whole number of them, one pair and one element.  A token's pieces: its query heads', its key heads', its values'.
+// Pair (x, y) number p of a head, at position n, turns by the angle n inv_freq[p]:
+// (x cos - y sin, y cos + x sin).  A rotated piece holds 16 bytes of both halves of a head (of
+// neighbouring pairs: 16 bytes), the others 16 bytes, at any address of the element's alignment;
+// without VEC, where the rotated part is no whole number of them, one pair and one element.  A token's
+// pieces: its query heads', its key heads', its values'.  Angles of a token are computed once, into LDS.
+//
+// Bound by memory, a few tokens by the call: 13800 tokens of 32 query and 8 key heads of 128 in
+// bfloat16: 76.5 us, 4.4 TB/s read and written (a large copy 5.0); 2112 tokens in 256 entries 12.7 us; one
+// 8.3 us.  Four tokens to a workgroup: with 2 it is 78.7 us, with 8 83.8, with 16 101.
 template <int DT, bool VEC, bool INTER>
 __global__ __launch_bounds__(ATTN_WG) void k_append(AppendArgs a)
 {

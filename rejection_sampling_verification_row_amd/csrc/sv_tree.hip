@@ -109,14 +109,21 @@ template <int DT> __device__ inline u32x4 end_group(const char *row, int e, int 
     return v;
 }
 
-// What decides between all rows at once and depth by depth.
-constexpr double TREE_RATE = 6e6;        // bytes a microsecond
-constexpr double TREE_ALL_US = 9.0, TREE_LEVEL_US = 4.5;
+// What decides between all rows at once and depth by depth, from times of both: bytes a microsecond
+// that either reads, the two launches for all rows, and each launch of a depth.  In us, bfloat16, all rows
+// and depth by depth: 16 trees of 64 nodes, 128256 ids, depth 8: 47.0 and 39.3; 64 of them 165.5 and 49.2;
+// 32 trees of 64 nodes, 32000 ids, depth 8: 27.8 and 39.8; 256 of 16 nodes, depth 5: 47.5 and 40.8; 64 of 8
+// nodes, 128256 ids, depth 4: 27.4 and 32.9.
+constexpr double TREE_RATE = 6.5e6;
+constexpr double TREE_ALL_US = 7.0, TREE_LEVEL_US = 3.3;
 
-// One depth of every walk, `groups` workgroups to a sequence.  Workgroup (b, c): the node that the walk stands on after the `level`
-// tokens before (from the row that the launch before reduced), and chunk c of its row.  The sequence's
-// first workgroup writes what is known.  Partials alternate between two halves, since others of the
-// sequence may still read those before.
+// One depth of every walk, `groups` workgroups to a sequence.  Workgroup (b, c): the node that the walk
+// stands on after the `level` tokens before (from the row that the launch before reduced), and chunk c
+// of its row.  The sequence's first workgroup writes what is known.  Partials alternate between two
+// halves, since others of the sequence may still read those before.
+//
+// Bound by the launches, which wait for one another: 64 trees, depth 8, 128256 ids in bfloat16: 10
+// launches, 49 us, of which 16 us go to at most 148 MB of rows.
 template <int DT>
 __global__ __launch_bounds__(WG) void k_tree_level(const char *__restrict__ tgt, const int *tokens,
                                                    const int *parents, const int *counts, int T, int V, int depth,
@@ -234,7 +241,8 @@ constexpr int KEEP_WG = 256;
 // A thread has sizeof(V) bytes of a token in one pool and moves them for every node of the path in
 // turn, so that a place is read before the thread writes it: places ascend, and a node moves down
 // or stays.  Four loads are under way at once: the places that they are stored to are below those
-// that later ones read.
+// that later ones read (one at a time: 29 us where it is 18.4 now, 69 MB at 3.8 TB/s).  Few paths are
+// bound by the call: 6.5 us.
 template <typename V> __global__ __launch_bounds__(KEEP_WG) void k_keep_path(CacheView c, int n, int max_count,
                                                                             int groups, const int *seqs,
                                                                             const int *accepted, const int *path,
