@@ -1171,14 +1171,23 @@ __global__ __launch_bounds__(ATTN_WIDE_WG, 1) void k_attend_wide(AttnArgs a)
 }
 
 // LG lanes join what the parts of one row left, 4 elements each; eight parts' loads under way at once.
+// SPLIT: a workgroup has one row, and its groups of lanes every GROUPS-th part, joined in their order.
 // Rows of one part are done.  Bound by memory where many rows are split (65536 rows of 128 in two
-// parts: 28 us for 84 MB), by the launch else (4 us).
-template <int DT, int LG> __global__ __launch_bounds__(ATTN_WG) void k_attend_join(AttnArgs a, int rows_per_tile)
+// parts: 29 us for 84 MB), by the launch and the latency of its loads else (32 rows of 8 parts: 4 us).
+//
+// Up to JOIN_SPLIT rows to a compute unit are split: attend of 5 nodes over 250001 tokens (160 rows of 32
+// parts) 182 -> 178 us, of one node 199 -> 190 us; for 2048 rows of two parts it is 213 us against 211.
+constexpr int JOIN_SPLIT = 4;
+
+template <int DT, int LG, bool SPLIT>
+__global__ __launch_bounds__(ATTN_WG) void k_attend_join(AttnArgs a, int rows_per_tile)
 {
-    constexpr int ES = Tile<DT>::ES;
-    const int lane = threadIdx.x & (LG - 1);
+    constexpr int ES = Tile<DT>::ES, GROUPS = ATTN_WG / LG, STEP = SPLIT ? GROUPS : 1;
+    __shared__ f32x4 s_acc[SPLIT ? GROUPS : 1][LG];
+    __shared__ float2 s_ml[SPLIT ? GROUPS : 1];
+    const int lane = threadIdx.x & (LG - 1), group = threadIdx.x / LG;
     const uint32_t per = (uint32_t)a.nv.max_count * a.a.q_heads;       // the launch's work-items fit 32 bits
-    const uint32_t at = blockIdx.x * (ATTN_WG / LG) + threadIdx.x / LG;
+    const uint32_t at = SPLIT ? blockIdx.x : blockIdx.x * GROUPS + group;
     const int i = (int)(at / per), rest = (int)(at - i * per);
     if (i >= a.nv.n)
         return;
@@ -1192,19 +1201,21 @@ template <int DT, int LG> __global__ __launch_bounds__(ATTN_WG) void k_attend_jo
     const int gr = node * a.a.group + qh - head * a.a.group, mt = gr / rows_per_tile, row = gr - mt * rows_per_tile;
     const double base = p.base + (double)(head * p.tiles_of_rows + mt) * p.tiles;
     const int w0 = (int)(base / share), parts = (int)((base + (p.tiles - 1)) / share) - w0 + 1;
-    if (parts < 2 || !sound || lane * 4 >= D)
+    if (parts < 2 || !sound)
         return;
-    float top = -INFINITY, z = 0.0f, acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    for (int c0 = 0; c0 < parts; c0 += 8) {
+    const int d = lane * 4 < D ? lane * 4 : 0;
+    float top = -INFINITY, z = 0.0f;
+    f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
+    for (int c0 = SPLIT ? group : 0; c0 < parts; c0 += 8 * STEP) {
         float2 ml[8];
         f32x4 v[8];
 #pragma unroll
         for (int c = 0; c < 8; ++c) {
             // the last part again where there is none, without weight
-            const int part = min(c0 + c, parts - 1);
+            const int part = min(c0 + c * STEP, parts - 1);
             const int64_t kept = (int64_t)(2 * (w0 + part) + (part == 0)) * rows_per_tile + row;
             ml[c] = a.a.part_ml[kept];
-            v[c] = load_global<f32x4>(a.a.part_o + kept * D + lane * 4);
+            v[c] = load_global<f32x4>(a.a.part_o + kept * D + d);
         }
         const float was = top;
 #pragma unroll
@@ -1212,19 +1223,35 @@ template <int DT, int LG> __global__ __launch_bounds__(ATTN_WG) void k_attend_jo
             top = fmaxf(top, ml[c].x);
         const float old = was == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(was - top);
         z *= old;
-#pragma unroll
-        for (int x = 0; x < 4; ++x)
-            acc[x] *= old;
+        acc *= old;
 #pragma unroll
         for (int c = 0; c < 8; ++c)
-            if (c0 + c < parts) {
+            if (c0 + c * STEP < parts) {
                 const float f = ml[c].x == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(ml[c].x - top);
                 z += f * ml[c].y;
-#pragma unroll
-                for (int x = 0; x < 4; ++x)
-                    acc[x] += f * v[c][x];
+                acc += f * v[c];
             }
     }
+    if constexpr (SPLIT) {
+        s_acc[group][lane] = acc;
+        if (lane == 0)
+            s_ml[group] = make_float2(top, z);
+        __syncthreads();
+        if (group > 0)
+            return;
+        for (int g = 1; g < min(parts, GROUPS); ++g)
+            top = fmaxf(top, s_ml[g].x);
+        z = 0.0f;
+        acc = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        for (int g = 0; g < min(parts, GROUPS); ++g) {
+            const float2 ml = s_ml[g];
+            const float f = ml.x == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(ml.x - top);
+            z += f * ml.y;
+            acc += f * s_acc[g][lane];
+        }
+    }
+    if (lane * 4 >= D)
+        return;
     char *to = a.out + (int64_t)(p.start + node) * a.out_stride + ((int64_t)qh * D + lane * 4) * ES;
 #pragma unroll
     for (int x = 0; x < 4; ++x) {
@@ -1238,6 +1265,15 @@ template <int DT, int LG> __global__ __launch_bounds__(ATTN_WG) void k_attend_jo
         a.lse[(int64_t)(p.start + node) * a.a.q_heads + qh] = z == 0.0f ? -INFINITY : (top + log2f(z)) * LN2;
 }
 
+template <int LG> void join_with(hipStream_t st, bool bf16, const AttnArgs &a, int rows, int64_t joined)
+{
+    const bool split = joined <= JOIN_SPLIT * a.a.num_cus;
+    const unsigned groups = (unsigned)(split ? joined : (joined * LG + ATTN_WG - 1) / ATTN_WG);
+    auto join = split ? (bf16 ? k_attend_join<1, LG, true> : k_attend_join<0, LG, true>)
+                      : (bf16 ? k_attend_join<1, LG, false> : k_attend_join<0, LG, false>);
+    join<<<groups, ATTN_WG, 0, st>>>(a, rows);
+}
+
 // The launch of a form for tiles of `rows` rows.
 template <typename K> hipError_t attend_with(hipStream_t st, K kernel, AttnArgs a, int threads, int rows, int per_cu)
 {
@@ -1246,17 +1282,16 @@ template <typename K> hipError_t attend_with(hipStream_t st, K kernel, AttnArgs 
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess)
         return e;
-    const int lanes = a.a.head_dim <= 64 ? 16 : a.a.head_dim <= 128 ? 32 : 64;
-    const int64_t joined = (int64_t)a.nv.n * a.nv.max_count * a.a.q_heads, each = ATTN_WG / lanes;
-    const unsigned groups = (unsigned)((joined + each - 1) / each);
-    if (groups > 0) {
-        auto join = a.a.dtype == 1 ? k_attend_join<1, 64> : k_attend_join<0, 64>;
-        if (lanes == 16)
-            join = a.a.dtype == 1 ? k_attend_join<1, 16> : k_attend_join<0, 16>;
-        else if (lanes == 32)
-            join = a.a.dtype == 1 ? k_attend_join<1, 32> : k_attend_join<0, 32>;
-        join<<<groups, ATTN_WG, 0, st>>>(a, rows);
-    }
+    const int64_t joined = (int64_t)a.nv.n * a.nv.max_count * a.a.q_heads;
+    if (joined == 0)
+        return hipSuccess;
+    const bool bf16 = a.a.dtype == 1;
+    if (a.a.head_dim <= 64)
+        join_with<16>(st, bf16, a, rows, joined);
+    else if (a.a.head_dim <= 128)
+        join_with<32>(st, bf16, a, rows, joined);
+    else
+        join_with<64>(st, bf16, a, rows, joined);
     return hipGetLastError();
 }
 
