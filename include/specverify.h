@@ -542,7 +542,7 @@ int specverify_attn_append(specverify_attn *attn, void *hip_stream, int key_pool
  * window > 0: a token is seen only from positions less than `window` after its own.  Tokens whose
  * page is out of range are not seen; a row that sees nothing, or nothing above -inf, gets zeros and
  * -inf.  What a row does not see does not touch it, whatever its values.
- * queries, out: [rows][q_heads][head_dim].  Scores, maxima and sums are fp32; for bfloat16 the
+ * queries, out: [rows][q_heads][head_dim], which must not overlap.  Scores, maxima and sums are fp32; for bfloat16 the
  * weights exp(s_j - max) are rounded to bfloat16 for the product with the values (their sum is
  * not), and the result once more at the end.  The order of the sums depends on the call's lengths
  * only: the same call gives the same bits.
