@@ -493,7 +493,9 @@ typedef struct specverify_nodes {
 /*
  * Create a handle for attention over `cache`, which has to live while calls are made.  Allocates the
  * handle's workspace on the cache's device (what parts of a sequence leave for their joining: about
- * 70 MB for heads of 128).
+ * 70 MB for heads of 128).  The workspace serves one specverify_attn_attend at a time: calls on one
+ * handle, and replays of captured ones, have to be ordered, on one stream or by events; concurrent
+ * streams take a handle each.
  * Errors: EINVAL (NULL pointers, sizes < 1, q_heads not a multiple of kv_heads, head_dim elements
  * not a multiple of 16 bytes, page_bytes other than said above), EUNSUPPORTED (dtype), ECAPACITY
  * (head_dim, max_nodes or max_entries above the limits, q_heads above 2^16), EHIP, ENOMEM.

@@ -937,6 +937,7 @@ int specverify_attn_create(specverify_attn **out, const specverify_cache *cache,
         return SPECVERIFY_ENOMEM;
     a->bytes = b_plan + b_sound + b_share + b_ml + b_o;
     if (hipMalloc(&a->mem, a->bytes) != hipSuccess) {
+        (void)hipGetLastError();          // else the next launch would report it
         delete a;
         return SPECVERIFY_ENOMEM;
     }

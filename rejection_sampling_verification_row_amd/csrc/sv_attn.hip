@@ -287,7 +287,8 @@ template <int KT> __device__ inline bool next_job(const AttnArgs &a, int rows_pe
             int entry = uniform(job.entry);
             Entry e = {uniform(job.e.seq), uniform(job.e.start), uniform(job.e.count), uniform(job.e.len)};
             Work w = entry_work<KT>(a, e, rows_per_tile);
-            while (at >= base + w.all()) {
+            // `entry` stays below n whatever other work does to the lengths meanwhile
+            while (at >= base + w.all() && entry + 1 < a.nv.n) {
                 base += w.all();
                 e = load_entry(a.c, a.nv, ++entry);
                 w = entry_work<KT>(a, e, rows_per_tile);
