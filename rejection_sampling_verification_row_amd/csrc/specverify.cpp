@@ -431,9 +431,10 @@ int specverify_run_greedy_tree(specverify_ctx *ctx, void *hip_stream, int dtype,
         return SPECVERIFY_EHIP;
     hipEvent_t *ev = next_events(ctx);
     sv::Launch ln{static_cast<hipStream_t>(hip_stream), ev, ctx->prof_mask};
-    const hipError_t e = sv::launch_greedy_tree(ln, ctx->ws, dtype, B, T, V, depth, target_logits, tokens,
-                                                parents, counts, accepted_len, path, out_tokens);
-    note_call(ctx, ev, (1u << sv::KIND_ARGMAX) | (1u << sv::KIND_GREEDY_EMIT));
+    unsigned kinds = 0;
+    const hipError_t e = sv::launch_greedy_tree(ln, ctx->ws, ctx->num_cus, dtype, B, T, V, depth, target_logits,
+                                                tokens, parents, counts, accepted_len, path, out_tokens, &kinds);
+    note_call(ctx, ev, kinds);
     return e == hipSuccess ? SPECVERIFY_OK : SPECVERIFY_EHIP;
 }
 

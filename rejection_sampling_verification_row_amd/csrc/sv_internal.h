@@ -359,11 +359,11 @@ hipError_t launch_append(hipStream_t st, const CacheView &c, const AttnShape &a,
 hipError_t launch_keep_path(hipStream_t st, const CacheView &c, int n, int max_count, const int *seqs,
                             const int *accepted, const int *path, int *status);
 
-// greedy verify of a drafted tree, rows read all at once or depth by depth
-hipError_t launch_greedy_tree(const Launch &ln, const Workspace &ws, int dtype, int B, int T, int V,
+// greedy verify of a drafted tree, in one launch, with all rows at once or depth by depth; *kinds: what was launched
+hipError_t launch_greedy_tree(const Launch &ln, const Workspace &ws, int cus, int dtype, int B, int T, int V,
                               int depth, const void *tgt, const int32_t *tokens,
                               const int32_t *parents, const int32_t *counts, int32_t *acc_len,
-                              int32_t *path, int32_t *out_tokens);
+                              int32_t *path, int32_t *out_tokens, unsigned *kinds);
 // k_argmax over `rows` rows in a row: the chunks' partials in ws.part
 hipError_t launch_argmax_rows(const Launch &ln, const Workspace &ws, int dtype, size_t rows, int V,
                               const void *tgt);

@@ -4,7 +4,7 @@
 // everything and a launch that walks; depth by depth is a launch for each depth, which reads one row
 // of each sequence that is still walking.  In a launch of the latter every workgroup merges its
 // sequence's partials of the depth before, finds the next node and reads its chunk of that row, so
-// that no workgroup waits for another.
+// that no workgroup waits for another.  Trees whose rows are short take one launch: a workgroup has one.
 #include <algorithm>
 #include <limits.h>
 
@@ -109,13 +109,83 @@ template <int DT> __device__ inline u32x4 end_group(const char *row, int e, int 
     return v;
 }
 
-// What decides between all rows at once and depth by depth, from times of both: bytes a microsecond
-// that either reads, the two launches for all rows, and each launch of a depth.  In us, bfloat16, all rows
-// and depth by depth: 16 trees of 64 nodes, 128256 ids, depth 8: 47.0 and 39.3; 64 of them 165.5 and 49.2;
-// 32 trees of 64 nodes, 32000 ids, depth 8: 27.8 and 39.8; 256 of 16 nodes, depth 5: 47.5 and 40.8; 64 of 8
-// nodes, 128256 ids, depth 4: 27.4 and 32.9.
-constexpr double TREE_RATE = 6.5e6;
-constexpr double TREE_ALL_US = 7.0, TREE_LEVEL_US = 3.3;
+// A whole tree: each wave the argmaxes of every TREE_WAVES-th row, then the walk.  Bound by the call for a
+// few short rows (one tree of 8 nodes, 1000 ids: 8.2 us, of which the host's 8), by what a compute unit reads else
+// (256 trees of 64 nodes, 4000 ids, bfloat16: 23 us, 5.7 TB/s; all rows first: 53 us).
+constexpr int TREE_WAVES = 16, TREE_LOADS = 4;
+template <int DT>
+__global__ __launch_bounds__(64 * TREE_WAVES) void k_tree_short(const char *__restrict__ tgt, const int *tokens,
+                                                                const int *parents, const int *counts, int T, int V,
+                                                                int depth, int *acc, int *path, int *out)
+{
+    constexpr int E = Elt<DT>::EPV;
+    __shared__ int best[MAX_NODES];
+    const int b = blockIdx.x, lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+    const Nodes n = load_nodes(tokens, parents, counts, b, T, V);
+    for (int i = w; i < T && n.sound && i < n.count; i += blockDim.x >> 6) {
+        const char *row = tgt + ((size_t)b * T + i) * (size_t)V * Elt<DT>::BYTES;
+        float bv = -INFINITY;
+        int bi = lane * E < V ? lane * E : INT_MAX;
+        for (int base = 0; base < V; base += 64 * E * TREE_LOADS) {
+            u32x4 raw[TREE_LOADS];
+#pragma unroll
+            for (int k = 0; k < TREE_LOADS; ++k) {
+                const int e = base + (k * 64 + lane) * E;
+                raw[k] = e + E <= V ? load_group<DT>(row, e) : low_group<DT>();
+                if (e < V && e + E > V)
+                    raw[k] = end_group<DT>(row, e, V);
+            }
+#pragma unroll
+            for (int k = 0; k < TREE_LOADS; ++k) {
+                float x[E];
+                Elt<DT>::unpack(make_uint4(raw[k][0], raw[k][1], raw[k][2], raw[k][3]), x);
+#pragma unroll
+                for (int j = 0; j < E; ++j)
+                    if (x[j] > bv) {
+                        bv = x[j];
+                        bi = base + (k * 64 + lane) * E + j;
+                    }
+            }
+        }
+        wave_argmax(bv, bi);
+        if (lane == 0)
+            best[i] = bi;
+    }
+    __syncthreads();
+    if (w > 0)
+        return;
+    int at = n.sound ? 0 : -1, L = -1, my_node = -1, my_token = -1;
+    while (at >= 0) {
+        const int g = best[at];
+        ++L;
+        if (lane == L) {
+            my_node = at;
+            my_token = g;
+        }
+        at = L < depth ? child_of(n, at, g) : -1;
+    }
+    if (lane <= depth) {
+        path[(size_t)b * (depth + 1) + lane] = my_node;
+        out[(size_t)b * (depth + 1) + lane] = my_token;
+    }
+    if (lane == 0)
+        acc[b] = L;
+}
+
+// What decides between the three, in us, from times of each: all rows are bound by the bytes or by
+// workgroups of which each reads 16 KB or less; depth by depth adds a launch each; in one launch a compute unit reads a
+// tree's rows by itself, a round of TREE_WAVES rows after another.  Calls take TREE_LEAST of the host.
+// Measured, bfloat16 (trees, nodes, ids, depth: all rows, depth by depth, one launch):
+//     1,  8,   1000, 4:  9.5, 21,   8.2      64, 16,   4000, 4: 10.4,   -,  8.3
+//     1, 64,   4000, 8:  9.7, 31,  17.5     256, 64,   1000, 8: 51.9,   -, 12.5
+//    16, 64, 128256, 8: 47.0, 39.3,   -     256, 16,   8000, 4: 20.8,   -, 12.8
+//    32, 64,  32000, 8: 27.8, 39.8,   -     256, 64,   4000, 8: 53.3,   -, 22.9
+//    64,  8, 128256, 4: 27.4, 32.9,   -      64, 16,  16000, 5: 13.4,   -, 16.6
+//    64, 64, 128256, 8: 165,  49.2,   -     256, 16,  32000, 5: 47.5, 40.8,  -
+constexpr double TREE_RATE = 6.5e6, TREE_UNIT_RATE = 4.5e4;       // bytes a us: the card, a compute unit
+constexpr double TREE_GROUP_US = 0.0026;                          // a workgroup among many
+constexpr double TREE_ALL_US = 7.0, TREE_LEVEL_US = 3.3, TREE_SHORT_US = 4.0, TREE_ROUND_US = 1.0;
+constexpr double TREE_LEAST_ALL = 9.5, TREE_LEAST_SHORT = 8.0;
 
 // One depth of every walk, `groups` workgroups to a sequence.  Workgroup (b, c): the node that the walk
 // stands on after the `level` tokens before (from the row that the launch before reduced), and chunk c
@@ -212,18 +282,36 @@ hipError_t tree_by_levels(const Launch &ln, const Workspace &ws, int B, int T, i
 
 }  // namespace
 
-hipError_t launch_greedy_tree(const Launch &ln, const Workspace &ws, int dtype, int B, int T, int V,
+hipError_t launch_greedy_tree(const Launch &ln, const Workspace &ws, int cus, int dtype, int B, int T, int V,
                               int depth, const void *tgt, const int32_t *tokens,
                               const int32_t *parents, const int32_t *counts, int32_t *acc_len,
-                              int32_t *path, int32_t *out_tokens)
+                              int32_t *path, int32_t *out_tokens, unsigned *kinds)
 {
-    const double row = (double)V * (dtype == 1 ? 2 : 4), us_all = TREE_ALL_US + B * T * row / TREE_RATE,
-                 us_levels = (depth + 2) * TREE_LEVEL_US + (depth + 1) * B * row / TREE_RATE;
+    const double row = (double)V * (dtype == 1 ? 2 : 4);
+    const int nch = num_chunks(NV_ARGMAX, dtype, V), rounds = (T + TREE_WAVES - 1) / TREE_WAVES;
+    const double us_rows = std::max((double)B * T * row / TREE_RATE, (double)B * T * nch * TREE_GROUP_US);
+    const double us_all = std::max(TREE_ALL_US + us_rows, TREE_LEAST_ALL);
+    const double us_levels = (depth + 2) * TREE_LEVEL_US + (depth + 1) * us_rows / T;
+    const double us_short =
+        std::max(TREE_SHORT_US + rounds * TREE_ROUND_US + (B + cus - 1) / cus * (T * row / TREE_UNIT_RATE),
+                 TREE_LEAST_SHORT);
+    if (us_short < std::min(us_all, us_levels)) {
+        const dim3 threads(64 * std::min(T, TREE_WAVES));
+        *kinds = 1u << KIND_GREEDY_EMIT;
+        if (dtype == 1)
+            SV_LAUNCH(ln, KIND_GREEDY_EMIT, k_tree_short<1>, dim3(B), threads, 0, static_cast<const char *>(tgt),
+                      tokens, parents, counts, T, V, depth, acc_len, path, out_tokens);
+        else
+            SV_LAUNCH(ln, KIND_GREEDY_EMIT, k_tree_short<0>, dim3(B), threads, 0, static_cast<const char *>(tgt),
+                      tokens, parents, counts, T, V, depth, acc_len, path, out_tokens);
+        return hipGetLastError();
+    }
+    *kinds = 1u << KIND_ARGMAX | 1u << KIND_GREEDY_EMIT;
     if (us_levels < us_all)
         return (dtype == 1 ? tree_by_levels<1> : tree_by_levels<0>)(ln, ws, B, T, V, depth,
                                                                   static_cast<const char *>(tgt), tokens, parents,
                                                                   counts, acc_len, path, out_tokens);
-    const int np = num_chunks(NV_ARGMAX, dtype, V) * WAVES;
+    const int np = nch * WAVES;
     const hipError_t e = launch_argmax_rows(ln, ws, dtype, (size_t)B * T, V, tgt);
     if (e != hipSuccess)
         return e;

@@ -78,9 +78,9 @@ def test_many_split_rows_are_joined(dt, D):
 
 
 def test_tree_and_path_calls_on_a_stream_and_in_a_replayed_graph():
-    """Both ways of the tree's walk and a path's move, captured once, replayed with other inputs."""
+    """The three ways of the tree's walk and a path's move, captured once, replayed with other inputs."""
     r = np.random.RandomState(5)
-    for B, T, V, depth in ((3, 12, 900, 4), (96, 64, 32000, 3)):
+    for B, T, V, depth in ((3, 12, 900, 4), (5, 33, 9000, 6), (96, 64, 32000, 3)):
         ctx = sv.specverify_create(0, B, T - 1, V)
         n = min(B, 8)
         books = Books(8, list(r.randint(0, 40, n)), [T] * n, 64, 2, seed=B)
@@ -88,8 +88,8 @@ def test_tree_and_path_calls_on_a_stream_and_in_a_replayed_graph():
         pools = [dev(p) for p in books.pools]
         cache = sv.specverify_cache_create(0, books.P, 8, books.S, books.mb, 64 * 8, pools, *state)
         seqs = dev(books.seqs)
-        kinds = [forest(r, B, T, V, 1, 0.8) if V < 1000 else None for _ in range(3)]
-        if V > 1000:
+        kinds = [forest(r, B, T, V, 1, 0.8) if V < 10000 else None for _ in range(3)]
+        if V > 10000:
             tok = torch.randint(0, V, (B, T), **I32)
             par = (torch.arange(T, **I32) - 1).repeat(B, 1).contiguous()
             x = torch.randn((B, T, V), device="cuda").bfloat16()
@@ -111,7 +111,7 @@ def test_tree_and_path_calls_on_a_stream_and_in_a_replayed_graph():
         with torch.cuda.graph(graph, stream=side):
             both(side)
         for i in range(4):
-            if V > 1000:
+            if V > 10000:
                 x.copy_(torch.randn_like(x))
                 best = tok.roll(-1, 1).long()[:, :, None]
                 x.scatter_(2, best, (torch.rand((B, T, 1), device="cuda") < 0.7).to(x.dtype) * 9)
