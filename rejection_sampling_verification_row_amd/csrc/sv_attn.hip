@@ -29,8 +29,8 @@
 #include <algorithm>
 #include <type_traits>
 
-#include "sv_device.h"
 #include "sv_internal.h"
+#include "sv_memory.h"
 
 namespace sv {
 

@@ -364,9 +364,6 @@ hipError_t launch_greedy_tree(const Launch &ln, const Workspace &ws, int cus, in
                               int depth, const void *tgt, const int32_t *tokens,
                               const int32_t *parents, const int32_t *counts, int32_t *acc_len,
                               int32_t *path, int32_t *out_tokens, unsigned *kinds);
-// k_argmax over `rows` rows in a row: the chunks' partials in ws.part
-hipError_t launch_argmax_rows(const Launch &ln, const Workspace &ws, int dtype, size_t rows, int V,
-                              const void *tgt);
 
 // The workspace of the entry point that allocates nothing: a file-scope device array of
 // STATIC_SCRATCH_BYTES per device (see static_scratch in the kernels' source).

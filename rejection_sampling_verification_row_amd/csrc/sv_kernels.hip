@@ -3110,18 +3110,6 @@ hipError_t launch_early_exit(const Launch &ln, const Workspace &ws, int mode, in
              rest_grid);
 }
 
-hipError_t launch_argmax_rows(const Launch &ln, const Workspace &ws, int dtype, size_t rows, int V,
-                              const void *tgt)
-{
-    const int nch = num_chunks(NV_ARGMAX, dtype, V);
-    const char *t = static_cast<const char *>(tgt);
-    if (dtype == 1)
-        SV_LAUNCH(ln, KIND_ARGMAX, k_argmax<1>, dim3((unsigned)(rows * nch)), dim3(WG), 0, t, V, nch, 1, ws.part);
-    else
-        SV_LAUNCH(ln, KIND_ARGMAX, k_argmax<0>, dim3((unsigned)(rows * nch)), dim3(WG), 0, t, V, nch, 1, ws.part);
-    return hipGetLastError();
-}
-
 hipError_t launch_greedy_heads(const Launch &ln, const Workspace &ws, int dtype, int B, int K,
                                int H, int V, const void *logits, const int32_t *props,
                                int32_t *acc_len, int32_t *out_tokens, int32_t *next_props)

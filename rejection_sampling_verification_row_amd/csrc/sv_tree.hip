@@ -8,8 +8,8 @@
 #include <algorithm>
 #include <limits.h>
 
-#include "sv_device.h"
 #include "sv_internal.h"
+#include "sv_memory.h"
 
 namespace sv {
 
@@ -109,6 +109,54 @@ template <int DT> __device__ inline u32x4 end_group(const char *row, int e, int 
     return v;
 }
 
+// Chunk c of a row: each wave's maximum and the lowest id that has it.
+template <int DT> __device__ __forceinline__ void chunk_best(const char *row, int V, int c, float2 *to)
+{
+    constexpr int E = Elt<DT>::EPV;
+    const int t = threadIdx.x;
+    const int base = c * WG * NV_ARGMAX * E;
+    u32x4 raw[NV_ARGMAX];
+    if (base + WG * NV_ARGMAX * E <= V) {
+#pragma unroll
+        for (int i = 0; i < NV_ARGMAX; ++i)
+            raw[i] = load_group<DT>(row, base + (i * WG + t) * E);
+    } else {
+        // the row's end: what is past it reads as -inf
+#pragma unroll
+        for (int i = 0; i < NV_ARGMAX; ++i) {
+            const int e = base + (i * WG + t) * E;
+            raw[i] = e + E <= V ? load_group<DT>(row, e) : low_group<DT>();
+            if (e < V && e + E > V)
+                raw[i] = end_group<DT>(row, e, V);
+        }
+    }
+    float bv = -INFINITY;
+    int bi = base + t * E < V ? base + t * E : INT_MAX;
+#pragma unroll
+    for (int i = 0; i < NV_ARGMAX; ++i) {
+        float x[E];
+        Elt<DT>::unpack(make_uint4(raw[i][0], raw[i][1], raw[i][2], raw[i][3]), x);
+#pragma unroll
+        for (int k = 0; k < E; ++k)
+            if (x[k] > bv) {
+                bv = x[k];
+                bi = base + (i * WG + t) * E + k;
+            }
+    }
+    wave_argmax(bv, bi);
+    if ((t & 63) == 0)
+        to[t >> 6] = make_float2(bv, __int_as_float(bi));
+}
+
+// All rows, a workgroup to a chunk.
+template <int DT>
+__global__ __launch_bounds__(WG) void k_tree_rows(const char *__restrict__ tgt, int V, int nch, float2 *part)
+{
+    const size_t r = blockIdx.x / nch;
+    chunk_best<DT>(tgt + r * (size_t)V * Elt<DT>::BYTES, V, (int)(blockIdx.x - r * nch),
+                   part + (size_t)blockIdx.x * WAVES);
+}
+
 // A whole tree: each wave the argmaxes of every TREE_WAVES-th row, then the walk.  Bound by the call for a
 // few short rows (one tree of 8 nodes, 1000 ids: 8.2 us, of which the host's 8), by what a compute unit reads else
 // (256 trees of 64 nodes, 4000 ids, bfloat16: 23 us, 5.7 TB/s; all rows first: 53 us).
@@ -200,8 +248,7 @@ __global__ __launch_bounds__(WG) void k_tree_level(const char *__restrict__ tgt,
                                                    int level, int groups, int nch, const float2 *before,
                                                    float2 *part, int *acc, int *path, int *out)
 {
-    constexpr int E = Elt<DT>::EPV;
-    const int b = blockIdx.x / groups, c = blockIdx.x - b * groups, t = threadIdx.x, lane = t & 63, w = t >> 6;
+    const int b = blockIdx.x / groups, c = blockIdx.x - b * groups, t = threadIdx.x;
     int *p = path + (size_t)b * (depth + 1), *o = out + (size_t)b * (depth + 1);
     const Nodes n = load_nodes(tokens, parents, counts, b, T, V);
     const bool first = c == 0 && t == 0;
@@ -227,38 +274,7 @@ __global__ __launch_bounds__(WG) void k_tree_level(const char *__restrict__ tgt,
     if (at < 0)
         return;
     const char *row = tgt + ((size_t)b * T + at) * (size_t)V * Elt<DT>::BYTES;
-    const int base = c * WG * NV_ARGMAX * E;
-    u32x4 raw[NV_ARGMAX];
-    if (base + WG * NV_ARGMAX * E <= V) {
-#pragma unroll
-        for (int i = 0; i < NV_ARGMAX; ++i)
-            raw[i] = load_group<DT>(row, base + (i * WG + t) * E);
-    } else {
-        // the row's end: what is past it reads as -inf
-#pragma unroll
-        for (int i = 0; i < NV_ARGMAX; ++i) {
-            const int e = base + (i * WG + t) * E;
-            raw[i] = e + E <= V ? load_group<DT>(row, e) : low_group<DT>();
-            if (e < V && e + E > V)
-                raw[i] = end_group<DT>(row, e, V);
-        }
-    }
-    float bv = -INFINITY;
-    int bi = base + t * E < V ? base + t * E : INT_MAX;
-#pragma unroll
-    for (int i = 0; i < NV_ARGMAX; ++i) {
-        float x[E];
-        Elt<DT>::unpack(make_uint4(raw[i][0], raw[i][1], raw[i][2], raw[i][3]), x);
-#pragma unroll
-        for (int k = 0; k < E; ++k)
-            if (x[k] > bv) {
-                bv = x[k];
-                bi = base + (i * WG + t) * E + k;
-            }
-    }
-    wave_argmax(bv, bi);
-    if (lane == 0)
-        part[(size_t)blockIdx.x * WAVES + w] = make_float2(bv, __int_as_float(bi));
+    chunk_best<DT>(row, V, c, part + (size_t)blockIdx.x * WAVES);
 }
 
 template <int DT>
@@ -312,9 +328,11 @@ hipError_t launch_greedy_tree(const Launch &ln, const Workspace &ws, int cus, in
                                                                   static_cast<const char *>(tgt), tokens, parents,
                                                                   counts, acc_len, path, out_tokens);
     const int np = nch * WAVES;
-    const hipError_t e = launch_argmax_rows(ln, ws, dtype, (size_t)B * T, V, tgt);
-    if (e != hipSuccess)
-        return e;
+    const dim3 chunks((unsigned)((size_t)B * T * nch));
+    if (dtype == 1)
+        SV_LAUNCH(ln, KIND_ARGMAX, k_tree_rows<1>, chunks, dim3(WG), 0, static_cast<const char *>(tgt), V, nch, ws.part);
+    else
+        SV_LAUNCH(ln, KIND_ARGMAX, k_tree_rows<0>, chunks, dim3(WG), 0, static_cast<const char *>(tgt), V, nch, ws.part);
     SV_LAUNCH(ln, KIND_GREEDY_EMIT, k_tree_walk, dim3(B), dim3(64), 0, tokens, parents, counts, T, V, depth, np,
               ws.part, acc_len, path, out_tokens);
     return hipGetLastError();
