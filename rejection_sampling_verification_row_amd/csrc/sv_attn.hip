@@ -178,15 +178,16 @@ template <int WG_SIZE> __device__ inline double block_scan(double v, double *lds
     return before + inc;
 }
 
-// An entry's work: segments (key heads times tiles of rows) and tiles of KT tokens from `low` on.
+// An entry's work: segments (key heads times tiles of rows) and tiles of KT tokens from `low` on.  A
+// segment counts AHEAD tiles more, which stand before its own: what it takes to begin and to end one.
 struct Work {
-    int tiles_of_rows, segments, low, tiles;
-    __device__ double all() const { return (double)segments * (double)tiles; }
+    int tiles_of_rows, segments, low, tiles, counted;
+    __device__ double all() const { return (double)segments * (double)counted; }
 };
 
-template <int KT> __device__ inline Work entry_work(const AttnArgs &a, const Entry &e, int rows_per_tile)
+template <int KT, int AHEAD> __device__ inline Work entry_work(const AttnArgs &a, const Entry &e, int rows_per_tile)
 {
-    Work w = {0, 0, 0, 0};
+    Work w = {0, 0, 0, 0, 0};
     if (e.count <= 0)
         return w;
     w.tiles_of_rows = (e.count * a.a.group + rows_per_tile - 1) / rows_per_tile;
@@ -194,6 +195,7 @@ template <int KT> __device__ inline Work entry_work(const AttnArgs &a, const Ent
     // the root is the first to see least far back
     w.low = a.window > 0 ? max(e.len - a.window + 1, 0) / KT : 0;
     w.tiles = (int)(((unsigned)e.len + e.count + KT - 1) / KT) - w.low;
+    w.counted = w.tiles + AHEAD;
     return w;
 }
 
@@ -214,7 +216,7 @@ struct Job {
 
 // This workgroup's stretch and the entry that it begins in.  Workgroup 0 also leaves the plan for the
 // join, and the status of entries that have no work.  False: there is no stretch for it.
-template <int WG_SIZE, int KT>
+template <int WG_SIZE, int KT, int AHEAD>
 __device__ bool find_stretch(const AttnArgs &a, int rows_per_tile, int least, Job &job)
 {
     __shared__ double lds[WG_SIZE / 64];
@@ -222,14 +224,14 @@ __device__ bool find_stretch(const AttnArgs &a, int rows_per_tile, int least, Jo
     Entry e = {-1, 0, -1, 0};
     if (t < n)
         e = load_entry(a.c, a.nv, t);
-    Work w = entry_work<KT>(a, e, rows_per_tile);
+    Work w = entry_work<KT, AHEAD>(a, e, rows_per_tile);
     double sum, first = block_scan<WG_SIZE>(w.all(), lds, &sum) - w.all();
     const double part = sum;             // of the first WG_SIZE entries
     for (int i0 = WG_SIZE; i0 < n; i0 += WG_SIZE) {
         const int i = i0 + t;
         double more = 0.0, all;
         if (i < n)
-            more = entry_work<KT>(a, load_entry(a.c, a.nv, i), rows_per_tile).all();
+            more = entry_work<KT, AHEAD>(a, load_entry(a.c, a.nv, i), rows_per_tile).all();
         block_scan<WG_SIZE>(more, lds, &all);
         sum += all;
     }
@@ -249,7 +251,7 @@ __device__ bool find_stretch(const AttnArgs &a, int rows_per_tile, int least, Jo
             e = {-1, 0, -1, 0};
             if (i < n)
                 e = load_entry(a.c, a.nv, i);
-            w = entry_work<KT>(a, e, rows_per_tile);
+            w = entry_work<KT, AHEAD>(a, e, rows_per_tile);
             double all;
             first = base + block_scan<WG_SIZE>(w.all(), lds, &all) - w.all();
             base += all;
@@ -263,7 +265,7 @@ __device__ bool find_stretch(const AttnArgs &a, int rows_per_tile, int least, Jo
             job.e = e;
         }
         if (blockIdx.x == 0 && i < n) {
-            a.a.plan[i] = {first, w.tiles, w.tiles_of_rows, e.start, max(e.count, 0)};
+            a.a.plan[i] = {first, w.counted, w.tiles, w.tiles_of_rows, e.start, max(e.count, 0)};
             if (a.status && w.segments == 0)
                 a.status[i] = e.count < 0 ? -1 : 0;
         }
@@ -275,39 +277,45 @@ __device__ bool find_stretch(const AttnArgs &a, int rows_per_tile, int least, Jo
 }
 
 // The next job of the stretch, found by the first wave; false at its end.
-template <int KT> __device__ inline bool next_job(const AttnArgs &a, int rows_per_tile, Job &job)
+template <int KT, int AHEAD> __device__ inline bool next_job(const AttnArgs &a, int rows_per_tile, Job &job)
 {
     if (threadIdx.x < 64) {
-        const double at = uniform(job.at), end = uniform(job.end);
-        if (at >= end) {
-            if (threadIdx.x == 0)
-                job.mine = -1;
-        } else {
-            double base = uniform(job.base);
-            int entry = uniform(job.entry);
-            Entry e = {uniform(job.e.seq), uniform(job.e.start), uniform(job.e.count), uniform(job.e.len)};
-            Work w = entry_work<KT>(a, e, rows_per_tile);
+        double at = uniform(job.at), base = uniform(job.base);
+        const double end = uniform(job.end);
+        int entry = uniform(job.entry), t0 = 0, t1 = 0;
+        double segment = 0.0;
+        Entry e = {uniform(job.e.seq), uniform(job.e.start), uniform(job.e.count), uniform(job.e.len)};
+        Work w = entry_work<KT, AHEAD>(a, e, rows_per_tile);
+        // what ends before a segment's own tiles is no job
+        while (at < end && t0 == t1) {
             // `entry` stays below n whatever other work does to the lengths meanwhile
             while (at >= base + w.all() && entry + 1 < a.nv.n) {
                 base += w.all();
                 e = load_entry(a.c, a.nv, ++entry);
-                w = entry_work<KT>(a, e, rows_per_tile);
+                w = entry_work<KT, AHEAD>(a, e, rows_per_tile);
             }
-            const double rel = at - base, segment = floor(rel / w.tiles);
-            const int off = (int)(rel - segment * w.tiles);
-            const int take = (int)fmin((double)(w.tiles - off), end - at);
-            if (threadIdx.x == 0) {
-                job.at = at + take;
+            segment = floor((at - base) / w.counted);
+            const int off = (int)(at - base - segment * w.counted);
+            const int take = max((int)fmin((double)(w.counted - off), end - at), 1);
+            at += take;
+            t0 = max(off - AHEAD, 0);
+            t1 = max(off + take - AHEAD, 0);
+        }
+        if (threadIdx.x == 0) {
+            if (t0 == t1) {
+                job.mine = -1;
+            } else {
+                job.at = at;
                 job.base = base;
                 job.entry = entry;
                 job.e = e;
                 job.head = (int)segment / w.tiles_of_rows;
                 job.mt = (int)segment - job.head * w.tiles_of_rows;
-                job.t0 = w.low + off;
-                job.t1 = w.low + off + take;
-                job.opens = rel == 0.0;
-                job.whole = take == w.tiles;
-                job.slot = 2 * job.mine + (off == 0);
+                job.t0 = w.low + t0;
+                job.t1 = w.low + t1;
+                job.opens = segment == 0.0 && t0 == 0;
+                job.whole = t0 == 0 && t1 == w.tiles;
+                job.slot = 2 * job.mine + (t0 == 0);
             }
         }
     }
@@ -544,7 +552,7 @@ __global__ __launch_bounds__(ATTN_WG, OCC) void k_attend(AttnArgs args)
     constexpr int KS = DP * ES / 64;              // 16-byte pieces of a key row to a lane
     constexpr int NB = DP / (16 * VW);            // pieces of a value row to a lane
     constexpr int NT = DP / 16;
-    constexpr int ROWS = 16 * R, PITCH = DP + 4;
+    constexpr int ROWS = 16 * R, PITCH = DP + 4, AHEAD = 8;
     typedef typename Chunk<VW * ES>::type vchunk;
 
     __shared__ float s_o[4 * ROWS][PITCH];
@@ -554,9 +562,9 @@ __global__ __launch_bounds__(ATTN_WG, OCC) void k_attend(AttnArgs args)
     __shared__ int s_low[ROWS];
     __shared__ Job job;
 
-    if (!find_stretch<ATTN_WG, KT>(args, ROWS, 128 / KT, job))
+    if (!find_stretch<ATTN_WG, KT, AHEAD>(args, ROWS, 128 / KT, job))
         return;
-    while (next_job<KT>(args_afresh(), ROWS, job)) {
+    while (next_job<KT, AHEAD>(args_afresh(), ROWS, job)) {
         const AttnArgs a = args_afresh();
         const int thread = afresh(threadIdx.x), lane = thread & 63, w = uniform(thread >> 6);
         const int col = lane & 15, grp = lane >> 4;
@@ -860,7 +868,7 @@ __global__ __launch_bounds__(ATTN_WIDE_WG, 1) void k_attend_wide(AttnArgs a)
     constexpr bool SHIFT = STAGES == 4;
     constexpr int ROWS = 16 * R * WR, PITCH = DP + 4, DEPTH = SHIFT ? STAGES - 2 : STAGES - 1;
     constexpr int HALF = TK * ROW, LOADS = HALF / 1024 / WAVES8;      // bytes of keys in a stage; a wave's loads
-    constexpr int PAGE_AHEAD = 2 * DEPTH + 1;
+    constexpr int PAGE_AHEAD = 2 * DEPTH + 1, AHEAD = 2;
     constexpr int EARLY = NT < 8 ? NT : 8;        // pieces of values read before the weights are there
     static_assert(LOADS * 1024 * WAVES8 == HALF && DEPTH <= 3 && TK <= ATTN_WIDE_WG, "whole loads, rings of 4 stages");
     constexpr int MERGE = WAVES8 * 16 * R * PITCH * 4;
@@ -875,9 +883,9 @@ __global__ __launch_bounds__(ATTN_WIDE_WG, 1) void k_attend_wide(AttnArgs a)
 
     const int t = threadIdx.x, lane = t & 63, w = uniform(t >> 6), col = lane & 15, grp = lane >> 4;
     const int rw = w % WR, kg = w / WR;
-    if (!find_stretch<ATTN_WIDE_WG, TK>(a, ROWS, 1, job))
+    if (!find_stretch<ATTN_WIDE_WG, TK, AHEAD>(a, ROWS, 1, job))
         return;
-    while (next_job<TK>(a, ROWS, job)) {
+    while (next_job<TK, AHEAD>(a, ROWS, job)) {
         uint64_t lane_seen;
         int lane_depth;
         const bool ok = open_job(a, job, lane_seen, lane_depth);
@@ -1200,7 +1208,7 @@ __global__ __launch_bounds__(ATTN_WG) void k_attend_join(AttnArgs a, int rows_pe
         return;
     const int D = a.a.head_dim, head = divide(qh, a.a.by_group);
     const int gr = node * a.a.group + qh - head * a.a.group, mt = gr / rows_per_tile, row = gr - mt * rows_per_tile;
-    const double base = p.base + (double)(head * p.tiles_of_rows + mt) * p.tiles;
+    const double base = p.base + (double)(head * p.tiles_of_rows + mt) * p.counted + (p.counted - p.tiles);
     const int w0 = (int)(base / share), parts = (int)((base + (p.tiles - 1)) / share) - w0 + 1;
     if (parts < 2 || !sound)
         return;

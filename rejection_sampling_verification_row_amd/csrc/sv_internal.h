@@ -320,11 +320,11 @@ struct NodesView {
     const int *seqs, *starts, *counts, *parents;
 };
 
-// An entry's work, for the joining of its parts: its first tile among all, the tiles of tokens of a
-// segment (a key head and a tile of rows), the tiles of rows, its rows.
+// An entry's work, for the joining of its parts: its first tile among all, the tiles of tokens that a
+// segment (a key head and a tile of rows) counts and has, the tiles of rows, its rows.
 struct AttnPlan {
     double base;
-    int tiles, tiles_of_rows, start, count;
+    int counted, tiles, tiles_of_rows, start, count;
 };
 
 struct AttnShape {
