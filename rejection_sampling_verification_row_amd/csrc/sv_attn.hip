@@ -552,7 +552,7 @@ __global__ __launch_bounds__(ATTN_WG, OCC) void k_attend(AttnArgs args)
     constexpr int KS = DP * ES / 64;              // 16-byte pieces of a key row to a lane
     constexpr int NB = DP / (16 * VW);            // pieces of a value row to a lane
     constexpr int NT = DP / 16;
-    constexpr int ROWS = 16 * R, PITCH = DP + 4, AHEAD = 8;
+    constexpr int ROWS = 16 * R, PITCH = DP + 4, AHEAD = 6;
     typedef typename Chunk<VW * ES>::type vchunk;
 
     __shared__ float s_o[4 * ROWS][PITCH];
@@ -868,7 +868,7 @@ __global__ __launch_bounds__(ATTN_WIDE_WG, 1) void k_attend_wide(AttnArgs a)
     constexpr bool SHIFT = STAGES == 4;
     constexpr int ROWS = 16 * R * WR, PITCH = DP + 4, DEPTH = SHIFT ? STAGES - 2 : STAGES - 1;
     constexpr int HALF = TK * ROW, LOADS = HALF / 1024 / WAVES8;      // bytes of keys in a stage; a wave's loads
-    constexpr int PAGE_AHEAD = 2 * DEPTH + 1, AHEAD = 2;
+    constexpr int PAGE_AHEAD = 2 * DEPTH + 1, AHEAD = 768 / TK;
     constexpr int EARLY = NT < 8 ? NT : 8;        // pieces of values read before the weights are there
     static_assert(LOADS * 1024 * WAVES8 == HALF && DEPTH <= 3 && TK <= ATTN_WIDE_WG, "whole loads, rings of 4 stages");
     constexpr int MERGE = WAVES8 * 16 * R * PITCH * 4;
