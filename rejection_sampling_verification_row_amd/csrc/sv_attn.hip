@@ -179,7 +179,11 @@ template <int WG_SIZE> __device__ inline double block_scan(double v, double *lds
 }
 
 // An entry's work: segments (key heads times tiles of rows) and tiles of KT tokens from `low` on.  A
-// segment counts AHEAD tiles more, which stand before its own: what it takes to begin and to end one.
+// segment counts AHEAD tiles more, which stand before its own: what it takes to begin and to end one
+// (queries, first loads, the waves' sums).  Without, stretches of many short segments were the last to end.
+// 64 sequences of 300 to 8200 tokens in k_attend_wide, AHEAD of 0, 768 and 1536 tokens: 32 rows 236, 210
+// and 216 us, 128 rows 375, 270 and 274 us; in k_attend, 24 float32 sequences in a window of 2000, 0, 6 and
+// 20 tiles: 72, 59 and 61 us.
 struct Work {
     int tiles_of_rows, segments, low, tiles, counted;
     __device__ double all() const { return (double)segments * (double)counted; }
@@ -534,11 +538,10 @@ __device__ inline void finish(const AttnArgs &a, const Job &j, int rows_per_tile
 // segment's end.
 //
 // Bound by memory, for one sequence by the way to the first load: 64 sequences of 300 to 8200 tokens,
-// 8 key heads of 128 in bfloat16, 4 rows each: 211 us, 5.3 TB/s (values brought through LDS: 212 us);
-// float32, 4 key heads of 128: 197 us, 5.7 TB/s; one sequence of 1000 tokens: 9 us and 4 us of the join.  Of those
-// 9 us the loop is 2; what comes before it is short because it is not kept in registers from one job
-// to the next (args_afresh: 14.5 -> 12.9 us) and because stretches are counted in doubles (64-bit
-// integer division: 15.4 -> 14.6 us).
+// 8 key heads of 128 in bfloat16, 4 rows each: 211 us, 5.3 TB/s; float32, 4 key heads of 128: 193 us,
+// 5.8 TB/s; one sequence of 1000 tokens: 9 us and 4 us of the join.  Of those 9 us the loop is 2; what comes
+// before it is short because it is not kept in registers from one job to the next (args_afresh: 14.5 ->
+// 12.9 us) and because stretches are counted in doubles (64-bit integer division: 15.4 -> 14.6 us).
 //
 // DP: head_dim or more; VW: elements of a value row that a lane loads at once, 16 lanes side by
 // side; R: tiles of 16 rows.  Left operands of the products: row lane % 16, 16 bytes (4 for float32)
@@ -853,13 +856,13 @@ __device__ inline void load_to_lds4(const void *from, uint32_t to)
 // 120 others with 16 exponentials (about 630 cycles), which overlap only if the two waves of a SIMD do
 // different things.  So with four stages the upper half of the waves meets the stage's barrier between
 // its scores and its weights, when the lower half begins with scores, and matrix instructions have
-// priority: 16 sequences of 64 nodes, 64 query and 8 key heads, 8000 to 16000 tokens: 531 -> 520 us,
-// 711 TFLOP/s, where a large library product reaches 1352 TFLOP/s.  The matrix units are busy 36% of the time;
+// priority (531 -> 520 us): 16 sequences of 64 nodes, 64 query and 8 key heads, 8000 to 16000 tokens: 501 us,
+// 739 TFLOP/s, where a large library product reaches 1352 TFLOP/s.  The matrix units are busy 36% of the time;
 // waves wait for barriers and LDS 29% of theirs and for their turn to issue 27%.  Not kept: the next block's
 // keys read, or its scores computed, before the weights of this one (no registers are left, 2 times slower).
 //
 // Fewer rows are bound by memory: 64 sequences of 300 to 8200 tokens with 8 key heads of 128: 32 rows
-// 236 us (4.75 TB/s), 64 rows 270 us, 128 rows 375 us.
+// 210 us (5.35 TB/s), 64 rows 226 us, 128 rows 270 us.
 template <int DP, int R, int WR, int KB, int STAGES>
 __global__ __launch_bounds__(ATTN_WIDE_WG, 1) void k_attend_wide(AttnArgs a)
 {
@@ -1320,21 +1323,24 @@ hipError_t launch_attend(hipStream_t st, const CacheView &c, const AttnShape &s,
     AttnArgs a = {c, s, nodes, key_pool, value_pool, scale == 0.0f ? 1.0f : fabsf(scale) * LOG2E,
                   scale > 0.0f ? 1.0f : scale < 0.0f ? -1.0f : 0.0f, window, static_cast<const char *>(q),
                   q_stride * es, static_cast<char *>(out), out_stride * es, lse, status, 0};
-    // Forms with tiles of as many rows as there are, or the largest.  Up to 16 rows k_attend is as fast
-    // as k_attend_wide or faster (heads of 128: one sequence 12.9 against 15.3 us, 64 of them 211 and 212 us;
-    // of 64: 227 and 252; of 256: 215 and 234).  It has as many workgroups on a compute unit as its
-    // registers allow (float32 heads of 64: 3, 70 us; 2, 79 us; 4, 100 us for spills); float32 has no other
-    // form, since its matrix instructions are 8 times slower than the bfloat16 ones and decide.
-    // k_attend_wide has what its registers and 160 KB of LDS allow, and of that the fastest, in us for 64 sequences
-    // of 300 to 8200 tokens (waves over the rows, rows of a wave, tokens and number of stages):
-    //   heads of 64:  32 rows  2 x 16, 128 x 4: 272;  x 2: 290
-    //                 64 rows  2 x 32, 128 x 4: 338;  4 x 16, 64 x 4: 348
-    //                128 rows  4 x 32, 128 x 4: 450;  64 x 4: 485;  8 x 16, 64 x 4: 534
-    //                256 rows  8 x 32, 128 x 4: 362;  64 x 4: 378  (half the heads)
-    //   of 128:       64 rows  4 x 16,  64 x 4: 271;  2 x 32, 128 x 2: 308
-    //                128 rows  4 x 32,  64 x 4: 375;  8 x 16, 64 x 4: 389;  32 x 4: 409
-    //                256 rows  8 x 32,  64 x 4: 519;  32 x 4: 541  (16 sequences of 512 rows)
-    //   of 256:      128 rows  8 x 16,  32 x 4: 349;  64 x 2: 389
+    // Forms with tiles of as many rows as there are, or the largest.  Up to 16 rows k_attend begins and ends
+    // faster, k_attend_wide reads long sequences faster, and the lengths are not known here: in us, k_attend
+    // and k_attend_wide, heads of 128 and 4 rows, one sequence of 1000 tokens 13.3 and 15.6, of 250001 190 and 176;
+    // 64 sequences of 50 to 400 tokens 30 and 37, of 300 to 2000 72 and 72, of 300 to 8200 211 and 197; the
+    // last with heads of 64 224 and 194, of 80 198 and 203, of 256 203 and 224.
+    // k_attend has as many workgroups on a compute unit as its registers allow (float32 heads of 64, when it
+    // was chosen: 3, 70 us; 2, 79 us; 4, 100 us for spills); float32 has no other form, since its matrix
+    // instructions are 8 times slower than the bfloat16 ones and decide.
+    // k_attend_wide has what its registers and 160 KB of LDS allow, and of that the fastest, in us for 64
+    // sequences of 300 to 8200 tokens (waves over the rows x rows of a wave, tokens x number of stages):
+    //   heads of 64:  32 rows  2 x 16, 128 x 4: 206;  x 2: 229
+    //                 64 rows  2 x 32, 128 x 4: 232;  4 x 16, 64 x 4: 248
+    //                128 rows  4 x 32, 128 x 4: 311;  64 x 4: 342;  8 x 16, 64 x 4: 407
+    //                256 rows  8 x 32, 128 x 4: 271;  64 x 4: 288  (half the heads)
+    //   of 128:       64 rows  4 x 16,  64 x 4: 226;  2 x 32, 128 x 2: 250
+    //                128 rows  4 x 32,  64 x 4: 270;  8 x 16, 64 x 4: 298;  32 x 4: 307
+    //                256 rows  8 x 32,  64 x 4: 501;  32 x 4: 527  (16 sequences of 512 rows)
+    //   of 256:      128 rows  8 x 16,  32 x 4: 280;  64 x 2: 305
 #define NARROW(DT, DP, VW, R, OCC) attend_with(st, k_attend<DT, DP, VW, R, OCC>, a, ATTN_WG, 16 * R, OCC < 2 ? 2 : OCC)
 #define WIDE(DP, R, WR, KB, STAGES) \
     attend_with(st, k_attend_wide<DP, R, WR, KB, STAGES>, a, ATTN_WIDE_WG, 16 * R * WR, 1)
