@@ -1,0 +1,112 @@
+"""Attention over a paged cache at the ends of its ranges: scores so large that one token takes all, windows
+and many entries in every form for many rows, sequences of a quarter of a million tokens.  Bounds are those of
+test_gpu_attn where nothing else is said."""
+import numpy as np
+import pytest
+import torch
+
+import attn_model as model
+from test_gpu_attn import E, HALF, TD, Setup
+
+pytestmark = pytest.mark.gpu
+
+# query heads of a key head, nodes and head sizes: one of each form for more than 16 rows
+WIDE = [(64, 4, 8), (64, 8, 8), (64, 16, 8), (64, 8, 32), (128, 4, 8), (128, 8, 8), (128, 16, 8), (128, 8, 32),
+        (256, 8, 8), (256, 16, 8)]
+
+
+def scores(s, scale):
+    """For each row and head its tokens' places in the pool and their scores, from the definition."""
+    st, out = s.step(), {}
+    kp = s.pools[0][1].reshape(-1, s.Hk, s.D)
+    for i in range(s.n):
+        q, a, m, ln, par = st.entry(i)
+        for t in range(m):
+            at = [st.slot(q, j) for j in [*range(ln), *(ln + b for b in model.sees(par, t))]]
+            for h in range(s.H):
+                out[a + t, h] = at, scale * (kp[at, h // (s.H // s.Hk)] @ s.q64[a + t, h])
+    return out
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("D,group,m", [(64, 2, 7), (128, 4, 3), (256, 1, 9), (64, 4, 8), (128, 8, 8), (128, 8, 32), (256, 8, 8)])
+@pytest.mark.parametrize("scale", [40.0, -40.0])
+def test_one_token_takes_all(dt, D, group, m, scale):
+    """Where one score leads by more than 40, the other weights are below n e^-40, and the result is
+    that token's value: its weight, the same in sum and product but for half a step of bfloat16, and
+    two roundings.  The log-sum-exp is that score: D + 6 roundings of sum |q k| and four of itself."""
+    s = Setup(dt, 2 * group, 2, D, 8, [70, 9, 300], [m, min(m, 5), m], seed=D + m).device()
+    got, lse, status = s.attend(scale)
+    got, lse = got.double().cpu().numpy(), lse.double().cpu().numpy()
+    vp = s.pools[1][1].reshape(-1, 2, D)
+    S = abs(scale) * np.abs(s.q64).sum(2).max() * np.abs(s.pools[0][1]).max()
+    clear = 0
+    for (row, h), (at, x) in scores(s, scale).items():
+        first, second = np.argsort(x)[::-1][:2]
+        if x[first] - x[second] < 40 + 2 * (D + 6) * S * E:
+            continue
+        clear += 1
+        v = vp[at[first], h // group]
+        tol = ((HALF["bf16"] if dt == "bf16" else 0) + HALF[dt] * 1.01 + 8 * E) * np.abs(v) + 1e-14
+        assert np.all(np.abs(got[row, h] - v) <= tol)
+        assert abs(lse[row, h] - x[first]) <= (D + 6) * S * E + 4 * E * abs(x[first])
+    assert status.tolist() == [0, 0, 0] and clear >= (2 * m + min(m, 5)) * 2 * group // 2
+
+
+@pytest.mark.parametrize("D,group,m", WIDE)
+@pytest.mark.parametrize("window", [1, 3, 100, 190, 449])
+def test_windows_in_every_form_for_many_rows(D, group, m, window):
+    """Windows that begin in the nodes, and inside blocks and stages of the cached tokens."""
+    s = Setup("bf16", 2 * group, 2, D, 16, [700, 0, 129], [m, m, max(m - 1, 1)], seed=window)
+    s.device().check_attend(window=window)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("D,group,m", [(64, 4, 8), (128, 8, 8), (256, 16, 5)])
+def test_many_entries_of_many_rows(dt, D, group, m):
+    """More entries than a workgroup has threads, twice over, some of them empty or refused."""
+    r = np.random.RandomState(D)
+    n = 1100
+    s = Setup(dt, group, 1, D, 4, r.randint(0, 25, n).tolist(), r.randint(0, m + 1, n).tolist(), seed=3, max_count=m)
+    s.given["counts"][700] = m + 1
+    s.given["parents"][s.given["starts"][1050] + 1] = 7 if s.given["counts"][1050] > 1 else -5
+    s.device().check_attend()
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("D,group,m,window", [(64, 4, 1, 0), (128, 4, 2, 0), (64, 6, 3, 0), (128, 20, 1, 0), (256, 17, 1, 0),
+                                              (128, 6, 3, 200000)])
+def test_a_quarter_of_a_million_tokens(dt, D, group, m, window):
+    """Tokens all along the sequence, the first and the last among them, hold about half of the weight
+    together, so that none of the parts can be missing.  A term of a sum passes at most n / 256 roundings
+    in its workgroup, which has no more tokens, and 600 in the joining of at most 768 parts, of which a
+    group of lanes adds a quarter or less."""
+    ln, scale = 250001, D ** -0.5
+    s = Setup(dt, group, 1, D, 64, [ln], [m], seed=D, parents=False)
+    st = s.step()
+    q, a = st.entry(0)[0], st.entry(0)[1]
+    # one query for all heads and nodes, but for a little; keys that score log(n / 24) or so with it
+    r = np.random.RandomState(1)
+    u = r.standard_normal(D)
+    s.q = torch.from_numpy((u + 0.05 * r.standard_normal(s.q64.shape)).astype(np.float32)).to(TD[dt])
+    s.q64[:] = s.q.double().numpy()
+    places = [0, 1, 31, 32, 63, 64, 65535, 65536, 99999, 131071, 131072, 180000, 200001, 230017, ln - 33, ln - 32, ln - 2, ln - 1]
+    t, f = s.pools[0]
+    flat, flat64 = t.view(-1, 1, D), f.reshape(-1, 1, D)
+    for j in places:
+        at = st.slot(q, j)
+        flat[at] = torch.from_numpy(u * (np.log(ln / 24.0) + 0.5) / scale / (u @ u)).to(TD[dt])
+        flat64[at] = flat[at].double().numpy()
+    got, lse, status = s.device().attend(scale, window)
+    kp, vp = (p[1].reshape(-1, 1, D) for p in s.pools)
+    rows = np.arange(a, a + m)
+    want, want_lse, _, _, size = model.attend(st, kp, vp, s.q64, scale, window, 1)
+    S = scale * np.abs(s.q64).sum(2).max() * np.abs(kp).max()
+    rel = (2 * (D + 6) * S + 16 + ln / 256 + 600) * E
+    tol = (rel + (HALF["bf16"] if dt == "bf16" else 0)) * size + HALF[dt] * np.abs(want) * 1.01
+    got, lse = got.double().cpu().numpy(), lse.double().cpu().numpy()
+    assert status.tolist() == [0]
+    # what one of the places weighs is far above the bounds
+    assert np.abs(want[rows]).mean() > 6 * tol[rows].mean()
+    assert np.all(np.abs(got - want)[rows] <= tol[rows])
+    assert np.all(np.abs(lse - want_lse)[rows] <= rel + 4 * E * np.abs(want_lse[rows]))
