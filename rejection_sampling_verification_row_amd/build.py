@@ -16,6 +16,7 @@ LIB = os.path.join(PKG, "libspecverify.so")
 SOURCES = [os.path.join(CSRC, f) for f in ("sv_kernels.hip", "sv_filter.hip", "sv_cache.hip",
                                            "sv_attn.hip", "sv_tree.hip", "specverify.cpp")]
 HEADERS = [os.path.join(CSRC, "sv_internal.h"), os.path.join(CSRC, "sv_device.h"), os.path.join(CSRC, "sv_memory.h"),
+           os.path.join(CSRC, "sv_tree.h"),
            os.path.join(INCLUDE, "specverify.h")]
 
 ARCH = "gfx950"

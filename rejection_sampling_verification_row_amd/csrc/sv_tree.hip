@@ -10,6 +10,7 @@
 
 #include "sv_internal.h"
 #include "sv_memory.h"
+#include "sv_tree.h"
 
 namespace sv {
 
@@ -160,7 +161,7 @@ __global__ __launch_bounds__(WG) void k_tree_rows(const char *__restrict__ tgt, 
 // A whole tree: each wave the argmaxes of every TREE_WAVES-th row, then the walk.  Bound by the call for a
 // few short rows (one tree of 8 nodes, 1000 ids: 8.2 us, of which the host's 8), by what a compute unit reads else
 // (256 trees of 64 nodes, 4000 ids, bfloat16: 23 us, 5.7 TB/s; all rows first: 53 us).
-constexpr int TREE_WAVES = 16, TREE_LOADS = 4;
+constexpr int TREE_LOADS = 4;
 template <int DT>
 __global__ __launch_bounds__(64 * TREE_WAVES) void k_tree_short(const char *__restrict__ tgt, const int *tokens,
                                                                 const int *parents, const int *counts, int T, int V,
@@ -219,21 +220,6 @@ __global__ __launch_bounds__(64 * TREE_WAVES) void k_tree_short(const char *__re
     if (lane == 0)
         acc[b] = L;
 }
-
-// What decides between the three, in us, from times of each: all rows are bound by the bytes or by
-// workgroups of which each reads 16 KB or less; depth by depth adds a launch each; in one launch a compute unit reads a
-// tree's rows by itself, a round of TREE_WAVES rows after another.  Calls take TREE_LEAST of the host.
-// Measured, bfloat16 (trees, nodes, ids, depth: all rows, depth by depth, one launch):
-//     1,  8,   1000, 4:  9.5, 21,   8.2      64, 16,   4000, 4: 10.4,   -,  8.3
-//     1, 64,   4000, 8:  9.7, 31,  17.5     256, 64,   1000, 8: 51.9,   -, 12.5
-//    16, 64, 128256, 8: 47.0, 39.3,   -     256, 16,   8000, 4: 20.8,   -, 12.8
-//    32, 64,  32000, 8: 27.8, 39.8,   -     256, 64,   4000, 8: 53.3,   -, 22.9
-//    64,  8, 128256, 4: 27.4, 32.9,   -      64, 16,  16000, 5: 13.4,   -, 16.6
-//    64, 64, 128256, 8: 165,  49.2,   -     256, 16,  32000, 5: 47.5, 40.8,  -
-constexpr double TREE_RATE = 6.5e6, TREE_UNIT_RATE = 4.5e4;       // bytes a us: the card, a compute unit
-constexpr double TREE_GROUP_US = 0.0026;                          // a workgroup among many
-constexpr double TREE_ALL_US = 7.0, TREE_LEVEL_US = 3.3, TREE_SHORT_US = 4.0, TREE_ROUND_US = 1.0;
-constexpr double TREE_LEAST_ALL = 9.5, TREE_LEAST_SHORT = 8.0;
 
 // One depth of every walk, `groups` workgroups to a sequence.  Workgroup (b, c): the node that the walk
 // stands on after the `level` tokens before (from the row that the launch before reduced), and chunk c
@@ -303,15 +289,8 @@ hipError_t launch_greedy_tree(const Launch &ln, const Workspace &ws, int cus, in
                               const int32_t *parents, const int32_t *counts, int32_t *acc_len,
                               int32_t *path, int32_t *out_tokens, unsigned *kinds)
 {
-    const double row = (double)V * (dtype == 1 ? 2 : 4);
-    const int nch = num_chunks(NV_ARGMAX, dtype, V), rounds = (T + TREE_WAVES - 1) / TREE_WAVES;
-    const double us_rows = std::max((double)B * T * row / TREE_RATE, (double)B * T * nch * TREE_GROUP_US);
-    const double us_all = std::max(TREE_ALL_US + us_rows, TREE_LEAST_ALL);
-    const double us_levels = (depth + 2) * TREE_LEVEL_US + (depth + 1) * us_rows / T;
-    const double us_short =
-        std::max(TREE_SHORT_US + rounds * TREE_ROUND_US + (B + cus - 1) / cus * (T * row / TREE_UNIT_RATE),
-                 TREE_LEAST_SHORT);
-    if (us_short < std::min(us_all, us_levels)) {
+    const TreeForm form = tree_form(cus, dtype, B, T, V, depth);
+    if (form == TREE_SHORT) {
         const dim3 threads(64 * std::min(T, TREE_WAVES));
         *kinds = 1u << KIND_GREEDY_EMIT;
         if (dtype == 1)
@@ -323,11 +302,11 @@ hipError_t launch_greedy_tree(const Launch &ln, const Workspace &ws, int cus, in
         return hipGetLastError();
     }
     *kinds = 1u << KIND_ARGMAX | 1u << KIND_GREEDY_EMIT;
-    if (us_levels < us_all)
+    if (form == TREE_LEVELS)
         return (dtype == 1 ? tree_by_levels<1> : tree_by_levels<0>)(ln, ws, B, T, V, depth,
                                                                   static_cast<const char *>(tgt), tokens, parents,
                                                                   counts, acc_len, path, out_tokens);
-    const int np = nch * WAVES;
+    const int nch = num_chunks(NV_ARGMAX, dtype, V), np = nch * WAVES;
     const dim3 chunks((unsigned)((size_t)B * T * nch));
     if (dtype == 1)
         SV_LAUNCH(ln, KIND_ARGMAX, k_tree_rows<1>, chunks, dim3(WG), 0, static_cast<const char *>(tgt), V, nch, ws.part);

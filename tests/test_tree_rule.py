@@ -1,0 +1,80 @@
+"""The rule by which the greedy verify of drafted trees takes one of its three forms: on a card of 256
+compute units, against measured times of all three."""
+import subprocess
+
+import pytest
+
+from rejection_sampling_verification_row_amd import build
+
+RULE = r"""
+#include <cstdio>
+#include "sv_tree.h"
+
+int main()
+{
+    int cus, dtype, B, T, V, depth;
+    while (std::scanf("%d %d %d %d %d %d", &cus, &dtype, &B, &T, &V, &depth) == 6)
+        std::printf("%d\n", (int)sv::tree_form(cus, dtype, B, T, V, depth));
+    return 0;
+}
+"""
+ALL, LEVELS, SHORT = range(3)
+
+
+@pytest.fixture(scope="module")
+def rule(tmp_path_factory):
+    """Forms of shapes (dtype, trees, nodes, ids, depth)."""
+    at = tmp_path_factory.mktemp("rule")
+    src, exe = at / "r.hip", str(at / "r")
+    src.write_text(RULE)
+    subprocess.run([build.hipcc(), "--offload-arch=gfx950", "-std=c++17", "-O1", "-I", build.INCLUDE, "-I", build.CSRC,
+                    str(src), "-o", exe], check=True, capture_output=True)
+
+    def forms(shapes):
+        text = "".join("256 %d %d %d %d %d\n" % s for s in shapes)
+        r = subprocess.run([exe], input=text, capture_output=True, text=True, timeout=60, check=True)
+        return [int(x) for x in r.stdout.split()]
+
+    return forms
+
+
+# (dtype, trees, nodes, ids, depth): us of all rows, depth by depth, one launch; MI355X, drafts accepted 7 in 10
+MEASURED = {
+    (1, 1, 8, 1000, 4): (10.8, 20.0, 7.3), (1, 1, 64, 4000, 8): (10.8, 29.8, 17.3),
+    (1, 16, 64, 128256, 8): (47.0, 41.0, 389.2), (1, 32, 64, 32000, 8): (29.7, 42.6, 104.2),
+    (1, 64, 8, 128256, 4): (27.0, 33.1, 73.0), (1, 64, 64, 128256, 8): (165.2, 49.2, 394.0),
+    (1, 64, 16, 4000, 4): (11.1, 26.2, 7.7), (1, 256, 64, 1000, 8): (53.1, 43.5, 12.3),
+    (1, 256, 16, 8000, 4): (21.1, 28.2, 13.5), (1, 256, 64, 4000, 8): (53.1, 44.5, 22.9),
+    (1, 64, 16, 16000, 5): (15.0, 35.5, 16.8), (1, 256, 16, 32000, 5): (48.1, 40.3, 42.5),
+    (1, 256, 16, 16000, 5): (30.0, 37.3, 23.9), (1, 256, 16, 24000, 5): (37.6, 36.7, 31.9),
+    (1, 256, 8, 32000, 5): (29.7, 40.4, 24.6), (1, 512, 16, 8000, 5): (33.3, 36.5, 22.4),
+    (1, 1024, 8, 4000, 4): (30.1, 34.9, 13.2), (0, 256, 16, 8000, 4): (27.7, 31.4, 22.6),
+    (0, 256, 16, 16000, 5): (45.8, 37.9, 39.5), (0, 64, 16, 32000, 5): (27.1, 34.4, 43.3),
+    (1, 128, 16, 16000, 5): (20.2, 36.5, 17.2), (1, 256, 64, 8000, 8): (56.3, 46.1, 41.4),
+    (1, 9, 64, 2154, 10): (12.0, 41.0, 18.5), (1, 258, 2, 4189, 1): (10.9, 13.9, 7.2),
+    (0, 107, 64, 2080, 6): (19.8, 33.7, 18.3), (1, 134, 4, 94255, 1): (23.9, 21.5, 57.5),
+    (1, 3, 12, 3004, 10): (10.4, 36.5, 7.1), (0, 82, 4, 108509, 3): (27.1, 32.9, 112.7),
+    (1, 10, 48, 45182, 9): (15.6, 43.3, 113.6), (1, 3, 32, 653, 3): (10.8, 18.5, 7.4),
+    (0, 19, 48, 2098, 9): (10.7, 38.4, 15.3), (1, 424, 12, 616, 1): (20.2, 13.3, 7.0),
+    (0, 10, 16, 9385, 2): (10.7, 16.4, 15.9), (0, 32, 12, 98583, 4): (29.3, 30.2, 107.8),
+    (1, 524, 24, 1149, 10): (44.7, 59.1, 15.9), (1, 3, 32, 3378, 9): (10.7, 32.9, 10.3),
+    (1, 18, 24, 2697, 9): (10.8, 40.7, 9.0), (0, 22, 48, 6685, 5): (13.4, 30.5, 30.1),
+    (0, 30, 24, 54976, 2): (29.1, 18.0, 119.6), (0, 71, 16, 12239, 7): (18.1, 39.1, 20.9),
+}
+
+
+def test_the_rule_takes_the_fastest_form(rule):
+    """To 5 percent, by which times differ from run to run."""
+    for form, (shape, us) in zip(rule(MEASURED), MEASURED.items()):
+        assert us[form] <= 1.05 * min(us), (shape, form)
+
+
+def test_shapes_of_the_tests_reach_every_form(rule):
+    """What is compared with the definition is compared in each form."""
+    from test_gpu_tree_levels import SHAPES
+    levels = SHAPES + [(96, 64, 32000, 3)]
+    assert set(rule((dt, *s) for dt in (0, 1) for s in levels)) == {LEVELS}
+    # of test_gpu_tree
+    few, many = [(3, 2, 50, 1), (130, 8, 257, 7)], [(5, 33, 9000, 6), (40, 16, 33000, 5), (9, 64, 20000, 3)]
+    assert set(rule((dt, *s) for dt in (0, 1) for s in few)) == {SHORT}
+    assert set(rule((dt, *s) for dt in (0, 1) for s in many)) == {ALL}
