@@ -69,6 +69,25 @@ def test_the_rule_takes_the_fastest_form(rule):
         assert us[form] <= 1.05 * min(us), (shape, form)
 
 
+# trees whose walk is one row or few, and few rows in all: what a call takes of the host decides, or a wave's rate
+SMALL = {
+    (1, 1, 1, 128256, 0): (10.5, 9.5, 48.6), (1, 1, 8, 1000, 0): (10.5, 9.8, 7.7), (1, 64, 8, 1000, 0): (10.7, 9.6, 7.9),
+    (1, 64, 1, 32000, 0): (10.6, 9.6, 16.7), (1, 1, 8, 128256, 0): (10.5, 9.4, 69.6), (1, 8, 64, 32000, 1): (12.3, 12.5, 102.9),
+    (1, 1, 64, 128256, 1): (10.4, 11.9, 385.4), (1, 4, 64, 128256, 1): (15.3, 12.0, 386.5),
+    (1, 4, 32, 42239, 0): (11.0, 9.7, 78.7), (1, 17, 4, 17112, 1): (10.5, 12.2, 11.9), (1, 3, 1, 1656, 0): (10.5, 9.8, 7.1),
+    (0, 2, 1, 3942, 0): (10.6, 9.7, 7.0), (0, 186, 2, 3334, 0): (10.7, 9.8, 7.1), (0, 187, 2, 2941, 1): (10.8, 12.6, 7.1),
+    (0, 90, 4, 7831, 0): (10.6, 9.7, 11.2), (1, 9, 1, 113746, 0): (10.5, 9.7, 51.1), (0, 1, 12, 1379, 2): (10.4, 14.6, 7.1),
+    (0, 1, 32, 1259, 9): (10.9, 33.0, 8.5), (0, 44, 1, 1942, 0): (10.8, 9.7, 7.3), (1, 16, 24, 919, 2): (10.6, 17.5, 7.2),
+    (1, 13, 12, 2639, 2): (10.7, 17.8, 6.9), (0, 23, 16, 1400, 8): (10.5, 34.6, 7.1), (0, 142, 2, 44741, 0): (12.9, 10.4, 39.2),
+    (1, 8, 12, 118842, 2): (11.0, 17.0, 78.8),
+}
+
+
+def test_small_calls_take_one_launch_where_it_is_faster(rule):
+    for form, (shape, us) in zip(rule(SMALL), SMALL.items()):
+        assert us[form] <= 1.05 * min(us), (shape, form)
+
+
 def test_shapes_of_the_tests_reach_every_form(rule):
     """What is compared with the definition is compared in each form."""
     from test_gpu_tree_levels import SHAPES
