@@ -588,7 +588,8 @@ const char *specverify_strerror(int status);
  * ... are timed (stride 1 = every call).  In a timed call every kernel whose kind k has bit
  * (1 << k) set in `kinds` (0 = every kind) is launched with its start and stop events
  * attached to the dispatch (hipExtLaunchKernel), on the call's stream; its duration is the
- * kernel's own execution.  A timed dispatch costs a few microseconds more than an untimed
+ * kernel's own execution.  The row argmax of a tree verify that reads its rows depth by depth is
+ * several launches, which count as one, from the first one's start to the last one's end.  A timed dispatch costs a few microseconds more than an untimed
  * one, so a stride above 1 keeps the timing out of the rate of a long run of calls.
  * specverify_profile_launches(ctx, kind, ms, cap), between begin and end, synchronises on the
  * events of the timed launches of kernel kind `kind` so far and writes their durations in

@@ -269,12 +269,20 @@ hipError_t tree_by_levels(const Launch &ln, const Workspace &ws, int B, int T, i
 {
     const int nch = num_chunks(NV_ARGMAX, DT, V);
     float2 *half[2] = {ws.part, ws.part + (size_t)B * nch * WAVES};
-    const Launch plain = {ln.stream, nullptr, 0};
+    // the argmax kind is timed from the first depth's start to the last's end
+    const bool time = timed(ln, KIND_ARGMAX);
+    hipEvent_t first[2 * NUM_KINDS] = {}, last[2 * NUM_KINDS] = {};
+    if (time) {
+        first[2 * KIND_ARGMAX] = ln.ev[2 * KIND_ARGMAX];
+        (depth > 0 ? last : first)[2 * KIND_ARGMAX + 1] = ln.ev[2 * KIND_ARGMAX + 1];
+    }
+    const Launch plain = {ln.stream, nullptr, 0}, begin = {ln.stream, time ? first : nullptr, ln.mask},
+                 finish = {ln.stream, time ? last : nullptr, ln.mask};
     for (int level = 0; level <= depth + 1; ++level) {
         // the last one finishes the walks that went all the way down
         const bool end = level > depth;
         const int groups = end ? 1 : nch;
-        const Launch &l = level == 0 || end ? ln : plain;
+        const Launch &l = end ? ln : level == 0 ? begin : level == depth ? finish : plain;
         SV_LAUNCH(l, end ? KIND_GREEDY_EMIT : KIND_ARGMAX, k_tree_level<DT>, dim3((unsigned)((size_t)B * groups)),
                   dim3(WG), 0, tgt, tokens, parents, counts, T, V, depth, level, groups, nch, half[(level + 1) & 1],
                   half[level & 1], acc, path, out);

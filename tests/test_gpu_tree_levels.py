@@ -131,3 +131,34 @@ def test_the_start_of_a_chain_is_the_greedy_verify(dtype):
     assert acc2.tolist() == acc and torch.equal(acc2, acc3) and torch.equal(out2, out3)
     sv.specverify_destroy(ctx)
     sv.specverify_destroy(ctx3)
+
+
+@pytest.mark.parametrize("dtype", [0, 1])
+def test_timing_spans_every_depth(dtype):
+    """The timed launches of the argmax kind: one for a call, from the first depth's start to the last's
+    end.  All walks go down to the end, so that 13 depths, which wait for one another, take several
+    times what one does; and all of the call takes longer than they do."""
+    r = np.random.RandomState(14)
+    B, T, V = 192, 64, 32000
+    x, tok, par = forest(r, B, T, V, dtype, 1.0, far=0.0)
+    ctx = sv.specverify_create(0, B, T - 1, V)
+    us = {}
+    for depth in (0, 12):
+        acc, path, out = (torch.empty(s, **I32) for s in ((B,), (B, depth + 1), (B, depth + 1)))
+        args = (ctx, None, dtype, B, T, V, depth, x, dev(tok), dev(par), None, acc, path, out)
+        for _ in range(3):
+            sv.specverify_run_greedy_tree(*args)
+        sv.specverify_profile_begin(ctx, 8, ["row_argmax", "greedy_emit"])
+        begin, end = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+        begin.record()
+        for _ in range(8):
+            sv.specverify_run_greedy_tree(*args)
+        end.record()
+        ms = sv.specverify_profile_launches(ctx, "row_argmax")
+        emit = sv.specverify_profile_launches(ctx, "greedy_emit")
+        sv.specverify_profile_end(ctx)
+        assert len(ms) == len(emit) == 8 and min(ms) > 0 and acc.min().item() == depth
+        assert sum(ms) + sum(emit) <= begin.elapsed_time(end) * 1.05
+        us[depth] = sorted(ms)[4] * 1e3
+    assert us[12] >= 4 * us[0], us
+    sv.specverify_destroy(ctx)
