@@ -45,6 +45,9 @@ constexpr float LN2 = 0.6931471805599453f;
 // How far, in powers of 2, scores may exceed the running maximum before k_attend_wide lets it follow:
 // weights up to 2^8 lose nothing in fp32 sums or in bfloat16, and most rows' maxima need to follow once.
 constexpr float LAG = 8.0f;
+// Raw scores from FAR / c1 on would pass fp32 once they are in powers of 2; weights are then formed from
+// differences of raw scores.  What waves and parts hand on of their maxima is a quarter, which any score's is in fp32.
+constexpr float FAR = 3e38f, QUARTER = 0.25f;
 
 __device__ inline bool in_range(int i, int n) { return (unsigned)i < (unsigned)n; }
 
@@ -136,6 +139,7 @@ struct AttnArgs {
     NodesView nv;
     int key_pool, value_pool;
     float c1;            // |scale| log2(e), 1 for scale 0
+    float far;           // FAR / c1
     float q_sign;        // the queries' factor: scale's sign
     int window;
     const char *q;
@@ -465,27 +469,52 @@ __device__ inline void follow(const f32x4 (&s)[R][SUB], f32x4 (&o)[R][NT], float
     }
 }
 
-// Scores of a tile become weights against the maxima, and are summed.
-template <int SUB, int R>
-__device__ inline void weigh(f32x4 (&s)[R][SUB], const float (&m)[R], float (&l)[R], float c1)
+// Whether a maximum is FAR, though not of nothing.
+template <int R> __device__ inline bool any_far(const float (&m)[R], float far)
+{
+    bool any = false;
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+        any |= !(fabsf(m[r]) < far) && m[r] != -INFINITY;
+    return __ballot(any) != 0;
+}
+
+// Scores of a tile become weights against the maxima, and are summed.  DIFF: maxima may be FAR; else rows of such
+// have no scores here but -inf and NaN.
+template <bool DIFF, int SUB, int R>
+__device__ inline void weigh(f32x4 (&s)[R][SUB], const float (&m)[R], float (&l)[R], float c1, float far)
 {
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-        const float ref = m[r] == -INFINITY ? 0.0f : m[r] * c1;
+        const float ref = DIFF ? (m[r] == -INFINITY ? 0.0f : m[r]) : fabsf(m[r]) < far ? m[r] * c1 : 0.0f;
         float sum[SUB];
 #pragma unroll
         for (int x = 0; x < SUB; ++x) {
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                s[r][x][i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[r][x][i], c1, -ref));
+                s[r][x][i] = __builtin_amdgcn_exp2f(DIFF ? (s[r][x][i] - ref) * c1
+                                                         : __builtin_fmaf(s[r][x][i], c1, -ref));
             sum[x] = (s[r][x][0] + s[r][x][1]) + (s[r][x][2] + s[r][x][3]);
         }
         l[r] += SUB == 2 ? sum[0] + sum[SUB - 1] : sum[0];
     }
 }
 
+// What sums under a maximum count under a higher one, of quarters; the log of a whole sum.
+__device__ inline float scale_down(float was, float top)
+{
+    return was == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f((was - top) / QUARTER);
+}
+__device__ inline float log_sum(float top, float z)
+{
+    const float whole = top / QUARTER;
+    if (fabsf(whole) == INFINITY && fabsf(top) < INFINITY)
+        return top * (LN2 / QUARTER);          // beside which log z is nothing
+    return z == 0.0f ? -INFINITY : (whole + log2f(z)) * LN2;
+}
+
 // The sums of `waves` waves over a tile of rows, joined, to the output or to the kept ones: row i at
-// o[wave * wave_step + i], its maximum and sum at ml of the same index.
+// o[wave * wave_step + i], its maximum (a quarter) and sum at ml of the same index.
 template <int DT, int WG_SIZE, int PITCH>
 __device__ inline void finish(const AttnArgs &a, const Job &j, int rows_per_tile, const float (*o)[PITCH],
                               const float2 *ml, int waves, int wave_step)
@@ -501,7 +530,7 @@ __device__ inline void finish(const AttnArgs &a, const Job &j, int rows_per_tile
         float z = 0.0f, acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
         for (int k = 0; k < waves; ++k) {
             const float2 p = ml[k * wave_step + row];
-            const float f = p.x == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(p.x - top);
+            const float f = scale_down(p.x, top);
             z += f * p.y;
             const float4 v = *reinterpret_cast<const float4 *>(&o[k * wave_step + row][d]);
             acc[0] += f * v.x;
@@ -527,8 +556,7 @@ __device__ inline void finish(const AttnArgs &a, const Job &j, int rows_per_tile
                 reinterpret_cast<float *>(to)[x] = v;
         }
         if (a.lse && d == 0)
-            a.lse[(int64_t)(j.e.start + node) * a.a.q_heads + qh] =
-                z == 0.0f ? -INFINITY : (top + log2f(z)) * LN2;
+            a.lse[(int64_t)(j.e.start + node) * a.a.q_heads + qh] = log_sum(top, z);
     }
 }
 
@@ -644,6 +672,7 @@ __global__ __launch_bounds__(ATTN_WG, OCC) void k_attend(AttnArgs args)
                 o[r][i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
         }
 
+        bool far = false;
         int t = t0 + w, buf = 0, next_page = 0;
         const int last = t1 - 1 - (t1 - 1 - t & 3);          // this wave's last tile
         uint32_t lost = 0;
@@ -695,9 +724,14 @@ __global__ __launch_bounds__(ATTN_WG, OCC) void k_attend(AttnArgs args)
 #pragma unroll
             for (int r = 0; r < R; ++r)
                 grew |= tile_max<SUB>(s[r]) > m[r];
-            if (__ballot(grew) != 0)
+            if (__ballot(grew) != 0) {
                 follow<SUB, NT, R>(s, o, m, l, a.c1);
-            weigh<SUB, R>(s, m, l, a.c1);
+                far = any_far<R>(m, a.far);
+            }
+            if (far)
+                weigh<true, SUB, R>(s, m, l, a.c1, a.far);
+            else
+                weigh<false, SUB, R>(s, m, l, a.c1, a.far);
             if (masked) {
                 // What a row does not see may be anything: rows of values with an infinity or a NaN are left
                 // out of the product and added to the rows that see them, one by one.
@@ -796,7 +830,7 @@ __global__ __launch_bounds__(ATTN_WG, OCC) void k_attend(AttnArgs args)
             const float sum = row_sum(l[r]);
             const int at = w * ROWS + r * 16 + col;
             if (grp == 0)
-                s_ml[at] = make_float2(m[r] == -INFINITY ? -INFINITY : m[r] * a.c1, sum);
+                s_ml[at] = make_float2(m[r] == -INFINITY ? -INFINITY : m[r] * (a.c1 * QUARTER), sum);
 #pragma unroll
             for (int b = 0; b < NB; ++b)
 #pragma unroll
@@ -1060,7 +1094,7 @@ __global__ __launch_bounds__(ATTN_WIDE_WG, 1) void k_attend_wide(AttnArgs a)
                     __builtin_amdgcn_sched_barrier(0);
             }
         };
-        // A block that some row does not see all of, or whose maximum the running one must follow.
+        // A block that some row does not see all of, or whose maximum the running one must follow, or whose is FAR.
         auto slow_block = [&](int block_at, int j0, uint32_t lost) {
             score();
             uint32_t odd = 0;
@@ -1087,7 +1121,10 @@ __global__ __launch_bounds__(ATTN_WIDE_WG, 1) void k_attend_wide(AttnArgs a)
                         sc[r][x][y] = vis[r] >> (grp * 4) & (1u << (x * 16 + y)) ? sc[r][x][y] : -INFINITY;
             }
             follow<2, NT, R>(sc, o, m, l, a.c1);
-            weigh<2, R>(sc, m, l, a.c1);
+            if (any_far<R>(m, a.far))
+                weigh<true, 2, R>(sc, m, l, a.c1, a.far);
+            else
+                weigh<false, 2, R>(sc, m, l, a.c1, a.far);
 #pragma unroll 1
             for (uint32_t left = odd; left != 0; left &= left - 1) {
                 const int key = __builtin_ctz(left);
@@ -1145,7 +1182,7 @@ __global__ __launch_bounds__(ATTN_WIDE_WG, 1) void k_attend_wide(AttnArgs a)
                 bool grew = uniform(lost_here) != 0;
 #pragma unroll
                 for (int r = 0; r < R; ++r)
-                    grew |= tile_max<2>(sc[r]) > (m[r] == -INFINITY ? m[r] : m[r] + slack);
+                    grew |= tile_max<2>(sc[r]) > (fabsf(m[r]) < a.far ? m[r] + slack : -INFINITY);
                 if (__ballot(grew) != 0)
                     break;
                 if (SHIFT && late && kb == KB - 1 && i + 1 < stages) {
@@ -1154,7 +1191,7 @@ __global__ __launch_bounds__(ATTN_WIDE_WG, 1) void k_attend_wide(AttnArgs a)
                 }
                 if constexpr (SHIFT)
                     read_early(block_at);
-                weigh<2, R>(sc, m, l, a.c1);
+                weigh<false, 2, R>(sc, m, l, a.c1, a.far);
                 add_values(std::true_type(), block_at, 0);
             }
             if (b < blocks && (unsigned)j0 < (unsigned)total) {
@@ -1170,7 +1207,7 @@ __global__ __launch_bounds__(ATTN_WIDE_WG, 1) void k_attend_wide(AttnArgs a)
             const float sum = row_sum(l[r]);
             const int at = w * 16 * R + r * 16 + col;
             if (grp == 0)
-                s_ml[at] = make_float2(m[r] == -INFINITY ? -INFINITY : m[r] * a.c1, sum);
+                s_ml[at] = make_float2(m[r] == -INFINITY ? -INFINITY : m[r] * (a.c1 * QUARTER), sum);
 #pragma unroll
             for (int x = 0; x < NT; ++x)
                 *reinterpret_cast<f32x4 *>(&s_o[at][x * 16 + grp * 4]) = o[r][x];
@@ -1233,13 +1270,13 @@ __global__ __launch_bounds__(ATTN_WG) void k_attend_join(AttnArgs a, int rows_pe
 #pragma unroll
         for (int c = 0; c < 8; ++c)
             top = fmaxf(top, ml[c].x);
-        const float old = was == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(was - top);
+        const float old = scale_down(was, top);
         z *= old;
         acc *= old;
 #pragma unroll
         for (int c = 0; c < 8; ++c)
             if (c0 + c * STEP < parts) {
-                const float f = ml[c].x == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(ml[c].x - top);
+                const float f = scale_down(ml[c].x, top);
                 z += f * ml[c].y;
                 acc += f * v[c];
             }
@@ -1257,7 +1294,7 @@ __global__ __launch_bounds__(ATTN_WG) void k_attend_join(AttnArgs a, int rows_pe
         acc = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
         for (int g = 0; g < min(parts, GROUPS); ++g) {
             const float2 ml = s_ml[g];
-            const float f = ml.x == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(ml.x - top);
+            const float f = scale_down(ml.x, top);
             z += f * ml.y;
             acc += f * s_acc[g][lane];
         }
@@ -1274,7 +1311,7 @@ __global__ __launch_bounds__(ATTN_WG) void k_attend_join(AttnArgs a, int rows_pe
             reinterpret_cast<float *>(to)[x] = o;
     }
     if (a.lse && lane == 0)
-        a.lse[(int64_t)(p.start + node) * a.a.q_heads + qh] = z == 0.0f ? -INFINITY : (top + log2f(z)) * LN2;
+        a.lse[(int64_t)(p.start + node) * a.a.q_heads + qh] = log_sum(top, z);
 }
 
 template <int LG> void join_with(hipStream_t st, bool bf16, const AttnArgs &a, int rows, int64_t joined)
@@ -1320,7 +1357,8 @@ hipError_t launch_attend(hipStream_t st, const CacheView &c, const AttnShape &s,
                          int64_t q_stride, void *out, int64_t out_stride, float *lse, int *status)
 {
     const int D = s.head_dim, M = nodes.max_count * s.group, es = s.dtype == 1 ? 2 : 4;
-    AttnArgs a = {c, s, nodes, key_pool, value_pool, scale == 0.0f ? 1.0f : fabsf(scale) * LOG2E,
+    const float c1 = scale == 0.0f ? 1.0f : fabsf(scale) * LOG2E;
+    AttnArgs a = {c, s, nodes, key_pool, value_pool, c1, FAR / c1,
                   scale > 0.0f ? 1.0f : scale < 0.0f ? -1.0f : 0.0f, window, static_cast<const char *>(q),
                   q_stride * es, static_cast<char *>(out), out_stride * es, lse, status, 0};
     // Forms with tiles of as many rows as there are, or the largest.  Up to 16 rows k_attend begins and ends

@@ -334,7 +334,7 @@ struct AttnShape {
     AttnPlan *plan;      // [max_entries]
     int *sound;          // [max_entries] the parents are; written by the entry's first workgroup
     double *share;       // tiles to a workgroup
-    float2 *part_ml;     // [2 workgroups][rows of a tile] maximum (times scale, in powers of 2) and sum
+    float2 *part_ml;     // [2 workgroups][rows of a tile] maximum (times scale, in powers of 16) and sum
     float *part_o;       // [2 workgroups][rows of a tile][head_dim] sums of weighted values
 };
 

@@ -110,3 +110,40 @@ def test_a_quarter_of_a_million_tokens(dt, D, group, m, window):
     assert np.abs(want[rows]).mean() > 6 * tol[rows].mean()
     assert np.all(np.abs(got - want)[rows] <= tol[rows])
     assert np.all(np.abs(lse - want_lse)[rows] <= rel + 4 * E * np.abs(want_lse[rows]))
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("D,group,m", [(64, 2, 7), (128, 4, 3), (256, 1, 9), (64, 4, 8), (128, 8, 8), (128, 8, 32), (256, 8, 8)])
+def test_scores_at_the_ends_of_the_range(dt, D, group, m):
+    """Keys with the type's lowest value, whose scores of -3.4e38 pass fp32 times log2 e: they have no
+    weight, also where they come first, and a row of nothing else is a mean.  A token whose score is as far
+    above 0 takes all.  Log-sum-exps as large are off by six roundings, and may round to infinity."""
+    s = Setup(dt, 2 * group, 2, D, 8, [300, 40, 90], [m, min(m, 4), m], seed=D + m)
+    st, top = s.step(), torch.finfo(TD[dt]).max
+    s.q[:, :, 0] = 1.0
+    s.q64[:, :, 0] = 1.0
+    t, f = s.pools[0]
+    flat, flat64 = t.view(-1, 2, D), f.reshape(-1, 2, D)
+    places = [(0, j) for j in range(150)] + [(1, j) for j in range(40 + min(m, 4))]
+    last = st.entry(2)[2] - 1                        # a leaf
+    for i, j in places + [(2, 90 + last)]:
+        at = st.slot(st.entry(i)[0], j)
+        flat[at, :, 0] = top if i == 2 else -top
+        flat64[at, :, 0] = float(top if i == 2 else -top)
+    got, lse, status = s.device().attend(1.0)
+    kp, vp = (p[1].reshape(-1, 2, D) for p in s.pools)
+    with np.errstate(over="ignore"):
+        want, want_lse, _, _, size = model.attend(st, kp, vp, s.q64, 1.0, 0, 2)
+    got, lse = got.double().cpu().numpy(), lse.double().cpu().numpy()
+    S = np.abs(s.q64).sum(2).max() * np.abs(kp[np.abs(kp) < 1e30]).max()
+    rel = (2 * (D + 6) * S + 16 + 400) * E
+    tol = (rel + (HALF["bf16"] if dt == "bf16" else 0)) * size + HALF[dt] * np.abs(want) * 1.01
+    a0, a1, a2 = (st.entry(i)[1] for i in range(3))
+    assert status.tolist() == [0, 0, 0]
+    rows = [a + x for a, c in ((a0, m), (a1, min(m, 4)), (a2, m)) for x in range(c)]
+    assert np.all(np.abs(got - want)[rows] <= tol[rows])
+    a, b = lse[rows], want_lse[rows]
+    past = np.isinf(a) & (np.sign(a) == np.sign(b)) & (np.abs(b) * (1 + 6 * E) > np.finfo(np.float32).max)
+    assert np.abs(want_lse[a1]).min() > 3e38 and np.abs(want_lse[a2 + last]).min() > 3e38
+    with np.errstate(invalid="ignore"):
+        assert np.all(past | (np.abs(a - b) <= rel + 6 * E * np.abs(b)))
