@@ -1099,7 +1099,7 @@ __global__ __launch_bounds__(ATTN_WIDE_WG, 1) void k_attend_wide(AttnArgs a)
             score();
             uint32_t odd = 0;
             // as in k_attend: rows of values with an infinity or a NaN are added one by one
-            if (j0 + 32 > len || lost != 0 || j0 < low_most) {
+            if ((unsigned)j0 + 32 > (unsigned)len || lost != 0 || j0 < low_most) {
 #pragma unroll 1
                 for (int x = 0; x < 32 * PIECES / 64; ++x) {
                     const int p = x * 64 + lane, row = p / PIECES;
@@ -1171,7 +1171,7 @@ __global__ __launch_bounds__(ATTN_WIDE_WG, 1) void k_attend_wide(AttnArgs a)
                     begin_stage(i);
                 }
                 const int b0 = (kg * KB + kb) * 32;
-                j0 = (t0 + i) * TK + b0;
+                j0 = (int)((unsigned)(t0 + i) * TK + b0);
                 block_at = i % STAGES * 2 * HALF + b0 * ROW;
                 if (b >= blocks || (unsigned)j0 + 32 > (unsigned)len || j0 < low_most)
                     break;

@@ -147,3 +147,42 @@ def test_scores_at_the_ends_of_the_range(dt, D, group, m):
     assert np.abs(want_lse[a1]).min() > 3e38 and np.abs(want_lse[a2 + last]).min() > 3e38
     with np.errstate(invalid="ignore"):
         assert np.all(past | (np.abs(a - b) <= rel + 6 * E * np.abs(b)))
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("group,m", [(2, 6), (2, 30), (8, 33)])
+def test_the_last_places_that_a_cache_can_have(dt, group, m):
+    """A sequence up to place 2^31 - 3, of which a window is seen: blocks of 32 tokens end at 2^31.  What
+    siblings do not see there is NaN."""
+    pt, blocks, D = 2718, 790097, 8                  # 2^31 - 2 tokens
+    s = Setup(dt, group, 1, D, pt, [0], [m], seed=m)
+    q = s.given["seqs"][0]
+    s.mb = blocks
+    tables = np.full((len(s.blocks), blocks), -1, np.int32)
+    tables[q] = 0
+    # the places of the nodes and of the window have a page of their own
+    tables[q, -1] = s.tables[q, 0]
+    tables[q, :-1] = (s.tables[q, 0] + 1) % s.P
+    s.tables, s.blocks[q], s.lengths[q] = tables, blocks, pt * blocks - m
+    st = s.step()
+    ln, a = pt * blocks - m, s.given["starts"][0]
+    par = s.given["parents"]
+    par[a + m - 2] = par[a + m - 1] = 0              # two leaves
+    for x in (m - 2, m - 1):
+        at = st.slot(q, ln + x)
+        for t, f in s.pools:
+            f.reshape(-1, 1, D)[at] = np.nan
+            t.view(-1, 1, D)[at] = float("nan")
+    window = 50
+    got, lse, status = s.device().attend(0.3, window)
+    kp, vp = (p[1].reshape(-1, 1, D) for p in s.pools)
+    want, want_lse, _, rows, size = model.attend(st, kp, vp, s.q64, 0.3, window, 1)
+    got, lse = got.double().cpu().numpy(), lse.double().cpu().numpy()
+    assert status.tolist() == [0]
+    clean = [r for r in rows if r < a + m - 2]
+    assert np.isnan(got[a + m - 2:a + m]).all() and not np.isnan(want[clean]).any()
+    S = 0.3 * np.abs(s.q64).sum(2).max() * np.nanmax(np.abs(kp))
+    rel = (2 * (D + 6) * S + 16 + window + m) * E
+    tol = (rel + (HALF["bf16"] if dt == "bf16" else 0)) * size + HALF[dt] * np.abs(want) * 1.01
+    assert np.all(np.abs(got - want)[clean] <= tol[clean])
+    assert np.all(np.abs(lse - want_lse)[clean] <= rel + 4 * E * np.abs(want_lse[clean]))
