@@ -541,6 +541,7 @@ int specverify_attn_append(specverify_attn *attn, void *hip_stream, int key_pool
  * Attention of the nodes over the cached tokens of their sequence, their ancestors and themselves,
  * whose keys and values have to be in place: with s_j = scale * <q, k_j> over the tokens seen,
  * out = sum_j exp(s_j) v_j / sum_j exp(s_j) and lse (or NULL) [rows][q_heads] = log sum_j exp(s_j).
+ * For scale 0 queries count as 0, whatever their values.
  * window > 0: a token is seen only from positions less than `window` after its own.  Tokens whose
  * page is out of range are not seen; a row that sees nothing, or nothing above -inf, gets zeros and
  * -inf.  What a row does not see does not touch it, whatever its values.

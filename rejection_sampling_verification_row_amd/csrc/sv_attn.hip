@@ -9,7 +9,9 @@
 // One pass over the tokens: m is a running maximum, and what was summed under an older one is scaled
 // by exp(old - new).  Scores, maxima and sums are fp32, and so is the product with the values, whose
 // right side, the weights, is rounded to bfloat16 in bfloat16 pools: a weight is off by at most 2^-8 of
-// itself, as the values and the output already are.  exp is computed as a power of 2.
+// itself, as the values and the output already are.  (Over whole outputs of random rows the mean square error relative
+// to theirs is 2.1e-3 to 2.4e-3, of which the output's own rounding is 1.66e-3; weights in fp32 would take
+// matrix instructions at a ninth of the rate, or twice as many.)  exp is computed as a power of 2.
 //
 // All rows of a key head and an entry read the same keys, so that they are the columns of one matrix:
 // S^T = K Q^T, then O^T = V^T P^T.  In the accumulator layout of a 16x16 matrix instruction a lane then
@@ -1367,13 +1369,14 @@ hipError_t launch_attend(hipStream_t st, const CacheView &c, const AttnShape &s,
     // 64 sequences of 50 to 400 tokens 30 and 37, of 300 to 2000 72 and 72, of 300 to 8200 211 and 197; the
     // last with heads of 64 224 and 194, of 80 198 and 203, of 256 203 and 224.
     // k_attend has as many workgroups on a compute unit as its registers allow (float32 heads of 64, when it
-    // was chosen: 3, 70 us; 2, 79 us; 4, 100 us for spills); float32 has no other form, since its matrix
-    // instructions are 8 times slower than the bfloat16 ones and decide.
+    // was chosen: 3, 70 us; 2, 79 us; 4, 100 us for spills).  Float32 has no other form: 16 sequences of 1000 to 5000
+    // tokens, 4 key heads of 128, 32, 64, 128 and 512 rows: 78, 115, 187 and 598 us, where its matrix
+    // instructions alone take 19, 38, 75 and 300 and the bytes 40; every 32 rows (16 of heads of 256) read them again.
     // k_attend_wide has what its registers and 160 KB of LDS allow, and of that the fastest, in us for 64
     // sequences of 300 to 8200 tokens (waves over the rows x rows of a wave, tokens x number of stages):
     //   heads of 64:  32 rows  2 x 16, 128 x 4: 206;  x 2: 229
-    //                 64 rows  2 x 32, 128 x 4: 232;  4 x 16, 64 x 4: 248
-    //                128 rows  4 x 32, 128 x 4: 311;  64 x 4: 342;  8 x 16, 64 x 4: 407
+    //                 64 rows  2 x 32, 128 x 4: 236;  4 x 16, 64 x 4: 248
+    //                128 rows  4 x 32, 128 x 4: 318;  64 x 4: 342;  8 x 16, 64 x 4: 407
     //                256 rows  8 x 32, 128 x 4: 271;  64 x 4: 288  (half the heads)
     //   of 128:       64 rows  4 x 16,  64 x 4: 226;  2 x 32, 128 x 2: 250
     //                128 rows  4 x 32,  64 x 4: 270;  8 x 16, 64 x 4: 298;  32 x 4: 307
@@ -1490,7 +1493,8 @@ template <int DT, bool VEC> __device__ inline void copy_piece(char *to, const ch
 //
 // Bound by memory, a few tokens by the call: 13800 tokens of 32 query and 8 key heads of 128 in
 // bfloat16: 76.5 us, 4.4 TB/s read and written (a large copy 5.0); 2112 tokens in 256 entries 12.7 us; one
-// 8.3 us.  Four tokens to a workgroup: with 2 it is 78.7 us, with 8 83.8, with 16 101.
+// 8.3 us.  Four tokens to a workgroup: with 2 it is 78.7 us, with 8 83.8, with 16 101.  Without VEC it is bound by
+// its loads of one element: heads of 80, 13800 tokens, 80 rotated dimensions 50.5 us, 40 and 20 130 and 142.
 template <int DT, bool VEC, bool INTER>
 __global__ __launch_bounds__(ATTN_WG) void k_append(AppendArgs a)
 {

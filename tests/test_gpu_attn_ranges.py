@@ -186,3 +186,13 @@ def test_the_last_places_that_a_cache_can_have(dt, group, m):
     tol = (rel + (HALF["bf16"] if dt == "bf16" else 0)) * size + HALF[dt] * np.abs(want) * 1.01
     assert np.all(np.abs(got - want)[clean] <= tol[clean])
     assert np.all(np.abs(lse - want_lse)[clean] <= rel + 4 * E * np.abs(want_lse[clean]))
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("D,group,m", [(64, 2, 7), (128, 8, 8)])
+def test_scale_zero_takes_the_mean_whatever_the_queries(dt, D, group, m):
+    s = Setup(dt, 2 * group, 2, D, 8, [300, 9], [m, 3], seed=D)
+    s.q[::2] = float("inf")
+    s.q[1::3] = float("nan")
+    s.q64[:] = 0.0
+    s.device().check_attend(scale=0.0)
