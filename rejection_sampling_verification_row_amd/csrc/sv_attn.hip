@@ -10,7 +10,7 @@
 // by exp(old - new).  Scores, maxima and sums are fp32, and so is the product with the values, whose
 // right side, the weights, is rounded to bfloat16 in bfloat16 pools: a weight is off by at most 2^-8 of
 // itself, as the values and the output already are.  (Over whole outputs of random rows the mean square error relative
-// to theirs is 2.1e-3 to 2.4e-3, of which the output's own rounding is 1.66e-3; weights in fp32 would take
+// to theirs is 2.0e-3 to 2.4e-3, of which the output's own rounding is 1.66e-3; weights in fp32 would take
 // matrix instructions at a ninth of the rate, or twice as many.)  exp is computed as a power of 2.
 //
 // All rows of a key head and an entry read the same keys, so that they are the columns of one matrix:
@@ -892,8 +892,8 @@ __device__ inline void load_to_lds4(const void *from, uint32_t to)
 // 120 others with 16 exponentials (about 630 cycles), which overlap only if the two waves of a SIMD do
 // different things.  So with four stages the upper half of the waves meets the stage's barrier between
 // its scores and its weights, when the lower half begins with scores, and matrix instructions have
-// priority (531 -> 520 us): 16 sequences of 64 nodes, 64 query and 8 key heads, 8000 to 16000 tokens: 501 us,
-// 739 TFLOP/s, where a large library product reaches 1352 TFLOP/s.  The matrix units are busy 36% of the time;
+// priority (531 -> 520 us): 16 sequences of 64 nodes, 64 query and 8 key heads, 8000 to 16000 tokens: 505 us,
+// 733 TFLOP/s, where a large library product reaches 1352 TFLOP/s.  The matrix units are busy 36% of the time;
 // waves wait for barriers and LDS 29% of theirs and for their turn to issue 27%.  Not kept: the next block's
 // keys read, or its scores computed, before the weights of this one (no registers are left, 2 times slower).
 //
