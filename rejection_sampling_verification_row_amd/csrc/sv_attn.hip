@@ -44,8 +44,10 @@ typedef short s16x4 __attribute__((ext_vector_type(4)));
 
 constexpr float LOG2E = 1.4426950408889634f;
 constexpr float LN2 = 0.6931471805599453f;
-// How far, in powers of 2, scores may exceed the running maximum before k_attend_wide lets it follow:
-// weights up to 2^8 lose nothing in fp32 sums or in bfloat16, and most rows' maxima need to follow once.
+// How far, in powers of 2, scores may exceed the running maximum before k_attend_wide lets it follow: most
+// rows' maxima need to follow once.  It weighs against a reference as much above the maximum, so that no
+// weight is above 1 and sums pass fp32 only where values do; weights of 2^-8 where 1 would stand lose nothing.
+// (512 rows of heads of 128 505 -> 510 us; the others alike.)
 constexpr float LAG = 8.0f;
 // Raw scores from FAR / c1 on would pass fp32 once they are in powers of 2; weights are then formed from
 // differences of raw scores.  What waves and parts hand on of their maxima is a quarter, which any score's is in fp32.
@@ -481,20 +483,21 @@ template <int R> __device__ inline bool any_far(const float (&m)[R], float far)
     return __ballot(any) != 0;
 }
 
-// Scores of a tile become weights against the maxima, and are summed.  DIFF: maxima may be FAR; else rows of such
-// have no scores here but -inf and NaN.
+// Scores of a tile become weights against what is `above` the maxima in powers of 2, and are summed.  DIFF: maxima
+// may be FAR; else rows of such have no scores here but -inf and NaN.
 template <bool DIFF, int SUB, int R>
-__device__ inline void weigh(f32x4 (&s)[R][SUB], const float (&m)[R], float (&l)[R], float c1, float far)
+__device__ inline void weigh(f32x4 (&s)[R][SUB], const float (&m)[R], float (&l)[R], float c1, float far,
+                             float above)
 {
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-        const float ref = DIFF ? (m[r] == -INFINITY ? 0.0f : m[r]) : fabsf(m[r]) < far ? m[r] * c1 : 0.0f;
+        const float ref = DIFF ? (m[r] == -INFINITY ? 0.0f : m[r]) : fabsf(m[r]) < far ? m[r] * c1 + above : 0.0f;
         float sum[SUB];
 #pragma unroll
         for (int x = 0; x < SUB; ++x) {
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                s[r][x][i] = __builtin_amdgcn_exp2f(DIFF ? (s[r][x][i] - ref) * c1
+                s[r][x][i] = __builtin_amdgcn_exp2f(DIFF ? __builtin_fmaf(s[r][x][i] - ref, c1, -above)
                                                          : __builtin_fmaf(s[r][x][i], c1, -ref));
             sum[x] = (s[r][x][0] + s[r][x][1]) + (s[r][x][2] + s[r][x][3]);
         }
@@ -731,9 +734,9 @@ __global__ __launch_bounds__(ATTN_WG, OCC) void k_attend(AttnArgs args)
                 far = any_far<R>(m, a.far);
             }
             if (far)
-                weigh<true, SUB, R>(s, m, l, a.c1, a.far);
+                weigh<true, SUB, R>(s, m, l, a.c1, a.far, 0.0f);
             else
-                weigh<false, SUB, R>(s, m, l, a.c1, a.far);
+                weigh<false, SUB, R>(s, m, l, a.c1, a.far, 0.0f);
             if (masked) {
                 // What a row does not see may be anything: rows of values with an infinity or a NaN are left
                 // out of the product and added to the rows that see them, one by one.
@@ -1124,9 +1127,9 @@ __global__ __launch_bounds__(ATTN_WIDE_WG, 1) void k_attend_wide(AttnArgs a)
             }
             follow<2, NT, R>(sc, o, m, l, a.c1);
             if (any_far<R>(m, a.far))
-                weigh<true, 2, R>(sc, m, l, a.c1, a.far);
+                weigh<true, 2, R>(sc, m, l, a.c1, a.far, LAG);
             else
-                weigh<false, 2, R>(sc, m, l, a.c1, a.far);
+                weigh<false, 2, R>(sc, m, l, a.c1, a.far, LAG);
 #pragma unroll 1
             for (uint32_t left = odd; left != 0; left &= left - 1) {
                 const int key = __builtin_ctz(left);
@@ -1193,7 +1196,7 @@ __global__ __launch_bounds__(ATTN_WIDE_WG, 1) void k_attend_wide(AttnArgs a)
                 }
                 if constexpr (SHIFT)
                     read_early(block_at);
-                weigh<false, 2, R>(sc, m, l, a.c1, a.far);
+                weigh<false, 2, R>(sc, m, l, a.c1, a.far, LAG);
                 add_values(std::true_type(), block_at, 0);
             }
             if (b < blocks && (unsigned)j0 < (unsigned)total) {
@@ -1209,7 +1212,8 @@ __global__ __launch_bounds__(ATTN_WIDE_WG, 1) void k_attend_wide(AttnArgs a)
             const float sum = row_sum(l[r]);
             const int at = w * 16 * R + r * 16 + col;
             if (grp == 0)
-                s_ml[at] = make_float2(m[r] == -INFINITY ? -INFINITY : m[r] * (a.c1 * QUARTER), sum);
+                s_ml[at] = make_float2(m[r] == -INFINITY ? -INFINITY
+                                                         : __builtin_fmaf(m[r], a.c1 * QUARTER, LAG * QUARTER), sum);
 #pragma unroll
             for (int x = 0; x < NT; ++x)
                 *reinterpret_cast<f32x4 *>(&s_o[at][x * 16 + grp * 4]) = o[r][x];

@@ -196,3 +196,26 @@ def test_scale_zero_takes_the_mean_whatever_the_queries(dt, D, group, m):
     s.q[1::3] = float("nan")
     s.q64[:] = 0.0
     s.device().check_attend(scale=0.0)
+
+
+@pytest.mark.parametrize("D,group,m", WIDE)
+def test_values_near_the_types_largest(D, group, m):
+    """A token of a large weight, not among the first, whose values are 1e38: no weight is above 1, so that
+    the sums pass fp32 only where the weighted values do."""
+    s = Setup("bf16", group, 1, D, 16, [900, 1300], [m, m], seed=D + m, parents=False)
+    st, scale = s.step(), D ** -0.5
+    r = np.random.RandomState(3)
+    u = r.standard_normal(D)
+    s.q = torch.from_numpy((u + 0.02 * r.standard_normal(s.q64.shape)).astype(np.float32)).bfloat16()
+    s.q64[:] = s.q.double().numpy()
+    (kt, kf), (vt, vf) = s.pools
+    kt.mul_(0.25)
+    kf[:] = kt.double().numpy()
+    for i, j in ((0, 500), (1, 777)):
+        at = st.slot(st.entry(i)[0], j)
+        kt.view(-1, 1, D)[at] = torch.from_numpy(u * 4.5 / scale / (u @ u)).bfloat16()
+        kf.reshape(-1, 1, D)[at] = kt.view(-1, 1, D)[at].double().numpy()
+        vt.view(-1, 1, D)[at] *= 1e38 / vt.view(-1, 1, D)[at].abs().max()
+        vf.reshape(-1, 1, D)[at] = vt.view(-1, 1, D)[at].double().numpy()
+    got = s.device().check_attend(scale)
+    assert np.isfinite(got).all() and np.abs(got).max() > 1e35
