@@ -529,6 +529,7 @@ typedef struct specverify_rotation {
  * commit moves them.
  * Arithmetic in fp32, one rounding at the end.  The places' pages have to be the sequence's own, as
  * after a reserve; a token whose page is out of range is not written.
+ * EINVAL also for key_pool equal to value_pool (an attend may read both from one pool).
  */
 int specverify_attn_append(specverify_attn *attn, void *hip_stream, int key_pool, int value_pool,
                            int n, int max_count, int rows, const specverify_nodes *nodes,

@@ -986,7 +986,9 @@ int specverify_attn_append(specverify_attn *attn, void *hip_stream, int key_pool
                            const void *queries, int64_t query_stride, void *rotated,
                            int64_t rotated_stride, int32_t *status)
 {
-    if (!attn || n < 0 || max_count < 0 || rows < 0 || bad_pools(attn, key_pool, value_pool))
+    // keys and values would be written to the same places at once
+    if (!attn || n < 0 || max_count < 0 || rows < 0 || bad_pools(attn, key_pool, value_pool) ||
+        key_pool == value_pool)
         return SPECVERIFY_EINVAL;
     const sv::AttnShape &s = attn->shape;
     sv::RotationView rot = {nullptr, 0, 0};

@@ -6,6 +6,7 @@ import pytest
 import torch
 
 import attn_model as model
+from rejection_sampling_verification_row_amd import binding as sv
 from test_gpu_attn import E, HALF, TD, Setup
 
 pytestmark = pytest.mark.gpu
@@ -219,3 +220,23 @@ def test_values_near_the_types_largest(D, group, m):
         vf.reshape(-1, 1, D)[at] = vt.view(-1, 1, D)[at].double().numpy()
     got = s.device().check_attend(scale)
     assert np.isfinite(got).all() and np.abs(got).max() > 1e35
+
+
+def test_one_pool_for_keys_and_values():
+    """An append into it is refused and writes nothing; attention may read both from it."""
+    s = Setup("bf16", 4, 2, 64, 8, [30, 20], [5, 4], seed=1).device()
+    lib = sv.load()
+    status = torch.full((2,), -7, dtype=torch.int32, device="cuda")
+    for pool in (0, 1):
+        assert lib.specverify_attn_append(s.h, None, pool, pool, 2, 5, s.rows, sv.ctypes.byref(s.nodes), None, s.dk.data_ptr(),
+                                          s.wide, s.dv.data_ptr(), s.wide, None, 0, None, 0,
+                                          status.data_ptr()) == sv.SPECVERIFY_EINVAL
+    out = torch.zeros(s.rows, 4, 64, dtype=torch.bfloat16, device="cuda")
+    sv.specverify_attn_attend(s.h, None, 1, 1, 2, 5, s.rows, s.nodes, 0.1, 0, s.dq, s.wide, out, 256)
+    torch.cuda.synchronize()
+    assert status.tolist() == [-7, -7]
+    for (t, _), d in zip(s.pools, s.dpools):
+        assert torch.equal(t, d.cpu())
+    vp = s.pools[1][1].reshape(-1, 2, 64)
+    want, _, _, rows, size = model.attend(s.step(), vp, vp, s.q64, 0.1, 0, 2)
+    assert np.all(np.abs(out.double().cpu().numpy() - want)[rows] <= (2.0 ** -7 * size + 1e-4)[rows])
