@@ -550,7 +550,7 @@ int specverify_attn_append(specverify_attn *attn, void *hip_stream, int key_pool
  * weights exp(s_j - max) are rounded to bfloat16 for the product with the values (their sum is
  * not), and the result once more at the end.  The order of the sums depends on the call's lengths
  * only: the same call gives the same bits.
- * EINVAL also for a scale that is not finite, window < 0.
+ * EINVAL also for a scale that is not finite or above 2e38 in size, window < 0.
  */
 int specverify_attn_attend(specverify_attn *attn, void *hip_stream, int key_pool, int value_pool,
                            int n, int max_count, int rows, const specverify_nodes *nodes,

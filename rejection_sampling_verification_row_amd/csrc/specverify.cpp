@@ -1031,7 +1031,7 @@ int specverify_attn_attend(specverify_attn *attn, void *hip_stream, int key_pool
                            void *out, int64_t out_stride, float *lse, int32_t *status)
 {
     if (!attn || n < 0 || max_count < 0 || rows < 0 || bad_pools(attn, key_pool, value_pool) ||
-        !isfinite(scale) || window < 0)
+        !(fabsf(scale) <= 2e38f) || window < 0)          // times log2(e) it is finite
         return SPECVERIFY_EINVAL;
     const sv::AttnShape &s = attn->shape;
     sv::NodesView nv;

@@ -240,3 +240,22 @@ def test_one_pool_for_keys_and_values():
     vp = s.pools[1][1].reshape(-1, 2, 64)
     want, _, _, rows, size = model.attend(s.step(), vp, vp, s.q64, 0.1, 0, 2)
     assert np.all(np.abs(out.double().cpu().numpy() - want)[rows] <= (2.0 ** -7 * size + 1e-4)[rows])
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("D,group,m", [(64, 2, 7), (128, 8, 8)])
+def test_the_largest_scale(dt, D, group, m):
+    """Scores of 0 at a scale of 2e38: a mean.  Above it the scale's powers of two pass fp32, and the call is
+    refused."""
+    s = Setup(dt, 2 * group, 2, D, 8, [300, 9], [m, 3], seed=D)
+    s.q.zero_()
+    s.q64[:] = 0.0
+    s.device().check_attend(scale=float(np.float32(2e38)))
+    out = torch.full((s.rows, s.H, D), 7.0, dtype=TD[dt], device="cuda")
+    for scale in (2.1e38, -2.1e38, 3.4e38):
+        with pytest.raises(sv.SpecVerifyError) as e:
+            sv.specverify_attn_attend(s.h, None, 0, 1, s.n, s.max_count, s.rows, s.nodes, scale, 0, s.dq, s.wide, out,
+                                      s.H * D)
+        assert e.value.status == sv.SPECVERIFY_EINVAL
+    torch.cuda.synchronize()
+    assert torch.all(out == 7)
