@@ -895,8 +895,8 @@ __device__ inline void load_to_lds4(const void *from, uint32_t to)
 // 120 others with 16 exponentials (about 630 cycles), which overlap only if the two waves of a SIMD do
 // different things.  So with four stages the upper half of the waves meets the stage's barrier between
 // its scores and its weights, when the lower half begins with scores, and matrix instructions have
-// priority (531 -> 520 us): 16 sequences of 64 nodes, 64 query and 8 key heads, 8000 to 16000 tokens: 505 us,
-// 733 TFLOP/s, where a large library product reaches 1352 TFLOP/s.  The matrix units are busy 36% of the time;
+// priority (531 -> 520 us): 16 sequences of 64 nodes, 64 query and 8 key heads, 8000 to 16000 tokens: 510 us,
+// 726 TFLOP/s, where a large library product reaches 1352 TFLOP/s.  The matrix units are busy 36% of the time;
 // waves wait for barriers and LDS 29% of theirs and for their turn to issue 27%.  Not kept: the next block's
 // keys read, or its scores computed, before the weights of this one (no registers are left, 2 times slower).
 //
